@@ -199,3 +199,125 @@ class SeparateAttention:
 
     def error_flags(self) -> int:
         return int(self.err_flags.item())
+
+
+def _require(ok: bool, message: str):
+    if not ok:
+        raise B.PaError(B.PA_ERR_INVALID_ARGUMENT, message)
+
+
+class PagePool:
+    """Pages of a set of paged caches, kept on the device: which sequence
+    holds which (``block_table``), how often each is held (``refcount``) and
+    how many tokens each sequence has cached (``past``).
+
+    ``caches``: the paged tensors that share the page ids, ``[num_blocks,
+    block_size, ...]`` and contiguous in a page (the layers' ``key_cache`` /
+    ``value_cache`` of the attention objects above). ``block_table`` [B, mb],
+    ``past`` [B] and ``refcount`` [num_blocks] are int32 tensors: pass those in
+    use, or leave them out for an empty pool of ``max_seqs`` sequences of up to
+    ``max_blocks_per_seq`` pages. The three go to ``forward`` as they are.
+
+    Every method only enqueues kernels on ``stream`` (the current stream of
+    the pool's device by default) and can be captured in a CUDA graph after
+    one eager call; calls on one pool have to be ordered by the caller. See
+    include/pa_pages.h for what each does with arguments that make no sense;
+    ``error_flags`` reads what the device reported."""
+
+    def __init__(self, caches, *, block_size: int, block_table: Optional[torch.Tensor] = None,
+                 past: Optional[torch.Tensor] = None, refcount: Optional[torch.Tensor] = None,
+                 max_seqs: Optional[int] = None, max_blocks_per_seq: Optional[int] = None):
+        self.caches = list(caches)
+        _require(len(self.caches) > 0, "a pool needs at least one cache")
+        first = self.caches[0]
+        self.device, self.num_blocks = first.device, int(first.shape[0])
+        _require(self.device.type == "cuda", "caches must be CUDA tensors")
+        for c in self.caches:
+            _require(c.device == self.device and c.dim() >= 2 and int(c.shape[0]) == self.num_blocks
+                     and int(c.shape[1]) == block_size,
+                     "every cache must be [num_blocks, block_size, ...] on one device")
+            _require(c[0].is_contiguous() and (self.num_blocks == 1 or c.stride(0) == c[0].numel()),
+                     "caches must be contiguous")
+            _require(c.data_ptr() % 16 == 0 and c[0, 0].numel() * c.element_size() % 16 == 0,
+                     "cache rows must be multiples of 16 bytes, 16-byte aligned")
+        if block_table is None:
+            _require(max_seqs is not None and max_blocks_per_seq is not None,
+                     "without a block_table, max_seqs and max_blocks_per_seq are needed")
+            block_table = torch.full((max_seqs, max_blocks_per_seq), -1, dtype=torch.int32,
+                                     device=self.device)
+        _require(block_table.dim() == 2, "block_table must be [num_seqs, max_blocks_per_seq]")
+        if past is None:
+            past = torch.zeros(block_table.shape[0], dtype=torch.int32, device=self.device)
+        if refcount is None:
+            refcount = torch.zeros(self.num_blocks, dtype=torch.int32, device=self.device)
+        self._ints(block_table=block_table, past=past, refcount=refcount)
+        _require(past.numel() == block_table.shape[0], "past must be [num_seqs]")
+        _require(refcount.numel() == self.num_blocks, "refcount must be [num_blocks]")
+        self.block_table, self.past, self.refcount = block_table, past, refcount
+        self.params = B.make_pages_params(num_blocks=self.num_blocks, block_size=block_size,
+                                          max_blocks_per_seq=block_table.shape[1],
+                                          num_seqs=block_table.shape[0])
+        s = B.pa_pages_validate(self.params)
+        if s != B.PA_OK:
+            raise B.PaError(s, B.last_error())
+        self._list = B.make_page_caches(self.caches)
+        self.workspace = torch.empty(B.pa_pages_workspace_size(self.params), dtype=torch.uint8,
+                                     device=self.device)
+        self.err_flags = torch.zeros(1, dtype=torch.int32, device=self.device)
+        #: pages held after the last ``compact`` (int32 [1] on the device)
+        self.live = torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    def _ints(self, **tensors):
+        for name, t in tensors.items():
+            _require(t.dtype == torch.int32 and t.device == self.device and t.is_contiguous(),
+                     f"{name} must be a contiguous int32 tensor on {self.device}")
+
+    def _call(self, fn, *args, stream):
+        with torch.cuda.device(self.device):
+            fn(self.params, *args, err_flags=self.err_flags, stream=stream)
+
+    def copy(self, src, dst, rows=None, stream=None):
+        """Pages ``src[i]`` -> ``dst[i]`` (their first ``rows[i]`` rows) in every cache."""
+        self._ints(src=src, dst=dst, **({} if rows is None else {"rows": rows}))
+        _require(dst.numel() == src.numel() and (rows is None or rows.numel() == src.numel()),
+                 "src, dst and rows must have one entry per pair")
+        self._call(B.pa_pages_copy, self._list, len(self.caches), src, dst, rows, self.workspace,
+                   stream=stream)
+
+    def fork(self, parents, children, stream=None):
+        """Sequence ``children[i]`` becomes a copy of ``parents[i]``: full pages
+        shared, the rows of the last one copied into a page of its own."""
+        self._ints(parents=parents, children=children)
+        _require(parents.numel() == children.numel(), "parents and children must pair up")
+        self._call(B.pa_pages_fork, self._list, len(self.caches), parents, children,
+                   self.block_table, self.past, self.refcount, self.workspace, stream=stream)
+
+    def free(self, seqs, stream=None):
+        """Takes the pages of ``seqs`` back (their rows become -1, their past 0)."""
+        self._ints(seqs=seqs)
+        self._call(B.pa_pages_free, seqs, self.block_table, self.past, self.refcount,
+                   stream=stream)
+
+    def reserve(self, cumseq, slot_mapping, stream=None) -> torch.Tensor:
+        """Pages for the ``cumseq[b+1] - cumseq[b]`` next tokens of every
+        sequence; fills ``slot_mapping`` [T] for the write phase and returns
+        it. ``past`` stays (add the new tokens once they are written)."""
+        self._ints(cumseq=cumseq, slot_mapping=slot_mapping)
+        _require(cumseq.numel() == self.past.numel() + 1, "cumseq must be [num_seqs + 1]")
+        self._call(B.pa_pages_reserve, cumseq, self.block_table, self.past, self.refcount,
+                   slot_mapping, self.workspace, stream=stream)
+        return slot_mapping
+
+    def compact(self, stream=None) -> torch.Tensor:
+        """Moves the held pages to the lowest ids; returns ``live`` (their
+        number, on the device)."""
+        self._call(B.pa_pages_compact, self._list, len(self.caches), self.block_table,
+                   self.refcount, self.live, self.workspace, stream=stream)
+        return self.live
+
+    def error_flags(self) -> int:
+        """Reads the device error word (synchronises with the device)."""
+        return int(self.err_flags.item())
+
+    def reset_error_flags(self):
+        self.err_flags.zero_()

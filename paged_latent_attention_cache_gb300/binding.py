@@ -51,6 +51,13 @@ EXPORTED = ("pa_latent_validate", "pa_latent_write", "pa_latent_decode", "pa_lat
             "pa_separate_write", "pa_separate_decode", "pa_separate_prefill",
             "pa_separate_workspace_size")
 
+# include/pa_pages.h
+EXPORTED_PAGES = ("pa_pages_validate", "pa_pages_workspace_size", "pa_pages_copy",
+                  "pa_pages_fork", "pa_pages_free", "pa_pages_reserve", "pa_pages_compact")
+
+PA_DEVERR_POOL = 0x100
+PA_DEVERR_PAGE = 0x200
+
 
 class PaError(RuntimeError):
     def __init__(self, status: int, message: str):
@@ -102,6 +109,19 @@ class pa_separate_params(ctypes.Structure):
     ]
 
 
+class pa_pages_params(ctypes.Structure):
+    _fields_ = [
+        ("num_blocks", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("max_blocks_per_seq", ctypes.c_int32),
+        ("num_seqs", ctypes.c_int32),
+    ]
+
+
+class pa_pages_cache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_bytes", ctypes.c_int64)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run "
@@ -146,6 +166,18 @@ def _load() -> ctypes.CDLL:
     lib.pa_separate_prefill.restype = ctypes.c_int
     lib.pa_separate_workspace_size.argtypes = [S, i32, i64]
     lib.pa_separate_workspace_size.restype = sz
+    G, C = ctypes.POINTER(pa_pages_params), ctypes.POINTER(pa_pages_cache)
+    lib.pa_pages_validate.argtypes = [G]
+    lib.pa_pages_workspace_size.argtypes = [G]
+    lib.pa_pages_workspace_size.restype = sz
+    lib.pa_pages_copy.argtypes = [G, C, i32, vp, vp, vp, i32, vp, sz, vp, vp]
+    lib.pa_pages_fork.argtypes = [G, C, i32, vp, vp, i32, vp, vp, vp, vp, sz, vp, vp]
+    lib.pa_pages_free.argtypes = [G, vp, i32, vp, vp, vp, vp, vp]
+    lib.pa_pages_reserve.argtypes = [G, vp, i64, vp, vp, vp, vp, vp, sz, vp, vp]
+    lib.pa_pages_compact.argtypes = [G, C, i32, vp, vp, vp, vp, sz, vp, vp]
+    for name in EXPORTED_PAGES:
+        if name != "pa_pages_workspace_size":
+            getattr(lib, name).restype = ctypes.c_int
     return lib
 
 
@@ -345,6 +377,66 @@ def pa_separate_prefill(p, query, key_cache, value_cache, cos_cache, sin_cache, 
     _sread(lib.pa_separate_prefill, p, query, key_cache, value_cache, cos_cache, sin_cache,
            q_norm_weight, head_sink, cumseq, past, block_table, out, seq_begin, seq_end,
            workspace, err_flags, stream)
+
+
+def make_pages_params(*, num_blocks, block_size, max_blocks_per_seq, num_seqs) -> pa_pages_params:
+    return pa_pages_params(int(num_blocks), int(block_size), int(max_blocks_per_seq),
+                           int(num_seqs))
+
+
+def make_page_caches(caches):
+    """The host array of pa_pages_cache for paged tensors [num_blocks, ...]."""
+    arr = (pa_pages_cache * max(len(caches), 1))()
+    for i, c in enumerate(caches):
+        arr[i].data = c.data_ptr()
+        arr[i].page_bytes = c.stride(0) * c.element_size()
+    return arr
+
+
+def pa_pages_validate(p: pa_pages_params) -> int:
+    return int(lib.pa_pages_validate(ctypes.byref(p)))
+
+
+def pa_pages_workspace_size(p: pa_pages_params) -> int:
+    return int(lib.pa_pages_workspace_size(ctypes.byref(p)))
+
+
+def _ws(workspace):
+    n = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return _ptr(workspace), ctypes.c_size_t(n)
+
+
+def pa_pages_copy(p, caches, num_caches, src, dst, rows, workspace, err_flags=None, stream=None):
+    _check(lib.pa_pages_copy(ctypes.byref(p), caches, int(num_caches), _ptr(src), _ptr(dst),
+                             _ptr(rows), int(src.numel()), *_ws(workspace), _ptr(err_flags),
+                             _stream(stream)))
+
+
+def pa_pages_fork(p, caches, num_caches, parents, children, block_table, past, refcount,
+                  workspace, err_flags=None, stream=None):
+    _check(lib.pa_pages_fork(ctypes.byref(p), caches, int(num_caches), _ptr(parents),
+                             _ptr(children), int(parents.numel()), _ptr(block_table), _ptr(past),
+                             _ptr(refcount), *_ws(workspace), _ptr(err_flags), _stream(stream)))
+
+
+def pa_pages_free(p, seqs, block_table, past, refcount, err_flags=None, stream=None):
+    _check(lib.pa_pages_free(ctypes.byref(p), _ptr(seqs), int(seqs.numel()), _ptr(block_table),
+                             _ptr(past), _ptr(refcount), _ptr(err_flags), _stream(stream)))
+
+
+def pa_pages_reserve(p, cumseq, block_table, past, refcount, slot_mapping, workspace,
+                     err_flags=None, stream=None):
+    _check(lib.pa_pages_reserve(ctypes.byref(p), _ptr(cumseq), int(slot_mapping.numel()),
+                                _ptr(block_table), _ptr(past), _ptr(refcount),
+                                _ptr(slot_mapping), *_ws(workspace), _ptr(err_flags),
+                                _stream(stream)))
+
+
+def pa_pages_compact(p, caches, num_caches, block_table, refcount, live, workspace,
+                     err_flags=None, stream=None):
+    _check(lib.pa_pages_compact(ctypes.byref(p), caches, int(num_caches), _ptr(block_table),
+                                _ptr(refcount), _ptr(live), *_ws(workspace), _ptr(err_flags),
+                                _stream(stream)))
 
 
 def default_scale(head_size: int) -> float:
