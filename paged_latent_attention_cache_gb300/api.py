@@ -206,6 +206,161 @@ def _require(ok: bool, message: str):
         raise B.PaError(B.PA_ERR_INVALID_ARGUMENT, message)
 
 
+class DifferentialAttention:
+    """Differential attention over paged caches (include/pa_diff.h): two query
+    and key maps per head and one value, the difference of the two softmax
+    maps with the layer's learned lambda, RMSNorm per head. Holds the
+    parameters, the workspace and the error word; ``forward`` issues write ->
+    decode -> prefill like ``PagedLatentAttention``.
+
+    ``query`` [T, H*2*hs], ``key`` [T, kvH*2*hs], ``value`` [T, kvH*vhs],
+    ``key_cache`` [num_blocks, bs, kvH, 2, hs], ``value_cache`` [num_blocks,
+    bs, kvH, vhs], ``lambda_vectors`` float32 [4, hs], ``norm_weight`` [vhs];
+    ``v_head_size`` 0 means 2 * hs. The block tables and slots can come from a
+    ``PagePool`` over the two caches."""
+
+    def __init__(self, *, dtype: torch.dtype, num_heads: int, kv_num_heads: int, head_size: int,
+                 v_head_size: int = 0, rotary_offset: int = 0, rotary_dim: int = 0,
+                 rotary_interleaved: int = 0, cos_rows: int = 1, block_size: int,
+                 num_blocks: int, max_blocks_per_seq: int, scale: float = 0.0,
+                 softcap: float = 0.0, local_window_size: int = -1, lambda_init: float,
+                 norm_eps: float = 1e-5, max_seqs: int, max_tokens: int, device="cuda",
+                 own_slots: bool = False):
+        self.dtype = dtype
+        self.num_heads, self.kv_num_heads = num_heads, kv_num_heads
+        self.head_size, self.v_head_size = head_size, v_head_size or 2 * head_size
+        self.params = B.make_diff_params(
+            dtype=dtype, num_heads=num_heads, kv_num_heads=kv_num_heads, head_size=head_size,
+            v_head_size=v_head_size, rotary_offset=rotary_offset, rotary_dim=rotary_dim,
+            rotary_interleaved=rotary_interleaved, cos_rows=cos_rows, block_size=block_size,
+            num_blocks=num_blocks, max_blocks_per_seq=max_blocks_per_seq, scale=scale,
+            softcap=softcap, local_window_size=local_window_size, lambda_init=lambda_init,
+            norm_eps=norm_eps)
+        s = B.pa_diff_validate(self.params)
+        if s != B.PA_OK:
+            raise B.PaError(s, B.last_error())
+        # as in PagedLatentAttention: the first read call after the write phase
+        self.params_after_write = B.pa_diff_params.from_buffer_copy(self.params)
+        self.params_after_write.flags |= B.PA_FLAG_AFTER_WRITE | (
+            B.PA_FLAG_OWN_SLOTS if own_slots else 0)
+        self.device = torch.empty(0, device=device).device
+        self.max_seqs, self.max_tokens = max_seqs, max_tokens
+        with torch.cuda.device(self.device):
+            n = B.pa_diff_workspace_size(self.params, max_seqs, max_tokens)
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
+        self.err_flags = torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    def _check(self, halves, ints, lambda_vectors=None):
+        p = self.params
+        for name, t, last in halves:
+            _require(t.dtype == self.dtype and t.device == self.device and t.is_contiguous()
+                     and (last is None or t.shape[-1] == last),
+                     f"{name} must be a contiguous {self.dtype} tensor on {self.device}"
+                     + ("" if last is None else f" with {last} columns"))
+        for name, t in ints:
+            _require(t.dtype == torch.int32 and t.device == self.device and t.is_contiguous(),
+                     f"{name} must be a contiguous int32 tensor on {self.device}")
+        if lambda_vectors is not None:
+            _require(lambda_vectors.dtype == torch.float32 and lambda_vectors.is_contiguous()
+                     and lambda_vectors.device == self.device
+                     and lambda_vectors.numel() == 4 * p.head_size,
+                     "lambda_vectors must be a contiguous float32 [4, head_size] tensor")
+
+    def _check_caches(self, key_cache, value_cache, cos_cache, sin_cache):
+        p = self.params
+        rows = p.num_blocks * p.block_size * p.kv_num_heads
+        self._check([("key_cache", key_cache, p.head_size),
+                     ("value_cache", value_cache, self.v_head_size)]
+                    + ([("cos_cache", cos_cache, p.rotary_dim // 2),
+                        ("sin_cache", sin_cache, p.rotary_dim // 2)] if p.rotary_dim else []), [])
+        _require(key_cache.numel() == rows * 2 * p.head_size
+                 and value_cache.numel() == rows * self.v_head_size,
+                 "key_cache must be [num_blocks, bs, kvH, 2, hs], value_cache [num_blocks, bs, "
+                 "kvH, vhs]")
+        _require(not p.rotary_dim or (cos_cache.shape[0] >= p.cos_rows
+                                      and sin_cache.shape[0] >= p.cos_rows),
+                 "cos_cache and sin_cache must have cos_rows rows")
+
+    def write(self, key, value, key_cache, value_cache, cos_cache, sin_cache, slot_mapping,
+              cumseq, past, stream=None):
+        """Rotates the new keys and stores keys and values in their slots."""
+        p = self.params
+        self._check([("key", key, p.kv_num_heads * 2 * p.head_size),
+                     ("value", value, p.kv_num_heads * self.v_head_size)],
+                    [("slot_mapping", slot_mapping), ("cumseq", cumseq), ("past", past)])
+        self._check_caches(key_cache, value_cache, cos_cache, sin_cache)
+        _require(value.shape[0] == key.shape[0] == slot_mapping.numel()
+                 and cumseq.numel() == past.numel() + 1,
+                 "key, value and slot_mapping must have a row per token, cumseq num_seqs + 1")
+        with torch.cuda.device(self.device):
+            B.pa_diff_write(self.params, key, value, cos_cache, sin_cache, slot_mapping, cumseq,
+                            past, key_cache, value_cache, self.err_flags, stream)
+
+    def _read(self, fn, query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
+              norm_weight, cumseq, past, block_table, out, seq_begin, seq_end, stream,
+              after_write):
+        p = self.params
+        self._check([("query", query, p.num_heads * 2 * p.head_size),
+                     ("norm_weight", norm_weight, self.v_head_size),
+                     ("out", out, p.num_heads * self.v_head_size)],
+                    [("cumseq", cumseq), ("past", past), ("block_table", block_table)],
+                    lambda_vectors)
+        self._check_caches(key_cache, value_cache, cos_cache, sin_cache)
+        _require(out.shape[0] == query.shape[0] and cumseq.numel() == past.numel() + 1
+                 and block_table.numel() == past.numel() * p.max_blocks_per_seq,
+                 "out must have a row per token, cumseq num_seqs + 1 entries and block_table "
+                 "[num_seqs, max_blocks_per_seq]")
+        with torch.cuda.device(self.device):
+            fn(self.params_after_write if after_write else p, query, key_cache, value_cache,
+               cos_cache, sin_cache, lambda_vectors, norm_weight, cumseq, past, block_table, out,
+               seq_begin, seq_end, self.workspace, self.err_flags, stream)
+
+    def decode(self, query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
+               norm_weight, cumseq, past, block_table, out, seq_begin=0, seq_end=None,
+               stream=None, after_write: bool = False):
+        """Sequences [seq_begin, seq_end) with one new token each.
+        ``after_write``: this call directly follows ``write`` on the same
+        stream (see PA_FLAG_AFTER_WRITE)."""
+        self._read(B.pa_diff_decode, query, key_cache, value_cache, cos_cache, sin_cache,
+                   lambda_vectors, norm_weight, cumseq, past, block_table, out, seq_begin,
+                   seq_end, stream, after_write)
+
+    def prefill(self, query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
+                norm_weight, cumseq, past, block_table, out, seq_begin=0, seq_end=None,
+                stream=None, after_write: bool = False):
+        """Sequences [seq_begin, seq_end) with any number of new tokens."""
+        self._read(B.pa_diff_prefill, query, key_cache, value_cache, cos_cache, sin_cache,
+                   lambda_vectors, norm_weight, cumseq, past, block_table, out, seq_begin,
+                   seq_end, stream, after_write)
+
+    def forward(self, query, key, value, key_cache, value_cache, cos_cache, sin_cache,
+                lambda_vectors, norm_weight, cumseq, past, block_table, slot_mapping,
+                num_decode_seqs: int, out: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+        """Write phase over all tokens, then decode over sequences [0,
+        num_decode_seqs) and prefill over the rest; returns ``out``."""
+        nseq = past.shape[0]
+        if out is None:
+            out = torch.empty(query.shape[0], self.num_heads * self.v_head_size,
+                              dtype=self.dtype, device=query.device)
+        self.write(key, value, key_cache, value_cache, cos_cache, sin_cache, slot_mapping,
+                   cumseq, past, stream)
+        args = (query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors, norm_weight,
+                cumseq, past, block_table, out)
+        if num_decode_seqs > 0:
+            self.decode(*args, 0, num_decode_seqs, stream, after_write=True)
+        if num_decode_seqs < nseq:
+            self.prefill(*args, num_decode_seqs, nseq, stream, after_write=num_decode_seqs == 0)
+        return out
+
+    def error_flags(self) -> int:
+        """Reads the device error word (synchronises with the device)."""
+        return int(self.err_flags.item())
+
+    def reset_error_flags(self):
+        self.err_flags.zero_()
+
+
 class PagePool:
     """Pages of a set of paged caches, kept on the device: which sequence
     holds which (``block_table``), how often each is held (``refcount``) and

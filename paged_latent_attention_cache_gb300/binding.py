@@ -55,6 +55,10 @@ EXPORTED = ("pa_latent_validate", "pa_latent_write", "pa_latent_decode", "pa_lat
 EXPORTED_PAGES = ("pa_pages_validate", "pa_pages_workspace_size", "pa_pages_copy",
                   "pa_pages_fork", "pa_pages_free", "pa_pages_reserve", "pa_pages_compact")
 
+# include/pa_diff.h
+EXPORTED_DIFF = ("pa_diff_validate", "pa_diff_write", "pa_diff_decode", "pa_diff_prefill",
+                 "pa_diff_workspace_size")
+
 PA_DEVERR_POOL = 0x100
 PA_DEVERR_PAGE = 0x200
 
@@ -122,6 +126,29 @@ class pa_pages_cache(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("page_bytes", ctypes.c_int64)]
 
 
+class pa_diff_params(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("kv_num_heads", ctypes.c_int32),
+        ("head_size", ctypes.c_int32),
+        ("v_head_size", ctypes.c_int32),
+        ("rotary_offset", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("rotary_interleaved", ctypes.c_int32),
+        ("cos_rows", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32),
+        ("max_blocks_per_seq", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("softcap", ctypes.c_float),
+        ("local_window_size", ctypes.c_int32),
+        ("lambda_init", ctypes.c_float),
+        ("norm_eps", ctypes.c_float),
+        ("flags", ctypes.c_int32),
+    ]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run "
@@ -175,8 +202,16 @@ def _load() -> ctypes.CDLL:
     lib.pa_pages_free.argtypes = [G, vp, i32, vp, vp, vp, vp, vp]
     lib.pa_pages_reserve.argtypes = [G, vp, i64, vp, vp, vp, vp, vp, sz, vp, vp]
     lib.pa_pages_compact.argtypes = [G, C, i32, vp, vp, vp, vp, sz, vp, vp]
-    for name in EXPORTED_PAGES:
-        if name != "pa_pages_workspace_size":
+    D = ctypes.POINTER(pa_diff_params)
+    lib.pa_diff_validate.argtypes = [D]
+    lib.pa_diff_write.argtypes = [D, vp, vp, i64, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp]
+    dread = [D, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, sz, vp, vp, vp]
+    lib.pa_diff_decode.argtypes = dread
+    lib.pa_diff_prefill.argtypes = dread
+    lib.pa_diff_workspace_size.argtypes = [D, i32, i64]
+    lib.pa_diff_workspace_size.restype = sz
+    for name in EXPORTED_PAGES + EXPORTED_DIFF:
+        if not name.endswith("workspace_size"):
             getattr(lib, name).restype = ctypes.c_int
     return lib
 
@@ -437,6 +472,63 @@ def pa_pages_compact(p, caches, num_caches, block_table, refcount, live, workspa
     _check(lib.pa_pages_compact(ctypes.byref(p), caches, int(num_caches), _ptr(block_table),
                                 _ptr(refcount), _ptr(live), *_ws(workspace), _ptr(err_flags),
                                 _stream(stream)))
+
+
+def make_diff_params(*, dtype, num_heads, kv_num_heads, head_size, v_head_size=0,
+                     rotary_offset=0, rotary_dim=0, rotary_interleaved=0, cos_rows=1,
+                     block_size, num_blocks, max_blocks_per_seq, scale=0.0, softcap=0.0,
+                     local_window_size=-1, lambda_init, norm_eps=1e-5, flags=0) -> pa_diff_params:
+    if isinstance(dtype, torch.dtype):
+        dtype = {torch.float16: PA_DTYPE_F16, torch.bfloat16: PA_DTYPE_BF16}.get(dtype, -1)
+    return pa_diff_params(int(dtype), int(num_heads), int(kv_num_heads), int(head_size),
+                          int(v_head_size), int(rotary_offset), int(rotary_dim),
+                          int(rotary_interleaved), int(cos_rows), int(block_size),
+                          int(num_blocks), int(max_blocks_per_seq), float(scale),
+                          float(softcap), int(local_window_size), float(lambda_init),
+                          float(norm_eps), int(flags))
+
+
+def pa_diff_validate(p: pa_diff_params) -> int:
+    return int(lib.pa_diff_validate(ctypes.byref(p)))
+
+
+def pa_diff_workspace_size(p: pa_diff_params, num_seqs: int, num_tokens: int) -> int:
+    return int(lib.pa_diff_workspace_size(ctypes.byref(p), int(num_seqs), int(num_tokens)))
+
+
+def pa_diff_write(p, key, value, cos_cache, sin_cache, slot_mapping, cumseq, past, key_cache,
+                  value_cache, err_flags=None, stream=None):
+    _check(lib.pa_diff_write(ctypes.byref(p), _ptr(key), _ptr(value), int(key.shape[0]),
+                             _ptr(cos_cache), _ptr(sin_cache), _ptr(slot_mapping), _ptr(cumseq),
+                             _ptr(past), int(past.shape[0]), _ptr(key_cache), _ptr(value_cache),
+                             _ptr(err_flags), _stream(stream)))
+
+
+def _dread(fn, p, query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
+           norm_weight, cumseq, past, block_table, out, seq_begin, seq_end, workspace, err_flags,
+           stream):
+    n = past.shape[0]
+    _check(fn(ctypes.byref(p), _ptr(query), int(query.shape[0]), _ptr(key_cache),
+              _ptr(value_cache), _ptr(cos_cache), _ptr(sin_cache), _ptr(lambda_vectors),
+              _ptr(norm_weight), _ptr(cumseq), _ptr(past), _ptr(block_table), int(n),
+              int(seq_begin), int(n if seq_end is None else seq_end), *_ws(workspace),
+              _ptr(out), _ptr(err_flags), _stream(stream)))
+
+
+def pa_diff_decode(p, query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
+                   norm_weight, cumseq, past, block_table, out, seq_begin=0, seq_end=None,
+                   workspace=None, err_flags=None, stream=None):
+    _dread(lib.pa_diff_decode, p, query, key_cache, value_cache, cos_cache, sin_cache,
+           lambda_vectors, norm_weight, cumseq, past, block_table, out, seq_begin, seq_end,
+           workspace, err_flags, stream)
+
+
+def pa_diff_prefill(p, query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
+                    norm_weight, cumseq, past, block_table, out, seq_begin=0, seq_end=None,
+                    workspace=None, err_flags=None, stream=None):
+    _dread(lib.pa_diff_prefill, p, query, key_cache, value_cache, cos_cache, sin_cache,
+           lambda_vectors, norm_weight, cumseq, past, block_table, out, seq_begin, seq_end,
+           workspace, err_flags, stream)
 
 
 def default_scale(head_size: int) -> float:

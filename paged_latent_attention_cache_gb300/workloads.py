@@ -547,3 +547,75 @@ def separate_oracle_params(w: SeparateWorkload) -> Dict[str, object]:
 
 
 WORKLOADS["gqa_decode"] = gqa_decode
+
+
+# ---------------------------------------------------------------------------
+# Differential attention (include/pa_diff.h)
+# ---------------------------------------------------------------------------
+
+@dataclass
+class DiffWorkload:
+    """Inputs of differential attention: query [T, H*2*hs], key [T,
+    kvH*2*hs], value [T, kvH*vhs], key_cache [num_blocks, bs, kvH, 2, hs],
+    value_cache [num_blocks, bs, kvH, vhs], lambda_vectors float32 [4, hs],
+    norm_weight [vhs]; the index tensors as in ``Workload``. ``params`` are
+    the keyword arguments of ``api.DifferentialAttention``."""
+    name: str
+    params: Dict[str, object]
+    q_lens: List[int]
+    past_lens: List[int]
+    num_decode_seqs: int
+    tensors: Dict[str, torch.Tensor]
+
+    def __getattr__(self, name):
+        for d in ("params", "tensors"):
+            if name in self.__dict__.get(d, {}):
+                return self.__dict__[d][name]
+        raise AttributeError(name)
+
+    @property
+    def num_tokens(self) -> int:
+        return int(self.tensors["query"].shape[0])
+
+
+def make_diff_workload(name: str, q_lens: Sequence[int], past_lens: Sequence[int], *,
+                       dtype=torch.bfloat16, num_heads: int, kv_num_heads: int, head_size: int,
+                       v_head_size: Optional[int] = None, rotary_offset: int = 0,
+                       rotary_dim: Optional[int] = None, rotary_interleaved: int = 0,
+                       block_size: int, num_blocks: Optional[int] = None,
+                       max_blocks_per_seq: Optional[int] = None,
+                       cos_rows: Optional[int] = None, scale: float = 0.0, softcap: float = 0.0,
+                       local_window_size: int = -1, lambda_init: float = 0.5,
+                       norm_eps: float = 1e-5, seed: int = 0, std: float = 1.0,
+                       drop_slots: int = 0) -> DiffWorkload:
+    """Draw one seeded batch: the block placement, offsets and slots as
+    ``make_workload`` draws them; query, key, value and both cache pools
+    N(0, std^2); lambda vectors N(0, 0.1^2); norm weights N(1, 0.1^2).
+    Sequences with one new token come first."""
+    base = make_workload(name, q_lens, past_lens, dtype=dtype, num_heads=1, head_size=head_size,
+                         v_head_size=head_size, rotary_offset=rotary_offset,
+                         rotary_dim=head_size if rotary_dim is None else rotary_dim,
+                         rotary_interleaved=rotary_interleaved, block_size=block_size,
+                         num_blocks=num_blocks, max_blocks_per_seq=max_blocks_per_seq,
+                         cos_rows=cos_rows, seed=seed, drop_slots=drop_slots)
+    vhs = 2 * head_size if v_head_size is None else v_head_size
+    gen = torch.Generator().manual_seed(seed + 4242)
+    T, nb, kv = base.num_tokens, base.num_blocks, kv_num_heads
+    t = dict(query=_normal((T, num_heads * 2 * head_size), gen, std, dtype),
+             key=_normal((T, kv * 2 * head_size), gen, std, dtype),
+             value=_normal((T, kv * vhs), gen, std, dtype),
+             key_cache=_normal((nb, block_size, kv, 2, head_size), gen, std, dtype),
+             value_cache=_normal((nb, block_size, kv, vhs), gen, std, dtype),
+             lambda_vectors=0.1 * torch.randn(4, head_size, generator=gen),
+             norm_weight=(1.0 + 0.1 * torch.randn(vhs, generator=gen)).to(dtype),
+             cos_cache=base.cos_cache, sin_cache=base.sin_cache, cumseq=base.cumseq,
+             past=base.past, block_table=base.block_table, slot_mapping=base.slot_mapping)
+    params = dict(dtype=dtype, num_heads=num_heads, kv_num_heads=kv, head_size=head_size,
+                  v_head_size=vhs, rotary_offset=base.rotary_offset, rotary_dim=base.rotary_dim,
+                  rotary_interleaved=rotary_interleaved, cos_rows=base.cos_rows,
+                  block_size=block_size, num_blocks=nb,
+                  max_blocks_per_seq=base.max_blocks_per_seq, scale=scale, softcap=softcap,
+                  local_window_size=local_window_size, lambda_init=lambda_init,
+                  norm_eps=norm_eps)
+    return DiffWorkload(name=name, params=params, q_lens=base.q_lens, past_lens=base.past_lens,
+                        num_decode_seqs=base.num_decode_seqs, tensors=t)

@@ -1,0 +1,327 @@
+"""Differential attention on the GPU against the oracle.
+
+Tolerances: cache rows within 1 ulp where RoPE touches them and bit-equal
+elsewhere. Outputs: |err| <= 6 u noise, u the largest relative rounding error
+of the dtype (2^-8 bf16, 2^-11 fp16) and ``noise`` the oracle's sum of how far
+a rounding of size 1 of the probabilities, the query operand and the output
+moves an output: independent roundings of at most u have a standard deviation
+of u / sqrt(3) times that, so 6 u is over ten of them. On top 2^-20 of the
+largest output of the head for the f32 arithmetic (ex2, sums, norm)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import diff_oracle as D
+from paged_latent_attention_cache_gb300 import binding as B
+from paged_latent_attention_cache_gb300 import workloads as W
+from paged_latent_attention_cache_gb300.api import DifferentialAttention, PagePool
+from tests.harness import UNIT_ROUNDOFF, _ordered
+
+pytestmark = pytest.mark.gpu
+
+
+def _numpy(w):
+    return {k: W.to_bits(v) if v.dtype in (torch.bfloat16, torch.float16) else v.numpy()
+            for k, v in w.tensors.items()}
+
+
+def _op(w, **kw):
+    return DifferentialAttention(**w.params, max_seqs=max(len(w.q_lens), 1),
+                                 max_tokens=max(w.num_tokens, 1), **{"own_slots": True, **kw})
+
+
+def _args(d):
+    return (d["query"], d["key"], d["value"], d["key_cache"], d["value_cache"], d["cos_cache"],
+            d["sin_cache"], d["lambda_vectors"], d["norm_weight"], d["cumseq"], d["past"],
+            d["block_table"], d["slot_mapping"])
+
+
+def run_gpu(w, decodes=None, op=None):
+    d = {k: v.cuda() for k, v in w.tensors.items()}
+    op = op or _op(w)
+    out = torch.full((w.num_tokens, w.num_heads * w.v_head_size), float("nan"), dtype=w.dtype,
+                     device="cuda")
+    op.forward(*_args(d), w.num_decode_seqs if decodes is None else decodes, out=out)
+    torch.cuda.synchronize()
+    return d, out, op
+
+
+def check(w, tokens=None, decodes=None):
+    d, out, op = run_gpu(w, decodes)
+    assert op.error_flags() == 0, hex(op.error_flags())
+    tag = W.dtype_tag(w.dtype)
+    ref = D.run_bits(_numpy(w), w.params, tag, tokens)
+    assert np.array_equal(W.to_bits(d["value_cache"]), ref["value_cache"])
+    k0, k1 = W.to_bits(d["key_cache"]), ref["key_cache"]
+    ulp = np.abs(_ordered(k0) - _ordered(k1))
+    rot = np.zeros(w.head_size, bool)
+    rot[w.rotary_offset:w.rotary_offset + w.rotary_dim] = True
+    assert ulp[..., ~rot].max(initial=0) == 0 and ulp.max() <= 1
+    o = out if tokens is None else out[torch.as_tensor(list(tokens))]
+    got = o.double().cpu().numpy().reshape(ref["out"].shape)
+    assert np.isfinite(got).all()
+    err = np.abs(got - ref["out"])
+    bound = 6 * UNIT_ROUNDOFF[w.dtype] * ref["noise"] + 2.0 ** -20 * np.abs(ref["out"]).max(-1, keepdims=True)
+    worst = (err / bound).max()
+    rel = np.linalg.norm(got - ref["out"]) / np.linalg.norm(ref["out"])
+    print(f"RATIO {w.name}: {worst:.3f} of the bound, relative error {rel:.2e}")
+    assert worst <= 1, worst
+
+
+BASE = dict(q_lens=[1, 1, 1, 9, 0, 40, 130], past_lens=[700, 0, 63, 70, 5, 3, 129], num_heads=8,
+            kv_num_heads=2, head_size=64, block_size=64, seed=11, drop_slots=2)
+
+VARIANTS = {
+    "64_128": {},
+    "128_256": dict(head_size=128),
+    "fp16": dict(dtype=torch.float16),
+    "fp16_128_256": dict(dtype=torch.float16, head_size=128, num_heads=4),
+    "mha": dict(num_heads=4, kv_num_heads=4),
+    "mqa_16": dict(num_heads=16, kv_num_heads=1),
+    "grp_3": dict(num_heads=6, kv_num_heads=2),
+    "grp_12": dict(num_heads=12, kv_num_heads=1, head_size=32),
+    "grp_40": dict(num_heads=40, kv_num_heads=1, head_size=32),
+    "grp_128": dict(num_heads=128, kv_num_heads=1, head_size=16, q_lens=[1, 5], past_lens=[90, 40]),
+    "hs_16": dict(head_size=16),
+    "hs_48_vhs_80": dict(head_size=48, v_head_size=80),
+    "hs_96_vhs_192": dict(head_size=96),
+    "vhs_8": dict(v_head_size=8),
+    "vhs_136": dict(v_head_size=136),
+    "vhs_64": dict(v_head_size=64),
+    "hs_128_vhs_64": dict(head_size=128, v_head_size=64),
+    "bs_16": dict(block_size=16),
+    "bs_128": dict(block_size=128),
+    "bs_256": dict(block_size=256),
+    "window_1": dict(local_window_size=0),
+    "window_7": dict(local_window_size=7),
+    "window_100": dict(local_window_size=100),
+    "softcap": dict(softcap=2.0),
+    "softcap_window": dict(softcap=5.0, local_window_size=33, dtype=torch.float16),
+    "interleaved": dict(rotary_interleaved=1),
+    "partial_rope": dict(rotary_dim=32, rotary_offset=16),
+    "no_rope": dict(rotary_dim=0),
+    "lambda_0.8": dict(lambda_init=0.8),
+    "peaked": dict(std=4.0),
+    "flat": dict(std=0.1, lambda_init=0.2),
+    "scale": dict(scale=0.5),
+}
+
+
+def workload(name, **over):
+    kw = {**BASE, **VARIANTS[name], **over}
+    return W.make_diff_workload(name, kw.pop("q_lens"), kw.pop("past_lens"), **kw)
+
+
+@pytest.mark.parametrize("name", sorted(VARIANTS))
+def test_variants(name):
+    check(workload(name))
+
+
+@pytest.mark.parametrize("name", ["64_128", "128_256", "window_7"])
+def test_decodes_as_prefill(name):
+    """One-token sequences through the prefill call."""
+    check(workload(name, q_lens=[1, 1, 1], past_lens=[700, 0, 63]), decodes=0)
+
+
+@pytest.mark.parametrize("past", [0, 1, 14, 15, 16, 31, 62, 63, 64, 65, 126, 127, 128, 129, 255, 256, 511, 1023])
+def test_decode_lengths(past):
+    """Context lengths around every tile and page boundary."""
+    check(workload("64_128", q_lens=[1], past_lens=[past], block_size=16, num_heads=2, drop_slots=0))
+
+
+@pytest.mark.parametrize("q,past", [(2, 0), (31, 0), (32, 1), (33, 95), (64, 64), (127, 1), (128, 0), (129, 127), (300, 20)])
+def test_prefill_lengths(q, past):
+    check(workload("64_128", q_lens=[q], past_lens=[past], block_size=16, num_heads=2, drop_slots=0))
+
+
+def test_long_split_decode():
+    """One long sequence beside short ones: split over many CTAs and joined."""
+    check(workload("64_128", q_lens=[1, 1, 1], past_lens=[9000, 17, 300], num_heads=4, drop_slots=0))
+
+
+def test_many_sequences():
+    rng = np.random.default_rng(0)
+    check(workload("64_128", q_lens=[1] * 90, past_lens=[int(x) for x in rng.integers(0, 400, 90)], num_heads=2,
+                   kv_num_heads=1, block_size=16))
+
+
+@pytest.mark.parametrize("kind", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("name", ["64_128", "window_7", "128_256"])
+def test_unseen_rows_may_hold_anything(kind, name):
+    """Rows after a sequence's end in its last page, rows before its window
+    and pages of nobody hold NaN or infinities: no output changes."""
+    w = workload(name, block_size=128, num_blocks=16, drop_slots=0)
+    _, want, _ = run_gpu(w)
+    t = w.tensors
+    seen = torch.zeros(t["key_cache"].shape[0] * 128, dtype=torch.bool)
+    for b, (q, p) in enumerate(zip(w.q_lens, w.past_lens)):
+        lo = max(0, p - w.local_window_size) if w.local_window_size >= 0 else 0
+        if q:
+            j = torch.arange(lo, p + q)
+            seen[(t["block_table"][b, j // 128] * 128 + j % 128).long()] = True
+    for k in ("key_cache", "value_cache"):
+        t[k].view(len(seen), -1)[~seen] = kind
+    _, got, op = run_gpu(w)
+    assert op.error_flags() == 0
+    assert torch.equal(got, want)
+
+
+def test_flags_and_range_calls():
+    """write + one read call per sequence range, with and without the
+    after-write flags: bit-equal rows, other rows untouched."""
+    w = workload("64_128", drop_slots=0)
+    d, want, op = run_gpu(w)
+    for after in (False, True):
+        out = torch.full_like(want, -7.0)
+        read = (d["query"], d["key_cache"], d["value_cache"], d["cos_cache"], d["sin_cache"],
+                d["lambda_vectors"], d["norm_weight"], d["cumseq"], d["past"], d["block_table"], out)
+        op.write(d["key"], d["value"], d["key_cache"], d["value_cache"], d["cos_cache"],
+                 d["sin_cache"], d["slot_mapping"], d["cumseq"], d["past"])
+        op.decode(*read, 0, 3, after_write=after)
+        assert torch.equal(out[:3], want[:3]) and (out[3:] == -7).all()
+        op.prefill(*read, 5, 6)
+        assert torch.equal(out[12:52], want[12:52]) and (out[3:12] == -7).all() and (out[52:] == -7).all()
+    assert op.error_flags() == 0
+
+
+def test_graph_replay_two_graphs_one_workspace():
+    """A decode step and a prefill step captured apart share one operator's
+    workspace; replayed in turn they repeat the eager results bit for bit."""
+    wd = workload("64_128", q_lens=[1] * 4, past_lens=[2000, 100, 0, 5], drop_slots=0)
+    wp = workload("64_128", q_lens=[70, 3], past_lens=[100, 5], drop_slots=0, num_blocks=wd.num_blocks,
+                  max_blocks_per_seq=wd.max_blocks_per_seq, cos_rows=wd.cos_rows)
+    op = DifferentialAttention(**wd.params, max_seqs=4, max_tokens=128)
+    dd, want_d, _ = run_gpu(wd, op=op)
+    dp, want_p, _ = run_gpu(wp, op=op)
+    outs, graphs = [], []
+    for d, want, n in ((dd, want_d, 4), (dp, want_p, 0)):
+        out = torch.zeros_like(want)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            op.forward(*_args(d), n, out=out)
+        outs.append(out)
+        graphs.append(g)
+    side = torch.cuda.Stream()
+    for k in (0, 1, 1, 0, 0):
+        outs[k].fill_(3.0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graphs[k].replay()
+        side.synchronize()
+        assert torch.equal(outs[k], (want_d, want_p)[k])
+
+
+@pytest.mark.parametrize("what", ["block", "context", "past", "position", "qlen", "slot"])
+def test_bad_indices(what):
+    """Bad pages, lengths, positions and slots set their flag; the rows of
+    that sequence become zeros (or stay, for a wrong q_len), the others are
+    as if it were not there."""
+    w = workload("64_128", q_lens=[1, 1, 20, 30], past_lens=[100, 200, 10, 50], drop_slots=0)
+    _, want, _ = run_gpu(w)
+    t = w.tensors
+    if what == "block":
+        t["block_table"][1, 2] = 10 ** 6
+        t["block_table"][3, 0] = -1
+        flag, zero = B.PA_DEVERR_BLOCK, [1, 3]
+    elif what == "context":
+        t["past"][1] = 10 ** 6
+        t["past"][3] = w.max_blocks_per_seq * 64 - 10
+        flag, zero = B.PA_DEVERR_CONTEXT, [1, 3]
+    elif what == "past":
+        t["past"][1], t["past"][3] = -5, -40
+        flag, zero = B.PA_DEVERR_CONTEXT, [1, 3]
+    elif what == "position":
+        w.params["cos_rows"] = 150
+        flag, zero = B.PA_DEVERR_POSITION, [1]
+    elif what == "qlen":
+        flag, zero = B.PA_DEVERR_DECODE_QLEN, []
+    else:
+        t["slot_mapping"][0], t["slot_mapping"][5] = 10 ** 8, -2
+        flag, zero = B.PA_DEVERR_SLOT, []
+    op = _op(w, own_slots=False)
+    _, got, _ = run_gpu(w, op=op, decodes=3 if what == "qlen" else None)
+    assert op.error_flags() & flag, hex(op.error_flags())
+    assert op.error_flags() & ~(flag | B.PA_DEVERR_CONTEXT | B.PA_DEVERR_POSITION) == 0
+    cum = t["cumseq"].tolist()
+    for b in range(4):
+        rows = got[cum[b]:cum[b + 1]]
+        if b in zero:
+            assert (rows == 0).all() or (what in ("context", "past") and b == 3), b
+            if b == 3:
+                assert torch.isfinite(rows.float()).all()
+        elif what == "qlen" and b == 2:
+            assert torch.isnan(rows.float()).all()
+        elif what != "slot":
+            assert torch.equal(rows, want[cum[b]:cum[b + 1]]), b
+
+
+def test_rows_behind_the_last_sequence_stay():
+    w = workload("64_128", q_lens=[1, 1, 20], past_lens=[100, 200, 10], drop_slots=0)
+    d = {k: v.cuda() for k, v in w.tensors.items()}
+    for k in ("query", "key", "value"):
+        d[k] = torch.cat([d[k], d[k][:9]])
+    d["slot_mapping"] = torch.cat([d["slot_mapping"], torch.full((9,), -1, dtype=torch.int32, device="cuda")])
+    op = DifferentialAttention(**w.params, max_seqs=3, max_tokens=64)
+    out = torch.full((31, w.num_heads * w.v_head_size), -7.0, dtype=w.dtype, device="cuda")
+    op.forward(*_args(d), 2, out=out)
+    _, want, _ = run_gpu(w)
+    assert torch.equal(out[:22], want) and (out[22:] == -7).all()
+
+
+def test_refuses_bad_tensors():
+    w = workload("64_128", q_lens=[1, 4], past_lens=[10, 3], drop_slots=0)
+    d, _, op = run_gpu(w)
+    for name, bad in [("query", d["query"].float()), ("key", d["key"][:, ::2]), ("value", d["value"].cpu()),
+                      ("cumseq", d["cumseq"].long()), ("past", d["past"][:1]), ("block_table", d["block_table"][:1]),
+                      ("lambda_vectors", d["lambda_vectors"].double()), ("norm_weight", d["norm_weight"][:64]),
+                      ("key_cache", d["key_cache"][:1]), ("cos_cache", d["cos_cache"][:2]),
+                      ("slot_mapping", d["slot_mapping"][:2])]:
+        e = dict(d)
+        e[name] = bad
+        with pytest.raises(B.PaError):
+            op.forward(*_args(e), 1)
+
+
+def test_serving_run_with_pages():
+    """Prompts, forks, tokens and a compaction through a PagePool over both
+    caches: forks answer as their parent, compaction changes no output bit."""
+    w = workload("64_128", q_lens=[37, 64, 5, 0, 0], past_lens=[0] * 5, block_size=16, num_blocks=64,
+                 max_blocks_per_seq=8, cos_rows=128, drop_slots=0)
+    d = {k: v.cuda() for k, v in w.tensors.items()}
+    pool = PagePool([d["key_cache"], d["value_cache"]], block_size=16, max_seqs=5, max_blocks_per_seq=8)
+    op = _op(w)
+    i32 = lambda v: torch.tensor(list(v), dtype=torch.int32, device="cuda")
+
+    def step(q_lens, q, k, v, decodes):
+        cum = i32([0] + list(np.cumsum(q_lens)))
+        slots = pool.reserve(cum, torch.empty(sum(q_lens), dtype=torch.int32, device="cuda"))
+        out = op.forward(q, k, v, d["key_cache"], d["value_cache"], d["cos_cache"], d["sin_cache"],
+                         d["lambda_vectors"], d["norm_weight"], cum, pool.past, pool.block_table,
+                         slots, decodes)
+        pool.past += cum[1:] - cum[:-1]
+        return out
+
+    first = step(w.q_lens, d["query"], d["key"], d["value"], 0)
+    _, want, _ = run_gpu(w)
+    assert torch.equal(first, want)  # the same batch on other pages
+    pool.free(i32([1]))
+    pool.fork(i32([0, 0, 2]), i32([1, 3, 4]))
+    pick = [0, 0, 1, 0, 1]
+    out = step([1] * 5, d["query"][pick].contiguous(), d["key"][pick].contiguous(),
+               d["value"][pick].contiguous(), 5)
+    assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[3]) and torch.equal(out[2], out[4])
+
+    def read():
+        o = torch.zeros_like(out)
+        op.decode(d["query"][pick].contiguous(), d["key_cache"], d["value_cache"], d["cos_cache"],
+                  d["sin_cache"], d["lambda_vectors"], d["norm_weight"], i32(range(6)),
+                  pool.past - 1, pool.block_table, o)
+        return o
+
+    before = read()
+    assert torch.equal(before, out)
+    pool.free(i32([0, 2]))
+    pool.compact()
+    after = read()
+    assert torch.equal(before[[1, 3, 4]], after[[1, 3, 4]])
+    assert pool.error_flags() == 0
