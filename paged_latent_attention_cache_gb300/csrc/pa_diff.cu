@@ -165,7 +165,13 @@ pa_status read(Phase ph, const pa_diff_params* p, DiffArgs a) {
     return fail(PA_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
   a.lambda_init = p->lambda_init;
   a.norm_eps = p->norm_eps;
-  const cudaError_t e = launch_simple(g, ph, a);
+  if (ph == Phase::kDecode) {
+    const size_t need = decode_workspace(g, a.seq_end - a.seq_begin);
+    if (!a.workspace || a.workspace_bytes < need)
+      return fail(PA_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu needed",
+                  a.workspace ? a.workspace_bytes : (size_t)0, need);
+  }
+  const cudaError_t e = ph == Phase::kDecode ? launch_decode(g, a) : launch_simple(g, a);
   if (e != cudaSuccess)
     return fail(PA_ERR_CUDA, "differential attention launch: %s", cudaGetErrorString(e));
   return PA_OK;
@@ -260,7 +266,7 @@ pa_status pa_diff_prefill(const pa_diff_params* p, const void* query, int64_t nu
 size_t pa_diff_workspace_size(const pa_diff_params* p, int32_t num_seqs, int64_t num_tokens) {
   Geometry g;
   if (diff::resolve(p, &g) != PA_OK || num_seqs <= 0 || num_tokens <= 0) return 0;
-  return 0;
+  return diff::decode_workspace(g, num_seqs);
 }
 
 }  // extern "C"

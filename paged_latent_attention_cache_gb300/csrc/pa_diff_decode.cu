@@ -1,0 +1,769 @@
+// Differential attention, decode: one new token per sequence (include/pa_diff.h).
+//
+// Bound by HBM: each visible key of a kv head is read once (2 hs + vhs
+// channels, 512 bytes at 64 / 128) for 2 * (hs + vhs) * 2 multiply-adds per
+// head. The work is cut for that:
+//
+// * A tile is 16 keys of one (sequence, kv head, chunk of 8 heads): 16 rows of
+//   one page. Up to 8 heads share a tile's bytes. The rows of an mma.sync
+//   m16n8k16 are the 8 heads with map 0 (rows 0-7) and map 1 (rows 8-15), so
+//   both maps share one product with V; a tcgen05 tile (128 rows) would be
+//   filled to an eighth at most and its tensor memory round trip is longer
+//   than a tile's work.
+// * All tiles of the call, in the order (sequence, kv head and chunk, tile),
+//   form one line that is cut into equal parts, one per CTA, whatever the
+//   lengths; a part may start and end inside a sequence. Parts are joined by
+//   the combine kernel below, as are all results (one code path).
+// * Each warp copies its own tiles (every fourth of the CTA's part) with
+//   cp.async into a ring of its own and waits for nobody but itself: no
+//   barrier inside a part, and copies run ahead across sequences. Bytes in
+//   flight per SM are (stages - 1) * warps * 8 or 16 KB, over 64 KB, which
+//   the latency-bandwidth product (45 GB/s per SM * 1 us) asks for.
+// * Rows that no query sees are filled with zeros instead of being read, so
+//   what they hold cannot reach a sum.
+//
+// Precision: out = softmax_0 V - lambda softmax_1 V cancels, so errors of the
+// two maps weigh more than in a plain softmax. The rotated query and the
+// probabilities enter the products as two 16-bit parts each (value and
+// remainder, 2^-16 relative in bf16), which doubles the products; they stay
+// hidden behind the copies.
+#include <cmath>
+#include <type_traits>
+
+#include "pa_diff_internal.h"
+#include "pa_tc_common.cuh"
+
+namespace pa {
+namespace diff {
+namespace {
+
+using tc::ex2;
+using tc::grid_dep_launch;
+using tc::grid_dep_wait;
+using tc::pack2;
+using tc::smem_u32;
+
+constexpr int kWarps = 4;
+constexpr int kTileKeys = 16;
+constexpr int kHeads = 8;        // heads of a chunk
+constexpr int kRows = 2 * kHeads;
+constexpr int kMinTiles = 2 * kWarps;  // least part of a CTA (two tiles per warp)
+constexpr float kLazy = 8.f;     // a running maximum may lag by 2^8
+
+struct Args {
+  Geometry g;
+  DiffArgs a;
+  int grp, chunks, ng;  // heads per kv head, chunks of 8 of them, kvh * chunks
+  int pitch_k, pitch_v, stage, stages;
+  int slots;            // partials the workspace holds
+  float scale_log2, cap_in, cap_out;
+  float* ws_o;          // [slots][16][vhs]
+  float2* ws_ml;        // [slots][16] (log2-domain maximum, sum)
+  int64_t* ws_plan;     // [nseq] tiles before the sequence, then total tiles, CTAs in use
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// A pair of values as 16-bit parts: hi rounded, lo the rounded remainder.
+template <typename T>
+__device__ __forceinline__ void split2(float x, float y, uint32_t* hi, uint32_t* lo) {
+  const T hx = Half<T>::from_f32(x), hy = Half<T>::from_f32(y);
+  *hi = pack2<T>(x, y);
+  *lo = pack2<T>(x - Half<T>::to_f32(hx), y - Half<T>::to_f32(hy));
+}
+
+// Visible keys of decode sequence b: status 0 = [lo, pos]; 1 = not one new
+// token (its rows stay); 2 = positions or offsets out of range (zeros).
+struct Seq {
+  int64_t t, lo, pos;
+  int status, err;
+};
+__device__ __forceinline__ Seq seq_of(const Args& A, int b) {
+  const int32_t q0 = A.a.cumseq[b], q1 = A.a.cumseq[b + 1];
+  Seq s;
+  s.pos = A.a.past[b];
+  s.t = q0;
+  s.status = s.err = 0;
+  if (q1 - q0 != 1) {
+    s.status = 1;
+    s.err = PA_DEVERR_DECODE_QLEN;
+  } else if (q0 < 0 || q0 >= A.a.num_tokens) {
+    s.status = 1;
+    s.err = PA_DEVERR_CUMSEQ;
+  } else if (s.pos < 0 || s.pos >= (int64_t)A.g.max_blocks * A.g.bs) {
+    s.status = 2;
+    s.err = PA_DEVERR_CONTEXT;
+  } else if (A.g.rd > 0 && s.pos >= A.g.cos_rows) {
+    s.status = 2;
+    s.err = PA_DEVERR_POSITION;
+  }
+  s.lo = A.g.window >= 0 ? max((int64_t)0, s.pos - A.g.window) : 0;
+  return s;
+}
+__device__ __forceinline__ int tiles_of(const Args& A, int b) {
+  const Seq s = seq_of(A, b);
+  return s.status ? 0 : (int)(s.pos / kTileKeys - s.lo / kTileKeys) + 1;
+}
+
+// One warp: total tiles of the call's line, and (first, before) of the
+// sequence that holds its tile x (the tiles of the sequences before it).
+__device__ int64_t line_total(const Args& A, int nseq, int lane) {
+  int64_t sum = 0;
+  for (int i = lane; i < nseq; i += 32) sum += tiles_of(A, A.a.seq_begin + i);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum * A.ng;
+}
+// With `plan`, also stores every sequence's prefix.
+__device__ void line_find(const Args& A, int nseq, int lane, int64_t x, int* seq, int64_t* before,
+                          int64_t* plan) {
+  int64_t run = 0;
+  bool found = false;
+  for (int i0 = 0; i0 < nseq; i0 += 32) {
+    const int i = i0 + lane;
+    const int64_t n = i < nseq ? (int64_t)tiles_of(A, A.a.seq_begin + i) * A.ng : 0;
+    int64_t incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const int64_t start = run + incl - n;
+    if (plan && i < nseq) plan[i] = start;
+    const unsigned who = __ballot_sync(0xffffffffu, x >= start && x < start + n);
+    if (who && !found) {
+      const int src = __ffs(who) - 1;
+      *seq = i0 + src;
+      *before = __shfl_sync(0xffffffffu, start, src);
+      found = true;
+      if (!plan) return;
+    }
+    run += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+// A place on the line: sequence index, (kv head, chunk), tile, and the
+// sequence's range.
+struct Cursor {
+  int seq, gc, tile, tiles;
+  int64_t lo, pos;
+};
+__device__ __forceinline__ void cursor_load(const Args& A, Cursor& c) {
+  const Seq s = seq_of(A, A.a.seq_begin + c.seq);
+  c.lo = s.lo;
+  c.pos = s.pos;
+  c.tiles = s.status ? 0 : (int)(s.pos / kTileKeys - s.lo / kTileKeys) + 1;
+}
+// `step` tiles on, over the ends of (kv head, chunk)s and sequences.
+__device__ __forceinline__ void cursor_step(const Args& A, Cursor& c, int step, int nseq) {
+  c.tile += step;
+  while (c.tile >= c.tiles) {
+    c.tile -= c.tiles;
+    if (++c.gc == A.ng || c.tiles == 0) {
+      c.gc = 0;
+      if (++c.seq >= nseq) return;
+      cursor_load(A, c);
+    }
+  }
+}
+
+// KS >= hs / 16, VT >= vhs / 8 fix the register arrays.
+template <typename T, int KS, int VT>
+__global__ void __launch_bounds__(kWarps * 32, VT > 16 ? 1 : 2)
+diff_decode_kernel(const __grid_constant__ Args A) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int s_seq;
+  __shared__ int64_t s_before, s_total;
+  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+  __shared__ int s_bad[kWarps];
+  const Geometry& g = A.g;
+  const DiffArgs& a = A.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nseq = a.seq_end - a.seq_begin;
+  const int hs = g.hs, vhs = g.vhs, nks = hs >> 4, nvt = vhs >> 3;
+  const int sh = __ffs(g.bs) - 1;
+  const bool early = (g.flags & PA_FLAG_AFTER_WRITE) != 0;
+  bool waited = !early;
+  if (!early) grid_dep_wait();
+  grid_dep_launch();
+
+  // ---- this CTA's part of the line
+  if (warp == 0) {
+    const int64_t total = line_total(A, nseq, lane);
+    const int64_t ctas = min((int64_t)gridDim.x, max((int64_t)1, total / kMinTiles));
+    int seq = 0;
+    int64_t before = 0;
+    int64_t* plan = blockIdx.x == 0 ? A.ws_plan : nullptr;
+    const int64_t x0 = blockIdx.x < ctas ? (int64_t)blockIdx.x * total / ctas : total;
+    if (blockIdx.x < ctas) line_find(A, nseq, lane, x0, &seq, &before, plan);
+    if (lane == 0) {
+      s_seq = seq;
+      s_before = before;
+      s_total = total;
+      if (plan) {
+        plan[nseq] = total;
+        plan[nseq + 1] = ctas;
+      }
+    }
+  }
+  __syncthreads();
+  const int64_t total = s_total;
+  const int64_t ctas = min((int64_t)gridDim.x, max((int64_t)1, total / kMinTiles));
+  if (blockIdx.x >= ctas || total == 0) {
+    if (!waited) grid_dep_wait();
+    return;
+  }
+  const int64_t x0 = (int64_t)blockIdx.x * total / ctas, x1 = ((int64_t)blockIdx.x + 1) * total / ctas;
+  const int count = (int)(x1 - x0);  // tiles of this CTA
+  Cursor first;
+  first.seq = s_seq;
+  cursor_load(A, first);
+  {
+    const int64_t off = x0 - s_before;
+    first.gc = (int)(off / first.tiles);
+    first.tile = (int)(off - (int64_t)first.gc * first.tiles);
+  }
+
+  uint8_t* ring = smem + (size_t)warp * A.stages * A.stage;
+  const uint32_t ring_u = smem_u32(ring);
+  uint4* q_hi = reinterpret_cast<uint4*>(smem + (size_t)kWarps * A.stages * A.stage);
+  uint4* q_lo = q_hi + KS * 32;
+  float* merge = reinterpret_cast<float*>(q_lo + KS * 32);
+  const int mpitch = VT * 8 + 8;
+
+  // ---- copies: this warp's tiles are x0 + warp, x0 + warp + 4, ...
+  const int mine = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;
+  Cursor lc = first;
+  uint32_t bad_stages = 0;  // bit s: the tile in stage s has no valid page
+  int issued = 0;
+  if (mine > 0 && warp > 0) cursor_step(A, lc, warp, nseq);
+  auto page_of = [&](const Cursor& c) {
+    const int64_t key0 = (c.lo / kTileKeys + c.tile) * kTileKeys;
+    return a.block_table[(int64_t)(a.seq_begin + c.seq) * g.max_blocks + (key0 >> sh)];
+  };
+  int next_page = mine > 0 ? page_of(lc) : 0;
+  auto issue = [&]() {
+    if (issued < mine) {
+      const int st = issued % A.stages;
+      const int64_t key0 = (lc.lo / kTileKeys + lc.tile) * kTileKeys;
+      if (!waited && (!(g.flags & PA_FLAG_OWN_SLOTS) || key0 + kTileKeys > lc.pos)) {
+        grid_dep_wait();  // from here on rows the write phase may store are read
+        waited = true;
+      }
+      const int page = next_page;
+      const bool ok = page >= 0 && page < g.num_blocks;
+      if (ok) {
+        bad_stages &= ~(1u << st);
+      } else {
+        bad_stages |= 1u << st;
+        if (lane == 0) raise_flag(a.err_flags, PA_DEVERR_BLOCK);
+      }
+      const int gk = lc.gc / A.chunks;
+      const int64_t row0 = ok ? (int64_t)page * g.bs + (key0 & (g.bs - 1)) : 0;
+      const int64_t kstr = (int64_t)g.kvh * 2 * hs, vstr = (int64_t)g.kvh * vhs;
+      const T* kp = (const T*)a.key_cache + row0 * kstr + (int64_t)gk * 2 * hs;
+      const T* vp = (const T*)a.value_cache + row0 * vstr + (int64_t)gk * vhs;
+      const uint32_t kd = ring_u + st * A.stage, vd = kd + kTileKeys * A.pitch_k;
+      const int c = lane & 7;
+      const int ck = hs >> 2;  // 16-byte chunks of a key row
+#pragma unroll
+      for (int rb = 0; rb < 4; ++rb) {  // 4 rows x 128 bytes per instruction
+        const int r = rb * 4 + (lane >> 3);
+        const bool on = ok && key0 + r >= lc.lo && key0 + r <= lc.pos;
+        const T* kr = kp + r * kstr;
+        const T* vr = vp + r * vstr;
+        const uint32_t sw = (uint32_t)((c ^ (r & 7)) << 4);
+#pragma unroll
+        for (int cb = 0; cb < KS / 2; ++cb)
+          if (cb * 8 + c < ck) cp16(kd + r * A.pitch_k + cb * 128 + sw, kr + (cb * 8 + c) * 8, on);
+#pragma unroll
+        for (int cb = 0; cb < VT / 8; ++cb)
+          if (cb * 8 + c < nvt) cp16(vd + r * A.pitch_v + cb * 128 + sw, vr + (cb * 8 + c) * 8, on);
+      }
+      ++issued;
+      if (issued < mine) {
+        cursor_step(A, lc, kWarps, nseq);
+        next_page = page_of(lc);
+      }
+    }
+    cp_commit();
+  };
+  for (int s = 0; s < A.stages - 1; ++s) issue();
+
+  // ---- the (sequence, kv head, chunk)s of the part, one after another
+  int done = 0;     // tiles of this warp already folded
+  int at = 0;       // tiles of the CTA before the current segment
+  Cursor cur = first;
+  while (at < count) {
+    const int seg = min(cur.tiles - cur.tile, count - at);  // tiles of this segment
+    const int b = a.seq_begin + cur.seq, gk = cur.gc / A.chunks;
+    const int h0 = gk * A.grp + (cur.gc - gk * A.chunks) * kHeads;
+    const int nh = min(kHeads, A.grp - (cur.gc - gk * A.chunks) * kHeads);
+    // the query rows (rows 0-7 map 0, rows 8-15 map 1), rotated, in the order
+    // of the A fragments: [k step][lane] of the four registers
+    {
+      const int64_t t = a.cumseq[b];
+      for (int i = tid; i < kRows * (hs >> 3); i += kWarps * 32) {
+        const int r = i & 15, d0 = (i >> 4) * 8, m = r >> 3, hh = r & 7;
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (hh < nh) {
+          const T* row = (const T*)a.query + ((t * g.H + h0 + hh) * 2 + m) * (int64_t)hs;
+          unpack8<T>(*reinterpret_cast<const uint4*>(row + d0), x);
+          if (g.rd > 0 && d0 >= g.ro && d0 < g.ro + g.rd) {
+            const int half = g.rd >> 1;
+            const int dp = g.interleaved ? d0 : d0 - g.ro < half ? d0 + half : d0 - half;
+            float xp[8];
+            unpack8<T>(*reinterpret_cast<const uint4*>(row + dp), xp);
+            rope8<T>(x, xp, d0, g.ro, g.rd, g.interleaved, (const T*)a.cos_cache + cur.pos * half,
+                     (const T*)a.sin_cache + cur.pos * half);
+          }
+        }
+        const int reg = (d0 & 8 ? 2 : 0) + m;
+        uint32_t* hi = reinterpret_cast<uint32_t*>(q_hi + (d0 >> 4) * 32 + hh * 4) + reg;
+        uint32_t* lo = reinterpret_cast<uint32_t*>(q_lo + (d0 >> 4) * 32 + hh * 4) + reg;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split2<T>(x[2 * e], x[2 * e + 1], hi + 4 * e, lo + 4 * e);
+      }
+      __syncthreads();
+    }
+
+    float o[VT][4];
+#pragma unroll
+    for (int i = 0; i < VT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+    float mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    bool bad = false;
+    // this warp's tiles of the segment: CTA tile numbers warp + 4 done in [at, at + seg)
+    for (int n = warp + done * kWarps; n < at + seg; n += kWarps, ++done) {
+      issue();
+      // all but the newest stages - 1 groups have landed
+      if (A.stages == 3) cp_wait<2>();
+      else if (A.stages == 4) cp_wait<3>();
+      else if (A.stages == 5) cp_wait<4>();
+      else cp_wait<5>();
+      __syncwarp();
+      const int st = done % A.stages;
+      bad |= (bad_stages >> st) & 1u;
+      const uint32_t kb = ring_u + st * A.stage, vb = kb + kTileKeys * A.pitch_k;
+
+      // scores: s[map][8-key half]; the other map's rows of A are zero
+      float s[2][2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[i][j][e] = 0.f;
+      {
+        // ldmatrix rows: lanes 0-7 keys 0-7 chunk 0, 8-15 keys 0-7 chunk 1,
+        // 16-23 keys 8-15 chunk 0, 24-31 keys 8-15 chunk 1
+        const int r = (lane & 7) + ((lane >> 4) << 3), hc = (lane >> 3) & 1;
+        const uint32_t rowb = kb + r * A.pitch_k;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          if (ks < nks) {
+            const uint4 qh = q_hi[ks * 32 + lane], ql = q_lo[ks * 32 + lane];
+            uint32_t k0[4], k1[4];
+            const int c0 = ks * 2 + hc, c1 = c0 + (hs >> 3);
+            ldsm4(k0, rowb + ((c0 & ~7) << 4) + (((c0 & 7) ^ (r & 7)) << 4));
+            ldsm4(k1, rowb + ((c1 & ~7) << 4) + (((c1 & 7) ^ (r & 7)) << 4));
+            mma<T>(s[0][0], qh.x, 0u, qh.z, 0u, k0[0], k0[1]);
+            mma<T>(s[0][1], qh.x, 0u, qh.z, 0u, k0[2], k0[3]);
+            mma<T>(s[1][0], 0u, qh.y, 0u, qh.w, k1[0], k1[1]);
+            mma<T>(s[1][1], 0u, qh.y, 0u, qh.w, k1[2], k1[3]);
+            mma<T>(s[0][0], ql.x, 0u, ql.z, 0u, k0[0], k0[1]);
+            mma<T>(s[0][1], ql.x, 0u, ql.z, 0u, k0[2], k0[3]);
+            mma<T>(s[1][0], 0u, ql.y, 0u, ql.w, k1[0], k1[1]);
+            mma<T>(s[1][1], 0u, ql.y, 0u, ql.w, k1[2], k1[3]);
+          }
+        }
+      }
+      // v[map][8-key half][key of the pair], log2 domain
+      float v[2][2][2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        v[0][j][0] = s[0][j][0];
+        v[0][j][1] = s[0][j][1];
+        v[1][j][0] = s[1][j][2];
+        v[1][j][1] = s[1][j][3];
+      }
+      if (A.cap_out > 0.f) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) v[i][j][e] = A.cap_out * tc::tanh_ex2(v[i][j][e] * A.cap_in);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) v[i][j][e] *= A.scale_log2;
+      }
+      const int64_t key0 = (cur.lo / kTileKeys + cur.tile + (n - at)) * kTileKeys;
+      if (key0 < cur.lo || key0 + kTileKeys - 1 > cur.pos) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int64_t key = key0 + j * 8 + (lane & 3) * 2 + e;
+            if (key < cur.lo || key > cur.pos) v[0][j][e] = v[1][j][e] = -INFINITY;
+          }
+      }
+      // running maxima (each head's row is held by four lanes)
+      float f[2] = {1.f, 1.f};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float t = fmaxf(fmaxf(v[i][0][0], v[i][0][1]), fmaxf(v[i][1][0], v[i][1][1]));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+        if (t > mx[i] + kLazy || mx[i] == -INFINITY) {
+          f[i] = mx[i] == -INFINITY ? 0.f : ex2(mx[i] - t);
+          mx[i] = t;
+          l[i] *= f[i];
+        }
+      }
+      if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+        for (int c = 0; c < VT; ++c) {
+          o[c][0] *= f[0];
+          o[c][1] *= f[0];
+          o[c][2] *= f[1];
+          o[c][3] *= f[1];
+        }
+      }
+      uint32_t ph[4], pl[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float mu = mx[i] == -INFINITY ? 0.f : mx[i];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float p0 = ex2(v[i][j][0] - mu), p1 = ex2(v[i][j][1] - mu);
+          l[i] += p0 + p1;
+          split2<T>(p0, p1, &ph[j * 2 + i], &pl[j * 2 + i]);
+        }
+      }
+      // o += P V: 16 keys are the K of one step; two 8-channel tiles a load
+      {
+        const int r = (lane & 7) + (((lane >> 3) & 1) << 3), hc = lane >> 4;
+        const uint32_t rowb = vb + r * A.pitch_v;
+#pragma unroll
+        for (int c = 0; c < VT; c += 2) {
+          if (c < nvt) {
+            uint32_t w[4];
+            const int ch = c + hc;
+            ldsm4_t(w, rowb + ((ch & ~7) << 4) + (((ch & 7) ^ (r & 7)) << 4));
+            mma<T>(o[c], ph[0], ph[1], ph[2], ph[3], w[0], w[1]);
+            mma<T>(o[c + 1], ph[0], ph[1], ph[2], ph[3], w[2], w[3]);
+            mma<T>(o[c], pl[0], pl[1], pl[2], pl[3], w[0], w[1]);
+            mma<T>(o[c + 1], pl[0], pl[1], pl[2], pl[3], w[2], w[3]);
+          }
+        }
+      }
+      __syncwarp();  // the stage may be overwritten by the next issue()
+    }
+
+    // ---- the four warps' results, joined in the order of the warps
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      if ((lane & 3) == 0) {
+        s_m[warp][i * 8 + (lane >> 2)] = mx[i];
+        s_l[warp][i * 8 + (lane >> 2)] = l[i];
+      }
+    }
+    if (lane == 0) s_bad[warp] = bad ? 1 : 0;
+    __syncthreads();
+    const int64_t pair = (int64_t)cur.seq * A.ng + cur.gc;
+    const int64_t slot = (int64_t)blockIdx.x + pair;
+    float w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = i * 8 + (lane >> 2);
+      float M = s_m[0][r];
+#pragma unroll
+      for (int k = 1; k < kWarps; ++k) M = fmaxf(M, s_m[k][r]);
+      w[i] = mx[i] == -INFINITY ? 0.f : ex2(mx[i] - M);
+      if (warp == kWarps - 1 && (lane & 3) == 0) {
+        float L = 0.f;
+        bool any = false;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+          L += s_m[k][r] == -INFINITY ? 0.f : ex2(s_m[k][r] - M) * s_l[k][r];
+          any |= s_bad[k] != 0;
+        }
+        A.ws_ml[slot * kRows + r] = make_float2(any ? __int_as_float(0x7fc00000) : M, L);
+      }
+    }
+    for (int k = 0; k < kWarps; ++k) {
+      if (warp == k) {
+        const int c = (lane & 3) * 2;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float* row = merge + (i * 8 + (lane >> 2)) * mpitch + c;
+          float* dst = A.ws_o + (slot * kRows + i * 8 + (lane >> 2)) * (int64_t)vhs + c;
+#pragma unroll
+          for (int n = 0; n < VT; ++n) {
+            if (n < nvt) {
+              float2 x = make_float2(o[n][2 * i] * w[i], o[n][2 * i + 1] * w[i]);
+              if (k > 0) {
+                const float2 y = *reinterpret_cast<const float2*>(row + n * 8);
+                x.x += y.x;
+                x.y += y.y;
+              }
+              if (k < kWarps - 1) *reinterpret_cast<float2*>(row + n * 8) = x;
+              else if ((lane >> 2) < nh) *reinterpret_cast<float2*>(dst + n * 8) = x;
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+    at += seg;
+    cursor_step(A, cur, seg, nseq);
+  }
+  cp_wait<0>();
+  if (!waited) grid_dep_wait();
+}
+
+// Joins the parts of each (sequence, head), takes the difference of the two
+// maps and the norm. One CTA per (sequence, kv head, chunk), one warp per
+// head, lane = channels lane, lane + 32, ...; parts of one head lie in
+// consecutive slots. Latency bound: one round trip for the plan, one per four
+// parts.
+template <typename T>
+__global__ void __launch_bounds__(kHeads * 32) diff_combine_kernel(const __grid_constant__ Args A) {
+  const Geometry& g = A.g;
+  const DiffArgs& a = A.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nseq = a.seq_end - a.seq_begin;
+  const int x = blockIdx.x, gc = blockIdx.y;
+  const int gk = gc / A.chunks, first = (gc - gk * A.chunks) * kHeads;
+  const int hs = g.hs, vhs = g.vhs;
+  // weights: older than the attention kernel
+  float d0 = 0.f, d1 = 0.f;
+  const float* lv = a.lambda_vectors;
+  for (int d = lane; d < hs; d += 32) {
+    d0 = fmaf(lv[d], lv[hs + d], d0);
+    d1 = fmaf(lv[2 * hs + d], lv[3 * hs + d], d1);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    d0 += __shfl_xor_sync(0xffffffffu, d0, o);
+    d1 += __shfl_xor_sync(0xffffffffu, d1, o);
+  }
+  const float lam = expf(d0) - expf(d1) + a.lambda_init;
+  grid_dep_wait();
+  const Seq s = seq_of(A, a.seq_begin + x);
+  if (s.status && gc == 0 && threadIdx.x == 0) raise_flag(a.err_flags, s.err);
+  if (s.status == 1 || first + warp >= A.grp) return;
+  const int h = gk * A.grp + first + warp;
+  T* out = (T*)a.out + (s.t * g.H + h) * (int64_t)vhs;
+  if (s.status) {
+    for (int c = lane; c < vhs; c += 32) out[c] = Half<T>::from_f32(0.f);
+    return;
+  }
+  const int64_t total = A.ws_plan[nseq], ctas = A.ws_plan[nseq + 1];
+  const int64_t tiles = s.pos / kTileKeys - s.lo / kTileKeys + 1;
+  const int64_t t0 = A.ws_plan[x] + gc * tiles, t1 = t0 + tiles - 1;
+  // the CTA of line tile t: the last whose part starts at or before it
+  const int64_t c0 = ((t0 + 1) * ctas - 1) / total, c1 = ((t1 + 1) * ctas - 1) / total;
+  const int64_t slot0 = c0 + (int64_t)x * A.ng + gc;
+  const int parts = (int)(c1 - c0) + 1;
+  float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f}, o[2][8] = {};
+  bool bad = false;
+  for (int p0 = 0; p0 < parts; p0 += 4) {
+    float2 ml[2][4];
+    float v[2][4][8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        ml[i][k] = make_float2(-INFINITY, 0.f);
+        if (p0 + k < parts) {
+          const int64_t row = (slot0 + p0 + k) * kRows + i * 8 + warp;
+          ml[i][k] = A.ws_ml[row];
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (c * 32 + lane < vhs) v[i][k][c] = A.ws_o[row * vhs + c * 32 + lane];
+        }
+      }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float m = ml[i][k].x;
+        bad |= isnan(m);
+        if (ml[i][k].y > 0.f && !isnan(m)) {
+          if (m > M[i]) {
+            const float f = ex2(M[i] - m);
+            L[i] *= f;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) o[i][c] *= f;
+            M[i] = m;
+          }
+          const float w = ex2(m - M[i]);
+          L[i] += w * ml[i][k].y;
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (c * 32 + lane < vhs) o[i][c] = fmaf(w, v[i][k][c], o[i][c]);
+        }
+      }
+  }
+  const float i0 = 1.f / L[0], i1 = lam / L[1];
+  float r[8], ss = 0.f;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    r[c] = c * 32 + lane < vhs ? o[0][c] * i0 - o[1][c] * i1 : 0.f;
+    ss = fmaf(r[c], r[c], ss);
+  }
+#pragma unroll
+  for (int q = 16; q > 0; q >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, q);
+  const float inv = (1.f - a.lambda_init) / sqrtf(ss / (float)vhs + a.norm_eps);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const int ch = c * 32 + lane;
+    if (ch < vhs)
+      out[ch] = Half<T>::from_f32(
+          bad ? 0.f : r[c] * inv * Half<T>::to_f32(((const T*)a.norm_weight)[ch]));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+struct Plan {
+  int pitch_k, pitch_v, stage, stages, per_sm, ks, vt;
+  size_t smem;
+};
+
+Plan plan_of(const Geometry& g) {
+  Plan p;
+  p.ks = g.hs <= 64 ? 4 : 8;
+  p.vt = g.vhs <= 128 ? 16 : 32;
+  p.pitch_k = (4 * g.hs + 127) / 128 * 128;
+  p.pitch_v = (2 * g.vhs + 127) / 128 * 128;
+  p.stage = kTileKeys * (p.pitch_k + p.pitch_v);
+  const size_t fixed = (size_t)p.ks * 32 * 16 * 2 + (size_t)kRows * (p.vt * 8 + 8) * 4;
+  // two CTAs per SM where three stages each fit (and their registers do),
+  // else one with all of the shared memory
+  const size_t half = 112 * 1024, whole = 225 * 1024;
+  p.per_sm = p.vt == 16 && fixed + (size_t)kWarps * 3 * p.stage <= half ? 2 : 1;
+  const size_t room = p.per_sm == 2 ? half : whole;
+  int s = (int)((room - fixed) / ((size_t)kWarps * p.stage));
+  p.stages = s > 6 ? 6 : s;
+  p.smem = fixed + (size_t)kWarps * p.stages * p.stage;
+  return p;
+}
+
+struct Layout {
+  int ctas, chunks, ng;
+  int64_t slots;
+  size_t o, ml, bytes;
+};
+Layout layout_of(const Geometry& g, const Plan& p, int64_t nseq) {
+  Layout l;
+  l.chunks = (g.H / g.kvh + kHeads - 1) / kHeads;
+  l.ng = g.kvh * l.chunks;
+  l.ctas = g.num_sms * p.per_sm;
+  l.slots = l.ctas + nseq * l.ng;
+  l.o = ((size_t)l.slots * kRows * g.vhs * 4 + 255) & ~(size_t)255;
+  l.ml = ((size_t)l.slots * kRows * 8 + 255) & ~(size_t)255;
+  l.bytes = l.o + l.ml + (size_t)(nseq + 2) * 8;
+  return l;
+}
+
+template <typename T, int KS, int VT>
+cudaError_t launch(const Args& A, const Plan& p, int ctas, cudaStream_t stream) {
+  static std::atomic<bool> configured[64];
+  auto kern = diff_decode_kernel<T, KS, VT>;
+  cudaError_t e = once_per_device(configured, A.g.device, [&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
+  });
+  if (e == cudaSuccess)
+    e = tc::launch_pdl(kern, dim3((unsigned)ctas), dim3(kWarps * 32), p.smem, stream, A);
+  if (e != cudaSuccess) return e;
+  return tc::launch_pdl(diff_combine_kernel<T>,
+                        dim3((unsigned)(A.a.seq_end - A.a.seq_begin), (unsigned)A.ng),
+                        dim3(kHeads * 32), 0, stream, A);
+}
+
+}  // namespace
+
+size_t decode_workspace(const Geometry& g, int64_t nseq) {
+  return layout_of(g, plan_of(g), nseq).bytes;
+}
+
+cudaError_t launch_decode(const Geometry& g, const DiffArgs& a) {
+  const Plan p = plan_of(g);
+  const Layout l = layout_of(g, p, a.seq_end - a.seq_begin);
+  Args A{};
+  A.g = g;
+  A.a = a;
+  A.grp = g.H / g.kvh;
+  A.chunks = l.chunks;
+  A.ng = l.ng;
+  A.pitch_k = p.pitch_k;
+  A.pitch_v = p.pitch_v;
+  A.stage = p.stage;
+  A.stages = p.stages;
+  A.slots = (int)l.slots;
+  A.scale_log2 = g.scale * tc::kLog2e;
+  A.cap_in = g.softcap > 0.f ? g.scale / g.softcap : 0.f;
+  A.cap_out = g.softcap > 0.f ? g.softcap * tc::kLog2e : 0.f;
+  char* w = static_cast<char*>(a.workspace);
+  A.ws_o = reinterpret_cast<float*>(w);
+  A.ws_ml = reinterpret_cast<float2*>(w + l.o);
+  A.ws_plan = reinterpret_cast<int64_t*>(w + l.o + l.ml);
+  auto go = [&](auto* typed) -> cudaError_t {
+    using T = std::remove_pointer_t<decltype(typed)>;
+    if (p.ks == 4 && p.vt == 16) return launch<T, 4, 16>(A, p, l.ctas, a.stream);
+    if (p.ks == 4) return launch<T, 4, 32>(A, p, l.ctas, a.stream);
+    if (p.vt == 16) return launch<T, 8, 16>(A, p, l.ctas, a.stream);
+    return launch<T, 8, 32>(A, p, l.ctas, a.stream);
+  };
+  return g.dtype == PA_DTYPE_BF16 ? go((__nv_bfloat16*)nullptr) : go((__half*)nullptr);
+}
+
+}  // namespace diff
+}  // namespace pa

@@ -32,7 +32,10 @@ struct DiffArgs {
   float lambda_init, norm_eps;
 };
 
-cudaError_t launch_simple(const Geometry& g, Phase ph, const DiffArgs& a);
+// decode (pa_diff_decode.cu); workspace bytes for nseq sequences
+size_t decode_workspace(const Geometry& g, int64_t nseq);
+cudaError_t launch_decode(const Geometry& g, const DiffArgs& a);
+cudaError_t launch_simple(const Geometry& g, const DiffArgs& a);
 
 }  // namespace diff
 }  // namespace pa

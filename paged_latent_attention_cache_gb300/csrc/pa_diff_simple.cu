@@ -31,7 +31,7 @@ __device__ __forceinline__ float block_reduce(float v, bool is_max, float* red) 
 
 template <typename T>
 __global__ void __launch_bounds__(kTile)
-diff_simple_kernel(Geometry g, DiffArgs a, int decode) {
+diff_simple_kernel(Geometry g, DiffArgs a) {
   __shared__ float q[2][128], p[2][kTile], red[kTile / 32];
   __shared__ int32_t s_bad;
   const int tid = threadIdx.x, h = blockIdx.x % g.H;
@@ -39,20 +39,9 @@ diff_simple_kernel(Geometry g, DiffArgs a, int decode) {
   const int hs = g.hs, vhs = g.vhs, gk = h / (g.H / g.kvh);
   int64_t t = unit, pos = 0;
   int32_t b = 0;
-  if (decode) {
-    b = a.seq_begin + (int)unit;
-    t = a.cumseq[b];
-    if (a.cumseq[b + 1] - t != 1 || t < 0 || t >= a.num_tokens) {
-      if (tid == 0)
-        raise_flag(a.err_flags, a.cumseq[b + 1] - t != 1 ? PA_DEVERR_DECODE_QLEN : PA_DEVERR_CUMSEQ);
-      return;
-    }
-    pos = a.past[b];
-  } else {
-    if (!locate_token(t, a.cumseq, a.past, a.num_seqs, tid == 0 ? a.err_flags : nullptr, &b, &pos))
-      return;
-    if (b < a.seq_begin || b >= a.seq_end) return;
-  }
+  if (!locate_token(t, a.cumseq, a.past, a.num_seqs, tid == 0 ? a.err_flags : nullptr, &b, &pos))
+    return;
+  if (b < a.seq_begin || b >= a.seq_end) return;
   T* out = (T*)a.out + (t * g.H + h) * (int64_t)vhs;
   const bool bad_ctx = a.past[b] < 0 || pos >= (int64_t)g.max_blocks * g.bs;
   const bool bad_pos = g.rd > 0 && pos >= g.cos_rows;
@@ -158,14 +147,10 @@ diff_simple_kernel(Geometry g, DiffArgs a, int decode) {
 
 }  // namespace
 
-cudaError_t launch_simple(const Geometry& g, Phase ph, const DiffArgs& a) {
-  const int64_t units =
-      ph == Phase::kDecode ? (int64_t)(a.seq_end - a.seq_begin) : a.num_tokens;
-  const dim3 grid((unsigned)(units * g.H));
-  if (g.dtype == PA_DTYPE_BF16)
-    diff_simple_kernel<__nv_bfloat16><<<grid, kTile, 0, a.stream>>>(g, a, ph == Phase::kDecode);
-  else
-    diff_simple_kernel<__half><<<grid, kTile, 0, a.stream>>>(g, a, ph == Phase::kDecode);
+cudaError_t launch_simple(const Geometry& g, const DiffArgs& a) {
+  const dim3 grid((unsigned)(a.num_tokens * g.H));
+  if (g.dtype == PA_DTYPE_BF16) diff_simple_kernel<__nv_bfloat16><<<grid, kTile, 0, a.stream>>>(g, a);
+  else diff_simple_kernel<__half><<<grid, kTile, 0, a.stream>>>(g, a);
   return cudaGetLastError();
 }
 

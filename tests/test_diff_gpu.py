@@ -214,8 +214,10 @@ def test_graph_replay_two_graphs_one_workspace():
 @pytest.mark.parametrize("what", ["block", "context", "past", "position", "qlen", "slot"])
 def test_bad_indices(what):
     """Bad pages, lengths, positions and slots set their flag; the rows of
-    that sequence become zeros (or stay, for a wrong q_len), the others are
-    as if it were not there."""
+    that sequence become zeros (or stay, for a wrong q_len), the others do not
+    change: within one step of the dtype, 2 u |x|, as a decode is cut by the
+    lengths of the whole batch and so sums in another order, where the f32 sums
+    themselves differ by under 2^-20 of the largest output."""
     w = workload("64_128", q_lens=[1, 1, 20, 30], past_lens=[100, 200, 10, 50], drop_slots=0)
     _, want, _ = run_gpu(w)
     t = w.tensors
@@ -252,7 +254,9 @@ def test_bad_indices(what):
         elif what == "qlen" and b == 2:
             assert torch.isnan(rows.float()).all()
         elif what != "slot":
-            assert torch.equal(rows, want[cum[b]:cum[b + 1]]), b
+            x, y = rows.double(), want[cum[b]:cum[b + 1]].double()
+            step = 2 * UNIT_ROUNDOFF[w.dtype] * torch.maximum(x.abs(), y.abs())
+            assert ((x - y).abs() <= step + 2.0 ** -20 * y.abs().max()).all(), b
 
 
 def test_rows_behind_the_last_sequence_stay():
