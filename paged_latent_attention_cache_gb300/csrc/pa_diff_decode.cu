@@ -14,19 +14,26 @@
 //   form one line that is cut into equal parts, one per CTA, whatever the
 //   lengths; a part may start and end inside a sequence. Parts are joined by
 //   the combine kernel below, as are all results (one code path).
-// * Each warp copies its own tiles (every fourth of the CTA's part) with
-//   cp.async into a ring of its own and waits for nobody but itself: no
-//   barrier inside a part, and copies run ahead across sequences. Bytes in
-//   flight per SM are (stages - 1) * warps * 8 or 16 KB, over 64 KB, which
-//   the latency-bandwidth product (45 GB/s per SM * 1 us) asks for.
-// * Rows that no query sees are filled with zeros instead of being read, so
-//   what they hold cannot reach a sum.
+// * Tiles are copied by TMA boxes of 64 channels x 16 rows into a ring of up to
+//   24 stages. Tile i of a CTA's part goes to warp i % 8, which folds it into
+//   running sums of its own and then starts the copy of tile i + stages into
+//   the stage it has just read: no barrier inside a part, no producer, and
+//   copies run ahead across sequences. A tile takes a warp some 3000 cycles
+//   (dependent products, row maxima), so one warp per scheduler cannot keep up
+//   with 23 bytes per cycle and SM; a ring per warp leaves room for only four
+//   warps (1.3 times slower), and one producer warp cannot issue the eight
+//   boxes of a tile fast enough (1.6 times). The stages that no warp reads are
+//   the bytes in flight (45 GB/s per SM at 1 us ask for 45 KB).
+// * Value rows that no query sees are overwritten with zeros after the copy,
+//   scores of such keys with -inf, so what they hold cannot reach a sum.
 //
 // Precision: out = softmax_0 V - lambda softmax_1 V cancels, so errors of the
 // two maps weigh more than in a plain softmax. The rotated query and the
 // probabilities enter the products as two 16-bit parts each (value and
-// remainder, 2^-16 relative in bf16), which doubles the products; they stay
-// hidden behind the copies.
+// remainder, 2^-16 relative in bf16). For the scores that is free: a product
+// of one map has 8 rows for the heads' values and 8 for their remainders, and
+// both sums of a score end up in one lane. For the values it doubles the
+// products.
 #include <cmath>
 #include <type_traits>
 
@@ -43,18 +50,22 @@ using tc::grid_dep_wait;
 using tc::pack2;
 using tc::smem_u32;
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
 constexpr int kTileKeys = 16;
 constexpr int kHeads = 8;        // heads of a chunk
 constexpr int kRows = 2 * kHeads;
-constexpr int kMinTiles = 2 * kWarps;  // least part of a CTA (two tiles per warp)
+constexpr int kMaxStages = 24;
+constexpr size_t kSmem = 225 * 1024;  // dynamic shared memory of a CTA (one per SM)
+constexpr int kThreads = kWarps * 32;
+constexpr int kBufs = 2;         // buffers of the join at the end of a segment
+constexpr int kMinTiles = kWarps;  // least part of a CTA
 constexpr float kLazy = 8.f;     // a running maximum may lag by 2^8
 
 struct Args {
   Geometry g;
   DiffArgs a;
   int grp, chunks, ng;  // heads per kv head, chunks of 8 of them, kvh * chunks
-  int pitch_k, pitch_v, stage, stages;
+  int vslabs, stage, stages;  // 64-channel value slabs; bytes and number of ring stages
   int slots;            // partials the workspace holds
   float scale_log2, cap_in, cap_out;
   float* ws_o;          // [slots][16][vhs]
@@ -62,16 +73,6 @@ struct Args {
   int64_t* ws_plan;     // [nseq] tiles before the sequence, then total tiles, CTAs in use
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(on ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -106,6 +107,30 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t* hi, uint32_t*
   const T hx = Half<T>::from_f32(x), hy = Half<T>::from_f32(y);
   *hi = pack2<T>(x, y);
   *lo = pack2<T>(x - Half<T>::to_f32(hx), y - Half<T>::to_f32(hy));
+}
+
+// Waits until tile n has landed in its stage. The tiles of a stage go to
+// different warps, so a warp may come here before the tile before n in that
+// stage was even read, when the barrier's parity still says "complete" for the
+// phase before: first the copy of n has to have been started (`last`, set by
+// the warp that read the tile before). Bounded like wait_bar.
+__device__ __forceinline__ bool wait_tile(uint64_t* full, volatile int* last, int n, uint32_t parity,
+                                          volatile int* abort, int32_t* err) {
+  if (*last != n) {
+    const uint64_t t0 = tc::globaltimer();
+    for (uint32_t i = 1; *last != n; ++i) {
+      if ((i & 63u) == 0) {
+        if (*abort) return false;
+        if (tc::globaltimer() - t0 > tc::kWaitLimitNs) {
+          *abort = 1;
+          raise_flag(err, PA_DEVERR_TIMEOUT);
+          return false;
+        }
+      }
+    }
+    __threadfence_block();
+  }
+  return tc::wait_bar(smem_u32(full), parity, abort, err);
 }
 
 // Visible keys of decode sequence b: status 0 = [lo, pos]; 1 = not one new
@@ -203,20 +228,32 @@ __device__ __forceinline__ void cursor_step(const Args& A, Cursor& c, int step, 
   }
 }
 
-// KS >= hs / 16, VT >= vhs / 8 fix the register arrays.
+// A stage of the ring: 16-row slabs of 64 channels (128-byte swizzle), map 0's,
+// map 1's, then the value's. KS >= hs / 16 (4 or 8), VT >= vhs / 8 fix the
+// register arrays.
+constexpr int kSlab = kTileKeys * 128;
+
 template <typename T, int KS, int VT>
-__global__ void __launch_bounds__(kWarps * 32, VT > 16 ? 1 : 2)
-diff_decode_kernel(const __grid_constant__ Args A) {
-  extern __shared__ __align__(128) uint8_t smem[];
+__global__ void __launch_bounds__(kThreads, 1)
+diff_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                   const __grid_constant__ Args A) {
+  constexpr int KSL = KS / 4;  // slabs of a map
+  extern __shared__ uint8_t smem_raw[];
   __shared__ int s_seq;
   __shared__ int64_t s_before, s_total;
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   __shared__ int s_bad[kWarps];
+  __shared__ int s_abort;
+  __shared__ uint64_t s_full[kMaxStages];
+  __shared__ int s_stage_bad[kMaxStages];  // the tile in the stage has no valid page
+  __shared__ int s_last[kMaxStages];       // the last tile copied into it
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~(uintptr_t)1023);
   const Geometry& g = A.g;
   const DiffArgs& a = A.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nseq = a.seq_end - a.seq_begin;
-  const int hs = g.hs, vhs = g.vhs, nks = hs >> 4, nvt = vhs >> 3;
+  const int hs = g.hs, vhs = g.vhs, nvt = vhs >> 3, stages = A.stages;
   const int sh = __ffs(g.bs) - 1;
   const bool early = (g.flags & PA_FLAG_AFTER_WRITE) != 0;
   bool waited = !early;
@@ -242,6 +279,16 @@ diff_decode_kernel(const __grid_constant__ Args A) {
       }
     }
   }
+  if (warp == 1 && lane == 0) {
+    for (int s = 0; s < stages; ++s) {
+      tc::mbar_init(smem_u32(&s_full[s]), 1);
+      s_last[s] = -1;
+    }
+    s_abort = 0;
+    tc::fence_barrier_init();
+    tc::prefetch_tmap(&kmap);
+    tc::prefetch_tmap(&vmap);
+  }
   __syncthreads();
   const int64_t total = s_total;
   const int64_t ctas = min((int64_t)gridDim.x, max((int64_t)1, total / kMinTiles));
@@ -260,89 +307,93 @@ diff_decode_kernel(const __grid_constant__ Args A) {
     first.tile = (int)(off - (int64_t)first.gc * first.tiles);
   }
 
-  uint8_t* ring = smem + (size_t)warp * A.stages * A.stage;
-  const uint32_t ring_u = smem_u32(ring);
-  uint4* q_hi = reinterpret_cast<uint4*>(smem + (size_t)kWarps * A.stages * A.stage);
-  uint4* q_lo = q_hi + KS * 32;
-  float* merge = reinterpret_cast<float*>(q_lo + KS * 32);
-  const int mpitch = VT * 8 + 8;
+  const uint32_t ring = smem_u32(smem);
+  uint4* q_s = reinterpret_cast<uint4*>(smem + (size_t)stages * A.stage);
+  float* merge = reinterpret_cast<float*>(q_s + 2 * KS * 32);
+  constexpr int mpitch = VT * 8 + 8;
 
-  // ---- copies: this warp's tiles are x0 + warp, x0 + warp + 4, ...
-  const int mine = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;
+  // ---- copies: the warp's tiles below `stages` now, tile i + stages after i.
+  // The cursor stands at the next one, whose page id is loaded a tile ahead.
   Cursor lc = first;
-  uint32_t bad_stages = 0;  // bit s: the tile in stage s has no valid page
-  int issued = 0;
-  if (mine > 0 && warp > 0) cursor_step(A, lc, warp, nseq);
-  auto page_of = [&](const Cursor& c) {
-    const int64_t key0 = (c.lo / kTileKeys + c.tile) * kTileKeys;
-    return a.block_table[(int64_t)(a.seq_begin + c.seq) * g.max_blocks + (key0 >> sh)];
+  int next_tile = warp < stages ? warp : warp + stages;
+  auto page_of = [&]() {
+    const int key0 = (int)(lc.lo / kTileKeys + lc.tile) * kTileKeys;
+    return a.block_table[(int64_t)(a.seq_begin + lc.seq) * g.max_blocks + (key0 >> sh)];
   };
-  int next_page = mine > 0 ? page_of(lc) : 0;
-  auto issue = [&]() {
-    if (issued < mine) {
-      const int st = issued % A.stages;
-      const int64_t key0 = (lc.lo / kTileKeys + lc.tile) * kTileKeys;
-      if (!waited && (!(g.flags & PA_FLAG_OWN_SLOTS) || key0 + kTileKeys > lc.pos)) {
-        grid_dep_wait();  // from here on rows the write phase may store are read
-        waited = true;
-      }
-      const int page = next_page;
-      const bool ok = page >= 0 && page < g.num_blocks;
-      if (ok) {
-        bad_stages &= ~(1u << st);
-      } else {
-        bad_stages |= 1u << st;
-        if (lane == 0) raise_flag(a.err_flags, PA_DEVERR_BLOCK);
-      }
-      const int gk = lc.gc / A.chunks;
-      const int64_t row0 = ok ? (int64_t)page * g.bs + (key0 & (g.bs - 1)) : 0;
-      const int64_t kstr = (int64_t)g.kvh * 2 * hs, vstr = (int64_t)g.kvh * vhs;
-      const T* kp = (const T*)a.key_cache + row0 * kstr + (int64_t)gk * 2 * hs;
-      const T* vp = (const T*)a.value_cache + row0 * vstr + (int64_t)gk * vhs;
-      const uint32_t kd = ring_u + st * A.stage, vd = kd + kTileKeys * A.pitch_k;
-      const int c = lane & 7;
-      const int ck = hs >> 2;  // 16-byte chunks of a key row
-#pragma unroll
-      for (int rb = 0; rb < 4; ++rb) {  // 4 rows x 128 bytes per instruction
-        const int r = rb * 4 + (lane >> 3);
-        const bool on = ok && key0 + r >= lc.lo && key0 + r <= lc.pos;
-        const T* kr = kp + r * kstr;
-        const T* vr = vp + r * vstr;
-        const uint32_t sw = (uint32_t)((c ^ (r & 7)) << 4);
-#pragma unroll
-        for (int cb = 0; cb < KS / 2; ++cb)
-          if (cb * 8 + c < ck) cp16(kd + r * A.pitch_k + cb * 128 + sw, kr + (cb * 8 + c) * 8, on);
-#pragma unroll
-        for (int cb = 0; cb < VT / 8; ++cb)
-          if (cb * 8 + c < nvt) cp16(vd + r * A.pitch_v + cb * 128 + sw, vr + (cb * 8 + c) * 8, on);
-      }
-      ++issued;
-      if (issued < mine) {
-        cursor_step(A, lc, kWarps, nseq);
-        next_page = page_of(lc);
-      }
+  int next_page = 0;
+  if (next_tile < count) {
+    cursor_step(A, lc, next_tile, nseq);
+    next_page = page_of();
+  }
+  auto issue = [&](int stage) {
+    if (next_tile >= count) return;
+    const int key0 = (int)(lc.lo / kTileKeys + lc.tile) * kTileKeys;
+    if (!waited && (!(g.flags & PA_FLAG_OWN_SLOTS) || key0 + kTileKeys > lc.pos)) {
+      grid_dep_wait();  // from here on rows the write phase may store are read
+      waited = true;
     }
-    cp_commit();
+    if (lane == 0) {
+      const int gk = lc.gc / A.chunks;
+      int row = g.num_blocks * g.bs;  // out of range: the copy fills zeros
+      const bool ok = next_page >= 0 && next_page < g.num_blocks;
+      if (ok) row = next_page * g.bs + (key0 & (g.bs - 1));
+      else raise_flag(a.err_flags, PA_DEVERR_BLOCK);
+      s_stage_bad[stage] = ok ? 0 : 1;
+      __threadfence_block();
+      *(volatile int*)&s_last[stage] = next_tile;
+      const uint32_t bar = smem_u32(&s_full[stage]);
+      uint32_t dst = ring + stage * A.stage;
+      tc::mbar_expect_tx(bar, (uint32_t)A.stage);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < KSL; ++k, dst += kSlab)
+          tc::tma_load_3d(dst, &kmap, k * 64, 2 * gk + i, row, bar);
+#pragma unroll
+      for (int k = 0; k < VT / 8; ++k, dst += kSlab)
+        if (k < A.vslabs) tc::tma_load_3d(dst, &vmap, k * 64, gk, row, bar);
+    }
+    __syncwarp();
+    // tiles below `stages` come one after another, later ones in step with
+    // the warp's own
+    const int step = next_tile + kWarps < stages || next_tile >= stages
+                         ? kWarps
+                         : warp + stages - next_tile;
+    next_tile += step;
+    if (next_tile < count) {
+      cursor_step(A, lc, step, nseq);
+      next_page = page_of();
+    }
   };
-  for (int s = 0; s < A.stages - 1; ++s) issue();
+  for (int t = warp; t < stages; t += kWarps) issue(t);
 
   // ---- the (sequence, kv head, chunk)s of the part, one after another
-  int done = 0;     // tiles of this warp already folded
-  int at = 0;       // tiles of the CTA before the current segment
+  int n = warp;      // this warp's next tile of the CTA, its stage and parity
+  int st = warp % stages;
+  uint32_t par = (uint32_t)(warp / stages) & 1u;
+  int at = 0;        // tiles of the CTA before the current segment
+  bool ok = true;
+  // ldmatrix addresses within a slab: keys (scores): lanes 0-7 keys 0-7 chunk
+  // 0, 8-15 keys 0-7 chunk 1, 16-23 keys 8-15 chunk 0, 24-31 keys 8-15 chunk 1;
+  // values (transposed): lanes 8-15 are keys 8-15 of chunk 0
+  const uint32_t k_row = (lane & 7) + ((lane >> 4) << 3), k_hc = (lane >> 3) & 1;
+  const uint32_t v_row = (lane & 7) + (((lane >> 3) & 1) << 3), v_hc = lane >> 4;
+  const uint32_t k_off = k_row * 128 + ((k_hc ^ (k_row & 7)) << 4);
+  const uint32_t v_off = v_row * 128 + ((v_hc ^ (v_row & 7)) << 4);
   Cursor cur = first;
   while (at < count) {
     const int seg = min(cur.tiles - cur.tile, count - at);  // tiles of this segment
     const int b = a.seq_begin + cur.seq, gk = cur.gc / A.chunks;
     const int h0 = gk * A.grp + (cur.gc - gk * A.chunks) * kHeads;
     const int nh = min(kHeads, A.grp - (cur.gc - gk * A.chunks) * kHeads);
-    // the query rows (rows 0-7 map 0, rows 8-15 map 1), rotated, in the order
-    // of the A fragments: [k step][lane] of the four registers
+    // the query rows, rotated, as A fragments of each map: rows 0-7 the heads'
+    // values, rows 8-15 the remainders; [map][k step][lane] of four registers
     {
       const int64_t t = a.cumseq[b];
-      for (int i = tid; i < kRows * (hs >> 3); i += kWarps * 32) {
-        const int r = i & 15, d0 = (i >> 4) * 8, m = r >> 3, hh = r & 7;
+      for (int i = tid; i < kRows * KS * 2; i += kWarps * 32) {
+        const int m = i & 1, hh = (i >> 1) & 7, d0 = (i >> 4) * 8;
         float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (hh < nh) {
+        if (hh < nh && d0 < hs) {
           const T* row = (const T*)a.query + ((t * g.H + h0 + hh) * 2 + m) * (int64_t)hs;
           unpack8<T>(*reinterpret_cast<const uint4*>(row + d0), x);
           if (g.rd > 0 && d0 >= g.ro && d0 < g.ro + g.rd) {
@@ -354,11 +405,10 @@ diff_decode_kernel(const __grid_constant__ Args A) {
                      (const T*)a.sin_cache + cur.pos * half);
           }
         }
-        const int reg = (d0 & 8 ? 2 : 0) + m;
-        uint32_t* hi = reinterpret_cast<uint32_t*>(q_hi + (d0 >> 4) * 32 + hh * 4) + reg;
-        uint32_t* lo = reinterpret_cast<uint32_t*>(q_lo + (d0 >> 4) * 32 + hh * 4) + reg;
+        uint32_t* f = reinterpret_cast<uint32_t*>(q_s + (m * KS + (d0 >> 4)) * 32 + hh * 4) +
+                      (d0 & 8 ? 2 : 0);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split2<T>(x[2 * e], x[2 * e + 1], hi + 4 * e, lo + 4 * e);
+        for (int e = 0; e < 4; ++e) split2<T>(x[2 * e], x[2 * e + 1], f + 4 * e, f + 4 * e + 1);
       }
       __syncthreads();
     }
@@ -370,20 +420,20 @@ diff_decode_kernel(const __grid_constant__ Args A) {
       for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
     float mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     bool bad = false;
-    // this warp's tiles of the segment: CTA tile numbers warp + 4 done in [at, at + seg)
-    for (int n = warp + done * kWarps; n < at + seg; n += kWarps, ++done) {
-      issue();
-      // all but the newest stages - 1 groups have landed
-      if (A.stages == 3) cp_wait<2>();
-      else if (A.stages == 4) cp_wait<3>();
-      else if (A.stages == 5) cp_wait<4>();
-      else cp_wait<5>();
-      __syncwarp();
-      const int st = done % A.stages;
-      bad |= (bad_stages >> st) & 1u;
-      const uint32_t kb = ring_u + st * A.stage, vb = kb + kTileKeys * A.pitch_k;
+    for (; n < at + seg; n += kWarps) {
+      if (ok)
+        ok = __all_sync(0xffffffffu,
+                        wait_tile(&s_full[st], &s_last[st], n, par, &s_abort, a.err_flags));
+      if (!ok) {
+        bad = true;
+        continue;
+      }
+      bad |= s_stage_bad[st] != 0;
+      const uint32_t kb = ring + st * A.stage + k_off;
+      const uint32_t vb0 = ring + st * A.stage + 2 * KSL * kSlab;
+      const uint32_t vb = vb0 + v_off;
 
-      // scores: s[map][8-key half]; the other map's rows of A are zero
+      // scores of both maps, two halves of 8 keys each
       float s[2][2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -391,39 +441,25 @@ diff_decode_kernel(const __grid_constant__ Args A) {
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[i][j][e] = 0.f;
-      {
-        // ldmatrix rows: lanes 0-7 keys 0-7 chunk 0, 8-15 keys 0-7 chunk 1,
-        // 16-23 keys 8-15 chunk 0, 24-31 keys 8-15 chunk 1
-        const int r = (lane & 7) + ((lane >> 4) << 3), hc = (lane >> 3) & 1;
-        const uint32_t rowb = kb + r * A.pitch_k;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          if (ks < nks) {
-            const uint4 qh = q_hi[ks * 32 + lane], ql = q_lo[ks * 32 + lane];
-            uint32_t k0[4], k1[4];
-            const int c0 = ks * 2 + hc, c1 = c0 + (hs >> 3);
-            ldsm4(k0, rowb + ((c0 & ~7) << 4) + (((c0 & 7) ^ (r & 7)) << 4));
-            ldsm4(k1, rowb + ((c1 & ~7) << 4) + (((c1 & 7) ^ (r & 7)) << 4));
-            mma<T>(s[0][0], qh.x, 0u, qh.z, 0u, k0[0], k0[1]);
-            mma<T>(s[0][1], qh.x, 0u, qh.z, 0u, k0[2], k0[3]);
-            mma<T>(s[1][0], 0u, qh.y, 0u, qh.w, k1[0], k1[1]);
-            mma<T>(s[1][1], 0u, qh.y, 0u, qh.w, k1[2], k1[3]);
-            mma<T>(s[0][0], ql.x, 0u, ql.z, 0u, k0[0], k0[1]);
-            mma<T>(s[0][1], ql.x, 0u, ql.z, 0u, k0[2], k0[3]);
-            mma<T>(s[1][0], 0u, ql.y, 0u, ql.w, k1[0], k1[1]);
-            mma<T>(s[1][1], 0u, ql.y, 0u, ql.w, k1[2], k1[3]);
-          }
+      for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 q = q_s[(i * KS + ks) * 32 + lane];
+          uint32_t k[4];
+          ldsm4(k, (kb ^ ((ks & 3) << 5)) + (i * KSL + (ks >> 2)) * kSlab);
+          mma<T>(s[i][0], q.x, q.y, q.z, q.w, k[0], k[1]);
+          mma<T>(s[i][1], q.x, q.y, q.z, q.w, k[2], k[3]);
         }
       }
       // v[map][8-key half][key of the pair], log2 domain
       float v[2][2][2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        v[0][j][0] = s[0][j][0];
-        v[0][j][1] = s[0][j][1];
-        v[1][j][0] = s[1][j][2];
-        v[1][j][1] = s[1][j][3];
-      }
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) v[i][j][e] = s[i][j][e] + s[i][j][2 + e];
       if (A.cap_out > 0.f) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -448,6 +484,17 @@ diff_decode_kernel(const __grid_constant__ Args A) {
             const int64_t key = key0 + j * 8 + (lane & 3) * 2 + e;
             if (key < cur.lo || key > cur.pos) v[0][j][e] = v[1][j][e] = -INFINITY;
           }
+        // zero the value rows of those keys: 16-byte pieces, a row after another
+        for (int i = lane; i < kTileKeys * A.vslabs * 8; i += 32) {
+          const int r = (i >> 3) & 15;
+          if (key0 + r < cur.lo || key0 + r > cur.pos)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             vb0 + (i >> 7) * kSlab + r * 128 + (i & 7) * 16),
+                         "r"(0)
+                         : "memory");
+        }
+        tc::fence_proxy_async();  // before the stage's next copy
+        __syncwarp();
       }
       // running maxima (each head's row is held by four lanes)
       float f[2] = {1.f, 1.f};
@@ -471,6 +518,7 @@ diff_decode_kernel(const __grid_constant__ Args A) {
           o[c][3] *= f[1];
         }
       }
+      // probabilities as A fragments: rows 0-7 map 0, rows 8-15 map 1
       uint32_t ph[4], pl[4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -482,27 +530,30 @@ diff_decode_kernel(const __grid_constant__ Args A) {
           split2<T>(p0, p1, &ph[j * 2 + i], &pl[j * 2 + i]);
         }
       }
-      // o += P V: 16 keys are the K of one step; two 8-channel tiles a load
-      {
-        const int r = (lane & 7) + (((lane >> 3) & 1) << 3), hc = lane >> 4;
-        const uint32_t rowb = vb + r * A.pitch_v;
+      // o += P V: the 16 keys are one k step; four 8-channel tiles at a
+      // time, so that the two products of a tile are not back to back
 #pragma unroll
-        for (int c = 0; c < VT; c += 2) {
-          if (c < nvt) {
-            uint32_t w[4];
-            const int ch = c + hc;
-            ldsm4_t(w, rowb + ((ch & ~7) << 4) + (((ch & 7) ^ (r & 7)) << 4));
-            mma<T>(o[c], ph[0], ph[1], ph[2], ph[3], w[0], w[1]);
-            mma<T>(o[c + 1], ph[0], ph[1], ph[2], ph[3], w[2], w[3]);
-            mma<T>(o[c], pl[0], pl[1], pl[2], pl[3], w[0], w[1]);
-            mma<T>(o[c + 1], pl[0], pl[1], pl[2], pl[3], w[2], w[3]);
-          }
+      for (int c = 0; c < VT; c += 4) {
+        if (c < nvt) {
+          uint32_t w[4], x[4];
+          ldsm4_t(w, (vb ^ ((c & 4) << 4)) + (c >> 3) * kSlab);
+          ldsm4_t(x, (vb ^ (((c & 4) + 2) << 4)) + (c >> 3) * kSlab);
+          mma<T>(o[c], ph[0], ph[1], ph[2], ph[3], w[0], w[1]);
+          mma<T>(o[c + 1], ph[0], ph[1], ph[2], ph[3], w[2], w[3]);
+          mma<T>(o[c + 2], ph[0], ph[1], ph[2], ph[3], x[0], x[1]);
+          mma<T>(o[c + 3], ph[0], ph[1], ph[2], ph[3], x[2], x[3]);
+          mma<T>(o[c], pl[0], pl[1], pl[2], pl[3], w[0], w[1]);
+          mma<T>(o[c + 1], pl[0], pl[1], pl[2], pl[3], w[2], w[3]);
+          mma<T>(o[c + 2], pl[0], pl[1], pl[2], pl[3], x[0], x[1]);
+          mma<T>(o[c + 3], pl[0], pl[1], pl[2], pl[3], x[2], x[3]);
         }
       }
-      __syncwarp();  // the stage may be overwritten by the next issue()
+      __syncwarp();
+      issue(st);
+      for (st += kWarps; st >= stages; st -= stages) par ^= 1;
     }
 
-    // ---- the four warps' results, joined in the order of the warps
+    // ---- the warps' results, joined in the order of the warps
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
@@ -535,35 +586,47 @@ diff_decode_kernel(const __grid_constant__ Args A) {
         A.ws_ml[slot * kRows + r] = make_float2(any ? __int_as_float(0x7fc00000) : M, L);
       }
     }
-    for (int k = 0; k < kWarps; ++k) {
-      if (warp == k) {
-        const int c = (lane & 3) * 2;
+    // warps 0, 2, 4, 6 add up in buffer 0 while 1, 3, 5, 7 do in buffer 1
+    for (int k = 0; k < (kWarps + kBufs - 1) / kBufs; ++k) {
+      if (warp / kBufs == k) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float* row = merge + (i * 8 + (lane >> 2)) * mpitch + c;
-          float* dst = A.ws_o + (slot * kRows + i * 8 + (lane >> 2)) * (int64_t)vhs + c;
+          float* row = merge + (warp % kBufs) * kRows * mpitch + (i * 8 + (lane >> 2)) * mpitch +
+                       (lane & 3) * 2;
 #pragma unroll
-          for (int n = 0; n < VT; ++n) {
-            if (n < nvt) {
-              float2 x = make_float2(o[n][2 * i] * w[i], o[n][2 * i + 1] * w[i]);
+          for (int c = 0; c < VT; ++c) {
+            if (c < nvt) {
+              float2 x = make_float2(o[c][2 * i] * w[i], o[c][2 * i + 1] * w[i]);
               if (k > 0) {
-                const float2 y = *reinterpret_cast<const float2*>(row + n * 8);
+                const float2 y = *reinterpret_cast<const float2*>(row + c * 8);
                 x.x += y.x;
                 x.y += y.y;
               }
-              if (k < kWarps - 1) *reinterpret_cast<float2*>(row + n * 8) = x;
-              else if ((lane >> 2) < nh) *reinterpret_cast<float2*>(dst + n * 8) = x;
+              *reinterpret_cast<float2*>(row + c * 8) = x;
             }
           }
         }
       }
       __syncthreads();
     }
+    for (int i = tid; i < kRows * (vhs >> 2); i += kWarps * 32) {
+      const int r = i / (vhs >> 2), c = (i - r * (vhs >> 2)) * 4;
+      if ((r & 7) < nh) {
+        const float4 x = *reinterpret_cast<const float4*>(merge + r * mpitch + c);
+        const float4 y = *reinterpret_cast<const float4*>(merge + (kRows + r) * mpitch + c);
+        *reinterpret_cast<float4*>(A.ws_o + (slot * kRows + r) * (int64_t)vhs + c) =
+            make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+      }
+    }
+    // (the next segment's first barrier stands between these reads and its writes)
     at += seg;
     cursor_step(A, cur, seg, nseq);
   }
-  cp_wait<0>();
   if (!waited) grid_dep_wait();
+  // after a wait that gave up, copies may still be in flight
+  __syncthreads();
+  if (s_abort && tid < stages && s_last[tid] >= 0)
+    tc::drain_wait(smem_u32(&s_full[tid]), (uint32_t)(s_last[tid] / stages) & 1u, a.err_flags);
 }
 
 // Joins the parts of each (sequence, head), takes the difference of the two
@@ -673,7 +736,7 @@ __global__ void __launch_bounds__(kHeads * 32) diff_combine_kernel(const __grid_
 // Host side
 // ---------------------------------------------------------------------------
 struct Plan {
-  int pitch_k, pitch_v, stage, stages, per_sm, ks, vt;
+  int vslabs, stage, stages, ks, vt;
   size_t smem;
 };
 
@@ -681,18 +744,13 @@ Plan plan_of(const Geometry& g) {
   Plan p;
   p.ks = g.hs <= 64 ? 4 : 8;
   p.vt = g.vhs <= 128 ? 16 : 32;
-  p.pitch_k = (4 * g.hs + 127) / 128 * 128;
-  p.pitch_v = (2 * g.vhs + 127) / 128 * 128;
-  p.stage = kTileKeys * (p.pitch_k + p.pitch_v);
-  const size_t fixed = (size_t)p.ks * 32 * 16 * 2 + (size_t)kRows * (p.vt * 8 + 8) * 4;
-  // two CTAs per SM where three stages each fit (and their registers do),
-  // else one with all of the shared memory
-  const size_t half = 112 * 1024, whole = 225 * 1024;
-  p.per_sm = p.vt == 16 && fixed + (size_t)kWarps * 3 * p.stage <= half ? 2 : 1;
-  const size_t room = p.per_sm == 2 ? half : whole;
-  int s = (int)((room - fixed) / ((size_t)kWarps * p.stage));
-  p.stages = s > 6 ? 6 : s;
-  p.smem = fixed + (size_t)kWarps * p.stages * p.stage;
+  p.vslabs = (g.vhs + 63) / 64;
+  p.stage = kSlab * (p.ks / 2 + p.vslabs);
+  const size_t fixed = 1024 + (size_t)p.ks * 32 * 16 * 2 +
+                       (size_t)kBufs * kRows * (p.vt * 8 + 8) * 4;
+  const int s = (int)((kSmem - fixed) / (size_t)p.stage);
+  p.stages = s > kMaxStages ? kMaxStages : s;
+  p.smem = fixed + (size_t)p.stages * p.stage;
   return p;
 }
 
@@ -705,7 +763,7 @@ Layout layout_of(const Geometry& g, const Plan& p, int64_t nseq) {
   Layout l;
   l.chunks = (g.H / g.kvh + kHeads - 1) / kHeads;
   l.ng = g.kvh * l.chunks;
-  l.ctas = g.num_sms * p.per_sm;
+  l.ctas = g.num_sms;
   l.slots = l.ctas + nseq * l.ng;
   l.o = ((size_t)l.slots * kRows * g.vhs * 4 + 255) & ~(size_t)255;
   l.ml = ((size_t)l.slots * kRows * 8 + 255) & ~(size_t)255;
@@ -713,15 +771,37 @@ Layout layout_of(const Geometry& g, const Plan& p, int64_t nseq) {
   return l;
 }
 
+// The cache as [slots][rows][channels], boxes of 64 channels x 1 row x 16 slots
+// (channels past the width read as zeros).
+cudaError_t encode(CUtensorMap* map, bool bf16, const void* base, int width, int rows,
+                   int64_t slots) {
+  tc::EncodeTiledFn enc = tc::encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)slots};
+  const cuuint64_t str[2] = {(cuuint64_t)width * 2, (cuuint64_t)rows * width * 2};
+  const cuuint32_t box[3] = {64, 1, kTileKeys}, estr[3] = {1, 1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+             const_cast<void*>(base), dims, str, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
 template <typename T, int KS, int VT>
 cudaError_t launch(const Args& A, const Plan& p, int ctas, cudaStream_t stream) {
   static std::atomic<bool> configured[64];
   auto kern = diff_decode_kernel<T, KS, VT>;
   cudaError_t e = once_per_device(configured, A.g.device, [&] {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   });
+  const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+  const int64_t slots = (int64_t)A.g.num_blocks * A.g.bs;
+  CUtensorMap kmap, vmap;
+  if (e == cudaSuccess) e = encode(&kmap, bf16, A.a.key_cache, A.g.hs, 2 * A.g.kvh, slots);
+  if (e == cudaSuccess) e = encode(&vmap, bf16, A.a.value_cache, A.g.vhs, A.g.kvh, slots);
   if (e == cudaSuccess)
-    e = tc::launch_pdl(kern, dim3((unsigned)ctas), dim3(kWarps * 32), p.smem, stream, A);
+    e = tc::launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), p.smem, stream, kmap, vmap, A);
   if (e != cudaSuccess) return e;
   return tc::launch_pdl(diff_combine_kernel<T>,
                         dim3((unsigned)(A.a.seq_end - A.a.seq_begin), (unsigned)A.ng),
@@ -743,8 +823,7 @@ cudaError_t launch_decode(const Geometry& g, const DiffArgs& a) {
   A.grp = g.H / g.kvh;
   A.chunks = l.chunks;
   A.ng = l.ng;
-  A.pitch_k = p.pitch_k;
-  A.pitch_v = p.pitch_v;
+  A.vslabs = p.vslabs;
   A.stage = p.stage;
   A.stages = p.stages;
   A.slots = (int)l.slots;

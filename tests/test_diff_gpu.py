@@ -134,9 +134,12 @@ def test_prefill_lengths(q, past):
     check(workload("64_128", q_lens=[q], past_lens=[past], block_size=16, num_heads=2, drop_slots=0))
 
 
-def test_long_split_decode():
-    """One long sequence beside short ones: split over many CTAs and joined."""
-    check(workload("64_128", q_lens=[1, 1, 1], past_lens=[9000, 17, 300], num_heads=4, drop_slots=0))
+@pytest.mark.parametrize("name,past", [
+    ("64_128", [9000, 17, 300]), ("128_256", [9000, 17, 300]), ("128_256", [40000]), ("hs_96_vhs_192", [30000, 5]),
+    ("hs_128_vhs_64", [30000, 5]), ("vhs_136", [30000, 5])])
+def test_long_split_decode(name, past):
+    """Long sequences, split over many CTAs whose rings turn many times, and joined."""
+    check(workload(name, q_lens=[1] * len(past), past_lens=past, num_heads=4, drop_slots=0))
 
 
 def test_many_sequences():
