@@ -171,7 +171,7 @@ pa_status read(Phase ph, const pa_diff_params* p, DiffArgs a) {
       return fail(PA_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu needed",
                   a.workspace ? a.workspace_bytes : (size_t)0, need);
   }
-  const cudaError_t e = ph == Phase::kDecode ? launch_decode(g, a) : launch_simple(g, a);
+  const cudaError_t e = ph == Phase::kDecode ? launch_decode(g, a) : launch_prefill(g, a);
   if (e != cudaSuccess)
     return fail(PA_ERR_CUDA, "differential attention launch: %s", cudaGetErrorString(e));
   return PA_OK;

@@ -35,7 +35,8 @@ struct DiffArgs {
 // decode (pa_diff_decode.cu); workspace bytes for nseq sequences
 size_t decode_workspace(const Geometry& g, int64_t nseq);
 cudaError_t launch_decode(const Geometry& g, const DiffArgs& a);
-cudaError_t launch_simple(const Geometry& g, const DiffArgs& a);
+// prefill (pa_diff_prefill.cu); needs no workspace
+cudaError_t launch_prefill(const Geometry& g, const DiffArgs& a);
 
 }  // namespace diff
 }  // namespace pa
