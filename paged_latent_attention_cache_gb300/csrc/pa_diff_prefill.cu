@@ -13,12 +13,20 @@
 // Nothing but the output leaves the chip.
 //
 // Inside a CTA, per tile of 128 keys:
-//   warp 8    TMA: key and value rows of the tile through the block table,
-//             a ring of stages
-//   warp 9    QK^T (S: 128 x 128 f32 in TMEM), PV (A = P from TMEM, O: 128 x vg)
+//   warps 8-10 TMA through the block table: a ring of key tiles, and one of value
+//             half tiles (64 keys), which are freed at other times: a key tile
+//             by QK^T, a value half by its half of PV. One ring of whole stages
+//             held keys until PV and left two stages at 128 / 256. All slabs of
+//             a tile come by one 4-D box where the width is a multiple of 64: a
+//             copy costs its thread some 190 cycles, and one warp with a copy
+//             per slab was the slowest part of the kernel (2500 cycles a tile).
+//   warp 11   QK^T (S: 128 x 128 f32 in TMEM), PV (A = P from TMEM, O: 128 x vg)
 //   warps 0-7 softmax: two threads per row, 64 columns each, held in registers:
 //             S is read from TMEM once and is free for the next QK^T before
-//             the exponentials start; P (16 bit) goes to one of two buffers
+//             the exponentials start; P (16 bit) goes to one of two buffers.
+//             Two groups of four warps on alternate tiles (one thread per row)
+//             were no faster at 64 / 128, and at 128 / 256 there is no room for
+//             a second S beside P.
 // TMEM columns: O vg <= 256 | S 128 | P 2 x 64.
 //
 // Bound: per tile and map the MMAs take 128 * 128 * (hs + vhs) / 4096 cycles
@@ -31,6 +39,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "pa_diff_common.cuh"
 #include "pa_diff_internal.h"
 #include "pa_tc_cluster.cuh"
 
@@ -43,14 +52,16 @@ using namespace pa::tc;
 constexpr int kN = 128;             // keys of a tile
 constexpr int kSoftWarps = 8;
 constexpr int kSoft = kSoftWarps * 32;
-constexpr int kProdWarp = 8, kMmaWarp = 9;
-constexpr int kPreThreads = 320;
+constexpr int kProdWarp = 8, kMmaWarp = 11;  // warps 8, 9, 10: keys, value halves 0 and 1
+constexpr int kPreThreads = 384;
 constexpr int kBox = kN * 128;      // bytes of a 64-channel slab of 128 rows
-constexpr int kMaxStages = 8;
+constexpr int kMaxK = 4, kMaxV = 16;  // slots of the rings
+constexpr int kVKeys = 64;            // keys of a value slot
+constexpr int kVBox = kVKeys * 128;   // bytes of its 64-channel slab
 constexpr size_t kSmemMax = 225 * 1024;
 
 struct PreBars {
-  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t k_full[kMaxK], k_empty[kMaxK], v_full[kMaxV], v_empty[kMaxV];
   uint64_t s_full, s_free, p_full[2], pv_done[2];
   uint64_t q_tma, q_full, drain;
   uint32_t tmem_base;
@@ -60,18 +71,25 @@ struct PreBars {
 struct PreArgs {
   Params P;           // what the shared helpers read
   int hs;
+  int nk, nv, v_bytes, v_rows;  // slots of the rings; bytes of a value slot, rows of its boxes
+  bool k_whole, v_whole;        // widths that are multiples of 64: see cache_map
   const float* lambda_vectors;
   const void* norm_weight;
   float lambda_init, norm_eps;
 };
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                            int z, int w, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-      : "memory");
+// One arrival for the whole warp (256 threads on one barrier queue up there).
+__device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(bar));
+}
+__device__ __forceinline__ uint64_t pack_f32(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ void unpack_f32(uint64_t v, float* a, float* b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v));
 }
 __device__ __forceinline__ void st_peer4(uint32_t raddr, float a, float b, float c, float d) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(raddr), "f"(a), "f"(b),
@@ -84,40 +102,93 @@ __device__ __forceinline__ void st_peer(uint32_t raddr, float a) {
 
 // The rotation of one query row in place in its swizzled slabs (16-byte chunk
 // c of row r at c ^ (r & 7)), by two threads (`part` 0 and 1), in f32, rounded
-// once.
+// once. The table entries of a half-split row are loaded (`load`) before the
+// query has landed; 8-channel groups g = part, part + 2, .. of the first half.
 template <typename T>
-__device__ __noinline__ void rotate_row(uint8_t* q_s, int row, int part, const Params& P,
-                                        int64_t pos) {
-  auto at = [&](int d0) -> uint4* {
-    return reinterpret_cast<uint4*>(q_s + (d0 >> 6) * kBox + row * 128 +
-                                    ((((d0 >> 3) & 7) ^ (row & 7)) << 4));
-  };
+struct RowAngles {
+  uint4 c[4], s[4];
+  __device__ __forceinline__ void load(const Params& P, int part, int64_t pos) {
+    const int half = P.rd >> 1;
+    const T* crow = reinterpret_cast<const T*>(P.cos_cache) + pos * half;
+    const T* srow = reinterpret_cast<const T*>(P.sin_cache) + pos * half;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int d = (2 * i + part) * 8;
+      if (d < half) {
+        c[i] = *reinterpret_cast<const uint4*>(crow + d);
+        s[i] = *reinterpret_cast<const uint4*>(srow + d);
+      }
+    }
+  }
+};
+__device__ __forceinline__ uint4* q_chunk(uint8_t* q_s, int row, int d0) {
+  return reinterpret_cast<uint4*>(q_s + (d0 >> 6) * kBox + row * 128 +
+                                  ((((d0 >> 3) & 7) ^ (row & 7)) << 4));
+}
+template <typename T>
+__device__ __forceinline__ void rotate_row(uint8_t* q_s, int row, int part, const Params& P,
+                                           int64_t pos, const RowAngles<T>& A) {
   const int half = P.rd >> 1;
-  const T* crow = reinterpret_cast<const T*>(P.cos_cache) + pos * half;
-  const T* srow = reinterpret_cast<const T*>(P.sin_cache) + pos * half;
   if (P.interleaved) {
+    const T* crow = reinterpret_cast<const T*>(P.cos_cache) + pos * half;
+    const T* srow = reinterpret_cast<const T*>(P.sin_cache) + pos * half;
+#pragma unroll 1
     for (int d0 = P.ro + part * 8; d0 < P.ro + P.rd; d0 += 16) {
       float a[8], none[8];
-      unpack8<T>(*at(d0), a);
+      unpack8<T>(*q_chunk(q_s, row, d0), a);
       rope8<T>(a, none, d0, P.ro, P.rd, 1, crow, srow);
-      *at(d0) = pack8<T>(a);
+      *q_chunk(q_s, row, d0) = pack8<T>(a);
     }
     return;
   }
-  for (int d0 = P.ro + part * 8; d0 < P.ro + half; d0 += 16) {
-    float a[8], b[8], na[8], nb[8];
-    unpack8<T>(*at(d0), a);
-    unpack8<T>(*at(d0 + half), b);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      na[e] = a[e];
-      nb[e] = b[e];
+  for (int i = 0; i < 4; ++i) {
+    const int d = (2 * i + part) * 8;
+    if (d < half) {
+      float x[8], y[8], c[8], sn[8], u[8], v[8];
+      unpack8<T>(*q_chunk(q_s, row, P.ro + d), x);
+      unpack8<T>(*q_chunk(q_s, row, P.ro + half + d), y);
+      unpack8<T>(A.c[i], c);
+      unpack8<T>(A.s[i], sn);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {  // as rope8
+        u[e] = fmaf(x[e], c[e], -y[e] * sn[e]);
+        v[e] = fmaf(y[e], c[e], x[e] * sn[e]);
+      }
+      *q_chunk(q_s, row, P.ro + d) = pack8<T>(u);
+      *q_chunk(q_s, row, P.ro + half + d) = pack8<T>(v);
     }
-    rope8<T>(na, b, d0, P.ro, P.rd, 0, crow, srow);
-    rope8<T>(nb, a, d0 + half, P.ro, P.rd, 0, crow, srow);
-    *at(d0) = pack8<T>(na);
-    *at(d0 + half) = pack8<T>(nb);
   }
+}
+
+// 2^(v sl + nm) of 32 raw scores of a row, packed to 16 bits; returns the sum
+// of the unrounded values. In three passes over the registers, so that the 32
+// exponentials issue back to back (element by element the warp waited for each
+// one: twice the time), the multiply-adds and sums on pairs.
+template <typename T>
+__device__ __forceinline__ float exp_row(uint32_t (&r)[32], uint32_t (&pk)[16], float sl, float nm) {
+  const uint64_t sl2 = pack_f32(sl, sl), nm2 = pack_f32(nm, nm);
+  uint64_t x[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(x[e])
+        : "l"(pack_f32(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]))), "l"(sl2), "l"(nm2));
+  float p[32];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) unpack_f32(x[e], &p[2 * e], &p[2 * e + 1]);
+#pragma unroll
+  for (int e = 0; e < 32; ++e) p[e] = ex2(p[e]);
+  uint64_t sum[2] = {pack_f32(0.f, 0.f), pack_f32(0.f, 0.f)};
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[e & 1]) : "l"(pack_f32(p[2 * e], p[2 * e + 1])));
+    pk[e] = pack2<T>(p[2 * e], p[2 * e + 1]);
+  }
+  float a, b, c, d;
+  unpack_f32(sum[0], &a, &b);
+  unpack_f32(sum[1], &c, &d);
+  return (a + b) + (c + d);
 }
 
 template <typename T, bool CAP>
@@ -132,14 +203,15 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
   uint8_t* q_s = smem;
-  uint8_t* k_s = smem + P.q_bytes;  // stage: key slabs, then value slabs, kN rows each
+  uint8_t* k_s = smem + P.q_bytes;         // key slots: slabs of kN rows
+  uint8_t* v_s = k_s + A.nk * P.k_bytes;   // value slots: slabs of kVKeys rows
   // in the query's place, once the last QK^T is done: the halves' sums, and
   // [CTA * 2 + half] sums of squares, the peer's too
   float (*s_sum)[kRows] = reinterpret_cast<float (*)[kRows]>(q_s);
   float (*s_ss)[kRows] = s_sum + 2;
   PreBars* bars = &bars_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slabs = P.slabs, vslabs = P.vslabs, vg = P.vg, stages = P.stages;
+  const int slabs = P.slabs, vslabs = P.vslabs, vg = P.vg;
   const int kvh = P.kvh, grp = P.grp, vhs = P.vhs;
   const int map = (int)cluster_rank();
   const int pair = blockIdx.x >> 1;
@@ -171,18 +243,22 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     }
     if (lane == 0) work = w;
   } else if (warp == 1 && lane == 0) {
-    for (int s = 0; s < stages; ++s) {
-      mbar_init(smem_u32(&bars->full[s]), 1);
-      mbar_init(smem_u32(&bars->empty[s]), 1);
+    for (int s = 0; s < A.nk; ++s) {
+      mbar_init(smem_u32(&bars->k_full[s]), 1);
+      mbar_init(smem_u32(&bars->k_empty[s]), 1);
+    }
+    for (int s = 0; s < A.nv; ++s) {
+      mbar_init(smem_u32(&bars->v_full[s]), 1);
+      mbar_init(smem_u32(&bars->v_empty[s]), 1);
     }
     mbar_init(smem_u32(&bars->s_full), 1);
-    mbar_init(smem_u32(&bars->s_free), kSoft);
+    mbar_init(smem_u32(&bars->s_free), kSoftWarps);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bars->p_full[i]), kSoft);
+      mbar_init(smem_u32(&bars->p_full[i]), kSoftWarps);
       mbar_init(smem_u32(&bars->pv_done[i]), 1);
     }
     mbar_init(smem_u32(&bars->q_tma), 1);
-    mbar_init(smem_u32(&bars->q_full), kSoft);
+    mbar_init(smem_u32(&bars->q_full), kSoftWarps);
     mbar_init(smem_u32(&bars->drain), 1);
     bars->bad = 0;
     bars->abort = 0;
@@ -224,6 +300,8 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       // =================== softmax ===================
       const int64_t pos_r = row < rows ? pos + row / grp : -1;
       const int64_t lo_r = P.window >= 0 ? max((int64_t)0, pos_r - P.window) : 0;
+      RowAngles<T> ang;
+      if (row < rows && P.rd > 0 && !P.interleaved) ang.load(P, half, pos_r);
       float lam = 0.f;
       if (map == 1) {
         float d0 = 0.f, d1 = 0.f;
@@ -240,47 +318,54 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         lam = expf(d0) - expf(d1) + A.lambda_init;
       }
       ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->q_tma), 0, abort, P.err_flags));
-      if (ok && row < rows && P.rd > 0) rotate_row<T>(q_s, row, half, P, pos_r);
+      if (ok && row < rows && P.rd > 0) rotate_row<T>(q_s, row, half, P, pos_r, ang);
       fence_proxy_async();
-      mbar_arrive(smem_u32(&bars->q_full));
+      arrive_warp(&bars->q_full, lane);
 
       float m_used = -INFINITY, l = 0.f;
       const float sl = CAP ? 1.f : P.scale_log2;
       // Every warp goes through all n tiles and meets its partner of the
       // quadrant twice in each; after a wait that gave up (ok false) it does
       // nothing else.
+#pragma unroll 1
       for (int k = 0; k < n; ++k) {
         const int pb = k & 1;
         const int64_t j0 = (t_begin + k) * kN;
         const bool edge = j0 < lo_hi || j0 + kN - 1 > pos;
+        // (S of tile k is committed behind PV of tile k - 2, so this also
+        // says that P's buffer may be written again)
         if (ok)
           ok = __all_sync(0xffffffffu,
                           wait_bar(smem_u32(&bars->s_full), k & 1, abort, P.err_flags));
-        uint32_t s0[32], s1[32];
+        uint32_t s[2][32];
         if (live && ok) {
           tc_fence_after();
-          tmem_ld32_nowait(lane_addr + col_s + half * 64, s0);
-          tmem_ld32_nowait(lane_addr + col_s + half * 64 + 32, s1);
+          tmem_ld32_nowait(lane_addr + col_s + half * 64, s[0]);
+          tmem_ld32_nowait(lane_addr + col_s + half * 64 + 32, s[1]);
           tmem_wait_ld();
-          reg_fence(s0);
-          reg_fence(s1);
+          reg_fence(s[0]);
+          reg_fence(s[1]);
           tc_fence_before();
         }
-        if (ok) mbar_arrive(smem_u32(&bars->s_free));  // the next QK^T may overwrite S
+        if (ok) arrive_warp(&bars->s_free, lane);  // the next QK^T may overwrite S
         if (edge && ok) {  // zero the value rows of keys no row of the unit sees
-          uint8_t* vst = k_s + (k % stages) * P.stage_bytes + P.k_bytes;
-          for (int i = tid; i < kN * vslabs * 8; i += kSoft) {
-            const int rr = (i >> 3) & (kN - 1);
-            const int64_t j = j0 + rr;
-            if (j < lo || j > pos_hi)
-              *reinterpret_cast<uint4*>(vst + (i >> 10) * kBox + rr * 128 + (i & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
+          const int v0 = 2 * k;
+          for (int i = 0; i < 2 && ok; ++i)
+            ok = __all_sync(0xffffffffu,
+                            wait_bar(smem_u32(&bars->v_full[(v0 + i) % A.nv]),
+                                     (uint32_t)((v0 + i) / A.nv) & 1u, abort, P.err_flags));
+          if (ok) {
+            for (int i = tid; i < kN * vslabs * 8; i += kSoft) {
+              const int rr = (i >> 3) & (kN - 1);
+              const int64_t j = j0 + rr;
+              if (j < lo || j > pos_hi)
+                *reinterpret_cast<uint4*>(v_s + ((v0 + (rr >> 6)) % A.nv) * A.v_bytes +
+                                          (i >> 10) * kVBox + (rr & 63) * 128 + (i & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async();
           }
-          fence_proxy_async();
         }
-        if (k >= 2 && ok)
-          ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->pv_done[pb]),
-                                                ((k - 2) >> 1) & 1, abort, P.err_flags));
         float factor = 1.f;
         bool rescale = false;
         if (live && ok) {
@@ -288,18 +373,22 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             const int c0 = (int)min((int64_t)kN, max((int64_t)0, lo_r - j0)) - half * 64;
             const int c1 = (int)max((int64_t)-1, min((int64_t)(kN - 1), pos_r - j0)) - half * 64;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if (e < c0 || e > c1) s0[e] = __float_as_uint(-INFINITY);
-              if (e + 32 < c0 || e + 32 > c1) s1[e] = __float_as_uint(-INFINITY);
-            }
-          }
-          float v0 = -INFINITY, v1 = -INFINITY;
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            v0 = fmaxf(v0, __uint_as_float(s0[e]));
-            v1 = fmaxf(v1, __uint_as_float(s1[e]));
+              for (int e = 0; e < 32; ++e)
+                if (c * 32 + e < c0 || c * 32 + e > c1) s[c][e] = __float_as_uint(-INFINITY);
           }
-          s_max[half][row] = fmaxf(v0, v1);
+          float v[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t* x = s[c >> 1] + (c & 1) * 16;
+            v[c] = __uint_as_float(x[0]);
+#pragma unroll
+            for (int e = 1; e < 15; e += 2)
+              v[c] = fmaxf(v[c], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+            v[c] = fmaxf(v[c], __uint_as_float(x[15]));
+          }
+          s_max[half][row] = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
         }
         if (live) named_sync(1 + (warp & 3), 64);
         if (live && ok) {
@@ -316,13 +405,20 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             rescale = true;
           }
           const float mu = m_used == -INFINITY ? 0.f : m_used;
-          const ExpArgs E{sl, mu, P.cap_in, P.cap_out, 0.f, 0.f, 0.f, 0.f, 0.f};
-          uint32_t pk[16];
           const uint32_t dst = lane_addr + col_p + pb * 64 + half * 32;
-          l += exp_chunk<T, CAP ? 2 : 0>(s0, pk, E);
-          tmem_st16(dst, pk);
-          l += exp_chunk<T, CAP ? 2 : 0>(s1, pk, E);
-          tmem_st16(dst + 16, pk);
+          uint32_t pk[16];
+          if (CAP) {
+            const ExpArgs E{sl, mu, P.cap_in, P.cap_out, 0.f, 0.f, 0.f, 0.f, 0.f};
+            l += exp_chunk<T, 2>(s[0], pk, E);
+            tmem_st16(dst, pk);
+            l += exp_chunk<T, 2>(s[1], pk, E);
+            tmem_st16(dst + 16, pk);
+          } else {
+            l += exp_row<T>(s[0], pk, sl, -mu);
+            tmem_st16(dst, pk);
+            l += exp_row<T>(s[1], pk, sl, -mu);
+            tmem_st16(dst + 16, pk);
+          }
           if (__any_sync(0xffffffffu, rescale)) {
             // (k >= 1) each half scales half of O, once the PV before has added to it
             ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->pv_done[(k - 1) & 1]),
@@ -343,22 +439,24 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           tmem_wait_st();
           tc_fence_before();
         }
+        if (ok) arrive_warp(&bars->p_full[pb], lane);
         if (live) named_sync(1 + (warp & 3), 64);  // before s_max is used again
-        if (ok) mbar_arrive(smem_u32(&bars->p_full[pb]));
       }
       grid_dep_launch();
-      if (live) s_sum[half][row] = l;
       named_sync(5, kSoft);
       ok = __all_sync(0xffffffffu, ok && !*abort);
       if (ok && n > 0)
         ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->pv_done[(n - 1) & 1]),
                                               ((n - 1) >> 1) & 1, abort, P.err_flags));
       tc_fence_after();
+      if (live) s_sum[half][row] = l;
+      named_sync(5, kSoft);
       const float lt = s_sum[0][row] + s_sum[1][row];
       coef = lt > 0.f ? (map == 0 ? 1.f : lam) / lt : 0.f;
-    } else if (warp == kProdWarp) {
-      // =================== TMA producer ===================
-      if (lane == 0) {
+    } else if (warp < kMmaWarp) {
+      // =================== TMA producers ===================
+      const bool keys = warp == kProdWarp;
+      if (keys && lane == 0) {
         const uint32_t qb = smem_u32(&bars->q_tma);
         mbar_expect_tx(qb, (uint32_t)(slabs * grp * P.tpc * 128));
         for (int slab = 0; slab < slabs; ++slab)
@@ -367,124 +465,136 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       int dirty_from = 0;
       if (P.early && P.own_slots) dirty_from = (int)max((int64_t)0, W.past / kN - t_begin);
       bool waited = !P.early;
-      const int nsub = kN / P.box_rows;
       const int32_t* bt = P.block_table + (int64_t)W.b * P.max_blocks;
       const int sh = __ffs(P.bs) - 1;
-      int issued = 0, stage = 0;
+      // keys: a tile per slot; values: this warp's half tile, every second slot
+      const int slots = keys ? A.nk : A.nv, step = keys ? 1 : 2, h = keys ? 0 : warp - kProdWarp - 1;
+      uint64_t* full = keys ? bars->k_full : bars->v_full;
+      uint64_t* empty = keys ? bars->k_empty : bars->v_empty;
+      const uint32_t bytes = keys ? (uint32_t)P.k_bytes : (uint32_t)A.v_bytes;
+      const uint32_t base = keys ? smem_u32(k_s) : smem_u32(v_s);
+      const uint32_t slab_bytes = keys ? kBox : kVBox;
+      const int box = keys ? P.box_rows : A.v_rows, nbox = (keys ? kN : kVKeys) / box;
+      const CUtensorMap* tm = keys ? &kmap : &vmap;
+      const int head = keys ? 2 * gk + map : gk, nslab = keys ? slabs : vslabs;
+      const bool whole = keys ? A.k_whole : A.v_whole;
+      int slot = h, issued = 0;
       uint32_t par = 1;
       for (int k = 0; k < n; ++k) {
         if (!waited && k >= dirty_from) {
           grid_dep_wait();
           waited = true;
         }
-        int y = (int)P.num_slots;  // out of range: TMA fills zeros
-        if (lane < nsub) {
-          const int64_t key0 = (t_begin + k) * kN + (int64_t)lane * P.box_rows;
-          if (key0 <= pos_hi && key0 + P.box_rows - 1 >= lo) {
-            const int32_t phys = bt[key0 >> sh];
-            if (phys >= 0 && phys < P.num_blocks) {
-              y = (int)((int64_t)phys * P.bs + (key0 & (int64_t)(P.bs - 1)));
-            } else {
-              bars->bad = 1;
-              raise_flag(P.err_flags, PA_DEVERR_BLOCK);
-            }
+        // cache row of box `lane` (out of range where no row of the unit sees
+        // it, or its page is invalid: TMA fills zeros)
+        int y = (int)P.num_slots;
+        const int64_t key0 = (t_begin + k) * kN + h * kVKeys + (int64_t)lane * box;
+        if (lane < nbox && key0 <= pos_hi && key0 + box - 1 >= lo) {
+          const int32_t phys = bt[key0 >> sh];
+          if (phys >= 0 && phys < P.num_blocks) {
+            y = (int)((int64_t)phys * P.bs + (key0 & (int64_t)(P.bs - 1)));
+          } else {
+            bars->bad = 1;
+            raise_flag(P.err_flags, PA_DEVERR_BLOCK);
           }
         }
-        if (k >= stages) {
-          bool okw = true;
-          if (lane == 0) okw = wait_bar(smem_u32(&bars->empty[stage]), par, abort, P.err_flags);
-          if (!__shfl_sync(0xffffffffu, okw ? 1 : 0, 0)) break;
+        if (issued * step + h >= slots) {
+          bool w = true;
+          if (lane == 0) w = wait_bar(smem_u32(&empty[slot]), par, abort, P.err_flags);
+          if (!__shfl_sync(0xffffffffu, w ? 1 : 0, 0)) break;
         }
-        if (lane == 0) mbar_expect_tx(smem_u32(&bars->full[stage]), (uint32_t)P.stage_bytes);
+        const uint32_t bar = smem_u32(&full[slot]), dst0 = base + slot * bytes;
+        if (elect_one()) mbar_expect_tx(bar, bytes);
         __syncwarp();
-        if (lane < nsub) {
-          const uint32_t full = smem_u32(&bars->full[stage]);
-          const uint32_t dst0 = smem_u32(k_s + stage * P.stage_bytes) + lane * P.box_rows * 128;
 #pragma unroll 1
-          for (int slab = 0; slab < slabs; ++slab)
-            tma_load_3d(dst0 + slab * kBox, &kmap, slab * 64, 2 * gk + map, y, full);
+        for (int i = 0; i < nbox; ++i) {  // one lane issues, box after box
+          const int yi = __shfl_sync(0xffffffffu, y, i);
+          const uint32_t dst = dst0 + i * box * 128;
+          if (elect_one()) {
+            if (whole && nbox == 1) {
+              tma_load_4d(dst, tm, 0, head, yi, 0, bar);
+            } else {
 #pragma unroll 1
-          for (int slab = 0; slab < vslabs; ++slab)
-            tma_load_3d(dst0 + P.k_bytes + slab * kBox, &vmap, slab * 64, gk, y, full);
+              for (int c = 0; c < nslab; ++c)
+                tma_load_4d(dst + c * slab_bytes, tm, whole ? 0 : c * 64, head, yi, whole ? c : 0,
+                            bar);
+            }
+          }
+          __syncwarp();
         }
-        issued = k + 1;
-        if (++stage == stages) {
-          stage = 0;
+        ++issued;
+        slot += step;
+        if (slot >= slots) {
+          slot -= slots;
           par ^= 1;
         }
         __syncwarp();
       }
       if (!waited) grid_dep_wait();
-      if (*abort && lane == 0) {
-        drain_wait(smem_u32(&bars->q_tma), 0, P.err_flags);
-        for (int st = 0; st < stages && st < issued; ++st)
-          drain_wait(smem_u32(&bars->full[st]), ((issued - 1 - st) / stages) & 1, P.err_flags);
+      if (*abort && lane == 0) {  // copies may be in flight: wait for each slot's last
+        if (keys) drain_wait(smem_u32(&bars->q_tma), 0, P.err_flags);
+        for (int i = 0; i < issued && i < slots / step; ++i)
+          drain_wait(smem_u32(&full[i * step + h]), ((issued - 1 - i) / (slots / step)) & 1,
+                     P.err_flags);
       }
       __syncwarp();
     } else if (warp == kMmaWarp) {
       // =================== MMA issuer ===================
-      if (lane == 0) {
+      if (elect_one()) {
         constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
         constexpr uint32_t id_qk = idesc_f16(kBf16, kRows, kN, false);
         const uint32_t id_pv = idesc_f16(kBf16, kRows, vg, true);
         const int nk = P.hs >> 4;
         const uint64_t q_desc = sdesc(smem_u32(q_s), 16, 1024);
-        const uint32_t k_base = smem_u32(k_s);
-        bool go = wait_bar(smem_u32(&bars->q_full), 0, abort, P.err_flags);
-        if (go) {
+        const uint32_t k_base = smem_u32(k_s), v_base = smem_u32(v_s);
+        int sk = 0, sv = 0;  // next slots, and their parities
+        uint32_t kpar = 0, vpar = 0;
+        auto wait = [&](uint64_t* bar, uint32_t par) {
+          return wait_bar(smem_u32(bar), par, abort, P.err_flags);
+        };
+        auto qk = [&]() {
+          if (!wait(&bars->k_full[sk], kpar)) return false;
           tc_fence_after();
-          int kq = 0, kp = 0, sq = 0, sp = 0;
-          uint32_t fpar = 0;
-          const uint64_t t0 = globaltimer();
-          uint32_t spins = 0;
-          while (kp < n) {
-            bool progressed = false;
-            // QK^T of the next tile first: the softmax warps wait for it, and
-            // it runs while they turn the tile before into probabilities
-            if (kq < n && kq <= kp + 1 &&
-                (kq == 0 || mbar_test_wait(smem_u32(&bars->s_free), (kq - 1) & 1)) &&
-                mbar_test_wait(smem_u32(&bars->full[sq]), fpar)) {
-              tc_fence_after();
-              const uint64_t kd = sdesc(k_base + sq * P.stage_bytes, 16, 1024);
-              for (int kk = 0; kk < nk; ++kk) {
-                const uint32_t o = (uint32_t)(kk >> 2) * (kBox >> 4) + (uint32_t)(kk & 3) * 2;
-                mma_ss(tmem + col_s, q_desc + o, kd + o, id_qk, kk > 0 ? 1u : 0u);
-              }
-              tc_commit(smem_u32(&bars->s_full));
-              ++kq;
-              if (++sq == stages) {
-                sq = 0;
-                fpar ^= 1;
-              }
-              progressed = true;
-            }
-            if (kp < kq && mbar_test_wait(smem_u32(&bars->p_full[kp & 1]), (kp >> 1) & 1)) {
-              tc_fence_after();
-              const uint64_t vd = sdesc(k_base + sp * P.stage_bytes + P.k_bytes, kBox, 1024);
-              const uint32_t pa = tmem + col_p + (kp & 1) * 64;
+          const uint64_t kd = sdesc(k_base + sk * P.k_bytes, 16, 1024);
 #pragma unroll
-              for (int kk = 0; kk < kN / 16; ++kk)
-                mma_ts(tmem, pa + kk * 8, vd + (uint64_t)(kk * 128), id_pv,
-                       (kp > 0 || kk > 0) ? 1u : 0u);
-              tc_commit(smem_u32(&bars->pv_done[kp & 1]));
-              tc_commit(smem_u32(&bars->empty[sp]));
-              ++kp;
-              if (++sp == stages) sp = 0;
-              progressed = true;
-            }
-            if (progressed) {
-              spins = 0;
-              continue;
-            }
-            if ((++spins & 15u) == 0) {
-              if (*abort) break;
-              if (globaltimer() - t0 > kWaitLimitNs * 4) {
-                *abort = 1;
-                raise_flag(P.err_flags, PA_DEVERR_TIMEOUT);
-                break;
-              }
+          for (int kk = 0; kk < 8; ++kk) {
+            if (kk < nk) {
+              const uint32_t o = (uint32_t)(kk >> 2) * (kBox >> 4) + (uint32_t)(kk & 3) * 2;
+              mma_ss(tmem + col_s, q_desc + o, kd + o, id_qk, kk > 0 ? 1u : 0u);
             }
           }
+          tc_commit(smem_u32(&bars->s_full));
+          tc_commit(smem_u32(&bars->k_empty[sk]));
+          if (++sk == A.nk) {
+            sk = 0;
+            kpar ^= 1;
+          }
+          return true;
+        };
+        auto pv = [&](int k, int hp) {
+          if (!wait(&bars->v_full[sv], vpar)) return false;
+          tc_fence_after();
+          const uint64_t vd = sdesc(v_base + sv * A.v_bytes, kVBox, 1024);
+          const uint32_t pa = tmem + col_p + (k & 1) * 64 + hp * 32;
+#pragma unroll
+          for (int kk = 0; kk < kVKeys / 16; ++kk)
+            mma_ts(tmem, pa + kk * 8, vd + (uint64_t)(kk * 128), id_pv,
+                   (k > 0 || hp || kk > 0) ? 1u : 0u);
+          tc_commit(smem_u32(&bars->v_empty[sv]));
+          if (++sv == A.nv) {
+            sv = 0;
+            vpar ^= 1;
+          }
+          return true;
+        };
+        // QK^T of the next tile before PV of this one: its S is free as soon as
+        // the softmax warps have read it, and it runs while they work. The
+        // commit of S(k + 1) stands behind PV(k - 1) (see the softmax's use).
+        bool go = wait(&bars->q_full, 0) && qk();
+        for (int k = 0; k < n && go; ++k) {
+          if (k + 1 < n) go = wait(&bars->s_free, k & 1) && qk();
+          go = go && wait(&bars->p_full[k & 1], (k >> 1) & 1) && pv(k, 0) && pv(k, 1);
+          if (go) tc_commit(smem_u32(&bars->pv_done[k & 1]));
         }
         tc_commit(smem_u32(&bars->drain));
         drain_wait(smem_u32(&bars->drain), 0, P.err_flags);
@@ -545,22 +655,39 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     st_peer(map_peer(smem_u32(&s_ss[map * 2 + half][row]), 1 - map), ss);
   }
   cluster_sync_all();
-  if (live && ok && n > 0 && row < rows) {
+  // the finished 16-bit channels go through shared memory (behind the received
+  // ones), so that a warp writes whole rows: 2 rows of 256 bytes at vg 256
+  uint8_t* o_s = k_s + kRows * vg * 2;
+  const int pitch = vg <= 128 ? 128 : 256;
+  const int first = map * (vg >> 1);  // this CTA's channels
+  if (live && ok && n > 0) {
     ss = (s_ss[0][row] + s_ss[1][row]) + (s_ss[2][row] + s_ss[3][row]);
     const float inv =
         bars->bad ? 0.f : (1.f - A.lambda_init) / sqrtf(ss / (float)vhs + A.norm_eps);
-    const int ch0 = map * (vg >> 1) + half * cols;
-    T* dst = reinterpret_cast<T*>(P.out) +
-             ((W.t + row / grp) * P.H + gk * grp + row % grp) * (int64_t)vhs + ch0;
-    const T* nw = reinterpret_cast<const T*>(A.norm_weight) + ch0;
+    const T* nw = reinterpret_cast<const T*>(A.norm_weight) + first + half * cols;
 #pragma unroll
     for (int c = 0; c < 64; c += 8) {
-      if (c < cols && ch0 + c < vhs) {
+      if (c < cols && first + half * cols + c < vhs) {
         float w[8], o[8];
         unpack8<T>(*reinterpret_cast<const uint4*>(nw + c), w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = bars->bad ? 0.f : x[c + e] * inv * w[e];
-        *reinterpret_cast<uint4*>(dst + c) = pack8<T>(o);
+        *reinterpret_cast<uint4*>(o_s + row * pitch + ((((half * cols + c) >> 3) ^ (row & 7)) << 4)) =
+            pack8<T>(o);
+      }
+    }
+  }
+  if (warp < kSoftWarps) {
+    named_sync(5, kSoft);
+    ok = ok && !*abort;
+    const int nc = max(0, min(vg >> 1, vhs - first)) >> 3;  // 16-byte pieces of a row
+    if (ok && n > 0) {
+      for (int i = tid; i < rows * nc; i += kSoft) {
+        const int r = i / nc, c = i - r * nc;
+        T* dst = reinterpret_cast<T*>(P.out) +
+                 ((W.t + r / grp) * P.H + gk * grp + r % grp) * (int64_t)vhs + first + c * 8;
+        *reinterpret_cast<uint4*>(dst) =
+            *reinterpret_cast<const uint4*>(o_s + r * pitch + ((c ^ (r & 7)) << 4));
       }
     }
   }
@@ -588,6 +715,24 @@ cudaError_t encode(CUtensorMap* map, bool bf16, const void* base, int rank, cons
              : cudaErrorInvalidValue;
 }
 
+// A cache of `heads` rows of `width` channels per slot, as (channel, head, slot,
+// slab). A width that is a multiple of 64 is cut into slabs of 64 channels (the
+// fourth dimension, 128 bytes apart), so that one box of `rows` slots holds all
+// of them, slab after slab; otherwise the channels stay one dimension, which
+// ends at the width (zeros behind it), and a box holds one slab.
+// `all`: boxes of all slabs (else of one).
+cudaError_t cache_map(CUtensorMap* map, bool bf16, const void* base, int width, int heads,
+                      cuuint64_t slots, int rows, bool all) {
+  const bool whole = width % 64 == 0;
+  const cuuint64_t wb = (cuuint64_t)width * 2;
+  const cuuint64_t dims[4] = {whole ? 64u : (cuuint64_t)width, (cuuint64_t)heads, slots,
+                              whole ? (cuuint64_t)(width / 64) : 1u};
+  const cuuint64_t str[3] = {wb, wb * heads, 128};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)rows,
+                             whole && all ? (cuuint32_t)(width / 64) : 1u};
+  return encode(map, bf16, base, 4, dims, str, box);
+}
+
 template <typename T, bool CAP>
 cudaError_t launch(const Geometry& g, const DiffArgs& a, const PreArgs& A, int64_t units) {
   static std::atomic<bool> configured[64];
@@ -600,25 +745,18 @@ cudaError_t launch(const Geometry& g, const DiffArgs& a, const PreArgs& A, int64
   const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   const cuuint64_t slots = (cuuint64_t)g.num_blocks * g.bs, hb = (cuuint64_t)g.hs * 2;
   CUtensorMap kmap, vmap, qmap;
-  {
-    const cuuint64_t dims[3] = {(cuuint64_t)g.hs, (cuuint64_t)(2 * g.kvh), slots};
-    const cuuint64_t str[2] = {hb, hb * 2 * g.kvh};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)P.box_rows};
-    if ((e = encode(&kmap, bf16, a.key_cache, 3, dims, str, box)) != cudaSuccess) return e;
-  }
-  {
-    const cuuint64_t dims[3] = {(cuuint64_t)g.vhs, (cuuint64_t)g.kvh, slots};
-    const cuuint64_t str[2] = {(cuuint64_t)g.vhs * 2, (cuuint64_t)g.vhs * 2 * g.kvh};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)P.box_rows};
-    if ((e = encode(&vmap, bf16, a.value_cache, 3, dims, str, box)) != cudaSuccess) return e;
-  }
+  e = cache_map(&kmap, bf16, a.key_cache, g.hs, 2 * g.kvh, slots, P.box_rows, P.box_rows == kN);
+  if (e == cudaSuccess)
+    e = cache_map(&vmap, bf16, a.value_cache, g.vhs, g.kvh, slots, A.v_rows, A.v_rows == kVKeys);
+  if (e != cudaSuccess) return e;
   {  // query [T][H][2][hs]: boxes of 64 channels x one map x grp heads x tpc tokens
     const cuuint64_t dims[4] = {(cuuint64_t)g.hs, 2, (cuuint64_t)g.H, (cuuint64_t)a.num_tokens};
     const cuuint64_t str[3] = {hb, 2 * hb, 2 * hb * g.H};
     const cuuint32_t box[4] = {64, 1, (cuuint32_t)P.grp, (cuuint32_t)P.tpc};
     if ((e = encode(&qmap, bf16, a.query, 4, dims, str, box)) != cudaSuccess) return e;
   }
-  const size_t smem = 1024 + (size_t)P.q_bytes + (size_t)P.stages * P.stage_bytes;
+  const size_t smem =
+      1024 + (size_t)P.q_bytes + (size_t)A.nk * P.k_bytes + (size_t)A.nv * A.v_bytes;
   return launch_pdl(kern, dim3((unsigned)(units * g.kvh * 2)), dim3(kPreThreads), smem, a.stream,
                     kmap, vmap, qmap, A);
 }
@@ -666,9 +804,15 @@ cudaError_t launch_prefill(const Geometry& g, const DiffArgs& a) {
   P.vg = 64 * P.vslabs;
   P.q_bytes = P.slabs * kBox;
   P.k_bytes = P.slabs * kBox;
-  P.stage_bytes = (P.slabs + P.vslabs) * kBox;
-  P.stages = (int)((kSmemMax - 1024 - P.q_bytes) / P.stage_bytes);
-  if (P.stages > kMaxStages) P.stages = kMaxStages;
+  A.v_rows = g.bs < kVKeys ? g.bs : kVKeys;
+  A.v_bytes = P.vslabs * kVBox;
+  // four key tiles (two of 32 KB), the rest for values: at least four halves
+  A.nk = P.slabs == 1 ? 4 : 2;
+  A.nv = (int)((kSmemMax - 1024 - P.q_bytes - (size_t)A.nk * P.k_bytes) / A.v_bytes);
+  if (A.nv > kMaxV) A.nv = kMaxV;
+  A.nv &= ~1;  // (the two value warps have slots of their own)
+  A.k_whole = g.hs % 64 == 0;
+  A.v_whole = g.vhs % 64 == 0;
   A.hs = g.hs;
   A.lambda_vectors = a.lambda_vectors;
   A.norm_weight = a.norm_weight;
