@@ -63,7 +63,7 @@ constexpr size_t kSmemMax = 225 * 1024;
 struct PreBars {
   uint64_t k_full[kMaxK], k_empty[kMaxK], v_full[kMaxV], v_empty[kMaxV];
   uint64_t s_full, s_free, p_full[2], pv_done[2];
-  uint64_t q_tma, q_full, drain;
+  uint64_t q_tma, q_full, drain, x_full;
   uint32_t tmem_base;
   int bad, abort;
 };
@@ -91,10 +91,29 @@ __device__ __forceinline__ uint64_t pack_f32(float a, float b) {
 __device__ __forceinline__ void unpack_f32(uint64_t v, float* a, float* b) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v));
 }
-__device__ __forceinline__ void st_peer4(uint32_t raddr, float a, float b, float c, float d) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(raddr), "f"(a), "f"(b),
-               "f"(c), "f"(d)
-               : "memory");
+// `bytes` of this CTA's shared memory into the peer's, counted on its barrier.
+__device__ __forceinline__ void bulk_copy_peer(uint32_t dst, uint32_t src, uint32_t bytes,
+                                               uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+      "[%3];" ::"r"(dst), "r"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]),
+                 "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 __device__ __forceinline__ void st_peer(uint32_t raddr, float a) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(raddr), "f"(a) : "memory");
@@ -191,6 +210,46 @@ __device__ __forceinline__ float exp_row(uint32_t (&r)[32], uint32_t (&pk)[16], 
   return (a + b) + (c + d);
 }
 
+// prefill_group_warp for up to 32 sequences: one round of loads, the rest in
+// registers (a chain of three rounds was 2000 cycles of every unit's start).
+__device__ __forceinline__ Work unit_warp(const Params& P, int unit, int lane) {
+  const int nseq = P.pf_end - P.pf_begin;
+  if (nseq > 32) return prefill_group_warp(P, unit, P.tpc);
+  int q0 = 0, q1 = 0, past = 0;
+  if (lane < nseq) {
+    q0 = P.cumseq[P.pf_begin + lane];
+    q1 = P.cumseq[P.pf_begin + lane + 1];
+    past = P.past[P.pf_begin + lane];
+  }
+  const int cnt = q1 > q0 ? ceil_div32(q1 - q0, P.tpc) : 0;
+  int incl = cnt;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  Work w;
+  w.status = 1;
+  w.splits = 1;
+  w.ntok = 0;
+  w.decode = 0;
+  const int u = __shfl_sync(0xffffffffu, incl, 31) - 1 - unit;  // the last tokens first
+  const unsigned who = __ballot_sync(0xffffffffu, u >= 0 && u >= incl - cnt && u < incl);
+  if (who) {
+    const int src = __ffs(who) - 1;
+    const int g = __shfl_sync(0xffffffffu, u - (incl - cnt), src);
+    const int first = __shfl_sync(0xffffffffu, q0, src);
+    const int len = __shfl_sync(0xffffffffu, q1 - q0, src);
+    w.past = __shfl_sync(0xffffffffu, past, src);
+    w.b = P.pf_begin + src;
+    w.t = first + (int64_t)g * P.tpc;
+    w.ntok = min(P.tpc, len - g * P.tpc);
+    w.pos = w.past + (int64_t)g * P.tpc;
+    w.status = 0;
+  }
+  return w;
+}
+
 template <typename T, bool CAP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPreThreads, 1)
 diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -200,15 +259,17 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   __shared__ Work work;
   __shared__ PreBars bars_s;
   __shared__ float s_max[2][kRows];
+  __shared__ int s_again[2][2][4];  // [tile parity][half][quadrant]
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
   uint8_t* q_s = smem;
   uint8_t* k_s = smem + P.q_bytes;         // key slots: slabs of kN rows
   uint8_t* v_s = k_s + A.nk * P.k_bytes;   // value slots: slabs of kVKeys rows
-  // in the query's place, once the last QK^T is done: the halves' sums, and
-  // [CTA * 2 + half] sums of squares, the peer's too
+  // in the query's place, once the last QK^T is done: the halves' sums,
+  // [CTA * 2 + half] sums of squares (the peer's too), and the norm's weights
   float (*s_sum)[kRows] = reinterpret_cast<float (*)[kRows]>(q_s);
   float (*s_ss)[kRows] = s_sum + 2;
+  uint4* s_norm = reinterpret_cast<uint4*>(s_ss + 4);  // the norm's weights
   PreBars* bars = &bars_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slabs = P.slabs, vslabs = P.vslabs, vg = P.vg;
@@ -219,7 +280,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 
   if (warp == 0) {
     if (!P.early) grid_dep_wait();
-    Work w = prefill_group_warp(P, unit, P.tpc);
+    Work w = unit_warp(P, unit, lane);
     if (w.status == 0) {
       const int64_t pos_hi = w.pos + w.ntok - 1;
       const bool bad_ctx = w.past < 0 || pos_hi >= (int64_t)P.max_blocks * P.bs || w.t < 0 ||
@@ -260,6 +321,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     mbar_init(smem_u32(&bars->q_tma), 1);
     mbar_init(smem_u32(&bars->q_full), kSoftWarps);
     mbar_init(smem_u32(&bars->drain), 1);
+    mbar_init(smem_u32(&bars->x_full), 1);
     bars->bad = 0;
     bars->abort = 0;
     fence_barrier_init();
@@ -325,8 +387,8 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       float m_used = -INFINITY, l = 0.f;
       const float sl = CAP ? 1.f : P.scale_log2;
       // Every warp goes through all n tiles and meets its partner of the
-      // quadrant twice in each; after a wait that gave up (ok false) it does
-      // nothing else.
+      // quadrant in each; after a wait that gave up (ok false) it does nothing
+      // else.
 #pragma unroll 1
       for (int k = 0; k < n; ++k) {
         const int pb = k & 1;
@@ -366,8 +428,32 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             fence_proxy_async();
           }
         }
-        float factor = 1.f;
-        bool rescale = false;
+        // The exponentials use the running maximum as it stands; the tile's own
+        // maximum is taken beside them, and only if it passes the running one by
+        // more than 2^8 (or there is none yet) do the two warps of the quadrant
+        // exchange maxima and compute the tile again. Waiting for the exchange
+        // first cost 400 of 1900 cycles a tile.
+        const uint32_t dst = lane_addr + col_p + pb * 64 + half * 32;
+        float vmax = -INFINITY, lsum = 0.f;
+        auto exps = [&]() {
+          const float mu = m_used == -INFINITY ? 0.f : m_used;
+          uint32_t pk[16];
+          if (CAP) {
+            const ExpArgs E{sl, mu, P.cap_in, P.cap_out, 0.f, 0.f, 0.f, 0.f, 0.f};
+            lsum = exp_chunk<T, 2>(s[0], pk, E);
+            tmem_st16(dst, pk);
+            lsum += exp_chunk<T, 2>(s[1], pk, E);
+          } else {
+            lsum = exp_row<T>(s[0], pk, sl, -mu);
+            tmem_st16(dst, pk);
+            lsum += exp_row<T>(s[1], pk, sl, -mu);
+          }
+          tmem_st16(dst + 16, pk);
+        };
+        auto score = [&](float v) {  // log2-domain score of a raw one
+          return !CAP ? v * sl : v == -INFINITY ? -INFINITY : P.cap_out * tanh_ex2(v * P.cap_in);
+        };
+        bool again = false;
         if (live && ok) {
           if (edge) {
             const int c0 = (int)min((int64_t)kN, max((int64_t)0, lo_r - j0)) - half * 64;
@@ -378,6 +464,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
               for (int e = 0; e < 32; ++e)
                 if (c * 32 + e < c0 || c * 32 + e > c1) s[c][e] = __float_as_uint(-INFINITY);
           }
+          if (k > 0) exps();
           float v[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -388,61 +475,58 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
               v[c] = fmaxf(v[c], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
             v[c] = fmaxf(v[c], __uint_as_float(x[15]));
           }
-          s_max[half][row] = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+          vmax = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+          again = __any_sync(0xffffffffu,
+                             row < rows && (m_used == -INFINITY ||
+                                            score(vmax) > m_used + kRescaleLog2));
         }
-        if (live) named_sync(1 + (warp & 3), 64);
-        if (live && ok) {
-          const float vmax = fmaxf(s_max[0][row], s_max[1][row]);
-          const float mt = !CAP ? vmax * sl
-                           : vmax == -INFINITY ? -INFINITY
-                                               : P.cap_out * tanh_ex2(vmax * P.cap_in);
-          if (m_used == -INFINITY) {
-            m_used = mt;  // (nothing but zeros was added before a first visible key)
-          } else if (mt > m_used + kRescaleLog2) {
-            factor = ex2(m_used - mt);
-            m_used = mt;
-            l *= factor;
-            rescale = true;
-          }
-          const float mu = m_used == -INFINITY ? 0.f : m_used;
-          const uint32_t dst = lane_addr + col_p + pb * 64 + half * 32;
-          uint32_t pk[16];
-          if (CAP) {
-            const ExpArgs E{sl, mu, P.cap_in, P.cap_out, 0.f, 0.f, 0.f, 0.f, 0.f};
-            l += exp_chunk<T, 2>(s[0], pk, E);
-            tmem_st16(dst, pk);
-            l += exp_chunk<T, 2>(s[1], pk, E);
-            tmem_st16(dst + 16, pk);
-          } else {
-            l += exp_row<T>(s[0], pk, sl, -mu);
-            tmem_st16(dst, pk);
-            l += exp_row<T>(s[1], pk, sl, -mu);
-            tmem_st16(dst + 16, pk);
-          }
-          if (__any_sync(0xffffffffu, rescale)) {
-            // (k >= 1) each half scales half of O, once the PV before has added to it
-            ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->pv_done[(k - 1) & 1]),
-                                                  ((k - 1) >> 1) & 1, abort, P.err_flags));
+        if (live) {
+          if (lane == 0) s_again[pb][half][warp & 3] = again ? 1 : 0;
+          named_sync(1 + (warp & 3), 64);
+          if (s_again[pb][0][warp & 3] | s_again[pb][1][warp & 3]) {
+            s_max[half][row] = vmax;
+            named_sync(1 + (warp & 3), 64);
             if (ok) {
-              tc_fence_after();
+              const float mt = score(fmaxf(s_max[0][row], s_max[1][row]));
+              float factor = 1.f;
+              bool rescale = false;
+              if (m_used == -INFINITY) {
+                m_used = mt;  // (nothing but zeros was added before a first visible key)
+              } else if (mt > m_used + kRescaleLog2) {
+                factor = ex2(m_used - mt);
+                m_used = mt;
+                l *= factor;
+                rescale = true;
+              }
+              exps();
+              if (__any_sync(0xffffffffu, rescale)) {
+                // (k >= 1) each half scales half of O, once the PV before has added to it
+                ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->pv_done[(k - 1) & 1]),
+                                                      ((k - 1) >> 1) & 1, abort, P.err_flags));
+                if (ok) {
+                  tc_fence_after();
 #pragma unroll 1
-              for (int c = half * (vg >> 1); c < (half + 1) * (vg >> 1); c += 16) {
-                uint32_t r[16];
-                tmem_ld16(lane_addr + c, r);
+                  for (int c = half * (vg >> 1); c < (half + 1) * (vg >> 1); c += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(lane_addr + c, r);
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  r[e] = __float_as_uint(__uint_as_float(r[e]) * factor);
-                tmem_st16(lane_addr + c, r);
+                    for (int e = 0; e < 16; ++e)
+                      r[e] = __float_as_uint(__uint_as_float(r[e]) * factor);
+                    tmem_st16(lane_addr + c, r);
+                  }
+                }
               }
             }
           }
+          l += lsum;
           tmem_wait_st();
           tc_fence_before();
         }
         if (ok) arrive_warp(&bars->p_full[pb], lane);
-        if (live) named_sync(1 + (warp & 3), 64);  // before s_max is used again
       }
       grid_dep_launch();
+      uint4 nw = make_uint4(0, 0, 0, 0);
+      if (tid * 8 < vhs) nw = reinterpret_cast<const uint4*>(A.norm_weight)[tid];
       named_sync(5, kSoft);
       ok = __all_sync(0xffffffffu, ok && !*abort);
       if (ok && n > 0)
@@ -450,6 +534,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                                               ((n - 1) >> 1) & 1, abort, P.err_flags));
       tc_fence_after();
       if (live) s_sum[half][row] = l;
+      if (tid * 8 < vhs) s_norm[tid] = nw;
       named_sync(5, kSoft);
       const float lt = s_sum[0][row] + s_sum[1][row];
       coef = lt > 0.f ? (map == 0 ? 1.f : lam) / lt : 0.f;
@@ -607,43 +692,71 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   }
 
   // =================== epilogue ===================
-  // The cluster barriers are met by every thread of both CTAs, whatever the
-  // unit's state. First: nobody uses the rings any more.
-  const int cols = vg >> 2;  // columns a thread sends, and columns it finishes
-  cluster_sync_all();
-  if (live && ok && n > 0) {
-    const uint32_t peer = map_peer(smem_u32(k_s), 1 - map);
-    const int c0 = half * cols;  // within the peer's half of the channels
-#pragma unroll 1
-    for (int c = 0; c < cols; c += 16) {
-      uint32_t r[16];
-      tmem_ld16(lane_addr + (1 - map) * (vg >> 1) + c0 + c, r);
+  // CTA r finishes channels [r vg / 2, (r + 1) vg / 2). The cluster barriers are
+  // met by every thread of both CTAs, whatever the unit's state.
+  const int cols = vg >> 2;  // columns a thread hands over, and columns it finishes
+  const int xbytes = kRows * vg * 2;  // half the channels of every row, f32
+  uint8_t* x_out = k_s;               // in the rings, which nobody uses any more
+  uint8_t* x_in = k_s + xbytes;
+  const bool fin = live && ok && n > 0;
+  // 16-byte chunk ch of row r stands at ch ^ (r & 7)
+  auto chunk = [&](uint8_t* at, int pitch, int ch) {
+    return at + row * pitch + ((ch ^ (row & 7)) << 4);
+  };
+  uint32_t r[4][16];
+  auto load_cols = [&](int first) {  // this thread's columns from `first` on
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int ch = ((c0 + c) >> 2) + e;
-        st_peer4(peer + row * vg * 2 + ((ch ^ (row & 7)) << 4), __uint_as_float(r[4 * e]) * coef,
-                 __uint_as_float(r[4 * e + 1]) * coef, __uint_as_float(r[4 * e + 2]) * coef,
-                 __uint_as_float(r[4 * e + 3]) * coef);
+    for (int c = 0; c < 4; ++c)
+      if (c * 16 < cols) tmem_ld16_nowait(lane_addr + first + half * cols + c * 16, r[c]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) reg_fence16(r[c]);
+  };
+  if (fin) {
+    load_cols((1 - map) * (vg >> 1));
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (c * 16 < cols) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<float4*>(chunk(x_out, vg * 2, ((half * cols + c * 16) >> 2) + e)) =
+              make_float4(__uint_as_float(r[c][4 * e]) * coef, __uint_as_float(r[c][4 * e + 1]) * coef,
+                          __uint_as_float(r[c][4 * e + 2]) * coef,
+                          __uint_as_float(r[c][4 * e + 3]) * coef);
       }
-    }
+    fence_proxy_async();
   }
-  cluster_sync_all();
+  cluster_sync_all();  // also: the peer's rings are free, its outgoing columns written
+  if (run && warp == 0) {
+    if (elect_one()) {
+      mbar_expect_tx(smem_u32(&bars->x_full), (uint32_t)xbytes);
+      if (ok)
+        bulk_copy_peer(map_peer(smem_u32(x_in), 1 - map), smem_u32(x_out), (uint32_t)xbytes,
+                       map_peer(smem_u32(&bars->x_full), 1 - map));
+    }
+    __syncwarp();
+  }
   float x[64], ss = 0.f;
-  if (live && ok && n > 0) {
+  if (run && warp < kSoftWarps) {
+    if (fin) load_cols(map * (vg >> 1));
+    if (ok)
+      ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->x_full), 0, abort, P.err_flags));
+    else if (tid == 0)  // the peer may write into this CTA until then
+      drain_wait(smem_u32(&bars->x_full), 0, P.err_flags);
+    __syncwarp();
+  }
+  if (fin && ok) {
 #pragma unroll
     for (int c = 0; c < 64; c += 16) {
       if (c < cols) {
-        uint32_t r[16];
-        tmem_ld16(lane_addr + map * (vg >> 1) + half * cols + c, r);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int ch = ((half * cols + c) >> 2) + e;
           const float4 p =
-              *reinterpret_cast<const float4*>(k_s + row * vg * 2 + ((ch ^ (row & 7)) << 4));
+              *reinterpret_cast<const float4*>(chunk(x_in, vg * 2, ((half * cols + c) >> 2) + e));
           const float pv[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float own = __uint_as_float(r[4 * e + i]) * coef;
+            const float own = __uint_as_float(r[c >> 4][4 * e + i]) * coef;
             const float d = map == 0 ? own - pv[i] : pv[i] - own;
             x[c + 4 * e + i] = d;
             ss = fmaf(d, d, ss);
@@ -655,39 +768,37 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     st_peer(map_peer(smem_u32(&s_ss[map * 2 + half][row]), 1 - map), ss);
   }
   cluster_sync_all();
-  // the finished 16-bit channels go through shared memory (behind the received
-  // ones), so that a warp writes whole rows: 2 rows of 256 bytes at vg 256
-  uint8_t* o_s = k_s + kRows * vg * 2;
+  // the finished 16-bit channels go through shared memory, so that a warp
+  // writes whole rows: 2 rows of 256 bytes at vg 256
   const int pitch = vg <= 128 ? 128 : 256;
   const int first = map * (vg >> 1);  // this CTA's channels
-  if (live && ok && n > 0) {
+  if (fin && ok) {
     ss = (s_ss[0][row] + s_ss[1][row]) + (s_ss[2][row] + s_ss[3][row]);
     const float inv =
         bars->bad ? 0.f : (1.f - A.lambda_init) / sqrtf(ss / (float)vhs + A.norm_eps);
-    const T* nw = reinterpret_cast<const T*>(A.norm_weight) + first + half * cols;
 #pragma unroll
     for (int c = 0; c < 64; c += 8) {
-      if (c < cols && first + half * cols + c < vhs) {
+      const int ch = half * cols + c;
+      if (c < cols && first + ch < vhs) {
         float w[8], o[8];
-        unpack8<T>(*reinterpret_cast<const uint4*>(nw + c), w);
+        unpack8<T>(s_norm[(first + ch) >> 3], w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = bars->bad ? 0.f : x[c + e] * inv * w[e];
-        *reinterpret_cast<uint4*>(o_s + row * pitch + ((((half * cols + c) >> 3) ^ (row & 7)) << 4)) =
-            pack8<T>(o);
+        *reinterpret_cast<uint4*>(chunk(x_out, pitch, ch >> 3)) = pack8<T>(o);
       }
     }
   }
-  if (warp < kSoftWarps) {
+  if (run && warp < kSoftWarps) {
     named_sync(5, kSoft);
-    ok = ok && !*abort;
-    const int nc = max(0, min(vg >> 1, vhs - first)) >> 3;  // 16-byte pieces of a row
-    if (ok && n > 0) {
-      for (int i = tid; i < rows * nc; i += kSoft) {
-        const int r = i / nc, c = i - r * nc;
-        T* dst = reinterpret_cast<T*>(P.out) +
-                 ((W.t + r / grp) * P.H + gk * grp + r % grp) * (int64_t)vhs + first + c * 8;
-        *reinterpret_cast<uint4*>(dst) =
-            *reinterpret_cast<const uint4*>(o_s + r * pitch + ((c ^ (r & 7)) << 4));
+    // 16 lanes a row; r / grp by a product (rows below 128)
+    const int nc = max(0, min(vg >> 1, vhs - first)) >> 3, c = lane & 15;
+    const uint32_t inv_grp = 65536u / (uint32_t)grp + 1u;
+    if (ok && !*abort && c < nc) {
+      T* base = reinterpret_cast<T*>(P.out) + (W.t * P.H + gk * grp) * (int64_t)vhs + first + c * 8;
+      for (int q = warp * 2 + (lane >> 4); q < rows; q += kSoftWarps * 2) {
+        const int tok = (int)(((uint32_t)q * inv_grp) >> 16);
+        *reinterpret_cast<uint4*>(base + ((int64_t)tok * P.H + (q - tok * grp)) * vhs) =
+            *reinterpret_cast<const uint4*>(x_out + q * pitch + ((c ^ (q & 7)) << 4));
       }
     }
   }
