@@ -8,6 +8,7 @@ safe to record into a CUDA graph after one eager call.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Optional
 
 import torch
@@ -206,6 +207,14 @@ def _require(ok: bool, message: str):
         raise B.PaError(B.PA_ERR_INVALID_ARGUMENT, message)
 
 
+_NOTHING = contextlib.nullcontext()
+
+
+def _device(index: int):
+    """Makes a device current for a block (nothing to do where it is)."""
+    return _NOTHING if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+
 class DifferentialAttention:
     """Differential attention over paged caches (include/pa_diff.h): two query
     and key maps per head and one value, the difference of the two softmax
@@ -244,76 +253,80 @@ class DifferentialAttention:
         self.params_after_write.flags |= B.PA_FLAG_AFTER_WRITE | (
             B.PA_FLAG_OWN_SLOTS if own_slots else 0)
         self.device = torch.empty(0, device=device).device
+        self._index = self.device.index
         self.max_seqs, self.max_tokens = max_seqs, max_tokens
-        with torch.cuda.device(self.device):
+        with _device(self._index):
             n = B.pa_diff_workspace_size(self.params, max_seqs, max_tokens)
         self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
         self.err_flags = torch.zeros(1, dtype=torch.int32, device=self.device)
 
-    def _check(self, halves, ints, lambda_vectors=None):
-        p = self.params
-        for name, t, last in halves:
-            _require(t.dtype == self.dtype and t.device == self.device and t.is_contiguous()
-                     and (last is None or t.shape[-1] == last),
-                     f"{name} must be a contiguous {self.dtype} tensor on {self.device}"
-                     + ("" if last is None else f" with {last} columns"))
-        for name, t in ints:
-            _require(t.dtype == torch.int32 and t.device == self.device and t.is_contiguous(),
-                     f"{name} must be a contiguous int32 tensor on {self.device}")
-        if lambda_vectors is not None:
-            _require(lambda_vectors.dtype == torch.float32 and lambda_vectors.is_contiguous()
-                     and lambda_vectors.device == self.device
-                     and lambda_vectors.numel() == 4 * p.head_size,
-                     "lambda_vectors must be a contiguous float32 [4, head_size] tensor")
+    # -- argument checks: types, devices and sizes the C side cannot see
+    def _tensors(self, dtype, **tensors):
+        for name, t in tensors.items():
+            if t.dtype is not dtype or t.get_device() != self._index or not t.is_contiguous():
+                _require(False, f"{name} must be a contiguous {dtype} tensor on {self.device}")
 
-    def _check_caches(self, key_cache, value_cache, cos_cache, sin_cache):
-        p = self.params
+    def _check_caches(self, key_cache, value_cache, cos_cache, sin_cache, cumseq, past):
+        p, hs, vhs = self.params, self.head_size, self.v_head_size
+        self._tensors(self.dtype, key_cache=key_cache, value_cache=value_cache)
+        self._tensors(torch.int32, cumseq=cumseq, past=past)
         rows = p.num_blocks * p.block_size * p.kv_num_heads
-        self._check([("key_cache", key_cache, p.head_size),
-                     ("value_cache", value_cache, self.v_head_size)]
-                    + ([("cos_cache", cos_cache, p.rotary_dim // 2),
-                        ("sin_cache", sin_cache, p.rotary_dim // 2)] if p.rotary_dim else []), [])
-        _require(key_cache.numel() == rows * 2 * p.head_size
-                 and value_cache.numel() == rows * self.v_head_size,
+        _require(key_cache.numel() == rows * 2 * hs and value_cache.numel() == rows * vhs,
                  "key_cache must be [num_blocks, bs, kvH, 2, hs], value_cache [num_blocks, bs, "
                  "kvH, vhs]")
-        _require(not p.rotary_dim or (cos_cache.shape[0] >= p.cos_rows
-                                      and sin_cache.shape[0] >= p.cos_rows),
-                 "cos_cache and sin_cache must have cos_rows rows")
+        _require(cumseq.numel() == past.numel() + 1, "cumseq must be [num_seqs + 1]")
+        if p.rotary_dim:
+            self._tensors(self.dtype, cos_cache=cos_cache, sin_cache=sin_cache)
+            n = p.cos_rows * (p.rotary_dim // 2)
+            _require(cos_cache.shape[-1] == sin_cache.shape[-1] == p.rotary_dim // 2
+                     and cos_cache.numel() >= n and sin_cache.numel() >= n,
+                     "cos_cache and sin_cache must be [cos_rows, rotary_dim / 2]")
+
+    def _check_write(self, key, value, slot_mapping):
+        self._tensors(self.dtype, key=key, value=value)
+        self._tensors(torch.int32, slot_mapping=slot_mapping)
+        n = key.shape[0]
+        _require(key.numel() == n * self.kv_num_heads * 2 * self.head_size
+                 and value.shape[0] == n and value.numel() == n * self.kv_num_heads * self.v_head_size
+                 and slot_mapping.numel() == n,
+                 "key must be [T, kvH*2*hs], value [T, kvH*vhs], slot_mapping [T]")
+
+    def _check_read(self, query, lambda_vectors, norm_weight, past, block_table, out):
+        self._tensors(self.dtype, query=query, norm_weight=norm_weight, out=out)
+        self._tensors(torch.int32, block_table=block_table)
+        self._tensors(torch.float32, lambda_vectors=lambda_vectors)
+        n = query.shape[0]
+        _require(query.numel() == n * self.num_heads * 2 * self.head_size
+                 and out.shape[0] == n and out.numel() == n * self.num_heads * self.v_head_size
+                 and norm_weight.numel() == self.v_head_size
+                 and lambda_vectors.numel() == 4 * self.head_size
+                 and block_table.numel() == past.numel() * self.params.max_blocks_per_seq,
+                 "query must be [T, H*2*hs], out [T, H*vhs], norm_weight [vhs], lambda_vectors "
+                 "[4, hs], block_table [num_seqs, max_blocks_per_seq]")
+
+    def _on_device(self):
+        return _device(self._index)
 
     def write(self, key, value, key_cache, value_cache, cos_cache, sin_cache, slot_mapping,
               cumseq, past, stream=None):
         """Rotates the new keys and stores keys and values in their slots."""
-        p = self.params
-        self._check([("key", key, p.kv_num_heads * 2 * p.head_size),
-                     ("value", value, p.kv_num_heads * self.v_head_size)],
-                    [("slot_mapping", slot_mapping), ("cumseq", cumseq), ("past", past)])
-        self._check_caches(key_cache, value_cache, cos_cache, sin_cache)
-        _require(value.shape[0] == key.shape[0] == slot_mapping.numel()
-                 and cumseq.numel() == past.numel() + 1,
-                 "key, value and slot_mapping must have a row per token, cumseq num_seqs + 1")
-        with torch.cuda.device(self.device):
+        self._check_caches(key_cache, value_cache, cos_cache, sin_cache, cumseq, past)
+        self._check_write(key, value, slot_mapping)
+        with self._on_device():
             B.pa_diff_write(self.params, key, value, cos_cache, sin_cache, slot_mapping, cumseq,
                             past, key_cache, value_cache, self.err_flags, stream)
 
-    def _read(self, fn, query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
-              norm_weight, cumseq, past, block_table, out, seq_begin, seq_end, stream,
-              after_write):
-        p = self.params
-        self._check([("query", query, p.num_heads * 2 * p.head_size),
-                     ("norm_weight", norm_weight, self.v_head_size),
-                     ("out", out, p.num_heads * self.v_head_size)],
-                    [("cumseq", cumseq), ("past", past), ("block_table", block_table)],
-                    lambda_vectors)
-        self._check_caches(key_cache, value_cache, cos_cache, sin_cache)
-        _require(out.shape[0] == query.shape[0] and cumseq.numel() == past.numel() + 1
-                 and block_table.numel() == past.numel() * p.max_blocks_per_seq,
-                 "out must have a row per token, cumseq num_seqs + 1 entries and block_table "
-                 "[num_seqs, max_blocks_per_seq]")
-        with torch.cuda.device(self.device):
-            fn(self.params_after_write if after_write else p, query, key_cache, value_cache,
-               cos_cache, sin_cache, lambda_vectors, norm_weight, cumseq, past, block_table, out,
-               seq_begin, seq_end, self.workspace, self.err_flags, stream)
+    def _read(self, fn, args, seq_begin, seq_end, stream, after_write):
+        fn(self.params_after_write if after_write else self.params, *args, seq_begin, seq_end,
+           self.workspace, self.err_flags, stream)
+
+    def _read_checked(self, fn, args, *rest):
+        (query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors, norm_weight, cumseq,
+         past, block_table, out) = args
+        self._check_caches(key_cache, value_cache, cos_cache, sin_cache, cumseq, past)
+        self._check_read(query, lambda_vectors, norm_weight, past, block_table, out)
+        with self._on_device():
+            self._read(fn, args, *rest)
 
     def decode(self, query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
                norm_weight, cumseq, past, block_table, out, seq_begin=0, seq_end=None,
@@ -321,17 +334,19 @@ class DifferentialAttention:
         """Sequences [seq_begin, seq_end) with one new token each.
         ``after_write``: this call directly follows ``write`` on the same
         stream (see PA_FLAG_AFTER_WRITE)."""
-        self._read(B.pa_diff_decode, query, key_cache, value_cache, cos_cache, sin_cache,
-                   lambda_vectors, norm_weight, cumseq, past, block_table, out, seq_begin,
-                   seq_end, stream, after_write)
+        self._read_checked(B.pa_diff_decode,
+                           (query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
+                            norm_weight, cumseq, past, block_table, out),
+                           seq_begin, seq_end, stream, after_write)
 
     def prefill(self, query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
                 norm_weight, cumseq, past, block_table, out, seq_begin=0, seq_end=None,
                 stream=None, after_write: bool = False):
         """Sequences [seq_begin, seq_end) with any number of new tokens."""
-        self._read(B.pa_diff_prefill, query, key_cache, value_cache, cos_cache, sin_cache,
-                   lambda_vectors, norm_weight, cumseq, past, block_table, out, seq_begin,
-                   seq_end, stream, after_write)
+        self._read_checked(B.pa_diff_prefill,
+                           (query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
+                            norm_weight, cumseq, past, block_table, out),
+                           seq_begin, seq_end, stream, after_write)
 
     def forward(self, query, key, value, key_cache, value_cache, cos_cache, sin_cache,
                 lambda_vectors, norm_weight, cumseq, past, block_table, slot_mapping,
@@ -340,17 +355,29 @@ class DifferentialAttention:
         """Write phase over all tokens, then decode over sequences [0,
         num_decode_seqs) and prefill over the rest; returns ``out``."""
         nseq = past.shape[0]
-        if out is None:
-            out = torch.empty(query.shape[0], self.num_heads * self.v_head_size,
-                              dtype=self.dtype, device=query.device)
-        self.write(key, value, key_cache, value_cache, cos_cache, sin_cache, slot_mapping,
-                   cumseq, past, stream)
-        args = (query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors, norm_weight,
-                cumseq, past, block_table, out)
-        if num_decode_seqs > 0:
-            self.decode(*args, 0, num_decode_seqs, stream, after_write=True)
-        if num_decode_seqs < nseq:
-            self.prefill(*args, num_decode_seqs, nseq, stream, after_write=num_decode_seqs == 0)
+        _require(0 <= num_decode_seqs <= nseq, "num_decode_seqs must be in 0..num_seqs")
+        with self._on_device():
+            if out is None:
+                shape = (query.shape[0], self.num_heads * self.v_head_size)
+                if isinstance(stream, torch.cuda.Stream):  # memory of the stream that writes it
+                    with torch.cuda.stream(stream):
+                        out = torch.empty(shape, dtype=self.dtype, device=self.device)
+                else:
+                    out = torch.empty(shape, dtype=self.dtype, device=self.device)
+            stream = B.raw_stream(stream)
+            self._check_caches(key_cache, value_cache, cos_cache, sin_cache, cumseq, past)
+            self._check_write(key, value, slot_mapping)
+            self._check_read(query, lambda_vectors, norm_weight, past, block_table, out)
+            _require(key.shape[0] == query.shape[0], "query and key must have a row per token")
+            B.pa_diff_write(self.params, key, value, cos_cache, sin_cache, slot_mapping, cumseq,
+                            past, key_cache, value_cache, self.err_flags, stream)
+            args = (query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
+                    norm_weight, cumseq, past, block_table, out)
+            if num_decode_seqs > 0:
+                self._read(B.pa_diff_decode, args, 0, num_decode_seqs, stream, True)
+            if num_decode_seqs < nseq:
+                self._read(B.pa_diff_prefill, args, num_decode_seqs, nseq, stream,
+                           num_decode_seqs == 0)
         return out
 
     def error_flags(self) -> int:
@@ -386,6 +413,7 @@ class PagePool:
         _require(len(self.caches) > 0, "a pool needs at least one cache")
         first = self.caches[0]
         self.device, self.num_blocks = first.device, int(first.shape[0])
+        self._index = self.device.index
         _require(self.device.type == "cuda", "caches must be CUDA tensors")
         for c in self.caches:
             _require(c.device == self.device and c.dim() >= 2 and int(c.shape[0]) == self.num_blocks
@@ -424,11 +452,11 @@ class PagePool:
 
     def _ints(self, **tensors):
         for name, t in tensors.items():
-            _require(t.dtype == torch.int32 and t.device == self.device and t.is_contiguous(),
-                     f"{name} must be a contiguous int32 tensor on {self.device}")
+            if t.dtype is not torch.int32 or t.get_device() != self._index or not t.is_contiguous():
+                _require(False, f"{name} must be a contiguous int32 tensor on {self.device}")
 
     def _call(self, fn, *args, stream):
-        with torch.cuda.device(self.device):
+        with _device(self._index):
             fn(self.params, *args, err_flags=self.err_flags, stream=stream)
 
     def copy(self, src, dst, rows=None, stream=None):

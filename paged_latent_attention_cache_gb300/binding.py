@@ -428,6 +428,20 @@ def make_page_caches(caches):
     return arr
 
 
+# the current stream's handle without a Stream object (3 us apiece)
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def raw_stream(stream) -> int:
+    if type(stream) is int:
+        return stream
+    if stream is None:
+        if _current_raw is not None:
+            return _current_raw(torch.cuda.current_device())
+        stream = torch.cuda.current_stream()
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
 def pa_pages_validate(p: pa_pages_params) -> int:
     return int(lib.pa_pages_validate(ctypes.byref(p)))
 
@@ -436,42 +450,46 @@ def pa_pages_workspace_size(p: pa_pages_params) -> int:
     return int(lib.pa_pages_workspace_size(ctypes.byref(p)))
 
 
+def _addr(t: Optional[torch.Tensor]):
+    """The address as a plain int (the argument types make it a pointer)."""
+    return None if t is None else t.data_ptr()
+
+
 def _ws(workspace):
-    n = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    return _ptr(workspace), ctypes.c_size_t(n)
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
 
 
 def pa_pages_copy(p, caches, num_caches, src, dst, rows, workspace, err_flags=None, stream=None):
-    _check(lib.pa_pages_copy(ctypes.byref(p), caches, int(num_caches), _ptr(src), _ptr(dst),
-                             _ptr(rows), int(src.numel()), *_ws(workspace), _ptr(err_flags),
-                             _stream(stream)))
+    _check(lib.pa_pages_copy(ctypes.byref(p), caches, num_caches, _addr(src), _addr(dst),
+                             _addr(rows), src.numel(), *_ws(workspace), _addr(err_flags),
+                             raw_stream(stream)))
 
 
 def pa_pages_fork(p, caches, num_caches, parents, children, block_table, past, refcount,
                   workspace, err_flags=None, stream=None):
-    _check(lib.pa_pages_fork(ctypes.byref(p), caches, int(num_caches), _ptr(parents),
-                             _ptr(children), int(parents.numel()), _ptr(block_table), _ptr(past),
-                             _ptr(refcount), *_ws(workspace), _ptr(err_flags), _stream(stream)))
+    _check(lib.pa_pages_fork(ctypes.byref(p), caches, num_caches, _addr(parents),
+                             _addr(children), parents.numel(), _addr(block_table), _addr(past),
+                             _addr(refcount), *_ws(workspace), _addr(err_flags), raw_stream(stream)))
 
 
 def pa_pages_free(p, seqs, block_table, past, refcount, err_flags=None, stream=None):
-    _check(lib.pa_pages_free(ctypes.byref(p), _ptr(seqs), int(seqs.numel()), _ptr(block_table),
-                             _ptr(past), _ptr(refcount), _ptr(err_flags), _stream(stream)))
+    _check(lib.pa_pages_free(ctypes.byref(p), _addr(seqs), seqs.numel(), _addr(block_table),
+                             _addr(past), _addr(refcount), _addr(err_flags), raw_stream(stream)))
 
 
 def pa_pages_reserve(p, cumseq, block_table, past, refcount, slot_mapping, workspace,
                      err_flags=None, stream=None):
-    _check(lib.pa_pages_reserve(ctypes.byref(p), _ptr(cumseq), int(slot_mapping.numel()),
-                                _ptr(block_table), _ptr(past), _ptr(refcount),
-                                _ptr(slot_mapping), *_ws(workspace), _ptr(err_flags),
-                                _stream(stream)))
+    _check(lib.pa_pages_reserve(ctypes.byref(p), _addr(cumseq), slot_mapping.numel(),
+                                _addr(block_table), _addr(past), _addr(refcount),
+                                _addr(slot_mapping), *_ws(workspace), _addr(err_flags),
+                                raw_stream(stream)))
 
 
 def pa_pages_compact(p, caches, num_caches, block_table, refcount, live, workspace,
                      err_flags=None, stream=None):
-    _check(lib.pa_pages_compact(ctypes.byref(p), caches, int(num_caches), _ptr(block_table),
-                                _ptr(refcount), _ptr(live), *_ws(workspace), _ptr(err_flags),
-                                _stream(stream)))
+    _check(lib.pa_pages_compact(ctypes.byref(p), caches, num_caches, _addr(block_table),
+                                _addr(refcount), _addr(live), *_ws(workspace), _addr(err_flags),
+                                raw_stream(stream)))
 
 
 def make_diff_params(*, dtype, num_heads, kv_num_heads, head_size, v_head_size=0,
@@ -498,21 +516,21 @@ def pa_diff_workspace_size(p: pa_diff_params, num_seqs: int, num_tokens: int) ->
 
 def pa_diff_write(p, key, value, cos_cache, sin_cache, slot_mapping, cumseq, past, key_cache,
                   value_cache, err_flags=None, stream=None):
-    _check(lib.pa_diff_write(ctypes.byref(p), _ptr(key), _ptr(value), int(key.shape[0]),
-                             _ptr(cos_cache), _ptr(sin_cache), _ptr(slot_mapping), _ptr(cumseq),
-                             _ptr(past), int(past.shape[0]), _ptr(key_cache), _ptr(value_cache),
-                             _ptr(err_flags), _stream(stream)))
+    _check(lib.pa_diff_write(ctypes.byref(p), _addr(key), _addr(value), key.shape[0],
+                             _addr(cos_cache), _addr(sin_cache), _addr(slot_mapping), _addr(cumseq),
+                             _addr(past), past.shape[0], _addr(key_cache), _addr(value_cache),
+                             _addr(err_flags), raw_stream(stream)))
 
 
 def _dread(fn, p, query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
            norm_weight, cumseq, past, block_table, out, seq_begin, seq_end, workspace, err_flags,
            stream):
     n = past.shape[0]
-    _check(fn(ctypes.byref(p), _ptr(query), int(query.shape[0]), _ptr(key_cache),
-              _ptr(value_cache), _ptr(cos_cache), _ptr(sin_cache), _ptr(lambda_vectors),
-              _ptr(norm_weight), _ptr(cumseq), _ptr(past), _ptr(block_table), int(n),
-              int(seq_begin), int(n if seq_end is None else seq_end), *_ws(workspace),
-              _ptr(out), _ptr(err_flags), _stream(stream)))
+    _check(fn(ctypes.byref(p), _addr(query), query.shape[0], _addr(key_cache),
+              _addr(value_cache), _addr(cos_cache), _addr(sin_cache), _addr(lambda_vectors),
+              _addr(norm_weight), _addr(cumseq), _addr(past), _addr(block_table), n,
+              seq_begin, n if seq_end is None else seq_end, *_ws(workspace),
+              _addr(out), _addr(err_flags), raw_stream(stream)))
 
 
 def pa_diff_decode(p, query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
