@@ -14,8 +14,9 @@
 //   form one line that is cut into equal parts, one per CTA, whatever the
 //   lengths; a part may start and end inside a sequence. Parts are joined by
 //   the combine kernel below, as are all results (one code path).
-// * Tiles are copied by TMA boxes of 64 channels x 16 rows into a ring of up to
-//   24 stages. Tile i of a CTA's part goes to warp i % 8, which folds it into
+// * Tiles are copied by TMA, the keys of both maps with one box and the values
+//   with another (a box per 64 channels where a width is no multiple of 64),
+//   into a ring of up to 24 stages. Tile i of a CTA's part goes to warp i % 8, which folds it into
 //   running sums of its own and then starts the copy of tile i + stages into
 //   the stage it has just read: no barrier inside a part, no producer, and
 //   copies run ahead across sequences. A tile takes a warp some 3000 cycles
@@ -37,8 +38,8 @@
 #include <cmath>
 #include <type_traits>
 
+#include "pa_diff_common.cuh"
 #include "pa_diff_internal.h"
-#include "pa_tc_common.cuh"
 
 namespace pa {
 namespace diff {
@@ -57,7 +58,8 @@ constexpr int kRows = 2 * kHeads;
 constexpr int kMaxStages = 24;
 constexpr size_t kSmem = 225 * 1024;  // dynamic shared memory of a CTA (one per SM)
 constexpr int kThreads = kWarps * 32;
-constexpr int kBufs = 2;         // buffers of the join at the end of a segment
+constexpr int kJoin = 64;        // channels joined at a time at the end of a segment
+constexpr int kJoinPitch = 72;   // floats of a row there (8 rows x 8 bytes x 4 lanes: no bank twice)
 constexpr int kMinTiles = kWarps;  // least part of a CTA
 constexpr float kLazy = 8.f;     // a running maximum may lag by 2^8
 
@@ -66,6 +68,7 @@ struct Args {
   DiffArgs a;
   int grp, chunks, ng;  // heads per kv head, chunks of 8 of them, kvh * chunks
   int vslabs, stage, stages;  // 64-channel value slabs; bytes and number of ring stages
+  bool k_whole, v_whole;      // one box per tile (see cache_map)
   int slots;            // partials the workspace holds
   float scale_log2, cap_in, cap_out;
   float* ws_o;          // [slots][16][vhs]
@@ -207,12 +210,13 @@ __device__ void line_find(const Args& A, int nseq, int lane, int64_t x, int* seq
 // sequence's range.
 struct Cursor {
   int seq, gc, tile, tiles;
-  int64_t lo, pos;
+  int64_t lo, pos, t;  // the sequence's visible keys and token
 };
 __device__ __forceinline__ void cursor_load(const Args& A, Cursor& c) {
   const Seq s = seq_of(A, A.a.seq_begin + c.seq);
   c.lo = s.lo;
   c.pos = s.pos;
+  c.t = s.t;
   c.tiles = s.status ? 0 : (int)(s.pos / kTileKeys - s.lo / kTileKeys) + 1;
 }
 // `step` tiles on, over the ends of (kv head, chunk)s and sequences.
@@ -239,8 +243,8 @@ diff_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                    const __grid_constant__ Args A) {
   constexpr int KSL = KS / 4;  // slabs of a map
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int s_seq;
-  __shared__ int64_t s_before, s_total;
+  __shared__ Cursor s_first;
+  __shared__ int s_count;
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   __shared__ int s_bad[kWarps];
   __shared__ int s_abort;
@@ -262,22 +266,48 @@ diff_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 
   // ---- this CTA's part of the line
   if (warp == 0) {
-    const int64_t total = line_total(A, nseq, lane);
-    const int64_t ctas = min((int64_t)gridDim.x, max((int64_t)1, total / kMinTiles));
-    int seq = 0;
-    int64_t before = 0;
     int64_t* plan = blockIdx.x == 0 ? A.ws_plan : nullptr;
-    const int64_t x0 = blockIdx.x < ctas ? (int64_t)blockIdx.x * total / ctas : total;
-    if (blockIdx.x < ctas) line_find(A, nseq, lane, x0, &seq, &before, plan);
-    if (lane == 0) {
-      s_seq = seq;
-      s_before = before;
-      s_total = total;
-      if (plan) {
-        plan[nseq] = total;
-        plan[nseq + 1] = ctas;
+    Cursor c;
+    int64_t total, n = 0, incl = 0;
+    if (nseq <= 32) {  // one round of loads, the rest in registers
+      c.tiles = 0;
+      if (lane < nseq) {
+        c.seq = lane;
+        cursor_load(A, c);
       }
+      n = incl = (int64_t)c.tiles * A.ng;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      total = __shfl_sync(0xffffffffu, incl, 31);
+      if (plan && lane < nseq) plan[lane] = incl - n;
+    } else {
+      total = line_total(A, nseq, lane);
     }
+    const int64_t ctas = min((int64_t)gridDim.x, max((int64_t)1, total / kMinTiles));
+    if (plan && lane == 0) {
+      plan[nseq] = total;
+      plan[nseq + 1] = ctas;
+    }
+    const bool some = blockIdx.x < ctas && total > 0;
+    const int64_t x0 = some ? (int64_t)blockIdx.x * total / ctas : 0;
+    const int64_t x1 = some ? ((int64_t)blockIdx.x + 1) * total / ctas : 0;
+    int64_t before = incl - n;
+    bool mine = x0 >= before && x0 < incl;  // the lane whose sequence holds tile x0
+    if (nseq > 32) {
+      if (some || plan) line_find(A, nseq, lane, x0, &c.seq, &before, plan);
+      if (some) cursor_load(A, c);
+      mine = lane == 0;
+    }
+    if (some && mine) {
+      const int64_t off = x0 - before;
+      c.gc = (int)(off / c.tiles);
+      c.tile = (int)(off - (int64_t)c.gc * c.tiles);
+      s_first = c;
+    }
+    if (lane == 0) s_count = (int)(x1 - x0);
   }
   if (warp == 1 && lane == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -290,27 +320,16 @@ diff_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     tc::prefetch_tmap(&vmap);
   }
   __syncthreads();
-  const int64_t total = s_total;
-  const int64_t ctas = min((int64_t)gridDim.x, max((int64_t)1, total / kMinTiles));
-  if (blockIdx.x >= ctas || total == 0) {
+  const int count = s_count;  // tiles of this CTA
+  if (count == 0) {
     if (!waited) grid_dep_wait();
     return;
   }
-  const int64_t x0 = (int64_t)blockIdx.x * total / ctas, x1 = ((int64_t)blockIdx.x + 1) * total / ctas;
-  const int count = (int)(x1 - x0);  // tiles of this CTA
-  Cursor first;
-  first.seq = s_seq;
-  cursor_load(A, first);
-  {
-    const int64_t off = x0 - s_before;
-    first.gc = (int)(off / first.tiles);
-    first.tile = (int)(off - (int64_t)first.gc * first.tiles);
-  }
+  const Cursor first = s_first;
 
   const uint32_t ring = smem_u32(smem);
   uint4* q_s = reinterpret_cast<uint4*>(smem + (size_t)stages * A.stage);
-  float* merge = reinterpret_cast<float*>(q_s + 2 * KS * 32);
-  constexpr int mpitch = VT * 8 + 8;
+  float* join = reinterpret_cast<float*>(q_s + 2 * KS * 32);
 
   // ---- copies: the warp's tiles below `stages` now, tile i + stages after i.
   // The cursor stands at the next one, whose page id is loaded a tile ahead.
@@ -332,26 +351,31 @@ diff_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       grid_dep_wait();  // from here on rows the write phase may store are read
       waited = true;
     }
-    if (lane == 0) {
-      const int gk = lc.gc / A.chunks;
-      int row = g.num_blocks * g.bs;  // out of range: the copy fills zeros
-      const bool ok = next_page >= 0 && next_page < g.num_blocks;
-      if (ok) row = next_page * g.bs + (key0 & (g.bs - 1));
-      else raise_flag(a.err_flags, PA_DEVERR_BLOCK);
+    const int gk = lc.gc / A.chunks;
+    const bool ok = next_page >= 0 && next_page < g.num_blocks;
+    // (no such page: a row out of range, which the copy fills with zeros)
+    const int row = ok ? next_page * g.bs + (key0 & (g.bs - 1)) : g.num_blocks * g.bs;
+    if (elect_one()) {
+      if (!ok) raise_flag(a.err_flags, PA_DEVERR_BLOCK);
       s_stage_bad[stage] = ok ? 0 : 1;
       __threadfence_block();
       *(volatile int*)&s_last[stage] = next_tile;
       const uint32_t bar = smem_u32(&s_full[stage]);
-      uint32_t dst = ring + stage * A.stage;
+      const uint32_t dst = ring + stage * A.stage, vdst = dst + 2 * KSL * kSlab;
       tc::mbar_expect_tx(bar, (uint32_t)A.stage);
+      if (A.k_whole) {
+        tma_load_4d(dst, &kmap, 0, gk, row, 0, bar);
+      } else {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int k = 0; k < KSL; ++k, dst += kSlab)
-          tc::tma_load_3d(dst, &kmap, k * 64, 2 * gk + i, row, bar);
-#pragma unroll
-      for (int k = 0; k < VT / 8; ++k, dst += kSlab)
-        if (k < A.vslabs) tc::tma_load_3d(dst, &vmap, k * 64, gk, row, bar);
+        for (int i = 0; i < 2 * KSL; ++i)
+          tma_load_4d(dst + i * kSlab, &kmap, (i % KSL) * 64, 2 * gk + i / KSL, row, 0, bar);
+      }
+      if (A.v_whole) {
+        tma_load_4d(vdst, &vmap, 0, gk, row, 0, bar);
+      } else {
+        for (int k = 0; k < A.vslabs; ++k)
+          tma_load_4d(vdst + k * kSlab, &vmap, k * 64, gk, row, 0, bar);
+      }
     }
     __syncwarp();
     // tiles below `stages` come one after another, later ones in step with
@@ -383,18 +407,17 @@ diff_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   Cursor cur = first;
   while (at < count) {
     const int seg = min(cur.tiles - cur.tile, count - at);  // tiles of this segment
-    const int b = a.seq_begin + cur.seq, gk = cur.gc / A.chunks;
+    const int gk = cur.gc / A.chunks;
     const int h0 = gk * A.grp + (cur.gc - gk * A.chunks) * kHeads;
     const int nh = min(kHeads, A.grp - (cur.gc - gk * A.chunks) * kHeads);
     // the query rows, rotated, as A fragments of each map: rows 0-7 the heads'
     // values, rows 8-15 the remainders; [map][k step][lane] of four registers
     {
-      const int64_t t = a.cumseq[b];
       for (int i = tid; i < kRows * KS * 2; i += kWarps * 32) {
         const int m = i & 1, hh = (i >> 1) & 7, d0 = (i >> 4) * 8;
         float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (hh < nh && d0 < hs) {
-          const T* row = (const T*)a.query + ((t * g.H + h0 + hh) * 2 + m) * (int64_t)hs;
+          const T* row = (const T*)a.query + ((cur.t * g.H + h0 + hh) * 2 + m) * (int64_t)hs;
           unpack8<T>(*reinterpret_cast<const uint4*>(row + d0), x);
           if (g.rd > 0 && d0 >= g.ro && d0 < g.ro + g.rd) {
             const int half = g.rd >> 1;
@@ -586,36 +609,36 @@ diff_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         A.ws_ml[slot * kRows + r] = make_float2(any ? __int_as_float(0x7fc00000) : M, L);
       }
     }
-    // warps 0, 2, 4, 6 add up in buffer 0 while 1, 3, 5, 7 do in buffer 1
-    for (int k = 0; k < (kWarps + kBufs - 1) / kBufs; ++k) {
-      if (warp / kBufs == k) {
+    // 64 channels at a time: every warp leaves its rows in shared memory, thread
+    // (row, four channels) adds them up. (Warp after warp adding to one buffer
+    // took 17000 cycles a segment, this 2000.)
+#pragma unroll
+    for (int cc = 0; cc < VT / 8; ++cc) {
+      if (cc * 8 < nvt) {
+        if (cc > 0) __syncthreads();  // (behind the reads of the chunk before)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float* row = merge + (warp % kBufs) * kRows * mpitch + (i * 8 + (lane >> 2)) * mpitch +
-                       (lane & 3) * 2;
+          float* row = join + (warp * kRows + i * 8 + (lane >> 2)) * kJoinPitch + (lane & 3) * 2;
 #pragma unroll
-          for (int c = 0; c < VT; ++c) {
-            if (c < nvt) {
-              float2 x = make_float2(o[c][2 * i] * w[i], o[c][2 * i + 1] * w[i]);
-              if (k > 0) {
-                const float2 y = *reinterpret_cast<const float2*>(row + c * 8);
-                x.x += y.x;
-                x.y += y.y;
-              }
-              *reinterpret_cast<float2*>(row + c * 8) = x;
-            }
-          }
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<float2*>(row + c * 8) =
+                make_float2(o[cc * 8 + c][2 * i] * w[i], o[cc * 8 + c][2 * i + 1] * w[i]);
         }
-      }
-      __syncthreads();
-    }
-    for (int i = tid; i < kRows * (vhs >> 2); i += kWarps * 32) {
-      const int r = i / (vhs >> 2), c = (i - r * (vhs >> 2)) * 4;
-      if ((r & 7) < nh) {
-        const float4 x = *reinterpret_cast<const float4*>(merge + r * mpitch + c);
-        const float4 y = *reinterpret_cast<const float4*>(merge + (kRows + r) * mpitch + c);
-        *reinterpret_cast<float4*>(A.ws_o + (slot * kRows + r) * (int64_t)vhs + c) =
-            make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        __syncthreads();
+        const int r = tid >> 4, c = (tid & 15) * 4;
+        if ((r & 7) < nh && cc * kJoin + c < vhs) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < kWarps; ++k) {
+            const float4 y =
+                *reinterpret_cast<const float4*>(join + (k * kRows + r) * kJoinPitch + c);
+            x.x += y.x;
+            x.y += y.y;
+            x.z += y.z;
+            x.w += y.w;
+          }
+          *reinterpret_cast<float4*>(A.ws_o + (slot * kRows + r) * (int64_t)vhs + cc * kJoin + c) = x;
+        }
       }
     }
     // (the next segment's first barrier stands between these reads and its writes)
@@ -747,7 +770,7 @@ Plan plan_of(const Geometry& g) {
   p.vslabs = (g.vhs + 63) / 64;
   p.stage = kSlab * (p.ks / 2 + p.vslabs);
   const size_t fixed = 1024 + (size_t)p.ks * 32 * 16 * 2 +
-                       (size_t)kBufs * kRows * (p.vt * 8 + 8) * 4;
+                       (size_t)kWarps * kRows * kJoinPitch * 4;
   const int s = (int)((kSmem - fixed) / (size_t)p.stage);
   p.stages = s > kMaxStages ? kMaxStages : s;
   p.smem = fixed + (size_t)p.stages * p.stage;
@@ -771,16 +794,22 @@ Layout layout_of(const Geometry& g, const Plan& p, int64_t nseq) {
   return l;
 }
 
-// The cache as [slots][rows][channels], boxes of 64 channels x 1 row x 16 slots
-// (channels past the width read as zeros).
-cudaError_t encode(CUtensorMap* map, bool bf16, const void* base, int width, int rows,
-                   int64_t slots) {
+// A cache of `heads` rows of `width` channels per slot, as (channel, head, slot,
+// slab), in boxes of 16 slots. With `whole` (a width that is a multiple of 64)
+// the channels are cut into slabs of 64 (the fourth dimension, 128 bytes apart)
+// and one box holds a row's slabs one after another; otherwise a box holds one
+// slab and the channel dimension ends at the width (zeros behind it).
+cudaError_t cache_map(CUtensorMap* map, bool bf16, const void* base, int width, int heads,
+                      int64_t slots, bool whole) {
   tc::EncodeTiledFn enc = tc::encode_fn();
   if (!enc) return cudaErrorNotSupported;
-  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)slots};
-  const cuuint64_t str[2] = {(cuuint64_t)width * 2, (cuuint64_t)rows * width * 2};
-  const cuuint32_t box[3] = {64, 1, kTileKeys}, estr[3] = {1, 1, 1};
-  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+  const cuuint64_t wb = (cuuint64_t)width * 2;
+  const cuuint32_t slabs = whole ? (cuuint32_t)(width / 64) : 1u;
+  const cuuint64_t dims[4] = {whole ? 64u : (cuuint64_t)width, (cuuint64_t)heads,
+                              (cuuint64_t)slots, slabs};
+  const cuuint64_t str[3] = {wb, wb * heads, 128};
+  const cuuint32_t box[4] = {64, 1, kTileKeys, slabs}, estr[4] = {1, 1, 1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
              const_cast<void*>(base), dims, str, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
@@ -798,8 +827,11 @@ cudaError_t launch(const Args& A, const Plan& p, int ctas, cudaStream_t stream) 
   const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   const int64_t slots = (int64_t)A.g.num_blocks * A.g.bs;
   CUtensorMap kmap, vmap;
-  if (e == cudaSuccess) e = encode(&kmap, bf16, A.a.key_cache, A.g.hs, 2 * A.g.kvh, slots);
-  if (e == cudaSuccess) e = encode(&vmap, bf16, A.a.value_cache, A.g.vhs, A.g.kvh, slots);
+  if (e == cudaSuccess)  // (both maps of a kv head are one row of 2 hs channels)
+    e = A.k_whole ? cache_map(&kmap, bf16, A.a.key_cache, 2 * A.g.hs, A.g.kvh, slots, true)
+                  : cache_map(&kmap, bf16, A.a.key_cache, A.g.hs, 2 * A.g.kvh, slots, false);
+  if (e == cudaSuccess)
+    e = cache_map(&vmap, bf16, A.a.value_cache, A.g.vhs, A.g.kvh, slots, A.v_whole);
   if (e == cudaSuccess)
     e = tc::launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), p.smem, stream, kmap, vmap, A);
   if (e != cudaSuccess) return e;
@@ -824,6 +856,8 @@ cudaError_t launch_decode(const Geometry& g, const DiffArgs& a) {
   A.chunks = l.chunks;
   A.ng = l.ng;
   A.vslabs = p.vslabs;
+  A.k_whole = g.hs % 64 == 0;
+  A.v_whole = g.vhs % 64 == 0;
   A.stage = p.stage;
   A.stages = p.stages;
   A.slots = (int)l.slots;
