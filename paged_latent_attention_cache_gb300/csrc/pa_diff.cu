@@ -21,6 +21,10 @@ namespace {
 // kvH * (2 hs + vhs) channels, keys first; 16-byte loads and stores, every
 // byte once (a rotary group also reads its partner group, from L1).
 // ---------------------------------------------------------------------------
+// Largest batch whose offsets are staged in shared memory (the search for a
+// token's sequence is then no chain of global loads).
+constexpr int kStagedSeqs = 8191;
+
 template <typename T>
 __global__ void __launch_bounds__(256)
 diff_write_kernel(const T* __restrict__ key, const T* __restrict__ value,
@@ -33,6 +37,13 @@ diff_write_kernel(const T* __restrict__ key, const T* __restrict__ value,
   // a read kernel launched with programmatic dependent launch may start its
   // prologue; it waits for this grid before it reads the cache
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ int32_t s_cum[];  // cumseq[0..num_seqs] when staged
+  const int32_t* cum = cumseq;
+  if (num_seqs <= kStagedSeqs) {
+    for (int i = threadIdx.x; i <= num_seqs; i += blockDim.x) s_cum[i] = cumseq[i];
+    __syncthreads();
+    cum = s_cum;
+  }
   const int kg = kvh * 2 * (hs >> 3), vg = kvh * (vhs >> 3), groups = kg + vg;
   const int64_t total = num_tokens * groups;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
@@ -57,7 +68,7 @@ diff_write_kernel(const T* __restrict__ key, const T* __restrict__ value,
     }
     int32_t b;
     int64_t pos;
-    if (!locate_token(t, cumseq, past, num_seqs, first ? err_flags : nullptr, &b, &pos)) continue;
+    if (!locate_token(t, cum, past, num_seqs, first ? err_flags : nullptr, &b, &pos)) continue;
     if (rd > 0 && (pos < 0 || pos >= cos_rows)) {  // the token's row is skipped
       if (first) raise_flag(err_flags, pos < 0 ? PA_DEVERR_CONTEXT : PA_DEVERR_POSITION);
       continue;
@@ -218,9 +229,11 @@ pa_status pa_diff_write(const pa_diff_params* p, const void* key, const void* va
   int64_t blocks = (total + 255) / 256;
   const int64_t cap = (int64_t)g.num_sms * 16;
   if (blocks > cap) blocks = cap;
+  const size_t smem =
+      num_seqs <= diff::kStagedSeqs ? (size_t)(num_seqs + 1) * sizeof(int32_t) : 0;
   auto go = [&](auto* typed) {
     using T = std::remove_pointer_t<decltype(typed)>;
-    diff::diff_write_kernel<T><<<(unsigned)blocks, 256, 0, (cudaStream_t)stream>>>(
+    diff::diff_write_kernel<T><<<(unsigned)blocks, 256, smem, (cudaStream_t)stream>>>(
         (const T*)key, (const T*)value, (const T*)cos_cache, (const T*)sin_cache, slot_mapping,
         cumseq, past, num_seqs, (T*)key_cache, (T*)value_cache, num_tokens, g.kvh, g.hs, g.vhs,
         g.ro, g.rd, g.interleaved, g.cos_rows, (int64_t)g.num_blocks * g.bs, err_flags);

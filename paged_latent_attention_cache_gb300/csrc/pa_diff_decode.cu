@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(kHeads * 32) diff_combine_kernel(const __grid_
   const int x = blockIdx.x, gc = blockIdx.y;
   const int gk = gc / A.chunks, first = (gc - gk * A.chunks) * kHeads;
   const int hs = g.hs, vhs = g.vhs;
-  // weights: older than the attention kernel
+  // weights and the sequence: older than the attention kernel
   float d0 = 0.f, d1 = 0.f;
   const float* lv = a.lambda_vectors;
   for (int d = lane; d < hs; d += 32) {
@@ -679,8 +679,12 @@ __global__ void __launch_bounds__(kHeads * 32) diff_combine_kernel(const __grid_
     d1 += __shfl_xor_sync(0xffffffffu, d1, o);
   }
   const float lam = expf(d0) - expf(d1) + a.lambda_init;
-  grid_dep_wait();
+  float nw[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    nw[c] = c * 32 + lane < vhs ? Half<T>::to_f32(((const T*)a.norm_weight)[c * 32 + lane]) : 0.f;
   const Seq s = seq_of(A, a.seq_begin + x);
+  grid_dep_wait();
   if (s.status && gc == 0 && threadIdx.x == 0) raise_flag(a.err_flags, s.err);
   if (s.status == 1 || first + warp >= A.grp) return;
   const int h = gk * A.grp + first + warp;
@@ -750,8 +754,7 @@ __global__ void __launch_bounds__(kHeads * 32) diff_combine_kernel(const __grid_
   for (int c = 0; c < 8; ++c) {
     const int ch = c * 32 + lane;
     if (ch < vhs)
-      out[ch] = Half<T>::from_f32(
-          bad ? 0.f : r[c] * inv * Half<T>::to_f32(((const T*)a.norm_weight)[ch]));
+      out[ch] = Half<T>::from_f32(bad ? 0.f : r[c] * inv * nw[c]);
   }
 }
 
