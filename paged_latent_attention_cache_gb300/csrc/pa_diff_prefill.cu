@@ -21,13 +21,13 @@
 //             copy costs its thread some 190 cycles, and one warp with a copy
 //             per slab was the slowest part of the kernel (2500 cycles a tile).
 //   warp 11   QK^T (S: 128 x 128 f32 in TMEM), PV (A = P from TMEM, O: 128 x vg)
-//   warps 0-7 softmax: two threads per row, 64 columns each, held in registers:
-//             S is read from TMEM once and is free for the next QK^T before
-//             the exponentials start; P (16 bit) goes to one of two buffers.
-//             Two groups of four warps on alternate tiles (one thread per row)
-//             were no faster at 64 / 128, and at 128 / 256 there is no room for
-//             a second S beside P.
-// TMEM columns: O vg <= 256 | S 128 | P 2 x 64.
+//   warps 0-7 softmax. Values wider than 128 channels: two threads per row, 64
+//             columns each; S is read into registers once and is free for the
+//             next QK^T before the exponentials start; P (16 bit) goes to one of
+//             two buffers. TMEM columns: O vg <= 256 | S 128 | P 2 x 64.
+//             Narrower values leave room for a second S: two groups of four
+//             warps on alternate tiles, one thread per row. TMEM: O vg <= 128 |
+//             S 2 x 128 | P 2 x 64.
 //
 // Bound: per tile and map the MMAs take 128 * 128 * (hs + vhs) / 4096 cycles
 // (1536 at 128 / 256, 768 at 64 / 128) and the exponentials 16384 / 16 per SM.
@@ -62,7 +62,7 @@ constexpr size_t kSmemMax = 225 * 1024;
 
 struct PreBars {
   uint64_t k_full[kMaxK], k_empty[kMaxK], v_full[kMaxV], v_empty[kMaxV];
-  uint64_t s_full, s_free, p_full[2], pv_done[2];
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
   uint64_t q_tma, q_full, drain, x_full;
   uint32_t tmem_base;
   int bad, abort;
@@ -180,6 +180,17 @@ __device__ __forceinline__ void rotate_row(uint8_t* q_s, int row, int part, cons
   }
 }
 
+// Largest of 32 scores (three-operand maxima).
+__device__ __forceinline__ float max32(const uint32_t (&x)[32]) {
+  float v[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
+#pragma unroll
+  for (int e = 2; e < 30; e += 4) {
+    v[0] = fmaxf(v[0], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+    v[1] = fmaxf(v[1], fmaxf(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])));
+  }
+  return fmaxf(fmaxf(v[0], v[1]), fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31])));
+}
+
 // 2^(v sl + nm) of 32 raw scores of a row, packed to 16 bits; returns the sum
 // of the unrounded values. In three passes over the registers, so that the 32
 // exponentials issue back to back (element by element the warp waited for each
@@ -250,7 +261,8 @@ __device__ __forceinline__ Work unit_warp(const Params& P, int unit, int lane) {
   return w;
 }
 
-template <typename T, bool CAP>
+// TWO: vg <= 128, two groups of softmax warps on alternate tiles.
+template <typename T, bool CAP, bool TWO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPreThreads, 1)
 diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                     const __grid_constant__ CUtensorMap qmap, const __grid_constant__ PreArgs A) {
@@ -312,10 +324,10 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       mbar_init(smem_u32(&bars->v_full[s]), 1);
       mbar_init(smem_u32(&bars->v_empty[s]), 1);
     }
-    mbar_init(smem_u32(&bars->s_full), 1);
-    mbar_init(smem_u32(&bars->s_free), kSoftWarps);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bars->p_full[i]), kSoftWarps);
+      mbar_init(smem_u32(&bars->s_full[i]), 1);
+      mbar_init(smem_u32(&bars->s_free[i]), TWO ? 4 : kSoftWarps);
+      mbar_init(smem_u32(&bars->p_full[i]), TWO ? 4 : kSoftWarps);
       mbar_init(smem_u32(&bars->pv_done[i]), 1);
     }
     mbar_init(smem_u32(&bars->q_tma), 1);
@@ -338,7 +350,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  const uint32_t col_s = vg, col_p = vg + kN;
+  const uint32_t col_s = vg, col_p = vg + (TWO ? 2 : 1) * kN;  // P: two buffers of 64
   volatile int* abort = &bars->abort;
   const Work W = work;
   const bool run = W.status == 0;
@@ -386,6 +398,140 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 
       float m_used = -INFINITY, l = 0.f;
       const float sl = CAP ? 1.f : P.scale_log2;
+      auto score = [&](float v) {  // log2-domain score of a raw one
+        return !CAP ? v * sl : v == -INFINITY ? -INFINITY : P.cap_out * tanh_ex2(v * P.cap_in);
+      };
+      // Zeroes the value rows of tile k's keys that no row of the unit sees, by
+      // `threads` threads.
+      auto zero_values = [&](int k, int64_t j0, int me, int threads) {
+        const int v0 = 2 * k;
+        bool w = true;
+        for (int i = 0; i < 2 && w; ++i)
+          w = __all_sync(0xffffffffu,
+                         wait_bar(smem_u32(&bars->v_full[(v0 + i) % A.nv]),
+                                  (uint32_t)((v0 + i) / A.nv) & 1u, abort, P.err_flags));
+        if (w) {
+          for (int i = me; i < kN * vslabs * 8; i += threads) {
+            const int rr = (i >> 3) & (kN - 1);
+            const int64_t j = j0 + rr;
+            if (j < lo || j > pos_hi)
+              *reinterpret_cast<uint4*>(v_s + ((v0 + (rr >> 6)) % A.nv) * A.v_bytes +
+                                        (i >> 10) * kVBox + (rr & 63) * 128 + (i & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+        }
+        return w;
+      };
+      // Scales columns [c0, c1) of this row of O, once the PV before tile k has
+      // added to it.
+      auto rescale_o = [&](int k, float factor, int c0, int c1) {
+        const bool w = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->pv_done[(k - 1) & 1]),
+                                                        ((k - 1) >> 1) & 1, abort, P.err_flags));
+        if (w) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = c0; c < c1; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(lane_addr + c, r);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * factor);
+            tmem_st16(lane_addr + c, r);
+          }
+        }
+        return w;
+      };
+      if constexpr (TWO) {
+        // Group `half` takes tiles half, half + 2, ..., one thread per row, so that
+        // one group's loads, maxima and waits run under the other's exponentials
+        // (1.5 times faster at 64 / 128 than all warps on one tile). The groups
+        // share the rows' running maxima: s_max[0][row] is handed from tile to
+        // tile, by the barriers 1 + q (group 0 to 1) and 5 + q (back) of
+        // quadrant q, on which one warp arrives and the other waits. Every warp
+        // goes through all of its tiles and hand-overs; after a wait that gave
+        // up (ok false) it does nothing else. Here m_used is what l refers to.
+#pragma unroll 1
+        for (int k = half; k < n; k += 2) {
+          const int64_t j0 = (t_begin + k) * kN;
+          const bool edge = j0 < lo_hi || j0 + kN - 1 > pos;
+          const uint32_t par = (uint32_t)(k >> 1) & 1u;
+          if (ok)
+            ok = __all_sync(0xffffffffu,
+                            wait_bar(smem_u32(&bars->s_full[half]), par, abort, P.err_flags));
+          uint32_t s[4][32];
+          if (live && ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              tmem_ld32_nowait(lane_addr + col_s + half * kN + c * 32, s[c]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) reg_fence(s[c]);
+            tc_fence_before();
+          }
+          if (ok) arrive_warp(&bars->s_free[half], lane);  // a later QK^T may overwrite S
+          if (edge && ok) ok = zero_values(k, j0, row, kRows);
+          float mt = -INFINITY;
+          if (live && ok) {
+            if (edge) {
+              const int c0 = (int)min((int64_t)kN, max((int64_t)0, lo_r - j0));
+              const int c1 = (int)max((int64_t)-1, min((int64_t)(kN - 1), pos_r - j0));
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (c * 32 + e < c0 || c * 32 + e > c1) s[c][e] = __float_as_uint(-INFINITY);
+            }
+            float v[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] = max32(s[c]);
+            mt = score(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
+          }
+          float factor = 1.f;
+          bool rescale = false;
+          if (live) {
+            if (k > 0) named_sync(half ? 1 + (warp & 3) : 5 + (warp & 3), 64);
+            if (ok) {
+              float m = k > 0 ? s_max[0][row] : -INFINITY;
+              if (m == -INFINITY) {
+                m = mt;  // (nothing but zeros was added before a first visible key)
+              } else if (mt > m + kRescaleLog2) {
+                factor = ex2(m - mt);
+                m = mt;
+                rescale = true;
+              }
+              s_max[0][row] = m;
+              if (m_used != m) {
+                l = m_used == -INFINITY ? 0.f : l * ex2(m_used - m);
+                m_used = m;
+              }
+            }
+            if (k + 1 < n) named_arrive(half ? 5 + (warp & 3) : 1 + (warp & 3), 64);
+          }
+          if (k >= 2 && ok)  // P's buffer: PV of tile k - 2 has read it
+            ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->pv_done[half]), par ^ 1u, abort,
+                                                  P.err_flags));
+          if (live && ok) {
+            const float mu = m_used == -INFINITY ? 0.f : m_used;
+            const uint32_t dst = lane_addr + col_p + half * 64;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t pk[16];
+              if (CAP) {
+                const ExpArgs E{sl, mu, P.cap_in, P.cap_out, 0.f, 0.f, 0.f, 0.f, 0.f};
+                l += exp_chunk<T, 2>(s[c], pk, E);
+              } else {
+                l += exp_row<T>(s[c], pk, sl, -mu);
+              }
+              tmem_st16(dst + c * 16, pk);
+            }
+            if (__any_sync(0xffffffffu, rescale)) ok = rescale_o(k, factor, 0, vg);
+            tmem_wait_st();
+            tc_fence_before();
+          }
+          if (ok) arrive_warp(&bars->p_full[half], lane);
+        }
+      } else {
       // Every warp goes through all n tiles and meets its partner of the
       // quadrant in each; after a wait that gave up (ok false) it does nothing
       // else.
@@ -398,7 +544,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         // says that P's buffer may be written again)
         if (ok)
           ok = __all_sync(0xffffffffu,
-                          wait_bar(smem_u32(&bars->s_full), k & 1, abort, P.err_flags));
+                          wait_bar(smem_u32(&bars->s_full[0]), k & 1, abort, P.err_flags));
         uint32_t s[2][32];
         if (live && ok) {
           tc_fence_after();
@@ -409,25 +555,8 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           reg_fence(s[1]);
           tc_fence_before();
         }
-        if (ok) arrive_warp(&bars->s_free, lane);  // the next QK^T may overwrite S
-        if (edge && ok) {  // zero the value rows of keys no row of the unit sees
-          const int v0 = 2 * k;
-          for (int i = 0; i < 2 && ok; ++i)
-            ok = __all_sync(0xffffffffu,
-                            wait_bar(smem_u32(&bars->v_full[(v0 + i) % A.nv]),
-                                     (uint32_t)((v0 + i) / A.nv) & 1u, abort, P.err_flags));
-          if (ok) {
-            for (int i = tid; i < kN * vslabs * 8; i += kSoft) {
-              const int rr = (i >> 3) & (kN - 1);
-              const int64_t j = j0 + rr;
-              if (j < lo || j > pos_hi)
-                *reinterpret_cast<uint4*>(v_s + ((v0 + (rr >> 6)) % A.nv) * A.v_bytes +
-                                          (i >> 10) * kVBox + (rr & 63) * 128 + (i & 7) * 16) =
-                    make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async();
-          }
-        }
+        if (ok) arrive_warp(&bars->s_free[0], lane);  // the next QK^T may overwrite S
+        if (edge && ok) ok = zero_values(k, j0, tid, kSoft);
         // The exponentials use the running maximum as it stands; the tile's own
         // maximum is taken beside them, and only if it passes the running one by
         // more than 2^8 (or there is none yet) do the two warps of the quadrant
@@ -450,9 +579,6 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           }
           tmem_st16(dst + 16, pk);
         };
-        auto score = [&](float v) {  // log2-domain score of a raw one
-          return !CAP ? v * sl : v == -INFINITY ? -INFINITY : P.cap_out * tanh_ex2(v * P.cap_in);
-        };
         bool again = false;
         if (live && ok) {
           if (edge) {
@@ -465,17 +591,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                 if (c * 32 + e < c0 || c * 32 + e > c1) s[c][e] = __float_as_uint(-INFINITY);
           }
           if (k > 0) exps();
-          float v[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t* x = s[c >> 1] + (c & 1) * 16;
-            v[c] = __uint_as_float(x[0]);
-#pragma unroll
-            for (int e = 1; e < 15; e += 2)
-              v[c] = fmaxf(v[c], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
-            v[c] = fmaxf(v[c], __uint_as_float(x[15]));
-          }
-          vmax = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+          vmax = fmaxf(max32(s[0]), max32(s[1]));
           again = __any_sync(0xffffffffu,
                              row < rows && (m_used == -INFINITY ||
                                             score(vmax) > m_used + kRescaleLog2));
@@ -499,23 +615,9 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                 rescale = true;
               }
               exps();
-              if (__any_sync(0xffffffffu, rescale)) {
-                // (k >= 1) each half scales half of O, once the PV before has added to it
-                ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->pv_done[(k - 1) & 1]),
-                                                      ((k - 1) >> 1) & 1, abort, P.err_flags));
-                if (ok) {
-                  tc_fence_after();
-#pragma unroll 1
-                  for (int c = half * (vg >> 1); c < (half + 1) * (vg >> 1); c += 16) {
-                    uint32_t r[16];
-                    tmem_ld16(lane_addr + c, r);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                      r[e] = __float_as_uint(__uint_as_float(r[e]) * factor);
-                    tmem_st16(lane_addr + c, r);
-                  }
-                }
-              }
+              // (k >= 1) each half scales half of O
+              if (__any_sync(0xffffffffu, rescale))
+                ok = rescale_o(k, factor, half * (vg >> 1), (half + 1) * (vg >> 1));
             }
           }
           l += lsum;
@@ -524,18 +626,22 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         }
         if (ok) arrive_warp(&bars->p_full[pb], lane);
       }
+      }
       grid_dep_launch();
       uint4 nw = make_uint4(0, 0, 0, 0);
       if (tid * 8 < vhs) nw = reinterpret_cast<const uint4*>(A.norm_weight)[tid];
-      named_sync(5, kSoft);
+      named_sync(9, kSoft);
       ok = __all_sync(0xffffffffu, ok && !*abort);
       if (ok && n > 0)
         ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->pv_done[(n - 1) & 1]),
                                               ((n - 1) >> 1) & 1, abort, P.err_flags));
       tc_fence_after();
-      if (live) s_sum[half][row] = l;
+      if (live) {
+        if (TWO) l = m_used == -INFINITY ? 0.f : l * ex2(m_used - s_max[0][row]);
+        s_sum[half][row] = l;
+      }
       if (tid * 8 < vhs) s_norm[tid] = nw;
-      named_sync(5, kSoft);
+      named_sync(9, kSoft);
       const float lt = s_sum[0][row] + s_sum[1][row];
       coef = lt > 0.f ? (map == 0 ? 1.f : lam) / lt : 0.f;
     } else if (warp < kMmaWarp) {
@@ -637,7 +743,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         auto wait = [&](uint64_t* bar, uint32_t par) {
           return wait_bar(smem_u32(bar), par, abort, P.err_flags);
         };
-        auto qk = [&]() {
+        auto qk = [&](int sb) {
           if (!wait(&bars->k_full[sk], kpar)) return false;
           tc_fence_after();
           const uint64_t kd = sdesc(k_base + sk * P.k_bytes, 16, 1024);
@@ -645,10 +751,10 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           for (int kk = 0; kk < 8; ++kk) {
             if (kk < nk) {
               const uint32_t o = (uint32_t)(kk >> 2) * (kBox >> 4) + (uint32_t)(kk & 3) * 2;
-              mma_ss(tmem + col_s, q_desc + o, kd + o, id_qk, kk > 0 ? 1u : 0u);
+              mma_ss(tmem + col_s + sb * kN, q_desc + o, kd + o, id_qk, kk > 0 ? 1u : 0u);
             }
           }
-          tc_commit(smem_u32(&bars->s_full));
+          tc_commit(smem_u32(&bars->s_full[sb]));
           tc_commit(smem_u32(&bars->k_empty[sk]));
           if (++sk == A.nk) {
             sk = 0;
@@ -672,12 +778,16 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           }
           return true;
         };
-        // QK^T of the next tile before PV of this one: its S is free as soon as
-        // the softmax warps have read it, and it runs while they work. The
-        // commit of S(k + 1) stands behind PV(k - 1) (see the softmax's use).
-        bool go = wait(&bars->q_full, 0) && qk();
+        // QK^T of the next tile (TWO: the one after) before PV of this one: its S
+        // is free as soon as the softmax warps have read it, and it runs while
+        // they work. With one S, the commit of S(k + 1) stands behind PV(k - 1)
+        // (see the softmax's use).
+        constexpr int kAhead = TWO ? 2 : 1;
+        bool go = wait(&bars->q_full, 0) && qk(0);
+        if (TWO && n > 1) go = go && qk(1);
         for (int k = 0; k < n && go; ++k) {
-          if (k + 1 < n) go = wait(&bars->s_free, k & 1) && qk();
+          const int b = TWO ? k & 1 : 0;
+          if (k + kAhead < n) go = wait(&bars->s_free[b], TWO ? (k >> 1) & 1 : k & 1) && qk(b);
           go = go && wait(&bars->p_full[k & 1], (k >> 1) & 1) && pv(k, 0) && pv(k, 1);
           if (go) tc_commit(smem_u32(&bars->pv_done[k & 1]));
         }
@@ -789,7 +899,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     }
   }
   if (run && warp < kSoftWarps) {
-    named_sync(5, kSoft);
+    named_sync(9, kSoft);
     // 16 lanes a row; r / grp by a product (rows below 128)
     const int nc = max(0, min(vg >> 1, vhs - first)) >> 3, c = lane & 15;
     const uint32_t inv_grp = 65536u / (uint32_t)grp + 1u;
@@ -844,10 +954,10 @@ cudaError_t cache_map(CUtensorMap* map, bool bf16, const void* base, int width, 
   return encode(map, bf16, base, 4, dims, str, box);
 }
 
-template <typename T, bool CAP>
+template <typename T, bool CAP, bool TWO>
 cudaError_t launch(const Geometry& g, const DiffArgs& a, const PreArgs& A, int64_t units) {
   static std::atomic<bool> configured[64];
-  auto kern = diff_prefill_kernel<T, CAP>;
+  auto kern = diff_prefill_kernel<T, CAP, TWO>;
   cudaError_t e = once_per_device(configured, g.device, [&] {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
   });
@@ -930,11 +1040,13 @@ cudaError_t launch_prefill(const Geometry& g, const DiffArgs& a) {
   A.lambda_init = a.lambda_init;
   A.norm_eps = a.norm_eps;
   const int64_t units = (a.num_tokens + P.tpc - 1) / P.tpc + (a.seq_end - a.seq_begin);
-  const bool cap = g.softcap > 0.f;
-  if (g.dtype == PA_DTYPE_BF16)
-    return cap ? launch<__nv_bfloat16, true>(g, a, A, units)
-               : launch<__nv_bfloat16, false>(g, a, A, units);
-  return cap ? launch<__half, true>(g, a, A, units) : launch<__half, false>(g, a, A, units);
+  const bool cap = g.softcap > 0.f, two = P.vg <= 128;
+  auto go = [&](auto* typed) {
+    using T = std::remove_pointer_t<decltype(typed)>;
+    if (cap) return two ? launch<T, true, true>(g, a, A, units) : launch<T, true, false>(g, a, A, units);
+    return two ? launch<T, false, true>(g, a, A, units) : launch<T, false, false>(g, a, A, units);
+  };
+  return g.dtype == PA_DTYPE_BF16 ? go((__nv_bfloat16*)nullptr) : go((__half*)nullptr);
 }
 
 }  // namespace diff
