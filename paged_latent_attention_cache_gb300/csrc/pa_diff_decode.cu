@@ -69,7 +69,7 @@ struct Args {
   int grp, chunks, ng;  // heads per kv head, chunks of 8 of them, kvh * chunks
   int vslabs, stage, stages;  // 64-channel value slabs; bytes and number of ring stages
   bool k_whole, v_whole;      // one box per tile (see cache_map)
-  int slots;            // partials the workspace holds
+  int64_t slots;        // partials the workspace holds
   float scale_log2, cap_in, cap_out;
   float* ws_o;          // [slots][16][vhs]
   float2* ws_ml;        // [slots][16] (log2-domain maximum, sum)
@@ -243,7 +243,7 @@ diff_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                    const __grid_constant__ Args A) {
   constexpr int KSL = KS / 4;  // slabs of a map
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Cursor s_first;
+  __shared__ Cursor s_first, s_cur;
   __shared__ int s_count;
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   __shared__ int s_bad[kWarps];
@@ -336,6 +336,7 @@ diff_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   Cursor lc = first;
   int next_tile = warp < stages ? warp : warp + stages;
   auto page_of = [&]() {
+    if (lc.seq >= nseq) return -1;  // (the lengths changed under the kernel)
     const int key0 = (int)(lc.lo / kTileKeys + lc.tile) * kTileKeys;
     return a.block_table[(int64_t)(a.seq_begin + lc.seq) * g.max_blocks + (key0 >> sh)];
   };
@@ -407,6 +408,7 @@ diff_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   Cursor cur = first;
   while (at < count) {
     const int seg = min(cur.tiles - cur.tile, count - at);  // tiles of this segment
+    if (seg <= 0 || cur.seq >= nseq) break;  // (the lengths changed under the kernel)
     const int gk = cur.gc / A.chunks;
     const int h0 = gk * A.grp + (cur.gc - gk * A.chunks) * kHeads;
     const int nh = min(kHeads, A.grp - (cur.gc - gk * A.chunks) * kHeads);
@@ -641,9 +643,14 @@ diff_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         }
       }
     }
-    // (the next segment's first barrier stands between these reads and its writes)
+    // one thread moves on to the next segment, so that all warps agree on it
     at += seg;
-    cursor_step(A, cur, seg, nseq);
+    if (tid == 0 && at < count) {
+      cursor_step(A, cur, seg, nseq);
+      s_cur = cur;
+    }
+    __syncthreads();
+    if (at < count) cur = s_cur;
   }
   if (!waited) grid_dep_wait();
   // after a wait that gave up, copies may still be in flight
@@ -699,7 +706,8 @@ __global__ void __launch_bounds__(kHeads * 32) diff_combine_kernel(const __grid_
   // the CTA of line tile t: the last whose part starts at or before it
   const int64_t c0 = ((t0 + 1) * ctas - 1) / total, c1 = ((t1 + 1) * ctas - 1) / total;
   const int64_t slot0 = c0 + (int64_t)x * A.ng + gc;
-  const int parts = (int)(c1 - c0) + 1;
+  // (within the workspace even if the lengths changed under the kernels)
+  const int parts = (int)max((int64_t)0, min(c1 - c0 + 1, A.slots - slot0));
   float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f}, o[2][8] = {};
   bool bad = false;
   for (int p0 = 0; p0 < parts; p0 += 4) {
@@ -863,7 +871,7 @@ cudaError_t launch_decode(const Geometry& g, const DiffArgs& a) {
   A.v_whole = g.vhs % 64 == 0;
   A.stage = p.stage;
   A.stages = p.stages;
-  A.slots = (int)l.slots;
+  A.slots = l.slots;
   A.scale_log2 = g.scale * tc::kLog2e;
   A.cap_in = g.softcap > 0.f ? g.scale / g.softcap : 0.f;
   A.cap_out = g.softcap > 0.f ? g.softcap * tc::kLog2e : 0.f;

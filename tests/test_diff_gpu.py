@@ -332,3 +332,107 @@ def test_serving_run_with_pages():
     after = read()
     assert torch.equal(before[[1, 3, 4]], after[[1, 3, 4]])
     assert pool.error_flags() == 0
+
+
+def test_many_prompts():
+    """More than 32 sequences with any number of new tokens, none among them."""
+    rng = np.random.default_rng(1)
+    q = [int(x) for x in rng.integers(0, 30, 45)]
+    past = [int(x) for x in rng.integers(0, 200, 45)]
+    w = workload("64_128", q_lens=q, past_lens=past, num_heads=2, kv_num_heads=1, block_size=16)
+    check(w, decodes=0)
+
+
+@pytest.mark.parametrize("name", ["64_128", "128_256"])
+def test_maximum_moves_in_every_tile(name):
+    """Keys that grow with their position: every tile's largest score passes
+    the running maximum by far, so that O is scaled again and again."""
+    w = workload(name, q_lens=[1, 200], past_lens=[1500, 900], drop_slots=0, rotary_dim=0, num_heads=4)
+    t = w.tensors
+    q = t["query"].view(w.num_tokens, 4, 2, -1)
+    q.copy_(q.abs())
+    for b, (n, p) in enumerate(zip(w.q_lens, w.past_lens)):
+        j = torch.arange(p + n)
+        rows = (t["block_table"][b, j // 64] * 64 + j % 64).long()
+        kc = t["key_cache"].view(-1, 2, 2, w.head_size)
+        grow = (j.float() / 25).view(-1, 1, 1, 1) * torch.tensor([1.0, 0.5]).view(1, 1, 2, 1)
+        kc[rows] = (kc[rows].float() * 0.1 + grow).to(w.dtype)
+    check(w)
+
+
+def test_far_pages():
+    """Pages beyond 2^32 bytes of both caches (and 2^31 elements of the keys)."""
+    nb, bs, kv, hs = 70000, 64, 4, 64
+    free = torch.cuda.mem_get_info()[0]
+    if free < 40 << 30:
+        pytest.skip("needs 20 GB of device memory")
+    w = workload("64_128", q_lens=[1, 40], past_lens=[500, 100], kv_num_heads=kv, num_heads=8, drop_slots=0)
+    d, want, _ = run_gpu(w)
+    small = w.tensors["block_table"]
+    t = {k: v.cuda() for k, v in w.tensors.items()}
+    for k, width in (("key_cache", 2 * hs), ("value_cache", 128)):
+        big = torch.full((nb, bs, kv, width), float("nan"), dtype=w.dtype, device="cuda")
+        n = t[k].shape[0]
+        big[nb - n:] = t[k].view(n, bs, kv, width)
+        t[k] = big.view(nb, bs, kv, 2, hs) if k == "key_cache" else big
+    n = w.num_blocks
+    t["block_table"] = torch.where(small >= 0, small + nb - n, small).cuda()
+    t["slot_mapping"] = torch.where(t["slot_mapping"] >= 0, t["slot_mapping"] + (nb - n) * bs, -1).int()
+    op = DifferentialAttention(**{**w.params, "num_blocks": nb}, max_seqs=2, max_tokens=64)
+    out = op.forward(*_args(t), 1)
+    assert op.error_flags() == 0 and torch.equal(out, want)
+    pool = PagePool([t["key_cache"], t["value_cache"]], block_size=bs, max_seqs=2, max_blocks_per_seq=4)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    pool.copy(i32(nb - 1, nb - 2), i32(1, nb - n - 1))
+    for c in (t["key_cache"], t["value_cache"]):
+        assert torch.equal(c[1].view(torch.int16), c[nb - 1].view(torch.int16))
+        assert torch.equal(c[nb - n - 1].view(torch.int16), c[nb - 2].view(torch.int16))
+    assert pool.error_flags() == 0
+
+
+def test_two_operators_on_two_streams():
+    """Two operators with workspaces of their own run at the same time, each on
+    the stream it is given while another one is current."""
+    wa = workload("64_128", q_lens=[1] * 6, past_lens=[3000, 10, 700, 64, 5, 900], drop_slots=0)
+    wb = workload("128_256", q_lens=[1, 1, 90], past_lens=[2000, 17, 300], drop_slots=0)
+    (da, want_a, _), (db, want_b, _) = run_gpu(wa), run_gpu(wb)
+    oa, ob = _op(wa), _op(wb)
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(5):
+        outs.append((oa.forward(*_args(da), 6, stream=sa), ob.forward(*_args(db), 2, stream=sb)))
+    torch.cuda.synchronize()
+    for a, b in outs:
+        assert torch.equal(a, want_a) and torch.equal(b, want_b)
+
+
+def test_nothing_to_do():
+    w = workload("64_128", q_lens=[0, 0], past_lens=[10, 0], drop_slots=0)
+    d, out, op = run_gpu(w)
+    assert out.shape == (0, 8 * 128) and op.error_flags() == 0
+    before = d["key_cache"].clone()
+    op.forward(*_args(d), 0)
+    torch.cuda.synchronize()
+    assert torch.equal(before, d["key_cache"])
+
+
+@pytest.mark.parametrize("name", ["64_128", "128_256"])
+def test_same_bits_every_time(name):
+    w = workload(name, q_lens=[1] * 20 + [150, 33], past_lens=list(range(0, 4000, 200)) + [1000, 5], drop_slots=0)
+    op = _op(w)
+    _, want, _ = run_gpu(w, op=op)
+    for _ in range(10):
+        _, got, _ = run_gpu(w, op=op)
+        assert torch.equal(got, want)
+
+
+def test_workspace_refused_before_launch():
+    w = workload("64_128", q_lens=[1] * 3, past_lens=[3000, 10, 700], drop_slots=0)
+    d, want, op = run_gpu(w)
+    op.workspace = op.workspace[:256]
+    with pytest.raises(B.PaError, match="workspace"):
+        op.forward(*_args(d), 3)
+    op.workspace = None
+    with pytest.raises(B.PaError, match="workspace"):
+        op.forward(*_args(d), 3)
