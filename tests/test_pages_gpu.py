@@ -87,6 +87,17 @@ def test_copy_conflicts(src, dst, rows):
     s.check(O.copy(s.caches, src, dst, rows, s.bs))
 
 
+@pytest.mark.parametrize("n", [1, 63, 64, 65, 300])
+def test_copy_conflicts_by_count(n):
+    """Random pairs with every kind of conflict, on both sides of the number
+    up to which a copy is one kernel."""
+    s = Pair(n, nb=400)
+    src, dst = s.rng.integers(-1, 401, size=n), s.rng.integers(-1, 401, size=n)
+    rows = s.rng.integers(-1, 18, size=n)
+    s.pool.copy(s.ints(src), s.ints(dst), s.ints(rows))
+    s.check(O.copy(s.caches, src, dst, rows, s.bs))
+
+
 def test_copy_many_caches_and_page_sizes():
     """More caches than one launch takes, pages from 256 bytes to 96 KB."""
     widths = [16 * (1 + i % 7) for i in range(150)] + [1536 * 4]
