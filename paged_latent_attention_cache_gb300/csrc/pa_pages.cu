@@ -152,12 +152,19 @@ __device__ void warp_prefix(const Plan& id, const int (&v)[K], int (&base)[K], i
   }
 }
 
+constexpr int kBatch = 8;  // loads of a lane in flight: every step here waits for memory
+
 // Pages of [lo, hi) that are free (ref == 0; `held` counts the others).
 __device__ __forceinline__ int count_pages(const int32_t* ref, int lo, int hi, bool held,
                                            int lane) {
   int n = 0;
-#pragma unroll 4
-  for (int i = lo + lane; i < hi; i += 32) n += (ref[i] != 0) == held ? 1 : 0;
+  for (int i0 = lo + lane; i0 < hi; i0 += 32 * kBatch) {
+    int r[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) r[k] = i0 + 32 * k < hi ? ref[i0 + 32 * k] : 0;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) n += i0 + 32 * k < hi && (r[k] != 0) == held ? 1 : 0;
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   return n;
@@ -168,13 +175,22 @@ __device__ __forceinline__ int count_pages(const int32_t* ref, int lo, int hi, b
 template <typename F>
 __device__ __forceinline__ void list_pages(const int32_t* ref, int lo, int hi, bool held, int lane,
                                            int base, int most, F&& f) {
-  for (int i0 = lo; i0 < hi && base < most; i0 += 32) {
-    const int i = i0 + lane;
-    const bool hit = i < hi && (ref[i] != 0) == held;
-    const unsigned who = __ballot_sync(0xffffffffu, hit);
-    const int rank = base + __popc(who & ((1u << lane) - 1u));
-    if (hit && rank < most) f(rank, i);
-    base += __popc(who);
+  for (int i0 = lo; i0 < hi && base < most; i0 += 32 * kBatch) {
+    int r[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + 32 * k + lane;
+      r[k] = i < hi ? ref[i] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + 32 * k + lane;
+      const bool hit = i < hi && (r[k] != 0) == held;
+      const unsigned who = __ballot_sync(0xffffffffu, hit);
+      const int rank = base + __popc(who & ((1u << lane) - 1u));
+      if (hit && rank < most) f(rank, i);
+      base += __popc(who);
+    }
   }
 }
 
@@ -358,14 +374,22 @@ free_kernel(State st, const int32_t* __restrict__ seqs, int n) {
 // ---------------------------------------------------------------------------
 // reserve
 // ---------------------------------------------------------------------------
+constexpr int kStagedSeqs = 4096;
+
 __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
 reserve_kernel(State st, Scratch ws, const int32_t* __restrict__ cumseq, int64_t num_tokens,
                int32_t* __restrict__ slot_mapping) {
   __shared__ int buf[2][kPlanWarps];
+  __shared__ int32_t s_cum[kStagedSeqs + 1];  // cumseq for the searches, where it fits
   cg::cluster_group cl = cg::this_cluster();
   const Plan id = plan_ids();
   const int nb = st.num_blocks, ns = st.num_seqs, mb = st.max_blocks;
   const int sh = __ffs(st.bs) - 1;
+  const int32_t* cum = cumseq;
+  if (ns <= kStagedSeqs) {
+    for (int i = threadIdx.x; i <= ns; i += kPlanThreads) s_cum[i] = cumseq[i];
+    cum = s_cum;  // (read behind the cluster's barriers)
+  }
   int lo, hi, plo, phi;
   share(ns, id.warp, &lo, &hi);
   share(nb, id.warp, &plo, &phi);
@@ -422,35 +446,69 @@ reserve_kernel(State st, Scratch ws, const int32_t* __restrict__ cumseq, int64_t
       const int first = (int)(past >> sh), last = (int)((past + q - 1) >> sh);
       int32_t* row = st.table + (int64_t)b * mb;
       int at = rank;
-      for (int j0 = first; j0 <= last; j0 += 32) {
-        const int j = j0 + id.lane;
-        const bool hit = j <= last && row[j] == -1;
-        const unsigned who = __ballot_sync(0xffffffffu, hit);
-        if (hit) {
-          const int page = fresh(&ws.list[at + __popc(who & ((1u << id.lane) - 1u))]);
-          row[j] = page;
-          st.ref[page] = 1;
+      for (int j0 = first; j0 <= last; j0 += 32 * kBatch) {
+        int held[kBatch], page[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int j = j0 + 32 * k + id.lane;
+          held[k] = j <= last ? row[j] : 0;
         }
-        at += __popc(who);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const unsigned who = __ballot_sync(0xffffffffu, held[k] == -1);
+          page[k] = held[k] == -1 ? fresh(&ws.list[at + __popc(who & ((1u << id.lane) - 1u))]) : -1;
+          at += __popc(who);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          if (page[k] >= 0) {
+            row[j0 + 32 * k + id.lane] = page[k];
+            st.ref[page[k]] = 1;
+          }
+        }
       }
     }
     rank = (int)min((int64_t)INT_MAX, (int64_t)rank + lack);
   }
   cl.sync();
 
-  // token t belongs to the first sequence whose end exceeds it
-  for (int64_t t = id.thread; t < num_tokens; t += 32 * kPlanWarps) {
-    int a = 0, z = ns - 1;
-    while (a < z) {
-      const int mid = (a + z) >> 1;
-      if (t < cumseq[mid + 1]) z = mid; else a = mid + 1;
+  // Token t belongs to the first sequence whose end exceeds it. A thread looks
+  // up kTokens tokens side by side.
+  constexpr int kTokens = 4;
+  for (int64_t t0 = id.thread; t0 < num_tokens; t0 += 32 * kPlanWarps * kTokens) {
+    int seq[kTokens];
+    int64_t pos[kTokens];
+    bool ok[kTokens];
+#pragma unroll
+    for (int k = 0; k < kTokens; ++k) {
+      const int64_t t = t0 + (int64_t)k * 32 * kPlanWarps;
+      int a = 0, z = ns - 1;
+      while (a < z) {
+        const int mid = (a + z) >> 1;
+        if (t < cum[mid + 1]) z = mid; else a = mid + 1;
+      }
+      seq[k] = a;
+      ok[k] = t < num_tokens && t >= cum[a] && t < cum[a + 1];
+      pos[k] = t - cum[a];
     }
-    int slot = -1;
-    if (t >= cumseq[a] && t < cumseq[a + 1] && fresh(&ws.need[a]) >= 0) {
-      const int64_t pos = (int64_t)st.past[a] + (t - cumseq[a]);
-      slot = fresh(&st.table[(int64_t)a * mb + (pos >> sh)]) * st.bs + (int)(pos & (st.bs - 1));
+    int need[kTokens], past[kTokens], page[kTokens];
+#pragma unroll
+    for (int k = 0; k < kTokens; ++k) {
+      need[k] = fresh(&ws.need[seq[k]]);
+      past[k] = st.past[seq[k]];
     }
-    slot_mapping[t] = slot;
+#pragma unroll
+    for (int k = 0; k < kTokens; ++k) {
+      ok[k] = ok[k] && need[k] >= 0;
+      pos[k] += past[k];
+      page[k] = ok[k] ? fresh(&st.table[(int64_t)seq[k] * mb + (pos[k] >> sh)]) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kTokens; ++k) {
+      const int64_t t = t0 + (int64_t)k * 32 * kPlanWarps;
+      if (t < num_tokens)
+        slot_mapping[t] = ok[k] ? page[k] * st.bs + (int)(pos[k] & (st.bs - 1)) : -1;
+    }
   }
 }
 
