@@ -34,9 +34,10 @@ diff_write_kernel(const T* __restrict__ key, const T* __restrict__ value,
                   T* __restrict__ value_cache, int64_t num_tokens, int kvh, int hs, int vhs,
                   int ro, int rd, int interleaved, int cos_rows, int64_t num_slots,
                   int32_t* err_flags) {
-  // a read kernel launched with programmatic dependent launch may start its
-  // prologue; it waits for this grid before it reads the cache
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // This kernel takes its place while the one before it ends; once that is
+  // complete, a read kernel behind this one may start its prologue (it waits for
+  // this grid before it reads the cache).
+  asm volatile("griddepcontrol.wait;\n griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ int32_t s_cum[];  // cumseq[0..num_seqs] when staged
   const int32_t* cum = cumseq;
   if (num_seqs <= kStagedSeqs) {
@@ -233,14 +234,24 @@ pa_status pa_diff_write(const pa_diff_params* p, const void* key, const void* va
       num_seqs <= diff::kStagedSeqs ? (size_t)(num_seqs + 1) * sizeof(int32_t) : 0;
   auto go = [&](auto* typed) {
     using T = std::remove_pointer_t<decltype(typed)>;
-    diff::diff_write_kernel<T><<<(unsigned)blocks, 256, smem, (cudaStream_t)stream>>>(
-        (const T*)key, (const T*)value, (const T*)cos_cache, (const T*)sin_cache, slot_mapping,
-        cumseq, past, num_seqs, (T*)key_cache, (T*)value_cache, num_tokens, g.kvh, g.hs, g.vhs,
-        g.ro, g.rd, g.interleaved, g.cos_rows, (int64_t)g.num_blocks * g.bs, err_flags);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(
+        &cfg, diff::diff_write_kernel<T>, (const T*)key, (const T*)value, (const T*)cos_cache,
+        (const T*)sin_cache, slot_mapping, cumseq, past, num_seqs, (T*)key_cache,
+        (T*)value_cache, num_tokens, g.kvh, g.hs, g.vhs, g.ro, g.rd, g.interleaved, g.cos_rows,
+        (int64_t)g.num_blocks * g.bs, err_flags);
   };
-  if (g.dtype == PA_DTYPE_BF16) go((__nv_bfloat16*)nullptr);
-  else go((__half*)nullptr);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      g.dtype == PA_DTYPE_BF16 ? go((__nv_bfloat16*)nullptr) : go((__half*)nullptr);
   if (e != cudaSuccess)
     return fail(PA_ERR_CUDA, "differential write launch: %s", cudaGetErrorString(e));
   return PA_OK;

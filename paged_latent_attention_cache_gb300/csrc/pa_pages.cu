@@ -93,10 +93,11 @@ __device__ __forceinline__ int4 fresh(const int4* p) {
                : "memory");
   return v;
 }
-// Programmatic dependent launch: the copy kernel may take its place on the
-// SMs now; it waits for this grid before it reads anything.
-__device__ __forceinline__ void let_next_start() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+// Programmatic dependent launch: a kernel of this file starts while the one
+// before it on the stream still runs, waits here for all of it, and lets the
+// next one take its place on the SMs.
+__device__ __forceinline__ void chain() {
+  asm volatile("griddepcontrol.wait;\n griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -204,7 +205,7 @@ copy_plan_kernel(State st, Scratch ws, const int32_t* __restrict__ src,
   cg::cluster_group cl = cg::this_cluster();
   const Plan id = plan_ids();
   const int nb = st.num_blocks;
-  let_next_start();
+  chain();
   auto in_range = [&](int i) {
     return src[i] >= 0 && src[i] < nb && dst[i] >= 0 && dst[i] < nb &&
            (!rows || (rows[i] >= 0 && rows[i] <= st.bs));
@@ -244,7 +245,7 @@ fork_plan_kernel(State st, Scratch ws, const int32_t* __restrict__ parents,
   cg::cluster_group cl = cg::this_cluster();
   const Plan id = plan_ids();
   const int nb = st.num_blocks, ns = st.num_seqs, mb = st.max_blocks;
-  let_next_start();
+  chain();
   auto named = [&](int i) {
     return parents[i] >= 0 && parents[i] < ns && children[i] >= 0 && children[i] < ns;
   };
@@ -349,6 +350,7 @@ fork_plan_kernel(State st, Scratch ws, const int32_t* __restrict__ parents,
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256)
 free_kernel(State st, const int32_t* __restrict__ seqs, int n) {
+  chain();
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
     const int s = seqs[i];
     if (s < 0 || s >= st.num_seqs) {
@@ -385,6 +387,7 @@ reserve_kernel(State st, Scratch ws, const int32_t* __restrict__ cumseq, int64_t
   const Plan id = plan_ids();
   const int nb = st.num_blocks, ns = st.num_seqs, mb = st.max_blocks;
   const int sh = __ffs(st.bs) - 1;
+  chain();
   const int32_t* cum = cumseq;
   if (ns <= kStagedSeqs) {
     for (int i = threadIdx.x; i <= ns; i += kPlanThreads) s_cum[i] = cumseq[i];
@@ -522,7 +525,7 @@ compact_plan_kernel(State st, Scratch ws, int32_t* live_out) {
   __shared__ int buf2[2][kPlanWarps];
   cg::cluster_group cl = cg::this_cluster();
   const Plan id = plan_ids();
-  let_next_start();
+  chain();
   int lo, hi;
   share(st.num_blocks, id.warp, &lo, &hi);
   int live[1] = {count_pages(st.ref, lo, hi, true, id.lane)}, before[1], all[1];
@@ -577,6 +580,7 @@ move_kernel(const __grid_constant__ CacheList cl, int num_caches, State st, cons
   __shared__ int4 s_pairs[SMALL ? kSmallPairs : 1];
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
+  chain();
   if (SMALL) {
     const int i = threadIdx.x, nb = st.num_blocks;
     if (i < n) {  // z < 0: out of range; x == y: nothing to copy
@@ -600,8 +604,6 @@ move_kernel(const __grid_constant__ CacheList cl, int num_caches, State st, cons
     __syncthreads();
     if (i < n && (bad || !copies)) s_pairs[i].z = 0;
     __syncthreads();
-  } else {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
   }
   if (!SMALL && new_id) {  // compact: the table follows the pages
     const int64_t entries = (int64_t)st.num_seqs * st.max_blocks;
@@ -743,6 +745,21 @@ State state(const pa_pages_params& p, int32_t* table, int32_t* past, int32_t* re
   return State{table, past, ref, err, p.num_blocks, p.block_size, p.max_blocks_per_seq, p.num_seqs};
 }
 
+template <typename K, typename... Args>
+cudaError_t launch_chained(K kernel, unsigned grid, unsigned block, cudaStream_t stream,
+                           Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // A copy call's own arrays, for the copy of a few pairs.
 struct FewPairs {
   const int32_t *src, *dst, *rows;
@@ -773,24 +790,13 @@ pa_status launch_move(const State& st, const Scratch& ws, const pa_pages_cache* 
     int64_t blocks = (work + 7) / 8;
     const int64_t cap = (int64_t)sms() * 8;
     if (blocks > cap) blocks = cap;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = few ? 0 : 1;
     const int4* pairs = few ? nullptr : ws.pairs;
     const int32_t* count = few ? nullptr : ws.count;
     const int32_t* ids = c0 == 0 ? new_id : nullptr;
     const FewPairs f = few ? *few : FewPairs{nullptr, nullptr, nullptr, 0};
-    const cudaError_t e =
-        few ? cudaLaunchKernelEx(&cfg, move_kernel<true>, cl, m, st, pairs, count, ids, f.src,
-                                 f.dst, f.rows, f.n)
-            : cudaLaunchKernelEx(&cfg, move_kernel<false>, cl, m, st, pairs, count, ids, f.src,
-                                 f.dst, f.rows, f.n);
+    const cudaError_t e = launch_chained(few ? move_kernel<true> : move_kernel<false>,
+                                         (unsigned)blocks, 256u, stream, cl, m, st, pairs, count,
+                                         ids, f.src, f.dst, f.rows, f.n);
     if (e != cudaSuccess) return launched(e, "page copy launch");
   }
   return PA_OK;
@@ -831,8 +837,10 @@ pa_status pa_pages_copy(const pa_pages_params* p, const pa_pages_cache* caches,
     const FewPairs few{src, dst, rows, n};
     return launch_move(st, ws, caches, num_caches, n, nullptr, &few, str);
   }
-  copy_plan_kernel<<<kClusterCtas, kPlanThreads, 0, str>>>(st, ws, src, dst, rows, n);
-  if ((s = launched(cudaGetLastError(), "page copy plan launch")) != PA_OK) return s;
+  s = launched(launch_chained(copy_plan_kernel, kClusterCtas, kPlanThreads, str, st, ws, src, dst,
+                              rows, n),
+               "page copy plan launch");
+  if (s != PA_OK) return s;
   return launch_move(st, ws, caches, num_caches, n, nullptr, nullptr, str);
 }
 
@@ -853,8 +861,10 @@ pa_status pa_pages_fork(const pa_pages_params* p, const pa_pages_cache* caches,
   if ((s = check_workspace(p, workspace, workspace_bytes, &ws)) != PA_OK) return s;
   const State st = state(*p, block_table, past, refcount, err_flags);
   const cudaStream_t str = reinterpret_cast<cudaStream_t>(stream);
-  fork_plan_kernel<<<kClusterCtas, kPlanThreads, 0, str>>>(st, ws, parents, children, n);
-  if ((s = launched(cudaGetLastError(), "fork launch")) != PA_OK) return s;
+  s = launched(launch_chained(fork_plan_kernel, kClusterCtas, kPlanThreads, str, st, ws, parents,
+                              children, n),
+               "fork launch");
+  if (s != PA_OK) return s;
   return launch_move(st, ws, caches, num_caches, n, nullptr, nullptr, str);
 }
 
@@ -869,8 +879,9 @@ pa_status pa_pages_free(const pa_pages_params* p, const int32_t* seqs, int32_t n
   if ((s = check_ints(err_flags, seqs, block_table, past, refcount)) != PA_OK) return s;
   const State st = state(*p, block_table, past, refcount, err_flags);
   const int cap = sms() * 8;
-  free_kernel<<<n < cap ? n : cap, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(st, seqs, n);
-  return launched(cudaGetLastError(), "free launch");
+  return launched(launch_chained(free_kernel, (unsigned)(n < cap ? n : cap), 256u,
+                                 reinterpret_cast<cudaStream_t>(stream), st, seqs, (int)n),
+                  "free launch");
 }
 
 pa_status pa_pages_reserve(const pa_pages_params* p, const int32_t* cumseq, int64_t num_tokens,
@@ -887,9 +898,10 @@ pa_status pa_pages_reserve(const pa_pages_params* p, const int32_t* cumseq, int6
     return s;
   if ((s = check_workspace(p, workspace, workspace_bytes, &ws)) != PA_OK) return s;
   const State st = state(*p, block_table, const_cast<int32_t*>(past), refcount, err_flags);
-  reserve_kernel<<<kClusterCtas, kPlanThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      st, ws, cumseq, num_tokens, slot_mapping);
-  return launched(cudaGetLastError(), "reserve launch");
+  return launched(launch_chained(reserve_kernel, kClusterCtas, kPlanThreads,
+                                 reinterpret_cast<cudaStream_t>(stream), st, ws, cumseq,
+                                 num_tokens, slot_mapping),
+                  "reserve launch");
 }
 
 pa_status pa_pages_compact(const pa_pages_params* p, const pa_pages_cache* caches,
@@ -905,8 +917,9 @@ pa_status pa_pages_compact(const pa_pages_params* p, const pa_pages_cache* cache
   if ((s = check_workspace(p, workspace, workspace_bytes, &ws)) != PA_OK) return s;
   const State st = state(*p, block_table, nullptr, refcount, err_flags);
   const cudaStream_t str = reinterpret_cast<cudaStream_t>(stream);
-  compact_plan_kernel<<<kClusterCtas, kPlanThreads, 0, str>>>(st, ws, live);
-  if ((s = launched(cudaGetLastError(), "compact launch")) != PA_OK) return s;
+  s = launched(launch_chained(compact_plan_kernel, kClusterCtas, kPlanThreads, str, st, ws, live),
+               "compact launch");
+  if (s != PA_OK) return s;
   return launch_move(st, ws, caches, num_caches, p->num_blocks / 2, ws.mark, nullptr, str);
 }
 
