@@ -202,6 +202,26 @@ def test_reserve_random(seed):
     s.check(err)
 
 
+@pytest.mark.parametrize("tokens", [24575, 24576, 24577, 60000])
+def test_reserve_many_tokens(tokens):
+    """Both sides of the number of tokens up to which one kernel does it all;
+    the pool gives out before the last sequence."""
+    s = Pair(7, nb=4000, ns=40, mb=200, fill=0.0, share=False, widths=(16,))
+    q = np.full(40, tokens // 40)
+    q[7], q[20] = 0, q[20] + q[7]
+    q[39] += tokens - q.sum()
+    cum = np.concatenate([[0], np.cumsum(q)])
+    if tokens == 60000:
+        s.ref[:1000] = 1  # held by nobody's row, but held
+        s.upload()
+    slots = torch.full((tokens,), 12345, dtype=torch.int32, device="cuda")
+    s.pool.reserve(s.ints(cum), slots)
+    err, want = O.reserve(s.table, s.past, s.ref, cum, tokens, s.bs)
+    assert np.array_equal(slots.cpu().numpy(), want)
+    assert (err == O.POOL) == (tokens == 60000)
+    s.check(err)
+
+
 @pytest.mark.parametrize("break_it", ["past", "long", "hole", "shared", "range", "free", "cumseq", "start", "far"])
 def test_reserve_broken_state(break_it):
     s = _forkable()
