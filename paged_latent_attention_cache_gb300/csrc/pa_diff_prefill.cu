@@ -695,24 +695,24 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           if (!__shfl_sync(0xffffffffu, w ? 1 : 0, 0)) break;
         }
         const uint32_t bar = smem_u32(&full[slot]), dst0 = base + slot * bytes;
+        const int y0 = __shfl_sync(0xffffffffu, y, 0);
         if (elect_one()) mbar_expect_tx(bar, bytes);
         __syncwarp();
-#pragma unroll 1
-        for (int i = 0; i < nbox; ++i) {  // one lane issues, box after box
-          const int yi = __shfl_sync(0xffffffffu, y, i);
-          const uint32_t dst = dst0 + i * box * 128;
+        if (nbox == 1) {
           if (elect_one()) {
-            if (whole && nbox == 1) {
-              tma_load_4d(dst, tm, 0, head, yi, 0, bar);
+            if (whole) {
+              tma_load_4d(dst0, tm, 0, head, y0, 0, bar);
             } else {
-#pragma unroll 1
               for (int c = 0; c < nslab; ++c)
-                tma_load_4d(dst + c * slab_bytes, tm, whole ? 0 : c * 64, head, yi, whole ? c : 0,
-                            bar);
+                tma_load_4d(dst0 + c * slab_bytes, tm, c * 64, head, y0, 0, bar);
             }
           }
-          __syncwarp();
+        } else if (lane < nbox) {  // a lane per box
+          const uint32_t dst = dst0 + lane * box * 128;
+          for (int c = 0; c < nslab; ++c)
+            tma_load_4d(dst + c * slab_bytes, tm, whole ? 0 : c * 64, head, y, whole ? c : 0, bar);
         }
+        __syncwarp();
         ++issued;
         slot += step;
         if (slot >= slots) {
