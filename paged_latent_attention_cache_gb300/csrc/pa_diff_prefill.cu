@@ -37,6 +37,7 @@
 // tensor time here.
 #include <cfloat>
 #include <cmath>
+#include <cstddef>
 #include <type_traits>
 
 #include "pa_diff_common.cuh"
@@ -63,10 +64,14 @@ constexpr size_t kSmemMax = 225 * 1024;
 struct PreBars {
   uint64_t k_full[kMaxK], k_empty[kMaxK], v_full[kMaxV], v_empty[kMaxV];
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
-  uint64_t q_tma, q_full, drain, x_full;
+  uint64_t q_full, drain, x_full;
+  uint64_t q_tma;  // (set up by the warp that uses it first)
   uint32_t tmem_base;
   int bad, abort;
 };
+
+constexpr int kNumBars = 2 * kMaxK + 2 * kMaxV + 8 + 3;  // all but q_tma
+static_assert(offsetof(PreBars, q_tma) == kNumBars * 8, "barriers in one row");
 
 struct PreArgs {
   Params P;           // what the shared helpers read
@@ -291,6 +296,10 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   const int unit = pair / kvh, gk = pair - unit * kvh;
 
   if (warp == 0) {
+    if (lane == 0) {
+      mbar_init(smem_u32(&bars->q_tma), 1);
+      fence_barrier_init();
+    }
     if (!P.early) grid_dep_wait();
     Work w = unit_warp(P, unit, lane);
     if (w.status == 0) {
@@ -315,27 +324,28 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       }
     }
     if (lane == 0) work = w;
-  } else if (warp == 1 && lane == 0) {
-    for (int s = 0; s < A.nk; ++s) {
-      mbar_init(smem_u32(&bars->k_full[s]), 1);
-      mbar_init(smem_u32(&bars->k_empty[s]), 1);
+    __syncwarp();
+    if (w.status == 0 && elect_one()) {  // the query, ahead of everything else
+      const uint32_t qb = smem_u32(&bars->q_tma);
+      mbar_expect_tx(qb, (uint32_t)(slabs * grp * P.tpc * 128));
+      for (int slab = 0; slab < slabs; ++slab)
+        tma_load_4d(smem_u32(q_s) + slab * kBox, &qmap, slab * 64, map, gk * grp, (int)w.t, qb);
     }
-    for (int s = 0; s < A.nv; ++s) {
-      mbar_init(smem_u32(&bars->v_full[s]), 1);
-      mbar_init(smem_u32(&bars->v_empty[s]), 1);
+  } else if (warp == 1) {
+    // a lane per barrier
+    uint64_t* all = bars->k_full;
+    for (int i = lane; i < kNumBars; i += 32) {
+      uint32_t count = 1;
+      if (all + i == bars->s_free || all + i == bars->s_free + 1 || all + i == bars->p_full ||
+          all + i == bars->p_full + 1)
+        count = TWO ? 4 : kSoftWarps;
+      if (all + i == &bars->q_full) count = kSoftWarps;
+      mbar_init(smem_u32(all + i), count);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bars->s_full[i]), 1);
-      mbar_init(smem_u32(&bars->s_free[i]), TWO ? 4 : kSoftWarps);
-      mbar_init(smem_u32(&bars->p_full[i]), TWO ? 4 : kSoftWarps);
-      mbar_init(smem_u32(&bars->pv_done[i]), 1);
+    if (lane == 0) {
+      bars->bad = 0;
+      bars->abort = 0;
     }
-    mbar_init(smem_u32(&bars->q_tma), 1);
-    mbar_init(smem_u32(&bars->q_full), kSoftWarps);
-    mbar_init(smem_u32(&bars->drain), 1);
-    mbar_init(smem_u32(&bars->x_full), 1);
-    bars->bad = 0;
-    bars->abort = 0;
     fence_barrier_init();
   } else if (warp == kProdWarp && lane == 0) {
     prefetch_tmap(&kmap);
@@ -365,7 +375,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   bool ok = true;
 
   if (run) {
-    const int64_t t = W.t, pos = W.pos, t_begin = W.t_begin;
+    const int64_t pos = W.pos, t_begin = W.t_begin;
     const int64_t pos_hi = pos + ntok - 1;
     const int64_t lo = P.window >= 0 ? max((int64_t)0, pos - P.window) : 0;
     const int64_t lo_hi = P.window >= 0 ? max((int64_t)0, pos_hi - P.window) : 0;
@@ -647,12 +657,6 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     } else if (warp < kMmaWarp) {
       // =================== TMA producers ===================
       const bool keys = warp == kProdWarp;
-      if (keys && lane == 0) {
-        const uint32_t qb = smem_u32(&bars->q_tma);
-        mbar_expect_tx(qb, (uint32_t)(slabs * grp * P.tpc * 128));
-        for (int slab = 0; slab < slabs; ++slab)
-          tma_load_4d(smem_u32(q_s) + slab * kBox, &qmap, slab * 64, map, gk * grp, (int)t, qb);
-      }
       int dirty_from = 0;
       if (P.early && P.own_slots) dirty_from = (int)max((int64_t)0, W.past / kN - t_begin);
       bool waited = !P.early;
