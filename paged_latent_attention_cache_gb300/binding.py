@@ -424,7 +424,7 @@ def make_page_caches(caches):
     arr = (pa_pages_cache * max(len(caches), 1))()
     for i, c in enumerate(caches):
         arr[i].data = c.data_ptr()
-        arr[i].page_bytes = c.stride(0) * c.element_size()
+        arr[i].page_bytes = c[0].numel() * c.element_size()
     return arr
 
 

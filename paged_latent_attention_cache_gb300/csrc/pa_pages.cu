@@ -819,6 +819,7 @@ pa_status launch_move(const State& st, const Scratch& ws, const pa_pages_cache* 
     int64_t blocks = (work + 7) / 8;
     const int64_t cap = (int64_t)sms() * 8;
     if (blocks > cap) blocks = cap;
+    if (blocks < 1) blocks = 1;  // (one page: nothing can move)
     const int4* pairs = few ? nullptr : ws.pairs;
     const int32_t* count = few ? nullptr : ws.count;
     const int32_t* ids = c0 == 0 ? new_id : nullptr;

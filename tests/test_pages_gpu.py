@@ -391,3 +391,21 @@ def test_serving_run_with_attention():
     assert int(pool.block_table.max().item()) == live - 1
     after = read()
     assert torch.equal(before[1:], after[1:]) and pool.error_flags() == 0
+
+
+def test_one_page_in_many_caches():
+    """A pool of a single page: nothing can move, in any number of caches."""
+    caches = [torch.arange(16 * 16, dtype=torch.uint8, device="cuda").view(1, 16, 16) for _ in range(130)]
+    pool = PagePool(caches, block_size=16, max_seqs=2, max_blocks_per_seq=1)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    slots = pool.reserve(i32(0, 5, 5), torch.empty(5, dtype=torch.int32, device="cuda"))
+    assert slots.tolist() == [0, 1, 2, 3, 4]
+    assert pool.compact().tolist() == [1]
+    pool.copy(i32(0), i32(0))
+    assert pool.error_flags() == 0 and pool.block_table.tolist() == [[0], [-1]]
+    pool.past += i32(5, 0)
+    pool.fork(i32(0), i32(1))
+    assert pool.error_flags() == B.PA_DEVERR_POOL
+    pool.free(i32(0, 1))
+    assert pool.compact().tolist() == [0] and pool.refcount.tolist() == [0]
+    assert all(torch.equal(c, caches[0]) for c in caches)
