@@ -131,6 +131,8 @@ pa_status resolve(const pa_diff_params* p, Geometry* g) {
   if (p->v_head_size < 0) return fail(PA_ERR_INVALID_ARGUMENT, "v_head_size must be >= 0");
   g->vhs = p->v_head_size == 0 ? 2 * g->hs : p->v_head_size;
   g->rms_eps = p->norm_eps;
+  if (g->H > 65535)
+    return fail(PA_ERR_NOT_IMPLEMENTED, "num_heads %d exceeds the supported maximum 65535", g->H);
   if (g->hs > 128 || g->vhs > 256 || g->vhs % 8 != 0 || g->H / g->kvh > 128)
     return fail(PA_ERR_NOT_IMPLEMENTED,
                 "differential attention: head_size <= 128, v_head_size a multiple of 8 <= 256 "
@@ -184,8 +186,10 @@ pa_status read(Phase ph, const pa_diff_params* p, DiffArgs a) {
                   a.workspace ? a.workspace_bytes : (size_t)0, need);
   }
   const cudaError_t e = ph == Phase::kDecode ? launch_decode(g, a) : launch_prefill(g, a);
-  if (e != cudaSuccess)
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();  // not left behind for a later call
     return fail(PA_ERR_CUDA, "differential attention launch: %s", cudaGetErrorString(e));
+  }
   return PA_OK;
 }
 
@@ -252,8 +256,10 @@ pa_status pa_diff_write(const pa_diff_params* p, const void* key, const void* va
   };
   const cudaError_t e =
       g.dtype == PA_DTYPE_BF16 ? go((__nv_bfloat16*)nullptr) : go((__half*)nullptr);
-  if (e != cudaSuccess)
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();  // not left behind for a later call
     return fail(PA_ERR_CUDA, "differential write launch: %s", cudaGetErrorString(e));
+  }
   return PA_OK;
 }
 

@@ -57,6 +57,7 @@ def test_params_accepted(B, kw):
     (dict(softcap=float("inf")), 1, "softcap"), (dict(lambda_init=float("nan")), 1, "lambda_init"),
     (dict(lambda_init=float("inf")), 1, "lambda_init"), (dict(norm_eps=-1e-5), 1, "norm_eps"),
     (dict(norm_eps=float("nan")), 1, "norm_eps"), (dict(flags=1), 1, "flag"), (dict(flags=8), 1, "flag"),
+    (dict(num_heads=65536, kv_num_heads=65536), 2, "65535"),
     (dict(num_blocks=0), 1, "num_blocks"), (dict(max_blocks_per_seq=0), 1, "max_blocks_per_seq"),
 ])
 def test_params_refused(B, kw, status, needle):
