@@ -25,8 +25,10 @@
  * codes, err_flags and ownership are those of pa_latent.h; the pages can be
  * kept by the operators of pa_pages.h.
  *
- * Arithmetic: products accumulate in f32, softmax, lambda, the difference
- * and the norm are f32; out is rounded once.
+ * Arithmetic: products accumulate in f32; softmax, lambda, the difference
+ * and the norm are f32; out is rounded once. Operands of the products: keys
+ * and values as they are; the rotated query and the probabilities as two
+ * 16-bit parts each in decode, rounded to the dtype in prefill.
  */
 #ifndef PA_DIFF_H
 #define PA_DIFF_H
@@ -39,7 +41,7 @@ extern "C" {
 
 typedef struct pa_diff_params {
   int32_t dtype;              /* pa_dtype of every half-precision tensor             */
-  int32_t num_heads;          /* H heads (2 H query maps)                            */
+  int32_t num_heads;          /* H heads (2 H query maps), at most 65535             */
   int32_t kv_num_heads;       /* kvH >= 1, dividing H; H / kvH <= 128                */
   int32_t head_size;          /* hs, channels per map: multiple of 16, 16..128       */
   int32_t v_head_size;        /* vhs: multiple of 8, 8..256; 0 means 2 * hs          */
@@ -74,8 +76,12 @@ pa_status pa_diff_write(const pa_diff_params* p, const void* key, const void* va
  * per sequence, prefill any number. lambda_vectors is 4-byte, the other
  * tensors 16-byte aligned. The rest as pa_latent_decode / pa_latent_prefill:
  * the workspace is pa_diff_workspace_size bytes, rows of a sequence with
- * invalid positions or pages are zeros, those of a decode sequence with
- * another number of new tokens stay as they were. */
+ * invalid positions or pages are zeros (in prefill those of the tokens that
+ * meet one, and of tokens up to 128 / (H / kvH) beside them), those of a
+ * decode sequence with another number of new tokens stay as they were.
+ * What a token does not see (later tokens, rows before its window or behind
+ * its sequence, pages of others) may hold infinities or NaN; one in what it
+ * sees may make all of its row NaN. */
 pa_status pa_diff_decode(const pa_diff_params* p, const void* query, int64_t num_tokens,
                          const void* key_cache, const void* value_cache, const void* cos_cache,
                          const void* sin_cache, const float* lambda_vectors,

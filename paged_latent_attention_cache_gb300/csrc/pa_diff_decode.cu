@@ -72,7 +72,7 @@ struct Args {
   int64_t slots;        // partials the workspace holds
   float scale_log2, cap_in, cap_out;
   float* ws_o;          // [slots][16][vhs]
-  float2* ws_ml;        // [slots][16] (log2-domain maximum, sum)
+  float2* ws_ml;        // [slots][16] (log2-domain maximum, sum; sum -1: a bad page)
   int64_t* ws_plan;     // [nseq] tiles before the sequence, then total tiles, CTAs in use
 };
 
@@ -608,7 +608,7 @@ diff_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           L += s_m[k][r] == -INFINITY ? 0.f : ex2(s_m[k][r] - M) * s_l[k][r];
           any |= s_bad[k] != 0;
         }
-        A.ws_ml[slot * kRows + r] = make_float2(any ? __int_as_float(0x7fc00000) : M, L);
+        A.ws_ml[slot * kRows + r] = make_float2(M, any ? -1.f : L);
       }
     }
     // 64 channels at a time: every warp leaves its rows in shared memory, thread
@@ -731,8 +731,8 @@ __global__ void __launch_bounds__(kHeads * 32) diff_combine_kernel(const __grid_
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float m = ml[i][k].x;
-        bad |= isnan(m);
-        if (ml[i][k].y > 0.f && !isnan(m)) {
+        bad |= ml[i][k].y < 0.f;
+        if (!(ml[i][k].y <= 0.f)) {  // (a sum that is not a number counts)
           if (m > M[i]) {
             const float f = ex2(M[i] - m);
             L[i] *= f;

@@ -35,7 +35,9 @@
 // P and the rotated query are rounded to the dtype for the products, as in
 // the other prefill kernels; two parts each (as decode takes) would double the
 // tensor time here.
+#include <algorithm>
 #include <cfloat>
+#include <climits>
 #include <cmath>
 #include <cstddef>
 #include <type_traits>
@@ -65,12 +67,17 @@ struct PreBars {
   uint64_t k_full[kMaxK], k_empty[kMaxK], v_full[kMaxV], v_empty[kMaxV];
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
   uint64_t q_full, drain, x_full;
+  uint64_t v_land[2][2];  // [half][tile parity] values whose unseen rows are zeroed before v_full
   uint64_t q_tma;  // (set up by the warp that uses it first)
   uint32_t tmem_base;
   int bad, abort;
+  // keys with a value that is not finite: position pos + i (after the unit's
+  // first token) in the first four words, lo + i (before its last window) behind
+  uint32_t odd[8];
+  int any_odd;
 };
 
-constexpr int kNumBars = 2 * kMaxK + 2 * kMaxV + 8 + 3;  // all but q_tma
+constexpr int kNumBars = 2 * kMaxK + 2 * kMaxV + 8 + 3 + 4;  // all but q_tma
 static_assert(offsetof(PreBars, q_tma) == kNumBars * 8, "barriers in one row");
 
 struct PreArgs {
@@ -83,6 +90,20 @@ struct PreArgs {
   float lambda_init, norm_eps;
 };
 
+// Not 0 if a 16-byte piece of values holds an infinity or NaN: x - x is +0 else.
+template <typename T>
+__device__ __forceinline__ uint32_t minus_itself(uint32_t v) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    asm("sub.bf16x2 %0, %0, %0;" : "+r"(v));
+  else
+    asm("sub.f16x2 %0, %0, %0;" : "+r"(v));
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t not_finite(const uint4& v) {
+  return minus_itself<T>(v.x) | minus_itself<T>(v.y) | minus_itself<T>(v.z) |
+         minus_itself<T>(v.w);
+}
 // One arrival for the whole warp (256 threads on one barrier queue up there).
 __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
   __syncwarp();
@@ -266,6 +287,62 @@ __device__ __forceinline__ Work unit_warp(const Params& P, int unit, int lane) {
   return w;
 }
 
+// Zeroes the rows of a value slot (keys j0 .. j0 + 63) that no row of the unit
+// sees, by one warp, 8 lanes a row, four rows at a time. A key that some rows see and others do not
+// has probability 0 in the latter, and 0 times infinity or NaN is NaN: such
+// values are zeroed as well, and the key is marked, so that the rows that see it
+// answer NaN in the end.
+template <typename T>
+__device__ __forceinline__ void zero_values(uint8_t* slot, PreBars* bars, int vslabs, int64_t j0,
+                                            int64_t lo, int64_t lo_hi, int64_t pos, int64_t pos_hi,
+                                            int lane) {
+  // rows from r_lo to r_hi that some row does not see, in them [s_lo, s_hi) that
+  // any does
+  const int r_lo = j0 < lo_hi ? 0 : (int)max((int64_t)0, pos + 1 - j0);
+  const int r_hi = j0 + kVKeys - 1 > pos ? kVKeys : (int)(lo_hi - j0);
+  const int s_lo = max(r_lo, (int)max((int64_t)0, lo - j0));
+  const int s_hi = (int)min((int64_t)r_hi, pos_hi + 1 - j0);
+  uint8_t* mine = slot + (lane >> 3) * 128 + (lane & 7) * 16;
+  uint32_t odd = 0;
+#pragma unroll 1
+  for (int c = 0; c < vslabs; ++c) {  // (four loads in flight: 16 rows)
+#pragma unroll 1
+    for (int r = s_lo & ~3; r < s_hi; r += 16) {
+      uint4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int q = r + 4 * k + (lane >> 3);
+        v[k] = q >= s_lo && q < s_hi
+                   ? *reinterpret_cast<const uint4*>(mine + c * kVBox + (r + 4 * k) * 128)
+                   : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) odd |= not_finite<T>(v[k]);
+    }
+  }
+  const bool any = __any_sync(0xffffffffu, odd != 0);
+#pragma unroll 1
+  for (int r = (r_lo & ~3) + (lane >> 3); r < r_hi; r += 4) {
+    const bool seen = r >= s_lo && r < s_hi;
+    const int64_t j = j0 + r;
+    if (r < r_lo || (seen && !any) || (j <= pos && j >= lo_hi)) continue;
+    bool hit = false;
+#pragma unroll 1
+    for (int c = 0; c < vslabs; ++c) {
+      uint4* at = reinterpret_cast<uint4*>(slot + c * kVBox + r * 128 + (lane & 7) * 16);
+      if (!seen || not_finite<T>(*at)) {
+        *at = make_uint4(0, 0, 0, 0);
+        hit = true;
+      }
+    }
+    if (seen && hit) {
+      const int bit = j > pos ? (int)(j - pos) : 128 + (int)(j - lo);
+      atomicOr(&bars->odd[bit >> 5], 1u << (bit & 31));
+      bars->any_odd = 1;
+    }
+  }
+}
+
 // TWO: vg <= 128, two groups of softmax warps on alternate tiles.
 template <typename T, bool CAP, bool TWO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPreThreads, 1)
@@ -345,7 +422,9 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     if (lane == 0) {
       bars->bad = 0;
       bars->abort = 0;
+      bars->any_odd = 0;
     }
+    if (lane < 8) bars->odd[lane] = 0;
     fence_barrier_init();
   } else if (warp == kProdWarp && lane == 0) {
     prefetch_tmap(&kmap);
@@ -411,28 +490,6 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       auto score = [&](float v) {  // log2-domain score of a raw one
         return !CAP ? v * sl : v == -INFINITY ? -INFINITY : P.cap_out * tanh_ex2(v * P.cap_in);
       };
-      // Zeroes the value rows of tile k's keys that no row of the unit sees, by
-      // `threads` threads.
-      auto zero_values = [&](int k, int64_t j0, int me, int threads) {
-        const int v0 = 2 * k;
-        bool w = true;
-        for (int i = 0; i < 2 && w; ++i)
-          w = __all_sync(0xffffffffu,
-                         wait_bar(smem_u32(&bars->v_full[(v0 + i) % A.nv]),
-                                  (uint32_t)((v0 + i) / A.nv) & 1u, abort, P.err_flags));
-        if (w) {
-          for (int i = me; i < kN * vslabs * 8; i += threads) {
-            const int rr = (i >> 3) & (kN - 1);
-            const int64_t j = j0 + rr;
-            if (j < lo || j > pos_hi)
-              *reinterpret_cast<uint4*>(v_s + ((v0 + (rr >> 6)) % A.nv) * A.v_bytes +
-                                        (i >> 10) * kVBox + (rr & 63) * 128 + (i & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async();
-        }
-        return w;
-      };
       // Scales columns [c0, c1) of this row of O, once the PV before tile k has
       // added to it.
       auto rescale_o = [&](int k, float factor, int c0, int c1) {
@@ -480,7 +537,6 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             tc_fence_before();
           }
           if (ok) arrive_warp(&bars->s_free[half], lane);  // a later QK^T may overwrite S
-          if (edge && ok) ok = zero_values(k, j0, row, kRows);
           float mt = -INFINITY;
           if (live && ok) {
             if (edge) {
@@ -566,7 +622,6 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           tc_fence_before();
         }
         if (ok) arrive_warp(&bars->s_free[0], lane);  // the next QK^T may overwrite S
-        if (edge && ok) ok = zero_values(k, j0, tid, kSoft);
         // The exponentials use the running maximum as it stands; the tile's own
         // maximum is taken beside them, and only if it passes the running one by
         // more than 2^8 (or there is none yet) do the two warps of the quadrant
@@ -654,6 +709,17 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       named_sync(9, kSoft);
       const float lt = s_sum[0][row] + s_sum[1][row];
       coef = lt > 0.f ? (map == 0 ? 1.f : lam) / lt : 0.f;
+      if (bars->any_odd) {
+        // (from the unit's record again: nothing of this is kept over the tiles)
+        const int64_t p0 = work.pos, last = p0 + row / P.grp;
+        const int64_t back = P.window >= 0 ? P.window : last;
+#pragma unroll 1
+        for (int i = 0; i < 256; ++i)
+          if (bars->odd[i >> 5] >> (i & 31) & 1u) {
+            const int64_t j = i < 128 ? p0 + i : max((int64_t)0, p0 - back) + (i - 128);
+            if (j <= last && j >= last - back) coef = NAN;
+          }
+      }
     } else if (warp < kMmaWarp) {
       // =================== TMA producers ===================
       const bool keys = warp == kProdWarp;
@@ -675,6 +741,26 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       const bool whole = keys ? A.k_whole : A.v_whole;
       int slot = h, issued = 0;
       uint32_t par = 1;
+      // Value slots at an end of the keys land on a barrier of their own; this
+      // warp zeroes what not all rows see, one tile later (the next copy is on
+      // its way then), and only then says that they are full.
+      uint64_t* land = bars->v_land[h];
+      uint32_t land_par = 0;  // a bit per barrier
+      int held = -1, held_slot = 0;
+      auto release = [&]() {
+        if (held < 0) return;
+        const uint32_t bar = smem_u32(&land[held & 1]), p = land_par >> (held & 1) & 1u;
+        if (__all_sync(0xffffffffu, wait_bar(bar, p, abort, P.err_flags))) {
+          zero_values<T>(v_s + held_slot * A.v_bytes, bars, vslabs,
+                         (t_begin + held) * kN + h * kVKeys, lo, lo_hi, pos, pos_hi, lane);
+          fence_proxy_async();
+        } else if (lane == 0) {
+          drain_wait(bar, p, P.err_flags);
+        }
+        land_par ^= 1u << (held & 1);
+        arrive_warp(&full[held_slot], lane);
+        held = -1;
+      };
       for (int k = 0; k < n; ++k) {
         if (!waited && k >= dirty_from) {
           grid_dep_wait();
@@ -698,7 +784,9 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           if (lane == 0) w = wait_bar(smem_u32(&empty[slot]), par, abort, P.err_flags);
           if (!__shfl_sync(0xffffffffu, w ? 1 : 0, 0)) break;
         }
-        const uint32_t bar = smem_u32(&full[slot]), dst0 = base + slot * bytes;
+        const int64_t h0 = (t_begin + k) * kN + h * kVKeys;
+        const bool ends = !keys && (h0 < lo_hi || h0 + kVKeys - 1 > pos);
+        const uint32_t bar = smem_u32(ends ? &land[k & 1] : &full[slot]), dst0 = base + slot * bytes;
         const int y0 = __shfl_sync(0xffffffffu, y, 0);
         if (elect_one()) mbar_expect_tx(bar, bytes);
         __syncwarp();
@@ -717,6 +805,11 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             tma_load_4d(dst + c * slab_bytes, tm, whole ? 0 : c * 64, head, y, whole ? c : 0, bar);
         }
         __syncwarp();
+        release();
+        if (ends) {
+          held = k;
+          held_slot = slot;
+        }
         ++issued;
         slot += step;
         if (slot >= slots) {
@@ -725,6 +818,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         }
         __syncwarp();
       }
+      release();
       if (!waited) grid_dep_wait();
       if (*abort && lane == 0) {  // copies may be in flight: wait for each slot's last
         if (keys) drain_wait(smem_u32(&bars->q_tma), 0, P.err_flags);
@@ -1043,7 +1137,10 @@ cudaError_t launch_prefill(const Geometry& g, const DiffArgs& a) {
   A.norm_weight = a.norm_weight;
   A.lambda_init = a.lambda_init;
   A.norm_eps = a.norm_eps;
-  const int64_t units = (a.num_tokens + P.tpc - 1) / P.tpc + (a.seq_end - a.seq_begin);
+  // (a sequence with tokens has at most one unit that is not full)
+  const int64_t units =
+      a.num_tokens / P.tpc + std::min((int64_t)(a.seq_end - a.seq_begin), a.num_tokens);
+  if (units * g.kvh * 2 > INT32_MAX) return cudaErrorInvalidConfiguration;
   const bool cap = g.softcap > 0.f, two = P.vg <= 128;
   auto go = [&](auto* typed) {
     using T = std::remove_pointer_t<decltype(typed)>;

@@ -436,3 +436,72 @@ def test_workspace_refused_before_launch():
     op.workspace = None
     with pytest.raises(B.PaError, match="workspace"):
         op.forward(*_args(d), 3)
+
+
+def _row(w, b, j):
+    """The cache row of position j of sequence b."""
+    return int(w.tensors["block_table"][b, j // w.block_size]) * w.block_size + j % w.block_size
+
+
+@pytest.mark.parametrize("name", ["64_128", "128_256", "mqa_16"])
+def test_decode_nan_in_a_seen_key(name):
+    """NaN in one seen key of one kv head and map: the rows of that head's
+    queries are NaN, wherever in a long sequence and its parts the key lies;
+    other heads and sequences do not change."""
+    for at in (0, 17, 2500, 5000):
+        w = workload(name, q_lens=[1, 1], past_lens=[5000, 100], drop_slots=0)
+        _, want, _ = run_gpu(w)
+        t = w.tensors
+        kv, last = w.kv_num_heads, w.kv_num_heads - 1
+        if at == 5000:  # the new token's own key
+            t["key"].view(2, kv, 2, -1)[0, last, 1] = float("nan")
+        else:
+            t["key_cache"].view(-1, kv, 2, w.head_size)[_row(w, 0, at), last, 1] = float("nan")
+        _, got, op = run_gpu(w)
+        assert op.error_flags() == 0
+        grp = w.num_heads // kv
+        got, want = got.view(2, w.num_heads, -1), want.view(2, w.num_heads, -1)
+        assert torch.isnan(got[0, last * grp:].float()).all()
+        assert torch.equal(got[0, :last * grp], want[0, :last * grp]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("kind", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("name", ["64_128", "128_256", "fp16", "fp16_128_256", "window_7", "window_100", "grp_40", "vhs_136"])
+def test_prefill_values_seen_by_some_rows(kind, name):
+    """A value that is not finite reaches no token that does not see its key
+    (an earlier one, or one whose window lies behind it): those rows are bit
+    for bit what they are with zeros there. With NaN the others are NaN."""
+    q, past = 90, 60
+    w = workload(name, q_lens=[q], past_lens=[past], block_size=16, drop_slots=0)
+    t = w.tensors
+    kv, win = w.kv_num_heads, w.local_window_size
+    rng = np.random.default_rng(3)
+    for j in (past, past + 1, past + 37, past + 67, past + q - 1, past - 5):
+        new = j >= past
+        target = t["value"].view(q, kv, -1)[j - past] if new else \
+            t["value_cache"].view(-1, kv, w.v_head_size)[_row(w, 0, j)]
+        keep, c = target.clone(), int(rng.integers(0, w.v_head_size))
+        outs = []
+        for v in (0.0, kind):
+            target[kv - 1, c] = v
+            _, o, op = run_gpu(w, decodes=0)
+            assert op.error_flags() == 0
+            outs.append(o.view(q, kv, -1))
+        target.copy_(keep)
+        pos = torch.arange(past, past + q)
+        sees = ((pos >= j) & ((pos - j <= win) if win >= 0 else (pos >= 0))).cuda()
+        zero, got = outs
+        assert torch.equal(got[:, :kv - 1], zero[:, :kv - 1])
+        if kind != kind:
+            assert torch.isnan(got[sees, kv - 1].float()).all()
+        assert torch.equal(got[~sees, kv - 1], zero[~sees, kv - 1]), j
+
+
+def test_more_sequences_than_tokens():
+    """Empty sequences between a few tokens."""
+    q = [0] * 200
+    for b in (0, 63, 64, 150, 199):
+        q[b] = 3
+    past = [b % 40 for b in range(200)]
+    check(workload("64_128", q_lens=q, past_lens=past, num_heads=2, kv_num_heads=1, block_size=16, drop_slots=0),
+          decodes=0)
