@@ -220,7 +220,8 @@ class DifferentialAttention:
     and key maps per head and one value, the difference of the two softmax
     maps with the layer's learned lambda, RMSNorm per head. Holds the
     parameters, the workspace and the error word; ``forward`` issues write ->
-    decode -> prefill like ``PagedLatentAttention``.
+    decode -> prefill like ``PagedLatentAttention``. Calls of one object share
+    its workspace: order them (one stream, or events).
 
     ``query`` [T, H*2*hs], ``key`` [T, kvH*2*hs], ``value`` [T, kvH*vhs],
     ``key_cache`` [num_blocks, bs, kvH, 2, hs], ``value_cache`` [num_blocks,
@@ -261,43 +262,48 @@ class DifferentialAttention:
         self.err_flags = torch.zeros(1, dtype=torch.int32, device=self.device)
 
     # -- argument checks: types, devices and sizes the C side cannot see
-    def _tensors(self, dtype, **tensors):
-        for name, t in tensors.items():
-            if t.dtype is not dtype or t.get_device() != self._index or not t.is_contiguous():
+    def _tensors(self, dtype, names, *tensors):
+        index = self._index
+        for t in tensors:
+            if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+                name = names.split()[[x is t for x in tensors].index(True)]
                 _require(False, f"{name} must be a contiguous {dtype} tensor on {self.device}")
 
     def _check_caches(self, key_cache, value_cache, cos_cache, sin_cache, cumseq, past):
         p, hs, vhs = self.params, self.head_size, self.v_head_size
-        self._tensors(self.dtype, key_cache=key_cache, value_cache=value_cache)
-        self._tensors(torch.int32, cumseq=cumseq, past=past)
+        if p.rotary_dim:
+            self._tensors(self.dtype, "key_cache value_cache cos_cache sin_cache", key_cache,
+                          value_cache, cos_cache, sin_cache)
+            half = p.rotary_dim // 2
+            n = p.cos_rows * half
+            _require(cos_cache.size(-1) == sin_cache.size(-1) == half
+                     and cos_cache.numel() >= n and sin_cache.numel() >= n,
+                     "cos_cache and sin_cache must be [cos_rows, rotary_dim / 2]")
+        else:
+            self._tensors(self.dtype, "key_cache value_cache", key_cache, value_cache)
+        self._tensors(torch.int32, "cumseq past", cumseq, past)
         rows = p.num_blocks * p.block_size * p.kv_num_heads
         _require(key_cache.numel() == rows * 2 * hs and value_cache.numel() == rows * vhs,
                  "key_cache must be [num_blocks, bs, kvH, 2, hs], value_cache [num_blocks, bs, "
                  "kvH, vhs]")
         _require(cumseq.numel() == past.numel() + 1, "cumseq must be [num_seqs + 1]")
-        if p.rotary_dim:
-            self._tensors(self.dtype, cos_cache=cos_cache, sin_cache=sin_cache)
-            n = p.cos_rows * (p.rotary_dim // 2)
-            _require(cos_cache.shape[-1] == sin_cache.shape[-1] == p.rotary_dim // 2
-                     and cos_cache.numel() >= n and sin_cache.numel() >= n,
-                     "cos_cache and sin_cache must be [cos_rows, rotary_dim / 2]")
 
     def _check_write(self, key, value, slot_mapping):
-        self._tensors(self.dtype, key=key, value=value)
-        self._tensors(torch.int32, slot_mapping=slot_mapping)
-        n = key.shape[0]
+        self._tensors(self.dtype, "key value", key, value)
+        self._tensors(torch.int32, "slot_mapping", slot_mapping)
+        n = key.size(0)
         _require(key.numel() == n * self.kv_num_heads * 2 * self.head_size
-                 and value.shape[0] == n and value.numel() == n * self.kv_num_heads * self.v_head_size
+                 and value.size(0) == n and value.numel() == n * self.kv_num_heads * self.v_head_size
                  and slot_mapping.numel() == n,
                  "key must be [T, kvH*2*hs], value [T, kvH*vhs], slot_mapping [T]")
 
     def _check_read(self, query, lambda_vectors, norm_weight, past, block_table, out):
-        self._tensors(self.dtype, query=query, norm_weight=norm_weight, out=out)
-        self._tensors(torch.int32, block_table=block_table)
-        self._tensors(torch.float32, lambda_vectors=lambda_vectors)
-        n = query.shape[0]
+        self._tensors(self.dtype, "query norm_weight out", query, norm_weight, out)
+        self._tensors(torch.int32, "block_table", block_table)
+        self._tensors(torch.float32, "lambda_vectors", lambda_vectors)
+        n = query.size(0)
         _require(query.numel() == n * self.num_heads * 2 * self.head_size
-                 and out.shape[0] == n and out.numel() == n * self.num_heads * self.v_head_size
+                 and out.size(0) == n and out.numel() == n * self.num_heads * self.v_head_size
                  and norm_weight.numel() == self.v_head_size
                  and lambda_vectors.numel() == 4 * self.head_size
                  and block_table.numel() == past.numel() * self.params.max_blocks_per_seq,
@@ -354,21 +360,21 @@ class DifferentialAttention:
                 stream=None) -> torch.Tensor:
         """Write phase over all tokens, then decode over sequences [0,
         num_decode_seqs) and prefill over the rest; returns ``out``."""
-        nseq = past.shape[0]
+        nseq = past.size(0)
         _require(0 <= num_decode_seqs <= nseq, "num_decode_seqs must be in 0..num_seqs")
         with self._on_device():
+            self._check_caches(key_cache, value_cache, cos_cache, sin_cache, cumseq, past)
+            self._check_write(key, value, slot_mapping)
+            _require(key.size(0) == query.size(0), "query and key must have a row per token")
             if out is None:
-                shape = (query.shape[0], self.num_heads * self.v_head_size)
+                shape = (query.size(0), self.num_heads * self.v_head_size)
                 if isinstance(stream, torch.cuda.Stream):  # memory of the stream that writes it
                     with torch.cuda.stream(stream):
                         out = torch.empty(shape, dtype=self.dtype, device=self.device)
                 else:
                     out = torch.empty(shape, dtype=self.dtype, device=self.device)
             stream = B.raw_stream(stream)
-            self._check_caches(key_cache, value_cache, cos_cache, sin_cache, cumseq, past)
-            self._check_write(key, value, slot_mapping)
             self._check_read(query, lambda_vectors, norm_weight, past, block_table, out)
-            _require(key.shape[0] == query.shape[0], "query and key must have a row per token")
             B.pa_diff_write(self.params, key, value, cos_cache, sin_cache, slot_mapping, cumseq,
                             past, key_cache, value_cache, self.err_flags, stream)
             args = (query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
@@ -433,7 +439,7 @@ class PagePool:
             past = torch.zeros(block_table.shape[0], dtype=torch.int32, device=self.device)
         if refcount is None:
             refcount = torch.zeros(self.num_blocks, dtype=torch.int32, device=self.device)
-        self._ints(block_table=block_table, past=past, refcount=refcount)
+        self._ints("block_table past refcount", block_table, past, refcount)
         _require(past.numel() == block_table.shape[0], "past must be [num_seqs]")
         _require(refcount.numel() == self.num_blocks, "refcount must be [num_blocks]")
         self.block_table, self.past, self.refcount = block_table, past, refcount
@@ -450,52 +456,59 @@ class PagePool:
         #: pages held after the last ``compact`` (int32 [1] on the device)
         self.live = torch.zeros(1, dtype=torch.int32, device=self.device)
 
-    def _ints(self, **tensors):
-        for name, t in tensors.items():
-            if t.dtype is not torch.int32 or t.get_device() != self._index or not t.is_contiguous():
+    def _ints(self, names, *tensors):
+        index = self._index
+        for t in tensors:
+            if t.dtype is not torch.int32 or t.get_device() != index or not t.is_contiguous():
+                name = names.split()[[x is t for x in tensors].index(True)]
                 _require(False, f"{name} must be a contiguous int32 tensor on {self.device}")
-
-    def _call(self, fn, *args, stream):
-        with _device(self._index):
-            fn(self.params, *args, err_flags=self.err_flags, stream=stream)
 
     def copy(self, src, dst, rows=None, stream=None):
         """Pages ``src[i]`` -> ``dst[i]`` (their first ``rows[i]`` rows) in every cache."""
-        self._ints(src=src, dst=dst, **({} if rows is None else {"rows": rows}))
+        if rows is None:
+            self._ints("src dst", src, dst)
+        else:
+            self._ints("src dst rows", src, dst, rows)
         _require(dst.numel() == src.numel() and (rows is None or rows.numel() == src.numel()),
                  "src, dst and rows must have one entry per pair")
-        self._call(B.pa_pages_copy, self._list, len(self.caches), src, dst, rows, self.workspace,
-                   stream=stream)
+        with _device(self._index):
+            B.pa_pages_copy(self.params, self._list, len(self.caches), src, dst, rows,
+                            self.workspace, self.err_flags, stream)
 
     def fork(self, parents, children, stream=None):
         """Sequence ``children[i]`` becomes a copy of ``parents[i]``: full pages
         shared, the rows of the last one copied into a page of its own."""
-        self._ints(parents=parents, children=children)
+        self._ints("parents children", parents, children)
         _require(parents.numel() == children.numel(), "parents and children must pair up")
-        self._call(B.pa_pages_fork, self._list, len(self.caches), parents, children,
-                   self.block_table, self.past, self.refcount, self.workspace, stream=stream)
+        with _device(self._index):
+            B.pa_pages_fork(self.params, self._list, len(self.caches), parents, children,
+                            self.block_table, self.past, self.refcount, self.workspace,
+                            self.err_flags, stream)
 
     def free(self, seqs, stream=None):
         """Takes the pages of ``seqs`` back (their rows become -1, their past 0)."""
-        self._ints(seqs=seqs)
-        self._call(B.pa_pages_free, seqs, self.block_table, self.past, self.refcount,
-                   stream=stream)
+        self._ints("seqs", seqs)
+        with _device(self._index):
+            B.pa_pages_free(self.params, seqs, self.block_table, self.past, self.refcount,
+                            self.err_flags, stream)
 
     def reserve(self, cumseq, slot_mapping, stream=None) -> torch.Tensor:
         """Pages for the ``cumseq[b+1] - cumseq[b]`` next tokens of every
         sequence; fills ``slot_mapping`` [T] for the write phase and returns
         it. ``past`` stays (add the new tokens once they are written)."""
-        self._ints(cumseq=cumseq, slot_mapping=slot_mapping)
+        self._ints("cumseq slot_mapping", cumseq, slot_mapping)
         _require(cumseq.numel() == self.past.numel() + 1, "cumseq must be [num_seqs + 1]")
-        self._call(B.pa_pages_reserve, cumseq, self.block_table, self.past, self.refcount,
-                   slot_mapping, self.workspace, stream=stream)
+        with _device(self._index):
+            B.pa_pages_reserve(self.params, cumseq, self.block_table, self.past, self.refcount,
+                               slot_mapping, self.workspace, self.err_flags, stream)
         return slot_mapping
 
     def compact(self, stream=None) -> torch.Tensor:
         """Moves the held pages to the lowest ids; returns ``live`` (their
         number, on the device)."""
-        self._call(B.pa_pages_compact, self._list, len(self.caches), self.block_table,
-                   self.refcount, self.live, self.workspace, stream=stream)
+        with _device(self._index):
+            B.pa_pages_compact(self.params, self._list, len(self.caches), self.block_table,
+                               self.refcount, self.live, self.workspace, self.err_flags, stream)
         return self.live
 
     def error_flags(self) -> int:

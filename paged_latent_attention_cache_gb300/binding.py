@@ -460,35 +460,35 @@ def _ws(workspace):
 
 
 def pa_pages_copy(p, caches, num_caches, src, dst, rows, workspace, err_flags=None, stream=None):
-    _check(lib.pa_pages_copy(ctypes.byref(p), caches, num_caches, _addr(src), _addr(dst),
+    _check(lib.pa_pages_copy(ctypes.byref(p), caches, num_caches, src.data_ptr(), dst.data_ptr(),
                              _addr(rows), src.numel(), *_ws(workspace), _addr(err_flags),
                              raw_stream(stream)))
 
 
 def pa_pages_fork(p, caches, num_caches, parents, children, block_table, past, refcount,
                   workspace, err_flags=None, stream=None):
-    _check(lib.pa_pages_fork(ctypes.byref(p), caches, num_caches, _addr(parents),
-                             _addr(children), parents.numel(), _addr(block_table), _addr(past),
-                             _addr(refcount), *_ws(workspace), _addr(err_flags), raw_stream(stream)))
+    _check(lib.pa_pages_fork(ctypes.byref(p), caches, num_caches, parents.data_ptr(),
+                             children.data_ptr(), parents.numel(), block_table.data_ptr(), past.data_ptr(),
+                             refcount.data_ptr(), *_ws(workspace), _addr(err_flags), raw_stream(stream)))
 
 
 def pa_pages_free(p, seqs, block_table, past, refcount, err_flags=None, stream=None):
-    _check(lib.pa_pages_free(ctypes.byref(p), _addr(seqs), seqs.numel(), _addr(block_table),
-                             _addr(past), _addr(refcount), _addr(err_flags), raw_stream(stream)))
+    _check(lib.pa_pages_free(ctypes.byref(p), seqs.data_ptr(), seqs.numel(), block_table.data_ptr(),
+                             past.data_ptr(), refcount.data_ptr(), _addr(err_flags), raw_stream(stream)))
 
 
 def pa_pages_reserve(p, cumseq, block_table, past, refcount, slot_mapping, workspace,
                      err_flags=None, stream=None):
-    _check(lib.pa_pages_reserve(ctypes.byref(p), _addr(cumseq), slot_mapping.numel(),
-                                _addr(block_table), _addr(past), _addr(refcount),
-                                _addr(slot_mapping), *_ws(workspace), _addr(err_flags),
+    _check(lib.pa_pages_reserve(ctypes.byref(p), cumseq.data_ptr(), slot_mapping.numel(),
+                                block_table.data_ptr(), past.data_ptr(), refcount.data_ptr(),
+                                slot_mapping.data_ptr(), *_ws(workspace), _addr(err_flags),
                                 raw_stream(stream)))
 
 
 def pa_pages_compact(p, caches, num_caches, block_table, refcount, live, workspace,
                      err_flags=None, stream=None):
-    _check(lib.pa_pages_compact(ctypes.byref(p), caches, num_caches, _addr(block_table),
-                                _addr(refcount), _addr(live), *_ws(workspace), _addr(err_flags),
+    _check(lib.pa_pages_compact(ctypes.byref(p), caches, num_caches, block_table.data_ptr(),
+                                refcount.data_ptr(), _addr(live), *_ws(workspace), _addr(err_flags),
                                 raw_stream(stream)))
 
 
@@ -516,37 +516,30 @@ def pa_diff_workspace_size(p: pa_diff_params, num_seqs: int, num_tokens: int) ->
 
 def pa_diff_write(p, key, value, cos_cache, sin_cache, slot_mapping, cumseq, past, key_cache,
                   value_cache, err_flags=None, stream=None):
-    _check(lib.pa_diff_write(ctypes.byref(p), _addr(key), _addr(value), key.shape[0],
-                             _addr(cos_cache), _addr(sin_cache), _addr(slot_mapping), _addr(cumseq),
-                             _addr(past), past.shape[0], _addr(key_cache), _addr(value_cache),
-                             _addr(err_flags), raw_stream(stream)))
+    _check(lib.pa_diff_write(ctypes.byref(p), key.data_ptr(), value.data_ptr(), key.size(0),
+                             _addr(cos_cache), _addr(sin_cache), slot_mapping.data_ptr(),
+                             cumseq.data_ptr(), past.data_ptr(), past.size(0),
+                             key_cache.data_ptr(), value_cache.data_ptr(), _addr(err_flags),
+                             raw_stream(stream)))
 
 
-def _dread(fn, p, query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
-           norm_weight, cumseq, past, block_table, out, seq_begin, seq_end, workspace, err_flags,
-           stream):
-    n = past.shape[0]
-    _check(fn(ctypes.byref(p), _addr(query), query.shape[0], _addr(key_cache),
-              _addr(value_cache), _addr(cos_cache), _addr(sin_cache), _addr(lambda_vectors),
-              _addr(norm_weight), _addr(cumseq), _addr(past), _addr(block_table), n,
-              seq_begin, n if seq_end is None else seq_end, *_ws(workspace),
-              _addr(out), _addr(err_flags), raw_stream(stream)))
+def _diff_read(fn):
+    def read(p, query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors, norm_weight,
+             cumseq, past, block_table, out, seq_begin=0, seq_end=None, workspace=None,
+             err_flags=None, stream=None):
+        n = past.size(0)
+        ws, ws_bytes = _ws(workspace)
+        _check(fn(ctypes.byref(p), query.data_ptr(), query.size(0), key_cache.data_ptr(),
+                  value_cache.data_ptr(), _addr(cos_cache), _addr(sin_cache),
+                  lambda_vectors.data_ptr(), norm_weight.data_ptr(), cumseq.data_ptr(),
+                  past.data_ptr(), block_table.data_ptr(), n, seq_begin,
+                  n if seq_end is None else seq_end, ws, ws_bytes, out.data_ptr(),
+                  _addr(err_flags), raw_stream(stream)))
+    return read
 
 
-def pa_diff_decode(p, query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
-                   norm_weight, cumseq, past, block_table, out, seq_begin=0, seq_end=None,
-                   workspace=None, err_flags=None, stream=None):
-    _dread(lib.pa_diff_decode, p, query, key_cache, value_cache, cos_cache, sin_cache,
-           lambda_vectors, norm_weight, cumseq, past, block_table, out, seq_begin, seq_end,
-           workspace, err_flags, stream)
-
-
-def pa_diff_prefill(p, query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
-                    norm_weight, cumseq, past, block_table, out, seq_begin=0, seq_end=None,
-                    workspace=None, err_flags=None, stream=None):
-    _dread(lib.pa_diff_prefill, p, query, key_cache, value_cache, cos_cache, sin_cache,
-           lambda_vectors, norm_weight, cumseq, past, block_table, out, seq_begin, seq_end,
-           workspace, err_flags, stream)
+pa_diff_decode = _diff_read(lib.pa_diff_decode)
+pa_diff_prefill = _diff_read(lib.pa_diff_prefill)
 
 
 def default_scale(head_size: int) -> float:
