@@ -86,8 +86,20 @@ struct PreBars {
 constexpr int kNumBars = 2 * kMaxK + 2 * kMaxV + 8 + 3 + 4;  // all but q_tma
 static_assert(offsetof(PreBars, q_tma) == kNumBars * 8, "barriers in one row");
 
+// Division by a number that the host knows, of dividends below 2^31, by a
+// product: n d' >> s with d' = ceil(2^s / d), s = 31 + ceil(log2 d) (Granlund and
+// Montgomery, 1994). The compiler's division is a hundred instructions, which
+// a CTA fetches cold at its start.
+struct Divisor {
+  uint32_t mul, shift;
+};
+__device__ __forceinline__ int divide(int n, const Divisor& d) {
+  return (int)(((uint64_t)(uint32_t)n * d.mul) >> d.shift);
+}
+
 struct PreArgs {
   Params P;           // what the shared helpers read
+  Divisor by_kvh, by_tpc, by_grp;
   int hs;
   int nk, nv, v_bytes, v_rows;  // slots of the rings; bytes of a value slot, rows of its boxes
   bool k_whole, v_whole;        // widths that are multiples of 64: see cache_map
@@ -253,8 +265,10 @@ __device__ __forceinline__ float exp_row(uint32_t (&r)[32], uint32_t (&pk)[16], 
 }
 
 // prefill_group_warp for up to 32 sequences: one round of loads, the rest in
-// registers, instead of a chain of three.
-__device__ __forceinline__ Work unit_warp(const Params& P, int unit, int lane) {
+// registers, instead of a chain of three. Short code: it is fetched cold in
+// every CTA (with divisions and the scan unrolled it took 2700 cycles).
+__device__ __forceinline__ Work unit_warp(const PreArgs& A, int unit, int lane) {
+  const Params& P = A.P;
   const int nseq = P.pf_end - P.pf_begin;
   if (nseq > 32) return prefill_group_warp(P, unit, P.tpc);
   int q0 = 0, q1 = 0, past = 0;
@@ -263,9 +277,9 @@ __device__ __forceinline__ Work unit_warp(const Params& P, int unit, int lane) {
     q1 = P.cumseq[P.pf_begin + lane + 1];
     past = P.past[P.pf_begin + lane];
   }
-  const int cnt = q1 > q0 ? ceil_div32(q1 - q0, P.tpc) : 0;
+  const int cnt = q1 > q0 ? divide(q1 - q0 - 1, A.by_tpc) + 1 : 0;
   int incl = cnt;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
@@ -304,46 +318,44 @@ __device__ __forceinline__ void zero_values(uint8_t* slot, PreBars* bars, int vs
   // rows from r_lo to r_hi that some row does not see, in them [s_lo, s_hi) that
   // any does
   const int r_lo = j0 < lo_hi ? 0 : (int)max((int64_t)0, pos + 1 - j0);
-  const int r_hi = j0 + kVKeys - 1 > pos ? kVKeys : (int)(lo_hi - j0);
-  const int s_lo = max(r_lo, (int)max((int64_t)0, lo - j0));
-  const int s_hi = (int)min((int64_t)r_hi, pos_hi + 1 - j0);
+  const int r_hi = j0 + kVKeys - 1 > pos ? kVKeys : (int)min((int64_t)kVKeys, lo_hi - j0);
+  const int s_lo = (int)max((int64_t)r_lo, min((int64_t)kVKeys, lo - j0));
+  const int s_hi = (int)max((int64_t)0, min((int64_t)r_hi, pos_hi + 1 - j0));
+  const uint4 zero = make_uint4(0, 0, 0, 0);
   uint8_t* mine = slot + (lane >> 3) * 128 + (lane & 7) * 16;
   uint32_t odd = 0;
 #pragma unroll 1
-  for (int c = 0; c < vslabs; ++c) {  // (four loads in flight: 16 rows)
+  for (int c = 0; c < vslabs; ++c) {  // 16 rows at a time, without branches
 #pragma unroll 1
-    for (int r = s_lo & ~3; r < s_hi; r += 16) {
+    for (int r = r_lo & ~3; r < r_hi; r += 16) {
       uint4 v[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int q = r + 4 * k + (lane >> 3);
-        v[k] = q >= s_lo && q < s_hi
-                   ? *reinterpret_cast<const uint4*>(mine + c * kVBox + (r + 4 * k) * 128)
-                   : make_uint4(0, 0, 0, 0);
+        uint4* at = reinterpret_cast<uint4*>(mine + c * kVBox + (r + 4 * k) * 128);
+        const bool seen = q >= s_lo && q < s_hi;
+        v[k] = zero;
+        if (seen) v[k] = *at;
+        if (!seen && q >= r_lo && q < r_hi) *at = zero;
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) odd |= not_finite<T>(v[k]);
     }
   }
-  const bool any = __any_sync(0xffffffffu, odd != 0);
+  if (!__any_sync(0xffffffffu, odd != 0)) return;
 #pragma unroll 1
-  for (int r = (r_lo & ~3) + (lane >> 3); r < r_hi; r += 4) {
-    const bool seen = r >= s_lo && r < s_hi;
+  for (int r = s_lo + (lane >> 3); r < s_hi; r += 4) {
     const int64_t j = j0 + r;
-    if (r < r_lo || (seen && !any) || (j <= pos && j >= lo_hi)) continue;
-    bool hit = false;
+    if (j <= pos && j >= lo_hi) continue;  // all rows see it
 #pragma unroll 1
     for (int c = 0; c < vslabs; ++c) {
       uint4* at = reinterpret_cast<uint4*>(slot + c * kVBox + r * 128 + (lane & 7) * 16);
-      if (!seen || not_finite<T>(*at)) {
-        *at = make_uint4(0, 0, 0, 0);
-        hit = true;
+      if (not_finite<T>(*at)) {
+        *at = zero;
+        const int bit = j > pos ? (int)(j - pos) : 128 + (int)(j - lo);
+        atomicOr(&bars->odd[bit >> 5], 1u << (bit & 31));
+        bars->any_odd = 1;
       }
-    }
-    if (seen && hit) {
-      const int bit = j > pos ? (int)(j - pos) : 128 + (int)(j - lo);
-      atomicOr(&bars->odd[bit >> 5], 1u << (bit & 31));
-      bars->any_odd = 1;
     }
   }
 }
@@ -375,7 +387,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   const int kvh = P.kvh, grp = P.grp, vhs = P.vhs;
   const int map = (int)cluster_rank();
   const int pair = blockIdx.x >> 1;
-  const int unit = pair / kvh, gk = pair - unit * kvh;
+  const int unit = divide(pair, A.by_kvh), gk = pair - unit * kvh;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -383,7 +395,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       fence_barrier_init();
     }
     if (!P.early) grid_dep_wait();
-    Work w = unit_warp(P, unit, lane);
+    Work w = unit_warp(A, unit, lane);
     if (w.status == 0) {
       const int64_t pos_hi = w.pos + w.ntok - 1;
       const bool bad_ctx = w.past < 0 || pos_hi >= (int64_t)P.max_blocks * P.bs || w.t < 0 ||
@@ -466,7 +478,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 
     if (warp < kSoftWarps) {
       // =================== softmax ===================
-      const int64_t pos_r = row < rows ? pos + row / grp : -1;
+      const int64_t pos_r = row < rows ? pos + divide(row, A.by_grp) : -1;
       const int64_t lo_r = P.window >= 0 ? max((int64_t)0, pos_r - P.window) : 0;
       RowAngles<T> ang;
       if (row < rows && P.rd > 0 && !P.interleaved) ang.load(P, half, pos_r);
@@ -716,7 +728,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       coef = lt > 0.f ? (map == 0 ? 1.f : lam) / lt : 0.f;
       if (bars->any_odd) {
         // (from the unit's record again: nothing of this is kept over the tiles)
-        const int64_t p0 = work.pos, last = p0 + row / P.grp;
+        const int64_t p0 = work.pos, last = p0 + divide(row, A.by_grp);
         const int64_t back = P.window >= 0 ? P.window : last;
 #pragma unroll 1
         for (int i = 0; i < 256; ++i)
@@ -785,6 +797,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           }
         }
         if (issued * step + h >= slots) {
+          release();  // (the wait may be for the product behind these values)
           bool w = true;
           if (lane == 0) w = wait_bar(smem_u32(&empty[slot]), par, abort, P.err_flags);
           if (!__shfl_sync(0xffffffffu, w ? 1 : 0, 0)) break;
@@ -1003,13 +1016,12 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   }
   if (run && warp < kSoftWarps) {
     named_sync(9, kSoft);
-    // 16 lanes a row; r / grp by a product (rows below 128)
+    // 16 lanes a row
     const int nc = max(0, min(vg >> 1, vhs - first)) >> 3, c = lane & 15;
-    const uint32_t inv_grp = 65536u / (uint32_t)grp + 1u;
     if (ok && !*abort && c < nc) {
       T* base = reinterpret_cast<T*>(P.out) + (W.t * P.H + gk * grp) * (int64_t)vhs + first + c * 8;
       for (int q = warp * 2 + (lane >> 4); q < rows; q += kSoftWarps * 2) {
-        const int tok = (int)(((uint32_t)q * inv_grp) >> 16);
+        const int tok = divide(q, A.by_grp);
         *reinterpret_cast<uint4*>(base + ((int64_t)tok * P.H + (q - tok * grp)) * vhs) =
             *reinterpret_cast<const uint4*>(x_out + q * pitch + ((c ^ (q & 7)) << 4));
       }
@@ -1087,6 +1099,12 @@ cudaError_t launch(const Geometry& g, const DiffArgs& a, const PreArgs& A, int64
 
 }  // namespace
 
+static Divisor divisor(uint32_t d) {
+  uint32_t l = 0;
+  while ((1ull << l) < d) ++l;
+  return {(uint32_t)(((1ull << (31 + l)) + d - 1) / d), 31 + l};
+}
+
 cudaError_t launch_prefill(const Geometry& g, const DiffArgs& a) {
   PreArgs A{};
   Params& P = A.P;
@@ -1123,6 +1141,9 @@ cudaError_t launch_prefill(const Geometry& g, const DiffArgs& a) {
   P.kvh = g.kvh;
   P.grp = grp;
   P.tpc = kRows / grp;
+  A.by_kvh = divisor((uint32_t)g.kvh);
+  A.by_tpc = divisor((uint32_t)P.tpc);
+  A.by_grp = divisor((uint32_t)grp);
   P.slabs = (g.hs + 63) / 64;
   P.vslabs = (g.vhs + 63) / 64;
   P.vg = 64 * P.vslabs;

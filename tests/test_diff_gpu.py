@@ -505,3 +505,12 @@ def test_more_sequences_than_tokens():
     past = [b % 40 for b in range(200)]
     check(workload("64_128", q_lens=q, past_lens=past, num_heads=2, kv_num_heads=1, block_size=16, drop_slots=0),
           decodes=0)
+
+
+@pytest.mark.parametrize("name", ["64_128", "128_256"])
+@pytest.mark.parametrize("window", [0, 31, 63, 64, 65, 100, 127, 128, 129, 200])
+def test_prefill_windows(name, window):
+    """Windows that begin anywhere in a tile of keys or in the half tiles that
+    its values come in, or leave such a half to nobody."""
+    check(workload(name, q_lens=[70, 150], past_lens=[301, 77], local_window_size=window, num_heads=4,
+                   block_size=16, drop_slots=0))
