@@ -72,7 +72,7 @@ constexpr size_t kSmemMax = 225 * 1024;
 struct PreBars {
   uint64_t k_full[kMaxK], k_empty[kMaxK], v_full[kMaxV], v_empty[kMaxV];
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
-  uint64_t q_full, drain, x_full;
+  uint64_t q_full, drain, x_full[4];  // (x_full: a quadrant of 32 rows each)
   uint64_t v_land[2][2];  // [half][tile parity] values whose unseen rows are zeroed before v_full
   uint64_t q_tma;  // (set up by the warp that uses it first)
   uint32_t tmem_base;
@@ -83,7 +83,7 @@ struct PreBars {
   int any_odd;
 };
 
-constexpr int kNumBars = 2 * kMaxK + 2 * kMaxV + 8 + 3 + 4;  // all but q_tma
+constexpr int kNumBars = 2 * kMaxK + 2 * kMaxV + 8 + 6 + 4;  // all but q_tma
 static_assert(offsetof(PreBars, q_tma) == kNumBars * 8, "barriers in one row");
 
 // Division by a number that the host knows, of dividends below 2^31, by a
@@ -143,21 +143,11 @@ __device__ __forceinline__ void bulk_copy_peer(uint32_t dst, uint32_t src, uint3
       "[%3];" ::"r"(dst), "r"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
-#pragma unroll
-  for (int i = 0; i < 16; i += 8)
-    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]),
-                 "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void st_peer(uint32_t raddr, float a) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(raddr), "f"(a) : "memory");
@@ -190,7 +180,7 @@ __device__ __forceinline__ uint4* q_chunk(uint8_t* q_s, int row, int d0) {
 }
 template <typename T>
 __device__ __forceinline__ void rotate_row(uint8_t* q_s, int row, int part, const Params& P,
-                                           int64_t pos, const RowAngles<T>& A) {
+                                           int64_t pos, RowAngles<T>& A) {
   const int half = P.rd >> 1;
   if (P.interleaved) {
     const T* crow = reinterpret_cast<const T*>(P.cos_cache) + pos * half;
@@ -204,22 +194,24 @@ __device__ __forceinline__ void rotate_row(uint8_t* q_s, int row, int part, cons
     }
     return;
   }
+#pragma unroll 1
+  for (int d = part * 8; d < half; d += 16) {
+    float x[8], y[8], c[8], sn[8], u[8], v[8];
+    unpack8<T>(*q_chunk(q_s, row, P.ro + d), x);
+    unpack8<T>(*q_chunk(q_s, row, P.ro + half + d), y);
+    unpack8<T>(A.c[0], c);
+    unpack8<T>(A.s[0], sn);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int d = (2 * i + part) * 8;
-    if (d < half) {
-      float x[8], y[8], c[8], sn[8], u[8], v[8];
-      unpack8<T>(*q_chunk(q_s, row, P.ro + d), x);
-      unpack8<T>(*q_chunk(q_s, row, P.ro + half + d), y);
-      unpack8<T>(A.c[i], c);
-      unpack8<T>(A.s[i], sn);
+    for (int e = 0; e < 8; ++e) {  // as rope8
+      u[e] = fmaf(x[e], c[e], -y[e] * sn[e]);
+      v[e] = fmaf(y[e], c[e], x[e] * sn[e]);
+    }
+    *q_chunk(q_s, row, P.ro + d) = pack8<T>(u);
+    *q_chunk(q_s, row, P.ro + half + d) = pack8<T>(v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {  // as rope8
-        u[e] = fmaf(x[e], c[e], -y[e] * sn[e]);
-        v[e] = fmaf(y[e], c[e], x[e] * sn[e]);
-      }
-      *q_chunk(q_s, row, P.ro + d) = pack8<T>(u);
-      *q_chunk(q_s, row, P.ro + half + d) = pack8<T>(v);
+    for (int i = 0; i < 3; ++i) {  // (a loop, with the next entries in place)
+      A.c[i] = A.c[i + 1];
+      A.s[i] = A.s[i + 1];
     }
   }
 }
@@ -919,75 +911,69 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 
   // =================== epilogue ===================
   // CTA r finishes channels [r vg / 2, (r + 1) vg / 2). The cluster barriers are
-  // met by every thread of both CTAs, whatever the unit's state.
-  const int cols = vg >> 2;  // columns a thread hands over, and columns it finishes
-  const int xbytes = kRows * vg * 2;  // half the channels of every row, f32
-  uint8_t* x_out = k_s;               // in the rings, which nobody uses any more
-  uint8_t* x_in = k_s + xbytes;
+  // met by every thread of both CTAs, whatever the unit's state. The outputs
+  // travel a quadrant of 32 rows at a time. Everything is a loop: straight code
+  // that a CTA runs once is fetched cold, at some ten cycles an instruction.
+  const int cols = vg >> 2;        // columns a thread hands over, and columns it finishes
+  const int xquad = 32 * vg * 2;   // half the channels of a quadrant's rows, f32
+  uint8_t* x_out = k_s;            // in the rings, which nobody uses any more
+  uint8_t* x_in = k_s + 4 * xquad;
+  const int quad = warp & 3;
   const bool fin = live && ok && n > 0;
   // 16-byte chunk ch of row r stands at ch ^ (r & 7)
   auto chunk = [&](uint8_t* at, int pitch, int ch) {
     return at + row * pitch + ((ch ^ (row & 7)) << 4);
   };
-  uint32_t r[4][16];
-  auto load_cols = [&](int first) {  // this thread's columns from `first` on
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (c * 16 < cols) tmem_ld16_nowait(lane_addr + first + half * cols + c * 16, r[c]);
-    tmem_wait_ld();
-#pragma unroll
-    for (int c = 0; c < 4; ++c) reg_fence16(r[c]);
-  };
+  cluster_arrive();  // this CTA's rings are free
   if (fin) {
-    load_cols((1 - map) * (vg >> 1));
+#pragma unroll 1
+    for (int c = 0; c < cols; c += 16) {
+      uint32_t r[16];
+      tmem_ld16(lane_addr + (1 - map) * (vg >> 1) + half * cols + c, r);
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (c * 16 < cols) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          *reinterpret_cast<float4*>(chunk(x_out, vg * 2, ((half * cols + c * 16) >> 2) + e)) =
-              make_float4(__uint_as_float(r[c][4 * e]) * coef, __uint_as_float(r[c][4 * e + 1]) * coef,
-                          __uint_as_float(r[c][4 * e + 2]) * coef,
-                          __uint_as_float(r[c][4 * e + 3]) * coef);
-      }
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<float4*>(chunk(x_out, vg * 2, ((half * cols + c) >> 2) + e)) =
+            make_float4(__uint_as_float(r[4 * e]) * coef, __uint_as_float(r[4 * e + 1]) * coef,
+                        __uint_as_float(r[4 * e + 2]) * coef, __uint_as_float(r[4 * e + 3]) * coef);
+    }
     fence_proxy_async();
   }
-  cluster_sync_all();  // also: the peer's rings are free, its outgoing columns written
-  if (run && warp == 0) {
-    if (elect_one()) {
-      mbar_expect_tx(smem_u32(&bars->x_full), (uint32_t)xbytes);
+  if (live) named_sync(1 + quad, 64);
+  cluster_wait();  // the peer's are
+  if (live) {
+    uint64_t* full = &bars->x_full[quad];
+    if (half == 0 && elect_one()) {
+      mbar_expect_tx(smem_u32(full), (uint32_t)xquad);
       if (ok)
-        bulk_copy_peer(map_peer(smem_u32(x_in), 1 - map), smem_u32(x_out), (uint32_t)xbytes,
-                       map_peer(smem_u32(&bars->x_full), 1 - map));
+        bulk_copy_peer(map_peer(smem_u32(x_in + quad * xquad), 1 - map),
+                       smem_u32(x_out + quad * xquad), (uint32_t)xquad,
+                       map_peer(smem_u32(full), 1 - map));
     }
     __syncwarp();
-  }
-  float x[64], ss = 0.f;
-  if (run && warp < kSoftWarps) {
-    if (fin) load_cols(map * (vg >> 1));
     if (ok)
-      ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->x_full), 0, abort, P.err_flags));
-    else if (tid == 0)  // the peer may write into this CTA until then
-      drain_wait(smem_u32(&bars->x_full), 0, P.err_flags);
+      ok = __all_sync(0xffffffffu, wait_bar(smem_u32(full), 0, abort, P.err_flags));
+    else if (half == 0 && lane == 0)  // the peer may write into this CTA until then
+      drain_wait(smem_u32(full), 0, P.err_flags);
     __syncwarp();
   }
-  if (fin && ok) {
+  if (fin && ok) {  // the difference, in place of the peer's part
+    float ss = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < cols; c += 16) {
+      uint32_t r[16];
+      tmem_ld16(lane_addr + map * (vg >> 1) + half * cols + c, r);
 #pragma unroll
-    for (int c = 0; c < 64; c += 16) {
-      if (c < cols) {
+      for (int e = 0; e < 4; ++e) {
+        float4* at = reinterpret_cast<float4*>(chunk(x_in, vg * 2, ((half * cols + c) >> 2) + e));
+        const float4 p = *at;
+        float d[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float4 p =
-              *reinterpret_cast<const float4*>(chunk(x_in, vg * 2, ((half * cols + c) >> 2) + e));
-          const float pv[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float own = __uint_as_float(r[c >> 4][4 * e + i]) * coef;
-            const float d = map == 0 ? own - pv[i] : pv[i] - own;
-            x[c + 4 * e + i] = d;
-            ss = fmaf(d, d, ss);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const float own = __uint_as_float(r[4 * e + i]) * coef;
+          d[i] = map == 0 ? own - d[i] : d[i] - own;
+          ss = fmaf(d[i], d[i], ss);
         }
+        *at = make_float4(d[0], d[1], d[2], d[3]);
       }
     }
     s_ss[map * 2 + half][row] = ss;
@@ -999,17 +985,20 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   const int pitch = vg <= 128 ? 128 : 256;
   const int first = map * (vg >> 1);  // this CTA's channels
   if (fin && ok) {
-    ss = (s_ss[0][row] + s_ss[1][row]) + (s_ss[2][row] + s_ss[3][row]);
-    const float inv =
-        bars->bad ? 0.f : (1.f - A.lambda_init) / sqrtf(ss / (float)vhs + A.norm_eps);
-#pragma unroll
-    for (int c = 0; c < 64; c += 8) {
+    const float ss = (s_ss[0][row] + s_ss[1][row]) + (s_ss[2][row] + s_ss[3][row]);
+    const bool bad = bars->bad != 0;
+    const float inv = (1.f - A.lambda_init) / sqrtf(ss / (float)vhs + A.norm_eps);
+#pragma unroll 1
+    for (int c = 0; c < cols; c += 8) {
       const int ch = half * cols + c;
-      if (c < cols && first + ch < vhs) {
+      if (first + ch < vhs) {
         float w[8], o[8];
         unpack8<T>(s_norm[(first + ch) >> 3], w);
+        const float4 p = *reinterpret_cast<const float4*>(chunk(x_in, vg * 2, ch >> 2));
+        const float4 q = *reinterpret_cast<const float4*>(chunk(x_in, vg * 2, (ch >> 2) + 1));
+        const float x[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = bars->bad ? 0.f : x[c + e] * inv * w[e];
+        for (int e = 0; e < 8; ++e) o[e] = bad ? 0.f : x[e] * inv * w[e];
         *reinterpret_cast<uint4*>(chunk(x_out, pitch, ch >> 3)) = pack8<T>(o);
       }
     }
