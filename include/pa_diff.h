@@ -28,7 +28,8 @@
  * Arithmetic: products accumulate in f32; softmax, lambda, the difference
  * and the norm are f32; out is rounded once. Operands of the products: keys
  * and values as they are; the rotated query and the probabilities as two
- * 16-bit parts each in decode, rounded to the dtype in prefill.
+ * 16-bit parts each (value and remainder), so that the difference of the two
+ * maps is as exact as its own rounding.
  */
 #ifndef PA_DIFF_H
 #define PA_DIFF_H

@@ -21,26 +21,31 @@
 //             copy costs its thread some 190 cycles, and one warp with a copy
 //             per slab was the slowest part of the kernel (2500 cycles a tile).
 //   warp 11   QK^T (S: 128 x 128 f32 in TMEM), PV (A = P from TMEM, O: 128 x vg)
-//   warps 0-7 softmax. Values wider than 128 channels: two threads per row, 64
-//             columns each; S is read into registers once and is free for the
-//             next QK^T before the exponentials start; P (16 bit) goes to one of
-//             two buffers. TMEM columns: O vg <= 256 | S 128 | P 2 x 64.
-//             Narrower values leave room for a second S: two groups of four
-//             warps on alternate tiles, one thread per row. TMEM: O vg <= 128 |
-//             S 2 x 128 | P 2 x 64.
+//   warps 0-7 softmax, two threads per row, 64 columns each. S is read into
+//             registers once, P is written over it. TMEM columns: O vg <= 256 |
+//             two buffers of 128 for S and P (three where vg <= 128): QK^T of the
+//             next tile runs while the softmax works on this one.
 //
-// Bound: per tile and map the MMAs take 128 * 128 * (hs + vhs) / 4096 cycles
-// (1536 at 128 / 256, 768 at 64 / 128) and the exponentials 16384 / 32 = 512,
-// beside some 300 for the maxima, sums and packing. Measured, 2 x 4096 new
-// tokens over 0 and 4096 cached ones, 16 heads over 4 kv heads, bf16: 128 / 256
-// 744 us, 1.38 PFLOP/s, 0.72 of a library product's rate (a tile takes 1650 to
-// 1850 cycles, a unit some 20000 outside its tiles: lookup and query, the
-// exchange, the norm); 64 / 128 617 us, bound by the softmax (0.43). Few short
-// prompts (2 x 250 tokens, 8 heads) take 32 us: a chain of latencies.
+// Precision: out = softmax_0 V - lambda softmax_1 V cancels, so errors of the
+// two maps weigh more than in a plain softmax. The rotated query and the
+// probabilities enter the products as two 16-bit parts each (value and
+// remainder), as in decode: P's parts side by side in the 64 columns that a
+// thread's scores had, the query's remainders in slabs of their own. The result
+// is then as exact as its own rounding. With both rounded to the dtype its error
+// was twice that (bf16 3.4e-3 instead of 1.7e-3 relative), and either of the two
+// roundings alone still makes it one and a half times; without the second parts
+// 128 / 256 took 732 us instead of 1140, 64 / 128 586 instead of 765.
 //
-// P and the rotated query are rounded to the dtype for the products, as in
-// the other prefill kernels; two parts each (as decode takes) would double the
-// tensor time here.
+// Bound: per tile and map the MMAs take 2 * 128 * 128 * (hs + vhs) / 4096 cycles
+// (3100 at 128 / 256, 1536 at 64 / 128) with both parts, and the exponentials
+// 16384 / 32 = 512 beside 1000 for maxima, sums, parts and packing. Measured, 2 x
+// 4096 new tokens over 0 and 4096 cached ones, 16 heads over 4 kv heads, bf16:
+// 128 / 256 1140 us, 1.8 PFLOP/s of products (0.93 of a library product's rate,
+// 0.47 counting the formula's own): a tile takes 3150 cycles, a unit some 24000
+// outside its tiles (lookup and query, the exchange, the norm). 64 / 128 765 us,
+// 2240 cycles a tile, bound by the softmax warps' instructions; two groups of
+// them on alternate tiles took 731, but 36 instead of 34 us for short prompts (2 x
+// 250 tokens, 8 heads), which are a chain of latencies, and were not kept.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -71,7 +76,7 @@ constexpr size_t kSmemMax = 225 * 1024;
 
 struct PreBars {
   uint64_t k_full[kMaxK], k_empty[kMaxK], v_full[kMaxV], v_empty[kMaxV];
-  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t s_full[3], p_full[3], pv_done[2];
   uint64_t q_full, drain, x_full[4];  // (x_full: a quadrant of 32 rows each)
   uint64_t v_land[2][2];  // [half][tile parity] values whose unseen rows are zeroed before v_full
   uint64_t q_tma;  // (set up by the warp that uses it first)
@@ -101,6 +106,8 @@ struct PreArgs {
   Params P;           // what the shared helpers read
   Divisor by_kvh, by_tpc, by_grp;
   int hs;
+  int lo0, lo1;       // k steps of QK^T that the rotation reaches: those take q's remainder too
+  int bufs;           // buffers of S and P
   int nk, nv, v_bytes, v_rows;  // slots of the rings; bytes of a value slot, rows of its boxes
   bool k_whole, v_whole;        // widths that are multiples of 64: see cache_map
   const float* lambda_vectors;
@@ -153,9 +160,32 @@ __device__ __forceinline__ void st_peer(uint32_t raddr, float a) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(raddr), "f"(a) : "memory");
 }
 
+template <typename T>
+__device__ __forceinline__ void unpack_half2(uint32_t v, float* a, float* b) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    *a = __uint_as_float(v << 16);
+    *b = __uint_as_float(v & 0xffff0000u);
+  } else {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+    *a = f.x;
+    *b = f.y;
+  }
+}
+
+// Eight values as 16-bit parts: rounded, and the rounded remainder.
+template <typename T>
+__device__ __forceinline__ void split8(const float (&x)[8], uint4* hi, uint4* lo) {
+  float h[8], d[8];
+  *hi = pack8<T>(x);
+  unpack8<T>(*hi, h);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) d[e] = x[e] - h[e];
+  *lo = pack8<T>(d);
+}
+
 // The rotation of one query row in place in its swizzled slabs (16-byte chunk
-// c of row r at c ^ (r & 7)), by two threads (`part` 0 and 1), in f32, rounded
-// once. The table entries of a half-split row are loaded (`load`) before the
+// c of row r at c ^ (r & 7)), by two threads (`part` 0 and 1), in f32; what
+// rounding takes away goes to the same place of the slabs `q_lo`. The table entries of a half-split row are loaded (`load`) before the
 // query has landed; 8-channel groups g = part, part + 2, .. of the first half.
 template <typename T>
 struct RowAngles {
@@ -179,9 +209,14 @@ __device__ __forceinline__ uint4* q_chunk(uint8_t* q_s, int row, int d0) {
                                   ((((d0 >> 3) & 7) ^ (row & 7)) << 4));
 }
 template <typename T>
-__device__ __forceinline__ void rotate_row(uint8_t* q_s, int row, int part, const Params& P,
+__device__ __forceinline__ void rotate_row(uint8_t* q_s, uint8_t* q_lo, int row, int part,
+                                           const Params& P,
                                            int64_t pos, RowAngles<T>& A) {
   const int half = P.rd >> 1;
+  if (part == 0) {  // the other half of a k step that the rotation ends in
+    if (P.ro & 8) *q_chunk(q_lo, row, P.ro - 8) = make_uint4(0, 0, 0, 0);
+    if ((P.ro + P.rd) & 8) *q_chunk(q_lo, row, P.ro + P.rd) = make_uint4(0, 0, 0, 0);
+  }
   if (P.interleaved) {
     const T* crow = reinterpret_cast<const T*>(P.cos_cache) + pos * half;
     const T* srow = reinterpret_cast<const T*>(P.sin_cache) + pos * half;
@@ -190,7 +225,7 @@ __device__ __forceinline__ void rotate_row(uint8_t* q_s, int row, int part, cons
       float a[8], none[8];
       unpack8<T>(*q_chunk(q_s, row, d0), a);
       rope8<T>(a, none, d0, P.ro, P.rd, 1, crow, srow);
-      *q_chunk(q_s, row, d0) = pack8<T>(a);
+      split8<T>(a, q_chunk(q_s, row, d0), q_chunk(q_lo, row, d0));
     }
     return;
   }
@@ -206,8 +241,8 @@ __device__ __forceinline__ void rotate_row(uint8_t* q_s, int row, int part, cons
       u[e] = fmaf(x[e], c[e], -y[e] * sn[e]);
       v[e] = fmaf(y[e], c[e], x[e] * sn[e]);
     }
-    *q_chunk(q_s, row, P.ro + d) = pack8<T>(u);
-    *q_chunk(q_s, row, P.ro + half + d) = pack8<T>(v);
+    split8<T>(u, q_chunk(q_s, row, P.ro + d), q_chunk(q_lo, row, P.ro + d));
+    split8<T>(v, q_chunk(q_s, row, P.ro + half + d), q_chunk(q_lo, row, P.ro + half + d));
 #pragma unroll
     for (int i = 0; i < 3; ++i) {  // (a loop, with the next entries in place)
       A.c[i] = A.c[i + 1];
@@ -227,28 +262,43 @@ __device__ __forceinline__ float max32(const uint32_t (&x)[32]) {
   return fmaxf(fmaxf(v[0], v[1]), fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31])));
 }
 
-// 2^(v sl + nm) of 32 raw scores of a row, packed to 16 bits; returns the sum
-// of the unrounded values. In three passes over the registers, so that the 32
-// exponentials issue back to back, the multiply-adds and sums on pairs.
-template <typename T>
-__device__ __forceinline__ float exp_row(uint32_t (&r)[32], uint32_t (&pk)[16], float sl, float nm) {
-  const uint64_t sl2 = pack_f32(sl, sl), nm2 = pack_f32(nm, nm);
+// 2^(v sl + nm) of 32 raw scores of a row (CAP: of their softcapped ones) as
+// 16-bit parts, rounded and remainder; returns the sum of the unrounded values.
+// In passes over the registers, so that the 32 exponentials issue back to back,
+// multiply-adds, sums and remainders on pairs.
+template <typename T, bool CAP>
+__device__ __forceinline__ float exp_row(const uint32_t (&r)[32], uint32_t (&hi)[16], uint32_t (&lo)[16],
+                                         const Params& P, float nm) {
+  auto score = [&](int e) {
+    const float v = __uint_as_float(r[e]);
+    return !CAP || v == -INFINITY ? v : P.cap_out * tanh_ex2(v * P.cap_in);
+  };
   uint64_t x[16];
+  const float sl = CAP ? 1.f : P.scale_log2;
+  const uint64_t sl2 = pack_f32(sl, sl), nm2 = pack_f32(nm, nm);
 #pragma unroll
   for (int e = 0; e < 16; ++e)
     asm("fma.rn.f32x2 %0, %1, %2, %3;"
         : "=l"(x[e])
-        : "l"(pack_f32(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]))), "l"(sl2), "l"(nm2));
+        : "l"(pack_f32(score(2 * e), score(2 * e + 1))), "l"(sl2), "l"(nm2));
   float p[32];
 #pragma unroll
   for (int e = 0; e < 16; ++e) unpack_f32(x[e], &p[2 * e], &p[2 * e + 1]);
 #pragma unroll
   for (int e = 0; e < 32; ++e) p[e] = ex2(p[e]);
+  const uint64_t minus = pack_f32(-1.f, -1.f);
   uint64_t sum[2] = {pack_f32(0.f, 0.f), pack_f32(0.f, 0.f)};
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
-    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[e & 1]) : "l"(pack_f32(p[2 * e], p[2 * e + 1])));
-    pk[e] = pack2<T>(p[2 * e], p[2 * e + 1]);
+    const uint64_t v = pack_f32(p[2 * e], p[2 * e + 1]);
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[e & 1]) : "l"(v));
+    hi[e] = pack2<T>(p[2 * e], p[2 * e + 1]);
+    float h0, h1, d0, d1;
+    unpack_half2<T>(hi[e], &h0, &h1);
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pack_f32(h0, h1)), "l"(minus), "l"(v));
+    unpack_f32(d, &d0, &d1);
+    lo[e] = pack2<T>(d0, d1);
   }
   float a, b, c, d;
   unpack_f32(sum[0], &a, &b);
@@ -352,8 +402,7 @@ __device__ __forceinline__ void zero_values(uint8_t* slot, PreBars* bars, int vs
   }
 }
 
-// TWO: vg <= 128, two groups of softmax warps on alternate tiles.
-template <typename T, bool CAP, bool TWO>
+template <typename T, bool CAP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPreThreads, 1)
 diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                     const __grid_constant__ CUtensorMap qmap, const __grid_constant__ PreArgs A) {
@@ -366,7 +415,8 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
   uint8_t* q_s = smem;
-  uint8_t* k_s = smem + P.q_bytes;         // key slots: slabs of kN rows
+  uint8_t* q_lo = smem + P.q_bytes;        // the query's remainders (with a rotation)
+  uint8_t* k_s = q_lo + (P.rd > 0 ? P.q_bytes : 0);  // key slots: slabs of kN rows
   uint8_t* v_s = k_s + A.nk * P.k_bytes;   // value slots: slabs of kVKeys rows
   // in the query's place, once the last QK^T is done: the halves' sums,
   // [CTA * 2 + half] sums of squares (the peer's too), and the norm's weights
@@ -422,10 +472,8 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     uint64_t* all = bars->k_full;
     for (int i = lane; i < kNumBars; i += 32) {
       uint32_t count = 1;
-      if (all + i == bars->s_free || all + i == bars->s_free + 1 || all + i == bars->p_full ||
-          all + i == bars->p_full + 1)
-        count = TWO ? 4 : kSoftWarps;
-      if (all + i == &bars->q_full) count = kSoftWarps;
+      if ((all + i >= bars->p_full && all + i < bars->p_full + 3) || all + i == &bars->q_full)
+        count = kSoftWarps;
       mbar_init(smem_u32(all + i), count);
     }
     if (lane == 0) {
@@ -448,7 +496,8 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  const uint32_t col_s = vg, col_p = vg + (TWO ? 2 : 1) * kN;  // P: two buffers of 64
+  const uint32_t col_s = vg;  // buffers of kN columns: S, then P in its place
+  const int bufs = A.bufs;
   volatile int* abort = &bars->abort;
   const Work W = work;
   const bool run = W.status == 0;
@@ -490,7 +539,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         lam = expf(d0) - expf(d1) + A.lambda_init;
       }
       ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->q_tma), 0, abort, P.err_flags));
-      if (ok && row < rows && P.rd > 0) rotate_row<T>(q_s, row, half, P, pos_r, ang);
+      if (ok && row < rows && P.rd > 0) rotate_row<T>(q_s, q_lo, row, half, P, pos_r, ang);
       fence_proxy_async();
       arrive_warp(&bars->q_full, lane);
 
@@ -517,141 +566,50 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         }
         return w;
       };
-      if constexpr (TWO) {
-        // Group `half` takes tiles half, half + 2, ..., one thread per row, so that
-        // one group's loads, maxima and waits run under the other's exponentials
-        // (64 / 128: 677 us with all warps on one tile, 617 so). The groups
-        // share the rows' running maxima: s_max[0][row] is handed from tile to
-        // tile, by the barriers 1 + q (group 0 to 1) and 5 + q (back) of
-        // quadrant q, on which one warp arrives and the other waits. Every warp
-        // goes through all of its tiles and hand-overs; after a wait that gave
-        // up (ok false) it does nothing else. Here m_used is what l refers to.
-#pragma unroll 1
-        for (int k = half; k < n; k += 2) {
-          const int64_t j0 = (t_begin + k) * kN;
-          const bool edge = j0 < lo_hi || j0 + kN - 1 > pos;
-          const uint32_t par = (uint32_t)(k >> 1) & 1u;
-          if (ok)
-            ok = __all_sync(0xffffffffu,
-                            wait_bar(smem_u32(&bars->s_full[half]), par, abort, P.err_flags));
-          uint32_t s[4][32];
-          if (live && ok) {
-            tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              tmem_ld32_nowait(lane_addr + col_s + half * kN + c * 32, s[c]);
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 4; ++c) reg_fence(s[c]);
-            tc_fence_before();
-          }
-          if (ok) arrive_warp(&bars->s_free[half], lane);  // a later QK^T may overwrite S
-          float mt = -INFINITY;
-          if (live && ok) {
-            if (edge) {
-              const int c0 = (int)min((int64_t)kN, max((int64_t)0, lo_r - j0));
-              const int c1 = (int)max((int64_t)-1, min((int64_t)(kN - 1), pos_r - j0));
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (c * 32 + e < c0 || c * 32 + e > c1) s[c][e] = __float_as_uint(-INFINITY);
-            }
-            float v[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) v[c] = max32(s[c]);
-            mt = score(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
-          }
-          float factor = 1.f;
-          bool rescale = false;
-          if (live) {
-            if (k > 0) named_sync(half ? 1 + (warp & 3) : 5 + (warp & 3), 64);
-            if (ok) {
-              float m = k > 0 ? s_max[0][row] : -INFINITY;
-              if (m == -INFINITY) {
-                m = mt;  // (nothing but zeros was added before a first visible key)
-              } else if (mt > m + kRescaleLog2) {
-                factor = ex2(m - mt);
-                m = mt;
-                rescale = true;
-              }
-              s_max[0][row] = m;
-              if (m_used != m) {
-                l = m_used == -INFINITY ? 0.f : l * ex2(m_used - m);
-                m_used = m;
-              }
-            }
-            if (k + 1 < n) named_arrive(half ? 5 + (warp & 3) : 1 + (warp & 3), 64);
-          }
-          if (k >= 2 && ok)  // P's buffer: PV of tile k - 2 has read it
-            ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->pv_done[half]), par ^ 1u, abort,
-                                                  P.err_flags));
-          if (live && ok) {
-            const float mu = m_used == -INFINITY ? 0.f : m_used;
-            const uint32_t dst = lane_addr + col_p + half * 64;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t pk[16];
-              if (CAP) {
-                const ExpArgs E{sl, mu, P.cap_in, P.cap_out, 0.f, 0.f, 0.f, 0.f, 0.f};
-                l += exp_chunk<T, 2>(s[c], pk, E);
-              } else {
-                l += exp_row<T>(s[c], pk, sl, -mu);
-              }
-              tmem_st16(dst + c * 16, pk);
-            }
-            if (__any_sync(0xffffffffu, rescale)) ok = rescale_o(k, factor, 0, vg);
-            tmem_wait_st();
-            tc_fence_before();
-          }
-          if (ok) arrive_warp(&bars->p_full[half], lane);
-        }
-      } else {
       // Every warp goes through all n tiles and meets its partner of the
       // quadrant in each; after a wait that gave up (ok false) it does nothing
       // else.
+      int buf = 0;
+      uint32_t spar = 0;
 #pragma unroll 1
       for (int k = 0; k < n; ++k) {
         const int pb = k & 1;
+        const uint32_t cols = lane_addr + col_s + buf * kN + half * 64;  // this thread's
         const int64_t j0 = (t_begin + k) * kN;
         const bool edge = j0 < lo_hi || j0 + kN - 1 > pos;
-        // (S of tile k is committed behind PV of tile k - 2, so this also
-        // says that P's buffer may be written again)
         if (ok)
           ok = __all_sync(0xffffffffu,
-                          wait_bar(smem_u32(&bars->s_full[0]), k & 1, abort, P.err_flags));
+                          wait_bar(smem_u32(&bars->s_full[buf]), spar, abort, P.err_flags));
+        uint64_t* p_full = &bars->p_full[buf];
+        if (++buf == bufs) {
+          buf = 0;
+          spar ^= 1;
+        }
         uint32_t s[2][32];
         if (live && ok) {
           tc_fence_after();
-          tmem_ld32_nowait(lane_addr + col_s + half * 64, s[0]);
-          tmem_ld32_nowait(lane_addr + col_s + half * 64 + 32, s[1]);
+          tmem_ld32_nowait(cols, s[0]);
+          tmem_ld32_nowait(cols + 32, s[1]);
           tmem_wait_ld();
           reg_fence(s[0]);
           reg_fence(s[1]);
           tc_fence_before();
         }
-        if (ok) arrive_warp(&bars->s_free[0], lane);  // the next QK^T may overwrite S
         // The exponentials use the running maximum as it stands; the tile's own
         // maximum is taken beside them, and only if it passes the running one by
         // more than 2^8 (or there is none yet) do the two warps of the quadrant
         // exchange maxima and compute the tile again (waiting for the exchange
-        // first: 806 us instead of 796).
-        const uint32_t dst = lane_addr + col_p + pb * 64 + half * 32;
+        // first was 1 % slower).
         float vmax = -INFINITY, lsum = 0.f;
         auto exps = [&]() {
           const float mu = m_used == -INFINITY ? 0.f : m_used;
-          uint32_t pk[16];
-          if (CAP) {
-            const ExpArgs E{sl, mu, P.cap_in, P.cap_out, 0.f, 0.f, 0.f, 0.f, 0.f};
-            lsum = exp_chunk<T, 2>(s[0], pk, E);
-            tmem_st16(dst, pk);
-            lsum += exp_chunk<T, 2>(s[1], pk, E);
-          } else {
-            lsum = exp_row<T>(s[0], pk, sl, -mu);
-            tmem_st16(dst, pk);
-            lsum += exp_row<T>(s[1], pk, sl, -mu);
-          }
-          tmem_st16(dst + 16, pk);
+          uint32_t hi[16], lo[16];
+          lsum = exp_row<T, CAP>(s[0], hi, lo, P, -mu);
+          tmem_st16(cols, hi);
+          tmem_st16(cols + 32, lo);
+          lsum += exp_row<T, CAP>(s[1], hi, lo, P, -mu);
+          tmem_st16(cols + 16, hi);
+          tmem_st16(cols + 48, lo);
         };
         bool again = false;
         if (live && ok) {
@@ -698,8 +656,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           tmem_wait_st();
           tc_fence_before();
         }
-        if (ok) arrive_warp(&bars->p_full[pb], lane);
-      }
+        if (ok) arrive_warp(p_full, lane);
       }
       grid_dep_launch();
       uint4 nw = make_uint4(0, 0, 0, 0);
@@ -711,7 +668,6 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                                               ((n - 1) >> 1) & 1, abort, P.err_flags));
       tc_fence_after();
       if (live) {
-        if (TWO) l = m_used == -INFINITY ? 0.f : l * ex2(m_used - s_max[0][row]);
         s_sum[half][row] = l;
       }
       if (tid * 8 < vhs) s_norm[tid] = nw;
@@ -737,7 +693,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       bool waited = !P.early;
       const int32_t* bt = P.block_table + (int64_t)W.b * P.max_blocks;
       const int sh = __ffs(P.bs) - 1;
-      // keys: a tile per slot; values: this warp's half tile, every second slot
+      // keys: a tile per slot; values: this warp's half tile, every second of the line
       const int slots = keys ? A.nk : A.nv, step = keys ? 1 : 2, h = keys ? 0 : warp - kProdWarp - 1;
       uint64_t* full = keys ? bars->k_full : bars->v_full;
       uint64_t* empty = keys ? bars->k_empty : bars->v_empty;
@@ -832,8 +788,8 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       if (!waited) grid_dep_wait();
       if (*abort && lane == 0) {  // copies may be in flight: wait for each slot's last
         if (keys) drain_wait(smem_u32(&bars->q_tma), 0, P.err_flags);
-        for (int i = 0; i < issued && i < slots / step; ++i)
-          drain_wait(smem_u32(&full[i * step + h]), ((issued - 1 - i) / (slots / step)) & 1,
+        for (int i = max(0, issued - (slots + step - 1) / step); i < issued; ++i)
+          drain_wait(smem_u32(&full[(i * step + h) % slots]), ((i * step + h) / slots) & 1,
                      P.err_flags);
       }
       __syncwarp();
@@ -851,7 +807,9 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         auto wait = [&](uint64_t* bar, uint32_t par) {
           return wait_bar(smem_u32(bar), par, abort, P.err_flags);
         };
-        auto qk = [&](int sb) {
+        const uint64_t lo_desc = sdesc(smem_u32(q_lo), 16, 1024);
+        int sb = 0;  // the next buffer of S
+        auto qk = [&]() {
           if (!wait(&bars->k_full[sk], kpar)) return false;
           tc_fence_after();
           const uint64_t kd = sdesc(k_base + sk * P.k_bytes, 16, 1024);
@@ -862,7 +820,15 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
               mma_ss(tmem + col_s + sb * kN, q_desc + o, kd + o, id_qk, kk > 0 ? 1u : 0u);
             }
           }
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            if (kk >= A.lo0 && kk < A.lo1) {
+              const uint32_t o = (uint32_t)(kk >> 2) * (kBox >> 4) + (uint32_t)(kk & 3) * 2;
+              mma_ss(tmem + col_s + sb * kN, lo_desc + o, kd + o, id_qk, 1u);
+            }
+          }
           tc_commit(smem_u32(&bars->s_full[sb]));
+          if (++sb == bufs) sb = 0;
           tc_commit(smem_u32(&bars->k_empty[sk]));
           if (++sk == A.nk) {
             sk = 0;
@@ -870,15 +836,18 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           }
           return true;
         };
-        auto pv = [&](int k, int hp) {
+        auto pv = [&](int k, int pbuf, int hp) {
           if (!wait(&bars->v_full[sv], vpar)) return false;
           tc_fence_after();
           const uint64_t vd = sdesc(v_base + sv * A.v_bytes, kVBox, 1024);
-          const uint32_t pa = tmem + col_p + (k & 1) * 64 + hp * 32;
+          const uint32_t pa = tmem + col_s + pbuf * kN + hp * 64;
 #pragma unroll
           for (int kk = 0; kk < kVKeys / 16; ++kk)
             mma_ts(tmem, pa + kk * 8, vd + (uint64_t)(kk * 128), id_pv,
                    (k > 0 || hp || kk > 0) ? 1u : 0u);
+#pragma unroll
+          for (int kk = 0; kk < kVKeys / 16; ++kk)  // the remainders
+            mma_ts(tmem, pa + 32 + kk * 8, vd + (uint64_t)(kk * 128), id_pv, 1u);
           tc_commit(smem_u32(&bars->v_empty[sv]));
           if (++sv == A.nv) {
             sv = 0;
@@ -886,18 +855,20 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           }
           return true;
         };
-        // QK^T of the next tile (TWO: the one after) before PV of this one: its S
-        // is free as soon as the softmax warps have read it, and it runs while
-        // they work. With one S, the commit of S(k + 1) stands behind PV(k - 1)
-        // (see the softmax's use).
-        constexpr int kAhead = TWO ? 2 : 1;
-        bool go = wait(&bars->q_full, 0) && qk(0);
-        if (TWO && n > 1) go = go && qk(1);
+        // QK^T runs `bufs` - 1 tiles ahead of PV. Its buffer held P of the tile whose
+        // PV was issued last, and products run in the order of their issue.
+        int pbuf = 0;
+        uint32_t ppar = 0;
+        bool go = wait(&bars->q_full, 0) && qk();
+        if (bufs == 3 && n > 1) go = go && qk();
         for (int k = 0; k < n && go; ++k) {
-          const int b = TWO ? k & 1 : 0;
-          if (k + kAhead < n) go = wait(&bars->s_free[b], TWO ? (k >> 1) & 1 : k & 1) && qk(b);
-          go = go && wait(&bars->p_full[k & 1], (k >> 1) & 1) && pv(k, 0) && pv(k, 1);
+          if (k + bufs - 1 < n) go = qk();
+          go = go && wait(&bars->p_full[pbuf], ppar) && pv(k, pbuf, 0) && pv(k, pbuf, 1);
           if (go) tc_commit(smem_u32(&bars->pv_done[k & 1]));
+          if (++pbuf == bufs) {
+            pbuf = 0;
+            ppar ^= 1;
+          }
         }
         tc_commit(smem_u32(&bars->drain));
         drain_wait(smem_u32(&bars->drain), 0, P.err_flags);
@@ -1058,10 +1029,10 @@ cudaError_t cache_map(CUtensorMap* map, bool bf16, const void* base, int width, 
   return encode(map, bf16, base, 4, dims, str, box);
 }
 
-template <typename T, bool CAP, bool TWO>
+template <typename T, bool CAP>
 cudaError_t launch(const Geometry& g, const DiffArgs& a, const PreArgs& A, int64_t units) {
   static std::atomic<bool> configured[64];
-  auto kern = diff_prefill_kernel<T, CAP, TWO>;
+  auto kern = diff_prefill_kernel<T, CAP>;
   cudaError_t e = once_per_device(configured, g.device, [&] {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
   });
@@ -1081,7 +1052,8 @@ cudaError_t launch(const Geometry& g, const DiffArgs& a, const PreArgs& A, int64
     if ((e = encode(&qmap, bf16, a.query, 4, dims, str, box)) != cudaSuccess) return e;
   }
   const size_t smem =
-      1024 + (size_t)P.q_bytes + (size_t)A.nk * P.k_bytes + (size_t)A.nv * A.v_bytes;
+      1024 + (size_t)P.q_bytes * (P.rd > 0 ? 2 : 1) + (size_t)A.nk * P.k_bytes +
+      (size_t)A.nv * A.v_bytes;
   return launch_pdl(kern, dim3((unsigned)(units * g.kvh * 2)), dim3(kPreThreads), smem, a.stream,
                     kmap, vmap, qmap, A);
 }
@@ -1140,11 +1112,13 @@ cudaError_t launch_prefill(const Geometry& g, const DiffArgs& a) {
   P.k_bytes = P.slabs * kBox;
   A.v_rows = g.bs < kVKeys ? g.bs : kVKeys;
   A.v_bytes = P.vslabs * kVBox;
-  // four key tiles (two of 32 KB), the rest for values: at least four halves
+  // four key tiles (two of 32 KB), the rest for values: at least three halves
   A.nk = P.slabs == 1 ? 4 : 2;
-  A.nv = (int)((kSmemMax - 1024 - P.q_bytes - (size_t)A.nk * P.k_bytes) / A.v_bytes);
+  A.nv = (int)((kSmemMax - 1024 - 2 * P.q_bytes - (size_t)A.nk * P.k_bytes) / A.v_bytes);
   if (A.nv > kMaxV) A.nv = kMaxV;
-  A.nv &= ~1;  // (the two value warps have slots of their own)
+  A.lo0 = g.rd > 0 ? g.ro / 16 : 0;
+  A.lo1 = g.rd > 0 ? (g.ro + g.rd + 15) / 16 : 0;
+  A.bufs = P.vg <= 128 ? 3 : 2;
   A.k_whole = g.hs % 64 == 0;
   A.v_whole = g.vhs % 64 == 0;
   A.hs = g.hs;
@@ -1156,11 +1130,10 @@ cudaError_t launch_prefill(const Geometry& g, const DiffArgs& a) {
   const int64_t units =
       a.num_tokens / P.tpc + std::min((int64_t)(a.seq_end - a.seq_begin), a.num_tokens);
   if (units * g.kvh * 2 > INT32_MAX) return cudaErrorInvalidConfiguration;
-  const bool cap = g.softcap > 0.f, two = P.vg <= 128;
+  const bool cap = g.softcap > 0.f;
   auto go = [&](auto* typed) {
     using T = std::remove_pointer_t<decltype(typed)>;
-    if (cap) return two ? launch<T, true, true>(g, a, A, units) : launch<T, true, false>(g, a, A, units);
-    return two ? launch<T, false, true>(g, a, A, units) : launch<T, false, false>(g, a, A, units);
+    return cap ? launch<T, true>(g, a, A, units) : launch<T, false>(g, a, A, units);
   };
   return g.dtype == PA_DTYPE_BF16 ? go((__nv_bfloat16*)nullptr) : go((__half*)nullptr);
 }

@@ -514,3 +514,23 @@ def test_prefill_windows(name, window):
     its values come in, or leave such a half to nobody."""
     check(workload(name, q_lens=[70, 150], past_lens=[301, 77], local_window_size=window, num_heads=4,
                    block_size=16, drop_slots=0))
+
+
+@pytest.mark.parametrize("decodes", [0, None])
+@pytest.mark.parametrize("name", ["64_128", "128_256", "fp16", "fp16_128_256", "hs_48_vhs_80", "grp_12", "window_100",
+                                  "interleaved", "partial_rope", "no_rope", "lambda_0.8", "peaked"])
+def test_as_exact_as_its_rounding(name, decodes):
+    """The query and the probabilities enter the products as two parts, so they
+    are off by u^2 at most (the remainder's rounding), and every output by its own
+    rounding, u |x|, plus c noise: c = 6 u^2 for the parts (as 6 u above), and
+    2^-15 for the f32 arithmetic: 6 deviations of sums of up to 1200 terms, 6 *
+    sqrt(1200) * 2^-24 < 2^-16, and as much again for scores and exponentials."""
+    w = workload(name)
+    d, out, op = run_gpu(w, decodes)
+    ref = D.run_bits(_numpy(w), w.params, W.dtype_tag(w.dtype))
+    got = out.double().cpu().numpy().reshape(ref["out"].shape)
+    u = UNIT_ROUNDOFF[w.dtype]
+    bound = u * np.abs(ref["out"]) + (6 * u * u + 2.0 ** -15) * ref["noise"]
+    worst = (np.abs(got - ref["out"]) / bound).max()
+    print(f"RATIO {name}: {worst:.3f}")
+    assert worst <= 1, worst
