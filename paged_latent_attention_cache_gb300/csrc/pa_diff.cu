@@ -33,7 +33,7 @@ diff_write_kernel(const T* __restrict__ key, const T* __restrict__ value,
                   const int32_t* __restrict__ past, int32_t num_seqs, T* __restrict__ key_cache,
                   T* __restrict__ value_cache, int64_t num_tokens, int kvh, int hs, int vhs,
                   int ro, int rd, int interleaved, int cos_rows, int64_t num_slots,
-                  int32_t* err_flags) {
+                  int32_t* err_flags, int step_t, int step_c) {
   // This kernel takes its place while the one before it ends; once that is
   // complete, a read kernel behind this one may start its prologue (it waits for
   // this grid before it reads the cache).
@@ -46,11 +46,16 @@ diff_write_kernel(const T* __restrict__ key, const T* __restrict__ value,
     cum = s_cum;
   }
   const int kg = kvh * 2 * (hs >> 3), vg = kvh * (vhs >> 3), groups = kg + vg;
-  const int64_t total = num_tokens * groups;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t t = i / groups;
-    const int c = (int)(i - t * groups);
+  // (t, c) is one division away from the thread's number (below 2^31); a step is
+  // the grid's threads, step_t tokens and step_c groups
+  const int first_item = (int)(blockIdx.x * blockDim.x + threadIdx.x);
+  int64_t t = first_item / groups;
+  int c = first_item - (int)t * groups;
+  for (; t < num_tokens; t += step_t, c += step_c) {
+    if (c >= groups) {
+      c -= groups;
+      if (++t >= num_tokens) break;
+    }
     const bool is_key = c < kg;
     const bool first = c == 0;  // one thread per token reports its errors
     const int32_t slot = slot_mapping[t];
@@ -230,10 +235,11 @@ pa_status pa_diff_write(const pa_diff_params* p, const void* key, const void* va
   if (!aligned(slot_mapping, 4) || !aligned(cumseq, 4) || !aligned(past, 4) ||
       !aligned(err_flags, 4))
     return fail(PA_ERR_INVALID_ARGUMENT, "int32 tensors must be 4-byte aligned");
-  const int64_t total = num_tokens * g.kvh * ((2 * g.hs + g.vhs) >> 3);
-  int64_t blocks = (total + 255) / 256;
+  const int64_t groups = (int64_t)g.kvh * ((2 * g.hs + g.vhs) >> 3);
+  int64_t blocks = (num_tokens * groups + 255) / 256;
   const int64_t cap = (int64_t)g.num_sms * 16;
   if (blocks > cap) blocks = cap;
+  const int step_t = (int)(blocks * 256 / groups), step_c = (int)(blocks * 256 % groups);
   const size_t smem =
       num_seqs <= diff::kStagedSeqs ? (size_t)(num_seqs + 1) * sizeof(int32_t) : 0;
   auto go = [&](auto* typed) {
@@ -252,7 +258,7 @@ pa_status pa_diff_write(const pa_diff_params* p, const void* key, const void* va
         &cfg, diff::diff_write_kernel<T>, (const T*)key, (const T*)value, (const T*)cos_cache,
         (const T*)sin_cache, slot_mapping, cumseq, past, num_seqs, (T*)key_cache,
         (T*)value_cache, num_tokens, g.kvh, g.hs, g.vhs, g.ro, g.rd, g.interleaved, g.cos_rows,
-        (int64_t)g.num_blocks * g.bs, err_flags);
+        (int64_t)g.num_blocks * g.bs, err_flags, step_t, step_c);
   };
   const cudaError_t e =
       g.dtype == PA_DTYPE_BF16 ? go((__nv_bfloat16*)nullptr) : go((__half*)nullptr);
