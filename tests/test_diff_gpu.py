@@ -534,3 +534,14 @@ def test_as_exact_as_its_rounding(name, decodes):
     worst = (np.abs(got - ref["out"]) / bound).max()
     print(f"RATIO {name}: {worst:.3f}")
     assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("name,offset,dim", [("64_128", 8, 32), ("64_128", 8, 16), ("64_128", 40, 16), ("128_256", 24, 80),
+                                             ("128_256", 8, 112), ("128_256", 0, 0), ("hs_48_vhs_80", 8, 32),
+                                             ("hs_16", 0, 16), ("fp16_128_256", 56, 64)])
+@pytest.mark.parametrize("interleaved", [0, 1])
+def test_rotations_that_end_in_a_k_step(name, offset, dim, interleaved):
+    """Rotary ranges that start or end inside the 16 channels of a product."""
+    check(workload(name, rotary_offset=offset, rotary_dim=dim, rotary_interleaved=interleaved))
+    check(workload(name, rotary_offset=offset, rotary_dim=dim, rotary_interleaved=interleaved, q_lens=[1, 1, 30],
+                   past_lens=[90, 3, 200]), decodes=0)
