@@ -129,6 +129,17 @@ __device__ __forceinline__ void share(int n, int warp, int* lo, int* hi) {
   *hi = min(n, *lo + per);
 }
 
+// A CTA of the cluster may be stored into only once it has started. A kernel
+// says so at its very start and waits for the others in front of its first such
+// store, behind loads that take longer; it has to do so, or pass another barrier
+// of the cluster, before its first warp_prefix.
+__device__ __forceinline__ void cluster_start() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_started() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // Exclusive prefix over the cluster's warps of K counts (the same value in
 // every lane of a warp) and their totals. `buf` is a shared-memory array of
 // its own for each use in a kernel.
@@ -450,6 +461,7 @@ reserve_kernel(State st, Scratch ws, const int32_t* __restrict__ cumseq, int64_t
                int32_t* __restrict__ slot_mapping, bool slots_here) {
   __shared__ int buf[2][kPlanWarps];
   __shared__ int32_t s_cum[kStagedSeqs + 1];  // cumseq for the searches, where it fits
+  cluster_start();
   cg::cluster_group cl = cg::this_cluster();
   const Plan id = plan_ids();
   const int nb = st.num_blocks, ns = st.num_seqs, mb = st.max_blocks;
@@ -507,6 +519,7 @@ reserve_kernel(State st, Scratch ws, const int32_t* __restrict__ cumseq, int64_t
   }
   v[0] = count_pages(st.ref, plo, phi, false, id.lane);
   int base[2], total[2];
+  cluster_started();
   warp_prefix<2>(id, v, base, total, buf);
   list_pages(st.ref, plo, phi, false, id.lane, base[0], min(total[0], total[1]),
              [&](int rank, int page) { ws.list[rank] = page; });
@@ -579,12 +592,14 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kPlanThre
 compact_plan_kernel(State st, Scratch ws, int32_t* live_out) {
   __shared__ int buf1[1][kPlanWarps];
   __shared__ int buf2[2][kPlanWarps];
+  cluster_start();
   cg::cluster_group cl = cg::this_cluster();
   const Plan id = plan_ids();
   chain();
   int lo, hi;
   share(st.num_blocks, id.warp, &lo, &hi);
   int live[1] = {count_pages(st.ref, lo, hi, true, id.lane)}, before[1], all[1];
+  cluster_started();
   warp_prefix<1>(id, live, before, all, buf1);
   const int L = all[0];
   // free pages below L and held pages from L on

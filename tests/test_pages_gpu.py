@@ -409,3 +409,30 @@ def test_one_page_in_many_caches():
     pool.free(i32(0, 1))
     assert pool.compact().tolist() == [0] and pool.refcount.tolist() == [0]
     assert all(torch.equal(c, caches[0]) for c in caches)
+
+
+def test_tiny_calls_in_a_row():
+    """Pools so small that nearly every warp of the bookkeeping has nothing to
+    look at: a long run of reserve, compact and free calls, none of which the
+    host waits for."""
+    s = Pair(11, nb=3, ns=2, mb=2, widths=(16,), fill=0.0, share=False)
+    cum = np.array([0, 17, 20])
+    seqs = s.ints([0])
+    slots = [torch.full((21,), 12345, dtype=torch.int32, device="cuda") for _ in range(60)]
+    cum_d, wants, lives = s.ints(cum), [], []
+    for t in slots:
+        s.pool.reserve(cum_d, t)
+        s.pool.free(seqs)
+        lives.append(s.pool.compact().clone())
+        s.pool.reserve(cum_d, t)
+    err = 0
+    for _ in slots:
+        err |= O.reserve(s.table, s.past, s.ref, cum, 21, s.bs)[0]
+        err |= O.free(s.table, s.past, s.ref, [0])
+        e, live = O.compact(s.caches, s.table, s.ref)
+        e2, want = O.reserve(s.table, s.past, s.ref, cum, 21, s.bs)
+        err |= e | e2
+        wants.append((live, want))
+    s.check(err)
+    for t, n, (live, want) in zip(slots, lives, wants):
+        assert np.array_equal(t.cpu().numpy(), want) and int(n.item()) == live
