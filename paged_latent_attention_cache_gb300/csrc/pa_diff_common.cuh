@@ -6,6 +6,23 @@
 namespace pa {
 namespace diff {
 
+// Probabilities enter the products as two T parts (value and remainder) of
+// 2^(s - m + shift), m the row's running maximum, which may lag behind by `lazy`;
+// their sum carries the same factor, so it cancels. bf16 has f32's exponents.
+// fp16 ends below 2^16 and its least step is 2^-24, which no remainder passes:
+// with shift + lazy = 15 a probability is off by 2^-25 / 2^shift = 2^-36 of the
+// row's largest at most. (With shift 0 and 2^-25, a key that takes nearly all of the
+// weight at a value near zero left relative errors of up to 4e-2, as the norm
+// scales up the small rest. Lazy 4 and not less: scores of spread 1 pass a
+// tile's maximum by 2^4 hardly ever, by 2^2 in every fifth tile of 128.)
+template <typename T> struct Prob;
+template <> struct Prob<__nv_bfloat16> {
+  static constexpr float lazy = 8.f, shift = 0.f;
+};
+template <> struct Prob<__half> {
+  static constexpr float lazy = 4.f, shift = 11.f;
+};
+
 // True in one lane of the warp (converged). Code behind `if (elect_one())` is
 // known to run in a single lane, so its TMA and MMA operands stay in uniform
 // registers; behind `if (lane == 0)` every such instruction moved them there

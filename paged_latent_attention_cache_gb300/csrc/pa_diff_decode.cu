@@ -37,7 +37,7 @@
 // Precision: out = softmax_0 V - lambda softmax_1 V cancels, so errors of the
 // two maps weigh more than in a plain softmax. The rotated query and the
 // probabilities enter the products as two 16-bit parts each (value and
-// remainder, 2^-16 relative in bf16). For the scores that is free: a product
+// remainder, 2^-16 relative in bf16; see Prob). For the scores that is free: a product
 // of one map has 8 rows for the heads' values and 8 for their remainders, and
 // both sums of a score end up in one lane. For the values it doubles the
 // products.
@@ -67,7 +67,6 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kJoin = 64;        // channels joined at a time at the end of a segment
 constexpr int kJoinPitch = 72;   // floats of a row there (8 rows x 8 bytes x 4 lanes: no bank twice)
 constexpr int kMinTiles = kWarps;  // least part of a CTA
-constexpr float kLazy = 8.f;     // a running maximum may lag by 2^8
 
 struct Args {
   Geometry g;
@@ -534,7 +533,7 @@ diff_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         float t = fmaxf(fmaxf(v[i][0][0], v[i][0][1]), fmaxf(v[i][1][0], v[i][1][1]));
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-        if (t > mx[i] + kLazy || mx[i] == -INFINITY) {
+        if (t > mx[i] + Prob<T>::lazy || mx[i] == -INFINITY) {
           f[i] = mx[i] == -INFINITY ? 0.f : ex2(mx[i] - t);
           mx[i] = t;
           l[i] *= f[i];
@@ -553,7 +552,7 @@ diff_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       uint32_t ph[4], pl[4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float mu = mx[i] == -INFINITY ? 0.f : mx[i];
+        const float mu = (mx[i] == -INFINITY ? 0.f : mx[i]) - Prob<T>::shift;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float p0 = ex2(v[i][j][0] - mu), p1 = ex2(v[i][j][1] - mu);

@@ -29,7 +29,7 @@
 // Precision: out = softmax_0 V - lambda softmax_1 V cancels, so errors of the
 // two maps weigh more than in a plain softmax. The rotated query and the
 // probabilities enter the products as two 16-bit parts each (value and
-// remainder), as in decode: P's parts side by side in the 64 columns that a
+// remainder), as in decode (see Prob): P's parts side by side in the 64 columns that a
 // thread's scores had, the query's remainders in slabs of their own. The result
 // is then as exact as its own rounding. With both rounded to the dtype its error
 // was twice that (bf16 3.4e-3 instead of 1.7e-3 relative), and either of the two
@@ -595,17 +595,17 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         }
         // The exponentials use the running maximum as it stands; the tile's own
         // maximum is taken beside them, and only if it passes the running one by
-        // more than 2^8 (or there is none yet) do the two warps of the quadrant
+        // more than 2^lazy (or there is none yet) do the two warps of the quadrant
         // exchange maxima and compute the tile again (waiting for the exchange
         // first was 1 % slower).
         float vmax = -INFINITY, lsum = 0.f;
         auto exps = [&]() {
-          const float mu = m_used == -INFINITY ? 0.f : m_used;
+          const float nm = Prob<T>::shift - (m_used == -INFINITY ? 0.f : m_used);
           uint32_t hi[16], lo[16];
-          lsum = exp_row<T, CAP>(s[0], hi, lo, P, -mu);
+          lsum = exp_row<T, CAP>(s[0], hi, lo, P, nm);
           tmem_st16(cols, hi);
           tmem_st16(cols + 32, lo);
-          lsum += exp_row<T, CAP>(s[1], hi, lo, P, -mu);
+          lsum += exp_row<T, CAP>(s[1], hi, lo, P, nm);
           tmem_st16(cols + 16, hi);
           tmem_st16(cols + 48, lo);
         };
@@ -624,7 +624,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           vmax = fmaxf(max32(s[0]), max32(s[1]));
           again = __any_sync(0xffffffffu,
                              row < rows && (m_used == -INFINITY ||
-                                            score(vmax) > m_used + kRescaleLog2));
+                                            score(vmax) > m_used + Prob<T>::lazy));
         }
         if (live) {
           if (lane == 0) s_again[pb][half][warp & 3] = again ? 1 : 0;
@@ -638,7 +638,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
               bool rescale = false;
               if (m_used == -INFINITY) {
                 m_used = mt;  // (nothing but zeros was added before a first visible key)
-              } else if (mt > m_used + kRescaleLog2) {
+              } else if (mt > m_used + Prob<T>::lazy) {
                 factor = ex2(m_used - mt);
                 m_used = mt;
                 l *= factor;

@@ -545,3 +545,37 @@ def test_rotations_that_end_in_a_k_step(name, offset, dim, interleaved):
     check(workload(name, rotary_offset=offset, rotary_dim=dim, rotary_interleaved=interleaved))
     check(workload(name, rotary_offset=offset, rotary_dim=dim, rotary_interleaved=interleaved, q_lens=[1, 1, 30],
                    past_lens=[90, 3, 200]), decodes=0)
+
+
+@pytest.mark.parametrize("gap", [14, 18, 22])
+@pytest.mark.parametrize("name,q,past,at", [
+    ("fp16", [1, 1], [32000, 700], 0), ("fp16", [1, 1], [32000, 700], 20000), ("fp16_128_256", [1], [9000], 5),
+    ("fp16", [9, 3], [8000, 300], 0), ("fp16", [9], [8000], 6000), ("fp16_128_256", [40], [2000], 0),
+    ("64_128", [1, 20], [32000, 8000], 0)])
+def test_one_key_takes_nearly_all(name, q, past, at, gap):
+    """A key with nearly all of the weight and a value of zero: the norm scales
+    up what the others add, 2^-gap of it each. Bound as in
+    test_as_exact_as_its_rounding, and in fp16 6 * 2^(gap - 36) noise: a
+    probability is off by 2^-36 of the row's largest at most, which is 2^(gap -
+    36) of the others' mean (noise weighs each key's value by its own)."""
+    w = workload(name, q_lens=q, past_lens=past, rotary_dim=0, num_heads=2, drop_slots=0)
+    t, hs = w.tensors, w.head_size
+    a = 8.0
+    t["query"].view(-1, 2, 2, hs)[..., 0] = a
+    t["key"].view(-1, 2, 2, hs)[..., 0] = 0
+    t["key_cache"][..., 0] = 0
+    for b, p in enumerate(past):
+        r = _row(w, b, min(at, p - 1))
+        t["key_cache"].view(-1, 2, 2, hs)[r] = 0
+        t["key_cache"].view(-1, 2, 2, hs)[r, :, :, 0] = gap * np.log(2.0) * hs ** 0.5 / a
+        t["value_cache"].view(-1, 2, w.v_head_size)[r] = 0
+    d, out, op = run_gpu(w)
+    assert op.error_flags() == 0
+    ref = D.run_bits(_numpy(w), w.params, W.dtype_tag(w.dtype))
+    got = out.double().cpu().numpy().reshape(ref["out"].shape)
+    u = UNIT_ROUNDOFF[w.dtype]
+    c = 6 * u * u + 2.0 ** -15 + (6 * 2.0 ** (gap - 36) if w.dtype is torch.float16 else 0.0)
+    worst = (np.abs(got - ref["out"]) / (u * np.abs(ref["out"]) + c * ref["noise"])).max()
+    rel = np.linalg.norm(got - ref["out"]) / np.linalg.norm(ref["out"])
+    print(f"RATIO {name} gap {gap}: {worst:.3f}, relative error {rel:.2e}")
+    assert worst <= 1, worst
