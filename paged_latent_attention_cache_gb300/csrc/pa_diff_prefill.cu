@@ -660,10 +660,13 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       uint4 nw = make_uint4(0, 0, 0, 0);
       if (tid * 8 < vhs) nw = reinterpret_cast<const uint4*>(A.norm_weight)[tid];
       named_sync(9, kSoft);
-      ok = __all_sync(0xffffffffu, ok && !*abort);
+      // All products, by a barrier with one phase. (pv_done has a phase for every
+      // second tile: with three buffers the scores of the last tile may be there
+      // before PV of tile n - 3 is, and a wait for tile n - 1's phase would return
+      // at once, as one for the phase before it does.)
       if (ok && n > 0)
-        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->pv_done[(n - 1) & 1]),
-                                              ((n - 1) >> 1) & 1, abort, P.err_flags));
+        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&bars->drain), 0, abort, P.err_flags));
+      ok = __all_sync(0xffffffffu, ok && !*abort);  // (a role that gave up comes here too)
       tc_fence_after();
       if (live) {
         s_sum[half][row] = l;

@@ -579,3 +579,37 @@ def test_one_key_takes_nearly_all(name, q, past, at, gap):
     rel = np.linalg.norm(got - ref["out"]) / np.linalg.norm(ref["out"])
     print(f"RATIO {name} gap {gap}: {worst:.3f}, relative error {rel:.2e}")
     assert worst <= 1, worst
+
+
+def test_values_that_come_late():
+    """Prompts over contexts of three key tiles whose values arrive long after
+    their keys: pages spread over 8 GB a cache, the values' lines and address
+    translations out of every cache, the keys just read. The same bits as from
+    small caches that are at hand."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 36 GB of device memory")
+    n, q, NB = 60, 8, 1 << 18
+    w = workload("64_128", q_lens=[q] * n, past_lens=[362 - i % 50 for i in range(n)], num_heads=2, drop_slots=0)
+    t = {k: v.cuda() for k, v in w.tensors.items()}
+    small = {k: t[k].clone() for k in ("key_cache", "value_cache")}
+    op = _op(w)
+    for _ in range(5):
+        want = op.forward(*_args(t), 0)
+    big = {k: torch.zeros(NB, *small[k].shape[1:], dtype=w.dtype, device="cuda") for k in small}
+    far = DifferentialAttention(**{**w.params, "num_blocks": NB}, max_seqs=n, max_tokens=n * q, own_slots=True)
+    other = torch.zeros(16 << 30, dtype=torch.uint8, device="cuda")
+    g = torch.Generator().manual_seed(1)
+    outs = []
+    for r in range(15):
+        perm = torch.randperm(NB, generator=g)[:w.num_blocks].cuda()
+        for k in big:
+            big[k][perm] = small[k]
+        bt = torch.where(t["block_table"] >= 0, perm[t["block_table"].clamp(min=0).long()], -1).int()
+        s = t["slot_mapping"].long()
+        slots = (perm[s // 64] * 64 + s % 64).int()
+        other[r::1 << 19] += 1
+        other[:1 << 28] += 1
+        big["key_cache"][perm].sum()
+        outs.append(far.forward(*_args({**t, **big, "block_table": bt, "slot_mapping": slots}), 0))
+    assert op.error_flags() == 0 and far.error_flags() == 0
+    assert [torch.equal(o, want) for o in outs] == [True] * 15

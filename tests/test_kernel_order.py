@@ -43,3 +43,48 @@ def test_cluster_has_started_before_its_shared_memory_is_written():
         assert body.count("cluster_start()") == body.count("cluster_started()"), name
         if "cluster_start()" in body:
             assert body.index("cluster_start()") < body.index("chain()") < body.index("cluster_started()"), name
+
+
+def _first_wrong_wait(n, bufs, last_wait):
+    """The order of one CTA of diff_prefill_kernel, values as late as can be:
+    the scores of tile k are there once the products issued before them are,
+    and PV of tile j waits for its values. Returns the tile at which a wait of
+    the softmax for PV passes although that PV is not done, else None.
+    ``pv_done`` has two barriers; a wait for a phase's parity passes when the
+    phase in progress has the other one."""
+    done = -1  # the last PV done
+    phases = [0, 0]
+
+    def finish(upto):
+        nonlocal done
+        while done < upto:
+            done += 1
+            phases[done & 1] += 1
+
+    def passes(k):  # a wait for PV of tile k
+        return phases[k & 1] & 1 != (k >> 1) & 1
+
+    for k in range(n):
+        finish(k - bufs)  # QK^T of tile k was issued behind PV of tile k - bufs
+        if k > 0 and passes(k - 1) and done < k - 1:
+            return k  # (O is scaled in place behind this one)
+    if last_wait == "pv_done" and passes(n - 1) and done < n - 1:
+        return n
+    return None
+
+
+def test_prefill_waits_for_all_products():
+    """A wait for the last tile's phase of pv_done can return at once with three
+    buffers, whatever the number of tiles above two; the waits inside the tiles
+    cannot. So the kernel's last wait is for a barrier with a single phase,
+    behind every product."""
+    for n in range(1, 40):
+        assert _first_wrong_wait(n, 2, "pv_done") is None
+        assert _first_wrong_wait(n, 3, "pv_done") == (n if n >= 3 else None)
+        assert _first_wrong_wait(n, 2, "drain") is None and _first_wrong_wait(n, 3, "drain") is None
+    body = _kernels(_source("pa_diff_prefill.cu"))["diff_prefill_kernel"]
+    softmax = body[body.index("auto rescale_o"):body.index("coef = lt")]
+    tiles, end = softmax[:softmax.index("grid_dep_launch()")], softmax[softmax.index("grid_dep_launch()"):]
+    assert tiles.count("pv_done") == 1 and "pv_done" not in end
+    assert "wait_bar(smem_u32(&bars->drain), 0," in end
+    assert body.count("tc_commit(smem_u32(&bars->drain))") == 1
