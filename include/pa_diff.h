@@ -29,9 +29,9 @@
  * and the norm are f32; out is rounded once. Operands of the products: keys
  * and values as they are; the rotated query and the probabilities as two
  * 16-bit parts each (value and remainder), so that the difference of the two
- * maps is as exact as its own rounding. In fp16 a probability is off by 2^-36
+ * maps is as exact as its own rounding. In fp16 a probability is off by 2^-34
  * of the row's largest at most: where the largest has a value near zero (an
- * attention sink), that holds for others down to about 2^-24 of it.
+ * attention sink), that holds for others down to about 2^-22 of it.
  */
 #ifndef PA_DIFF_H
 #define PA_DIFF_H

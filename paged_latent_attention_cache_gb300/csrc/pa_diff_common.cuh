@@ -10,17 +10,18 @@ namespace diff {
 // 2^(s - m + shift), m the row's running maximum, which may lag behind by `lazy`;
 // their sum carries the same factor, so it cancels. bf16 has f32's exponents.
 // fp16 ends below 2^16 and its least step is 2^-24, which no remainder passes:
-// with shift + lazy = 15 a probability is off by 2^-25 / 2^shift = 2^-36 of the
+// with shift + lazy = 15 a probability is off by 2^-25 / 2^shift = 2^-34 of the
 // row's largest at most. (With shift 0 and 2^-25, a key that takes nearly all of the
 // weight at a value near zero left relative errors of up to 4e-2, as the norm
-// scales up the small rest. Lazy 4 and not less: scores of spread 1 pass a
-// tile's maximum by 2^4 hardly ever, by 2^2 in every fifth tile of 128.)
+// scales up the small rest. A smaller lag leaves more room below, but a tile
+// whose maximum passes the running one by more is computed twice: prefill of
+// 26 drawn cases takes 1.3 % longer with 4 than with 8, 0.5 % with 6.)
 template <typename T> struct Prob;
 template <> struct Prob<__nv_bfloat16> {
   static constexpr float lazy = 8.f, shift = 0.f;
 };
 template <> struct Prob<__half> {
-  static constexpr float lazy = 4.f, shift = 11.f;
+  static constexpr float lazy = 6.f, shift = 9.f;
 };
 
 // True in one lane of the warp (converged). Code behind `if (elect_one())` is
