@@ -644,6 +644,7 @@ diff_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                 l *= factor;
                 rescale = true;
               }
+              tmem_wait_st();  // nothing else orders two stores to the same columns
               exps();
               // (k >= 1) each half scales half of O
               if (__any_sync(0xffffffffu, rescale))

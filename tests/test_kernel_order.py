@@ -88,3 +88,12 @@ def test_prefill_waits_for_all_products():
     assert tiles.count("pv_done") == 1 and "pv_done" not in end
     assert "wait_bar(smem_u32(&bars->drain), 0," in end
     assert body.count("tc_commit(smem_u32(&bars->drain))") == 1
+
+
+def test_prefill_stores_to_tensor_memory_in_order():
+    """The probabilities of a tile may be stored twice to the same columns:
+    tcgen05.st is asynchronous, so the first stores are waited for between."""
+    body = _kernels(_source("pa_diff_prefill.cu"))["diff_prefill_kernel"]
+    tile = body[body.index("bool again"):body.index("arrive_warp(p_full")]
+    first, second = [m.start() for m in re.finditer(r"\bexps\(\)", tile)]
+    assert "tmem_wait_st()" in tile[first:second]
