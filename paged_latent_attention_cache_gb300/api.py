@@ -215,6 +215,18 @@ def _device(index: int):
     return _NOTHING if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
+def _allocating(stream, index: int):
+    """What is allocated in this block is memory of ``stream``, a call's
+    argument: a torch stream, a handle, or None for the current stream."""
+    if stream is None:
+        return _NOTHING
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=index) if handle else \
+            torch.cuda.default_stream(index)
+    return torch.cuda.stream(stream)
+
+
 class DifferentialAttention:
     """Differential attention over paged caches (include/pa_diff.h): two query
     and key maps per head and one value, the difference of the two softmax
@@ -368,10 +380,7 @@ class DifferentialAttention:
             _require(key.size(0) == query.size(0), "query and key must have a row per token")
             if out is None:
                 shape = (query.size(0), self.num_heads * self.v_head_size)
-                if isinstance(stream, torch.cuda.Stream):  # memory of the stream that writes it
-                    with torch.cuda.stream(stream):
-                        out = torch.empty(shape, dtype=self.dtype, device=self.device)
-                else:
+                with _allocating(stream, self._index):
                     out = torch.empty(shape, dtype=self.dtype, device=self.device)
             stream = B.raw_stream(stream)
             self._check_read(query, lambda_vectors, norm_weight, past, block_table, out)

@@ -613,3 +613,23 @@ def test_values_that_come_late():
         outs.append(far.forward(*_args({**t, **big, "block_table": bt, "slot_mapping": slots}), 0))
     assert op.error_flags() == 0 and far.error_flags() == 0
     assert [torch.equal(o, want) for o in outs] == [True] * 15
+
+
+@pytest.mark.parametrize("kind", ["stream", "handle", "default"])
+def test_output_is_memory_of_its_stream(kind):
+    """The output that forward allocates belongs to the stream it is given, as
+    a torch stream or as a handle: once dropped, its memory is not handed to
+    the current stream, which the kernels that still write it do not wait for."""
+    w = workload("64_128", q_lens=[1, 40], past_lens=[100, 60], drop_slots=0)
+    d, want, op = run_gpu(w)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    stream = {"stream": side, "handle": side.cuda_stream, "default": 0}[kind]
+    with torch.cuda.stream(torch.cuda.Stream() if kind == "default" else torch.cuda.current_stream()):
+        out = op.forward(*_args(d), 1, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        at = out.data_ptr()
+        del out
+        others = [torch.empty_like(want) for _ in range(64)]
+        assert all(o.data_ptr() != at for o in others)
