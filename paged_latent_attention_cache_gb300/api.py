@@ -227,6 +227,28 @@ def _allocating(stream, index: int):
     return torch.cuda.stream(stream)
 
 
+class _Filled:
+    """Orders an object's first call behind what its constructor enqueued on
+    the stream that was current then, whatever stream the call is given. (Not
+    across a graph's borders: a capture starts behind everything, and could
+    not wait for an event from outside.)"""
+
+    def __init__(self, index: int):
+        with _device(index):
+            self.stream = B.raw_stream(None)
+            self.captured = torch.cuda.is_current_stream_capturing()
+            if not self.captured:
+                self.event = torch.cuda.Event()
+                self.event.record()
+
+    def before(self, stream):
+        """Makes ``stream`` wait."""
+        raw = B.raw_stream(stream)
+        if raw != self.stream and not (self.captured or torch.cuda.is_current_stream_capturing()):
+            with _allocating(raw, torch.cuda.current_device()):
+                self.event.wait()
+
+
 class DifferentialAttention:
     """Differential attention over paged caches (include/pa_diff.h): two query
     and key maps per head and one value, the difference of the two softmax
@@ -272,6 +294,11 @@ class DifferentialAttention:
             n = B.pa_diff_workspace_size(self.params, max_seqs, max_tokens)
         self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
         self.err_flags = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._filled = _Filled(self._index)
+
+    def _begin(self, stream):
+        self._filled.before(stream)
+        self._filled = None
 
     # -- argument checks: types, devices and sizes the C side cannot see
     def _tensors(self, dtype, names, *tensors):
@@ -331,6 +358,8 @@ class DifferentialAttention:
         self._check_caches(key_cache, value_cache, cos_cache, sin_cache, cumseq, past)
         self._check_write(key, value, slot_mapping)
         with self._on_device():
+            if self._filled is not None:
+                self._begin(stream)
             B.pa_diff_write(self.params, key, value, cos_cache, sin_cache, slot_mapping, cumseq,
                             past, key_cache, value_cache, self.err_flags, stream)
 
@@ -344,6 +373,8 @@ class DifferentialAttention:
         self._check_caches(key_cache, value_cache, cos_cache, sin_cache, cumseq, past)
         self._check_read(query, lambda_vectors, norm_weight, past, block_table, out)
         with self._on_device():
+            if self._filled is not None:
+                self._begin(rest[2])
             self._read(fn, args, *rest)
 
     def decode(self, query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
@@ -384,6 +415,8 @@ class DifferentialAttention:
                     out = torch.empty(shape, dtype=self.dtype, device=self.device)
             stream = B.raw_stream(stream)
             self._check_read(query, lambda_vectors, norm_weight, past, block_table, out)
+            if self._filled is not None:
+                self._begin(stream)
             B.pa_diff_write(self.params, key, value, cos_cache, sin_cache, slot_mapping, cumseq,
                             past, key_cache, value_cache, self.err_flags, stream)
             args = (query, key_cache, value_cache, cos_cache, sin_cache, lambda_vectors,
@@ -417,8 +450,10 @@ class PagePool:
 
     Every method only enqueues kernels on ``stream`` (the current stream of
     the pool's device by default) and can be captured in a CUDA graph after
-    one eager call; calls on one pool have to be ordered by the caller. See
-    include/pa_pages.h for what each does with arguments that make no sense;
+    one eager call; calls on one pool have to be ordered by the caller. (The
+    first call waits for the constructor's own fills; work on other streams
+    that reads ``block_table``, ``past`` or ``refcount`` before it has to be
+    ordered too.) See include/pa_pages.h for what each does with arguments that make no sense;
     ``error_flags`` reads what the device reported."""
 
     def __init__(self, caches, *, block_size: int, block_table: Optional[torch.Tensor] = None,
@@ -464,6 +499,11 @@ class PagePool:
         self.err_flags = torch.zeros(1, dtype=torch.int32, device=self.device)
         #: pages held after the last ``compact`` (int32 [1] on the device)
         self.live = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._filled = _Filled(self._index)
+
+    def _begin(self, stream):
+        self._filled.before(stream)
+        self._filled = None
 
     def _ints(self, names, *tensors):
         index = self._index
@@ -481,6 +521,8 @@ class PagePool:
         _require(dst.numel() == src.numel() and (rows is None or rows.numel() == src.numel()),
                  "src, dst and rows must have one entry per pair")
         with _device(self._index):
+            if self._filled is not None:
+                self._begin(stream)
             B.pa_pages_copy(self.params, self._list, len(self.caches), src, dst, rows,
                             self.workspace, self.err_flags, stream)
 
@@ -490,6 +532,8 @@ class PagePool:
         self._ints("parents children", parents, children)
         _require(parents.numel() == children.numel(), "parents and children must pair up")
         with _device(self._index):
+            if self._filled is not None:
+                self._begin(stream)
             B.pa_pages_fork(self.params, self._list, len(self.caches), parents, children,
                             self.block_table, self.past, self.refcount, self.workspace,
                             self.err_flags, stream)
@@ -498,6 +542,8 @@ class PagePool:
         """Takes the pages of ``seqs`` back (their rows become -1, their past 0)."""
         self._ints("seqs", seqs)
         with _device(self._index):
+            if self._filled is not None:
+                self._begin(stream)
             B.pa_pages_free(self.params, seqs, self.block_table, self.past, self.refcount,
                             self.err_flags, stream)
 
@@ -508,6 +554,8 @@ class PagePool:
         self._ints("cumseq slot_mapping", cumseq, slot_mapping)
         _require(cumseq.numel() == self.past.numel() + 1, "cumseq must be [num_seqs + 1]")
         with _device(self._index):
+            if self._filled is not None:
+                self._begin(stream)
             B.pa_pages_reserve(self.params, cumseq, self.block_table, self.past, self.refcount,
                                slot_mapping, self.workspace, self.err_flags, stream)
         return slot_mapping
@@ -516,6 +564,8 @@ class PagePool:
         """Moves the held pages to the lowest ids; returns ``live`` (their
         number, on the device)."""
         with _device(self._index):
+            if self._filled is not None:
+                self._begin(stream)
             B.pa_pages_compact(self.params, self._list, len(self.caches), self.block_table,
                                self.refcount, self.live, self.workspace, self.err_flags, stream)
         return self.live

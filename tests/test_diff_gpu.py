@@ -633,3 +633,19 @@ def test_output_is_memory_of_its_stream(kind):
         del out
         others = [torch.empty_like(want) for _ in range(64)]
         assert all(o.data_ptr() != at for o in others)
+
+
+def test_first_call_of_an_operator_on_another_stream():
+    """The error word is cleared on the constructor's stream: a first call on
+    another stream comes behind that, and what it reports stays."""
+    w = workload("64_128", q_lens=[1, 40], past_lens=[100, 60], drop_slots=0)
+    w.tensors["slot_mapping"][0] = 10 ** 8
+    d = {k: v.cuda() for k, v in w.tensors.items()}
+    _op(w).forward(*_args(d), 1)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # a tenth of a second, ahead of the fill
+    op = _op(w)
+    op.forward(*_args(d), 1, stream=side)
+    torch.cuda.synchronize()
+    assert op.error_flags() == B.PA_DEVERR_SLOT

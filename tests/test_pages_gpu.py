@@ -436,3 +436,31 @@ def test_tiny_calls_in_a_row():
     s.check(err)
     for t, n, (live, want) in zip(slots, lives, wants):
         assert np.array_equal(t.cpu().numpy(), want) and int(n.item()) == live
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_first_call_on_another_stream(handle):
+    """The constructor fills table, lengths and refcounts on the current stream;
+    a first call on another stream comes behind that, however late it is."""
+    cache = torch.zeros(64, 16, 16, dtype=torch.uint8, device="cuda")
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    cum, slots = i32([0, 20, 25]), torch.zeros(25, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    warm = PagePool([cache], block_size=16, max_seqs=2, max_blocks_per_seq=4)
+    warm.reserve(cum, slots, stream=side)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # a tenth of a second, ahead of the fills
+    pool = PagePool([cache], block_size=16, max_seqs=2, max_blocks_per_seq=4)
+    pool.reserve(cum, slots, stream=side.cuda_stream if handle else side)
+    torch.cuda.synchronize()
+    assert pool.error_flags() == 0
+    assert pool.block_table.tolist() == [[0, 1, -1, -1], [2, -1, -1, -1]]
+    assert pool.refcount.tolist() == [1, 1, 1] + [0] * 61
+    assert slots.tolist() == list(range(20)) + list(range(32, 37))
+    graph = torch.cuda.CUDAGraph()
+    late = PagePool([cache], block_size=16, max_seqs=2, max_blocks_per_seq=4)
+    with torch.cuda.graph(graph):  # its first call captured
+        late.reserve(cum, slots)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert late.block_table.tolist() == pool.block_table.tolist() and late.error_flags() == 0
