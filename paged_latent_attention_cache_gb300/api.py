@@ -462,6 +462,7 @@ class PagePool:
         self.caches = list(caches)
         _require(len(self.caches) > 0, "a pool needs at least one cache")
         first = self.caches[0]
+        _require(first.dim() >= 2 and first.shape[0] > 0, "caches need at least one page")
         self.device, self.num_blocks = first.device, int(first.shape[0])
         self._index = self.device.index
         _require(self.device.type == "cuda", "caches must be CUDA tensors")
@@ -469,6 +470,7 @@ class PagePool:
             _require(c.device == self.device and c.dim() >= 2 and int(c.shape[0]) == self.num_blocks
                      and int(c.shape[1]) == block_size,
                      "every cache must be [num_blocks, block_size, ...] on one device")
+            _require(c[0].numel() > 0, "cache rows must not be empty")
             _require(c[0].is_contiguous() and (self.num_blocks == 1 or c.stride(0) == c[0].numel()),
                      "caches must be contiguous")
             _require(c.data_ptr() % 16 == 0 and c[0, 0].numel() * c.element_size() % 16 == 0,

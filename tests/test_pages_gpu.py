@@ -464,3 +464,11 @@ def test_first_call_on_another_stream(handle):
     graph.replay()
     torch.cuda.synchronize()
     assert late.block_table.tolist() == pool.block_table.tolist() and late.error_flags() == 0
+
+
+def test_pool_refuses_empty_caches():
+    """Caches without a page, a row or a dimension for them."""
+    zeros = lambda *shape: torch.zeros(*shape, dtype=torch.uint8, device="cuda")
+    for bad in (zeros(0, 16, 16), zeros(8, 16, 0), zeros(8), zeros(8, 0, 16), zeros(())):
+        with pytest.raises(B.PaError):
+            PagePool([bad], block_size=16, max_seqs=1, max_blocks_per_seq=1)
