@@ -649,3 +649,60 @@ def test_first_call_of_an_operator_on_another_stream():
     op.forward(*_args(d), 1, stream=side)
     torch.cuda.synchronize()
     assert op.error_flags() == B.PA_DEVERR_SLOT
+
+
+@pytest.mark.parametrize("what", ["block", "context", "past", "position", "qlen", "slot"])
+def test_bad_indices_and_nothing_else(what):
+    """What a bad page, length, position or slot changes, exactly: the error
+    word, zeros in every row of its sequences, the cache rows of its tokens; the
+    other sequences stay within one step of the dtype, 2 u |x|, and 2^-20 of the
+    largest output where a decode is cut at other places."""
+    w = workload("64_128", q_lens=[1, 1, 20, 30], past_lens=[100, 200, 10, 50], drop_slots=0)
+    d0, want, _ = run_gpu(w)
+    t, cum = w.tensors, w.tensors["cumseq"].tolist()
+    old = {k: t[k].clone() for k in ("key_cache", "value_cache")}
+    slots = t["slot_mapping"].clone()
+    if what == "block":
+        t["block_table"][1, 2], t["block_table"][3, 0] = 10 ** 6, -1
+        flag, zero, unwritten = B.PA_DEVERR_BLOCK, [1, 3], []
+    elif what == "context":  # (the write has no angles for such positions)
+        t["past"][1], t["past"][3] = 10 ** 6, w.max_blocks_per_seq * 64 - 10
+        assert t["past"][3] >= w.cos_rows
+        flag, zero = B.PA_DEVERR_CONTEXT | B.PA_DEVERR_POSITION, [1, 3]
+        unwritten = [1] + list(range(cum[3], cum[4]))
+    elif what == "past":
+        t["past"][1], t["past"][3] = -5, -40
+        flag, zero, unwritten = B.PA_DEVERR_CONTEXT, [1, 3], [1] + list(range(cum[3], cum[4]))
+    elif what == "position":
+        w.params["cos_rows"] = 150
+        flag, zero, unwritten = B.PA_DEVERR_POSITION, [1], [1]
+    elif what == "qlen":
+        flag, zero, unwritten = B.PA_DEVERR_DECODE_QLEN, [], []
+    else:
+        t["slot_mapping"][0], t["slot_mapping"][5] = 10 ** 8, -2
+        flag, zero, unwritten = B.PA_DEVERR_SLOT, [], [0, 5]
+    op = _op(w, own_slots=False)
+    d, got, _ = run_gpu(w, op=op, decodes=3 if what == "qlen" else None)
+    assert op.error_flags() == flag, hex(op.error_flags())
+    for k in old:
+        rows = {k2: v.view(w.num_blocks * 64, -1) for k2, v in (("old", old[k].cuda()), ("new", d[k]), ("good", d0[k]))}
+        keep = torch.ones(w.num_blocks * 64, dtype=torch.bool, device="cuda")
+        for n, s in enumerate(slots.tolist()):
+            if n in unwritten:
+                assert torch.equal(rows["new"][s], rows["old"][s]), (k, n)
+                keep[s] = False
+        assert torch.equal(rows["new"][keep], rows["good"][keep]), k
+    if what == "slot":  # as if the two tokens had no slot
+        t["slot_mapping"][0] = t["slot_mapping"][5] = -1
+        _, dropped, op = run_gpu(w, op=_op(w, own_slots=False))
+        assert op.error_flags() == 0 and torch.equal(got, dropped)
+        want = dropped
+    for b in range(4):
+        rows, good = got[cum[b]:cum[b + 1]].double(), want[cum[b]:cum[b + 1]].double()
+        if b in zero:
+            assert (rows == 0).all(), b
+        elif what == "qlen" and b == 2:
+            assert torch.isnan(rows).all()
+        else:
+            step = 2 * UNIT_ROUNDOFF[w.dtype] * torch.maximum(rows.abs(), good.abs())
+            assert ((rows - good).abs() <= step + 2.0 ** -20 * good.abs().max()).all(), b
