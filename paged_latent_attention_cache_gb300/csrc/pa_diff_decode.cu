@@ -658,9 +658,10 @@ diff_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     if (at < count) cur = s_cur;
   }
   if (!waited) grid_dep_wait();
-  // after a wait that gave up, copies may still be in flight
+  // after a wait that gave up, or a part left early because the lengths changed,
+  // copies may still be in flight
   __syncthreads();
-  if (s_abort && tid < stages && s_last[tid] >= 0)
+  if ((s_abort || at < count) && tid < stages && s_last[tid] >= 0)
     tc::drain_wait(smem_u32(&s_full[tid]), (uint32_t)(s_last[tid] / stages) & 1u, a.err_flags);
 }
 

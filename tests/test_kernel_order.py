@@ -97,3 +97,13 @@ def test_prefill_stores_to_tensor_memory_in_order():
     tile = body[body.index("bool again"):body.index("arrive_warp(p_full")]
     first, second = [m.start() for m in re.finditer(r"\bexps\(\)", tile)]
     assert "tmem_wait_st()" in tile[first:second]
+
+
+def test_decode_leaves_no_copy_in_flight():
+    """Every way out of the loop over a CTA's part that leaves tiles unread is
+    followed by a wait for the copies that were started."""
+    body = _kernels(_source("pa_diff_decode.cu"))["diff_decode_kernel"]
+    assert re.search(r"if \(seg <= 0[^;]*\) break;", body)  # tiles left: at < count
+    end = body[body.index("s_cur = cur;"):]
+    wait = end[:end.index("drain_wait")]
+    assert "s_abort || at < count" in wait
