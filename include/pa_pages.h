@@ -91,6 +91,8 @@ pa_status pa_pages_copy(const pa_pages_params* p, const pa_pages_cache* caches,
  * of this call, or a page of the parent is out of range or free; it sets
  * PA_DEVERR_CONTEXT when past[parent] is negative or beyond its row, and
  * PA_DEVERR_POOL when no page is left for its last rows.
+ * A beam step that permutes its own rows takes two sets of them: it forks the
+ * rows of one set into the empty rows of the other, then frees the first set.
  */
 pa_status pa_pages_fork(const pa_pages_params* p, const pa_pages_cache* caches,
                         int32_t num_caches, const int32_t* parents, const int32_t* children,

@@ -530,7 +530,9 @@ class PagePool:
 
     def fork(self, parents, children, stream=None):
         """Sequence ``children[i]`` becomes a copy of ``parents[i]``: full pages
-        shared, the rows of the last one copied into a page of its own."""
+        shared, the rows of the last one copied into a page of its own. A
+        child's row has to be empty: beams that go on from one another fork
+        into a second set of rows, and the first is freed behind that."""
         self._ints("parents children", parents, children)
         _require(parents.numel() == children.numel(), "parents and children must pair up")
         with _device(self._index):

@@ -472,3 +472,35 @@ def test_pool_refuses_empty_caches():
     for bad in (zeros(0, 16, 16), zeros(8, 16, 0), zeros(8), zeros(8, 0, 16), zeros(())):
         with pytest.raises(B.PaError):
             PagePool([bad], block_size=16, max_seqs=1, max_blocks_per_seq=1)
+
+
+@pytest.mark.parametrize("seed", range(3))
+def test_beam_steps_between_two_sets_of_rows(seed):
+    """Beams that go on from one another, step by step: each forks into the
+    other set of rows, the first set is freed, and every beam gets a token."""
+    beams, steps = 4, 12
+    s = Pair(seed, nb=80, ns=2 * beams, mb=6, fill=0.0, share=False)
+    s.table[:beams, :2] = np.arange(2 * beams).reshape(beams, 2)
+    s.past[:beams] = s.rng.integers(17, 33, size=beams)
+    s.ref = np.bincount(s.table[s.table >= 0], minlength=s.nb).astype(np.int32)
+    s.upload()
+    here = 0
+    for _ in range(steps):
+        there = beams - here
+        parents, children = here + s.rng.integers(0, beams, beams), there + np.arange(beams)
+        rows = here + np.arange(beams)
+        q = np.zeros(2 * beams, int)
+        q[children] = 1
+        cum = np.concatenate([[0], np.cumsum(q)])
+        slots = torch.zeros(beams, dtype=torch.int32, device="cuda")
+        s.pool.fork(s.ints(parents), s.ints(children))
+        s.pool.free(s.ints(rows))
+        s.pool.reserve(s.ints(cum), slots)
+        err = O.fork(s.caches, s.table, s.past, s.ref, parents, children, s.bs)
+        err |= O.free(s.table, s.past, s.ref, rows)
+        e, want = O.reserve(s.table, s.past, s.ref, cum, beams, s.bs)
+        assert err | e == 0 and np.array_equal(slots.cpu().numpy(), want)
+        s.past[children] += 1
+        s.pool.past += s.ints(q)
+        s.check(0)
+        here = there
