@@ -706,3 +706,14 @@ def test_bad_indices_and_nothing_else(what):
         else:
             step = 2 * UNIT_ROUNDOFF[w.dtype] * torch.maximum(rows.abs(), good.abs())
             assert ((rows - good).abs() <= step + 2.0 ** -20 * good.abs().max()).all(), b
+
+
+@pytest.mark.parametrize("n", [8191, 8192])
+def test_thousands_of_sequences(n):
+    """Both sides of the number of sequences whose offsets the write keeps in
+    shared memory: one token each, and a few prompts behind them."""
+    rng = np.random.default_rng(n)
+    q = [1] * (n - 3) + [9, 0, 17]
+    past = [int(x) for x in rng.integers(0, 20, n)]
+    w = workload("64_128", q_lens=q, past_lens=past, num_heads=1, kv_num_heads=1, head_size=16, block_size=16)
+    check(w, tokens=list(range(0, 40)) + sorted(rng.choice(n, 300, replace=False).tolist()) + list(range(n - 3, n + 23)))

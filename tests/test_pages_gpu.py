@@ -504,3 +504,32 @@ def test_beam_steps_between_two_sets_of_rows(seed):
         s.pool.past += s.ints(q)
         s.check(0)
         here = there
+
+
+@pytest.mark.parametrize("ns,long", [(4096, False), (4097, False), (4097, True), (9000, True), (20000, False)])
+def test_thousands_of_sequences(ns, long):
+    """More sequences than their offsets' place in shared memory, with the slots
+    filled by the cluster (up to 24576 tokens) and apart, pages for half of the
+    needs; forks, and all freed."""
+    s = Pair(ns, nb=2 * ns, ns=ns, mb=3, fill=0.3, widths=(16,))
+    q = np.where(s.rng.random(ns) < 0.9, 1, 0)
+    if long:
+        q *= s.rng.integers(1, 20, size=ns)
+    q = np.minimum(q, s.mb * s.bs - s.past)
+    cum = np.concatenate([[0], np.cumsum(q)])
+    T = int(cum[-1]) + 3
+    lack = int((-(-(s.past + q) // s.bs) - (s.table >= 0).sum(1)).clip(0).sum())
+    free = np.flatnonzero(s.ref == 0)
+    s.ref[s.rng.permutation(free)[lack // 2:]] = 1  # held by nobody's row, but held
+    s.upload()
+    slots = torch.full((T,), 12345, dtype=torch.int32, device="cuda")
+    s.pool.reserve(s.ints(cum), slots)
+    err, want = O.reserve(s.table, s.past, s.ref, cum, T, s.bs)
+    assert np.array_equal(slots.cpu().numpy(), want) and err & O.POOL and (want >= 0).sum() > T // 4
+    s.check(err)
+    parents, children = s.rng.integers(0, ns, size=ns), s.rng.permutation(ns)
+    s.pool.fork(s.ints(parents), s.ints(children))
+    s.check(O.fork(s.caches, s.table, s.past, s.ref, parents, children, s.bs))
+    seqs = s.rng.permutation(ns)
+    s.pool.free(s.ints(seqs))
+    s.check(O.free(s.table, s.past, s.ref, seqs))
