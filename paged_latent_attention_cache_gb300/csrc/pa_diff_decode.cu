@@ -2,7 +2,7 @@
 //
 // Bound by HBM: each visible key of a kv head is read once (2 hs + vhs
 // channels, 512 bytes at 64 / 128) for 2 * (hs + vhs) * 2 multiply-adds per
-// head. The work is cut for that:
+// head, with up to 8 heads per kv head (more: below). The work is cut for that:
 //
 // * A tile is 16 keys of one (sequence, kv head, chunk of 8 heads): 16 rows of
 //   one page. Up to 8 heads share a tile's bytes. The rows of an mma.sync
@@ -33,6 +33,11 @@
 // left is the start of the first copies and the last parts' joins. Two sequences
 // of 300 to 1000 keys, 8 heads, fp16 64 / 128: 11 us, latency only (with the
 // write before and the combine behind it 20 us).
+//
+// With more than 8 heads per kv head every chunk of 8 is a stretch of the line of
+// its own and copies the keys again, from L2 at best. The same 32 sequences, 8 kv
+// heads: 64 heads 226 us, 128 heads (two chunks) 419; one kv head (floor 23 us): 8
+// heads 54 us, 16 69, 32 100, 64 177, 128 (16 chunks) 323, with the combine.
 //
 // Precision: out = softmax_0 V - lambda softmax_1 V cancels, so errors of the
 // two maps weigh more than in a plain softmax. The rotated query and the
