@@ -244,9 +244,10 @@ class _Filled:
     def before(self, stream):
         """Makes ``stream`` wait."""
         raw = B.raw_stream(stream)
-        if raw != self.stream and not (self.captured or torch.cuda.is_current_stream_capturing()):
+        if raw != self.stream and not self.captured:
             with _allocating(raw, torch.cuda.current_device()):
-                self.event.wait()
+                if not torch.cuda.is_current_stream_capturing():
+                    self.event.wait()
 
 
 class DifferentialAttention:
@@ -297,8 +298,10 @@ class DifferentialAttention:
         self._filled = _Filled(self._index)
 
     def _begin(self, stream):
-        self._filled.before(stream)
-        self._filled = None
+        filled = self._filled
+        if filled is not None:  # (not taken by another thread meanwhile)
+            filled.before(stream)
+            self._filled = None
 
     # -- argument checks: types, devices and sizes the C side cannot see
     def _tensors(self, dtype, names, *tensors):
@@ -453,8 +456,8 @@ class PagePool:
     one eager call; calls on one pool have to be ordered by the caller. (The
     first call waits for the constructor's own fills; work on other streams
     that reads ``block_table``, ``past`` or ``refcount`` before it has to be
-    ordered too.) See include/pa_pages.h for what each does with arguments that make no sense;
-    ``error_flags`` reads what the device reported."""
+    ordered too.) See include/pa_pages.h for what each does with arguments
+    that make no sense; ``error_flags`` reads what the device reported."""
 
     def __init__(self, caches, *, block_size: int, block_table: Optional[torch.Tensor] = None,
                  past: Optional[torch.Tensor] = None, refcount: Optional[torch.Tensor] = None,
@@ -504,8 +507,10 @@ class PagePool:
         self._filled = _Filled(self._index)
 
     def _begin(self, stream):
-        self._filled.before(stream)
-        self._filled = None
+        filled = self._filled
+        if filled is not None:  # (not taken by another thread meanwhile)
+            filled.before(stream)
+            self._filled = None
 
     def _ints(self, names, *tensors):
         index = self._index

@@ -533,3 +533,25 @@ def test_thousands_of_sequences(ns, long):
     seqs = s.rng.permutation(ns)
     s.pool.free(s.ints(seqs))
     s.check(O.free(s.table, s.past, s.ref, seqs))
+
+
+def test_first_call_captured_by_its_handle():
+    """A capture of the given stream, while another one is current, takes no
+    wait for the constructor's event, which lies outside."""
+    cache = torch.zeros(64, 16, 16, dtype=torch.uint8, device="cuda")
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    cum, slots = i32([0, 20, 25]), torch.zeros(25, dtype=torch.int32, device="cuda")
+    PagePool([cache], block_size=16, max_seqs=2, max_blocks_per_seq=4).reserve(cum, slots)
+    pool = PagePool([cache], block_size=16, max_seqs=2, max_blocks_per_seq=4)
+    slots.fill_(7)
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        graph.capture_begin()
+    pool.reserve(cum, slots, stream=side.cuda_stream)
+    with torch.cuda.stream(side):
+        graph.capture_end()
+    assert slots.tolist() == [7] * 25
+    graph.replay()
+    torch.cuda.synchronize()
+    assert slots.tolist() == list(range(20)) + list(range(32, 37)) and pool.error_flags() == 0
