@@ -51,8 +51,13 @@ typedef struct pa_pages_params {
   int32_t num_seqs;           /* rows of block_table and past, 1..2^22                */
 } pa_pages_params;
 
+/* OR-ed into page_bytes: the tensor belongs to its pages as wholes (the scales
+ * of pa_quant.h), so a copy of any rows of a page copies all of it. */
+#define PA_PAGE_WHOLE ((int64_t)1 << 40)
+
 /* One paged tensor: 16-byte aligned, page_bytes a positive multiple of
- * 16 * block_size (rows of 16 bytes or a multiple). */
+ * 16 * block_size (rows of 16 bytes or a multiple), or PA_PAGE_WHOLE | bytes,
+ * bytes a positive multiple of 8, at most 2^32. */
 typedef struct pa_pages_cache {
   void* data;
   int64_t page_bytes;

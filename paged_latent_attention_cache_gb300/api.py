@@ -439,6 +439,288 @@ class DifferentialAttention:
         self.err_flags.zero_()
 
 
+class QuantizedAttention:
+    """Attention over paged caches in 8 bits (include/pa_quant.h): E4M3 codes with
+    a power of two per page, kv head and cache. The SEPARATE mode's attention
+    (grouped queries, optional head sink and q/k RMSNorm) over such a cache, or
+    with ``cross`` the attention of a decoder's tokens to an encoder's states in
+    it. Holds the parameters, the workspace and the error word; calls of one
+    object share its workspace: order them (one stream, or events).
+
+    ``query`` [T, H*hs], ``key`` [T, kvH*hs], ``value`` [T, kvH*vhs] in ``dtype``;
+    ``key_cache`` [num_blocks, bs, kvH, hs] and ``value_cache`` [num_blocks, bs, kvH,
+    vhs] of one byte per channel (uint8 or float8_e4m3fn); ``scales`` float32
+    [num_blocks, kvH, 2], zeros in the beginning; ``head_sink`` [H], norm weights
+    [hs]. ``v_head_size`` 0 means hs. ``new_caches`` makes an empty cache; a
+    ``PagePool`` over the two caches takes ``scales`` among its ``page_tensors``.
+
+    With ``cross`` an encoder's states are written once as the tokens of their
+    sequence (``write`` with past 0); ``past`` of ``attend`` is then their number,
+    ``cumseq`` counts the decoder's tokens, and there is no rotation (``cos_cache``
+    and ``sin_cache`` None)."""
+
+    def __init__(self, *, dtype: torch.dtype, num_heads: int, kv_num_heads: int, head_size: int,
+                 v_head_size: int = 0, rotary_offset: int = 0, rotary_dim: int = 0,
+                 rotary_interleaved: int = 0, cos_rows: int = 1, block_size: int,
+                 num_blocks: int, max_blocks_per_seq: int, scale: float = 0.0,
+                 softcap: float = 0.0, local_window_size: int = -1, rms_eps: float = 1e-6,
+                 cross: bool = False, max_seqs: int, max_tokens: int, device="cuda",
+                 own_slots: bool = False):
+        self.dtype = dtype
+        self.num_heads, self.kv_num_heads = num_heads, kv_num_heads
+        self.head_size, self.v_head_size = head_size, v_head_size or head_size
+        self.params = B.make_quant_params(
+            dtype=dtype, num_heads=num_heads, kv_num_heads=kv_num_heads, head_size=head_size,
+            v_head_size=v_head_size, rotary_offset=rotary_offset, rotary_dim=rotary_dim,
+            rotary_interleaved=rotary_interleaved, cos_rows=cos_rows, block_size=block_size,
+            num_blocks=num_blocks, max_blocks_per_seq=max_blocks_per_seq, scale=scale,
+            softcap=softcap, local_window_size=local_window_size, rms_eps=rms_eps, cross=cross)
+        s = B.pa_quant_validate(self.params)
+        if s != B.PA_OK:
+            raise B.PaError(s, B.last_error())
+        # as in PagedLatentAttention: the first read call after the write phase
+        self.params_after_write = B.pa_quant_params.from_buffer_copy(self.params)
+        self.params_after_write.flags |= B.PA_FLAG_AFTER_WRITE | (
+            B.PA_FLAG_OWN_SLOTS if own_slots else 0)
+        self.device = torch.empty(0, device=device).device
+        self._index = self.device.index
+        self.max_seqs, self.max_tokens = max_seqs, max_tokens
+        with _device(self._index):
+            n = B.pa_quant_workspace_size(self.params, max_seqs, max_tokens)
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
+        self.err_flags = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._filled = _Filled(self._index)
+
+    def new_caches(self):
+        """An empty ``key_cache``, ``value_cache`` and ``scales``."""
+        p = self.params
+        rows = (p.num_blocks, p.block_size, p.kv_num_heads)
+        return (torch.zeros(*rows, self.head_size, dtype=torch.uint8, device=self.device),
+                torch.zeros(*rows, self.v_head_size, dtype=torch.uint8, device=self.device),
+                torch.zeros(p.num_blocks, p.kv_num_heads, 2, device=self.device))
+
+    def _begin(self, stream):
+        filled = self._filled
+        if filled is not None:  # (not taken by another thread meanwhile)
+            filled.before(stream)
+            self._filled = None
+
+    # -- argument checks: types, devices and sizes the C side cannot see
+    def _tensors(self, dtype, names, *tensors):
+        index = self._index
+        for t in tensors:
+            if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+                name = names.split()[[x is t for x in tensors].index(True)]
+                _require(False, f"{name} must be a contiguous {dtype} tensor on {self.device}")
+
+    def _check_caches(self, key_cache, value_cache, scales, cumseq, past):
+        p, index = self.params, self._index
+        for t in (key_cache, value_cache):
+            if (t.dtype is not torch.uint8 and t.dtype is not torch.float8_e4m3fn) or \
+                    t.get_device() != index or not t.is_contiguous():
+                name = "key_cache" if t is key_cache else "value_cache"
+                _require(False, f"{name} must be a contiguous uint8 or float8_e4m3fn tensor on "
+                                f"{self.device}")
+        self._tensors(torch.float32, "scales", scales)
+        self._tensors(torch.int32, "cumseq past", cumseq, past)
+        rows = p.num_blocks * p.block_size * p.kv_num_heads
+        _require(key_cache.numel() == rows * self.head_size
+                 and value_cache.numel() == rows * self.v_head_size
+                 and scales.numel() == p.num_blocks * p.kv_num_heads * 2,
+                 "key_cache must be [num_blocks, bs, kvH, hs], value_cache [num_blocks, bs, kvH, "
+                 "vhs], scales [num_blocks, kvH, 2]")
+        _require(cumseq.numel() == past.numel() + 1, "cumseq must be [num_seqs + 1]")
+
+    def _check_rotary(self, cos_cache, sin_cache):
+        p = self.params
+        if p.rotary_dim:
+            self._tensors(self.dtype, "cos_cache sin_cache", cos_cache, sin_cache)
+            half = p.rotary_dim // 2
+            n = p.cos_rows * half
+            _require(cos_cache.size(-1) == sin_cache.size(-1) == half
+                     and cos_cache.numel() >= n and sin_cache.numel() >= n,
+                     "cos_cache and sin_cache must be [cos_rows, rotary_dim / 2]")
+
+    def _check_norm(self, name, weight):
+        if weight is not None:
+            self._tensors(self.dtype, name, weight)
+            _require(weight.numel() == self.head_size, f"{name} must be [hs]")
+
+    def _check_write(self, key, value, slot_mapping, k_norm_weight):
+        self._tensors(self.dtype, "key value", key, value)
+        self._tensors(torch.int32, "slot_mapping", slot_mapping)
+        self._check_norm("k_norm_weight", k_norm_weight)
+        n = key.size(0)
+        _require(key.numel() == n * self.kv_num_heads * self.head_size
+                 and value.size(0) == n and value.numel() == n * self.kv_num_heads * self.v_head_size
+                 and slot_mapping.numel() == n,
+                 "key must be [T, kvH*hs], value [T, kvH*vhs], slot_mapping [T]")
+
+    def _check_read(self, query, past, block_table, out, head_sink, q_norm_weight):
+        self._tensors(self.dtype, "query out", query, out)
+        self._tensors(torch.int32, "block_table", block_table)
+        self._check_norm("q_norm_weight", q_norm_weight)
+        if head_sink is not None:
+            self._tensors(self.dtype, "head_sink", head_sink)
+            _require(head_sink.numel() == self.num_heads, "head_sink must be [H]")
+        n = query.size(0)
+        _require(query.numel() == n * self.num_heads * self.head_size
+                 and out.size(0) == n and out.numel() == n * self.num_heads * self.v_head_size
+                 and block_table.numel() == past.numel() * self.params.max_blocks_per_seq,
+                 "query must be [T, H*hs], out [T, H*vhs], block_table [num_seqs, "
+                 "max_blocks_per_seq]")
+
+    def _output(self, query, out, stream):
+        if out is not None:
+            return out
+        with _allocating(stream, self._index):
+            return torch.empty((query.size(0), self.num_heads * self.v_head_size),
+                               dtype=self.dtype, device=self.device)
+
+    def write(self, key, value, key_cache, value_cache, scales, cos_cache, sin_cache,
+              slot_mapping, cumseq, past, k_norm_weight=None, stream=None):
+        """Normalizes and rotates the new keys, and stores keys and values as codes
+        in their slots; the scales of their pages grow where they have to."""
+        self._check_caches(key_cache, value_cache, scales, cumseq, past)
+        self._check_rotary(cos_cache, sin_cache)
+        self._check_write(key, value, slot_mapping, k_norm_weight)
+        with _device(self._index):
+            if self._filled is not None:
+                self._begin(stream)
+            B.pa_quant_write(self.params, key, value, cos_cache, sin_cache, k_norm_weight,
+                             slot_mapping, cumseq, past, key_cache, value_cache, scales,
+                             self.err_flags, stream)
+
+    def restore(self, key_cache, value_cache, scales, cumseq, past, block_table, num_tokens: int,
+                key: Optional[torch.Tensor] = None, value: Optional[torch.Tensor] = None,
+                stream=None):
+        """Cached rows in 16 bits: ``key`` [num_tokens, kvH*hs] and ``value``
+        [num_tokens, kvH*vhs], row t of sequence b from position past[b] + t -
+        cumseq[b]. Both are allocated unless given."""
+        self._check_caches(key_cache, value_cache, scales, cumseq, past)
+        self._tensors(torch.int32, "block_table", block_table)
+        _require(block_table.numel() == past.numel() * self.params.max_blocks_per_seq,
+                 "block_table must be [num_seqs, max_blocks_per_seq]")
+        _require(num_tokens >= 0, "num_tokens must be >= 0")
+        with _device(self._index):
+            with _allocating(stream, self._index):
+                if key is None:
+                    key = torch.empty((num_tokens, self.kv_num_heads * self.head_size),
+                                      dtype=self.dtype, device=self.device)
+                if value is None:
+                    value = torch.empty((num_tokens, self.kv_num_heads * self.v_head_size),
+                                        dtype=self.dtype, device=self.device)
+            self._tensors(self.dtype, "key value", key, value)
+            _require(key.size(0) == value.size(0) == num_tokens
+                     and key.numel() == num_tokens * self.kv_num_heads * self.head_size
+                     and value.numel() == num_tokens * self.kv_num_heads * self.v_head_size,
+                     "key must be [num_tokens, kvH*hs], value [num_tokens, kvH*vhs]")
+            if self._filled is not None:
+                self._begin(stream)
+            B.pa_quant_restore(self.params, key_cache, value_cache, scales, cumseq, past,
+                               block_table, key, value, self.err_flags, stream)
+        return key, value
+
+    def _read_checked(self, fn, query, key_cache, value_cache, scales, cos_cache, sin_cache,
+                      cumseq, past, block_table, out, seq_begin, seq_end, head_sink,
+                      q_norm_weight, stream, after_write):
+        self._check_caches(key_cache, value_cache, scales, cumseq, past)
+        self._check_rotary(cos_cache, sin_cache)
+        self._check_read(query, past, block_table, out, head_sink, q_norm_weight)
+        with _device(self._index):
+            if self._filled is not None:
+                self._begin(stream)
+            fn(self.params_after_write if after_write else self.params, query, key_cache,
+               value_cache, scales, cos_cache, sin_cache, q_norm_weight, head_sink, cumseq, past,
+               block_table, out, seq_begin, seq_end, self.workspace, self.err_flags, stream)
+
+    def decode(self, query, key_cache, value_cache, scales, cos_cache, sin_cache, cumseq, past,
+               block_table, out, seq_begin=0, seq_end=None, head_sink=None, q_norm_weight=None,
+               stream=None, after_write: bool = False):
+        """Sequences [seq_begin, seq_end) with one new token each.
+        ``after_write``: this call directly follows ``write`` on the same
+        stream (see PA_FLAG_AFTER_WRITE)."""
+        self._read_checked(B.pa_quant_decode, query, key_cache, value_cache, scales, cos_cache,
+                           sin_cache, cumseq, past, block_table, out, seq_begin, seq_end,
+                           head_sink, q_norm_weight, stream, after_write)
+
+    def prefill(self, query, key_cache, value_cache, scales, cos_cache, sin_cache, cumseq, past,
+                block_table, out, seq_begin=0, seq_end=None, head_sink=None, q_norm_weight=None,
+                stream=None, after_write: bool = False):
+        """Sequences [seq_begin, seq_end) with any number of new tokens."""
+        self._read_checked(B.pa_quant_prefill, query, key_cache, value_cache, scales, cos_cache,
+                           sin_cache, cumseq, past, block_table, out, seq_begin, seq_end,
+                           head_sink, q_norm_weight, stream, after_write)
+
+    def attend(self, query, key_cache, value_cache, scales, cos_cache, sin_cache, cumseq, past,
+               block_table, num_decode_seqs: int, head_sink=None, q_norm_weight=None,
+               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Reads without a write: decode over sequences [0, num_decode_seqs) and
+        prefill over the rest; returns ``out``. (``past`` as in ``forward``: what
+        was cached before the tokens of ``query``, or with ``cross`` all there is.)"""
+        nseq = past.size(0)
+        _require(0 <= num_decode_seqs <= nseq, "num_decode_seqs must be in 0..num_seqs")
+        with _device(self._index):
+            self._check_caches(key_cache, value_cache, scales, cumseq, past)
+            self._check_rotary(cos_cache, sin_cache)
+            out = self._output(query, out, stream)
+            stream = B.raw_stream(stream)
+            self._check_read(query, past, block_table, out, head_sink, q_norm_weight)
+            if self._filled is not None:
+                self._begin(stream)
+            self._reads(query, key_cache, value_cache, scales, cos_cache, sin_cache, cumseq, past,
+                        block_table, num_decode_seqs, nseq, head_sink, q_norm_weight, out, stream,
+                        False)
+        return out
+
+    def _reads(self, query, key_cache, value_cache, scales, cos_cache, sin_cache, cumseq, past,
+               block_table, num_decode_seqs, nseq, head_sink, q_norm_weight, out, stream, after):
+        p = self.params_after_write if after else self.params
+        if num_decode_seqs > 0:
+            B.pa_quant_decode(p, query, key_cache, value_cache, scales, cos_cache, sin_cache,
+                              q_norm_weight, head_sink, cumseq, past, block_table, out, 0,
+                              num_decode_seqs, self.workspace, self.err_flags, stream)
+            p = self.params
+        if num_decode_seqs < nseq:
+            B.pa_quant_prefill(p, query, key_cache, value_cache, scales, cos_cache, sin_cache,
+                               q_norm_weight, head_sink, cumseq, past, block_table, out,
+                               num_decode_seqs, nseq, self.workspace, self.err_flags, stream)
+
+    def forward(self, query, key, value, key_cache, value_cache, scales, cos_cache, sin_cache,
+                cumseq, past, block_table, slot_mapping, num_decode_seqs: int, head_sink=None,
+                q_norm_weight=None, k_norm_weight=None, out: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+        """Write phase over all tokens, then decode over sequences [0,
+        num_decode_seqs) and prefill over the rest; returns ``out``."""
+        nseq = past.size(0)
+        _require(not self.params.cross, "cross attention writes and attends apart: see attend")
+        _require(0 <= num_decode_seqs <= nseq, "num_decode_seqs must be in 0..num_seqs")
+        with _device(self._index):
+            self._check_caches(key_cache, value_cache, scales, cumseq, past)
+            self._check_rotary(cos_cache, sin_cache)
+            self._check_write(key, value, slot_mapping, k_norm_weight)
+            _require(key.size(0) == query.size(0), "query and key must have a row per token")
+            out = self._output(query, out, stream)
+            stream = B.raw_stream(stream)
+            self._check_read(query, past, block_table, out, head_sink, q_norm_weight)
+            if self._filled is not None:
+                self._begin(stream)
+            B.pa_quant_write(self.params, key, value, cos_cache, sin_cache, k_norm_weight,
+                             slot_mapping, cumseq, past, key_cache, value_cache, scales,
+                             self.err_flags, stream)
+            self._reads(query, key_cache, value_cache, scales, cos_cache, sin_cache, cumseq, past,
+                        block_table, num_decode_seqs, nseq, head_sink, q_norm_weight, out, stream,
+                        True)
+        return out
+
+    def error_flags(self) -> int:
+        """Reads the device error word (synchronises with the device)."""
+        return int(self.err_flags.item())
+
+    def reset_error_flags(self):
+        self.err_flags.zero_()
+
+
 class PagePool:
     """Pages of a set of paged caches, kept on the device: which sequence
     holds which (``block_table``), how often each is held (``refcount``) and
@@ -450,6 +732,8 @@ class PagePool:
     ``past`` [B] and ``refcount`` [num_blocks] are int32 tensors: pass those in
     use, or leave them out for an empty pool of ``max_seqs`` sequences of up to
     ``max_blocks_per_seq`` pages. The three go to ``forward`` as they are.
+    ``page_tensors``: tensors ``[num_blocks, ...]`` that belong to their pages as
+    wholes and go where those go (the ``scales`` of ``QuantizedAttention``).
 
     Every method only enqueues kernels on ``stream`` (the current stream of
     the pool's device by default) and can be captured in a CUDA graph after
@@ -461,8 +745,9 @@ class PagePool:
 
     def __init__(self, caches, *, block_size: int, block_table: Optional[torch.Tensor] = None,
                  past: Optional[torch.Tensor] = None, refcount: Optional[torch.Tensor] = None,
-                 max_seqs: Optional[int] = None, max_blocks_per_seq: Optional[int] = None):
-        self.caches = list(caches)
+                 max_seqs: Optional[int] = None, max_blocks_per_seq: Optional[int] = None,
+                 page_tensors=()):
+        self.caches, self.page_tensors = list(caches), list(page_tensors)
         _require(len(self.caches) > 0, "a pool needs at least one cache")
         first = self.caches[0]
         _require(first.dim() >= 2 and first.shape[0] > 0, "caches need at least one page")
@@ -478,6 +763,12 @@ class PagePool:
                      "caches must be contiguous")
             _require(c.data_ptr() % 16 == 0 and c[0, 0].numel() * c.element_size() % 16 == 0,
                      "cache rows must be multiples of 16 bytes, 16-byte aligned")
+        for c in self.page_tensors:
+            _require(c.device == self.device and c.dim() >= 1 and int(c.shape[0]) == self.num_blocks,
+                     "every page tensor must be [num_blocks, ...] on the caches' device")
+            _require(c.numel() > 0 and c.is_contiguous() and c.data_ptr() % 16 == 0
+                     and c[0].numel() * c.element_size() % 8 == 0,
+                     "page tensors must be contiguous, 16-byte aligned, a multiple of 8 bytes a page")
         if block_table is None:
             _require(max_seqs is not None and max_blocks_per_seq is not None,
                      "without a block_table, max_seqs and max_blocks_per_seq are needed")
@@ -498,7 +789,8 @@ class PagePool:
         s = B.pa_pages_validate(self.params)
         if s != B.PA_OK:
             raise B.PaError(s, B.last_error())
-        self._list = B.make_page_caches(self.caches)
+        self._list = B.make_page_caches(self.caches, self.page_tensors)
+        self._count = len(self.caches) + len(self.page_tensors)
         self.workspace = torch.empty(B.pa_pages_workspace_size(self.params), dtype=torch.uint8,
                                      device=self.device)
         self.err_flags = torch.zeros(1, dtype=torch.int32, device=self.device)
@@ -530,7 +822,7 @@ class PagePool:
         with _device(self._index):
             if self._filled is not None:
                 self._begin(stream)
-            B.pa_pages_copy(self.params, self._list, len(self.caches), src, dst, rows,
+            B.pa_pages_copy(self.params, self._list, self._count, src, dst, rows,
                             self.workspace, self.err_flags, stream)
 
     def fork(self, parents, children, stream=None):
@@ -543,7 +835,7 @@ class PagePool:
         with _device(self._index):
             if self._filled is not None:
                 self._begin(stream)
-            B.pa_pages_fork(self.params, self._list, len(self.caches), parents, children,
+            B.pa_pages_fork(self.params, self._list, self._count, parents, children,
                             self.block_table, self.past, self.refcount, self.workspace,
                             self.err_flags, stream)
 
@@ -575,7 +867,7 @@ class PagePool:
         with _device(self._index):
             if self._filled is not None:
                 self._begin(stream)
-            B.pa_pages_compact(self.params, self._list, len(self.caches), self.block_table,
+            B.pa_pages_compact(self.params, self._list, self._count, self.block_table,
                                self.refcount, self.live, self.workspace, self.err_flags, stream)
         return self.live
 

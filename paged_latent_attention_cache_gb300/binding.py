@@ -59,8 +59,13 @@ EXPORTED_PAGES = ("pa_pages_validate", "pa_pages_workspace_size", "pa_pages_copy
 EXPORTED_DIFF = ("pa_diff_validate", "pa_diff_write", "pa_diff_decode", "pa_diff_prefill",
                  "pa_diff_workspace_size")
 
+# include/pa_quant.h
+EXPORTED_QUANT = ("pa_quant_validate", "pa_quant_write", "pa_quant_restore", "pa_quant_decode",
+                  "pa_quant_prefill", "pa_quant_workspace_size")
+
 PA_DEVERR_POOL = 0x100
 PA_DEVERR_PAGE = 0x200
+PA_PAGE_WHOLE = 1 << 40
 
 
 class PaError(RuntimeError):
@@ -149,6 +154,29 @@ class pa_diff_params(ctypes.Structure):
     ]
 
 
+class pa_quant_params(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("kv_num_heads", ctypes.c_int32),
+        ("head_size", ctypes.c_int32),
+        ("v_head_size", ctypes.c_int32),
+        ("rotary_offset", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("rotary_interleaved", ctypes.c_int32),
+        ("cos_rows", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32),
+        ("max_blocks_per_seq", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("softcap", ctypes.c_float),
+        ("local_window_size", ctypes.c_int32),
+        ("rms_eps", ctypes.c_float),
+        ("cross", ctypes.c_int32),
+        ("flags", ctypes.c_int32),
+    ]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run "
@@ -210,7 +238,16 @@ def _load() -> ctypes.CDLL:
     lib.pa_diff_prefill.argtypes = dread
     lib.pa_diff_workspace_size.argtypes = [D, i32, i64]
     lib.pa_diff_workspace_size.restype = sz
-    for name in EXPORTED_PAGES + EXPORTED_DIFF:
+    Q = ctypes.POINTER(pa_quant_params)
+    lib.pa_quant_validate.argtypes = [Q]
+    lib.pa_quant_write.argtypes = [Q, vp, vp, i64, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp]
+    lib.pa_quant_restore.argtypes = [Q, vp, vp, vp, vp, vp, vp, i32, i64, vp, vp, vp, vp]
+    qread = [Q, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, sz, vp, vp, vp]
+    lib.pa_quant_decode.argtypes = qread
+    lib.pa_quant_prefill.argtypes = qread
+    lib.pa_quant_workspace_size.argtypes = [Q, i32, i64]
+    lib.pa_quant_workspace_size.restype = sz
+    for name in EXPORTED_PAGES + EXPORTED_DIFF + EXPORTED_QUANT:
         if not name.endswith("workspace_size"):
             getattr(lib, name).restype = ctypes.c_int
     return lib
@@ -419,12 +456,15 @@ def make_pages_params(*, num_blocks, block_size, max_blocks_per_seq, num_seqs) -
                            int(num_seqs))
 
 
-def make_page_caches(caches):
-    """The host array of pa_pages_cache for paged tensors [num_blocks, ...]."""
-    arr = (pa_pages_cache * max(len(caches), 1))()
-    for i, c in enumerate(caches):
+def make_page_caches(caches, page_tensors=()):
+    """The host array of pa_pages_cache for paged tensors [num_blocks, ...];
+    ``page_tensors``: those that belong to their pages as wholes."""
+    arr = (pa_pages_cache * max(len(caches) + len(page_tensors), 1))()
+    for i, c in enumerate([*caches, *page_tensors]):
         arr[i].data = c.data_ptr()
         arr[i].page_bytes = c[0].numel() * c.element_size()
+        if i >= len(caches):
+            arr[i].page_bytes |= PA_PAGE_WHOLE
     return arr
 
 
@@ -540,6 +580,64 @@ def _diff_read(fn):
 
 pa_diff_decode = _diff_read(lib.pa_diff_decode)
 pa_diff_prefill = _diff_read(lib.pa_diff_prefill)
+
+
+def make_quant_params(*, dtype, num_heads, kv_num_heads, head_size, v_head_size=0,
+                      rotary_offset=0, rotary_dim=0, rotary_interleaved=0, cos_rows=1,
+                      block_size, num_blocks, max_blocks_per_seq, scale=0.0, softcap=0.0,
+                      local_window_size=-1, rms_eps=1e-6, cross=0, flags=0) -> pa_quant_params:
+    if isinstance(dtype, torch.dtype):
+        dtype = {torch.float16: PA_DTYPE_F16, torch.bfloat16: PA_DTYPE_BF16}.get(dtype, -1)
+    return pa_quant_params(int(dtype), int(num_heads), int(kv_num_heads), int(head_size),
+                           int(v_head_size), int(rotary_offset), int(rotary_dim),
+                           int(rotary_interleaved), int(cos_rows), int(block_size),
+                           int(num_blocks), int(max_blocks_per_seq), float(scale),
+                           float(softcap), int(local_window_size), float(rms_eps), int(cross),
+                           int(flags))
+
+
+def pa_quant_validate(p: pa_quant_params) -> int:
+    return int(lib.pa_quant_validate(ctypes.byref(p)))
+
+
+def pa_quant_workspace_size(p: pa_quant_params, num_seqs: int, num_tokens: int) -> int:
+    return int(lib.pa_quant_workspace_size(ctypes.byref(p), int(num_seqs), int(num_tokens)))
+
+
+def pa_quant_write(p, key, value, cos_cache, sin_cache, k_norm_weight, slot_mapping, cumseq, past,
+                   key_cache, value_cache, scales, err_flags=None, stream=None):
+    _check(lib.pa_quant_write(ctypes.byref(p), key.data_ptr(), value.data_ptr(), key.size(0),
+                              _addr(cos_cache), _addr(sin_cache), _addr(k_norm_weight),
+                              slot_mapping.data_ptr(), cumseq.data_ptr(), past.data_ptr(),
+                              past.size(0), key_cache.data_ptr(), value_cache.data_ptr(),
+                              scales.data_ptr(), _addr(err_flags), raw_stream(stream)))
+
+
+def pa_quant_restore(p, key_cache, value_cache, scales, cumseq, past, block_table, key, value,
+                     err_flags=None, stream=None):
+    n = (key if key is not None else value).size(0)
+    _check(lib.pa_quant_restore(ctypes.byref(p), key_cache.data_ptr(), value_cache.data_ptr(),
+                                scales.data_ptr(), cumseq.data_ptr(), past.data_ptr(),
+                                block_table.data_ptr(), past.size(0), n, _addr(key), _addr(value),
+                                _addr(err_flags), raw_stream(stream)))
+
+
+def _quant_read(fn):
+    def read(p, query, key_cache, value_cache, scales, cos_cache, sin_cache, q_norm_weight,
+             head_sink, cumseq, past, block_table, out, seq_begin=0, seq_end=None, workspace=None,
+             err_flags=None, stream=None):
+        n = past.size(0)
+        ws, ws_bytes = _ws(workspace)
+        _check(fn(ctypes.byref(p), query.data_ptr(), query.size(0), key_cache.data_ptr(),
+                  value_cache.data_ptr(), scales.data_ptr(), _addr(cos_cache), _addr(sin_cache),
+                  _addr(q_norm_weight), _addr(head_sink), cumseq.data_ptr(), past.data_ptr(),
+                  block_table.data_ptr(), n, seq_begin, n if seq_end is None else seq_end, ws,
+                  ws_bytes, out.data_ptr(), _addr(err_flags), raw_stream(stream)))
+    return read
+
+
+pa_quant_decode = _quant_read(lib.pa_quant_decode)
+pa_quant_prefill = _quant_read(lib.pa_quant_prefill)
 
 
 def default_scale(head_size: int) -> float:

@@ -632,7 +632,7 @@ compact_plan_kernel(State st, Scratch ws, int32_t* live_out) {
 // ---------------------------------------------------------------------------
 struct CacheList {
   uint8_t* data[kMaxCaches];
-  int64_t page_bytes[kMaxCaches];
+  int64_t page_bytes[kMaxCaches];  // with PA_PAGE_WHOLE
   int32_t first[kMaxCaches + 1];  // pieces of the caches before this one
 };
 
@@ -699,9 +699,19 @@ move_kernel(const __grid_constant__ CacheList cl, int num_caches, State st, cons
       const int mid = (a + z) >> 1;
       if (piece < cl.first[mid + 1]) z = mid; else a = mid + 1;
     }
-    const int64_t pb = cl.page_bytes[a], at = (int64_t)(piece - cl.first[a]) * kPieceBytes;
-    const int64_t left = (pb >> sh) * p.z - at;  // bytes to copy from `at` on
+    const bool whole = (cl.page_bytes[a] & PA_PAGE_WHOLE) != 0;
+    const int64_t pb = cl.page_bytes[a] & ~PA_PAGE_WHOLE;
+    const int64_t at = (int64_t)(piece - cl.first[a]) * kPieceBytes;
+    // bytes to copy from `at` on
+    const int64_t left = (whole ? (p.z > 0 ? pb : 0) : (pb >> sh) * p.z) - at;
     if (left <= 0) continue;
+    if (whole) {  // (a page starts on 8 bytes, and there are few of them)
+      const int m = (int)(min(left, (int64_t)kPieceBytes) >> 3);
+      const uint2* s = reinterpret_cast<const uint2*>(cl.data[a] + p.x * pb + at);
+      uint2* d = reinterpret_cast<uint2*>(cl.data[a] + p.y * pb + at);
+      for (int k = lane; k < m; k += 32) d[k] = s[k];
+      continue;
+    }
     const uint4* s = reinterpret_cast<const uint4*>(cl.data[a] + p.x * pb + at);
     uint4* d = reinterpret_cast<uint4*>(cl.data[a] + p.y * pb + at);
     constexpr int kVec = kPieceBytes / 512;  // 16-byte vectors per lane
@@ -763,7 +773,14 @@ pa_status check_caches(const pa_pages_params* p, const pa_pages_cache* caches, i
   for (int i = 0; i < n; ++i) {
     if (!caches[i].data || !aligned(caches[i].data, 16))
       return fail(PA_ERR_INVALID_ARGUMENT, "cache %d must be a 16-byte aligned pointer", i);
-    const int64_t b = caches[i].page_bytes;
+    const int64_t b = caches[i].page_bytes, bytes = b & ~PA_PAGE_WHOLE;
+    if (b > 0 && b != bytes) {
+      if (bytes <= 0 || bytes % 8 != 0 || bytes > ((int64_t)1 << 32))
+        return fail(PA_ERR_INVALID_ARGUMENT,
+                    "cache %d: page_bytes %lld of a tensor of whole pages must be a positive "
+                    "multiple of 8, at most 2^32", i, (long long)bytes);
+      continue;
+    }
     if (b <= 0 || b % (16 * (int64_t)p->block_size) != 0 || b > ((int64_t)1 << 32))
       return fail(PA_ERR_INVALID_ARGUMENT,
                   "cache %d: page_bytes %lld must be a positive multiple of 16 * block_size, "
@@ -851,7 +868,8 @@ pa_status launch_move(const State& st, const Scratch& ws, const pa_pages_cache* 
       cl.data[i] = static_cast<uint8_t*>(caches[c0 + i].data);
       cl.page_bytes[i] = caches[c0 + i].page_bytes;
       cl.first[i + 1] =
-          cl.first[i] + (int32_t)((cl.page_bytes[i] + kPieceBytes - 1) / kPieceBytes);
+          cl.first[i] +
+          (int32_t)(((cl.page_bytes[i] & ~PA_PAGE_WHOLE) + kPieceBytes - 1) / kPieceBytes);
     }
     int64_t work = most * cl.first[m];  // warps
     if (new_id && c0 == 0) {
