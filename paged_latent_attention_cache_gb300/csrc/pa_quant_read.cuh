@@ -1,0 +1,151 @@
+// What the read kernels over 8-bit caches share: parameters, the range of keys
+// that a sequence's tokens see, warp products.
+#pragma once
+
+#include "pa_quant_common.cuh"
+#include "pa_quant_internal.h"
+#include "pa_tc_common.cuh"
+
+namespace pa {
+namespace quant {
+
+using tc::ex2;
+using tc::grid_dep_launch;
+using tc::grid_dep_wait;
+using tc::kLog2e;
+using tc::smem_u32;
+using tc::tanh_ex2;
+
+// A probability times the scale of its value enters the product with the codes
+// as fp16 2^(y - M + kShift): y = log2e s + e, s the score and 2^e the value's scale, M
+// the row's running maximum of y, which may lag behind by kLazy (the power is
+// below 2^(kShift + kLazy) = 2^15 then, fp16 ends at 2^16). So no value is scaled on
+// its own, and what fp16 cuts off (2^-25) is 2^-36 of the row's largest product. The
+// softmax's sum takes the scale out again, page by page, in f32: y - M >= -96 for
+// the keys that carry the sum, scales being 2^-48..2^48.
+constexpr float kLazy = 4.f, kShift = 11.f;
+
+struct ReadP {
+  const void* query;
+  const uint8_t* key_cache;
+  const uint8_t* value_cache;
+  const float2* scales;
+  const void* cos_cache;
+  const void* sin_cache;
+  const void* q_norm;
+  const void* head_sink;
+  const int32_t* cumseq;
+  const int32_t* past;
+  const int32_t* block_table;
+  void* out;
+  int32_t* err_flags;
+  int64_t num_tokens;
+  int seq_begin, nseq;
+  int H, kvh, grp, hs, vhs, ro, rd, interleaved, cos_rows, bs, sh, num_blocks, max_blocks;
+  int window, cross, bf16, early;
+  float scale_log2;  // scale * log2(e)
+  float cap_in;      // scale / softcap, 0 without softcap
+  float cap_out;     // softcap * log2(e)
+  float eps;
+};
+
+inline ReadP read_params(const Geometry& g, const QuantArgs& a) {
+  ReadP P{};
+  P.query = a.query;
+  P.key_cache = a.key_cache;
+  P.value_cache = a.value_cache;
+  P.scales = a.scales;
+  P.cos_cache = a.cos_cache;
+  P.sin_cache = a.sin_cache;
+  P.q_norm = a.q_norm;
+  P.head_sink = a.head_sink;
+  P.cumseq = a.cumseq;
+  P.past = a.past;
+  P.block_table = a.block_table;
+  P.out = a.out;
+  P.err_flags = a.err_flags;
+  P.num_tokens = a.num_tokens;
+  P.seq_begin = a.seq_begin;
+  P.nseq = a.seq_end - a.seq_begin;
+  P.H = g.H;
+  P.kvh = g.kvh;
+  P.grp = g.H / g.kvh;
+  P.hs = g.hs;
+  P.vhs = g.vhs;
+  P.ro = g.ro;
+  P.rd = g.rd;
+  P.interleaved = g.interleaved;
+  P.cos_rows = g.cos_rows;
+  P.bs = g.bs;
+  while ((1 << P.sh) < g.bs) ++P.sh;
+  P.num_blocks = g.num_blocks;
+  P.max_blocks = g.max_blocks;
+  P.window = g.window;
+  P.cross = a.cross;
+  P.bf16 = g.dtype == PA_DTYPE_BF16;
+  P.early = (g.flags & PA_FLAG_AFTER_WRITE) ? 1 : 0;
+  P.scale_log2 = g.scale * kLog2e;
+  P.cap_in = g.softcap > 0.f ? g.scale / g.softcap : 0.f;
+  P.cap_out = g.softcap * kLog2e;
+  P.eps = g.rms_eps;
+  return P;
+}
+
+// log2e times the softcapped score whose ratio to softcap is x.
+__device__ __forceinline__ float capped(const ReadP& P, float x) {
+  return P.cap_out * tanh_ex2(x);
+}
+
+// Eight channels of a query row as fp16, the row times a power of two that
+// brings its largest channel to [2^14, 2^15) (lanes of a row: the whole warp,
+// eight channels a lane). Returns what takes the factor back. (A row of zeros, or
+// one that is not finite, keeps factor 1.)
+__device__ __forceinline__ float scaled_row8(const float (&x)[8], uint4* h) {
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  int e = (int)(__float_as_uint(m) >> 23) - 127;  // m in [2^e, 2^(e + 1))
+  if (m == 0.f || e == 128) e = 14;
+  e = max(-112, e);  // (the factor ends at 2^126)
+  const float f = pow2(14 - e);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = tc::pack2<__half>(x[2 * i] * f, x[2 * i + 1] * f);
+  *h = make_uint4(w[0], w[1], w[2], w[3]);
+  return pow2(e - 14);
+}
+
+// Channels [8 lane, 8 lane + 8) of the query row i (token * H + head) in f32, after
+// norm and rotation (T: the dtype). The whole warp.
+template <typename T>
+__device__ __forceinline__ void query_row8(const ReadP& P, int64_t i, int64_t pos, float (&x)[8]) {
+  const int d0 = (threadIdx.x & 31) * 8;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = 0.f;
+  if (d0 < P.hs)
+    unpack8<T>(*reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(P.query) + i * P.hs + d0),
+               x);
+  norm_rotate8<T>(x, true, d0, P.hs, 32, reinterpret_cast<const T*>(P.q_norm), P.eps, P.ro, P.rd,
+                  P.interleaved, reinterpret_cast<const T*>(P.cos_cache),
+                  reinterpret_cast<const T*>(P.sin_cache), pos);
+}
+
+__device__ __forceinline__ float to_f32(const ReadP& P, const void* p, int64_t i) {
+  return P.bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i])
+                : __half2float(reinterpret_cast<const __half*>(p)[i]);
+}
+__device__ __forceinline__ uint32_t pack_out(const ReadP& P, float a, float b) {
+  return P.bf16 ? tc::pack2<__nv_bfloat16>(a, b) : tc::pack2<__half>(a, b);
+}
+
+// Two E4M3 codes (the low 16 bits) as fp16.
+__device__ __forceinline__ uint32_t codes2(uint32_t two) {
+  uint32_t r;
+  asm("{\n .reg .b16 h;\n cvt.u16.u32 h, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(r) : "r"(two));
+  return r;
+}
+
+}  // namespace quant
+}  // namespace pa
