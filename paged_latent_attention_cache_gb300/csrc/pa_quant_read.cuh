@@ -97,15 +97,14 @@ __device__ __forceinline__ float capped(const ReadP& P, float x) {
 }
 
 // Eight channels of a query row as fp16, the row times a power of two that
-// brings its largest channel to [2^14, 2^15) (lanes of a row: the whole warp,
-// eight channels a lane). Returns what takes the factor back. (A row of zeros, or
-// one that is not finite, keeps factor 1.)
-__device__ __forceinline__ float scaled_row8(const float (&x)[8], uint4* h) {
+// brings its largest channel to [2^14, 2^15) (a row: `lpr` lanes, eight channels
+// each). Returns what takes the factor back. (A row of zeros, or one that is not
+// finite, keeps factor 1.)
+__device__ __forceinline__ float scaled_row8(const float (&x)[8], uint4* h, int lpr = 32) {
   float m = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = lpr >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   int e = (int)(__float_as_uint(m) >> 23) - 127;  // m in [2^e, 2^(e + 1))
   if (m == 0.f || e == 128) e = 14;
   e = max(-112, e);  // (the factor ends at 2^126)
