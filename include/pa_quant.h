@@ -46,7 +46,7 @@
  * rotated query times a power of two that brings its row's largest channel
  * to 2^14 (11 bits of each channel, and none lost down to 2^-28 of the
  * largest), probabilities times the values' scales relative to the row's
- * largest such product (11 bits, down to 2^-25 of it and finer below).
+ * largest such product (11 bits, down to 2^-22 of it; 2^-33 of it at worst below).
  */
 #ifndef PA_QUANT_H
 #define PA_QUANT_H

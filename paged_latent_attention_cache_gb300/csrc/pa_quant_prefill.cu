@@ -7,11 +7,12 @@
 // a unit's tiles and quant_join_kernel adds up their parts.
 //
 // Inside a CTA:
-//   warps 8-11  bring a tile's codes into registers, a tile ahead, and write them as
-//               fp16 (exactly) in the layout the products read: rings of two key and
-//               two value tiles. Both query tiles use what is converted once. Their
-//               pages are looked up two tiles ahead, the scales one.
-//   warp 12     S = Q K^T (N columns of TMEM per buffer), O += P V (A = P from TMEM,
+//   warp 17     copies a tile's codes (TMA through the block table), a tile ahead
+//   warp 18     a tile's scales: pages two tiles ahead, scales one
+//   warps 8-15  write them as fp16 (exactly) in the layout the products read, four keys
+//               and four values: rings of two key and two value tiles. Both query tiles
+//               use what is converted once.
+//   warp 16     S = Q K^T (N columns of TMEM per buffer), O += P V (A = P from TMEM,
 //               written over its S). QT 2: a buffer per query tile, whose softmax runs
 //               while the other's products do; QT 1: two buffers in turn.
 //   warps 0-7   softmax, a thread per row, warps 0-3 for query tile 0 (or the only
@@ -35,14 +36,14 @@ namespace {
 
 using namespace pa::tc;
 
-constexpr int kConvWarp = 8, kMmaWarp = 12, kThreads = 13 * 32;
+constexpr int kConvWarp = 8, kMmaWarp = 16, kCopyWarp = 17, kScaleWarp = 18, kThreads = 20 * 32;
 constexpr int kSlab = kRows * 128;  // bytes of a 64-channel slab of 128 query rows
-constexpr int kPasses = 8;          // 16-byte pieces of a tile per converting thread, at most
 constexpr int kAhead = 4;           // tiles whose scales are kept
 
 struct Bars {
   uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2];
   uint64_t sc_full[kAhead], pv_done, drain;
+  uint64_t c_full[2], c_empty[2];  // codes: of keys, of values
   uint32_t tmem_base;
   int bad, abort, any_odd;
   // keys with a NaN value that some rows of the unit see and others do not: position
@@ -50,16 +51,36 @@ struct Bars {
   // last one's window) behind
   uint32_t odd[16];
 };
-constexpr int kNumBars = 1 + 5 * 2 + 2 + kAhead + 2;
+constexpr int kNumBars = 1 + 6 * 2 + kAhead + 2 + 4;
 
 struct PreP {
   ReadP R;
   float* ws_o;   // [units * kvh * splits][QT * 128][vhs]
   float2* ws_ml; // [units * kvh * splits][QT * 128] maximum (log2 domain; NaN: an invalid page), sum
+  int64_t num_slots;
+  int box;       // rows of a copy: min(bs, N)
   int tpc;       // tokens of a query tile
   int splits;    // CTAs per unit
-  int slabs, vslabs, klpr, vlpr;  // 64-channel slabs, lanes per row of codes
+  int slabs, vslabs, klpr, vlpr;  // 64-channel slabs, lanes for a row's 8-byte pieces
 };
+
+// wait_bar in less code: that of a CTA's roles together has to fit the instruction
+// caches.
+__device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t par, volatile int* abort,
+                                           int32_t* err) {
+  uint64_t t0 = 0;
+  while (!mbar_try_wait(bar, par)) {
+    if (*abort) return false;
+    const uint64_t t = globaltimer();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitLimitNs) {
+      *abort = 1;
+      raise_flag(err, PA_DEVERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
 
 struct Unit {
   int64_t t, pos, lo, lo_hi, pos_hi, last0;  // see resolve()
@@ -146,51 +167,82 @@ __device__ __forceinline__ uint64_t pack_f32(float a, float b) {
 __device__ __forceinline__ void unpack_f32(uint64_t v, float* a, float* b) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v));
 }
-// Without waiting; tmem_wait_ld() and fence16() before the registers are read.
-__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
+// Registers of a warpgroup's threads, out of what the block was launched with:
+// 96 for each of five warpgroups, 2 x kSoftRegs + 2 x kConvRegs + kMmaRegs = 480.
+constexpr int kSoftRegs = 168, kConvRegs = 48, kMmaRegs = 48;
+template <int R>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
 }
-
+template <int R>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
 // The query rows of a tile (token, head), normalized and rotated, as fp16 in
 // swizzled slabs; mult: what takes a row's factor back, times the scale. Rows behind
 // the last are zeros. By the tile's four warps.
 template <typename T>
-__device__ __forceinline__ void load_query(const PreP& A, const Unit& u, int g, int tile, int rows,
-                                           int warp, int lane, uint8_t* q_s, float* mult) {
+__device__ __noinline__ void load_query(const PreP& A, const Unit& u, int g, int tile, int rows,
+                                        int warp, int lane, uint8_t* q_s, float* mult) {
   const ReadP& P = A.R;
   int lpr = 2;
   while (lpr * 8 < P.hs) lpr <<= 1;
-  const int d0 = (lane & (lpr - 1)) * 8, step = 32 / lpr;
+  const int d0 = (lane & (lpr - 1)) * 8, step = 32 / lpr, half = P.rd >> 1;
+  auto place = [&](int row) {
+    return reinterpret_cast<uint4*>(q_s + (d0 >> 6) * kSlab + row * 128 +
+                                    ((((d0 >> 3) & 7) ^ (row & 7)) << 4));
+  };
+  // all rows on their way, to the places where they are changed
 #pragma unroll 4
   for (int r0 = 0; r0 < 32; r0 += step) {
     const int row = warp * 32 + r0 + lane / lpr;
     const bool live = row < rows;
-    const int tok = live ? row / P.grp : 0, h = row - tok * P.grp;
-    const int64_t tt = tile * A.tpc + tok;
+    const int tok = live ? row / P.grp : 0, h = live ? row - tok * P.grp : 0;
+    const T* src = reinterpret_cast<const T*>(P.query) +
+                   ((u.t + tile * A.tpc + tok) * P.H + g * P.grp + h) * P.hs + d0;
+    if (d0 < P.hs)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(place(row))),
+                   "l"(live ? src : reinterpret_cast<const T*>(P.query)), "r"(live ? 16 : 0)
+                   : "memory");
+  }
+  if (P.rd > 0 && warp * 32 + lane < rows) {  // and the rows' angles
+    const int64_t at = (u.pos + tile * A.tpc + (warp * 32 + lane) / P.grp) * half;
+    for (int c = 0; c < half; c += 64) {
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(reinterpret_cast<const T*>(P.cos_cache) + at + c));
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(reinterpret_cast<const T*>(P.sin_cache) + at + c));
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += step) {
+    const int row = warp * 32 + r0 + lane / lpr;
+    const bool live = row < rows;
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    if (live && d0 < P.hs)
-      unpack8<T>(*reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(P.query) +
-                                                 ((u.t + tt) * P.H + g * P.grp + h) * P.hs + d0),
-                 x);
+    if (d0 < P.hs) unpack8<T>(*place(row), x);
     norm_rotate8<T>(x, live, d0, P.hs, lpr, reinterpret_cast<const T*>(P.q_norm), P.eps, P.ro, P.rd,
                     P.interleaved, reinterpret_cast<const T*>(P.cos_cache),
-                    reinterpret_cast<const T*>(P.sin_cache), u.pos + tt);
+                    reinterpret_cast<const T*>(P.sin_cache),
+                    u.pos + tile * A.tpc + (live ? row / P.grp : 0));
     uint4 hx;
     const float back = scaled_row8(x, &hx, lpr);
-    if (d0 < P.hs)
-      *reinterpret_cast<uint4*>(q_s + (d0 >> 6) * kSlab + row * 128 +
-                                ((((d0 >> 3) & 7) ^ (row & 7)) << 4)) = hx;
+    if (d0 < P.hs) *place(row) = hx;
     if (d0 == 0) mult[row] = back * (P.cap_in > 0.f ? P.cap_in : P.scale_log2);
   }
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts64(uint32_t a, uint2 v) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(v.x), "r"(v.y) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
 }
 
 // Four codes' NaNs as 0x80 in their bytes.
@@ -200,7 +252,8 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
 
 template <int QT, int N, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
-quant_prefill_kernel(const __grid_constant__ PreP A) {
+quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PreP A) {
   constexpr int kSegs = N / 16;
   constexpr int kColS = 256;      // first column of the S buffers
   constexpr int kKBox = N * 128;  // bytes of a 64-channel slab of N keys
@@ -210,6 +263,7 @@ quant_prefill_kernel(const __grid_constant__ PreP A) {
   __shared__ Bars bars_s;
   __shared__ float s_mult[QT * kRows];
   __shared__ float2 s_scale[kAhead][kSegs];  // key scale, exponent of the value's
+  __shared__ int2 s_in[kAhead];  // segments with a key, a value scale (or nothing to see), a bit each
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
   Bars* bars = &bars_s;
@@ -243,7 +297,9 @@ quant_prefill_kernel(const __grid_constant__ PreP A) {
       if (at == &bars->q_full) count = QT * 4;
       if ((at >= bars->k_full && at < bars->k_full + 2) || (at >= bars->v_full && at < bars->v_full + 2))
         count = 4;
-      if (at >= bars->p_full && at < bars->p_full + 2) count = 4;
+      if ((at >= bars->p_full && at < bars->p_full + 2) ||
+          (at >= bars->c_empty && at < bars->c_empty + 2))
+        count = 4;
       mbar_init(smem_u32(at), count);
     }
     if (lane < 16) bars->odd[lane] = 0;
@@ -262,7 +318,7 @@ quant_prefill_kernel(const __grid_constant__ PreP A) {
   const bool run = U.status == 0;
   const int n = run ? U.n : 0;
   auto wait = [&](uint64_t* bar, uint32_t par) {
-    return wait_bar(smem_u32(bar), par, abort, P.err_flags);
+    return wait_short(smem_u32(bar), par, abort, P.err_flags);
   };
   const int qt = QT == 2 ? warp >> 2 : 0;  // (softmax warps)
   const int quad = warp & 3, row = quad * 32 + lane;
@@ -273,8 +329,10 @@ quant_prefill_kernel(const __grid_constant__ PreP A) {
   float m = -INFINITY, l = 0.f;
   bool ok = true;
 
-  if (run && n > 0) {
-    if (soft) {
+  // (each role with its registers, and nothing common behind them but the end)
+  if (warp < kConvWarp) {
+    more_registers<kSoftRegs>();
+    if (n > 0 && soft) {
       // =================== softmax ===================
       uint8_t* q_t = q_s + qt * q_bytes;
       if (P.bf16) load_query<__nv_bfloat16>(A, U, g, qt, rows, quad, lane, q_t, s_mult + qt * kRows);
@@ -301,70 +359,41 @@ quant_prefill_kernel(const __grid_constant__ PreP A) {
         const float2* scale = s_scale[k % kAhead];
         const int c0 = (int)max((int64_t)0, min((int64_t)N, lo_r - j0));       // seen columns
         const int c1 = (int)max((int64_t)-1, min((int64_t)(N - 1), last_r - j0));
-        uint32_t pk[N / 2];
-        float lsum, top;
-        // The exponentials use the running maximum as it stands; the tile's own is taken
-        // beside them, and only where it passes that by more than 2^kLazy the tile is
-        // computed again.
-        auto tile = [&]() {
-          const float nm = kShift - (m == -INFINITY ? 0.f : m);
-          lsum = 0.f;
-          top = -INFINITY;
-          uint32_t s[2][16];
-          tmem_ld16_nowait(cols, s[0]);
+        uint32_t x[N / 32][32];
 #pragma unroll
-          for (int i = 0; i < kSegs; ++i) {
-            tmem_wait_ld();
-            uint32_t(&x)[16] = s[i & 1];
+        for (int c = 0; c < N / 32; ++c) tmem_ld32_nowait(cols + c * 32, x[c]);
+        tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; e += 8)
-              asm volatile("" : "+r"(x[e]), "+r"(x[e + 1]), "+r"(x[e + 2]), "+r"(x[e + 3]),
-                           "+r"(x[e + 4]), "+r"(x[e + 5]), "+r"(x[e + 6]), "+r"(x[e + 7]));
-            if (i + 1 < kSegs) tmem_ld16_nowait(cols + (i + 1) * 16, s[(i + 1) & 1]);
-            const float2 sc = scale[i];
-            const float f = fmaxf(sc.x * mult, 1e-37f);  // (a masked score, -inf, times 0 would be NaN)
-            if (CAP) {
+        for (int c = 0; c < N / 32; ++c) reg_fence(x[c]);
+        float top = -INFINITY;
+        if (edge) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                x[e] = __float_as_uint(capped(P, __uint_as_float(x[e]) * f));
-            }
-            if (edge) {
+          for (int c = 0; c < N / 32; ++c) {
+            // bits c0 - 32 c .. c1 - 32 c
+            const int a = min(32, max(0, c0 - 32 * c)), b = min(32, max(0, c1 + 1 - 32 * c));
+            const uint32_t seen = (b < 32 ? (1u << b) - 1 : ~0u) & (a < 32 ? ~0u << a : 0u);
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (i * 16 + e < c0 || i * 16 + e > c1) x[e] = __float_as_uint(-INFINITY);
-            }
-            float v0 = __uint_as_float(x[0]), v1 = __uint_as_float(x[1]);
-#pragma unroll
-            for (int e = 2; e < 14; e += 4) {
-              v0 = fmaxf(v0, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
-              v1 = fmaxf(v1, fmaxf(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])));
-            }
-            v0 = fmaxf(fmaxf(v0, v1), fmaxf(__uint_as_float(x[14]), __uint_as_float(x[15])));
-            top = fmaxf(top, CAP ? v0 + sc.y : fmaf(v0, f, sc.y));
-            const float fe = CAP ? 1.f : f, add = nm + sc.y;
-            const uint64_t f2 = pack_f32(fe, fe), a2 = pack_f32(add, add);
-            uint64_t sum = pack_f32(0.f, 0.f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              uint64_t y;
-              asm("fma.rn.f32x2 %0, %1, %2, %3;"
-                  : "=l"(y)
-                  : "l"(pack_f32(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]))), "l"(f2),
-                    "l"(a2));
-              float a, b;
-              unpack_f32(y, &a, &b);
-              a = ex2(a);
-              b = ex2(b);
-              const uint64_t p2 = pack_f32(a, b);
-              asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(p2));
-              pk[i * 8 + e] = pack2<__half>(a, b);
-            }
-            float a, b;
-            unpack_f32(sum, &a, &b);
-            lsum = fmaf(a + b, ex2(-sc.y), lsum);
+            for (int e = 0; e < 32; ++e)
+              if (!(seen >> e & 1u)) x[c][e] = __float_as_uint(-INFINITY);
           }
-        };
-        tile();
+        }
+        // (a masked score, -inf, times 0 would be NaN)
+        auto factor_of = [&](const float2& sc) { return fmaxf(sc.x * mult, 1e-37f); };
+        auto at = [&](int i) { return __uint_as_float(x[i / 32][i % 32]); };
+#pragma unroll
+        for (int i = 0; i < kSegs; ++i) {
+          const float2 sc = scale[i];
+          float v0 = at(16 * i), v1 = at(16 * i + 1);
+#pragma unroll
+          for (int e = 2; e < 14; e += 4) {
+            v0 = fmaxf(v0, fmaxf(at(16 * i + e), at(16 * i + e + 1)));
+            v1 = fmaxf(v1, fmaxf(at(16 * i + e + 2), at(16 * i + e + 3)));
+          }
+          v0 = fmaxf(fmaxf(v0, v1), fmaxf(at(16 * i + 14), at(16 * i + 15)));
+          const float f = factor_of(sc);
+          if (CAP) v0 = v0 == -INFINITY ? v0 : capped(P, v0 * f);
+          top = fmaxf(top, fmaf(v0, CAP ? 1.f : f, sc.y));
+        }
         if (__any_sync(0xffffffffu, top > m + kLazy)) {
           float factor = 1.f;
           if (top > m + kLazy) {
@@ -378,23 +407,49 @@ quant_prefill_kernel(const __grid_constant__ PreP A) {
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < P.vhs; c += 16) {
-              uint32_t r[16];
-              tmem_ld16(o_addr + c, r);
+            for (int c = 0; c < P.vhs; c += 32) {  // (columns behind vhs are nobody's)
+              uint32_t r[32];
+              tmem_ld32_nowait(o_addr + c, r);
+              tmem_wait_ld();
+              reg_fence(r);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * factor);
-              tmem_st16(o_addr + c, r);
+              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * factor);
+              tmem_st32(o_addr + c, r);
             }
           }
-          tile();
         }
-        l += lsum;
+        const float nm = kShift - (m == -INFINITY ? 0.f : m);
 #pragma unroll
-        for (int c = 0; c < N / 2; c += 16) {
-          uint32_t w[16];
+        for (int c = 0; c < N / 32; ++c) {
+          uint32_t p[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = pk[c + e];
-          tmem_st16(cols + c, w);
+          for (int h = 0; h < 2; ++h) {
+            const float2 sc = scale[2 * c + h];
+            const float f = factor_of(sc);
+            const float fe = CAP ? 1.f : f, add = nm + sc.y;
+            const uint64_t f2 = pack_f32(fe, fe), a2 = pack_f32(add, add);
+            uint64_t sum = pack_f32(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float a = __uint_as_float(x[c][16 * h + 2 * e]), b = __uint_as_float(x[c][16 * h + 2 * e + 1]);
+              if (CAP) {
+                a = a == -INFINITY ? a : capped(P, a * f);
+                b = b == -INFINITY ? b : capped(P, b * f);
+              }
+              uint64_t y;
+              asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(pack_f32(a, b)), "l"(f2), "l"(a2));
+              unpack_f32(y, &a, &b);
+              a = ex2(a);
+              b = ex2(b);
+              const uint64_t p2 = pack_f32(a, b);
+              asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(p2));
+              p[8 * h + e] = pack2<__half>(a, b);
+            }
+            float a, b;
+            unpack_f32(sum, &a, &b);
+            l = fmaf(a + b, ex2(-sc.y), l);
+          }
+          tmem_st16(cols + c * 16, p);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -403,126 +458,141 @@ quant_prefill_kernel(const __grid_constant__ PreP A) {
       grid_dep_launch();
       if (ok) ok = __all_sync(0xffffffffu, wait(&bars->drain, 0));
       tc_fence_after();
-    } else if (warp >= kConvWarp && warp < kMmaWarp) {
+    }
+    if (P.early) grid_dep_wait();
+    // =================== outputs ===================
+    if (run && soft && ok && !*abort && quad * 32 < rows) {
+      const bool live = row < rows, bad = bars->bad != 0;
+      const int tok = live ? row / P.grp : 0, h = g * P.grp + row - tok * P.grp;
+      const int64_t pos_r = U.pos + tok0 + tok;
+      if (bars->any_odd) {
+        const int64_t back = P.window >= 0 ? P.window : pos_r;
+#pragma unroll 1
+        for (int i = 0; i < 512; ++i)
+          if (bars->odd[i >> 5] >> (i & 31) & 1u) {
+            const int64_t j = i < 256 ? U.pos + 1 + i : U.lo + (i - 256);
+            if (j <= pos_r && j >= pos_r - back) l = NAN;
+          }
+      }
+      if (bad && lane == 0) raise_flag(P.err_flags, PA_DEVERR_BLOCK);
+      const uint32_t o_addr = lane_addr + (QT == 2 ? qt * 128 : 0);
+      if (A.splits == 1) {
+        float sum = l;
+        if (P.head_sink && live) sum += ex2(to_f32(P, P.head_sink, h) * kLog2e - m + kShift);
+        // (the sum is NaN where a NaN was seen)
+        const bool none = bad || n == 0 || (m == -INFINITY && l == 0.f);
+        const float inv = 1.f / sum;
+        __half* dst = reinterpret_cast<__half*>(P.out) + ((U.t + tok0 + tok) * P.H + h) * P.vhs;
+#pragma unroll 1
+        for (int c = 0; c < P.vhs; c += 16) {
+          uint32_t r[16], w[8];
+          if (n > 0) tmem_ld16(o_addr + c, r);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            w[e] = none ? 0u : pack_out(P, __uint_as_float(r[2 * e]) * inv,
+                                        __uint_as_float(r[2 * e + 1]) * inv);
+          if (live) {
+            reinterpret_cast<uint4*>(dst + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(dst + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        }
+      } else if (n > 0) {
+        const int64_t at = (int64_t)blockIdx.x * (QT * kRows) + qt * kRows + row;
+        float* dst = A.ws_o + at * P.vhs;
+#pragma unroll 1
+        for (int c = 0; c < P.vhs; c += 16) {
+          uint32_t r[16];
+          tmem_ld16(o_addr + c, r);
+          if (live)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+        }
+        if (live) A.ws_ml[at] = make_float2(bad ? NAN : m, l);
+      }
+    }
+  } else if (warp < kMmaWarp) {
+    fewer_registers<kConvRegs>();
+    if (n > 0) {
       // =================== codes to fp16 ===================
-      const int ct = tid - kConvWarp * 32;
       const int64_t lo = U.lo, hi = U.pos_hi, all_lo = U.lo_hi, all_hi = U.last0, pos = U.pos;
-      const int32_t* table = P.block_table + (int64_t)U.b * P.max_blocks;
-      // page of segment `lane` of a tile: -1 invalid, -2 nothing to see there
-      auto look_up = [&](int k) {
-        const int64_t key = (int64_t)(U.begin + k) * N + lane * 16;
-        if (k >= n || lane >= kSegs || key > hi || key + 15 < lo) return -2;
-        const int32_t page = table[key >> P.sh];
-        return page >= 0 && page < P.num_blocks ? page : -1;
-      };
-      auto scale_at = [&](int page) {
-        return page >= 0 ? P.scales[(int64_t)page * P.kvh + g] : make_float2(0.f, 0.f);
-      };
-      struct Rows {  // of a cache: this thread's pieces of a tile
-        const uint8_t* base;
-        int64_t step;  // bytes of a row of all heads
-        int pieces, piece, row, rows, passes;
-      };
-      auto rows_of = [&](const uint8_t* cache, int width, int lpr) {
-        Rows r;
-        r.step = (int64_t)P.kvh * width;
-        r.pieces = width >> 4;
-        r.piece = ct & (lpr - 1);
-        r.row = ct / lpr;
-        r.rows = 128 / lpr;
-        r.passes = N / r.rows;
-        r.base = cache + (int64_t)g * width + r.piece * 16;
-        return r;
-      };
-      const Rows KR = rows_of(P.key_cache, P.hs, A.klpr), VR = rows_of(P.value_cache, P.vhs, A.vlpr);
-      // (a warp's rows of a pass lie in one segment)
-      auto load = [&](const Rows& R, int k, int pages, uint4 (&c)[kPasses]) {
-#pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-          c[i] = make_uint4(0, 0, 0, 0);
-          if (i < R.passes) {
-            const int r = i * R.rows + R.row;
-            const int page = __shfl_sync(0xffffffffu, pages, r >> 4);
-            const int64_t key = (int64_t)(U.begin + k) * N + r;
-            if (page >= 0 && R.piece < R.pieces)
-              c[i] = *reinterpret_cast<const uint4*>(
-                  R.base + (((int64_t)page << P.sh) + (key & (P.bs - 1))) * R.step);
+      constexpr int kRowsW = N / 4, kSegsW = kRowsW / 16;  // of a tile per warp
+      const int w = warp & 3, h = (warp - kConvWarp) >> 2;  // four warps for keys, four for values
+      const int pitch = h ? P.vhs : P.hs;  // bytes of a row of codes
+      const int lpr = h ? A.vlpr : A.klpr;   // lanes (a power of two) for its 8-byte pieces
+      const int lr = lane / lpr, c = lane & (lpr - 1), rows = 32 / lpr;  // (rows at a time)
+      const bool mine = c * 8 < pitch;
+      const uint32_t src = smem_u32(v_s) + 2 * v_bytes + (h ? N * P.hs : 0) +
+                           (w * kRowsW + lr) * pitch + c * 8;
+      const uint32_t dst = smem_u32(h ? v_s : k_s) + (c >> 3) * kKBox + (w * kRowsW + lr) * 128;
+      // What the conversion must not see: rows of pages without a scale count as zeros;
+      // values that no row of the unit sees become zeros (0 times NaN is NaN), and a NaN
+      // that only some see as well: those are marked, and the rows that see them answer
+      // NaN. in: a bit per segment.
+      auto scrub = [&](int64_t j0, int in) {
+#pragma unroll 1
+        for (int r = 0; r < kRowsW; r += rows) {
+          const int at = w * kRowsW + r + lr;
+          const int64_t j = j0 + at;
+          if (!mine) continue;
+          const uint2 v = lds64(src + r * pitch);
+          if (!(in >> (at >> 4) & 1) || (h && (j < lo || j > hi))) {
+            sts64(src + r * pitch, make_uint2(0, 0));
+          } else if (h && (j < all_lo || j > all_hi) && (nan_codes(v.x) | nan_codes(v.y))) {
+            const int bit = j > all_hi ? (int)(j - pos) - 1 : 256 + (int)(j - lo);
+            atomicOr(&bars->odd[bit >> 5], 1u << (bit & 31));
+            bars->any_odd = 1;
+            sts64(src + r * pitch, make_uint2(0, 0));
           }
         }
       };
-      auto store = [&](const Rows& R, uint8_t* dst, const uint4 (&c)[kPasses], int in) {
-        const int flip = (R.piece >> 2) & 1;  // (eight lanes write eight different chunks)
+      // The warp's rows in fp16, eight channels a lane at a time: eight lanes write eight
+      // different chunks of a row (chunk ch of row q stands at ch ^ (q & 7)). Loads go
+      // ahead of the stores, which they may not pass.
+      constexpr int kBatch = 4;
+      uint32_t from[kBatch], to[kBatch];
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-          if (i < R.passes) {
-            const int r = i * R.rows + R.row;
-            const bool there = __shfl_sync(0xffffffffu, in, r >> 4) != 0;
-            if (R.piece < R.pieces) {
-              uint4 w = c[i];
-              if (!there) w = make_uint4(0, 0, 0, 0);
-              const uint4 a = make_uint4(codes2(w.x), codes2(w.x >> 16), codes2(w.y), codes2(w.y >> 16));
-              const uint4 b = make_uint4(codes2(w.z), codes2(w.z >> 16), codes2(w.w), codes2(w.w >> 16));
-              uint8_t* at = dst + (R.piece >> 2) * kKBox + r * 128;
-              const int c0 = (R.piece & 3) * 2, x = r & 7;
-              *reinterpret_cast<uint4*>(at + (((c0 + flip) ^ x) << 4)) = flip ? b : a;
-              *reinterpret_cast<uint4*>(at + (((c0 + 1 - flip) ^ x) << 4)) = flip ? a : b;
-            }
-          }
+      for (int i = 0; i < kBatch; ++i) {
+        from[i] = src + i * rows * pitch;
+        to[i] = i * rows * 128 + (((c ^ lr ^ (i * rows)) & 7) << 4);
+      }
+      auto convert = [&](uint32_t slot) {
+#pragma unroll 1
+        for (int r0 = 0; r0 < kRowsW; r0 += kBatch * rows) {
+          uint2 v[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            if (mine && r0 + i * rows < kRowsW) v[i] = lds64(from[i] + r0 * pitch);
+          const uint32_t base = slot + dst + r0 * 128, turn = (r0 & 7) << 4;
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            if (mine && r0 + i * rows < kRowsW)
+              sts128((base + to[i]) ^ turn, codes2(v[i].x), codes2(v[i].x >> 16), codes2(v[i].y),
+                     codes2(v[i].y >> 16));
         }
       };
-      // Values that no row sees become zeros (0 times NaN is NaN), and a NaN that only
-      // some see as well: those are marked, and the rows that see them answer NaN.
-      auto mask = [&](int k, uint4 (&c)[kPasses]) {
-#pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-          if (i >= VR.passes) continue;
-          const int64_t j = (int64_t)(U.begin + k) * N + i * VR.rows + VR.row;
-          if (j < lo || j > hi) {
-            c[i] = make_uint4(0, 0, 0, 0);
-          } else if (j < all_lo || j > all_hi) {
-            if (nan_codes(c[i].x) | nan_codes(c[i].y) | nan_codes(c[i].z) | nan_codes(c[i].w)) {
-              c[i] = make_uint4(0, 0, 0, 0);
-              const int bit = j > all_hi ? (int)(j - pos) - 1 : 256 + (int)(j - lo);
-              atomicOr(&bars->odd[bit >> 5], 1u << (bit & 31));
-              bars->any_odd = 1;
-            }
-          }
-        }
-      };
-      int pg0 = look_up(0), pg1 = look_up(1);
-      if (P.early) grid_dep_wait();
-      float2 sc0 = scale_at(pg0);
-      uint4 kc[kPasses], vc[kPasses];
-      load(KR, 0, pg0, kc);
+      uint64_t* empty = h ? bars->v_empty : bars->k_empty;
+      uint64_t* full = h ? bars->v_full : bars->k_full;
 #pragma unroll 1
       for (int k = 0; k < n; ++k) {
-        load(VR, k, pg0, vc);
-        const int pg2 = look_up(k + 2);
-        const float2 sc1 = scale_at(pg1);
-        const int ke = scale_exponent(sc0.x), ve = scale_exponent(sc0.y);
-        const int kin = pg0 >= 0 && ke != kNone, vin = pg0 >= 0 && ve != kNone;
-        if (pg0 == -1) bars->bad = 1;
-        const uint32_t par = ((k >> 1) & 1) ^ 1;
-        if (!__all_sync(0xffffffffu, k < 2 || wait(&bars->k_empty[k & 1], par))) break;
-        if (warp == kConvWarp) {  // (the tile four before is done with: see kAhead)
-          if (lane < kSegs) s_scale[k % kAhead][lane] = make_float2(kin ? sc0.x : 1.f, vin ? ve : kLeast);
-          arrive_warp(&bars->sc_full[k % kAhead], lane);
-        }
-        store(KR, k_s + (k & 1) * k_bytes, kc, kin);
-        fence_proxy_async();
-        arrive_warp(&bars->k_full[k & 1], lane);
-        if (k + 1 < n) load(KR, k + 1, pg1, kc);
+        if (!__all_sync(0xffffffffu, wait(&bars->sc_full[k % kAhead], (k / kAhead) & 1) &&
+                                         wait(&bars->c_full[h], k & 1) &&
+                                         (k < 2 || wait(&empty[k & 1], ((k >> 1) & 1) ^ 1))))
+          break;
+        const int2 in = s_in[k % kAhead];
         const int64_t j0 = (int64_t)(U.begin + k) * N;
-        if (j0 < all_lo || j0 + N - 1 > all_hi) mask(k, vc);
-        if (!__all_sync(0xffffffffu, k < 2 || wait(&bars->v_empty[k & 1], par))) break;
-        store(VR, v_s + (k & 1) * v_bytes, vc, vin);
+        if ((in.x & in.y) != (1 << kSegs) - 1 || (h && (j0 < all_lo || j0 + N - 1 > all_hi)))
+          scrub(j0, h ? in.y : in.x);
+        convert((k & 1) * (h ? v_bytes : k_bytes));
         fence_proxy_async();
-        arrive_warp(&bars->v_full[k & 1], lane);
-        pg0 = pg1;
-        pg1 = pg2;
-        sc0 = sc1;
+        arrive_warp(&full[k & 1], lane);
+        if (lane == 0) mbar_arrive(smem_u32(&bars->c_empty[h]));
       }
-    } else if (warp == kMmaWarp) {
+    }
+    if (P.early) grid_dep_wait();
+  } else {
+    fewer_registers<kMmaRegs>();
+    if (n > 0 && warp == kMmaWarp) {
       // =================== products ===================
       if (diff::elect_one()) {
         constexpr uint32_t id_qk = idesc_f16(false, kRows, N, false);
@@ -533,7 +603,7 @@ quant_prefill_kernel(const __grid_constant__ PreP A) {
           tc_fence_after();
           const uint64_t kd = sdesc(k_base + (k & 1) * k_bytes, 16, 1024);
           const uint64_t qd = sdesc(q_base + tile * q_bytes, 16, 1024);
-#pragma unroll 4
+#pragma unroll 2
           for (int i = 0; i < steps; ++i) {
             const uint32_t in = (uint32_t)(i & 3) * 2;
             mma_ss(tmem + kColS + buf * N, qd + (uint32_t)(i >> 2) * (kSlab >> 4) + in,
@@ -549,107 +619,118 @@ quant_prefill_kernel(const __grid_constant__ PreP A) {
             mma_ts(tmem + (QT == 2 ? tile * 128 : 0), tmem + kColS + buf * N + i * 8,
                    vd + (uint64_t)(i * 128), id_pv, (k > 0 || i > 0) ? 1u : 0u);
         };
-        auto full = [&](uint64_t* bar, int k) { return wait(&bar[k & 1], (k >> 1) & 1); };
+        // Scores run kLead tiles of a buffer ahead. QT 2: those of both query tiles for one
+        // key tile, then P V and the next scores of one after the other; QT 1: those of
+        // two key tiles. i counts (key tile, buffer) in the order of the products.
+        constexpr int kLead = 2;
+        const int total = QT * n;
         bool go = wait(&bars->q_full, 0);
-        if (QT == 2) {
-          go = go && full(bars->k_full, 0);
-          if (go) {
-            qk(0, 0, 0);
-            qk(0, 1, 1);
-            tc_commit(smem_u32(&bars->k_empty[0]));
-          }
-          for (int k = 0; k < n && go; ++k) {
-            for (int t = 0; t < 2 && go; ++t) {
-              go = wait(&bars->p_full[t], k & 1) && (t == 1 || full(bars->v_full, k));
-              if (!go) break;
-              pv(k, t, t);
-              if (k + 1 < n) {
-                go = t == 1 || full(bars->k_full, k + 1);
-                if (go) qk(k + 1, t, t);
-              }
-            }
-            if (go) {
-              tc_commit(smem_u32(&bars->v_empty[k & 1]));
-              tc_commit(smem_u32(&bars->k_empty[(k + 1) & 1]));
-            }
-          }
-        } else {
-          for (int k = 0; k < 2 && k < n && go; ++k) {
-            go = full(bars->k_full, k);
-            if (go) qk(k, k, 0);
-            if (go) tc_commit(smem_u32(&bars->k_empty[k]));
-          }
-          for (int k = 0; k < n && go; ++k) {
-            go = full(bars->p_full, k) && full(bars->v_full, k);
+#pragma unroll 1
+        for (int i = -kLead; i < total && go; ++i) {
+          if (i >= 0) {
+            const int k = QT == 2 ? i >> 1 : i, buf = i & 1;
+            const uint32_t turn = (i >> 1) & 1;  // of the buffer
+            go = wait(&bars->p_full[buf], turn) &&
+                 ((QT == 2 && buf == 1) || wait(&bars->v_full[k & 1], (k >> 1) & 1));
             if (!go) break;
-            pv(k, k & 1, 0);
-            tc_commit(smem_u32(&bars->pv_done));
-            tc_commit(smem_u32(&bars->v_empty[k & 1]));
-            if (k + 2 < n) {
-              go = full(bars->k_full, k + 2);
-              if (go) qk(k + 2, k & 1, 0);
-              if (go) tc_commit(smem_u32(&bars->k_empty[k & 1]));
-            }
+            pv(k, buf, QT == 2 ? buf : 0);
+            if (QT == 1) tc_commit(smem_u32(&bars->pv_done));
+            if (QT == 1 || buf == 1) tc_commit(smem_u32(&bars->v_empty[k & 1]));
+          }
+          const int s = i + kLead;
+          if (s < total) {
+            const int k = QT == 2 ? s >> 1 : s, buf = s & 1;
+            go = (QT == 2 && buf == 1) || wait(&bars->k_full[k & 1], (k >> 1) & 1);
+            if (!go) break;
+            qk(k, buf, QT == 2 ? buf : 0);
+            if (QT == 1 || buf == 1) tc_commit(smem_u32(&bars->k_empty[k & 1]));
           }
         }
         tc_commit(smem_u32(&bars->drain));
         drain_wait(smem_u32(&bars->drain), 0, P.err_flags);
       }
       __syncwarp();
-    }
-  }
-  if (P.early) grid_dep_wait();
-
-  // =================== outputs ===================
-  if (run && soft && ok && !*abort && quad * 32 < rows) {
-    const bool live = row < rows, bad = bars->bad != 0;
-    const int tok = live ? row / P.grp : 0, h = g * P.grp + row - tok * P.grp;
-    const int64_t pos_r = U.pos + tok0 + tok;
-    if (bars->any_odd) {
-      const int64_t back = P.window >= 0 ? P.window : pos_r;
+    } else if (n > 0 && warp == kCopyWarp) {
+      // =================== copies of codes ===================
+      const int64_t lo = U.lo, hi = U.pos_hi;
+      const int32_t* table = P.block_table + (int64_t)U.b * P.max_blocks;
+      const int nbox = N / A.box;
+      // cache row of box `lane`: behind the last one (zeros arrive) where there is
+      // nothing to see or no page
+      auto look_up = [&](int k) {
+        const int64_t key = (int64_t)(U.begin + k) * N + lane * A.box;
+        if (k >= n || lane >= nbox || key > hi || key + A.box - 1 < lo) return (int)A.num_slots;
+        const int32_t page = table[key >> P.sh];
+        return page >= 0 && page < P.num_blocks ? (page << P.sh) + (int)(key & (P.bs - 1))
+                                                : (int)A.num_slots;
+      };
+      int row = look_up(0);
+      if (P.early) grid_dep_wait();
+      const uint32_t codes = smem_u32(v_s + 2 * v_bytes);
+      int issued = 0;
 #pragma unroll 1
-      for (int i = 0; i < 512; ++i)
-        if (bars->odd[i >> 5] >> (i & 31) & 1u) {
-          const int64_t j = i < 256 ? U.pos + 1 + i : U.lo + (i - 256);
-          if (j <= pos_r && j >= pos_r - back) l = NAN;
+      for (int k = 0; k < n; ++k) {
+        const int next = look_up(k + 1);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          const int width = h ? P.vhs : P.hs;
+          const uint32_t dst = codes + (h ? N * P.hs : 0) + lane * A.box * width;
+          const uint32_t bar = smem_u32(&bars->c_full[h]);
+          if (!__all_sync(0xffffffffu, k == 0 || wait(&bars->c_empty[h], (k - 1) & 1))) break;
+          if (lane == 0) mbar_expect_tx(bar, N * width);
+          __syncwarp();
+          if (lane < nbox) tma_load_3d(dst, h ? &vmap : &kmap, 0, g, row, bar);
+          ++issued;
         }
-    }
-    if (bad && lane == 0) raise_flag(P.err_flags, PA_DEVERR_BLOCK);
-    const uint32_t o_addr = lane_addr + (QT == 2 ? qt * 128 : 0);
-    if (A.splits == 1) {
-      float sum = l;
-      if (P.head_sink && live) sum += ex2(to_f32(P, P.head_sink, h) * kLog2e - m + kShift);
-      // (the sum is NaN where a NaN was seen)
-      const bool none = bad || n == 0 || (m == -INFINITY && l == 0.f);
-      const float inv = 1.f / sum;
-      __half* dst = reinterpret_cast<__half*>(P.out) + ((U.t + tok0 + tok) * P.H + h) * P.vhs;
-#pragma unroll 1
-      for (int c = 0; c < P.vhs; c += 16) {
-        uint32_t r[16], w[8];
-        if (n > 0) tmem_ld16(o_addr + c, r);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          w[e] = none ? 0u : pack_out(P, __uint_as_float(r[2 * e]) * inv,
-                                      __uint_as_float(r[2 * e + 1]) * inv);
-        if (live) {
-          reinterpret_cast<uint4*>(dst + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          reinterpret_cast<uint4*>(dst + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        }
+        if (*abort) break;
+        row = next;
       }
-    } else if (n > 0) {
-      const int64_t at = (int64_t)blockIdx.x * (QT * kRows) + qt * kRows + row;
-      float* dst = A.ws_o + at * P.vhs;
-#pragma unroll 1
-      for (int c = 0; c < P.vhs; c += 16) {
-        uint32_t r[16];
-        tmem_ld16(o_addr + c, r);
-        if (live)
-#pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+      if (*abort && lane == 0) {  // copies may be in flight
+        if (issued > 0) drain_wait(smem_u32(&bars->c_full[0]), ((issued - 1) >> 1) & 1, P.err_flags);
+        if (issued > 1) drain_wait(smem_u32(&bars->c_full[1]), ((issued >> 1) - 1) & 1, P.err_flags);
       }
-      if (live) A.ws_ml[at] = make_float2(bad ? NAN : m, l);
+      __syncwarp();
+    } else if (n > 0 && warp == kScaleWarp) {
+      // =================== scales ===================
+      const int64_t lo = U.lo, hi = U.pos_hi;
+      const int32_t* table = P.block_table + (int64_t)U.b * P.max_blocks;
+      // page of segment `lane` of a tile: -1 invalid, -2 nothing to see there
+      auto look_up = [&](int k) {
+        const int64_t key = (int64_t)(U.begin + k) * N + lane * 16;
+        if (k >= n || lane >= kSegs || key > hi || key + 15 < lo) return -2;
+        const int32_t page = table[key >> P.sh];
+        return page >= 0 && page < P.num_blocks ? page : -1;
+      };
+      auto scale_at = [&](int page) {
+        return page >= 0 ? P.scales[(int64_t)page * P.kvh + g] : make_float2(0.f, 0.f);
+      };
+      int pg0 = look_up(0), pg1 = look_up(1);
+      if (P.early) grid_dep_wait();
+      float2 sc0 = scale_at(pg0);
+#pragma unroll 1
+      for (int k = 0; k < n; ++k) {
+        const int pg2 = look_up(k + 2);
+        const float2 sc1 = scale_at(pg1);
+        const int ke = scale_exponent(sc0.x), ve = scale_exponent(sc0.y);
+        const bool kin = pg0 >= 0 && ke != kNone, vin = pg0 >= 0 && ve != kNone;
+        if (pg0 == -1) bars->bad = 1;
+        // (the tile four before is done with once this tile's place is free: see kAhead)
+        if (!__all_sync(0xffffffffu,
+                        k < 2 || wait(&bars->k_empty[k & 1], ((k >> 1) & 1) ^ 1)))
+          break;
+        const unsigned kb = __ballot_sync(0xffffffffu, kin || pg0 < 0);
+        const unsigned vb = __ballot_sync(0xffffffffu, vin || pg0 < 0);
+        constexpr unsigned kAll = (1u << kSegs) - 1;
+        if (lane < kSegs)
+          s_scale[k % kAhead][lane] = make_float2(kin ? sc0.x : 1.f, vin ? ve : kLeast);
+        if (lane == 0) s_in[k % kAhead] = make_int2(kb & kAll, vb & kAll);
+        arrive_warp(&bars->sc_full[k % kAhead], lane);
+        pg0 = pg1;
+        pg1 = pg2;
+        sc0 = sc1;
+      }
     }
+    if (P.early) grid_dep_wait();
   }
   tc_fence_before();
   __syncthreads();
@@ -712,16 +793,36 @@ __global__ void __launch_bounds__(256) quant_join_kernel(const __grid_constant__
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
+// A cache as (channel, kv head, slot); boxes of one head's channels in `rows` slots.
+cudaError_t codes_map(CUtensorMap* map, const void* base, const Geometry& g, int width, int rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)g.kvh,
+                              (cuuint64_t)g.num_blocks * g.bs};
+  const cuuint64_t str[2] = {(cuuint64_t)width, (cuuint64_t)width * g.kvh};
+  const cuuint32_t box[3] = {(cuuint32_t)width, 1, (cuuint32_t)rows}, one[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, str, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
 template <int QT, int N, bool CAP>
 cudaError_t launch(const Geometry& g, const QuantArgs& a, const PreP& A, int64_t ctas) {
   static std::atomic<bool> configured[64];
   auto kern = quant_prefill_kernel<QT, N, CAP>;
-  const size_t smem = 1024 + (size_t)QT * A.slabs * kSlab + 2 * (size_t)(A.slabs + A.vslabs) * N * 128;
+  const size_t smem = 1024 + (size_t)QT * A.slabs * kSlab +
+                      2 * (size_t)(A.slabs + A.vslabs) * N * 128 + (size_t)N * (g.hs + g.vhs);
   cudaError_t e = once_per_device(configured, g.device, [&] {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
   });
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kern, dim3((unsigned)(ctas * A.splits)), dim3(kThreads), smem, a.stream, A);
+  CUtensorMap kmap, vmap;
+  if ((e = codes_map(&kmap, a.key_cache, g, g.hs, A.box)) != cudaSuccess) return e;
+  if ((e = codes_map(&vmap, a.value_cache, g, g.vhs, A.box)) != cudaSuccess) return e;
+  e = launch_pdl(kern, dim3((unsigned)(ctas * A.splits)), dim3(kThreads), smem, a.stream, kmap, vmap,
+                 A);
   if (e != cudaSuccess || A.splits == 1) return e;
   return launch_pdl(quant_join_kernel<QT, N>, dim3((unsigned)ctas, 8), dim3(256), 0, a.stream, A);
 }
@@ -746,11 +847,13 @@ cudaError_t launch_prefill(const Geometry& g, const QuantArgs& a) {
   A.vslabs = (g.vhs + 63) / 64;
   auto lanes = [](int width) {
     int l = 2;
-    while (l * 16 < width) l *= 2;
+    while (l * 8 < width) l *= 2;
     return l;
   };
   A.klpr = lanes(g.hs);
   A.vlpr = lanes(g.vhs);
+  A.box = std::min(g.bs, n);
+  A.num_slots = (int64_t)g.num_blocks * g.bs;
   A.ws_o = static_cast<float*>(a.workspace);
   A.ws_ml = reinterpret_cast<float2*>(A.ws_o + (size_t)g.num_sms * qt * kRows * g.vhs);
   // (a sequence with tokens has at most one unit that is not full)

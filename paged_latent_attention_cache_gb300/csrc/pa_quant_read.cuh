@@ -20,10 +20,10 @@ using tc::tanh_ex2;
 // as fp16 2^(y - M + kShift): y = log2e s + e, s the score and 2^e the value's scale, M
 // the row's running maximum of y, which may lag behind by kLazy (the power is
 // below 2^(kShift + kLazy) = 2^15 then, fp16 ends at 2^16). So no value is scaled on
-// its own, and what fp16 cuts off (2^-25) is 2^-36 of the row's largest product. The
+// its own, and what fp16 cuts off (2^-25) is 2^-33 of the row's largest product. The
 // softmax's sum takes the scale out again, page by page, in f32: y - M >= -96 for
 // the keys that carry the sum, scales being 2^-48..2^48.
-constexpr float kLazy = 4.f, kShift = 11.f;
+constexpr float kLazy = 7.f, kShift = 8.f;
 
 struct ReadP {
   const void* query;
