@@ -38,12 +38,13 @@ using namespace pa::tc;
 
 constexpr int kConvWarp = 8, kMmaWarp = 16, kCopyWarp = 17, kScaleWarp = 18, kThreads = 20 * 32;
 constexpr int kSlab = kRows * 128;  // bytes of a 64-channel slab of 128 query rows
-constexpr int kAhead = 4;           // tiles whose scales are kept
+constexpr int N = 64;               // keys of a tile
+constexpr int kMaxRing = 4, kAhead = 8;  // tiles converted ahead; tiles whose scales are kept
 
 struct Bars {
-  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2];
-  uint64_t sc_full[kAhead], pv_done, drain;
-  uint64_t c_full[2], c_empty[2];  // codes: of keys, of values
+  uint64_t q_full, k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
+  uint64_t s_full[4], p_full[4], sc_full[kAhead], pv_done[2], drain;
+  uint64_t c_full[2][2], c_empty[2][2];  // codes: of keys, of values
   uint32_t tmem_base;
   int bad, abort, any_odd;
   // keys with a NaN value that some rows of the unit see and others do not: position
@@ -51,7 +52,7 @@ struct Bars {
   // last one's window) behind
   uint32_t odd[16];
 };
-constexpr int kNumBars = 1 + 6 * 2 + kAhead + 2 + 4;
+constexpr int kNumBars = 1 + 4 * kMaxRing + 8 + kAhead + 3 + 8;
 
 struct PreP {
   ReadP R;
@@ -64,12 +65,16 @@ struct PreP {
   int slabs, vslabs, klpr, vlpr;  // 64-channel slabs, lanes for a row's 8-byte pieces
 };
 
-// wait_bar in less code: that of a CTA's roles together has to fit the instruction
-// caches.
+// wait_bar in less code (that of a CTA's roles together has to fit the instruction
+// caches) and fewer instructions: waiting warps took two thirds of all issued ones.
+// IDLE: for roles that run ahead, which sleep between two looks.
+template <bool IDLE>
 __device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t par, volatile int* abort,
                                            int32_t* err) {
   uint64_t t0 = 0;
-  while (!mbar_try_wait(bar, par)) {
+  for (uint32_t i = 1; !mbar_try_wait(bar, par); ++i) {
+    if (IDLE) __nanosleep(128);
+    if (i & 63) continue;
     if (*abort) return false;
     const uint64_t t = globaltimer();
     if (t0 == 0) t0 = t;
@@ -90,7 +95,7 @@ struct Unit {
 
 // Unit `unit` of the batch, by a warp: the sequences' units in order, the last
 // ones (with the most keys) first. first..: what is filled in for all lanes.
-template <int QT, int N>
+template <int QT>
 __device__ Unit resolve(const PreP& A, int unit, int split, int lane) {
   const ReadP& P = A.R;
   const int per = QT * A.tpc;
@@ -169,7 +174,7 @@ __device__ __forceinline__ void unpack_f32(uint64_t v, float* a, float* b) {
 }
 // Registers of a warpgroup's threads, out of what the block was launched with:
 // 96 for each of five warpgroups, 2 x kSoftRegs + 2 x kConvRegs + kMmaRegs = 480.
-constexpr int kSoftRegs = 168, kConvRegs = 48, kMmaRegs = 48;
+constexpr int kSoftRegs = 144, kConvRegs = 64, kMmaRegs = 64;
 template <int R>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
@@ -179,11 +184,12 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 // The query rows of a tile (token, head), normalized and rotated, as fp16 in
-// swizzled slabs; mult: what takes a row's factor back, times the scale. Rows behind
+// swizzled slabs; mult: what takes the factor of the lane's row back, times the scale. Rows behind
 // the last are zeros. By the tile's four warps.
 template <typename T>
 __device__ __noinline__ void load_query(const PreP& A, const Unit& u, int g, int tile, int rows,
                                         int warp, int lane, uint8_t* q_s, float* mult) {
+  float own = 0.f;  // of row 32 warp + lane
   const ReadP& P = A.R;
   int lpr = 2;
   while (lpr * 8 < P.hs) lpr <<= 1;
@@ -228,10 +234,29 @@ __device__ __noinline__ void load_query(const PreP& A, const Unit& u, int g, int
     uint4 hx;
     const float back = scaled_row8(x, &hx, lpr);
     if (d0 < P.hs) *place(row) = hx;
-    if (d0 == 0) mult[row] = back * (P.cap_in > 0.f ? P.cap_in : P.scale_log2);
+    const float v = __shfl_sync(0xffffffffu, back, ((lane - r0) & (step - 1)) * lpr);
+    if (lane >= r0 && lane < r0 + step) own = v;
   }
+  *mult = own * (P.cap_in > 0.f ? P.cap_in : P.scale_log2);
 }
 
+// mma_ss and mma_ts with descriptors of a common upper word.
+__device__ __forceinline__ void mma_ss_lo(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
+                                          uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n mov.b64 x, {%1, %3};\n"
+      " mov.b64 y, {%2, %3};\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_lo(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
+                                          uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n mov.b64 y, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
@@ -245,12 +270,25 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
                : "memory");
 }
 
+// A masked score. (As an instruction of its own: the compiler turned a branch around 64
+// selections into selections that every tile goes through.)
+__device__ __forceinline__ void hide_unless(uint32_t seen, uint32_t& x) {
+  asm volatile("{\n .reg .pred p;\n setp.eq.u32 p, %1, 0;\n @p mov.b32 %0, 0xff800000;\n}\n"
+               : "+r"(x)
+               : "r"(seen));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+  return m;
+}
+
 // Four codes' NaNs as 0x80 in their bytes.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
-template <int QT, int N, bool CAP>
+template <int QT, int R, int C, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
 quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PreP A) {
@@ -261,8 +299,7 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
   extern __shared__ uint8_t smem_raw[];
   __shared__ Unit s_unit;
   __shared__ Bars bars_s;
-  __shared__ float s_mult[QT * kRows];
-  __shared__ float2 s_scale[kAhead][kSegs];  // key scale, exponent of the value's
+  __shared__ float4 s_scale[kAhead][kSegs];  // key scale, exponent e of the value's, 2^-e
   __shared__ int2 s_in[kAhead];  // segments with a key, a value scale (or nothing to see), a bit each
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
@@ -271,13 +308,14 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
   const int q_bytes = A.slabs * kSlab, k_bytes = A.slabs * kKBox, v_bytes = A.vslabs * kKBox;
   uint8_t* q_s = smem;
   uint8_t* k_s = q_s + QT * q_bytes;
-  uint8_t* v_s = k_s + 2 * k_bytes;
+  uint8_t* v_s = k_s + R * k_bytes;
+  uint8_t* codes = v_s + R * v_bytes;  // C key tiles, C value tiles
   const int split = blockIdx.x % A.splits, rest = blockIdx.x / A.splits;
   const int g = rest % P.kvh, unit = rest / P.kvh;
 
   if (!P.early) grid_dep_wait();
   if (warp == 0) {
-    Unit u = resolve<QT, N>(A, unit, split, lane);
+    Unit u = resolve<QT>(A, unit, split, lane);
     if (u.status > 1) {  // invalid positions: told, and zeros
       if (lane == 0 && g == 0 && split == 0) raise_flag(P.err_flags, u.status);
       const int64_t t0 = max((int64_t)0, u.t), t1 = min(u.t + u.ntok, P.num_tokens);
@@ -295,10 +333,11 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
       uint64_t* at = all + i;
       uint32_t count = 1;
       if (at == &bars->q_full) count = QT * 4;
-      if ((at >= bars->k_full && at < bars->k_full + 2) || (at >= bars->v_full && at < bars->v_full + 2))
+      if ((at >= bars->k_full && at < bars->k_full + kMaxRing) ||
+          (at >= bars->v_full && at < bars->v_full + kMaxRing))
         count = 4;
-      if ((at >= bars->p_full && at < bars->p_full + 2) ||
-          (at >= bars->c_empty && at < bars->c_empty + 2))
+      if ((at >= bars->p_full && at < bars->p_full + 4) ||
+          (at >= bars->c_empty[0] && at < bars->c_empty[0] + 4))
         count = 4;
       mbar_init(smem_u32(at), count);
     }
@@ -318,7 +357,10 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
   const bool run = U.status == 0;
   const int n = run ? U.n : 0;
   auto wait = [&](uint64_t* bar, uint32_t par) {
-    return wait_short(smem_u32(bar), par, abort, P.err_flags);
+    return wait_short<false>(smem_u32(bar), par, abort, P.err_flags);
+  };
+  auto wait_idle = [&](uint64_t* bar, uint32_t par) {
+    return wait_short<true>(smem_u32(bar), par, abort, P.err_flags);
   };
   const int qt = QT == 2 ? warp >> 2 : 0;  // (softmax warps)
   const int quad = warp & 3, row = quad * 32 + lane;
@@ -335,20 +377,20 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
     if (n > 0 && soft) {
       // =================== softmax ===================
       uint8_t* q_t = q_s + qt * q_bytes;
-      if (P.bf16) load_query<__nv_bfloat16>(A, U, g, qt, rows, quad, lane, q_t, s_mult + qt * kRows);
-      else load_query<__half>(A, U, g, qt, rows, quad, lane, q_t, s_mult + qt * kRows);
+      float mult;
+      if (P.bf16) load_query<__nv_bfloat16>(A, U, g, qt, rows, quad, lane, q_t, &mult);
+      else load_query<__half>(A, U, g, qt, rows, quad, lane, q_t, &mult);
       fence_proxy_async();
       arrive_warp(&bars->q_full, lane);
       const int64_t pos_r = U.pos + tok0 + row / P.grp;
       const int64_t last_r = P.cross ? U.pos_hi : min(pos_r, U.pos_hi);
       const int64_t lo_r = P.window >= 0 ? max((int64_t)0, pos_r - P.window) : 0;
-      const float mult = s_mult[qt * kRows + row];
       const int64_t last0 = U.last0, lo_hi = U.lo_hi;
       const uint32_t o_addr = lane_addr + (QT == 2 ? qt * 128 : 0);
 #pragma unroll 1
       for (int k = 0; k < n; ++k) {
-        const int buf = QT == 2 ? qt : k & 1;
-        const uint32_t par = QT == 2 ? k & 1 : (k >> 1) & 1;
+        const int buf = qt + QT * (k & 1);
+        const uint32_t par = (k >> 1) & 1;
         const uint32_t cols = lane_addr + kColS + buf * N;
         const int64_t j0 = (int64_t)(U.begin + k) * N;
         const bool edge = j0 < lo_hi || j0 + N - 1 > last0;
@@ -356,7 +398,7 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
                                          wait(&bars->sc_full[k % kAhead], (k / kAhead) & 1));
         if (!ok) break;
         tc_fence_after();
-        const float2* scale = s_scale[k % kAhead];
+        const float4* scale = s_scale[k % kAhead];
         const int c0 = (int)max((int64_t)0, min((int64_t)N, lo_r - j0));       // seen columns
         const int c1 = (int)max((int64_t)-1, min((int64_t)(N - 1), last_r - j0));
         uint32_t x[N / 32][32];
@@ -373,83 +415,96 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
             const int a = min(32, max(0, c0 - 32 * c)), b = min(32, max(0, c1 + 1 - 32 * c));
             const uint32_t seen = (b < 32 ? (1u << b) - 1 : ~0u) & (a < 32 ? ~0u << a : 0u);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(seen >> e & 1u)) x[c][e] = __float_as_uint(-INFINITY);
+            for (int e = 0; e < 32; ++e) hide_unless(seen & (1u << e), x[c][e]);
           }
         }
         // (a masked score, -inf, times 0 would be NaN)
-        auto factor_of = [&](const float2& sc) { return fmaxf(sc.x * mult, 1e-37f); };
+        auto factor_of = [&](const float4& sc) { return fmaxf(sc.x * mult, 1e-37f); };
         auto at = [&](int i) { return __uint_as_float(x[i / 32][i % 32]); };
 #pragma unroll
         for (int i = 0; i < kSegs; ++i) {
-          const float2 sc = scale[i];
-          float v0 = at(16 * i), v1 = at(16 * i + 1);
+          const float4 sc = scale[i];
+          float v0 = max3(at(16 * i), at(16 * i + 1), at(16 * i + 2));
+          float v1 = max3(at(16 * i + 3), at(16 * i + 4), at(16 * i + 5));
 #pragma unroll
-          for (int e = 2; e < 14; e += 4) {
-            v0 = fmaxf(v0, fmaxf(at(16 * i + e), at(16 * i + e + 1)));
-            v1 = fmaxf(v1, fmaxf(at(16 * i + e + 2), at(16 * i + e + 3)));
+          for (int e = 6; e < 14; e += 4) {
+            v0 = max3(v0, at(16 * i + e), at(16 * i + e + 1));
+            v1 = max3(v1, at(16 * i + e + 2), at(16 * i + e + 3));
           }
-          v0 = fmaxf(fmaxf(v0, v1), fmaxf(at(16 * i + 14), at(16 * i + 15)));
+          v0 = max3(fmaxf(v0, v1), at(16 * i + 14), at(16 * i + 15));
           const float f = factor_of(sc);
           if (CAP) v0 = v0 == -INFINITY ? v0 : capped(P, v0 * f);
           top = fmaxf(top, fmaf(v0, CAP ? 1.f : f, sc.y));
         }
-        if (__any_sync(0xffffffffu, top > m + kLazy)) {
-          float factor = 1.f;
-          if (top > m + kLazy) {
-            factor = ex2(m - top);  // (from -inf: 0)
-            m = top;
-            l *= factor;
-          }
-          if (k > 0 && __any_sync(0xffffffffu, factor != 1.f)) {
-            if (QT == 1)  // (with two tiles S comes behind the last product)
-              ok = __all_sync(0xffffffffu, wait(&bars->pv_done, (k - 1) & 1));
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < P.vhs; c += 32) {  // (columns behind vhs are nobody's)
-              uint32_t r[32];
-              tmem_ld32_nowait(o_addr + c, r);
-              tmem_wait_ld();
-              reg_fence(r);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * factor);
-              tmem_st32(o_addr + c, r);
-            }
-          }
+        float factor = 1.f;
+        if (top > m + kLazy) {
+          factor = ex2(m - top);  // (from -inf: 0)
+          m = top;
+          l *= factor;
         }
         const float nm = kShift - (m == -INFINITY ? 0.f : m);
 #pragma unroll
         for (int c = 0; c < N / 32; ++c) {
-          uint32_t p[16];
+          // in passes over the registers, so that the exponentials issue back to back
+          float v[32];
+          float4 sc[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float2 sc = scale[2 * c + h];
-            const float f = factor_of(sc);
-            const float fe = CAP ? 1.f : f, add = nm + sc.y;
+            sc[h] = scale[2 * c + h];
+            const float f = factor_of(sc[h]);
+            const float fe = CAP ? 1.f : f, add = nm + sc[h].y;
             const uint64_t f2 = pack_f32(fe, fe), a2 = pack_f32(add, add);
-            uint64_t sum = pack_f32(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float a = __uint_as_float(x[c][16 * h + 2 * e]), b = __uint_as_float(x[c][16 * h + 2 * e + 1]);
+            for (int e = 16 * h; e < 16 * h + 16; e += 2) {
+              float a = __uint_as_float(x[c][e]), b = __uint_as_float(x[c][e + 1]);
               if (CAP) {
                 a = a == -INFINITY ? a : capped(P, a * f);
                 b = b == -INFINITY ? b : capped(P, b * f);
               }
               uint64_t y;
               asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(pack_f32(a, b)), "l"(f2), "l"(a2));
-              unpack_f32(y, &a, &b);
-              a = ex2(a);
-              b = ex2(b);
-              const uint64_t p2 = pack_f32(a, b);
-              asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(p2));
-              p[8 * h + e] = pack2<__half>(a, b);
+              unpack_f32(y, &v[e], &v[e + 1]);
             }
-            float a, b;
-            unpack_f32(sum, &a, &b);
-            l = fmaf(a + b, ex2(-sc.y), l);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = ex2(v[e]);
+          uint32_t p[16];
+          uint64_t sum[4];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            p[e] = pack2<__half>(v[2 * e], v[2 * e + 1]);
+            const uint64_t p2 = pack_f32(v[2 * e], v[2 * e + 1]);
+            const int q = (e >> 3) * 2 + (e & 1);  // two sums for each scale
+            if ((e & 7) < 2) sum[q] = p2;
+            else asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[q]) : "l"(p2));
           }
           tmem_st16(cols + c * 16, p);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[2 * h]) : "l"(sum[2 * h + 1]));
+            float a, b;
+            unpack_f32(sum[2 * h], &a, &b);
+            l = fmaf(a + b, sc[h].z, l);
+          }
+        }
+        if (k > 0 && __any_sync(0xffffffffu, factor != 1.f)) {
+          ok = __all_sync(0xffffffffu, wait(&bars->pv_done[qt], (k - 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < P.vhs; c += 128) {  // (columns behind vhs are nobody's)
+            uint32_t o[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_ld32_nowait(o_addr + c + i * 32, o[i]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              reg_fence(o[i]);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[i][e] = __float_as_uint(__uint_as_float(o[i][e]) * factor);
+              tmem_st32(o_addr + c + i * 32, o[i]);
+            }
+          }
         }
         tmem_wait_st();
         tc_fence_before();
@@ -516,33 +571,33 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
     if (n > 0) {
       // =================== codes to fp16 ===================
       const int64_t lo = U.lo, hi = U.pos_hi, all_lo = U.lo_hi, all_hi = U.last0, pos = U.pos;
-      constexpr int kRowsW = N / 4, kSegsW = kRowsW / 16;  // of a tile per warp
+      constexpr int kRowsW = N / 4;  // of a tile per warp
       const int w = warp & 3, h = (warp - kConvWarp) >> 2;  // four warps for keys, four for values
       const int pitch = h ? P.vhs : P.hs;  // bytes of a row of codes
       const int lpr = h ? A.vlpr : A.klpr;   // lanes (a power of two) for its 8-byte pieces
       const int lr = lane / lpr, c = lane & (lpr - 1), rows = 32 / lpr;  // (rows at a time)
       const bool mine = c * 8 < pitch;
-      const uint32_t src = smem_u32(v_s) + 2 * v_bytes + (h ? N * P.hs : 0) +
+      const uint32_t src = smem_u32(codes) + (h ? C * N * P.hs : 0) +
                            (w * kRowsW + lr) * pitch + c * 8;
       const uint32_t dst = smem_u32(h ? v_s : k_s) + (c >> 3) * kKBox + (w * kRowsW + lr) * 128;
       // What the conversion must not see: rows of pages without a scale count as zeros;
       // values that no row of the unit sees become zeros (0 times NaN is NaN), and a NaN
       // that only some see as well: those are marked, and the rows that see them answer
       // NaN. in: a bit per segment.
-      auto scrub = [&](int64_t j0, int in) {
+      auto scrub = [&](uint32_t code, int64_t j0, int in) {
 #pragma unroll 1
         for (int r = 0; r < kRowsW; r += rows) {
           const int at = w * kRowsW + r + lr;
           const int64_t j = j0 + at;
           if (!mine) continue;
-          const uint2 v = lds64(src + r * pitch);
+          const uint2 v = lds64(code + src + r * pitch);
           if (!(in >> (at >> 4) & 1) || (h && (j < lo || j > hi))) {
-            sts64(src + r * pitch, make_uint2(0, 0));
+            sts64(code + src + r * pitch, make_uint2(0, 0));
           } else if (h && (j < all_lo || j > all_hi) && (nan_codes(v.x) | nan_codes(v.y))) {
             const int bit = j > all_hi ? (int)(j - pos) - 1 : 256 + (int)(j - lo);
             atomicOr(&bars->odd[bit >> 5], 1u << (bit & 31));
             bars->any_odd = 1;
-            sts64(src + r * pitch, make_uint2(0, 0));
+            sts64(code + src + r * pitch, make_uint2(0, 0));
           }
         }
       };
@@ -556,13 +611,13 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
         from[i] = src + i * rows * pitch;
         to[i] = i * rows * 128 + (((c ^ lr ^ (i * rows)) & 7) << 4);
       }
-      auto convert = [&](uint32_t slot) {
+      auto convert = [&](uint32_t code, uint32_t slot) {  // from, to
 #pragma unroll 1
         for (int r0 = 0; r0 < kRowsW; r0 += kBatch * rows) {
           uint2 v[kBatch];
 #pragma unroll
           for (int i = 0; i < kBatch; ++i)
-            if (mine && r0 + i * rows < kRowsW) v[i] = lds64(from[i] + r0 * pitch);
+            if (mine && r0 + i * rows < kRowsW) v[i] = lds64(from[i] + code + r0 * pitch);
           const uint32_t base = slot + dst + r0 * 128, turn = (r0 & 7) << 4;
 #pragma unroll
           for (int i = 0; i < kBatch; ++i)
@@ -575,18 +630,18 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
       uint64_t* full = h ? bars->v_full : bars->k_full;
 #pragma unroll 1
       for (int k = 0; k < n; ++k) {
-        if (!__all_sync(0xffffffffu, wait(&bars->sc_full[k % kAhead], (k / kAhead) & 1) &&
-                                         wait(&bars->c_full[h], k & 1) &&
-                                         (k < 2 || wait(&empty[k & 1], ((k >> 1) & 1) ^ 1))))
+        if (!__all_sync(0xffffffffu, wait_idle(&bars->sc_full[k % kAhead], (k / kAhead) & 1) &&
+                                         wait_idle(&bars->c_full[h][k % C], (k / C) & 1) &&
+                                         (k < R || wait_idle(&empty[k % R], ((k / R) & 1) ^ 1))))
           break;
         const int2 in = s_in[k % kAhead];
         const int64_t j0 = (int64_t)(U.begin + k) * N;
         if ((in.x & in.y) != (1 << kSegs) - 1 || (h && (j0 < all_lo || j0 + N - 1 > all_hi)))
-          scrub(j0, h ? in.y : in.x);
-        convert((k & 1) * (h ? v_bytes : k_bytes));
+          scrub((k % C) * N * pitch, j0, h ? in.y : in.x);
+        convert((k % C) * N * pitch, (k % R) * (h ? v_bytes : k_bytes));
         fence_proxy_async();
-        arrive_warp(&full[k & 1], lane);
-        if (lane == 0) mbar_arrive(smem_u32(&bars->c_empty[h]));
+        arrive_warp(&full[k % R], lane);
+        if (lane == 0) mbar_arrive(smem_u32(&bars->c_empty[h][k % C]));
       }
     }
     if (P.early) grid_dep_wait();
@@ -599,52 +654,74 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
         const uint32_t id_pv = idesc_f16(false, kRows, P.vhs, true);
         const int steps = P.hs >> 4;
         const uint32_t k_base = smem_u32(k_s), v_base = smem_u32(v_s), q_base = smem_u32(q_s);
-        auto qk = [&](int k, int buf, int tile) {
+        // Descriptors by their lower words (the upper ones stay as they are), with offsets
+        // fixed at compile time in a slab: an MMA takes its thread some 12 cycles to issue
+        // so, and 75 to 100 with offsets worked out step by step.
+        const uint64_t qk_proto = sdesc(q_base, 16, 1024), v_proto = sdesc(v_base, kKBox, 1024);
+        const uint32_t qk_hi = (uint32_t)(qk_proto >> 32), v_hi = (uint32_t)(v_proto >> 32);
+        const uint32_t q_lo = (uint32_t)qk_proto, v_lo = (uint32_t)v_proto;
+        const uint32_t k_lo = (uint32_t)sdesc(k_base, 16, 1024);
+        const uint32_t q_step = q_bytes >> 4, k_step = k_bytes >> 4, v_step = v_bytes >> 4;
+        auto qk = [&](uint32_t slot, int buf, int tile) {
           tc_fence_after();
-          const uint64_t kd = sdesc(k_base + (k & 1) * k_bytes, 16, 1024);
-          const uint64_t qd = sdesc(q_base + tile * q_bytes, 16, 1024);
-#pragma unroll 2
-          for (int i = 0; i < steps; ++i) {
-            const uint32_t in = (uint32_t)(i & 3) * 2;
-            mma_ss(tmem + kColS + buf * N, qd + (uint32_t)(i >> 2) * (kSlab >> 4) + in,
-                   kd + (uint32_t)(i >> 2) * (kKBox >> 4) + in, id_qk, i > 0 ? 1u : 0u);
-          }
+          uint32_t qd = q_lo + tile * q_step, kd = k_lo + slot * k_step, add = 0;
+          const uint32_t d = tmem + kColS + buf * N;
+          int left = steps;
+#pragma unroll 1
+          for (; left >= 4; left -= 4, qd += kSlab >> 4, kd += kKBox >> 4, add = 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_ss_lo(d, qd + 2 * i, kd + 2 * i, qk_hi, id_qk, i > 0 ? 1u : add);
+#pragma unroll 1
+          for (; left > 0; --left, qd += 2, kd += 2, add = 1) mma_ss_lo(d, qd, kd, qk_hi, id_qk, add);
           tc_commit(smem_u32(&bars->s_full[buf]));
         };
-        auto pv = [&](int k, int buf, int tile) {
+        auto pv = [&](uint32_t slot, int buf, int tile, uint32_t add) {
           tc_fence_after();
-          const uint64_t vd = sdesc(v_base + (k & 1) * v_bytes, kKBox, 1024);
+          const uint32_t vd = v_lo + slot * v_step;
+          const uint32_t p = tmem + kColS + buf * N, d = tmem + (QT == 2 ? tile * 128 : 0);
 #pragma unroll
           for (int i = 0; i < kSegs; ++i)
-            mma_ts(tmem + (QT == 2 ? tile * 128 : 0), tmem + kColS + buf * N + i * 8,
-                   vd + (uint64_t)(i * 128), id_pv, (k > 0 || i > 0) ? 1u : 0u);
+            mma_ts_lo(d, p + i * 8, vd + i * 128, v_hi, id_pv, i > 0 ? 1u : add);
+          tc_commit(smem_u32(&bars->pv_done[tile]));
         };
-        // Scores run kLead tiles of a buffer ahead. QT 2: those of both query tiles for one
-        // key tile, then P V and the next scores of one after the other; QT 1: those of
-        // two key tiles. i counts (key tile, buffer) in the order of the products.
-        constexpr int kLead = 2;
-        const int total = QT * n;
+        // Scores run two key tiles ahead: those of tile k + 2 take the buffer of tile k's P,
+        // behind its product.
         bool go = wait(&bars->q_full, 0);
 #pragma unroll 1
-        for (int i = -kLead; i < total && go; ++i) {
-          if (i >= 0) {
-            const int k = QT == 2 ? i >> 1 : i, buf = i & 1;
-            const uint32_t turn = (i >> 1) & 1;  // of the buffer
-            go = wait(&bars->p_full[buf], turn) &&
-                 ((QT == 2 && buf == 1) || wait(&bars->v_full[k & 1], (k >> 1) & 1));
+        for (int k = 0; k < 2 && k < n && go; ++k) {
+          go = wait(&bars->k_full[k], 0);
+          if (!go) break;
+#pragma unroll
+          for (int t = 0; t < QT; ++t) qk(k, t + QT * k, t);
+          tc_commit(smem_u32(&bars->k_empty[k]));
+        }
+        uint32_t v_slot = 0, v_turn = 0, k_slot = 2 % R, k_turn = (2 / R) & 1, p_turn = 0;
+#pragma unroll 1
+        for (int k = 0; k < n && go; ++k) {
+          const int b0 = QT * (k & 1);
+          const bool more = k + 2 < n;
+          go = wait(&bars->v_full[v_slot], v_turn) &&
+               (!more || wait(&bars->k_full[k_slot], k_turn));
+#pragma unroll
+          for (int t = 0; t < QT; ++t) {
+            go = go && wait(&bars->p_full[b0 + t], p_turn);
             if (!go) break;
-            pv(k, buf, QT == 2 ? buf : 0);
-            if (QT == 1) tc_commit(smem_u32(&bars->pv_done));
-            if (QT == 1 || buf == 1) tc_commit(smem_u32(&bars->v_empty[k & 1]));
+            pv(v_slot, b0 + t, t, k > 0 ? 1u : 0u);
+            if (more) qk(k_slot, b0 + t, t);
           }
-          const int s = i + kLead;
-          if (s < total) {
-            const int k = QT == 2 ? s >> 1 : s, buf = s & 1;
-            go = (QT == 2 && buf == 1) || wait(&bars->k_full[k & 1], (k >> 1) & 1);
-            if (!go) break;
-            qk(k, buf, QT == 2 ? buf : 0);
-            if (QT == 1 || buf == 1) tc_commit(smem_u32(&bars->k_empty[k & 1]));
+          if (!go) break;
+          tc_commit(smem_u32(&bars->v_empty[v_slot]));
+          if (more) tc_commit(smem_u32(&bars->k_empty[k_slot]));
+          if (++v_slot == R) {
+            v_slot = 0;
+            v_turn ^= 1;
           }
+          if (++k_slot == R) {
+            k_slot = 0;
+            k_turn ^= 1;
+          }
+          p_turn ^= k & 1;
         }
         tc_commit(smem_u32(&bars->drain));
         drain_wait(smem_u32(&bars->drain), 0, P.err_flags);
@@ -666,7 +743,6 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
       };
       int row = look_up(0);
       if (P.early) grid_dep_wait();
-      const uint32_t codes = smem_u32(v_s + 2 * v_bytes);
       int issued = 0;
 #pragma unroll 1
       for (int k = 0; k < n; ++k) {
@@ -674,9 +750,12 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           const int width = h ? P.vhs : P.hs;
-          const uint32_t dst = codes + (h ? N * P.hs : 0) + lane * A.box * width;
-          const uint32_t bar = smem_u32(&bars->c_full[h]);
-          if (!__all_sync(0xffffffffu, k == 0 || wait(&bars->c_empty[h], (k - 1) & 1))) break;
+          const uint32_t dst = smem_u32(codes) + (h ? C * N * P.hs : 0) + (k % C) * N * width +
+                               lane * A.box * width;
+          const uint32_t bar = smem_u32(&bars->c_full[h][k % C]);
+          if (!__all_sync(0xffffffffu,
+                          k < C || wait_idle(&bars->c_empty[h][k % C], ((k / C) & 1) ^ 1)))
+            break;
           if (lane == 0) mbar_expect_tx(bar, N * width);
           __syncwarp();
           if (lane < nbox) tma_load_3d(dst, h ? &vmap : &kmap, 0, g, row, bar);
@@ -686,8 +765,10 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
         row = next;
       }
       if (*abort && lane == 0) {  // copies may be in flight
-        if (issued > 0) drain_wait(smem_u32(&bars->c_full[0]), ((issued - 1) >> 1) & 1, P.err_flags);
-        if (issued > 1) drain_wait(smem_u32(&bars->c_full[1]), ((issued >> 1) - 1) & 1, P.err_flags);
+        for (int i = max(0, issued - 2 * C); i < issued; ++i) {
+          const int k = i >> 1;
+          drain_wait(smem_u32(&bars->c_full[i & 1][k % C]), (k / C) & 1, P.err_flags);
+        }
       }
       __syncwarp();
     } else if (n > 0 && warp == kScaleWarp) {
@@ -714,15 +795,19 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
         const int ke = scale_exponent(sc0.x), ve = scale_exponent(sc0.y);
         const bool kin = pg0 >= 0 && ke != kNone, vin = pg0 >= 0 && ve != kNone;
         if (pg0 == -1) bars->bad = 1;
-        // (the tile four before is done with once this tile's place is free: see kAhead)
+        // Place k % kAhead held the scales of tile k - kAhead. Once this tile's place in the
+        // ring is free, S of tile k - R is done; it came behind P V of tile k - R - 2, and
+        // that behind the softmax of a tile and its values.
+        static_assert(kAhead >= R + 2, "scales");
         if (!__all_sync(0xffffffffu,
-                        k < 2 || wait(&bars->k_empty[k & 1], ((k >> 1) & 1) ^ 1)))
+                        k < R || wait_idle(&bars->k_empty[k % R], ((k / R) & 1) ^ 1)))
           break;
         const unsigned kb = __ballot_sync(0xffffffffu, kin || pg0 < 0);
         const unsigned vb = __ballot_sync(0xffffffffu, vin || pg0 < 0);
         constexpr unsigned kAll = (1u << kSegs) - 1;
         if (lane < kSegs)
-          s_scale[k % kAhead][lane] = make_float2(kin ? sc0.x : 1.f, vin ? ve : kLeast);
+          s_scale[k % kAhead][lane] = make_float4(kin ? sc0.x : 1.f, vin ? ve : kLeast,
+                                                  pow2(-(vin ? ve : kLeast)), 0.f);
         if (lane == 0) s_in[k % kAhead] = make_int2(kb & kAll, vb & kAll);
         arrive_warp(&bars->sc_full[k % kAhead], lane);
         pg0 = pg1;
@@ -741,7 +826,7 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
 }
 
 // Adds up the parts of a unit: four channels of a row a thread, eight rows a CTA.
-template <int QT, int N>
+template <int QT>
 __global__ void __launch_bounds__(256) quant_join_kernel(const __grid_constant__ PreP A) {
   grid_dep_wait();
   grid_dep_launch();
@@ -751,7 +836,7 @@ __global__ void __launch_bounds__(256) quant_join_kernel(const __grid_constant__
   if (threadIdx.x < 32) {
     PreP whole = A;
     whole.splits = 1;
-    const Unit u = resolve<QT, N>(whole, unit, 0, threadIdx.x);
+    const Unit u = resolve<QT>(whole, unit, 0, threadIdx.x);
     if (threadIdx.x == 0) s_unit = u;
   }
   __syncthreads();
@@ -808,14 +893,15 @@ cudaError_t codes_map(CUtensorMap* map, const void* base, const Geometry& g, int
              : cudaErrorInvalidValue;
 }
 
-template <int QT, int N, bool CAP>
+template <int QT, int R, int C, bool CAP>
 cudaError_t launch(const Geometry& g, const QuantArgs& a, const PreP& A, int64_t ctas) {
   static std::atomic<bool> configured[64];
-  auto kern = quant_prefill_kernel<QT, N, CAP>;
+  auto kern = quant_prefill_kernel<QT, R, C, CAP>;
   const size_t smem = 1024 + (size_t)QT * A.slabs * kSlab +
-                      2 * (size_t)(A.slabs + A.vslabs) * N * 128 + (size_t)N * (g.hs + g.vhs);
+                      (size_t)R * (A.slabs + A.vslabs) * N * 128 + (size_t)C * N * (g.hs + g.vhs);
   cudaError_t e = once_per_device(configured, g.device, [&] {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                225 * 1024);
   });
   if (e != cudaSuccess) return e;
   CUtensorMap kmap, vmap;
@@ -824,7 +910,7 @@ cudaError_t launch(const Geometry& g, const QuantArgs& a, const PreP& A, int64_t
   e = launch_pdl(kern, dim3((unsigned)(ctas * A.splits)), dim3(kThreads), smem, a.stream, kmap, vmap,
                  A);
   if (e != cudaSuccess || A.splits == 1) return e;
-  return launch_pdl(quant_join_kernel<QT, N>, dim3((unsigned)ctas, 8), dim3(256), 0, a.stream, A);
+  return launch_pdl(quant_join_kernel<QT>, dim3((unsigned)ctas, 8), dim3(256), 0, a.stream, A);
 }
 
 // One query tile where two accumulators do not fit in TMEM, or two queries beside
@@ -841,7 +927,7 @@ size_t prefill_workspace(const Geometry& g, int64_t, int64_t) {
 cudaError_t launch_prefill(const Geometry& g, const QuantArgs& a) {
   PreP A{};
   A.R = read_params(g, a);
-  const int qt = query_tiles(g), n = g.hs > 128 || g.vhs > 128 ? 64 : 128;
+  const int qt = query_tiles(g);
   A.tpc = kRows / A.R.grp;
   A.slabs = (g.hs + 63) / 64;
   A.vslabs = (g.vhs + 63) / 64;
@@ -852,7 +938,7 @@ cudaError_t launch_prefill(const Geometry& g, const QuantArgs& a) {
   };
   A.klpr = lanes(g.hs);
   A.vlpr = lanes(g.vhs);
-  A.box = std::min(g.bs, n);
+  A.box = std::min(g.bs, N);
   A.num_slots = (int64_t)g.num_blocks * g.bs;
   A.ws_o = static_cast<float*>(a.workspace);
   A.ws_ml = reinterpret_cast<float2*>(A.ws_o + (size_t)g.num_sms * qt * kRows * g.vhs);
@@ -861,13 +947,14 @@ cudaError_t launch_prefill(const Geometry& g, const QuantArgs& a) {
   const int64_t ctas = units * g.kvh;
   if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
   // parts of four tiles at least, as long as there are SMs
-  const int64_t tiles = ((int64_t)g.max_blocks * g.bs + n - 1) / n;
+  const int64_t tiles = ((int64_t)g.max_blocks * g.bs + N - 1) / N;
   A.splits = (int)std::max<int64_t>(1, std::min<int64_t>(g.num_sms / ctas, tiles / 4));
   const bool cap = g.softcap > 0.f;
-  if (qt == 2 && n == 128)
-    return cap ? launch<2, 128, true>(g, a, A, ctas) : launch<2, 128, false>(g, a, A, ctas);
-  if (qt == 2) return cap ? launch<2, 64, true>(g, a, A, ctas) : launch<2, 64, false>(g, a, A, ctas);
-  return cap ? launch<1, 64, true>(g, a, A, ctas) : launch<1, 64, false>(g, a, A, ctas);
+  if (qt == 2 && g.hs <= 128)
+    return cap ? launch<2, 4, 2, true>(g, a, A, ctas) : launch<2, 4, 2, false>(g, a, A, ctas);
+  if (qt == 2)
+    return cap ? launch<2, 2, 2, true>(g, a, A, ctas) : launch<2, 2, 2, false>(g, a, A, ctas);
+  return cap ? launch<1, 2, 1, true>(g, a, A, ctas) : launch<1, 2, 1, false>(g, a, A, ctas);
 }
 
 }  // namespace quant
