@@ -73,7 +73,7 @@ __device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t par, volatile 
                                            int32_t* err) {
   uint64_t t0 = 0;
   for (uint32_t i = 1; !mbar_try_wait(bar, par); ++i) {
-    if (IDLE) __nanosleep(128);
+    if (IDLE) __nanosleep(256);
     if (i & 63) continue;
     if (*abort) return false;
     const uint64_t t = globaltimer();
@@ -382,25 +382,25 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
       else load_query<__half>(A, U, g, qt, rows, quad, lane, q_t, &mult);
       fence_proxy_async();
       arrive_warp(&bars->q_full, lane);
-      const int64_t pos_r = U.pos + tok0 + row / P.grp;
-      const int64_t last_r = P.cross ? U.pos_hi : min(pos_r, U.pos_hi);
-      const int64_t lo_r = P.window >= 0 ? max((int64_t)0, pos_r - P.window) : 0;
-      const int64_t last0 = U.last0, lo_hi = U.lo_hi;
+      // keys counted from the first tile's first one
+      const int64_t key0 = (int64_t)U.begin * N, pos_r = U.pos + tok0 + row / P.grp;
+      const int last_r = (int)((P.cross ? U.pos_hi : min(pos_r, U.pos_hi)) - key0);
+      const int lo_r = (int)((P.window >= 0 ? max((int64_t)0, pos_r - P.window) : 0) - key0);
+      const int last0 = (int)(U.last0 - key0);
+      const int lo_hi = (int)(U.lo_hi - key0);
       const uint32_t o_addr = lane_addr + (QT == 2 ? qt * 128 : 0);
 #pragma unroll 1
       for (int k = 0; k < n; ++k) {
         const int buf = qt + QT * (k & 1);
         const uint32_t par = (k >> 1) & 1;
         const uint32_t cols = lane_addr + kColS + buf * N;
-        const int64_t j0 = (int64_t)(U.begin + k) * N;
+        const int j0 = k * N;
         const bool edge = j0 < lo_hi || j0 + N - 1 > last0;
-        ok = __all_sync(0xffffffffu, wait(&bars->s_full[buf], par) &&
-                                         wait(&bars->sc_full[k % kAhead], (k / kAhead) & 1));
+        // (S comes behind the conversion of its keys, and that behind the tile's scales)
+        ok = __all_sync(0xffffffffu, wait(&bars->s_full[buf], par));
         if (!ok) break;
         tc_fence_after();
         const float4* scale = s_scale[k % kAhead];
-        const int c0 = (int)max((int64_t)0, min((int64_t)N, lo_r - j0));       // seen columns
-        const int c1 = (int)max((int64_t)-1, min((int64_t)(N - 1), last_r - j0));
         uint32_t x[N / 32][32];
 #pragma unroll
         for (int c = 0; c < N / 32; ++c) tmem_ld32_nowait(cols + c * 32, x[c]);
@@ -409,6 +409,7 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
         for (int c = 0; c < N / 32; ++c) reg_fence(x[c]);
         float top = -INFINITY;
         if (edge) {
+          const int c0 = max(0, lo_r - j0), c1 = max(-1, min(N - 1, last_r - j0));  // seen columns
 #pragma unroll
           for (int c = 0; c < N / 32; ++c) {
             // bits c0 - 32 c .. c1 - 32 c
@@ -622,8 +623,12 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
 #pragma unroll
           for (int i = 0; i < kBatch; ++i)
             if (mine && r0 + i * rows < kRowsW)
-              sts128((base + to[i]) ^ turn, codes2(v[i].x), codes2(v[i].x >> 16), codes2(v[i].y),
-                     codes2(v[i].y >> 16));
+              {
+                uint32_t o[4];
+                codes4(v[i].x, &o[0], &o[1]);
+                codes4(v[i].y, &o[2], &o[3]);
+                sts128((base + to[i]) ^ turn, o[0], o[1], o[2], o[3]);
+              }
         }
       };
       uint64_t* empty = h ? bars->v_empty : bars->k_empty;

@@ -146,5 +146,13 @@ __device__ __forceinline__ uint32_t codes2(uint32_t two) {
   return r;
 }
 
+// Four codes as two words of fp16.
+__device__ __forceinline__ void codes4(uint32_t four, uint32_t* lo, uint32_t* hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+      : "=r"(*lo), "=r"(*hi)
+      : "r"(four));
+}
+
 }  // namespace quant
 }  // namespace pa
