@@ -422,13 +422,12 @@ pa_status read(Phase ph, const pa_quant_params* p, QuantArgs a) {
   if (a.workspace && !aligned(a.workspace, 256))
     return fail(PA_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
   const int64_t nseq = a.seq_end - a.seq_begin;
-  const size_t need = ph == Phase::kDecode ? decode_workspace(g, nseq)
-                                           : prefill_workspace(g, nseq, a.num_tokens);
+  const size_t need = ph == Phase::kDecode ? rows_workspace(g, nseq) : prefill_workspace(g, nseq);
   if (need > 0 && (!a.workspace || a.workspace_bytes < need))
     return fail(PA_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu needed",
                 a.workspace ? a.workspace_bytes : (size_t)0, need);
   a.cross = p->cross;
-  const cudaError_t e = ph == Phase::kDecode ? launch_decode(g, a) : launch_prefill(g, a);
+  const cudaError_t e = ph == Phase::kDecode ? launch_rows(g, a, true) : launch_prefill(g, a);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();  // not left behind for a later call
     return fail(PA_ERR_CUDA, "attention over an 8-bit cache: %s", cudaGetErrorString(e));
@@ -562,9 +561,7 @@ pa_status pa_quant_prefill(const pa_quant_params* p, const void* query, int64_t 
 size_t pa_quant_workspace_size(const pa_quant_params* p, int32_t num_seqs, int64_t num_tokens) {
   Geometry g;
   if (quant::resolve(p, &g) != PA_OK || num_seqs <= 0 || num_tokens <= 0) return 0;
-  const size_t d = quant::decode_workspace(g, num_seqs);
-  const size_t f = quant::prefill_workspace(g, num_seqs, num_tokens);
-  return d > f ? d : f;
+  return quant::prefill_workspace(g, num_seqs);  // (decode's is part of it)
 }
 
 }  // extern "C"

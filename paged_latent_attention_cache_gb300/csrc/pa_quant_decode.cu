@@ -1,24 +1,24 @@
-// Attention over 8-bit caches, decode: one new token per sequence
-// (include/pa_quant.h), bound by HBM.
+// Attention over 8-bit caches for few query rows (include/pa_quant.h): decode, one new
+// token per sequence, and prefill of a few tokens each. Bound by HBM.
 //
-// The line. A unit is a sequence, a kv head and up to 8 NB of its query heads; its
-// visible keys are cut into tiles of 16. All tiles of all units form one line,
-// which is cut into equal parts, one per CTA, whatever the lengths. A CTA's part
-// of a unit is a segment: its warps take the segment's tiles in turn, each with a
-// softmax of its own, and join at the segment's end. A unit that lies in several
+// The line. A unit is a sequence, a kv head and up to 8 NB of its query rows (token x
+// head of the group); its visible keys are cut into tiles of 16. All tiles of all units
+// form one line, which is cut into equal parts, one per CTA, whatever the lengths. A
+// CTA's part of a unit is a segment: its warps take the segment's tiles in turn, each
+// with a softmax of its own, and join at the segment's end. A unit that lies in several
 // parts is joined by quant_combine_kernel.
 //
-// Loads. Every lane copies (cp.async, 16 bytes) just the codes that it will
-// multiply itself into a ring of its own, D tiles ahead and past the ends of
-// segments, so there is no barrier between copies and products, and a tile's
-// pages are looked up a batch of 32 tiles before. Key rows and value rows of a
-// tile are read whole: 8 lanes of 16 bytes for 128 channels.
+// Loads. Every lane copies (cp.async, 16 bytes) just the codes that it will multiply
+// itself into a ring of its own, D tiles ahead and past the ends of segments, so there
+// is no barrier between copies and products, and a tile's pages are looked up a batch
+// of 32 tiles before. Key rows and value rows of a tile are read whole: 8 lanes of 16
+// bytes for 128 channels.
 //
-// Products. mma.sync m16n8k16, keys (then value channels) as the 16 rows and the
-// heads as the 8 columns: with rows of heads, as the usual order has it, a group of
-// eight or fewer would fill half of a product. The order of the 16 keys and of the
-// channels inside the products is chosen so that what a lane has copied is what its
-// registers of A hold: lane (g, t) = (lane / 4, lane % 4) owns
+// Products. mma.sync m16n8k16, keys (then value channels) as the 16 rows and the query
+// rows as the 8 columns: the other way round a group of eight or fewer would fill half
+// of a product. The order of the 16 keys and of the channels inside the products is
+// chosen so that what a lane has copied is what its registers of A hold: lane (g, t) =
+// (lane / 4, lane % 4) owns
 //   of key slot g and g + 8 (keys kappa = 4 (g / 2) + g % 2, and + 2): pieces of 16
 //     channels t, t + 4, ..; a word of 4 codes is one k step's A registers
 //   of the values of keys 4 t .. 4 t + 3: piece g (and g + 8); a byte of each of two
@@ -33,41 +33,46 @@ namespace pa {
 namespace quant {
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kTile = 16;
-constexpr size_t kSmemMax = 225 * 1024;
 
 struct DecP {
   ReadP R;
-  float4* ws_o;     // [2 CTAs][8 VP NB][32] accumulators as the lanes hold them
-  float2* ws_ml;    // [2 CTAs][8 NB] maximum (log2 domain), sum
-  int64_t* ws_plan; // [nseq + 1] tiles before each sequence, then the tiles of a part
-  int units;        // per sequence
-  int chunks;       // units per kv head
+  float4* ws_o;      // [2 CTAs][8 VP NB][32] accumulators as the lanes hold them
+  float2* ws_ml;     // [2 CTAs][8 NB] maximum (log2 domain), sum
+  int64_t* ws_line;  // [nseq + 1] tiles of the line before each sequence, then those of a part
+  int32_t* ws_units; // [nseq + 1] units before each sequence, then all
+  int decode;        // one token per sequence, others are told
+  int rows;          // 8 NB
   int min_part;
 };
 
-struct Span {  // the tiles that a sequence's token sees
-  int64_t lo, last, t;  // first and last key, token
-  int tiles, first;     // (first tile)
-  int err;              // PA_DEVERR_* that keeps it from being read, or 0
-  bool rows;            // it has a row of out
+struct Span {  // a sequence's tokens and the tiles that they see
+  int64_t pos, hi, lo, t;  // position of the first token, last and first key, first token
+  int q, tiles, first;     // tokens, tiles, first tile
+  int chunks;              // units per kv head
+  int err;                 // PA_DEVERR_* that keeps it from being read, or 0
+  bool rows;               // it has rows of out
 };
-__device__ __forceinline__ Span span_of(const ReadP& P, int b) {
+__device__ __forceinline__ Span span_of(const DecP& A, int b) {
+  const ReadP& P = A.R;
   const int64_t c0 = P.cumseq[P.seq_begin + b], c1 = P.cumseq[P.seq_begin + b + 1];
-  const int64_t past = P.past[P.seq_begin + b];
+  const int64_t past = P.past[P.seq_begin + b], q = c1 - c0;
   Span s;
   s.t = c0;
-  s.last = P.cross ? past - 1 : past;
-  s.lo = P.window >= 0 ? max((int64_t)0, s.last - P.window) : 0;
-  s.rows = c1 - c0 == 1 && c0 >= 0 && c0 < P.num_tokens;
-  s.err = c1 - c0 != 1                                                ? PA_DEVERR_DECODE_QLEN
-          : !s.rows                                                   ? PA_DEVERR_CUMSEQ
-          : past < 0 || s.last >= (int64_t)P.max_blocks * P.bs        ? PA_DEVERR_CONTEXT
-          : P.rd > 0 && s.last >= P.cos_rows                          ? PA_DEVERR_POSITION
-                                                                      : 0;
+  s.q = (int)max((int64_t)0, q);
+  s.pos = past;
+  s.hi = P.cross ? past - 1 : past + q - 1;
+  s.lo = P.window >= 0 ? max((int64_t)0, past - P.window) : 0;
+  s.rows = q > 0 && c0 >= 0 && c1 <= P.num_tokens && (q == 1 || !A.decode);
+  s.err = A.decode && q != 1                                     ? PA_DEVERR_DECODE_QLEN
+          : q < 0 || (q > 0 && !s.rows)                          ? PA_DEVERR_CUMSEQ
+          : q > 0 && (past < 0 || s.hi >= (int64_t)P.max_blocks * P.bs) ? PA_DEVERR_CONTEXT
+          : q > 0 && P.rd > 0 && s.hi >= P.cos_rows              ? PA_DEVERR_POSITION
+                                                                 : 0;
   s.first = (int)(s.lo / kTile);
-  s.tiles = s.err || s.last < s.lo ? 0 : (int)(s.last / kTile) - s.first + 1;
+  s.tiles = s.err || q <= 0 || s.hi < s.lo ? 0 : (int)(s.hi / kTile) - s.first + 1;
+  s.chunks = s.tiles ? (s.q * P.grp + A.rows - 1) / A.rows : 0;
   return s;
 }
 
@@ -75,27 +80,34 @@ __device__ __forceinline__ Span span_of(const ReadP& P, int b) {
 // and the line's end for this CTA.
 struct Walk {
   int64_t x, end, start;  // (start: of sequence b)
-  int b, tiles, first;
-  int unit, from, len;    // the segment: unit, first tile (in the cache), tiles
+  int b, tiles, first, chunks;
+  int g, chunk;           // the segment's unit
+  int from, len;          // first tile (in the cache), tiles
   __device__ __forceinline__ bool valid() const { return x < end; }
+  __device__ __forceinline__ void enter(const DecP& A, int seq, int64_t at) {
+    const Span s = span_of(A, seq);
+    b = seq;
+    start = at;
+    tiles = s.tiles;
+    first = s.first;
+    chunks = s.chunks;
+  }
   __device__ __forceinline__ void segment() {
-    if (!valid()) return;
     const uint64_t off = (uint64_t)(x - start);
-    unit = off >> 32 ? (int)(off / (uint32_t)tiles) : (int)((uint32_t)off / (uint32_t)tiles);
+    const int unit = off >> 32 ? (int)(off / (uint32_t)tiles) : (int)((uint32_t)off / (uint32_t)tiles);
     const int in = (int)(off - (uint64_t)unit * tiles);
+    g = unit / chunks;
+    chunk = unit - g * chunks;
     from = first + in;
     len = (int)min((int64_t)(tiles - in), end - x);
   }
   __device__ __forceinline__ void next(const DecP& A) {
     x += len;
     if (!valid()) return;
-    if (x == start + (int64_t)tiles * A.units) {
-      start = x;
-      do {
-        const Span s = span_of(A.R, ++b);
-        tiles = s.tiles;
-        first = s.first;
-      } while (tiles == 0);
+    if (x == start + (int64_t)tiles * A.R.kvh * chunks) {
+      int seq = b;
+      do enter(A, ++seq, x);
+      while (tiles == 0);
     }
     segment();
   }
@@ -114,10 +126,9 @@ __device__ __forceinline__ uint32_t transposed(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-// 16 bytes into shared memory; zeros where there is nothing to read.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(there ? 16 : 0)
+// 16 bytes into shared memory, zeros behind the first `bytes`.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
 
@@ -125,50 +136,61 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-// Accumulators i0..i0 + 3 of a head block (see the products): eight channels of two
-// heads, times inv, to out. `row`: the unit's first row of out.
+// Accumulators i0..i0 + 3 of a block of query rows (see the products): eight channels
+// of rows r and r + 1 of the unit, times inv, to out.
 template <typename F>
-__device__ __forceinline__ void store_heads(const ReadP& P, int64_t row, int nh, int h, int gq,
-                                            int i0, bool zero, const float (&inv)[2], F&& acc) {
+__device__ __forceinline__ void store_rows(const ReadP& P, const Span& sp, int g, int r0, int nr,
+                                           int r, int gq, int i0, bool zero, const float (&inv)[2],
+                                           F&& acc) {
   const int ch = 16 * (gq + (i0 & ~7)) + 2 * (i0 & 7);
   if (ch >= P.vhs) return;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    if (h + e >= nh) continue;
+    if (r + e >= nr) continue;
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       w[k] = zero ? 0 : pack_out(P, acc(k, e) * inv[e], acc(k, e + 2) * inv[e]);
-    *reinterpret_cast<uint4*>(reinterpret_cast<__half*>(P.out) + (row + h + e) * P.vhs + ch) =
+    const int tok = (r0 + r + e) / P.grp, h = g * P.grp + (r0 + r + e) - tok * P.grp;
+    *reinterpret_cast<uint4*>(reinterpret_cast<__half*>(P.out) +
+                              ((sp.t + tok) * P.H + h) * P.vhs + ch) =
         make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
-// What the sink of head h0 + h adds to a sum with maximum m.
-__device__ __forceinline__ float sink_part(const ReadP& P, int h0, int h, int nh, float m) {
-  return P.head_sink && h < nh ? ex2(to_f32(P, P.head_sink, h0 + h) * kLog2e - m + kShift) : 0.f;
+// 1 / sum of row r of a unit, whose maximum is m, with its head's sink. (A row that
+// saw nothing, m -inf and sum 0, answers zeros: 0 times 1.)
+__device__ __forceinline__ float inverse(const ReadP& P, int g, int r0, int r, int nr, float m,
+                                         float sum) {
+  if (m == -INFINITY && sum == 0.f) return 1.f;
+  if (P.head_sink && r < nr)
+    sum += ex2(to_f32(P, P.head_sink, g * P.grp + (r0 + r) % P.grp) * kLog2e - m + kShift);
+  return 1.f / sum;
 }
 
-// Shared memory of a CTA behind the rings: the query and the joining buffers.
+// CTAs per SM and the shared memory of one: rings, query, joining buffers. Twelve
+// warps an SM where the registers allow it: with eight (one CTA of 255 registers a
+// thread) 32 sequences of 1024 to 8192 keys (32 heads over 8, 128 / 128) took 104 us.
 template <int KP, int VP, int NB>
 struct Shape {
+  static constexpr int kCtas = VP * NB > 2 || KP * NB > 4 || KP * VP > 4 ? 2 : 3;
   static constexpr int kStage = (2 * KP + 4 * VP) * 512;  // bytes of a warp's tile
   static constexpr int kRow = KP * 64 + 8;                // halves of a query row
   static constexpr int kAcc = 8 * VP * NB;                // float4 accumulators of a lane
   static constexpr int kQ = 8 * NB * kRow * 2;
-  static constexpr int kJoin = (kWarps / 2) * (kAcc * 512 + NB * 128);
-  static constexpr int kLeft = (int)kSmemMax - kQ - kJoin - 8 * NB * 4 - 1024;
+  static constexpr int kJoin = (kWarps / 2) * (kAcc * 512 + NB * 64);
+  static constexpr int kLeft = 227 * 1024 / kCtas - 2048 - kQ - kJoin;
   static constexpr int kFit = kLeft / (kWarps * (kStage + 8));
   static constexpr int D = kFit > 8 ? 8 : kFit;
-  static constexpr int kSmem = kWarps * D * (kStage + 8) + kQ + kJoin + 8 * NB * 4;
+  static constexpr int kSmem = kWarps * D * (kStage + 8) + kQ + kJoin;
   static_assert(D >= 2, "ring");
 };
 
 template <int KP, int VP, int NB>
-__global__ void __launch_bounds__(kThreads, 1)
-quant_decode_kernel(const __grid_constant__ DecP A) {
+__global__ void __launch_bounds__(kThreads, Shape<KP, VP, NB>::kCtas)
+quant_rows_kernel(const __grid_constant__ DecP A) {
   using S = Shape<KP, VP, NB>;
-  constexpr int D = S::D;
+  constexpr int D = S::D, R = 8 * NB;
   const ReadP& P = A.R;
   extern __shared__ __align__(16) uint8_t smem[];
   uint8_t* ring = smem;
@@ -176,8 +198,9 @@ quant_decode_kernel(const __grid_constant__ DecP A) {
   __half* s_q = reinterpret_cast<__half*>(reinterpret_cast<uint8_t*>(meta) + kWarps * D * 8);
   float4* join_o = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(s_q) + S::kQ);
   float2* join_ml = reinterpret_cast<float2*>(join_o + (kWarps / 2) * S::kAcc * 32);
-  float* s_mult = reinterpret_cast<float*>(join_ml + (kWarps / 2) * NB * 16);
+  __shared__ float s_mult[R];
   __shared__ int64_t s_scan[kWarps];
+  __shared__ int s_scan_u[kWarps];
   __shared__ int64_t s_hit[2];  // sequence of this CTA's first tile, tiles before it
   __shared__ int s_bad;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -185,91 +208,128 @@ quant_decode_kernel(const __grid_constant__ DecP A) {
 
   if (!P.early) grid_dep_wait();
 
-  // ---- the plan: tiles before each sequence (a prefix sum, 256 sequences a round)
-  int64_t carry = 0, my_start = 0;
-  int mine = 0;
-  if (tid == 0) s_hit[0] = -1;
+  // ---- the plan: tiles and units before each sequence (prefix sums, 128 sequences a
+  // round)
+  int64_t carry = 0, my_start = 0, mine = 0;
+  int carry_u = 0;
   auto round = [&](int base) {  // start of sequence base + tid, and the carry behind the round
     const int b = base + tid;
-    mine = b < P.nseq ? span_of(P, b).tiles : 0;
+    int units = 0;
+    mine = 0;
+    if (b < P.nseq) {
+      const Span s = span_of(A, b);
+      units = s.chunks * P.kvh;
+      mine = (int64_t)s.tiles * units;
+    }
     int64_t v = mine;
+    int w = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += y;
+      const int z = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) {
+        v += y;
+        w += z;
+      }
     }
     __syncthreads();
-    if (lane == 31) s_scan[warp] = v;
+    if (lane == 31) {
+      s_scan[warp] = v;
+      s_scan_u[warp] = w;
+    }
     __syncthreads();
     int64_t before = carry;
+    int before_u = carry_u;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += s_scan[w];
-      carry += s_scan[w];
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) {
+        before += s_scan[i];
+        before_u += s_scan_u[i];
+      }
+      carry += s_scan[i];
+      carry_u += s_scan_u[i];
     }
     my_start = before + v - mine;
-    if (blockIdx.x == 0 && b < P.nseq) A.ws_plan[b] = my_start;
+    if (blockIdx.x == 0 && b < P.nseq) {
+      A.ws_line[b] = my_start;
+      A.ws_units[b] = before_u + w - units;
+    }
   };
+#pragma unroll 1
   for (int base = 0; base < P.nseq; base += kThreads) round(base);
-  const int64_t total = carry * A.units;
+  const int64_t total = carry;
   const int64_t part = max((int64_t)A.min_part, (total + gridDim.x - 1) / gridDim.x);
-  if (blockIdx.x == 0 && tid == 0) A.ws_plan[P.nseq] = part;
+  if (blockIdx.x == 0 && tid == 0) {
+    A.ws_line[P.nseq] = part;
+    A.ws_units[P.nseq] = carry_u;
+  }
   Walk W;
   W.x = min(total, blockIdx.x * part);
   W.end = min(total, W.x + part);
+#pragma unroll 1
   for (int base = 0; base < P.nseq && W.x < W.end; base += kThreads) {
     if (P.nseq > kThreads) {
-      if (base == 0) carry = 0;
+      if (base == 0) carry = carry_u = 0;
       round(base);
     }
-    if (mine > 0 && my_start * A.units <= W.x && W.x < (my_start + mine) * A.units) {
+    if (mine > 0 && my_start <= W.x && W.x < my_start + mine) {
       s_hit[0] = base + tid;
       s_hit[1] = my_start;
     }
   }
   __syncthreads();
   if (W.valid()) {
-    W.b = (int)s_hit[0];
-    W.start = s_hit[1] * A.units;
-    const Span s = span_of(P, W.b);
-    W.tiles = s.tiles;
-    W.first = s.first;
+    W.enter(A, (int)s_hit[0], s_hit[1]);
     W.segment();
   }
   if (P.early) grid_dep_wait();
 
   // ---- this warp's copies: a walk of its own ahead of the products
   Walk C = W;
-  int ct = 0;        // next tile of its segment (counting the warp's own)
+  int ct = 0, own = 0;          // next tile of its segment (counting the warp's own), all of them
   int page0 = 0, page1 = 0;     // of this batch's and the next batch's tiles, a lane each
   float2 sc0 = make_float2(0.f, 0.f), sc1 = sc0;
-  const int64_t krow = (int64_t)P.kvh * P.hs, vrow = (int64_t)P.kvh * P.vhs;
+  const int krow = P.kvh * P.hs, vrow = P.kvh * P.vhs;  // bytes
   const int npk = P.hs >> 4, npv = P.vhs >> 4;
-  auto own_tiles = [&](const Walk& w) {
-    return w.len > warp ? (w.len - warp + kWarps - 1) / kWarps : 0;
-  };
+  const int kappa = 4 * (gq >> 1) + (gq & 1);
+  uint8_t* my_ring = ring + warp * D * S::kStage + lane * 16;
+  // pieces of a key row that do not exist stay zeros (those of values are not stored)
+#pragma unroll
+  for (int i = 0; i < KP; ++i)
+    if (tq + 4 * i >= npk)
+#pragma unroll 1
+      for (int d = 0; d < D; ++d) {
+        *reinterpret_cast<uint4*>(my_ring + d * S::kStage + (2 * i) * 512) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(my_ring + d * S::kStage + (2 * i + 1) * 512) =
+            make_uint4(0, 0, 0, 0);
+      }
+  const uint8_t *k_lane = nullptr, *v_lane = nullptr;  // of the walk's kv head
   auto look_up = [&](int k) {  // the page of the warp's tile k + lane
     const int64_t key = (int64_t)(C.from + warp + (k + lane) * kWarps) * kTile;
-    return k + lane < own_tiles(C)
+    return k + lane < own
                ? P.block_table[(int64_t)(P.seq_begin + C.b) * P.max_blocks + (key >> P.sh)]
                : 0;
   };
   auto scale_at = [&](int page) {
-    return page >= 0 && page < P.num_blocks
-               ? P.scales[(int64_t)page * P.kvh + C.unit / A.chunks]
-               : make_float2(0.f, 0.f);
+    return page >= 0 && page < P.num_blocks ? P.scales[(int64_t)page * P.kvh + C.g]
+                                            : make_float2(0.f, 0.f);
   };
-  auto enter = [&]() {  // the first segment from here on with a tile of this warp
-    while (C.valid() && own_tiles(C) == 0) C.next(A);
+  auto begin = [&]() {  // the first segment from here on with a tile of this warp
+    own = 0;
+    while (C.valid()) {
+      own = C.len > warp ? (C.len - warp + kWarps - 1) / kWarps : 0;
+      if (own) break;
+      C.next(A);
+    }
     ct = 0;
     if (C.valid()) {
       page0 = look_up(0);
       sc0 = scale_at(page0);
+      k_lane = P.key_cache + (int64_t)kappa * krow + C.g * P.hs + tq * 16;
+      v_lane = P.value_cache + (int64_t)(4 * tq) * vrow + C.g * P.vhs + gq * 16;
     }
   };
   int put = 0;
-  const int kappa = 4 * (gq >> 1) + (gq & 1);
-  uint8_t* my_ring = ring + warp * D * S::kStage + lane * 16;
   auto produce = [&]() {
     if (C.valid()) {
       const int k = ct & 31;
@@ -282,32 +342,30 @@ quant_decode_kernel(const __grid_constant__ DecP A) {
       const bool kin = good && ke != kNone, vin = good && ve != kNone;
       const int tile = C.from + warp + ct * kWarps;
       const int64_t row = (good ? (int64_t)page << P.sh : 0) + ((tile * kTile) & (P.bs - 1));
-      const int g = C.unit / A.chunks;
       const uint32_t dst = smem_u32(my_ring + put * S::kStage);
-      const uint8_t* kr = P.key_cache + (row + kappa) * krow + g * P.hs;
-      const uint8_t* vr = P.value_cache + (row + 4 * tq) * vrow + g * P.vhs;
+      const uint8_t* kr = k_lane + row * krow;
+      const uint8_t* vr = v_lane + row * vrow;
+      const uint32_t kn = kin ? 16 : 0, vn = vin ? 16 : 0;
 #pragma unroll
       for (int i = 0; i < KP; ++i) {
-        const int piece = tq + 4 * i;
-        const bool in = kin && piece < npk;
-        const uint8_t* src = piece < npk ? kr + piece * 16 : kr;
-        copy16(dst + (2 * i) * 512, src, in);
-        copy16(dst + (2 * i + 1) * 512, src + 2 * krow, in);
+        if (tq + 4 * i < npk) {
+          copy16(dst + (2 * i) * 512, kr + 64 * i, kn);
+          copy16(dst + (2 * i + 1) * 512, kr + 64 * i + 2 * krow, kn);
+        }
       }
 #pragma unroll
       for (int i = 0; i < VP; ++i) {
-        const int piece = gq + 8 * i;
-        if (piece < npv) {
+        if (gq + 8 * i < npv) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            copy16(dst + (2 * KP + 4 * i + j) * 512, vr + j * vrow + piece * 16, vin);
+            copy16(dst + (2 * KP + 4 * i + j) * 512, vr + 128 * i + j * vrow, vn);
         }
       }
       if (lane == 0)
         meta[warp * D + put] = make_float2(good ? (kin ? ks : 1.f) : NAN, vin ? (float)ve : kLeast);
-      if (++ct == own_tiles(C)) {
+      if (++ct == own) {
         C.next(A);
-        enter();
+        begin();
       } else if ((ct & 31) == 0) {
         page0 = page1;
         sc0 = sc1;
@@ -316,7 +374,7 @@ quant_decode_kernel(const __grid_constant__ DecP A) {
     asm volatile("cp.async.commit_group;" ::: "memory");
     if (++put == D) put = 0;
   };
-  enter();
+  begin();
 #pragma unroll 1
   for (int i = 0; i < D; ++i) produce();
   int get = 0;
@@ -324,18 +382,19 @@ quant_decode_kernel(const __grid_constant__ DecP A) {
   // ---- segments
 #pragma unroll 1
   while (W.valid()) {
-    const int g = W.unit / A.chunks, h0 = (W.unit - g * A.chunks) * 8 * NB;
-    const int nh = min(8 * NB, P.grp - h0);
-    const Span sp = span_of(P, W.b);
-    const int64_t qrow = sp.t * P.H + g * P.grp + h0;
+    const int r0 = W.chunk * R;
+    const Span sp = span_of(A, W.b);
+    const int nr = min(R, sp.q * P.grp - r0);
     __syncthreads();
     if (tid == 0) s_bad = 0;
-    for (int r = warp; r < 8 * NB; r += kWarps) {
+    for (int r = warp; r < R; r += kWarps) {
       float x[8], back = 0.f;
       uint4 h = make_uint4(0, 0, 0, 0);
-      if (r < nh) {
-        if (P.bf16) query_row8<__nv_bfloat16>(P, qrow + r, sp.last, x);
-        else query_row8<__half>(P, qrow + r, sp.last, x);
+      if (r < nr) {
+        const int tok = (r0 + r) / P.grp, head = W.g * P.grp + (r0 + r) - tok * P.grp;
+        const int64_t i = (sp.t + tok) * P.H + head;
+        if (P.bf16) query_row8<__nv_bfloat16>(P, i, sp.pos + tok, x);
+        else query_row8<__half>(P, i, sp.pos + tok, x);
         back = scaled_row8(x, &h);
       }
       if (lane * 8 < KP * 64) *reinterpret_cast<uint4*>(s_q + r * S::kRow + lane * 8) = h;
@@ -373,13 +432,18 @@ quant_decode_kernel(const __grid_constant__ DecP A) {
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][nb][e] = 0.f;
+    // keys that all rows of the unit see, counted from the segment's first
+    const int64_t key0 = (int64_t)W.from * kTile;
+    const int tok_lo = r0 / P.grp, tok_hi = (r0 + nr - 1) / P.grp;
+    const int all_hi = (int)((P.cross ? sp.hi : sp.pos + tok_lo) - key0);
+    const int all_lo = (int)((P.window >= 0 ? max((int64_t)0, sp.pos + tok_hi - P.window) : 0) - key0);
 
     bool bad = false;
 #pragma unroll 1
-    for (int tile = W.from + warp; tile < W.from + W.len; tile += kWarps) {
+    for (int tile = warp; tile < W.len; tile += kWarps) {
       asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
       __syncwarp();
-      const uint4* at = reinterpret_cast<const uint4*>(my_ring + get * S::kStage);
+      uint4* at = reinterpret_cast<uint4*>(my_ring + get * S::kStage);
       const float2 mt = meta[warp * D + get];
       if (++get == D) get = 0;
       const float ks = mt.x, ev = mt.y;
@@ -391,8 +455,7 @@ quant_decode_kernel(const __grid_constant__ DecP A) {
         for (int e = 0; e < 4; ++e) c[nb][e] = 0.f;
 #pragma unroll
       for (int i = 0; i < KP; ++i) {
-        const uint4 r0 = at[(2 * i) * 32], r1 = at[(2 * i + 1) * 32];
-        const uint32_t a[4] = {r0.x, r0.y, r0.z, r0.w}, b[4] = {r1.x, r1.y, r1.z, r1.w};
+        const uint4 u0 = at[(2 * i) * 32], u1 = at[(2 * i + 1) * 32];
         uint32_t f[NB][8];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -405,29 +468,58 @@ quant_decode_kernel(const __grid_constant__ DecP A) {
         }
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          const uint32_t a0 = codes2(a[s]), a2 = codes2(a[s] >> 16);
-          const uint32_t a1 = codes2(b[s]), a3 = codes2(b[s] >> 16);
+          uint32_t a0, a1, a2, a3;
+          codes4(word(u0, s), &a0, &a2);
+          codes4(word(u1, s), &a1, &a3);
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) mma(c[nb], a0, a1, a2, a3, f[nb][2 * s], f[nb][2 * s + 1]);
         }
       }
-      // scores of keys kappa (c[0], c[1]) and kappa + 2 for heads 2 t and 2 t + 1
-      const int64_t j0 = (int64_t)tile * kTile;
-      const bool edge = j0 < sp.lo || j0 + kTile - 1 > sp.last;
-      bool rise = false;
+      // scores of keys kappa (c[0], c[1]) and kappa + 2 for rows 2 t and 2 t + 1
+      const int j0 = tile * kTile;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float f = ks * mult[nb][e & 1];
-          float y = P.cap_in > 0.f ? capped(P, c[nb][e] * f) + ev : fmaf(c[nb][e], f, ev);
-          if (edge) {
-            const int64_t j = j0 + kappa + (e & 2);
-            if (j < sp.lo || j > sp.last) y = -INFINITY;
-          }
-          c[nb][e] = y;
-          rise |= y > m[nb][e & 1] + kLazy;
+          c[nb][e] = P.cap_in > 0.f ? capped(P, c[nb][e] * f) + ev : fmaf(c[nb][e], f, ev);
         }
+      if (j0 < all_lo || j0 + kTile - 1 > all_hi) {
+        // an end of what the rows see: unseen values become zeros (0 times NaN is NaN),
+        // and a NaN among values that only some rows see goes over to their scores
+        const int hi = (int)(sp.hi - key0), lo = (int)(sp.lo - key0);
+        uint32_t odd = 0;
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          const int key = j0 + 4 * tq + j;
+          const bool none = key < lo || key > hi;
+#pragma unroll
+          for (int i = 0; i < VP; ++i) {
+            uint4& v = at[(2 * KP + 4 * i + j) * 32];
+            const bool nan = (nan_codes(v.x) | nan_codes(v.y) | nan_codes(v.z) | nan_codes(v.w)) &&
+                             gq + 8 * i < npv;
+            if (none || nan) v = make_uint4(0, 0, 0, 0);
+            if (nan && !none) odd |= 1u << (4 * tq + j);
+          }
+        }
+        odd = __reduce_or_sync(0xffffffffu, odd);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = kappa + (e & 2), tok = (r0 + nb * 8 + 2 * tq + (e & 1)) / P.grp;
+            const int64_t pos = sp.pos + tok - key0;
+            if (odd >> key & 1u) c[nb][e] = NAN;
+            if (j0 + key > (P.cross ? (int64_t)hi : pos) ||
+                (P.window >= 0 && pos - (j0 + key) > P.window))
+              c[nb][e] = -INFINITY;
+          }
+      }
+      bool rise = false;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) rise |= fmaxf(c[nb][e], c[nb][e + 2]) > m[nb][e] + kLazy;
       if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
@@ -450,14 +542,14 @@ quant_decode_kernel(const __grid_constant__ DecP A) {
           }
       }
       uint32_t pb[NB][2];
-      const float out_of = ex2(-ev);  // (a whole number: exact)
+      const float out_of = pow2(-(int)ev);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         float p[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float mm = m[nb][e & 1];
-          p[e] = ex2(c[nb][e] - (mm == -INFINITY ? 0.f : mm) + kShift);
+          p[e] = ex2(c[nb][e] - ((mm == -INFINITY ? 0.f : mm) - kShift));
         }
         l[nb][0] = fmaf(p[0] + p[2], out_of, l[nb][0]);
         l[nb][1] = fmaf(p[1] + p[3], out_of, l[nb][1]);
@@ -468,21 +560,18 @@ quant_decode_kernel(const __grid_constant__ DecP A) {
       for (int i = 0; i < VP; ++i) {
         uint4 v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[j] = at[(2 * KP + 4 * i + j) * 32];
-          if (edge && (j0 + 4 * tq + j < sp.lo || j0 + 4 * tq + j > sp.last))
-            v[j] = make_uint4(0, 0, 0, 0);  // (0 times NaN is NaN)
-        }
+        for (int j = 0; j < 4; ++j) v[j] = at[(2 * KP + 4 * i + j) * 32];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           const uint32_t w0 = word(v[0], s), w1 = word(v[1], s), w2 = word(v[2], s), w3 = word(v[3], s);
-          const uint32_t x01 = __byte_perm(w0, w1, 0x5140), y01 = __byte_perm(w0, w1, 0x7362);
-          const uint32_t x23 = __byte_perm(w2, w3, 0x5140), y23 = __byte_perm(w2, w3, 0x7362);
-          uint32_t a0 = codes2(x01), a1 = codes2(x01 >> 16), a2 = codes2(x23), a3 = codes2(x23 >> 16);
+          uint32_t a0, a1, a2, a3;
+          codes4(__byte_perm(w0, w1, 0x5140), &a0, &a1);
+          codes4(__byte_perm(w2, w3, 0x5140), &a2, &a3);
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
             mma(acc[i * 8 + 2 * s][nb], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
-          a0 = codes2(y01), a1 = codes2(y01 >> 16), a2 = codes2(y23), a3 = codes2(y23 >> 16);
+          codes4(__byte_perm(w0, w1, 0x7362), &a0, &a1);
+          codes4(__byte_perm(w2, w3, 0x7362), &a2, &a3);
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
             mma(acc[i * 8 + 2 * s + 1][nb], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
@@ -515,7 +604,7 @@ quant_decode_kernel(const __grid_constant__ DecP A) {
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              join_ml[(warp - n) * NB * 8 + nb * 8 + 2 * tq + e] = make_float2(m[nb][e], l[nb][e]);
+              join_ml[(warp - n) * R + nb * 8 + 2 * tq + e] = make_float2(m[nb][e], l[nb][e]);
         }
       }
       __syncthreads();
@@ -525,12 +614,13 @@ quant_decode_kernel(const __grid_constant__ DecP A) {
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float2 o = join_ml[warp * NB * 8 + nb * 8 + 2 * tq + e];
+            const float2 o = join_ml[warp * R + nb * 8 + 2 * tq + e];
             const float t = fmaxf(m[nb][e], o.x), base = t == -INFINITY ? 0.f : t;
             fa[nb][e] = ex2(m[nb][e] - base);
             fb[nb][e] = ex2(o.x - base);
-            m[nb][e] = t;
+            // (a row of NaN scores keeps maximum -inf: its sum has to stay NaN)
             l[nb][e] = l[nb][e] * fa[nb][e] + o.y * fb[nb][e];
+            m[nb][e] = t;
           }
 #pragma unroll
         for (int i = 0; i < 8 * VP; ++i)
@@ -553,14 +643,14 @@ quant_decode_kernel(const __grid_constant__ DecP A) {
           float inv[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            inv[e] = 1.f / (l[nb][e] + sink_part(P, g * P.grp + h0, nb * 8 + 2 * tq + e, nh, m[nb][e]));
+            inv[e] = inverse(P, W.g, r0, nb * 8 + 2 * tq + e, nr, m[nb][e], l[nb][e]);
 #pragma unroll
           for (int i = 0; i < 8 * VP; i += 4)
-            store_heads(P, qrow, nh, nb * 8 + 2 * tq, gq, i, any_bad, inv,
-                        [&](int k, int e) { return acc[i + k][nb][e]; });
+            store_rows(P, sp, W.g, r0, nr, nb * 8 + 2 * tq, gq, i, any_bad, inv,
+                       [&](int k, int e) { return acc[i + k][nb][e]; });
         }
       } else {
-        // the first part that starts in this CTA, or one behind another's end
+        // the first segment of this CTA's part, or one behind another's end
         const int64_t slot = 2 * (int64_t)blockIdx.x + (W.x > blockIdx.x * part ? 1 : 0);
 #pragma unroll
         for (int i = 0; i < 8 * VP; ++i)
@@ -573,7 +663,7 @@ quant_decode_kernel(const __grid_constant__ DecP A) {
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              A.ws_ml[slot * 8 * NB + nb * 8 + 2 * tq + e] =
+              A.ws_ml[slot * R + nb * 8 + 2 * tq + e] =
                   make_float2(any_bad ? NAN : m[nb][e], l[nb][e]);
         }
       }
@@ -583,33 +673,35 @@ quant_decode_kernel(const __grid_constant__ DecP A) {
   grid_dep_launch();
   // sequences without tiles: told, and zeros
   for (int b = blockIdx.x; b < P.nseq; b += gridDim.x) {
-    const Span s = span_of(P, b);
+    const Span s = span_of(A, b);
     if (s.err && tid == 0) raise_flag(P.err_flags, s.err);
     if (s.tiles == 0 && s.rows) {
       uint32_t* dst = reinterpret_cast<uint32_t*>(P.out) + s.t * P.H * P.vhs / 2;
-      for (int i = tid; i < P.H * P.vhs / 2; i += kThreads) dst[i] = 0;
+      const int64_t n = (int64_t)s.q * P.H * P.vhs / 2;
+      for (int64_t i = tid; i < n; i += kThreads) dst[i] = 0;
     }
   }
 }
 
-// Joins the parts of a unit: a warp for four accumulators of a head block.
+// Joins the parts of a unit: a warp for four accumulators of a block of rows.
 template <int VP, int NB>
 __global__ void __launch_bounds__(64 * VP * NB)
 quant_combine_kernel(const __grid_constant__ DecP A) {
   grid_dep_wait();
   grid_dep_launch();
-  constexpr int kAcc = 8 * VP * NB, kRound = 4;
+  constexpr int kAcc = 8 * VP * NB, kRound = 4, R = 8 * NB;
   const ReadP& P = A.R;
-  const int b = blockIdx.x / A.units, u = blockIdx.x - b * A.units;
-  const int64_t part = A.ws_plan[P.nseq], before = A.ws_plan[b];
-  const Span sp = span_of(P, b);
-  if (sp.tiles == 0) return;
-  const int64_t start = before * A.units + (int64_t)u * sp.tiles, end = start + sp.tiles;
+  const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+  const int b = find_sequence(A.ws_units, P.nseq, blockIdx.x, lane);
+  if (b < 0) return;
+  const int64_t part = A.ws_line[P.nseq], before = A.ws_line[b];
+  const int u = blockIdx.x - A.ws_units[b];
+  const Span sp = span_of(A, b);
+  const int64_t start = before + (int64_t)u * sp.tiles, end = start + sp.tiles;
   const int64_t c0 = start / part, c1 = (end - 1) / part;
   if (c0 == c1) return;
-  const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
   const int task = threadIdx.x >> 5, nb = task % NB, i0 = task / NB * 4;
-  const int g = u / A.chunks, h0 = (u - g * A.chunks) * 8 * NB, nh = min(8 * NB, P.grp - h0);
+  const int g = u / sp.chunks, r0 = (u - g * sp.chunks) * R, nr = min(R, sp.q * P.grp - r0);
   const int h = nb * 8 + 2 * tq;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, acc[4][4];
 #pragma unroll
@@ -624,7 +716,7 @@ quant_combine_kernel(const __grid_constant__ DecP A) {
     for (int r = 0; r < kRound; ++r) {
       if (c + r > c1) continue;
       const int64_t slot = 2 * (c + r) + (c + r == c0 && start > c0 * part ? 1 : 0);
-      ml[r] = *reinterpret_cast<const float4*>(A.ws_ml + slot * 8 * NB + h);
+      ml[r] = *reinterpret_cast<const float4*>(A.ws_ml + slot * R + h);
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[r][k] = A.ws_o[(slot * kAcc + (i0 + k) * NB + nb) * 32 + lane];
     }
@@ -653,69 +745,76 @@ quant_combine_kernel(const __grid_constant__ DecP A) {
   }
   float inv[2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) inv[e] = 1.f / (l[e] + sink_part(P, g * P.grp + h0, h + e, nh, m[e]));
-  store_heads(P, sp.t * P.H + g * P.grp + h0, nh, h, gq, i0, bad, inv,
-              [&](int k, int e) { return acc[k][e]; });
+  for (int e = 0; e < 2; ++e) inv[e] = inverse(P, g, r0, h + e, nr, m[e], l[e]);
+  store_rows(P, sp, g, r0, nr, h, gq, i0, bad, inv, [&](int k, int e) { return acc[k][e]; });
 }
 
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
 struct Plan {
-  int kp, vp, nb, chunks;
-  size_t o, ml, plan;  // bytes of the workspace's parts
+  int kp, vp, nb, ctas;
+  size_t o, ml, line, units;  // bytes of the workspace's parts
 };
-Plan plan_of(const Geometry& g, int64_t nseq) {
+Plan plan_of(const Geometry& g, int64_t nseq, int64_t rows) {
   Plan p;
   p.kp = (g.hs + 63) / 64;
   p.vp = (g.vhs + 127) / 128;
-  const int grp = g.H / g.kvh;
-  p.nb = grp > 8 ? 2 : 1;
-  p.chunks = (grp + 8 * p.nb - 1) / (8 * p.nb);
+  p.nb = rows > 8 ? 2 : 1;
+  p.ctas = p.vp * p.nb > 2 || p.kp * p.nb > 4 || p.kp * p.vp > 4 ? 2 : 3;
   auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
-  const size_t slots = 2 * (size_t)g.num_sms;
+  const size_t slots = 2 * (size_t)g.num_sms * p.ctas;
   p.o = up(slots * 8 * p.vp * p.nb * 512);
   p.ml = up(slots * 8 * p.nb * sizeof(float2));
-  p.plan = up((size_t)(nseq + 1) * sizeof(int64_t));
+  p.line = up((size_t)(nseq + 1) * sizeof(int64_t));
+  p.units = up((size_t)(nseq + 1) * sizeof(int32_t));
   return p;
 }
 
 template <int KP, int VP, int NB>
-cudaError_t launch(const Geometry& g, const QuantArgs& a, const DecP& A) {
+cudaError_t launch(const Geometry& g, const QuantArgs& a, const DecP& A, int64_t units) {
   using S = Shape<KP, VP, NB>;
   static std::atomic<bool> configured[64];
-  auto kern = quant_decode_kernel<KP, VP, NB>;
+  auto kern = quant_rows_kernel<KP, VP, NB>;
   cudaError_t e = once_per_device(configured, g.device, [&] {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   });
   if (e != cudaSuccess) return e;
-  e = tc::launch_pdl(kern, dim3((unsigned)g.num_sms), dim3(kThreads), S::kSmem, a.stream, A);
+  e = tc::launch_pdl(kern, dim3((unsigned)(g.num_sms * S::kCtas)), dim3(kThreads), S::kSmem,
+                     a.stream, A);
   if (e != cudaSuccess) return e;
-  return tc::launch_pdl(quant_combine_kernel<VP, NB>, dim3((unsigned)(A.R.nseq * A.units)),
-                        dim3(64 * VP * NB), 0, a.stream, A);
+  return tc::launch_pdl(quant_combine_kernel<VP, NB>, dim3((unsigned)units), dim3(64 * VP * NB), 0,
+                        a.stream, A);
 }
 
 }  // namespace
 
-size_t decode_workspace(const Geometry& g, int64_t nseq) {
-  const Plan p = plan_of(g, nseq);
-  return p.o + p.ml + p.plan;
+// (of any number of rows)
+size_t rows_workspace(const Geometry& g, int64_t nseq) {
+  const Plan p = plan_of(g, nseq, 8), q = plan_of(g, nseq, 16);
+  return std::max(p.o + p.ml, q.o + q.ml) + p.line + p.units;
 }
 
-cudaError_t launch_decode(const Geometry& g, const QuantArgs& a) {
+cudaError_t launch_rows(const Geometry& g, const QuantArgs& a, bool decode) {
   DecP A{};
   A.R = read_params(g, a);
-  const Plan p = plan_of(g, A.R.nseq);
+  const int64_t nseq = A.R.nseq, tokens = decode ? nseq : a.num_tokens;
+  // rows of a sequence: all have as many in decode; otherwise the mean says whether a
+  // unit takes 8 or 16
+  const int64_t rows = (tokens * A.R.grp + nseq - 1) / nseq;
+  const Plan p = plan_of(g, nseq, rows);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   A.ws_o = reinterpret_cast<float4*>(ws);
   A.ws_ml = reinterpret_cast<float2*>(ws + p.o);
-  A.ws_plan = reinterpret_cast<int64_t*>(ws + p.o + p.ml);
-  A.chunks = p.chunks;
-  A.units = g.kvh * p.chunks;
+  A.ws_line = reinterpret_cast<int64_t*>(ws + p.o + p.ml);
+  A.ws_units = reinterpret_cast<int32_t*>(ws + p.o + p.ml + p.line);
+  A.decode = decode;
+  A.rows = 8 * p.nb;
   A.min_part = 2 * kWarps;
-  if ((int64_t)A.R.nseq * A.units > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const int64_t units = g.kvh * (tokens * A.R.grp / A.rows + nseq);  // at most
+  if (units > INT32_MAX) return cudaErrorInvalidConfiguration;
   auto nb = [&](auto kp, auto vp) {
-    return p.nb == 1 ? launch<kp(), vp(), 1>(g, a, A) : launch<kp(), vp(), 2>(g, a, A);
+    return p.nb == 1 ? launch<kp(), vp(), 1>(g, a, A, units) : launch<kp(), vp(), 2>(g, a, A, units);
   };
   auto vp = [&](auto kp) {
     return p.vp == 1 ? nb(kp, std::integral_constant<int, 1>()) : nb(kp, std::integral_constant<int, 2>());

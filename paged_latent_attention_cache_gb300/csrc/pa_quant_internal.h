@@ -32,11 +32,12 @@ struct QuantArgs {
   int cross;
 };
 
-// decode (pa_quant_decode.cu); workspace bytes for nseq sequences
-size_t decode_workspace(const Geometry& g, int64_t nseq);
-cudaError_t launch_decode(const Geometry& g, const QuantArgs& a);
-// prefill (pa_quant_prefill.cu); workspace bytes for nseq sequences
-size_t prefill_workspace(const Geometry& g, int64_t nseq, int64_t num_tokens);
+// Few query rows per sequence (pa_quant_decode.cu): decode, and prefill of a few
+// tokens; workspace bytes for nseq sequences
+size_t rows_workspace(const Geometry& g, int64_t nseq);
+cudaError_t launch_rows(const Geometry& g, const QuantArgs& a, bool decode);
+// prefill (pa_quant_prefill.cu), which hands few rows to launch_rows; workspace bytes
+size_t prefill_workspace(const Geometry& g, int64_t nseq);
 cudaError_t launch_prefill(const Geometry& g, const QuantArgs& a);
 
 }  // namespace quant

@@ -44,7 +44,7 @@ constexpr int kMaxRing = 4, kAhead = 8;  // tiles converted ahead; tiles whose s
 struct Bars {
   uint64_t q_full, k_full[kMaxRing], k_empty[kMaxRing], v_full[kMaxRing], v_empty[kMaxRing];
   uint64_t s_full[4], p_full[4], sc_full[kAhead], pv_done[2], drain;
-  uint64_t c_full[2][2], c_empty[2][2];  // codes: of keys, of values
+  uint64_t c_full[4], c_empty[4];  // codes: two of keys, two of values
   uint32_t tmem_base;
   int bad, abort, any_odd;
   // keys with a NaN value that some rows of the unit see and others do not: position
@@ -283,11 +283,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return m;
 }
 
-// Four codes' NaNs as 0x80 in their bytes.
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
-  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-}
-
 template <int QT, int R, int C, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
 quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -337,7 +332,7 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
           (at >= bars->v_full && at < bars->v_full + kMaxRing))
         count = 4;
       if ((at >= bars->p_full && at < bars->p_full + 4) ||
-          (at >= bars->c_empty[0] && at < bars->c_empty[0] + 4))
+          (at >= bars->c_empty && at < bars->c_empty + 4))
         count = 4;
       mbar_init(smem_u32(at), count);
     }
@@ -636,7 +631,7 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
 #pragma unroll 1
       for (int k = 0; k < n; ++k) {
         if (!__all_sync(0xffffffffu, wait_idle(&bars->sc_full[k % kAhead], (k / kAhead) & 1) &&
-                                         wait_idle(&bars->c_full[h][k % C], (k / C) & 1) &&
+                                         wait_idle(&bars->c_full[2 * h + k % C], (k / C) & 1) &&
                                          (k < R || wait_idle(&empty[k % R], ((k / R) & 1) ^ 1))))
           break;
         const int2 in = s_in[k % kAhead];
@@ -646,7 +641,7 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
         convert((k % C) * N * pitch, (k % R) * (h ? v_bytes : k_bytes));
         fence_proxy_async();
         arrive_warp(&full[k % R], lane);
-        if (lane == 0) mbar_arrive(smem_u32(&bars->c_empty[h][k % C]));
+        if (lane == 0) mbar_arrive(smem_u32(&bars->c_empty[2 * h + k % C]));
       }
     }
     if (P.early) grid_dep_wait();
@@ -757,9 +752,9 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
           const int width = h ? P.vhs : P.hs;
           const uint32_t dst = smem_u32(codes) + (h ? C * N * P.hs : 0) + (k % C) * N * width +
                                lane * A.box * width;
-          const uint32_t bar = smem_u32(&bars->c_full[h][k % C]);
+          const uint32_t bar = smem_u32(&bars->c_full[2 * h + k % C]);
           if (!__all_sync(0xffffffffu,
-                          k < C || wait_idle(&bars->c_empty[h][k % C], ((k / C) & 1) ^ 1)))
+                          k < C || wait_idle(&bars->c_empty[2 * h + k % C], ((k / C) & 1) ^ 1)))
             break;
           if (lane == 0) mbar_expect_tx(bar, N * width);
           __syncwarp();
@@ -772,7 +767,7 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
       if (*abort && lane == 0) {  // copies may be in flight
         for (int i = max(0, issued - 2 * C); i < issued; ++i) {
           const int k = i >> 1;
-          drain_wait(smem_u32(&bars->c_full[i & 1][k % C]), (k / C) & 1, P.err_flags);
+          drain_wait(smem_u32(&bars->c_full[2 * (i & 1) + k % C]), (k / C) & 1, P.err_flags);
         }
       }
       __syncwarp();
@@ -918,18 +913,24 @@ cudaError_t launch(const Geometry& g, const QuantArgs& a, const PreP& A, int64_t
   return launch_pdl(quant_join_kernel<QT>, dim3((unsigned)ctas, 8), dim3(256), 0, a.stream, A);
 }
 
+// Batches with so few query rows per sequence and kv head, on average, go to the
+// kernel for few rows.
+constexpr int64_t kFewRows = 32;
+
 // One query tile where two accumulators do not fit in TMEM, or two queries beside
 // the rings in shared memory.
 int query_tiles(const Geometry& g) { return g.vhs <= 128 && g.hs <= 192 ? 2 : 1; }
 
 }  // namespace
 
-size_t prefill_workspace(const Geometry& g, int64_t, int64_t) {
+size_t prefill_workspace(const Geometry& g, int64_t nseq) {
   const size_t rows = (size_t)g.num_sms * query_tiles(g) * kRows;
-  return rows * g.vhs * sizeof(float) + rows * sizeof(float2);
+  return std::max(rows * g.vhs * sizeof(float) + rows * sizeof(float2), rows_workspace(g, nseq));
 }
 
 cudaError_t launch_prefill(const Geometry& g, const QuantArgs& a) {
+  const int64_t nseq = a.seq_end - a.seq_begin;
+  if (a.num_tokens * (g.H / g.kvh) <= kFewRows * nseq) return launch_rows(g, a, false);
   PreP A{};
   A.R = read_params(g, a);
   const int qt = query_tiles(g);

@@ -146,6 +146,11 @@ __device__ __forceinline__ uint32_t codes2(uint32_t two) {
   return r;
 }
 
+// Four codes' NaNs as 0x80 in their bytes.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
 // Four codes as two words of fp16.
 __device__ __forceinline__ void codes4(uint32_t four, uint32_t* lo, uint32_t* hi) {
   asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n"
