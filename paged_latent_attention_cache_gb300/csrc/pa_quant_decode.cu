@@ -8,25 +8,26 @@
 // with a softmax of its own, and join at the segment's end. A unit that lies in several
 // parts is joined by quant_combine_kernel.
 //
-// Loads. Every lane copies (cp.async, 16 bytes) just the codes that it will multiply
-// itself into a ring of its own, D tiles ahead and past the ends of segments, so there
-// is no barrier between copies and products, and a tile's pages are looked up a batch
-// of 32 tiles before. Key rows and value rows of a tile are read whole: 8 lanes of 16
-// bytes for 128 channels.
+// Loads. Each warp has a ring of its own, D tiles deep and kept full past the ends of
+// segments: 16 rows of 128 codes per TMA box, one lane issues them once the warp has read
+// the tile that was there, so a warp waits for nothing but its own copies. A tile's pages
+// are looked up a batch of 32 tiles before. (cp.async, 16 bytes a lane, stopped at 4.6
+// TB/s with 8, 12 and 16 warps an SM alike.)
 //
 // Products. mma.sync m16n8k16, keys (then value channels) as the 16 rows and the query
 // rows as the 8 columns: the other way round a group of eight or fewer would fill half
 // of a product. The order of the 16 keys and of the channels inside the products is
-// chosen so that what a lane has copied is what its registers of A hold: lane (g, t) =
-// (lane / 4, lane % 4) owns
-//   of key slot g and g + 8 (keys kappa = 4 (g / 2) + g % 2, and + 2): pieces of 16
+// chosen so that 16 bytes that a lane loads are registers of A as they are, without bank
+// conflicts in the boxes' 128-byte swizzle: lane (g, t) = (lane / 4, lane % 4) takes
+//   of key slot g and g + 8 (keys kappa = g / 2 + 4 (g % 2), and + 8): pieces of 16
 //     channels t, t + 4, ..; a word of 4 codes is one k step's A registers
-//   of the values of keys 4 t .. 4 t + 3: piece g (and g + 8); a byte of each of two
-//     words is a register.
+//   of the values of keys t, t + 4, t + 8, t + 12: piece g / 2 + 4 (g % 2) (and + 8); a
+//     byte of each of two words is a register.
 // E4M3 is exact in fp16; P^T becomes the B operand by movmatrix.
 #include <algorithm>
 #include <type_traits>
 
+#include "pa_diff_common.cuh"
 #include "pa_quant_read.cuh"
 
 namespace pa {
@@ -126,23 +127,17 @@ __device__ __forceinline__ uint32_t transposed(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-// 16 bytes into shared memory, zeros behind the first `bytes`.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
 // Accumulators i0..i0 + 3 of a block of query rows (see the products): eight channels
-// of rows r and r + 1 of the unit, times inv, to out.
+// of rows r and r + 1 of the unit, times inv, to out. piece: the lane's (of 16 channels).
 template <typename F>
 __device__ __forceinline__ void store_rows(const ReadP& P, const Span& sp, int g, int r0, int nr,
-                                           int r, int gq, int i0, bool zero, const float (&inv)[2],
+                                           int r, int piece, int i0, bool zero, const float (&inv)[2],
                                            F&& acc) {
-  const int ch = 16 * (gq + (i0 & ~7)) + 2 * (i0 & 7);
+  const int ch = 16 * (piece + (i0 & ~7)) + 2 * (i0 & 7);
   if (ch >= P.vhs) return;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
@@ -173,39 +168,50 @@ __device__ __forceinline__ float inverse(const ReadP& P, int g, int r0, int r, i
 // thread) 32 sequences of 1024 to 8192 keys (32 heads over 8, 128 / 128) took 104 us.
 template <int KP, int VP, int NB>
 struct Shape {
-  static constexpr int kCtas = VP * NB > 2 || KP * NB > 4 || KP * VP > 4 ? 2 : 3;
-  static constexpr int kStage = (2 * KP + 4 * VP) * 512;  // bytes of a warp's tile
+  static constexpr int kCtas = VP * NB > 1 || KP > 2 ? 2 : 4;
+  static constexpr int kBox = 16 * 128;                   // 16 rows of 128 codes
+  static constexpr int kKeys = (KP + 1) / 2 * kBox;       // of a warp's tile
+  static constexpr int kStage = kKeys + VP * kBox;
   static constexpr int kRow = KP * 64 + 8;                // halves of a query row
   static constexpr int kAcc = 8 * VP * NB;                // float4 accumulators of a lane
   static constexpr int kQ = 8 * NB * kRow * 2;
   static constexpr int kJoin = (kWarps / 2) * (kAcc * 512 + NB * 64);
-  static constexpr int kLeft = 227 * 1024 / kCtas - 2048 - kQ - kJoin;
-  static constexpr int kFit = kLeft / (kWarps * (kStage + 8));
+  static constexpr int kLeft = 227 * 1024 / kCtas - 3072 - kQ - kJoin;
+  static constexpr int kFit = kLeft / (kWarps * (kStage + 16));
   static constexpr int D = kFit > 8 ? 8 : kFit;
-  static constexpr int kSmem = kWarps * D * (kStage + 8) + kQ + kJoin;
+  static constexpr int kSmem = 1024 + kWarps * D * (kStage + 16) + kQ + kJoin;
   static_assert(D >= 2, "ring");
 };
 
 template <int KP, int VP, int NB>
 __global__ void __launch_bounds__(kThreads, Shape<KP, VP, NB>::kCtas)
-quant_rows_kernel(const __grid_constant__ DecP A) {
+quant_rows_kernel(const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ DecP A) {
   using S = Shape<KP, VP, NB>;
   constexpr int D = S::D, R = 8 * NB;
   const ReadP& P = A.R;
-  extern __shared__ __align__(16) uint8_t smem[];
-  uint8_t* ring = smem;
-  float2* meta = reinterpret_cast<float2*>(smem + kWarps * D * S::kStage);  // [warp][D]
-  __half* s_q = reinterpret_cast<__half*>(reinterpret_cast<uint8_t*>(meta) + kWarps * D * 8);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~(uintptr_t)1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + kWarps * D * S::kStage);  // [warp][D]
+  float2* meta = reinterpret_cast<float2*>(full + kWarps * D);                  // [warp][D]
+  __half* s_q = reinterpret_cast<__half*>(meta + kWarps * D);
   float4* join_o = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(s_q) + S::kQ);
   float2* join_ml = reinterpret_cast<float2*>(join_o + (kWarps / 2) * S::kAcc * 32);
   __shared__ float s_mult[R];
   __shared__ int64_t s_scan[kWarps];
   __shared__ int s_scan_u[kWarps];
   __shared__ int64_t s_hit[2];  // sequence of this CTA's first tile, tiles before it
-  __shared__ int s_bad;
+  __shared__ int s_bad, s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gq = lane >> 2, tq = lane & 3;
 
+  const int piece = (gq >> 1) + 4 * (gq & 1);  // of values; kappa as well
+  volatile int* abort = &s_abort;
+  uint64_t* my_full = full + warp * D;
+  if (lane < D) tc::mbar_init(smem_u32(my_full + lane), 1);
+  tc::fence_barrier_init();
+  if (tid == 0) s_abort = 0;
   if (!P.early) grid_dep_wait();
 
   // ---- the plan: tiles and units before each sequence (prefix sums, 128 sequences a
@@ -289,21 +295,9 @@ quant_rows_kernel(const __grid_constant__ DecP A) {
   int ct = 0, own = 0;          // next tile of its segment (counting the warp's own), all of them
   int page0 = 0, page1 = 0;     // of this batch's and the next batch's tiles, a lane each
   float2 sc0 = make_float2(0.f, 0.f), sc1 = sc0;
-  const int krow = P.kvh * P.hs, vrow = P.kvh * P.vhs;  // bytes
-  const int npk = P.hs >> 4, npv = P.vhs >> 4;
-  const int kappa = 4 * (gq >> 1) + (gq & 1);
-  uint8_t* my_ring = ring + warp * D * S::kStage + lane * 16;
-  // pieces of a key row that do not exist stay zeros (those of values are not stored)
-#pragma unroll
-  for (int i = 0; i < KP; ++i)
-    if (tq + 4 * i >= npk)
-#pragma unroll 1
-      for (int d = 0; d < D; ++d) {
-        *reinterpret_cast<uint4*>(my_ring + d * S::kStage + (2 * i) * 512) = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(my_ring + d * S::kStage + (2 * i + 1) * 512) =
-            make_uint4(0, 0, 0, 0);
-      }
-  const uint8_t *k_lane = nullptr, *v_lane = nullptr;  // of the walk's kv head
+  const int kappa = piece;
+  uint8_t* my_ring = ring + warp * D * S::kStage;
+  const int none = P.num_blocks << P.sh;  // (zeros arrive from behind the last slot)
   auto look_up = [&](int k) {  // the page of the warp's tile k + lane
     const int64_t key = (int64_t)(C.from + warp + (k + lane) * kWarps) * kTile;
     return k + lane < own
@@ -325,11 +319,9 @@ quant_rows_kernel(const __grid_constant__ DecP A) {
     if (C.valid()) {
       page0 = look_up(0);
       sc0 = scale_at(page0);
-      k_lane = P.key_cache + (int64_t)kappa * krow + C.g * P.hs + tq * 16;
-      v_lane = P.value_cache + (int64_t)(4 * tq) * vrow + C.g * P.vhs + gq * 16;
     }
   };
-  int put = 0;
+  int put = 0, issued = 0, taken = 0;
   auto produce = [&]() {
     if (C.valid()) {
       const int k = ct & 31;
@@ -341,28 +333,20 @@ quant_rows_kernel(const __grid_constant__ DecP A) {
       const int ke = scale_exponent(ks), ve = scale_exponent(vs);
       const bool kin = good && ke != kNone, vin = good && ve != kNone;
       const int tile = C.from + warp + ct * kWarps;
-      const int64_t row = (good ? (int64_t)page << P.sh : 0) + ((tile * kTile) & (P.bs - 1));
-      const uint32_t dst = smem_u32(my_ring + put * S::kStage);
-      const uint8_t* kr = k_lane + row * krow;
-      const uint8_t* vr = v_lane + row * vrow;
-      const uint32_t kn = kin ? 16 : 0, vn = vin ? 16 : 0;
-#pragma unroll
-      for (int i = 0; i < KP; ++i) {
-        if (tq + 4 * i < npk) {
-          copy16(dst + (2 * i) * 512, kr + 64 * i, kn);
-          copy16(dst + (2 * i + 1) * 512, kr + 64 * i + 2 * krow, kn);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < VP; ++i) {
-        if (gq + 8 * i < npv) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            copy16(dst + (2 * KP + 4 * i + j) * 512, vr + 128 * i + j * vrow, vn);
-        }
-      }
-      if (lane == 0)
+      const int row = (page << P.sh) + ((tile * kTile) & (P.bs - 1));
+      if (diff::elect_one()) {
         meta[warp * D + put] = make_float2(good ? (kin ? ks : 1.f) : NAN, vin ? (float)ve : kLeast);
+        const uint32_t dst = smem_u32(my_ring + put * S::kStage), bar = smem_u32(my_full + put);
+        tc::mbar_expect_tx(bar, S::kStage);
+#pragma unroll
+        for (int i = 0; i < (KP + 1) / 2; ++i)
+          tc::tma_load_3d(dst + i * S::kBox, &kmap, i * 128, C.g, kin ? row : none, bar);
+#pragma unroll
+        for (int i = 0; i < VP; ++i)
+          tc::tma_load_3d(dst + S::kKeys + i * S::kBox, &vmap, i * 128, C.g, vin ? row : none, bar);
+      }
+      __syncwarp();
+      ++issued;
       if (++ct == own) {
         C.next(A);
         begin();
@@ -371,13 +355,13 @@ quant_rows_kernel(const __grid_constant__ DecP A) {
         sc0 = sc1;
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
     if (++put == D) put = 0;
   };
   begin();
 #pragma unroll 1
   for (int i = 0; i < D; ++i) produce();
   int get = 0;
+  uint32_t turn = 0;
 
   // ---- segments
 #pragma unroll 1
@@ -441,11 +425,21 @@ quant_rows_kernel(const __grid_constant__ DecP A) {
     bool bad = false;
 #pragma unroll 1
     for (int tile = warp; tile < W.len; tile += kWarps) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
-      __syncwarp();
-      uint4* at = reinterpret_cast<uint4*>(my_ring + get * S::kStage);
+      if (!__all_sync(0xffffffffu,
+                      tc::wait_bar(smem_u32(my_full + get), turn, abort, P.err_flags)))
+        break;  // (told; the warp's part stays as it is, and nothing more is copied)
+      uint8_t* keys = my_ring + get * S::kStage;
+      uint8_t* values = keys + S::kKeys;
       const float2 mt = meta[warp * D + get];
-      if (++get == D) get = 0;
+      ++taken;
+      if (++get == D) {
+        get = 0;
+        turn ^= 1;
+      }
+      auto value = [&](int i, int j) {  // of key t + 4 j
+        return reinterpret_cast<uint4*>(values + i * S::kBox + (tq + 4 * j) * 128 +
+                                        ((piece ^ (tq + 4 * (j & 1))) << 4));
+      };
       const float ks = mt.x, ev = mt.y;
       bad |= isnan(ks);
       float c[NB][4];
@@ -455,7 +449,10 @@ quant_rows_kernel(const __grid_constant__ DecP A) {
         for (int e = 0; e < 4; ++e) c[nb][e] = 0.f;
 #pragma unroll
       for (int i = 0; i < KP; ++i) {
-        const uint4 u0 = at[(2 * i) * 32], u1 = at[(2 * i + 1) * 32];
+        const uint8_t* at = keys + (i >> 1) * S::kBox + kappa * 128 +
+                            (((tq + 4 * (i & 1)) ^ (kappa & 7)) << 4);
+        const uint4 u0 = *reinterpret_cast<const uint4*>(at);
+        const uint4 u1 = *reinterpret_cast<const uint4*>(at + 8 * 128);
         uint32_t f[NB][8];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -475,7 +472,7 @@ quant_rows_kernel(const __grid_constant__ DecP A) {
           for (int nb = 0; nb < NB; ++nb) mma(c[nb], a0, a1, a2, a3, f[nb][2 * s], f[nb][2 * s + 1]);
         }
       }
-      // scores of keys kappa (c[0], c[1]) and kappa + 2 for rows 2 t and 2 t + 1
+      // scores of keys kappa (c[0], c[1]) and kappa + 8 for rows 2 t and 2 t + 1
       const int j0 = tile * kTile;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -491,23 +488,24 @@ quant_rows_kernel(const __grid_constant__ DecP A) {
         uint32_t odd = 0;
 #pragma unroll 1
         for (int j = 0; j < 4; ++j) {
-          const int key = j0 + 4 * tq + j;
+          const int key = j0 + tq + 4 * j;
           const bool none = key < lo || key > hi;
 #pragma unroll
           for (int i = 0; i < VP; ++i) {
-            uint4& v = at[(2 * KP + 4 * i + j) * 32];
-            const bool nan = (nan_codes(v.x) | nan_codes(v.y) | nan_codes(v.z) | nan_codes(v.w)) &&
-                             gq + 8 * i < npv;
-            if (none || nan) v = make_uint4(0, 0, 0, 0);
-            if (nan && !none) odd |= 1u << (4 * tq + j);
+            uint4* at = value(i, j);
+            const uint4 v = *at;
+            const bool nan = nan_codes(v.x) | nan_codes(v.y) | nan_codes(v.z) | nan_codes(v.w);
+            if (none || nan) *at = make_uint4(0, 0, 0, 0);
+            if (nan && !none) odd |= 1u << (tq + 4 * j);
           }
         }
+        tc::fence_proxy_async();  // (a copy is the next to write there)
         odd = __reduce_or_sync(0xffffffffu, odd);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int key = kappa + (e & 2), tok = (r0 + nb * 8 + 2 * tq + (e & 1)) / P.grp;
+            const int key = kappa + 4 * (e & 2), tok = (r0 + nb * 8 + 2 * tq + (e & 1)) / P.grp;
             const int64_t pos = sp.pos + tok - key0;
             if (odd >> key & 1u) c[nb][e] = NAN;
             if (j0 + key > (P.cross ? (int64_t)hi : pos) ||
@@ -560,7 +558,7 @@ quant_rows_kernel(const __grid_constant__ DecP A) {
       for (int i = 0; i < VP; ++i) {
         uint4 v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = at[(2 * KP + 4 * i + j) * 32];
+        for (int j = 0; j < 4; ++j) v[j] = *value(i, j);
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           const uint32_t w0 = word(v[0], s), w1 = word(v[1], s), w2 = word(v[2], s), w3 = word(v[3], s);
@@ -577,7 +575,7 @@ quant_rows_kernel(const __grid_constant__ DecP A) {
             mma(acc[i * 8 + 2 * s + 1][nb], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
         }
       }
-      __syncwarp();  // (meta is read)
+      __syncwarp();  // (the tile is read)
       produce();
     }
     // a warp's sums over its key lanes
@@ -635,8 +633,8 @@ quant_rows_kernel(const __grid_constant__ DecP A) {
       }
     }
     if (warp == 0) {
-      const bool any_bad = s_bad != 0;
-      if (any_bad && lane == 0) raise_flag(P.err_flags, PA_DEVERR_BLOCK);
+      const bool any_bad = s_bad != 0 || *abort;
+      if (s_bad && lane == 0) raise_flag(P.err_flags, PA_DEVERR_BLOCK);
       if (W.len == W.tiles) {  // the whole unit
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -646,7 +644,7 @@ quant_rows_kernel(const __grid_constant__ DecP A) {
             inv[e] = inverse(P, W.g, r0, nb * 8 + 2 * tq + e, nr, m[nb][e], l[nb][e]);
 #pragma unroll
           for (int i = 0; i < 8 * VP; i += 4)
-            store_rows(P, sp, W.g, r0, nr, nb * 8 + 2 * tq, gq, i, any_bad, inv,
+            store_rows(P, sp, W.g, r0, nr, nb * 8 + 2 * tq, piece, i, any_bad, inv,
                        [&](int k, int e) { return acc[i + k][nb][e]; });
         }
       } else {
@@ -670,6 +668,10 @@ quant_rows_kernel(const __grid_constant__ DecP A) {
     }
     W.next(A);
   }
+  if (*abort && lane == 0)  // copies may be in flight
+    for (int i = taken; i < issued; ++i)
+      tc::drain_wait(smem_u32(my_full + i % D), (i / D) & 1, P.err_flags);
+  __syncwarp();
   grid_dep_launch();
   // sequences without tiles: told, and zeros
   for (int b = blockIdx.x; b < P.nseq; b += gridDim.x) {
@@ -746,7 +748,7 @@ quant_combine_kernel(const __grid_constant__ DecP A) {
   float inv[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) inv[e] = inverse(P, g, r0, h + e, nr, m[e], l[e]);
-  store_rows(P, sp, g, r0, nr, h, gq, i0, bad, inv, [&](int k, int e) { return acc[k][e]; });
+  store_rows(P, sp, g, r0, nr, h, (gq >> 1) + 4 * (gq & 1), i0, bad, inv, [&](int k, int e) { return acc[k][e]; });
 }
 
 // ---------------------------------------------------------------------------
@@ -761,7 +763,7 @@ Plan plan_of(const Geometry& g, int64_t nseq, int64_t rows) {
   p.kp = (g.hs + 63) / 64;
   p.vp = (g.vhs + 127) / 128;
   p.nb = rows > 8 ? 2 : 1;
-  p.ctas = p.vp * p.nb > 2 || p.kp * p.nb > 4 || p.kp * p.vp > 4 ? 2 : 3;
+  p.ctas = p.vp * p.nb > 1 || p.kp > 2 ? 2 : 4;
   auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
   const size_t slots = 2 * (size_t)g.num_sms * p.ctas;
   p.o = up(slots * 8 * p.vp * p.nb * 512);
@@ -780,8 +782,11 @@ cudaError_t launch(const Geometry& g, const QuantArgs& a, const DecP& A, int64_t
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   });
   if (e != cudaSuccess) return e;
+  CUtensorMap kmap, vmap;
+  if ((e = codes_map(&kmap, a.key_cache, g, g.hs, 128, kTile)) != cudaSuccess) return e;
+  if ((e = codes_map(&vmap, a.value_cache, g, g.vhs, 128, kTile)) != cudaSuccess) return e;
   e = tc::launch_pdl(kern, dim3((unsigned)(g.num_sms * S::kCtas)), dim3(kThreads), S::kSmem,
-                     a.stream, A);
+                     a.stream, kmap, vmap, A);
   if (e != cudaSuccess) return e;
   return tc::launch_pdl(quant_combine_kernel<VP, NB>, dim3((unsigned)units), dim3(64 * VP * NB), 0,
                         a.stream, A);

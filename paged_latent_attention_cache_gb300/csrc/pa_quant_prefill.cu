@@ -878,21 +878,6 @@ __global__ void __launch_bounds__(256) quant_join_kernel(const __grid_constant__
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-// A cache as (channel, kv head, slot); boxes of one head's channels in `rows` slots.
-cudaError_t codes_map(CUtensorMap* map, const void* base, const Geometry& g, int width, int rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return cudaErrorNotSupported;
-  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)g.kvh,
-                              (cuuint64_t)g.num_blocks * g.bs};
-  const cuuint64_t str[2] = {(cuuint64_t)width, (cuuint64_t)width * g.kvh};
-  const cuuint32_t box[3] = {(cuuint32_t)width, 1, (cuuint32_t)rows}, one[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, str, box, one,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? cudaSuccess
-             : cudaErrorInvalidValue;
-}
-
 template <int QT, int R, int C, bool CAP>
 cudaError_t launch(const Geometry& g, const QuantArgs& a, const PreP& A, int64_t ctas) {
   static std::atomic<bool> configured[64];
@@ -905,8 +890,8 @@ cudaError_t launch(const Geometry& g, const QuantArgs& a, const PreP& A, int64_t
   });
   if (e != cudaSuccess) return e;
   CUtensorMap kmap, vmap;
-  if ((e = codes_map(&kmap, a.key_cache, g, g.hs, A.box)) != cudaSuccess) return e;
-  if ((e = codes_map(&vmap, a.value_cache, g, g.vhs, A.box)) != cudaSuccess) return e;
+  if ((e = codes_map(&kmap, a.key_cache, g, g.hs, 0, A.box)) != cudaSuccess) return e;
+  if ((e = codes_map(&vmap, a.value_cache, g, g.vhs, 0, A.box)) != cudaSuccess) return e;
   e = launch_pdl(kern, dim3((unsigned)(ctas * A.splits)), dim3(kThreads), smem, a.stream, kmap, vmap,
                  A);
   if (e != cudaSuccess || A.splits == 1) return e;

@@ -91,6 +91,25 @@ inline ReadP read_params(const Geometry& g, const QuantArgs& a) {
   return P;
 }
 
+// A cache as (channel, kv head, slot); boxes of `rows` slots of one head: all of its
+// channels, or `swizzled` of them (128, swizzled; zeros behind the head's last).
+inline cudaError_t codes_map(CUtensorMap* map, const void* base, const Geometry& g, int width,
+                             int swizzled, int rows) {
+  tc::EncodeTiledFn enc = tc::encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)g.kvh,
+                              (cuuint64_t)g.num_blocks * g.bs};
+  const cuuint64_t str[2] = {(cuuint64_t)width, (cuuint64_t)width * g.kvh};
+  const cuuint32_t box[3] = {(cuuint32_t)(swizzled ? swizzled : width), 1, (cuuint32_t)rows};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, str, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE,
+             swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
 // log2e times the softcapped score whose ratio to softcap is x.
 __device__ __forceinline__ float capped(const ReadP& P, float x) {
   return P.cap_out * tanh_ex2(x);
