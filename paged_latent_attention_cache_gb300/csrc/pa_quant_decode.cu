@@ -388,9 +388,8 @@ quant_rows_kernel(const __grid_constant__ CUtensorMap kmap,
     constexpr bool kKeep = KP * NB <= 4;  // the query's fragments in registers
     uint32_t bq[kKeep ? NB : 1][kKeep ? KP : 1][8];
     auto q_frag = [&](int nb, int i, uint32_t (&f)[8]) {
-      const uint4* src =
-          reinterpret_cast<const uint4*>(s_q + (nb * 8 + gq) * S::kRow + 16 * (tq + 4 * i));
-      const uint4 u = src[0], v = src[1];
+      const uint32_t at = smem_u32(s_q + (nb * 8 + gq) * S::kRow + 16 * (tq + 4 * i));
+      const uint4 u = lds128(at), v = lds128(at + 16);
       f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
       f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
     };
@@ -428,17 +427,18 @@ quant_rows_kernel(const __grid_constant__ CUtensorMap kmap,
       if (!__all_sync(0xffffffffu,
                       tc::wait_bar(smem_u32(my_full + get), turn, abort, P.err_flags)))
         break;  // (told; the warp's part stays as it is, and nothing more is copied)
-      uint8_t* keys = my_ring + get * S::kStage;
-      uint8_t* values = keys + S::kKeys;
-      const float2 mt = meta[warp * D + get];
+      const uint32_t keys = smem_u32(my_ring) + get * S::kStage, values = keys + S::kKeys;
+      float2 mt;
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                   : "=f"(mt.x), "=f"(mt.y)
+                   : "r"(smem_u32(meta + warp * D + get)));
       ++taken;
       if (++get == D) {
         get = 0;
         turn ^= 1;
       }
       auto value = [&](int i, int j) {  // of key t + 4 j
-        return reinterpret_cast<uint4*>(values + i * S::kBox + (tq + 4 * j) * 128 +
-                                        ((piece ^ (tq + 4 * (j & 1))) << 4));
+        return values + i * S::kBox + (tq + 4 * j) * 128 + ((piece ^ (tq + 4 * (j & 1))) << 4);
       };
       const float ks = mt.x, ev = mt.y;
       bad |= isnan(ks);
@@ -449,10 +449,9 @@ quant_rows_kernel(const __grid_constant__ CUtensorMap kmap,
         for (int e = 0; e < 4; ++e) c[nb][e] = 0.f;
 #pragma unroll
       for (int i = 0; i < KP; ++i) {
-        const uint8_t* at = keys + (i >> 1) * S::kBox + kappa * 128 +
+        const uint32_t at = keys + (i >> 1) * S::kBox + kappa * 128 +
                             (((tq + 4 * (i & 1)) ^ (kappa & 7)) << 4);
-        const uint4 u0 = *reinterpret_cast<const uint4*>(at);
-        const uint4 u1 = *reinterpret_cast<const uint4*>(at + 8 * 128);
+        const uint4 u0 = lds128(at), u1 = lds128(at + 8 * 128);
         uint32_t f[NB][8];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -492,10 +491,10 @@ quant_rows_kernel(const __grid_constant__ CUtensorMap kmap,
           const bool none = key < lo || key > hi;
 #pragma unroll
           for (int i = 0; i < VP; ++i) {
-            uint4* at = value(i, j);
-            const uint4 v = *at;
+            const uint32_t at = value(i, j);
+            const uint4 v = lds128(at);
             const bool nan = nan_codes(v.x) | nan_codes(v.y) | nan_codes(v.z) | nan_codes(v.w);
-            if (none || nan) *at = make_uint4(0, 0, 0, 0);
+            if (none || nan) sts128(at, 0, 0, 0, 0);
             if (nan && !none) odd |= 1u << (tq + 4 * j);
           }
         }
@@ -558,7 +557,7 @@ quant_rows_kernel(const __grid_constant__ CUtensorMap kmap,
       for (int i = 0; i < VP; ++i) {
         uint4 v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = *value(i, j);
+        for (int j = 0; j < 4; ++j) v[j] = lds128(value(i, j));
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           const uint32_t w0 = word(v[0], s), w1 = word(v[1], s), w2 = word(v[2], s), w3 = word(v[3], s);
