@@ -35,7 +35,6 @@ namespace quant {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kTile = 16;
 
 struct DecP {
   ReadP R;
@@ -45,6 +44,8 @@ struct DecP {
   int32_t* ws_units; // [nseq + 1] units before each sequence, then all
   int decode;        // one token per sequence, others are told
   int rows;          // 8 NB
+  int tile;          // keys: 16 TH
+  int box;           // rows of a copy: min(bs, tile)
   int min_part;
 };
 
@@ -71,8 +72,8 @@ __device__ __forceinline__ Span span_of(const DecP& A, int b) {
           : q > 0 && (past < 0 || s.hi >= (int64_t)P.max_blocks * P.bs) ? PA_DEVERR_CONTEXT
           : q > 0 && P.rd > 0 && s.hi >= P.cos_rows              ? PA_DEVERR_POSITION
                                                                  : 0;
-  s.first = (int)(s.lo / kTile);
-  s.tiles = s.err || q <= 0 || s.hi < s.lo ? 0 : (int)(s.hi / kTile) - s.first + 1;
+  s.first = (int)(s.lo / A.tile);
+  s.tiles = s.err || q <= 0 || s.hi < s.lo ? 0 : (int)(s.hi / A.tile) - s.first + 1;
   s.chunks = s.tiles ? (s.q * P.grp + A.rows - 1) / A.rows : 0;
   return s;
 }
@@ -84,6 +85,7 @@ struct Walk {
   int b, tiles, first, chunks;
   int g, chunk;           // the segment's unit
   int from, len;          // first tile (in the cache), tiles
+  int lo, hi;             // keys that any of its tokens sees
   __device__ __forceinline__ bool valid() const { return x < end; }
   __device__ __forceinline__ void enter(const DecP& A, int seq, int64_t at) {
     const Span s = span_of(A, seq);
@@ -92,6 +94,8 @@ struct Walk {
     tiles = s.tiles;
     first = s.first;
     chunks = s.chunks;
+    lo = (int)s.lo;
+    hi = (int)s.hi;
   }
   __device__ __forceinline__ void segment() {
     const uint64_t off = (uint64_t)(x - start);
@@ -166,37 +170,38 @@ __device__ __forceinline__ float inverse(const ReadP& P, int g, int r0, int r, i
 // CTAs per SM and the shared memory of one: rings, query, joining buffers. Twelve
 // warps an SM where the registers allow it: with eight (one CTA of 255 registers a
 // thread) 32 sequences of 1024 to 8192 keys (32 heads over 8, 128 / 128) took 104 us.
-template <int KP, int VP, int NB>
+template <int KP, int VP, int NB, int TH>
 struct Shape {
-  static constexpr int kCtas = VP * NB > 1 || KP > 2 ? 2 : 4;
-  static constexpr int kBox = 16 * 128;                   // 16 rows of 128 codes
+  static constexpr int kCtas = TH == 2 && NB == 1 ? 3 : 2;
+  static constexpr int kBox = TH * 16 * 128;              // a tile's keys of 128 codes
   static constexpr int kKeys = (KP + 1) / 2 * kBox;       // of a warp's tile
   static constexpr int kStage = kKeys + VP * kBox;
   static constexpr int kRow = KP * 64 + 8;                // halves of a query row
   static constexpr int kAcc = 8 * VP * NB;                // float4 accumulators of a lane
   static constexpr int kQ = 8 * NB * kRow * 2;
   static constexpr int kJoin = (kWarps / 2) * (kAcc * 512 + NB * 64);
-  static constexpr int kLeft = 227 * 1024 / kCtas - 3072 - kQ - kJoin;
-  static constexpr int kFit = kLeft / (kWarps * (kStage + 16));
+  static constexpr int kBoth = kQ > kJoin ? kQ : kJoin;   // one after the other
+  static constexpr int kLeft = 228 * 1024 / kCtas - 1024 - 320 - 1024 - kBoth;
+  static constexpr int kFit = kLeft / (kWarps * (kStage + 24));
   static constexpr int D = kFit > 8 ? 8 : kFit;
-  static constexpr int kSmem = 1024 + kWarps * D * (kStage + 16) + kQ + kJoin;
+  static constexpr int kSmem = 1024 + kWarps * D * (kStage + 24) + kBoth;
   static_assert(D >= 2, "ring");
 };
 
-template <int KP, int VP, int NB>
-__global__ void __launch_bounds__(kThreads, Shape<KP, VP, NB>::kCtas)
+template <int KP, int VP, int NB, int TH>
+__global__ void __launch_bounds__(kThreads, Shape<KP, VP, NB, TH>::kCtas)
 quant_rows_kernel(const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ DecP A) {
-  using S = Shape<KP, VP, NB>;
-  constexpr int D = S::D, R = 8 * NB;
+  using S = Shape<KP, VP, NB, TH>;
+  constexpr int D = S::D, R = 8 * NB, kTile = 16 * TH;
   const ReadP& P = A.R;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + kWarps * D * S::kStage);  // [warp][D]
-  float2* meta = reinterpret_cast<float2*>(full + kWarps * D);                  // [warp][D]
+  float4* meta = reinterpret_cast<float4*>(full + kWarps * D);                  // [warp][D]
   __half* s_q = reinterpret_cast<__half*>(meta + kWarps * D);
-  float4* join_o = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(s_q) + S::kQ);
+  float4* join_o = reinterpret_cast<float4*>(s_q);
   float2* join_ml = reinterpret_cast<float2*>(join_o + (kWarps / 2) * S::kAcc * 32);
   __shared__ float s_mult[R];
   __shared__ int64_t s_scan[kWarps];
@@ -298,15 +303,18 @@ quant_rows_kernel(const __grid_constant__ CUtensorMap kmap,
   const int kappa = piece;
   uint8_t* my_ring = ring + warp * D * S::kStage;
   const int none = P.num_blocks << P.sh;  // (zeros arrive from behind the last slot)
-  auto look_up = [&](int k) {  // the page of the warp's tile k + lane
-    const int64_t key = (int64_t)(C.from + warp + (k + lane) * kWarps) * kTile;
-    return k + lane < own
-               ? P.block_table[(int64_t)(P.seq_begin + C.b) * P.max_blocks + (key >> P.sh)]
-               : 0;
+  // A lane of a batch: half lane % nbox of the warp's tile lane / nbox (a tile lies in a
+  // page, or in two of 16 rows).
+  const int nbox = TH == 2 ? kTile / A.box : 1, batch = 32 / nbox;
+  auto look_up = [&](int k) {  // its page behind the warp's tile k; -1 invalid, -2 not needed
+    const int t = k + (nbox == 2 ? lane >> 1 : lane);
+    const int64_t key = (int64_t)(C.from + warp + t * kWarps) * kTile + (nbox == 2 ? (lane & 1) * 16 : 0);
+    if (t >= own || key > C.hi || key + A.box - 1 < C.lo) return -2;
+    const int page = P.block_table[(int64_t)(P.seq_begin + C.b) * P.max_blocks + (key >> P.sh)];
+    return page >= 0 && page < P.num_blocks ? page : -1;
   };
   auto scale_at = [&](int page) {
-    return page >= 0 && page < P.num_blocks ? P.scales[(int64_t)page * P.kvh + C.g]
-                                            : make_float2(0.f, 0.f);
+    return page >= 0 ? P.scales[(int64_t)page * P.kvh + C.g] : make_float2(0.f, 0.f);
   };
   auto begin = [&]() {  // the first segment from here on with a tile of this warp
     own = 0;
@@ -324,33 +332,46 @@ quant_rows_kernel(const __grid_constant__ CUtensorMap kmap,
   int put = 0, issued = 0, taken = 0;
   auto produce = [&]() {
     if (C.valid()) {
-      const int k = ct & 31;
-      if (k == 8) page1 = look_up((ct & ~31) + 32);
-      if (k == 16) sc1 = scale_at(page1);
-      const int page = __shfl_sync(0xffffffffu, page0, k);
-      const float ks = __shfl_sync(0xffffffffu, sc0.x, k), vs = __shfl_sync(0xffffffffu, sc0.y, k);
-      const bool good = page >= 0 && page < P.num_blocks;
-      const int ke = scale_exponent(ks), ve = scale_exponent(vs);
-      const bool kin = good && ke != kNone, vin = good && ve != kNone;
+      const int k = ct & (batch - 1);
+      if (k == batch / 4) page1 = look_up((ct & ~(batch - 1)) + batch);
+      if (k == batch / 2) sc1 = scale_at(page1);
       const int tile = C.from + warp + ct * kWarps;
-      const int row = (page << P.sh) + ((tile * kTile) & (P.bs - 1));
-      if (diff::elect_one()) {
-        meta[warp * D + put] = make_float2(good ? (kin ? ks : 1.f) : NAN, vin ? (float)ve : kLeast);
-        const uint32_t dst = smem_u32(my_ring + put * S::kStage), bar = smem_u32(my_full + put);
-        tc::mbar_expect_tx(bar, S::kStage);
+      const uint32_t dst = smem_u32(my_ring + put * S::kStage), bar = smem_u32(my_full + put);
+      float4 mt;
 #pragma unroll
-        for (int i = 0; i < (KP + 1) / 2; ++i)
-          tc::tma_load_3d(dst + i * S::kBox, &kmap, i * 128, C.g, kin ? row : none, bar);
+      for (int h = 0; h < TH; ++h) {
+        if (h < nbox) {
+          const int from = k * nbox + h;
+          const int page = __shfl_sync(0xffffffffu, page0, from);
+          const float ks = __shfl_sync(0xffffffffu, sc0.x, from);
+          const float vs = __shfl_sync(0xffffffffu, sc0.y, from);
+          const int ve = scale_exponent(vs);
+          const bool kin = page >= 0 && scale_exponent(ks) != kNone, vin = page >= 0 && ve != kNone;
+          const int row = (page << P.sh) + ((tile * kTile + h * 16) & (P.bs - 1));
+          (h ? mt.z : mt.x) = page != -1 ? (kin ? ks : 1.f) : NAN;
+          (h ? mt.w : mt.y) = vin ? (float)ve : kLeast;
+          if (diff::elect_one()) {
+            if (h == 0) tc::mbar_expect_tx(bar, S::kStage);
 #pragma unroll
-        for (int i = 0; i < VP; ++i)
-          tc::tma_load_3d(dst + S::kKeys + i * S::kBox, &vmap, i * 128, C.g, vin ? row : none, bar);
+            for (int i = 0; i < (KP + 1) / 2; ++i)
+              tc::tma_load_3d(dst + i * S::kBox + h * 2048, &kmap, i * 128, C.g, kin ? row : none, bar);
+#pragma unroll
+            for (int i = 0; i < VP; ++i)
+              tc::tma_load_3d(dst + S::kKeys + i * S::kBox + h * 2048, &vmap, i * 128, C.g,
+                              vin ? row : none, bar);
+          }
+        } else {
+          mt.z = mt.x;
+          mt.w = mt.y;
+        }
       }
+      if (lane == 0) meta[warp * D + put] = mt;
       __syncwarp();
       ++issued;
       if (++ct == own) {
         C.next(A);
         begin();
-      } else if ((ct & 31) == 0) {
+      } else if ((ct & (batch - 1)) == 0) {
         page0 = page1;
         sc0 = sc1;
       }
@@ -428,30 +449,37 @@ quant_rows_kernel(const __grid_constant__ CUtensorMap kmap,
                       tc::wait_bar(smem_u32(my_full + get), turn, abort, P.err_flags)))
         break;  // (told; the warp's part stays as it is, and nothing more is copied)
       const uint32_t keys = smem_u32(my_ring) + get * S::kStage, values = keys + S::kKeys;
-      float2 mt;
-      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                   : "=f"(mt.x), "=f"(mt.y)
-                   : "r"(smem_u32(meta + warp * D + get)));
+      const uint4 mw = lds128(smem_u32(meta + warp * D + get));
+      const float ks[2] = {__uint_as_float(mw.x), __uint_as_float(mw.z)};
+      const float ev[2] = {__uint_as_float(mw.y), __uint_as_float(mw.w)};
       ++taken;
       if (++get == D) {
         get = 0;
         turn ^= 1;
       }
-      auto value = [&](int i, int j) {  // of key t + 4 j
-        return values + i * S::kBox + (tq + 4 * j) * 128 + ((piece ^ (tq + 4 * (j & 1))) << 4);
+      auto value = [&](int i, int h, int j) {  // of key 16 h + t + 4 j
+        return values + i * S::kBox + h * 2048 + (tq + 4 * j) * 128 +
+               ((piece ^ (tq + 4 * (j & 1))) << 4);
       };
-      const float ks = mt.x, ev = mt.y;
-      bad |= isnan(ks);
-      float c[NB][4];
+      float c[TH][NB][4];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int h = 0; h < TH; ++h) {
+        bad |= isnan(ks[h]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) c[nb][e] = 0.f;
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[h][nb][e] = 0.f;
+      }
 #pragma unroll
       for (int i = 0; i < KP; ++i) {
         const uint32_t at = keys + (i >> 1) * S::kBox + kappa * 128 +
                             (((tq + 4 * (i & 1)) ^ (kappa & 7)) << 4);
-        const uint4 u0 = lds128(at), u1 = lds128(at + 8 * 128);
+        uint4 u0[TH], u1[TH];
+#pragma unroll
+        for (int h = 0; h < TH; ++h) {
+          u0[h] = lds128(at + h * 2048);
+          u1[h] = lds128(at + h * 2048 + 8 * 128);
+        }
         uint32_t f[NB][8];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -463,66 +491,83 @@ quant_rows_kernel(const __grid_constant__ CUtensorMap kmap,
           }
         }
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          uint32_t a0, a1, a2, a3;
-          codes4(word(u0, s), &a0, &a2);
-          codes4(word(u1, s), &a1, &a3);
+        for (int s = 0; s < 4; ++s)
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma(c[nb], a0, a1, a2, a3, f[nb][2 * s], f[nb][2 * s + 1]);
-        }
+          for (int h = 0; h < TH; ++h) {
+            uint32_t a0, a1, a2, a3;
+            codes4(word(u0[h], s), &a0, &a2);
+            codes4(word(u1[h], s), &a1, &a3);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              mma(c[h][nb], a0, a1, a2, a3, f[nb][2 * s], f[nb][2 * s + 1]);
+          }
       }
-      // scores of keys kappa (c[0], c[1]) and kappa + 8 for rows 2 t and 2 t + 1
+      // scores of keys 16 h + kappa (c[0], c[1]) and + 8 for rows 2 t and 2 t + 1
       const int j0 = tile * kTile;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int h = 0; h < TH; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float f = ks * mult[nb][e & 1];
-          c[nb][e] = P.cap_in > 0.f ? capped(P, c[nb][e] * f) + ev : fmaf(c[nb][e], f, ev);
-        }
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float f = ks[h] * mult[nb][e & 1];
+            c[h][nb][e] = P.cap_in > 0.f ? capped(P, c[h][nb][e] * f) + ev[h]
+                                         : fmaf(c[h][nb][e], f, ev[h]);
+          }
       if (j0 < all_lo || j0 + kTile - 1 > all_hi) {
         // an end of what the rows see: unseen values become zeros (0 times NaN is NaN),
         // and a NaN among values that only some rows see goes over to their scores
         const int hi = (int)(sp.hi - key0), lo = (int)(sp.lo - key0);
         uint32_t odd = 0;
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          const int key = j0 + tq + 4 * j;
-          const bool none = key < lo || key > hi;
+        for (int j = 0; j < 4 * TH; ++j) {
+          const int key = tq + 4 * j;
+          const bool unseen = j0 + key < lo || j0 + key > hi;
 #pragma unroll
           for (int i = 0; i < VP; ++i) {
-            const uint32_t at = value(i, j);
+            const uint32_t at = value(i, j >> 2, j & 3);
             const uint4 v = lds128(at);
             const bool nan = nan_codes(v.x) | nan_codes(v.y) | nan_codes(v.z) | nan_codes(v.w);
-            if (none || nan) sts128(at, 0, 0, 0, 0);
-            if (nan && !none) odd |= 1u << (tq + 4 * j);
+            if (unseen || nan) sts128(at, 0, 0, 0, 0);
+            if (nan && !unseen) odd |= 1u << key;
           }
         }
         tc::fence_proxy_async();  // (a copy is the next to write there)
         odd = __reduce_or_sync(0xffffffffu, odd);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int h = 0; h < TH; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int key = kappa + 4 * (e & 2), tok = (r0 + nb * 8 + 2 * tq + (e & 1)) / P.grp;
-            const int64_t pos = sp.pos + tok - key0;
-            if (odd >> key & 1u) c[nb][e] = NAN;
-            if (j0 + key > (P.cross ? (int64_t)hi : pos) ||
-                (P.window >= 0 && pos - (j0 + key) > P.window))
-              c[nb][e] = -INFINITY;
-          }
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = 16 * h + kappa + 4 * (e & 2);
+              const int tok = (r0 + nb * 8 + 2 * tq + (e & 1)) / P.grp;
+              const int64_t pos = sp.pos + tok - key0;
+              if (odd >> key & 1u) c[h][nb][e] = NAN;
+              if (j0 + key > (P.cross ? (int64_t)hi : pos) ||
+                  (P.window >= 0 && pos - (j0 + key) > P.window))
+                c[h][nb][e] = -INFINITY;
+            }
       }
+      float top[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[nb][e] = fmaxf(c[0][nb][e], c[0][nb][e + 2]);
+          if (TH == 2) top[nb][e] = fmaxf(top[nb][e], fmaxf(c[TH - 1][nb][e], c[TH - 1][nb][e + 2]));
+        }
       bool rise = false;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) rise |= fmaxf(c[nb][e], c[nb][e + 2]) > m[nb][e] + kLazy;
+        for (int e = 0; e < 2; ++e) rise |= top[nb][e] > m[nb][e] + kLazy;
       if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float t = fmaxf(c[nb][e], c[nb][e + 2]);
+            float t = top[nb][e];
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
@@ -538,42 +583,47 @@ quant_rows_kernel(const __grid_constant__ CUtensorMap kmap,
             }
           }
       }
-      uint32_t pb[NB][2];
-      const float out_of = pow2(-(int)ev);
+      uint32_t pb[TH][NB][2];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        float p[4];
+      for (int h = 0; h < TH; ++h) {
+        const float out_of = pow2(-(int)ev[h]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float mm = m[nb][e & 1];
-          p[e] = ex2(c[nb][e] - ((mm == -INFINITY ? 0.f : mm) - kShift));
-        }
-        l[nb][0] = fmaf(p[0] + p[2], out_of, l[nb][0]);
-        l[nb][1] = fmaf(p[1] + p[3], out_of, l[nb][1]);
-        pb[nb][0] = transposed(tc::pack2<__half>(p[0], p[1]));
-        pb[nb][1] = transposed(tc::pack2<__half>(p[2], p[3]));
-      }
+        for (int nb = 0; nb < NB; ++nb) {
+          float p[4];
 #pragma unroll
-      for (int i = 0; i < VP; ++i) {
-        uint4 v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = lds128(value(i, j));
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const uint32_t w0 = word(v[0], s), w1 = word(v[1], s), w2 = word(v[2], s), w3 = word(v[3], s);
-          uint32_t a0, a1, a2, a3;
-          codes4(__byte_perm(w0, w1, 0x5140), &a0, &a1);
-          codes4(__byte_perm(w2, w3, 0x5140), &a2, &a3);
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-            mma(acc[i * 8 + 2 * s][nb], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
-          codes4(__byte_perm(w0, w1, 0x7362), &a0, &a1);
-          codes4(__byte_perm(w2, w3, 0x7362), &a2, &a3);
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-            mma(acc[i * 8 + 2 * s + 1][nb], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
+          for (int e = 0; e < 4; ++e) {
+            const float mm = m[nb][e & 1];
+            p[e] = ex2(c[h][nb][e] - ((mm == -INFINITY ? 0.f : mm) - kShift));
+          }
+          l[nb][0] = fmaf(p[0] + p[2], out_of, l[nb][0]);
+          l[nb][1] = fmaf(p[1] + p[3], out_of, l[nb][1]);
+          pb[h][nb][0] = transposed(tc::pack2<__half>(p[0], p[1]));
+          pb[h][nb][1] = transposed(tc::pack2<__half>(p[2], p[3]));
         }
       }
+#pragma unroll
+      for (int i = 0; i < VP; ++i)
+#pragma unroll
+        for (int h = 0; h < TH; ++h) {
+          uint4 v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = lds128(value(i, h, j));
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const uint32_t w0 = word(v[0], s), w1 = word(v[1], s), w2 = word(v[2], s), w3 = word(v[3], s);
+            uint32_t a0, a1, a2, a3;
+            codes4(__byte_perm(w0, w1, 0x5140), &a0, &a1);
+            codes4(__byte_perm(w2, w3, 0x5140), &a2, &a3);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              mma(acc[i * 8 + 2 * s][nb], a0, a1, a2, a3, pb[h][nb][0], pb[h][nb][1]);
+            codes4(__byte_perm(w0, w1, 0x7362), &a0, &a1);
+            codes4(__byte_perm(w2, w3, 0x7362), &a2, &a3);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              mma(acc[i * 8 + 2 * s + 1][nb], a0, a1, a2, a3, pb[h][nb][0], pb[h][nb][1]);
+          }
+        }
       __syncwarp();  // (the tile is read)
       produce();
     }
@@ -588,7 +638,7 @@ quant_rows_kernel(const __grid_constant__ CUtensorMap kmap,
     // joined by halves: warps [n, 2 n) hand over to warps [0, n)
 #pragma unroll 1
     for (int n = kWarps / 2; n > 0; n >>= 1) {
-      if (n < kWarps / 2) __syncthreads();  // the buffers are read
+      __syncthreads();  // the query, or the buffers, are read
       if (warp >= n && warp < 2 * n) {
 #pragma unroll
         for (int i = 0; i < 8 * VP; ++i)
@@ -754,7 +804,7 @@ quant_combine_kernel(const __grid_constant__ DecP A) {
 // Host side
 // ---------------------------------------------------------------------------
 struct Plan {
-  int kp, vp, nb, ctas;
+  int kp, vp, nb, th, ctas;
   size_t o, ml, line, units;  // bytes of the workspace's parts
 };
 Plan plan_of(const Geometry& g, int64_t nseq, int64_t rows) {
@@ -762,7 +812,8 @@ Plan plan_of(const Geometry& g, int64_t nseq, int64_t rows) {
   p.kp = (g.hs + 63) / 64;
   p.vp = (g.vhs + 127) / 128;
   p.nb = rows > 8 ? 2 : 1;
-  p.ctas = p.vp * p.nb > 1 || p.kp > 2 ? 2 : 4;
+  p.th = p.kp <= 2 && p.vp == 1 ? 2 : 1;
+  p.ctas = p.th == 2 && p.nb == 1 ? 3 : 2;  // (as Shape has it)
   auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
   const size_t slots = 2 * (size_t)g.num_sms * p.ctas;
   p.o = up(slots * 8 * p.vp * p.nb * 512);
@@ -772,18 +823,18 @@ Plan plan_of(const Geometry& g, int64_t nseq, int64_t rows) {
   return p;
 }
 
-template <int KP, int VP, int NB>
+template <int KP, int VP, int NB, int TH>
 cudaError_t launch(const Geometry& g, const QuantArgs& a, const DecP& A, int64_t units) {
-  using S = Shape<KP, VP, NB>;
+  using S = Shape<KP, VP, NB, TH>;
   static std::atomic<bool> configured[64];
-  auto kern = quant_rows_kernel<KP, VP, NB>;
+  auto kern = quant_rows_kernel<KP, VP, NB, TH>;
   cudaError_t e = once_per_device(configured, g.device, [&] {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   });
   if (e != cudaSuccess) return e;
   CUtensorMap kmap, vmap;
-  if ((e = codes_map(&kmap, a.key_cache, g, g.hs, 128, kTile)) != cudaSuccess) return e;
-  if ((e = codes_map(&vmap, a.value_cache, g, g.vhs, 128, kTile)) != cudaSuccess) return e;
+  if ((e = codes_map(&kmap, a.key_cache, g, g.hs, 128, A.box)) != cudaSuccess) return e;
+  if ((e = codes_map(&vmap, a.value_cache, g, g.vhs, 128, A.box)) != cudaSuccess) return e;
   e = tc::launch_pdl(kern, dim3((unsigned)(g.num_sms * S::kCtas)), dim3(kThreads), S::kSmem,
                      a.stream, kmap, vmap, A);
   if (e != cudaSuccess) return e;
@@ -814,14 +865,19 @@ cudaError_t launch_rows(const Geometry& g, const QuantArgs& a, bool decode) {
   A.ws_units = reinterpret_cast<int32_t*>(ws + p.o + p.ml + p.line);
   A.decode = decode;
   A.rows = 8 * p.nb;
+  A.tile = 16 * p.th;
+  A.box = std::min(g.bs, A.tile);
   A.min_part = 2 * kWarps;
   const int64_t units = g.kvh * (tokens * A.R.grp / A.rows + nseq);  // at most
   if (units > INT32_MAX) return cudaErrorInvalidConfiguration;
-  auto nb = [&](auto kp, auto vp) {
-    return p.nb == 1 ? launch<kp(), vp(), 1>(g, a, A, units) : launch<kp(), vp(), 2>(g, a, A, units);
+  // tiles of 32 keys where a ring of them fits
+  auto go = [&](auto kp, auto vp) {
+    constexpr int TH = kp() <= 2 && vp() == 1 ? 2 : 1;
+    return p.nb == 1 ? launch<kp(), vp(), 1, TH>(g, a, A, units)
+                     : launch<kp(), vp(), 2, TH>(g, a, A, units);
   };
   auto vp = [&](auto kp) {
-    return p.vp == 1 ? nb(kp, std::integral_constant<int, 1>()) : nb(kp, std::integral_constant<int, 2>());
+    return p.vp == 1 ? go(kp, std::integral_constant<int, 1>()) : go(kp, std::integral_constant<int, 2>());
   };
   switch (p.kp) {
     case 1: return vp(std::integral_constant<int, 1>());
