@@ -734,24 +734,32 @@ quant_rows_kernel(const __grid_constant__ CUtensorMap kmap,
   }
 }
 
-// Joins the parts of a unit: a warp for four accumulators of a block of rows.
+// Joins the parts of a unit: a warp for four accumulators of a block of rows and every
+// kSlices-th part, then the slices.
+constexpr int kSlices = 4;
 template <int VP, int NB>
-__global__ void __launch_bounds__(64 * VP * NB)
+__global__ void __launch_bounds__(64 * VP * NB * kSlices)
 quant_combine_kernel(const __grid_constant__ DecP A) {
   grid_dep_wait();
   grid_dep_launch();
-  constexpr int kAcc = 8 * VP * NB, kRound = 4, R = 8 * NB;
+  constexpr int kTasks = 2 * VP * NB, kAcc = 8 * VP * NB, R = 8 * NB;
   const ReadP& P = A.R;
+  __shared__ float4 s_acc[kSlices - 1][kTasks][4][32];
+  __shared__ float4 s_ml[kSlices - 1][kTasks][32];
   const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
-  const int b = find_sequence(A.ws_units, P.nseq, blockIdx.x, lane);
-  if (b < 0) return;
+  const int task = (threadIdx.x >> 5) % kTasks, slice = (threadIdx.x >> 5) / kTasks;
+  // (in decode every sequence that is read has as many units)
+  const int per = P.kvh * ((P.grp + R - 1) / R);
+  const int b = A.decode ? blockIdx.x / per : find_sequence(A.ws_units, P.nseq, blockIdx.x, lane);
+  if (b < 0 || b >= P.nseq) return;
+  const int u = blockIdx.x - (A.decode ? b * per : A.ws_units[b]);
   const int64_t part = A.ws_line[P.nseq], before = A.ws_line[b];
-  const int u = blockIdx.x - A.ws_units[b];
   const Span sp = span_of(A, b);
+  if (sp.tiles == 0) return;
   const int64_t start = before + (int64_t)u * sp.tiles, end = start + sp.tiles;
   const int64_t c0 = start / part, c1 = (end - 1) / part;
   if (c0 == c1) return;
-  const int task = threadIdx.x >> 5, nb = task % NB, i0 = task / NB * 4;
+  const int nb = task % NB, i0 = task / NB * 4;
   const int g = u / sp.chunks, r0 = (u - g * sp.chunks) * R, nr = min(R, sp.q * P.grp - r0);
   const int h = nb * 8 + 2 * tq;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, acc[4][4];
@@ -760,44 +768,55 @@ quant_combine_kernel(const __grid_constant__ DecP A) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[k][e] = 0.f;
   bool bad = false;
-  for (int64_t c = c0; c <= c1; c += kRound) {
-    float4 o[kRound][4];
-    float4 ml[kRound];  // maximum and sum of heads h and h + 1
+  auto add = [&](const float4& ml, const float4 (&o)[4]) {  // maxima and sums of rows h, h + 1
+    const float pm[2] = {ml.x, ml.z}, pl[2] = {ml.y, ml.w};
+    float fa[2], fb[2];
 #pragma unroll
-    for (int r = 0; r < kRound; ++r) {
-      if (c + r > c1) continue;
-      const int64_t slot = 2 * (c + r) + (c + r == c0 && start > c0 * part ? 1 : 0);
-      ml[r] = *reinterpret_cast<const float4*>(A.ws_ml + slot * R + h);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[r][k] = A.ws_o[(slot * kAcc + (i0 + k) * NB + nb) * 32 + lane];
+    for (int e = 0; e < 2; ++e) {
+      bad |= isnan(pm[e]);
+      const float t = fmaxf(m[e], pm[e]), base = t == -INFINITY ? 0.f : t;
+      fa[e] = ex2(m[e] - base);
+      fb[e] = ex2(pm[e] - base);
+      m[e] = t;
+      l[e] = l[e] * fa[e] + pl[e] * fb[e];
     }
 #pragma unroll
-    for (int r = 0; r < kRound; ++r) {
-      if (c + r > c1) continue;
-      const float pm[2] = {ml[r].x, ml[r].z}, pl[2] = {ml[r].y, ml[r].w};
-      float fa[2], fb[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        bad |= isnan(pm[e]);
-        const float t = fmaxf(m[e], pm[e]), base = t == -INFINITY ? 0.f : t;
-        fa[e] = ex2(m[e] - base);
-        fb[e] = ex2(pm[e] - base);
-        m[e] = t;
-        l[e] = l[e] * fa[e] + pl[e] * fb[e];
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        acc[k][0] = acc[k][0] * fa[0] + o[r][k].x * fb[0];
-        acc[k][1] = acc[k][1] * fa[1] + o[r][k].y * fb[1];
-        acc[k][2] = acc[k][2] * fa[0] + o[r][k].z * fb[0];
-        acc[k][3] = acc[k][3] * fa[1] + o[r][k].w * fb[1];
-      }
+    for (int k = 0; k < 4; ++k) {
+      acc[k][0] = acc[k][0] * fa[0] + o[k].x * fb[0];
+      acc[k][1] = acc[k][1] * fa[1] + o[k].y * fb[1];
+      acc[k][2] = acc[k][2] * fa[0] + o[k].z * fb[0];
+      acc[k][3] = acc[k][3] * fa[1] + o[k].w * fb[1];
     }
+  };
+#pragma unroll 2
+  for (int64_t c = c0 + slice; c <= c1; c += kSlices) {
+    const int64_t slot = 2 * c + (c == c0 && start > c0 * part ? 1 : 0);
+    const float4 ml = *reinterpret_cast<const float4*>(A.ws_ml + slot * R + h);
+    float4 o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = A.ws_o[(slot * kAcc + (i0 + k) * NB + nb) * 32 + lane];
+    add(ml, o);
+  }
+  if (slice > 0) {
+    s_ml[slice - 1][task][lane] = make_float4(bad ? NAN : m[0], l[0], bad ? NAN : m[1], l[1]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      s_acc[slice - 1][task][k][lane] = make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
+  }
+  __syncthreads();
+  if (slice > 0) return;
+#pragma unroll 1
+  for (int s = 0; s < min((int64_t)(kSlices - 1), c1 - c0); ++s) {
+    float4 o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = s_acc[s][task][k][lane];
+    add(s_ml[s][task][lane], o);
   }
   float inv[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) inv[e] = inverse(P, g, r0, h + e, nr, m[e], l[e]);
-  store_rows(P, sp, g, r0, nr, h, (gq >> 1) + 4 * (gq & 1), i0, bad, inv, [&](int k, int e) { return acc[k][e]; });
+  store_rows(P, sp, g, r0, nr, h, (gq >> 1) + 4 * (gq & 1), i0, bad, inv,
+             [&](int k, int e) { return acc[k][e]; });
 }
 
 // ---------------------------------------------------------------------------
@@ -838,7 +857,7 @@ cudaError_t launch(const Geometry& g, const QuantArgs& a, const DecP& A, int64_t
   e = tc::launch_pdl(kern, dim3((unsigned)(g.num_sms * S::kCtas)), dim3(kThreads), S::kSmem,
                      a.stream, kmap, vmap, A);
   if (e != cudaSuccess) return e;
-  return tc::launch_pdl(quant_combine_kernel<VP, NB>, dim3((unsigned)units), dim3(64 * VP * NB), 0,
+  return tc::launch_pdl(quant_combine_kernel<VP, NB>, dim3((unsigned)units), dim3(64 * VP * NB * kSlices), 0,
                         a.stream, A);
 }
 
@@ -868,7 +887,9 @@ cudaError_t launch_rows(const Geometry& g, const QuantArgs& a, bool decode) {
   A.tile = 16 * p.th;
   A.box = std::min(g.bs, A.tile);
   A.min_part = 2 * kWarps;
-  const int64_t units = g.kvh * (tokens * A.R.grp / A.rows + nseq);  // at most
+  const int64_t units =
+      decode ? nseq * g.kvh * ((A.R.grp + A.rows - 1) / A.rows)
+             : g.kvh * (tokens * A.R.grp / A.rows + nseq);  // at most
   if (units > INT32_MAX) return cudaErrorInvalidConfiguration;
   // tiles of 32 keys where a ring of them fits
   auto go = [&](auto kp, auto vp) {
