@@ -29,6 +29,11 @@ constexpr int kMaxBlock = 4096;  // rows of a page
 // first(b) = 2 b + cumseq[b] / bs on. It has at most (q - 1) / bs + 2 runs, and
 // first(b + 1) - first(b) >= q / bs + 2. So a CTA finds its sequence by a search
 // over cumseq, 128 offsets at a time.
+//
+// Bound by HBM for prompts and by its chain of loads for single tokens. All rows of a
+// run are on their way to shared memory (cp.async) before its slots are looked at; each
+// thread copies just what it will read, so no barrier stands between. With a load per
+// row where it was used, 14500 new tokens of 8 kv heads of 128 / 128 took 66 us.
 // ---------------------------------------------------------------------------
 constexpr int kWriteThreads = 128;
 
@@ -49,8 +54,23 @@ struct WriteArgs {
   int num_seqs, kvh, hs, vhs, ro, rd, interleaved, cos_rows, bs, max_blocks;
   float eps;
   int lpr;  // lanes per row: a power of two >= max(hs, vhs) / 8
+  int cap;  // rows that shared memory holds at once
 };
 
+__device__ __forceinline__ uint32_t smem_address(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 load16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ float finite_max8(const float (&x)[8], float m) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -68,7 +88,8 @@ template <typename T>
 __global__ void __launch_bounds__(kWriteThreads)
 quant_write_kernel(const __grid_constant__ WriteArgs A) {
   asm volatile("griddepcontrol.wait;\n griddepcontrol.launch_dependents;" ::: "memory");
-  extern __shared__ uint8_t s_new[];  // [bs] rows of the page that the call writes
+  extern __shared__ __align__(16) uint8_t s_rows[];  // [cap] keys, values; then s_new
+  uint8_t* s_new = s_rows + (size_t)A.cap * (A.hs + A.vhs) * 2;  // [bs] rows that the call writes
   __shared__ int s_first;
   __shared__ float s_max[2][kWriteThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -102,6 +123,26 @@ quant_write_kernel(const __grid_constant__ WriteArgs A) {
   const int n = (int)(end - begin), row0 = (int)(begin & (bs - 1));
   const int64_t t0 = c0 + (begin - p0);
 
+  const int lpr = A.lpr, rows_at_once = kWriteThreads / lpr, mine = tid / lpr;
+  const int d0 = (tid & (lpr - 1)) * 8;
+  const int64_t kstep = (int64_t)A.kvh * A.hs, vstep = (int64_t)A.kvh * A.vhs;
+  const T* key = reinterpret_cast<const T*>(A.key) + t0 * kstep + (int64_t)g * A.hs + d0;
+  const T* value = reinterpret_cast<const T*>(A.value) + t0 * vstep + (int64_t)g * A.vhs + d0;
+  const uint32_t k_at = smem_address(s_rows) + d0 * 2, v_at = k_at + A.cap * A.hs * 2;
+  auto fetch = [&](int j0) {  // rows j0 .. j0 + cap
+    for (int j = j0 + mine; j < min(n, j0 + A.cap); j += rows_at_once) {
+      if (d0 < A.hs) copy16(k_at + (j - j0) * A.hs * 2, key + j * kstep);
+      if (d0 < A.vhs) copy16(v_at + (j - j0) * A.vhs * 2, value + j * vstep);
+      if (A.rd > 0 && begin + j < A.cos_rows && d0 * 8 < A.rd >> 1) {
+        // (64 angles a line; lanes 0, 1, ..)
+        const int64_t a = (begin + j) * (A.rd >> 1) + d0 * 8;
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(reinterpret_cast<const T*>(A.cos_cache) + a));
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(reinterpret_cast<const T*>(A.sin_cache) + a));
+      }
+    }
+  };
+  fetch(0);
+
   // rows that the call writes: tokens with a slot of the page that the run's
   // first one names
   for (int r = tid; r < bs; r += kWriteThreads) s_new[r] = 0;
@@ -131,38 +172,40 @@ quant_write_kernel(const __grid_constant__ WriteArgs A) {
       }
   }
   if (err && tells) raise_flag(A.err_flags, err);
-  if (first_j >= n) return;
+  if (first_j >= n) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
   const int64_t page = A.slot_mapping[t0 + first_j] >> sh;
   __syncthreads();
 
-  const int lpr = A.lpr, rows_at_once = kWriteThreads / lpr, mine = tid / lpr;
-  const int d0 = (tid & (lpr - 1)) * 8;
-  const int64_t kstep = (int64_t)A.kvh * A.hs, vstep = (int64_t)A.kvh * A.vhs;
-  const T* key = reinterpret_cast<const T*>(A.key) + t0 * kstep + (int64_t)g * A.hs + d0;
-  const T* value = reinterpret_cast<const T*>(A.value) + t0 * vstep + (int64_t)g * A.vhs + d0;
-  auto load = [&](const T* src, bool there, float (&x)[8]) {
-    if (there) {
-      unpack8<T>(*reinterpret_cast<const uint4*>(src), x);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = 0.f;
+  float2* scale = A.scales + page * A.kvh + g;
+  const float2 was = s_new[0] ? make_float2(0.f, 0.f) : *scale;
+  auto rows = [&](int j0, auto&& use) {  // use(j, row, key, value) for this thread's rows
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    for (int j1 = 0; j1 < A.cap && j0 + j1 < n; j1 += rows_at_once) {
+      const int j = j0 + j1 + mine;
+      const bool row = j < n && s_new[row0 + j];
+      float x[8], v[8];
+      uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
+      if (row && d0 < A.hs) kw = load16(k_at + (j - j0) * A.hs * 2);
+      if (row && d0 < A.vhs) vw = load16(v_at + (j - j0) * A.vhs * 2);
+      unpack8<T>(kw, x);
+      unpack8<T>(vw, v);
+      norm_rotate8<T>(x, row, d0, A.hs, lpr, reinterpret_cast<const T*>(A.k_norm), A.eps, A.ro, A.rd,
+                      A.interleaved, reinterpret_cast<const T*>(A.cos_cache),
+                      reinterpret_cast<const T*>(A.sin_cache), begin + j);
+      use(j, row, x, v);
     }
   };
-  auto key8 = [&](int j, bool row, float (&x)[8]) {
-    load(key + j * kstep, row && d0 < A.hs, x);
-    norm_rotate8<T>(x, row, d0, A.hs, lpr, reinterpret_cast<const T*>(A.k_norm), A.eps, A.ro, A.rd,
-                    A.interleaved, reinterpret_cast<const T*>(A.cos_cache),
-                    reinterpret_cast<const T*>(A.sin_cache), begin + j);
-  };
   float km = 0.f, vm = 0.f;
-  for (int j0 = 0; j0 < n; j0 += rows_at_once) {
-    const int j = j0 + mine;
-    const bool row = j < n && s_new[row0 + j];
-    float x[8], v[8];
-    load(value + j * vstep, row && d0 < A.vhs, v);
-    key8(j, row, x);
-    km = finite_max8(x, km);
-    vm = finite_max8(v, vm);
+#pragma unroll 1
+  for (int j0 = 0; j0 < n; j0 += A.cap) {
+    if (j0 > 0) fetch(j0);
+    rows(j0, [&](int, bool, const float (&x)[8], const float (&v)[8]) {
+      km = finite_max8(x, km);
+      vm = finite_max8(v, vm);
+    });
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -179,23 +222,20 @@ quant_write_kernel(const __grid_constant__ WriteArgs A) {
     km = fmaxf(km, s_max[0][w]);
     vm = fmaxf(vm, s_max[1][w]);
   }
-  float2* scale = A.scales + page * A.kvh + g;
-  const float2 was = s_new[0] ? make_float2(0.f, 0.f) : *scale;
   const int ko = scale_exponent(was.x), vo = scale_exponent(was.y);
   const int ke = max(ko, needed_exponent(km)), ve = max(vo, needed_exponent(vm));
   uint8_t* kpage = A.key_cache + page * bs * kstep + (int64_t)g * A.hs;
   uint8_t* vpage = A.value_cache + page * bs * vstep + (int64_t)g * A.vhs;
   const float kinv = pow2(-ke), vinv = pow2(-ve);
-  for (int j0 = 0; j0 < n; j0 += rows_at_once) {
-    const int j = j0 + mine;
-    const bool row = j < n && s_new[row0 + j];
-    float x[8], v[8];
-    load(value + j * vstep, row && d0 < A.vhs, v);
-    key8(j, row, x);
-    if (row && d0 < A.hs)
-      *reinterpret_cast<uint2*>(kpage + (row0 + j) * kstep + d0) = encode8(x, kinv);
-    if (row && d0 < A.vhs)
-      *reinterpret_cast<uint2*>(vpage + (row0 + j) * vstep + d0) = encode8(v, vinv);
+#pragma unroll 1
+  for (int j0 = 0; j0 < n; j0 += A.cap) {
+    if (n > A.cap) fetch(j0);  // (else it is still there)
+    rows(j0, [&](int j, bool row, const float (&x)[8], const float (&v)[8]) {
+      if (row && d0 < A.hs)
+        *reinterpret_cast<uint2*>(kpage + (row0 + j) * kstep + d0) = encode8(x, kinv);
+      if (row && d0 < A.vhs)
+        *reinterpret_cast<uint2*>(vpage + (row0 + j) * vstep + d0) = encode8(v, vinv);
+    });
   }
   auto shrink = [&](uint8_t* at, int64_t step, int width, float f) {
     const int pieces = width >> 4;
@@ -214,7 +254,7 @@ quant_write_kernel(const __grid_constant__ WriteArgs A) {
 }
 
 // ---------------------------------------------------------------------------
-// Reading back: a warp per token, 16 codes a lane.
+// Reading back: a warp for a few tokens in a row, 16 codes a lane. Bound by HBM.
 // ---------------------------------------------------------------------------
 struct RestoreArgs {
   const uint8_t* key_cache;
@@ -268,25 +308,40 @@ quant_restore_kernel(const __grid_constant__ RestoreArgs A) {
   if (blockIdx.x == 0 && threadIdx.x == 0 &&
       (A.cumseq[0] != 0 || A.cumseq[A.num_seqs] != A.num_tokens))
     raise_flag(A.err_flags, PA_DEVERR_CUMSEQ);
-  for (int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); t < A.num_tokens;
-       t += warps) {
-    const int b = find_sequence(A.cumseq, A.num_seqs, t, lane);
-    if (b < 0) {
-      if (lane == 0) raise_flag(A.err_flags, PA_DEVERR_CUMSEQ);
-      continue;
+  // tokens [first, last) of this warp: the search and the table's entries serve several
+  const int64_t each = (A.num_tokens + warps - 1) / warps;
+  const int64_t first = ((int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * each;
+  const int64_t last = min(A.num_tokens, first + each);
+  int b = -1;
+  int64_t c0 = 0, c1 = 0, past = 0, block = -1;
+  int32_t page = -1;
+  for (int64_t t = first; t < last; ++t) {
+    if (t >= c1 || b < 0) {
+      b = find_sequence(A.cumseq, A.num_seqs, t, lane);
+      if (b < 0) {
+        if (lane == 0) raise_flag(A.err_flags, PA_DEVERR_CUMSEQ);
+        continue;
+      }
+      c0 = A.cumseq[b];
+      c1 = A.cumseq[b + 1];
+      past = A.past[b];
+      block = -1;
     }
-    const int64_t pos = (int64_t)A.past[b] + (t - A.cumseq[b]);
-    int32_t page = -1;
+    const int64_t pos = past + (t - c0);
     if (pos < 0 || pos >= (int64_t)A.max_blocks * A.bs) {
       if (lane == 0) raise_flag(A.err_flags, PA_DEVERR_CONTEXT);
-    } else {
-      page = A.block_table[(int64_t)b * A.max_blocks + (pos >> sh)];
+      page = -1;
+      block = -1;
+    } else if (pos >> sh != block) {
+      block = pos >> sh;
+      page = A.block_table[(int64_t)b * A.max_blocks + block];
       if (page < 0 || page >= A.num_blocks) {
         if (lane == 0) raise_flag(A.err_flags, PA_DEVERR_BLOCK);
         page = -1;
       }
     }
     const int64_t row = (int64_t)page * A.bs + (pos & (A.bs - 1));
+#pragma unroll 4
     for (int i = lane; i < kn + vn; i += 32) {
       const bool is_key = i < kn;
       const int at = is_key ? i : i - kn, per = is_key ? kp : vp;
@@ -476,19 +531,23 @@ pa_status pa_quant_write(const pa_quant_params* p, const void* key, const void* 
     return fail(PA_ERR_INVALID_ARGUMENT, "int32 tensors must be 4-byte aligned");
   int lpr = 2;
   while (lpr * 8 < g.hs || lpr * 8 < g.vhs) lpr *= 2;
+  const int row_bytes = (g.hs + g.vhs) * 2, at_once = quant::kWriteThreads / lpr;
+  int cap = 32768 / row_bytes / at_once * at_once;  // (at least 32 rows of 1 KB)
+  if (cap > g.bs) cap = (g.bs + at_once - 1) / at_once * at_once;
+  const size_t smem = (size_t)cap * row_bytes + g.bs;
   const quant::WriteArgs A{key, value, cos_cache, sin_cache, k_norm_weight, slot_mapping, cumseq,
                            past, (uint8_t*)key_cache, (uint8_t*)value_cache, (float2*)scales,
                            err_flags, num_tokens, (int64_t)g.num_blocks * g.bs, num_seqs, g.kvh,
                            g.hs, g.vhs, g.ro, g.rd, g.interleaved, g.cos_rows, g.bs, g.max_blocks,
-                           g.rms_eps, lpr};
+                           g.rms_eps, lpr, cap};
   // (first(num_seqs) numbers; see the kernel)
   const int64_t runs = 2 * (int64_t)num_seqs + num_tokens / g.bs;
   const dim3 grid((unsigned)runs, (unsigned)g.kvh);
   return g.dtype == PA_DTYPE_BF16
              ? quant::launch(quant::quant_write_kernel<__nv_bfloat16>, grid, quant::kWriteThreads,
-                             (size_t)g.bs, stream, A, "8-bit write launch")
+                             smem, stream, A, "8-bit write launch")
              : quant::launch(quant::quant_write_kernel<__half>, grid, quant::kWriteThreads,
-                             (size_t)g.bs, stream, A, "8-bit write launch");
+                             smem, stream, A, "8-bit write launch");
 }
 
 pa_status pa_quant_restore(const pa_quant_params* p, const void* key_cache,
