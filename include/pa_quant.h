@@ -131,6 +131,18 @@ pa_status pa_quant_prefill(const pa_quant_params* p, const void* query, int64_t 
                            int32_t num_seqs, int32_t seq_begin, int32_t seq_end, void* workspace,
                            size_t workspace_bytes, void* out, int32_t* err_flags, void* stream);
 
+/* One step of a serving batch in one call: pa_quant_write over all tokens, then
+ * pa_quant_decode over sequences [0, num_decode_seqs) and pa_quant_prefill over the
+ * rest, with the flags of a read that follows the write. Not with cross. */
+pa_status pa_quant_mixed(const pa_quant_params* p, const void* query, const void* key,
+                         const void* value, int64_t num_tokens, const void* cos_cache,
+                         const void* sin_cache, const void* q_norm_weight,
+                         const void* k_norm_weight, const void* head_sink,
+                         const int32_t* slot_mapping, const int32_t* cumseq, const int32_t* past,
+                         const int32_t* block_table, int32_t num_seqs, int32_t num_decode_seqs,
+                         void* key_cache, void* value_cache, float* scales, void* workspace,
+                         size_t workspace_bytes, void* out, int32_t* err_flags, void* stream);
+
 /* Workspace bytes a decode or prefill call over at most num_seqs sequences
  * and num_tokens tokens needs on the current device; 0 for invalid
  * parameters. */

@@ -668,23 +668,15 @@ class QuantizedAttention:
             self._check_read(query, past, block_table, out, head_sink, q_norm_weight)
             if self._filled is not None:
                 self._begin(stream)
-            self._reads(query, key_cache, value_cache, scales, cos_cache, sin_cache, cumseq, past,
-                        block_table, num_decode_seqs, nseq, head_sink, q_norm_weight, out, stream,
-                        False)
+            args = (query, key_cache, value_cache, scales, cos_cache, sin_cache, q_norm_weight,
+                    head_sink, cumseq, past, block_table, out)
+            if num_decode_seqs > 0:
+                B.pa_quant_decode(self.params, *args, 0, num_decode_seqs, self.workspace,
+                                  self.err_flags, stream)
+            if num_decode_seqs < nseq:
+                B.pa_quant_prefill(self.params, *args, num_decode_seqs, nseq, self.workspace,
+                                   self.err_flags, stream)
         return out
-
-    def _reads(self, query, key_cache, value_cache, scales, cos_cache, sin_cache, cumseq, past,
-               block_table, num_decode_seqs, nseq, head_sink, q_norm_weight, out, stream, after):
-        p = self.params_after_write if after else self.params
-        if num_decode_seqs > 0:
-            B.pa_quant_decode(p, query, key_cache, value_cache, scales, cos_cache, sin_cache,
-                              q_norm_weight, head_sink, cumseq, past, block_table, out, 0,
-                              num_decode_seqs, self.workspace, self.err_flags, stream)
-            p = self.params
-        if num_decode_seqs < nseq:
-            B.pa_quant_prefill(p, query, key_cache, value_cache, scales, cos_cache, sin_cache,
-                               q_norm_weight, head_sink, cumseq, past, block_table, out,
-                               num_decode_seqs, nseq, self.workspace, self.err_flags, stream)
 
     def forward(self, query, key, value, key_cache, value_cache, scales, cos_cache, sin_cache,
                 cumseq, past, block_table, slot_mapping, num_decode_seqs: int, head_sink=None,
@@ -705,12 +697,10 @@ class QuantizedAttention:
             self._check_read(query, past, block_table, out, head_sink, q_norm_weight)
             if self._filled is not None:
                 self._begin(stream)
-            B.pa_quant_write(self.params, key, value, cos_cache, sin_cache, k_norm_weight,
-                             slot_mapping, cumseq, past, key_cache, value_cache, scales,
+            B.pa_quant_mixed(self.params, query, key, value, cos_cache, sin_cache, q_norm_weight,
+                             k_norm_weight, head_sink, slot_mapping, cumseq, past, block_table,
+                             num_decode_seqs, key_cache, value_cache, scales, self.workspace, out,
                              self.err_flags, stream)
-            self._reads(query, key_cache, value_cache, scales, cos_cache, sin_cache, cumseq, past,
-                        block_table, num_decode_seqs, nseq, head_sink, q_norm_weight, out, stream,
-                        True)
         return out
 
     def error_flags(self) -> int:

@@ -61,7 +61,7 @@ EXPORTED_DIFF = ("pa_diff_validate", "pa_diff_write", "pa_diff_decode", "pa_diff
 
 # include/pa_quant.h
 EXPORTED_QUANT = ("pa_quant_validate", "pa_quant_write", "pa_quant_restore", "pa_quant_decode",
-                  "pa_quant_prefill", "pa_quant_workspace_size")
+                  "pa_quant_prefill", "pa_quant_mixed", "pa_quant_workspace_size")
 
 PA_DEVERR_POOL = 0x100
 PA_DEVERR_PAGE = 0x200
@@ -245,6 +245,8 @@ def _load() -> ctypes.CDLL:
     qread = [Q, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, sz, vp, vp, vp]
     lib.pa_quant_decode.argtypes = qread
     lib.pa_quant_prefill.argtypes = qread
+    lib.pa_quant_mixed.argtypes = [Q, vp, vp, vp, i64] + [vp] * 9 + [i32, i32, vp, vp, vp, vp, sz, vp,
+                                                                     vp, vp]
     lib.pa_quant_workspace_size.argtypes = [Q, i32, i64]
     lib.pa_quant_workspace_size.restype = sz
     for name in EXPORTED_PAGES + EXPORTED_DIFF + EXPORTED_QUANT:
@@ -634,6 +636,19 @@ def _quant_read(fn):
                   block_table.data_ptr(), n, seq_begin, n if seq_end is None else seq_end, ws,
                   ws_bytes, out.data_ptr(), _addr(err_flags), raw_stream(stream)))
     return read
+
+
+def pa_quant_mixed(p, query, key, value, cos_cache, sin_cache, q_norm_weight, k_norm_weight,
+                   head_sink, slot_mapping, cumseq, past, block_table, num_decode_seqs, key_cache,
+                   value_cache, scales, workspace, out, err_flags=None, stream=None):
+    ws, ws_bytes = _ws(workspace)
+    _check(lib.pa_quant_mixed(
+        ctypes.byref(p), query.data_ptr(), key.data_ptr(), value.data_ptr(), query.size(0),
+        _addr(cos_cache), _addr(sin_cache), _addr(q_norm_weight), _addr(k_norm_weight),
+        _addr(head_sink), slot_mapping.data_ptr(), cumseq.data_ptr(), past.data_ptr(),
+        block_table.data_ptr(), past.size(0), num_decode_seqs, key_cache.data_ptr(),
+        value_cache.data_ptr(), scales.data_ptr(), ws, ws_bytes, out.data_ptr(), _addr(err_flags),
+        raw_stream(stream)))
 
 
 pa_quant_decode = _quant_read(lib.pa_quant_decode)

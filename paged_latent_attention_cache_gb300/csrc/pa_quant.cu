@@ -446,8 +446,10 @@ pa_status launch(K kernel, dim3 grid, int threads, size_t smem, void* stream, co
   return fail(PA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-pa_status read(Phase ph, const pa_quant_params* p, QuantArgs a) {
-  Geometry g;
+// The checks of a read call; g: the geometry, a.cross is filled in.
+pa_status check_read(Phase ph, const pa_quant_params* p, QuantArgs* args, Geometry* geometry) {
+  QuantArgs& a = *args;
+  Geometry& g = *geometry;
   pa_status s = resolve(p, &g);
   if (s == PA_OK) s = check_tokens(a.num_tokens, a.num_seqs, g);
   if (s != PA_OK) return s;
@@ -482,12 +484,23 @@ pa_status read(Phase ph, const pa_quant_params* p, QuantArgs a) {
     return fail(PA_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu needed",
                 a.workspace ? a.workspace_bytes : (size_t)0, need);
   a.cross = p->cross;
+  return PA_OK;
+}
+
+pa_status launch_read(Phase ph, const Geometry& g, const QuantArgs& a) {
+  if (a.num_tokens == 0 || a.seq_end == a.seq_begin) return PA_OK;
   const cudaError_t e = ph == Phase::kDecode ? launch_rows(g, a, true) : launch_prefill(g, a);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();  // not left behind for a later call
     return fail(PA_ERR_CUDA, "attention over an 8-bit cache: %s", cudaGetErrorString(e));
   }
   return PA_OK;
+}
+
+pa_status read(Phase ph, const pa_quant_params* p, QuantArgs a) {
+  Geometry g;
+  const pa_status s = check_read(ph, p, &a, &g);
+  return s == PA_OK ? launch_read(ph, g, a) : s;
 }
 
 }  // namespace
@@ -615,6 +628,42 @@ pa_status pa_quant_prefill(const pa_quant_params* p, const void* query, int64_t 
                                       cos_cache, sin_cache, q_norm_weight, head_sink, cumseq, past,
                                       block_table, num_seqs, seq_begin, seq_end, workspace,
                                       workspace_bytes, out, err_flags, (cudaStream_t)stream, 0});
+}
+
+pa_status pa_quant_mixed(const pa_quant_params* p, const void* query, const void* key,
+                         const void* value, int64_t num_tokens, const void* cos_cache,
+                         const void* sin_cache, const void* q_norm_weight,
+                         const void* k_norm_weight, const void* head_sink,
+                         const int32_t* slot_mapping, const int32_t* cumseq, const int32_t* past,
+                         const int32_t* block_table, int32_t num_seqs, int32_t num_decode_seqs,
+                         void* key_cache, void* value_cache, float* scales, void* workspace,
+                         size_t workspace_bytes, void* out, int32_t* err_flags, void* stream) {
+  using quant::fail;
+  if (!p) return fail(PA_ERR_INVALID_ARGUMENT, "params is NULL");
+  if (p->cross)
+    return fail(PA_ERR_INVALID_ARGUMENT, "cross attention writes and reads in calls of their own");
+  if (num_decode_seqs < 0 || num_decode_seqs > num_seqs)
+    return fail(PA_ERR_INVALID_ARGUMENT, "num_decode_seqs %d outside [0, %d]", num_decode_seqs,
+                num_seqs);
+  // what the reads would refuse is refused before the write is enqueued
+  quant::QuantArgs a{query, num_tokens, (const uint8_t*)key_cache, (const uint8_t*)value_cache,
+                     (const float2*)scales, cos_cache, sin_cache, q_norm_weight, head_sink, cumseq,
+                     past, block_table, num_seqs, 0, num_decode_seqs, workspace, workspace_bytes,
+                     out, err_flags, (cudaStream_t)stream, 0};
+  quant::QuantArgs b = a;
+  b.seq_begin = num_decode_seqs;
+  b.seq_end = num_seqs;
+  Geometry g;
+  pa_status s = quant::check_read(Phase::kDecode, p, &a, &g);
+  if (s == PA_OK) s = quant::check_read(Phase::kPrefill, p, &b, &g);
+  if (s == PA_OK)
+    s = pa_quant_write(p, key, value, num_tokens, cos_cache, sin_cache, k_norm_weight, slot_mapping,
+                       cumseq, past, num_seqs, key_cache, value_cache, scales, err_flags, stream);
+  if (s != PA_OK) return s;
+  g.flags |= PA_FLAG_AFTER_WRITE;
+  if ((s = quant::launch_read(Phase::kDecode, g, a)) != PA_OK) return s;
+  if (num_decode_seqs > 0) g.flags &= ~PA_FLAG_AFTER_WRITE;
+  return quant::launch_read(Phase::kPrefill, g, b);
 }
 
 size_t pa_quant_workspace_size(const pa_quant_params* p, int32_t num_seqs, int64_t num_tokens) {

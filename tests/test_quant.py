@@ -129,6 +129,28 @@ def test_write_and_restore_refused(B):
     assert B.lib.pa_quant_restore(ctypes.byref(p), *good) == B.PA_OK  # nothing asked for
 
 
+def test_mixed_refused(B):
+    vp = ctypes.c_void_p
+    good = [vp(0x10000), vp(0x18000), vp(0x20000), 4, vp(0x28000), vp(0x30000), None, None, None, vp(0x38000), vp(0x40000),
+            vp(0x50000), vp(0x60000), 2, 1, vp(0x70000), vp(0x80000), vp(0x88000), vp(0x100000), ctypes.c_size_t(1 << 40),
+            vp(0x90000), vp(0xa0000), None]
+    for i, v, needle in [(0, None, "NULL"), (1, None, "NULL"), (2, None, "NULL"), (9, None, "NULL"), (12, None, "NULL"),
+                         (20, None, "NULL"), (4, None, "cos_cache"), (0, vp(0x10008), "16-byte"), (1, vp(0x18008), "16-byte"),
+                         (6, vp(0x18008), "16-byte"), (7, vp(0x18008), "16-byte"), (17, vp(0x88004), "8-byte"),
+                         (9, vp(0x38002), "4-byte"), (14, 3, "num_decode_seqs"), (14, -1, "num_decode_seqs"),
+                         (3, -1, "num_tokens"), (18, vp(0x100010), "256-byte")]:
+        a = list(good)
+        a[i] = v
+        assert B.lib.pa_quant_mixed(ctypes.byref(_params(B)), *a) == B.PA_ERR_INVALID_ARGUMENT, (i, B.last_error())
+        assert needle in B.last_error(), (i, B.last_error())
+    a = list(good)
+    a[19] = ctypes.c_size_t(16)
+    assert B.lib.pa_quant_mixed(ctypes.byref(_params(B)), *a) == B.PA_ERR_WORKSPACE
+    assert B.lib.pa_quant_mixed(ctypes.byref(_params(B, cross=1, rotary_dim=0)), *good) == B.PA_ERR_INVALID_ARGUMENT
+    good[3] = 0
+    assert B.lib.pa_quant_mixed(ctypes.byref(_params(B)), *good) == B.PA_OK
+
+
 def test_page_tensors_of_whole_pages(B):
     p = B.make_pages_params(num_blocks=8, block_size=16, max_blocks_per_seq=4, num_seqs=4)
     def copy(page_bytes):

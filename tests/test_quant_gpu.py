@@ -396,6 +396,20 @@ def test_cross_after_its_write():
         _check_out(out, ref, tol)
 
 
+def test_one_call_is_three():
+    """forward against write, decode and prefill by themselves."""
+    c = Case([1, 1, 40, 2], [10, 300, 64, 20], sink=True, norm=True, seed=28)
+    t, op = c.tensors(), c.op()
+    want = c.forward(op, t, 2)
+    t, out = c.tensors(), torch.empty_like(want)
+    op.write(t["key"], t["value"], t["kc"], t["vc"], t["scales"], t["cos"], t["sin"], t["slots"], t["cum"], t["past"],
+             k_norm_weight=t["k_norm"])
+    args = (t["query"], t["kc"], t["vc"], t["scales"], t["cos"], t["sin"], t["cum"], t["past"], t["table"], out)
+    op.decode(*args, 0, 2, head_sink=t["sink"], q_norm_weight=t["q_norm"], after_write=True)
+    op.prefill(*args, 2, 4, head_sink=t["sink"], q_norm_weight=t["q_norm"])
+    assert op.error_flags() == 0 and torch.equal(out, want)
+
+
 def test_mixed_batch():
     c = Case([1, 1, 1, 50, 9], [10, 300, 64, 20, 0], sink=True, seed=13)
     _run(c, 3)
