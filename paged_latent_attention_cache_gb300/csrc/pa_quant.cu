@@ -32,10 +32,12 @@ constexpr int kMaxBlock = 4096;  // rows of a page
 //
 // Bound by HBM for prompts and by its chain of loads for single tokens. All rows of a
 // run are on their way to shared memory (cp.async) before its slots are looked at; each
-// thread copies just what it will read, so no barrier stands between. With a load per
-// row where it was used, 14500 new tokens of 8 kv heads of 128 / 128 took 66 us.
+// thread copies just what it will read, so no barrier stands between. The rotated keys
+// stay there in f32 for their encoding. With a load per row where it was used, 14200 new
+// tokens of 8 kv heads of 128 / 128 took 66 us, with keys rotated twice 52.
 // ---------------------------------------------------------------------------
 constexpr int kWriteThreads = 128;
+constexpr int kRowBytes = 48 * 1024;  // of shared memory for rows
 
 struct WriteArgs {
   const void* key;
@@ -71,6 +73,27 @@ __device__ __forceinline__ uint4 load16(uint32_t a) {
                : "memory");
   return v;
 }
+__device__ __forceinline__ void store16(uint32_t a, const float* x) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+               "f"(x[3])
+               : "memory");
+}
+// The larger magnitudes of two pairs (NaN loses), and of the two of a pair.
+template <typename T>
+__device__ __forceinline__ uint32_t max_pairs(uint32_t a, uint32_t b) {
+  a &= 0x7fff7fffu;
+  b &= 0x7fff7fffu;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+  else
+    asm("max.f16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+  return a;
+}
+template <typename T>
+__device__ __forceinline__ float max_pair(uint32_t a) {
+  const T* h = reinterpret_cast<const T*>(&a);
+  return fmaxf(Half<T>::to_f32(h[0]), Half<T>::to_f32(h[1]));
+}
 __device__ __forceinline__ float finite_max8(const float (&x)[8], float m) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -88,8 +111,8 @@ template <typename T>
 __global__ void __launch_bounds__(kWriteThreads)
 quant_write_kernel(const __grid_constant__ WriteArgs A) {
   asm volatile("griddepcontrol.wait;\n griddepcontrol.launch_dependents;" ::: "memory");
-  extern __shared__ __align__(16) uint8_t s_rows[];  // [cap] keys, values; then s_new
-  uint8_t* s_new = s_rows + (size_t)A.cap * (A.hs + A.vhs) * 2;  // [bs] rows that the call writes
+  extern __shared__ __align__(16) uint8_t s_rows[];  // [cap] keys (then the first half of their f32 words), the others, values; s_new
+  uint8_t* s_new = s_rows + (size_t)A.cap * (2 * A.hs + A.vhs) * 2;  // [bs] rows that the call writes
   __shared__ int s_first;
   __shared__ float s_max[2][kWriteThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -128,7 +151,8 @@ quant_write_kernel(const __grid_constant__ WriteArgs A) {
   const int64_t kstep = (int64_t)A.kvh * A.hs, vstep = (int64_t)A.kvh * A.vhs;
   const T* key = reinterpret_cast<const T*>(A.key) + t0 * kstep + (int64_t)g * A.hs + d0;
   const T* value = reinterpret_cast<const T*>(A.value) + t0 * vstep + (int64_t)g * A.vhs + d0;
-  const uint32_t k_at = smem_address(s_rows) + d0 * 2, v_at = k_at + A.cap * A.hs * 2;
+  const uint32_t k_at = smem_address(s_rows) + d0 * 2, k_more = A.cap * A.hs * 2;
+  const uint32_t v_at = k_at + 2 * k_more;
   auto fetch = [&](int j0) {  // rows j0 .. j0 + cap
     for (int j = j0 + mine; j < min(n, j0 + A.cap); j += rows_at_once) {
       if (d0 < A.hs) copy16(k_at + (j - j0) * A.hs * 2, key + j * kstep);
@@ -181,31 +205,50 @@ quant_write_kernel(const __grid_constant__ WriteArgs A) {
 
   float2* scale = A.scales + page * A.kvh + g;
   const float2 was = s_new[0] ? make_float2(0.f, 0.f) : *scale;
-  auto rows = [&](int j0, auto&& use) {  // use(j, row, key, value) for this thread's rows
+  // Largest magnitudes of rows j0 .. j0 + cap; the keys rotated.
+  float km = 0.f, vm = 0.f;
+  auto transform = [&](int j0, bool finite) {
     asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 2
     for (int j1 = 0; j1 < A.cap && j0 + j1 < n; j1 += rows_at_once) {
       const int j = j0 + j1 + mine;
       const bool row = j < n && s_new[row0 + j];
-      float x[8], v[8];
+      const uint32_t k = k_at + (j1 + mine) * A.hs * 2;
+      float x[8];
       uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
-      if (row && d0 < A.hs) kw = load16(k_at + (j - j0) * A.hs * 2);
-      if (row && d0 < A.vhs) vw = load16(v_at + (j - j0) * A.vhs * 2);
+      if (row && d0 < A.hs) kw = load16(k);
+      if (row && d0 < A.vhs) vw = load16(v_at + (j1 + mine) * A.vhs * 2);
       unpack8<T>(kw, x);
-      unpack8<T>(vw, v);
       norm_rotate8<T>(x, row, d0, A.hs, lpr, reinterpret_cast<const T*>(A.k_norm), A.eps, A.ro, A.rd,
                       A.interleaved, reinterpret_cast<const T*>(A.cos_cache),
                       reinterpret_cast<const T*>(A.sin_cache), begin + j);
-      use(j, row, x, v);
+      if (row && d0 < A.hs) {
+        store16(k, x);
+        store16(k + k_more, x + 4);
+      }
+      if (finite) {
+        float v[8];
+        unpack8<T>(vw, v);
+        km = finite_max8(x, km);
+        vm = finite_max8(v, vm);
+      } else {  // (NaN loses a comparison, an infinity shows)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) km = fmaxf(km, fabsf(x[e]));
+        vm = fmaxf(vm, max_pair<T>(max_pairs<T>(max_pairs<T>(vw.x, vw.y), max_pairs<T>(vw.z, vw.w))));
+      }
     }
   };
-  float km = 0.f, vm = 0.f;
+  auto transform_all = [&](bool finite, bool again) {
 #pragma unroll 1
-  for (int j0 = 0; j0 < n; j0 += A.cap) {
-    if (j0 > 0) fetch(j0);
-    rows(j0, [&](int, bool, const float (&x)[8], const float (&v)[8]) {
-      km = finite_max8(x, km);
-      vm = finite_max8(v, vm);
-    });
+    for (int j0 = 0; j0 < n; j0 += A.cap) {
+      if (j0 > 0 || again) fetch(j0);
+      transform(j0, finite);
+    }
+  };
+  transform_all(false, false);
+  if (__syncthreads_or(km == INFINITY || vm == INFINITY)) {  // the largest finite ones then
+    km = vm = 0.f;
+    transform_all(true, true);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -229,13 +272,29 @@ quant_write_kernel(const __grid_constant__ WriteArgs A) {
   const float kinv = pow2(-ke), vinv = pow2(-ve);
 #pragma unroll 1
   for (int j0 = 0; j0 < n; j0 += A.cap) {
-    if (n > A.cap) fetch(j0);  // (else it is still there)
-    rows(j0, [&](int j, bool row, const float (&x)[8], const float (&v)[8]) {
-      if (row && d0 < A.hs)
+    if (n > A.cap) {  // (else they are still there)
+      fetch(j0);
+      transform(j0, true);
+    }
+#pragma unroll 2
+    for (int j1 = 0; j1 < A.cap && j0 + j1 < n; j1 += rows_at_once) {
+      const int j = j0 + j1 + mine;
+      if (j >= n || !s_new[row0 + j]) continue;
+      float x[8];
+      if (d0 < A.hs) {
+        const uint32_t k = k_at + (j1 + mine) * A.hs * 2;
+        const uint4 a = load16(k), b = load16(k + k_more);
+        x[0] = __uint_as_float(a.x); x[1] = __uint_as_float(a.y);
+        x[2] = __uint_as_float(a.z); x[3] = __uint_as_float(a.w);
+        x[4] = __uint_as_float(b.x); x[5] = __uint_as_float(b.y);
+        x[6] = __uint_as_float(b.z); x[7] = __uint_as_float(b.w);
         *reinterpret_cast<uint2*>(kpage + (row0 + j) * kstep + d0) = encode8(x, kinv);
-      if (row && d0 < A.vhs)
-        *reinterpret_cast<uint2*>(vpage + (row0 + j) * vstep + d0) = encode8(v, vinv);
-    });
+      }
+      if (d0 < A.vhs) {
+        unpack8<T>(load16(v_at + (j1 + mine) * A.vhs * 2), x);
+        *reinterpret_cast<uint2*>(vpage + (row0 + j) * vstep + d0) = encode8(x, vinv);
+      }
+    }
   }
   auto shrink = [&](uint8_t* at, int64_t step, int width, float f) {
     const int pieces = width >> 4;
@@ -544,8 +603,9 @@ pa_status pa_quant_write(const pa_quant_params* p, const void* key, const void* 
     return fail(PA_ERR_INVALID_ARGUMENT, "int32 tensors must be 4-byte aligned");
   int lpr = 2;
   while (lpr * 8 < g.hs || lpr * 8 < g.vhs) lpr *= 2;
-  const int row_bytes = (g.hs + g.vhs) * 2, at_once = quant::kWriteThreads / lpr;
-  int cap = 32768 / row_bytes / at_once * at_once;  // (at least 32 rows of 1 KB)
+  const int row_bytes = (2 * g.hs + g.vhs) * 2, at_once = quant::kWriteThreads / lpr;
+  // 64 rows of 128 / 128, at least 32
+  int cap = quant::kRowBytes / row_bytes / at_once * at_once;
   if (cap > g.bs) cap = (g.bs + at_once - 1) / at_once * at_once;
   const size_t smem = (size_t)cap * row_bytes + g.bs;
   const quant::WriteArgs A{key, value, cos_cache, sin_cache, k_norm_weight, slot_mapping, cumseq,
@@ -556,11 +616,20 @@ pa_status pa_quant_write(const pa_quant_params* p, const void* key, const void* 
   // (first(num_seqs) numbers; see the kernel)
   const int64_t runs = 2 * (int64_t)num_seqs + num_tokens / g.bs;
   const dim3 grid((unsigned)runs, (unsigned)g.kvh);
-  return g.dtype == PA_DTYPE_BF16
-             ? quant::launch(quant::quant_write_kernel<__nv_bfloat16>, grid, quant::kWriteThreads,
-                             smem, stream, A, "8-bit write launch")
-             : quant::launch(quant::quant_write_kernel<__half>, grid, quant::kWriteThreads,
-                             smem, stream, A, "8-bit write launch");
+  auto go = [&](auto* typed) {
+    auto kern = quant::quant_write_kernel<std::remove_pointer_t<decltype(typed)>>;
+    static std::atomic<bool> configured[64];
+    const cudaError_t e = once_per_device(configured, g.device, [&] {
+      return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  quant::kRowBytes + quant::kMaxBlock);
+    });
+    if (e != cudaSuccess) {
+      (void)cudaGetLastError();  // not left behind for a later call
+      return fail(PA_ERR_CUDA, "8-bit write launch: %s", cudaGetErrorString(e));
+    }
+    return quant::launch(kern, grid, quant::kWriteThreads, smem, stream, A, "8-bit write launch");
+  };
+  return g.dtype == PA_DTYPE_BF16 ? go((__nv_bfloat16*)nullptr) : go((__half*)nullptr);
 }
 
 pa_status pa_quant_restore(const pa_quant_params* p, const void* key_cache,
