@@ -185,10 +185,13 @@ __device__ __forceinline__ void fewer_registers() {
 }
 // The query rows of a tile (token, head), normalized and rotated, as fp16 in
 // swizzled slabs; mult: what takes the factor of the lane's row back, times the scale. Rows behind
-// the last are zeros. By the tile's four warps.
+// the last are zeros. By the tile's four warps. Rows in two addends (two_addends): the
+// second one into rest_s, laid out the same, and from there into TMEM where rest_t names
+// columns.
 template <typename T>
 __device__ __noinline__ void load_query(const PreP& A, const Unit& u, int g, int tile, int rows,
-                                        int warp, int lane, uint8_t* q_s, float* mult) {
+                                        int warp, int lane, uint8_t* q_s, uint8_t* rest_s,
+                                        uint32_t rest_t, float* mult) {
   float own = 0.f;  // of row 32 warp + lane
   const ReadP& P = A.R;
   int lpr = 2;
@@ -198,6 +201,7 @@ __device__ __noinline__ void load_query(const PreP& A, const Unit& u, int g, int
     return reinterpret_cast<uint4*>(q_s + (d0 >> 6) * kSlab + row * 128 +
                                     ((((d0 >> 3) & 7) ^ (row & 7)) << 4));
   };
+  constexpr bool kRest = std::is_same<T, __half>::value;
   // all rows on their way, to the places where they are changed
 #pragma unroll 4
   for (int r0 = 0; r0 < 32; r0 += step) {
@@ -232,10 +236,29 @@ __device__ __noinline__ void load_query(const PreP& A, const Unit& u, int g, int
                     reinterpret_cast<const T*>(P.sin_cache),
                     u.pos + tile * A.tpc + (live ? row / P.grp : 0));
     uint4 hx;
-    const float back = scaled_row8(x, &hx, lpr);
-    if (d0 < P.hs) *place(row) = hx;
+    uint4 rest;
+    const float back = scaled_row8(x, &hx, &rest, lpr);
+    if (d0 < P.hs) {
+      *place(row) = hx;
+      if (kRest && P.two) *(place(row) + ((rest_s - q_s) >> 4)) = rest;
+    }
     const float v = __shfl_sync(0xffffffffu, back, ((lane - r0) & (step - 1)) * lpr);
     if (lane >= r0 && lane < r0 + step) own = v;
+  }
+  if (kRest && rest_t) {  // (channels behind hs are not multiplied)
+    __syncwarp();
+    const int row = warp * 32 + lane;
+    for (int c = 0; c < A.slabs; ++c) {
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint4 v = *reinterpret_cast<const uint4*>(rest_s + c * kSlab + row * 128 + ((i ^ (row & 7)) << 4));
+        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+      }
+      tmem_st32(rest_t + c * 32, w);
+    }
+    tmem_wait_st();
+    tc_fence_before();
   }
   *mult = own * (P.cap_in > 0.f ? P.cap_in : P.scale_log2);
 }
@@ -278,7 +301,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return m;
 }
 
-template <int QT, int R, int C, bool CAP>
+template <int QT, int R, int C, bool CAP, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1)
 quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PreP A) {
@@ -297,7 +320,10 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q_bytes = A.slabs * kSlab, k_bytes = A.slabs * kKBox, v_bytes = A.vslabs * kKBox;
   uint8_t* q_s = smem;
-  uint8_t* k_s = q_s + QT * q_bytes;
+  // (the queries' second addends: behind the first ones, or in TMEM behind the scores, by
+  // way of the keys' ring, which is as large as they are)
+  uint8_t* k_s = q_s + (QT == 2 && TWO ? 2 : 1) * QT * q_bytes;
+  constexpr int kColRest = kColS + 2 * N;
   uint8_t* v_s = k_s + R * k_bytes;
   uint8_t* codes = v_s + R * v_bytes;  // C key tiles, C value tiles
   const int split = blockIdx.x % A.splits, rest = blockIdx.x / A.splits;
@@ -368,8 +394,9 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
       // =================== softmax ===================
       uint8_t* q_t = q_s + qt * q_bytes;
       float mult;
-      if (P.bf16) load_query<__nv_bfloat16>(A, U, g, qt, rows, quad, lane, q_t, &mult);
-      else load_query<__half>(A, U, g, qt, rows, quad, lane, q_t, &mult);
+      if (P.bf16) load_query<__nv_bfloat16>(A, U, g, qt, rows, quad, lane, q_t, q_t, 0, &mult);
+      else load_query<__half>(A, U, g, qt, rows, quad, lane, q_t, QT == 2 ? q_t + QT * q_bytes : k_s,
+                              QT == 1 && TWO ? lane_addr + kColRest : 0, &mult);
       fence_proxy_async();
       arrive_warp(&bars->q_full, lane);
       // keys counted from the first tile's first one
@@ -623,8 +650,10 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
       };
       uint64_t* empty = h ? bars->v_empty : bars->k_empty;
       uint64_t* full = h ? bars->v_full : bars->k_full;
+      // (the ring is not the keys' before the query has gone through it)
+      const bool go = QT == 2 || !TWO || h || wait_idle(&bars->q_full, 0);
 #pragma unroll 1
-      for (int k = 0; k < n; ++k) {
+      for (int k = 0; k < n && __all_sync(0xffffffffu, go); ++k) {
         if (!__all_sync(0xffffffffu, wait_idle(&bars->sc_full[k % kAhead], (k / kAhead) & 1) &&
                                          wait_idle(&bars->c_full[2 * h + k % C], (k / C) & 1) &&
                                          (k < R || wait_idle(&empty[k % R], ((k / R) & 1) ^ 1))))
@@ -669,6 +698,18 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
               mma_ss_lo(d, qd + 2 * i, kd + 2 * i, qk_hi, id_qk, i > 0 ? 1u : add);
 #pragma unroll 1
           for (; left > 0; --left, qd += 2, kd += 2, add = 1) mma_ss_lo(d, qd, kd, qk_hi, id_qk, add);
+          if (TWO) {
+            qd = q_lo + (QT + tile) * q_step;
+            kd = k_lo + slot * k_step;
+#pragma unroll 1
+            for (int s = 0; s < steps; s += 4, qd += kSlab >> 4, kd += kKBox >> 4)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (s + i >= steps) break;
+                if (QT == 2) mma_ss_lo(d, qd + 2 * i, kd + 2 * i, qk_hi, id_qk, 1);
+                else mma_ts_lo(d, tmem + kColRest + (s + i) * 8, kd + 2 * i, qk_hi, id_qk, 1);
+              }
+          }
           tc_commit(smem_u32(&bars->s_full[buf]));
         };
         auto pv = [&](uint32_t slot, int buf, int tile, uint32_t add) {
@@ -873,15 +914,19 @@ __global__ void __launch_bounds__(256) quant_join_kernel(const __grid_constant__
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-template <int QT, int R, int C, bool CAP>
-cudaError_t launch(const Geometry& g, const QuantArgs& a, const PreP& A, int64_t ctas) {
+constexpr size_t kMaxShared = 225 * 1024;  // (beside 2 KB of the kernel's own)
+size_t shared_bytes(const Geometry& g, const PreP& A, int qt, int ring, int codes) {
+  return 1024 + (size_t)qt * (qt == 2 && A.R.two ? 2 : 1) * A.slabs * kSlab +
+         (size_t)ring * (A.slabs + A.vslabs) * N * 128 + (size_t)codes * N * (g.hs + g.vhs);
+}
+
+template <int QT, int R, int C, bool CAP, bool TWO>
+cudaError_t launch_one(const Geometry& g, const QuantArgs& a, const PreP& A, int64_t ctas) {
   static std::atomic<bool> configured[64];
-  auto kern = quant_prefill_kernel<QT, R, C, CAP>;
-  const size_t smem = 1024 + (size_t)QT * A.slabs * kSlab +
-                      (size_t)R * (A.slabs + A.vslabs) * N * 128 + (size_t)C * N * (g.hs + g.vhs);
+  auto kern = quant_prefill_kernel<QT, R, C, CAP, TWO>;
+  const size_t smem = shared_bytes(g, A, QT, R, C);
   cudaError_t e = once_per_device(configured, g.device, [&] {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                225 * 1024);
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
   });
   if (e != cudaSuccess) return e;
   CUtensorMap kmap, vmap;
@@ -893,18 +938,29 @@ cudaError_t launch(const Geometry& g, const QuantArgs& a, const PreP& A, int64_t
   return launch_pdl(quant_join_kernel<QT>, dim3((unsigned)ctas, 8), dim3(256), 0, a.stream, A);
 }
 
+template <int QT, int R, int C>
+cudaError_t launch(const Geometry& g, const QuantArgs& a, const PreP& A, int64_t ctas) {
+  if (g.softcap > 0.f)
+    return A.R.two ? launch_one<QT, R, C, true, true>(g, a, A, ctas)
+                   : launch_one<QT, R, C, true, false>(g, a, A, ctas);
+  return A.R.two ? launch_one<QT, R, C, false, true>(g, a, A, ctas)
+                 : launch_one<QT, R, C, false, false>(g, a, A, ctas);
+}
+
 // Batches with so few query rows per sequence and kv head, on average, go to the
 // kernel for few rows.
 constexpr int64_t kFewRows = 32;
 
 // One query tile where two accumulators do not fit in TMEM, or two queries beside
 // the rings in shared memory.
-int query_tiles(const Geometry& g) { return g.vhs <= 128 && g.hs <= 192 ? 2 : 1; }
+int query_tiles(const Geometry& g, int two) {
+  return g.vhs <= 128 && g.hs <= (two ? 128 : 192) ? 2 : 1;
+}
 
 }  // namespace
 
 size_t prefill_workspace(const Geometry& g, int64_t nseq) {
-  const size_t rows = (size_t)g.num_sms * query_tiles(g) * kRows;
+  const size_t rows = (size_t)g.num_sms * query_tiles(g, 0) * kRows;  // (at most)
   return std::max(rows * g.vhs * sizeof(float) + rows * sizeof(float2), rows_workspace(g, nseq));
 }
 
@@ -913,7 +969,7 @@ cudaError_t launch_prefill(const Geometry& g, const QuantArgs& a) {
   if (a.num_tokens * (g.H / g.kvh) <= kFewRows * nseq) return launch_rows(g, a, false);
   PreP A{};
   A.R = read_params(g, a);
-  const int qt = query_tiles(g);
+  const int qt = query_tiles(g, A.R.two);
   A.tpc = kRows / A.R.grp;
   A.slabs = (g.hs + 63) / 64;
   A.vslabs = (g.vhs + 63) / 64;
@@ -935,12 +991,10 @@ cudaError_t launch_prefill(const Geometry& g, const QuantArgs& a) {
   // parts of four tiles at least, as long as there are SMs
   const int64_t tiles = ((int64_t)g.max_blocks * g.bs + N - 1) / N;
   A.splits = (int)std::max<int64_t>(1, std::min<int64_t>(g.num_sms / ctas, tiles / 4));
-  const bool cap = g.softcap > 0.f;
-  if (qt == 2 && g.hs <= 128)
-    return cap ? launch<2, 4, 2, true>(g, a, A, ctas) : launch<2, 4, 2, false>(g, a, A, ctas);
-  if (qt == 2)
-    return cap ? launch<2, 2, 2, true>(g, a, A, ctas) : launch<2, 2, 2, false>(g, a, A, ctas);
-  return cap ? launch<1, 2, 1, true>(g, a, A, ctas) : launch<1, 2, 1, false>(g, a, A, ctas);
+  // four tiles converted ahead where they fit
+  if (qt == 1) return launch<1, 2, 1>(g, a, A, ctas);
+  return shared_bytes(g, A, 2, 4, 2) <= kMaxShared ? launch<2, 4, 2>(g, a, A, ctas)
+                                                   : launch<2, 2, 2>(g, a, A, ctas);
 }
 
 }  // namespace quant

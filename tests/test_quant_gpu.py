@@ -410,6 +410,27 @@ def test_one_call_is_three():
     assert op.error_flags() == 0 and torch.equal(out, want)
 
 
+@pytest.mark.parametrize("q,past,kw", [
+    ([1] * 6, [3000] * 6, dict(heads=8, kv=2)), ([1] * 4, [2500] * 4, dict(heads=16, kv=1, hs=128)),
+    ([1] * 6, [2000] * 6, dict(heads=8, kv=2, hs=192, vhs=128)), ([2] * 3, [1500] * 3, dict(heads=16, kv=2, hs=256)),
+    ([70], [3000], dict(heads=4, kv=2)), ([65, 30], [1000, 2500], dict(heads=8, kv=2, hs=128)),
+    ([70], [2000], dict(heads=4, kv=2, hs=176, vhs=96)), ([70], [1000], dict(heads=4, kv=2, hs=256)),
+    ([70], [1000], dict(heads=4, kv=2, hs=256, vhs=64)), ([70], [1000], dict(heads=4, kv=2, hs=80, vhs=144)),
+    ([70], [2000], dict(heads=4, kv=2, rd=0, norm=True)), ([1] * 6, [3000] * 6, dict(heads=8, kv=2, rd=0, norm=True))])
+def test_fp16_keeps_its_bits(q, past, kw):
+    """Rotated and normalized queries keep more than fp16 holds. A rounding to fp16 is 2^-11 sqrt(0.541 / 3) =
+    2.07e-4 off in the 2-norm, 0.541 being the mean of 1 / m^2 over mantissas m in [1, 2) spread evenly in their
+    logarithm. The probabilities' and the output's own are allowed: 2.93e-4 together, and an eighth more for chance
+    (some 256 rows and more). A third one in the query, where scores spread by 1 or more, makes it 3.6e-4."""
+    c = Case(q, past, dtype=P.F16, bs=64, gain=4.0, seed=3, **kw)
+    t, op = c.tensors(), c.op()
+    out = c.forward(op, t, len(q) if max(q) == 1 else 0)
+    assert op.error_flags() == 0
+    want = c.oracle([t["kc"].cpu().numpy(), t["vc"].cpu().numpy(), t["scales"].cpu().numpy()])[0]
+    off = out.double().cpu().numpy().reshape(want.shape) - want
+    assert np.linalg.norm(off) < 3.3e-4 * np.linalg.norm(want), np.linalg.norm(off) / np.linalg.norm(want)
+
+
 def test_mixed_batch():
     c = Case([1, 1, 1, 50, 9], [10, 300, 64, 20, 0], sink=True, seed=13)
     _run(c, 3)
