@@ -2,8 +2,9 @@
 // token per sequence, and prefill of a few tokens each. Bound by HBM.
 //
 // The line. A unit is a sequence, a kv head and up to 8 NB of its query rows (token x
-// head of the group); its visible keys are cut into tiles of 16. All tiles of all units
-// form one line, which is cut into equal parts, one per CTA, whatever the lengths. A
+// head of the group); its visible keys are cut into tiles of 16 TH. All tiles of all units
+// form one line, every unit's behind `extra` that stand for the time that the unit takes
+// by itself. The line is cut into equal parts, one per CTA, whatever the lengths. A
 // CTA's part of a unit is a segment: its warps take the segment's tiles in turn, each
 // with a softmax of its own, and join at the segment's end. A unit that lies in several
 // parts is joined by quant_combine_kernel.
@@ -44,13 +45,14 @@ struct DecP {
   ReadP R;
   float4* ws_o;      // [2 CTAs][8 VP NB][32] accumulators as the lanes hold them
   float2* ws_ml;     // [2 CTAs][8 NB] maximum (log2 domain), sum
-  int64_t* ws_line;  // [nseq + 1] tiles of the line before each sequence, then those of a part
+  int64_t* ws_line;  // [nseq + 1] length of the line before each sequence, then that of a part
   int32_t* ws_units; // [nseq + 1] units before each sequence, then all
   int decode;        // one token per sequence, others are told
   int rows;          // 8 NB
   int tile;          // keys: 16 TH
   int box;           // rows of a copy: min(bs, tile)
   int min_part;
+  int extra;         // what a unit counts on the line beside its tiles
 };
 
 struct Span {  // a sequence's tokens and the tiles that they see
@@ -88,7 +90,8 @@ struct Walk {
   int64_t x, end, start;  // (start: of sequence b)
   int b, tiles, first, chunks;
   int g, chunk;           // the segment's unit
-  int from, len;          // first tile (in the cache), tiles
+  int step;               // its length on the line
+  int from, len;          // first tile (in the cache), tiles (0: the part ended before them)
   int lo, hi;             // keys that any of its tokens sees
   __device__ __forceinline__ bool valid() const { return x < end; }
   __device__ __forceinline__ void enter(const DecP& A, int seq, int64_t at) {
@@ -101,24 +104,27 @@ struct Walk {
     lo = (int)s.lo;
     hi = (int)s.hi;
   }
-  __device__ __forceinline__ void segment() {
+  __device__ __forceinline__ void segment(const DecP& A) {
     const uint64_t off = (uint64_t)(x - start);
-    const int unit = off >> 32 ? (int)(off / (uint32_t)tiles) : (int)((uint32_t)off / (uint32_t)tiles);
-    const int in = (int)(off - (uint64_t)unit * tiles);
+    const uint32_t all = tiles + A.extra;
+    const int unit = off >> 32 ? (int)(off / all) : (int)((uint32_t)off / all);
+    const int in = (int)(off - (uint64_t)unit * all);
     g = unit / chunks;
     chunk = unit - g * chunks;
-    from = first + in;
-    len = (int)min((int64_t)(tiles - in), end - x);
+    step = (int)min((int64_t)(all - in), end - x);
+    const int t0 = max(0, in - A.extra);
+    from = first + t0;
+    len = max(0, in + step - A.extra) - t0;
   }
   __device__ __forceinline__ void next(const DecP& A) {
-    x += len;
+    x += step;
     if (!valid()) return;
-    if (x == start + (int64_t)tiles * A.R.kvh * chunks) {
+    if (x == start + (int64_t)(tiles + A.extra) * A.R.kvh * chunks) {
       int seq = b;
       do enter(A, ++seq, x);
       while (tiles == 0);
     }
-    segment();
+    segment(A);
   }
 };
 
@@ -235,7 +241,7 @@ quant_rows_kernel(const __grid_constant__ CUtensorMap kmap,
     if (b < P.nseq) {
       const Span s = span_of(A, b);
       units = s.chunks * P.kvh;
-      mine = (int64_t)s.tiles * units;
+      mine = (int64_t)(s.tiles + A.extra) * units;
     }
     int64_t v = mine;
     int w = units;
@@ -296,7 +302,7 @@ quant_rows_kernel(const __grid_constant__ CUtensorMap kmap,
   __syncthreads();
   if (W.valid()) {
     W.enter(A, (int)s_hit[0], s_hit[1]);
-    W.segment();
+    W.segment(A);
   }
   if (P.early) grid_dep_wait();
 
@@ -392,6 +398,10 @@ quant_rows_kernel(const __grid_constant__ CUtensorMap kmap,
   // ---- segments
 #pragma unroll 1
   while (W.valid()) {
+    if (W.len == 0) {
+      W.next(A);
+      continue;
+    }
     const int r0 = W.chunk * R;
     const Span sp = span_of(A, W.b);
     const int nr = min(R, sp.q * P.grp - r0);
