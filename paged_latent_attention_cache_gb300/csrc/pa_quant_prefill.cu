@@ -886,19 +886,31 @@ __global__ void __launch_bounds__(256) quant_join_kernel(const __grid_constant__
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     bool bad = false;
-    for (int s = 0; s < A.splits; ++s) {
-      if ((int64_t)U.n * s / A.splits == (int64_t)U.n * (s + 1) / A.splits) continue;  // no tiles
-      const int64_t at =
-          ((int64_t)blockIdx.x * A.splits + s) * (QT * kRows) + tile * kRows + row;
-      const float2 ml = A.ws_ml[at];
-      const float4 v = *reinterpret_cast<const float4*>(A.ws_o + at * P.vhs + c);
-      bad |= isnan(ml.x);
-      const float t = fmaxf(m, ml.x), base = t == -INFINITY ? 0.f : t;
-      const float fa = ex2(m - base), fb = ex2(ml.x - base);
-      m = t;
-      l = l * fa + ml.y * fb;
-      o = make_float4(o.x * fa + v.x * fb, o.y * fa + v.y * fb, o.z * fa + v.z * fb,
-                      o.w * fa + v.w * fb);
+    // (loads of four parts at once: one part after the other was latency and nothing else)
+    for (int s0 = 0; s0 < A.splits; s0 += 4) {
+      float2 ml[4];
+      float4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int s = s0 + i;
+        const bool part = s < A.splits &&
+                          (int64_t)U.n * s / A.splits != (int64_t)U.n * (s + 1) / A.splits;  // has tiles
+        const int64_t at =
+            ((int64_t)blockIdx.x * A.splits + s) * (QT * kRows) + tile * kRows + row;
+        ml[i] = part ? A.ws_ml[at] : make_float2(-INFINITY, 0.f);
+        v[i] = part ? *reinterpret_cast<const float4*>(A.ws_o + at * P.vhs + c)
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        bad |= isnan(ml[i].x);
+        const float t = fmaxf(m, ml[i].x), base = t == -INFINITY ? 0.f : t;
+        const float fa = ex2(m - base), fb = ex2(ml[i].x - base);
+        m = t;
+        l = l * fa + ml[i].y * fb;
+        o = make_float4(o.x * fa + v[i].x * fb, o.y * fa + v[i].y * fb, o.z * fa + v[i].z * fb,
+                        o.w * fa + v[i].w * fb);
+      }
     }
     float sum = l;
     if (P.head_sink) sum += ex2(to_f32(P, P.head_sink, h) * kLog2e - m + kShift);
@@ -935,7 +947,7 @@ cudaError_t launch_one(const Geometry& g, const QuantArgs& a, const PreP& A, int
   e = launch_pdl(kern, dim3((unsigned)(ctas * A.splits)), dim3(kThreads), smem, a.stream, kmap, vmap,
                  A);
   if (e != cudaSuccess || A.splits == 1) return e;
-  return launch_pdl(quant_join_kernel<QT>, dim3((unsigned)ctas, 8), dim3(256), 0, a.stream, A);
+  return launch_pdl(quant_join_kernel<QT>, dim3((unsigned)ctas, QT * kRows * (g.vhs / 4) / 256), dim3(256), 0, a.stream, A);
 }
 
 template <int QT, int R, int C>
