@@ -1,6 +1,7 @@
 // Caches in 8 bits (include/pa_quant.h): entry points, write phase, reading back.
 #include <math.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <type_traits>
@@ -36,8 +37,13 @@ constexpr int kMaxBlock = 4096;  // rows of a page
 // stay there in f32 for their encoding. With a load per row where it was used, 14200 new
 // tokens of 8 kv heads of 128 / 128 took 66 us, with keys rotated twice 52.
 // ---------------------------------------------------------------------------
-constexpr int kWriteThreads = 128;
-constexpr int kRowBytes = 48 * 1024;  // of shared memory for rows
+// Write: shared memory for a run's rows, and threads. Warps by the kilobyte of rows:
+// what a run waits for is other runs' time, and the more rows there are the fewer runs an
+// SM holds. 128 threads up to kFewBytes of rows, 256 up to half of kRowBytes, then 512
+// with all of it. Measured with 128, 256, 512 threads (us; 20,000 rows of 8 heads of 128 / 128):
+// pages of 16 rows 42.6, 58.5, 114.8; 32: 37.8, 43.1, 66.8; 64: 47.7, 39.5, 49.0; 128: 70.3, 53.2, 43.3;
+// one row for each of 32 sequences 4.4, 5.2, 7.1.
+constexpr int kRowBytes = 96 * 1024, kFewBytes = 24 * 1024;
 
 struct WriteArgs {
   const void* key;
@@ -107,14 +113,14 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
                     encode2(x[4] * inv, x[5] * inv) | encode2(x[6] * inv, x[7] * inv) << 16);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kWriteThreads)
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS)
 quant_write_kernel(const __grid_constant__ WriteArgs A) {
   asm volatile("griddepcontrol.wait;\n griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ __align__(16) uint8_t s_rows[];  // [cap] keys (then the first half of their f32 words), the others, values; s_new
   uint8_t* s_new = s_rows + (size_t)A.cap * (2 * A.hs + A.vhs) * 2;  // [bs] rows that the call writes
   __shared__ int s_first;
-  __shared__ float s_max[2][kWriteThreads / 32];
+  __shared__ float s_max[2][THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = blockIdx.y, bs = A.bs, sh = __ffs(bs) - 1;
   const int run = blockIdx.x;
@@ -122,13 +128,13 @@ quant_write_kernel(const __grid_constant__ WriteArgs A) {
   auto first = [&](int b) { return 2 * (int64_t)b + (A.cumseq[b] >> sh); };
   if (run == 0 && tells) {  // offsets have to rise from 0 to the number of tokens
     bool bad = false;
-    for (int b = tid; b < A.num_seqs; b += kWriteThreads) bad |= A.cumseq[b] > A.cumseq[b + 1];
+    for (int b = tid; b < A.num_seqs; b += THREADS) bad |= A.cumseq[b] > A.cumseq[b + 1];
     if (tid == 0) bad |= A.cumseq[0] != 0 || A.cumseq[A.num_seqs] != A.num_tokens;
     if (bad) raise_flag(A.err_flags, PA_DEVERR_CUMSEQ);
   }
   int lo = 0, hi = A.num_seqs;
   while (hi - lo > 1) {
-    const int step = (hi - lo + kWriteThreads - 1) / kWriteThreads, at = lo + tid * step;
+    const int step = (hi - lo + THREADS - 1) / THREADS, at = lo + tid * step;
     const int n = __syncthreads_count(at < hi && (at == lo || first(at) <= run));
     lo += (n - 1) * step;
     hi = min(hi, lo + step);
@@ -146,7 +152,7 @@ quant_write_kernel(const __grid_constant__ WriteArgs A) {
   const int n = (int)(end - begin), row0 = (int)(begin & (bs - 1));
   const int64_t t0 = c0 + (begin - p0);
 
-  const int lpr = A.lpr, rows_at_once = kWriteThreads / lpr, mine = tid / lpr;
+  const int lpr = A.lpr, rows_at_once = THREADS / lpr, mine = tid / lpr;
   const int d0 = (tid & (lpr - 1)) * 8;
   const int64_t kstep = (int64_t)A.kvh * A.hs, vstep = (int64_t)A.kvh * A.vhs;
   const T* key = reinterpret_cast<const T*>(A.key) + t0 * kstep + (int64_t)g * A.hs + d0;
@@ -169,11 +175,11 @@ quant_write_kernel(const __grid_constant__ WriteArgs A) {
 
   // rows that the call writes: tokens with a slot of the page that the run's
   // first one names
-  for (int r = tid; r < bs; r += kWriteThreads) s_new[r] = 0;
+  for (int r = tid; r < bs; r += THREADS) s_new[r] = 0;
   if (tid == 0) s_first = n;
   __syncthreads();
   int err = 0;
-  for (int j = tid; j < n; j += kWriteThreads) {
+  for (int j = tid; j < n; j += THREADS) {
     const int32_t slot = A.slot_mapping[t0 + j];
     if (slot == -1) continue;
     if (slot < 0 || slot >= A.num_slots || (slot & (bs - 1)) != row0 + j) {
@@ -189,7 +195,7 @@ quant_write_kernel(const __grid_constant__ WriteArgs A) {
   const int first_j = s_first;
   if (first_j < n) {
     const int32_t page_of = A.slot_mapping[t0 + first_j] >> sh;
-    for (int j = tid; j < n; j += kWriteThreads)
+    for (int j = tid; j < n; j += THREADS)
       if (s_new[row0 + j] && A.slot_mapping[t0 + j] >> sh != page_of) {
         s_new[row0 + j] = 0;
         err |= PA_DEVERR_SLOT;
@@ -261,7 +267,7 @@ quant_write_kernel(const __grid_constant__ WriteArgs A) {
   }
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWriteThreads / 32; ++w) {
+  for (int w = 0; w < THREADS / 32; ++w) {
     km = fmaxf(km, s_max[0][w]);
     vm = fmaxf(vm, s_max[1][w]);
   }
@@ -298,7 +304,7 @@ quant_write_kernel(const __grid_constant__ WriteArgs A) {
   }
   auto shrink = [&](uint8_t* at, int64_t step, int width, float f) {
     const int pieces = width >> 4;
-    for (int i = tid; i < bs * pieces; i += kWriteThreads) {
+    for (int i = tid; i < bs * pieces; i += THREADS) {
       const int r = i / pieces;
       if (s_new[r]) continue;
       uint4* p = reinterpret_cast<uint4*>(at + r * step + (i - r * pieces) * 16);
@@ -603,9 +609,13 @@ pa_status pa_quant_write(const pa_quant_params* p, const void* key, const void* 
     return fail(PA_ERR_INVALID_ARGUMENT, "int32 tensors must be 4-byte aligned");
   int lpr = 2;
   while (lpr * 8 < g.hs || lpr * 8 < g.vhs) lpr *= 2;
-  const int row_bytes = (2 * g.hs + g.vhs) * 2, at_once = quant::kWriteThreads / lpr;
-  // 64 rows of 128 / 128, at least 32
-  int cap = quant::kRowBytes / row_bytes / at_once * at_once;
+  const int row_bytes = (2 * g.hs + g.vhs) * 2;
+  // rows of a run, as the batch has them on average; see kFewBytes
+  const int64_t mean = std::min<int64_t>(g.bs, (num_tokens + num_seqs - 1) / num_seqs) * row_bytes;
+  const int threads = mean <= quant::kFewBytes ? 128 : mean <= quant::kRowBytes / 2 ? 256 : 512;
+  const int room = threads == 512 ? quant::kRowBytes : quant::kRowBytes / 2;
+  const int at_once = threads / lpr;
+  int cap = room / row_bytes / at_once * at_once;
   if (cap > g.bs) cap = (g.bs + at_once - 1) / at_once * at_once;
   const size_t smem = (size_t)cap * row_bytes + g.bs;
   const quant::WriteArgs A{key, value, cos_cache, sin_cache, k_norm_weight, slot_mapping, cumseq,
@@ -616,8 +626,8 @@ pa_status pa_quant_write(const pa_quant_params* p, const void* key, const void* 
   // (first(num_seqs) numbers; see the kernel)
   const int64_t runs = 2 * (int64_t)num_seqs + num_tokens / g.bs;
   const dim3 grid((unsigned)runs, (unsigned)g.kvh);
-  auto go = [&](auto* typed) {
-    auto kern = quant::quant_write_kernel<std::remove_pointer_t<decltype(typed)>>;
+  auto go = [&](auto* typed, auto th) {
+    auto kern = quant::quant_write_kernel<std::remove_pointer_t<decltype(typed)>, th()>;
     static std::atomic<bool> configured[64];
     const cudaError_t e = once_per_device(configured, g.device, [&] {
       return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -627,9 +637,16 @@ pa_status pa_quant_write(const pa_quant_params* p, const void* key, const void* 
       (void)cudaGetLastError();  // not left behind for a later call
       return fail(PA_ERR_CUDA, "8-bit write launch: %s", cudaGetErrorString(e));
     }
-    return quant::launch(kern, grid, quant::kWriteThreads, smem, stream, A, "8-bit write launch");
+    return quant::launch(kern, grid, th(), smem, stream, A, "8-bit write launch");
   };
-  return g.dtype == PA_DTYPE_BF16 ? go((__nv_bfloat16*)nullptr) : go((__half*)nullptr);
+  auto typed = [&](auto* t) {
+    switch (threads) {
+      case 128: return go(t, std::integral_constant<int, 128>());
+      case 256: return go(t, std::integral_constant<int, 256>());
+      default: return go(t, std::integral_constant<int, 512>());
+    }
+  };
+  return g.dtype == PA_DTYPE_BF16 ? typed((__nv_bfloat16*)nullptr) : typed((__half*)nullptr);
 }
 
 pa_status pa_quant_restore(const pa_quant_params* p, const void* key_cache,

@@ -160,6 +160,9 @@ WRITES = [
     dict(q=[5, 130], past=[100, 126], bs=128, kv=1, heads=4, hs=128), dict(q=[20, 7], past=[3, 17], hs=80, vhs=48, rd=32, ro=8),
     dict(q=[20, 7], past=[3, 17], hs=256, vhs=256, inter=1), dict(q=[9, 30], past=[17, 0], hs=16, vhs=256, rd=16, kv=8),
     dict(q=[33, 2], past=[0, 50], rd=0, vhs=16), dict(q=[4] * 37, past=list(range(37)), kv=1, heads=1, hs=192, vhs=128, inter=1, rd=64, ro=128),
+    # as many threads as pages have rows: 256, and 512 with pages in one piece and in several
+    dict(q=[64, 50, 70], past=[0, 20, 63], bs=64, kv=1, heads=1, hs=128), dict(q=[200, 90], past=[5, 0], bs=128, kv=1, heads=1, hs=128, vhs=96),
+    dict(q=[300, 280], past=[100, 0], bs=512, kv=1, heads=1, hs=256, inter=1), dict(q=[4000, 1000], past=[60, 10], bs=4096, kv=1, heads=1, hs=16),
 ]
 
 
