@@ -31,7 +31,7 @@ quant_combine_kernel(const __grid_constant__ DecP A) {
   const int u = blockIdx.x - (A.decode ? b * per : A.ws_units[b]);
   const int64_t part = A.ws_line[P.nseq], before = A.ws_line[b];
   const Span sp = span_of(A, b);
-  if (sp.tiles == 0) return;
+  if (sp.tiles == 0 || u < 0 || u >= P.kvh * sp.chunks) return;  // (offsets that do not rise)
   const int64_t start = before + (int64_t)u * (sp.tiles + A.extra), end = start + A.extra + sp.tiles;
   const int64_t c0 = (start + A.extra) / part, c1 = (end - 1) / part;
   if (c0 == c1) return;

@@ -103,7 +103,7 @@ __device__ Unit resolve(const PreP& A, int unit, int split, int lane) {
     *q0 = *q = 0;
     if (i < P.nseq) {
       *q0 = P.cumseq[P.seq_begin + i];
-      *q = P.cumseq[P.seq_begin + i + 1] - *q0;
+      *q = (int)((uint32_t)P.cumseq[P.seq_begin + i + 1] - (uint32_t)*q0);  // (of any offsets)
     }
     return *q > 0 ? (*q - 1) / per + 1 : 0;
   };
@@ -363,6 +363,13 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
   } else if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&bars->tmem_base), 512);
     tmem_relinquish();
+  } else if (warp == kScaleWarp && blockIdx.x == 0) {  // offsets have to rise, within the tokens
+    bool bad = false;
+    for (int i = lane; i < P.nseq; i += 32) {
+      const int c0 = P.cumseq[P.seq_begin + i], c1 = P.cumseq[P.seq_begin + i + 1];
+      bad |= c0 < 0 || c0 > c1 || c1 > P.num_tokens;
+    }
+    if (bad) raise_flag(P.err_flags, PA_DEVERR_CUMSEQ);
   }
   tc_fence_before();
   __syncthreads();
@@ -959,9 +966,12 @@ cudaError_t launch(const Geometry& g, const QuantArgs& a, const PreP& A, int64_t
                  : launch_one<QT, R, C, false, false>(g, a, A, ctas);
 }
 
-// Batches with so few query rows per sequence and kv head, on average, go to the
-// kernel for few rows.
-constexpr int64_t kFewRows = 32;
+// Batches with so few query rows per sequence and kv head, on average, go to the kernel
+// for few rows, which reads the keys once per 16 of them; here they take as long whatever
+// their number, up to two tiles of 128. Measured, rows there and here (us; 8 kv heads of 128
+// with 4 query heads each): 16 sequences of 2000 to 16000 keys 16 rows 76, 270; 48: 167, 273;
+// 64: 214, 274; 96: 309, 274; 32 sequences of 100 to 1000 keys 48: 64, 68; 64: 84, 70.
+constexpr int64_t kFewRows = 48;
 
 // One query tile where two accumulators do not fit in TMEM, or two queries beside
 // the rings in shared memory.

@@ -544,6 +544,143 @@ def test_error_flags_and_rows():
     _check_out(out[[0, 3]], ref[[0, 3]], tol[[0, 3]])
 
 
+@pytest.mark.parametrize("vhs", [64, 256])
+def test_error_flags_of_long_prefill(vhs):
+    """As above, in sequences of many tokens (a kernel of its own): the others keep their results."""
+    B = _binding()
+    c = Case([60, 90, 40], [100, 300, 5], vhs=vhs, seed=31)
+    ref, tol = c.oracle(c.oracle_write())
+    want = lambda s: (ref[s], tol[s])
+
+    def run(change):
+        t, op = c.tensors(), c.op()
+        op.write(t["key"], t["value"], t["kc"], t["vc"], t["scales"], t["cos"], t["sin"], t["slots"], t["cum"], t["past"])
+        change(t)
+        out = torch.full((c.T, 8 * vhs), 7.0, dtype=torch.bfloat16, device="cuda")
+        op.attend(t["query"], t["kc"], t["vc"], t["scales"], t["cos"], t["sin"], t["cum"], t["past"], t["table"], 0, out=out)
+        return out, op.error_flags()
+
+    out, flags = run(lambda t: t["table"][1, 2].fill_(-1))
+    assert flags == B.PA_DEVERR_BLOCK and not out[60:150].any()
+    out, flags = run(lambda t: t["table"][1, 2].fill_(c.p["num_blocks"]))
+    assert flags == B.PA_DEVERR_BLOCK and not out[60:150].any()
+    _check_out(out[:60], *want(slice(0, 60)))
+    _check_out(out[150:], *want(slice(150, 190)))
+    for past in (c.mb * 16, -1, -(2 ** 31), 2 ** 31 - 1):
+        out, flags = run(lambda t: t["past"][0].fill_(past))
+        assert flags & B.PA_DEVERR_CONTEXT and not out[:60].any()
+        _check_out(out[60:], *want(slice(60, 190)))
+    for cum in ([0, 60, 40, 190], [0, 60, 150, 150], [0, 0, 0, 190]):  # (in bounds, whatever they say)
+        out, flags = run(lambda t: t["cum"].copy_(torch.tensor(cum, dtype=torch.int32)))
+        assert bool(flags & B.PA_DEVERR_CUMSEQ) == (cum[2] < cum[1])
+        assert torch.isfinite(out.float()).all()
+    for cum in ([0, 60, 150, 191], [0, 60, 2 ** 31 - 1, 190], [-5, 60, 150, 190], [-(2 ** 31), 60, 150, 190]):
+        out, flags = run(lambda t: t["cum"].copy_(torch.tensor(cum, dtype=torch.int32)))
+        assert flags & B.PA_DEVERR_CUMSEQ
+
+
+def test_offsets_that_do_not_rise():
+    """Reads of few tokens: told, and nothing out of place."""
+    B = _binding()
+    c = Case([1] * 6, [40, 3, 0, 100, 64, 9], seed=32)
+    for cum in ([0, 1, 5, 3, 4, 5, 6], [0, 1, 2, 7, 4, 5, 6], [-1, 1, 2, 3, 4, 5, 6], [0, 2 ** 31 - 1, -(2 ** 31), 3, 4, 5, 6]):
+        for nd in (0, 6):
+            t, op = c.tensors(), c.op()
+            t["cum"].copy_(torch.tensor(cum, dtype=torch.int32))
+            out = torch.full((6, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+            c.forward(op, t, nd, out=out)
+            assert op.error_flags() & (B.PA_DEVERR_CUMSEQ | B.PA_DEVERR_DECODE_QLEN)
+            op.restore(t["kc"], t["vc"], t["scales"], t["cum"], t["past"], t["table"], 6)
+
+
+@pytest.mark.parametrize("q,past,nd", [([1, 1, 1], [70, 3, 200], 3), ([5, 2], [40, 100], 0), ([70, 40], [30, 100], 0)])
+def test_caches_beyond_4_gb(q, past, nd):
+    """Pages at both ends of caches of 6 GB answer as those of a small one."""
+    c = Case(q, past, kv=8, heads=16, hs=256, bs=64, seed=33)
+    t, op = c.tensors(), c.op()
+    want = c.forward(op, t, nd)
+    small = c.p["num_blocks"]
+    big = 6 * 2 ** 30 // (64 * 8 * 256)
+    place = torch.arange(small, device="cuda") * ((big - 1) // (small - 1))
+    place[-1] = big - 1
+    c.p["num_blocks"] = big
+    far, op = c.tensors(), c.op()
+    for name in ("kc", "vc", "scales"):
+        whole = torch.empty(big, *far[name].shape[1:], dtype=far[name].dtype, device="cuda")
+        whole[place] = far[name]
+        far[name] = whole
+    far["table"] = torch.where(far["table"] >= 0, place[far["table"].long().clamp(min=0)].int(), -1).contiguous()
+    far["slots"] = (place[far["slots"].long() // 64] * 64 + far["slots"].long() % 64).int()
+    out = c.forward(op, far, nd)
+    assert op.error_flags() == 0 and torch.equal(out, want)
+    for name in ("kc", "vc", "scales"):
+        assert torch.equal(far[name][place].view(torch.uint8), t[name].view(torch.uint8))
+    rows = lambda op, t: op.restore(t["kc"], t["vc"], t["scales"], t["cum"], t["past"], t["table"], c.T)
+    c.p["num_blocks"] = small
+    for a, b in zip(rows(op, far), rows(c.op(), t)):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("heads,kv", [(128, 1), (96, 1), (127, 1), (33, 3), (35, 5)])
+@pytest.mark.parametrize("q", [1, 3, 40])
+def test_large_and_odd_groups(heads, kv, q):
+    _run(Case([q, q, 0], [70, 5, 30], heads=heads, kv=kv, hs=32, vhs=48, rd=16, seed=34), 2 if q == 1 else 0)
+
+
+@pytest.mark.parametrize("kw", [dict(bs=4096, past=[5000, 0, 4095]), dict(bs=16, past=[0, 0, 0], hs=16, vhs=16, rd=16, heads=1, kv=1),
+                                dict(bs=4096, past=[9000, 4096, 1], window=100)])
+@pytest.mark.parametrize("q", [1, 70])
+def test_page_sizes_at_the_ends(kw, q):
+    _run(Case([q] * 3, seed=35, spare=0, **kw), 3 if q == 1 else 0)
+
+
+def test_thousands_of_sequences():
+    rng = np.random.default_rng(36)
+    n = 2300
+    _run(Case([1] * n, list(rng.integers(0, 60, n)), kv=1, heads=2, hs=16, seed=36), n)
+    _run(Case(list(rng.integers(0, 3, n)), list(rng.integers(0, 60, n)), kv=1, heads=2, hs=16, seed=37), 0)
+    n = 500
+    _run(Case(list(rng.integers(0, 60, n)), list(rng.integers(0, 60, n)), kv=1, heads=2, hs=16, seed=38), 0)
+
+
+def test_two_objects_at_once():
+    """Objects on streams of their own, and graphs of one object replayed in turn."""
+    cases = [Case([1] * 20 + [90, 300], list(range(100, 2100, 100)) + [800, 50], heads=8, kv=2, hs=128, bs=64, seed=s) for s in (40, 41)]
+    want = [c.forward(c.op(), c.tensors(), 20).clone() for c in cases]
+    ops, ts = [c.op() for c in cases], [c.tensors() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(10):
+        for i in (0, 1):
+            outs[i].append(cases[i].forward(ops[i], ts[i], 20, stream=streams[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i in (0, 1) for o in outs[i])
+    graphs, held = [], [torch.zeros_like(w) for w in want]
+    for i in (0, 1):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            cases[i].forward(ops[0], ts[i], 20, out=held[i])
+        graphs.append(g)
+    for _ in range(5):
+        for i in (0, 1):
+            held[i].zero_()
+            graphs[i].replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(held[i], want[i]) for i in (0, 1))
+
+
+def test_pages_in_two_tables():
+    """A prefix that two sequences share, read by both."""
+    c = Case([1, 1, 40, 40], [200, 230, 160, 170], seed=42)
+    c.table[1, :12], c.table[3, :10] = c.table[0, :12], c.table[2, :10]
+    for nd in (2, 0):
+        t, op = c.tensors(), c.op()
+        out = c.forward(op, t, nd)
+        assert op.error_flags() == 0
+        _check_out(out, *c.oracle([t["kc"].cpu().numpy(), t["vc"].cpu().numpy(), t["scales"].cpu().numpy()]))
+
+
 @pytest.mark.parametrize("nd", [0, 2])
 def test_rows_behind_the_last_sequence(nd):
     c = Case([1, 1], [20, 30], seed=20)
