@@ -7,22 +7,31 @@
 // a unit's tiles and quant_join_kernel adds up their parts.
 //
 // Inside a CTA:
-//   warp 17     copies a tile's codes (TMA through the block table), a tile ahead
-//   warp 18     a tile's scales: pages two tiles ahead, scales one
-//   warps 8-15  write them as fp16 (exactly) in the layout the products read, four keys
-//               and four values: rings of two key and two value tiles. Both query tiles
-//               use what is converted once.
-//   warp 16     S = Q K^T (N columns of TMEM per buffer), O += P V (A = P from TMEM,
-//               written over its S). QT 2: a buffer per query tile, whose softmax runs
-//               while the other's products do; QT 1: two buffers in turn.
-//   warps 0-7   softmax, a thread per row, warps 0-3 for query tile 0 (or the only
-//               one), 4-7 for tile 1.
-// TMEM columns: O, 128 for each of two query tiles or 256 for one | two buffers of N.
+//   warp 25      copies a tile's codes (TMA through the block table), C tiles ahead
+//   warp 26      a tile's scales: pages two tiles ahead, scales one
+//   warps 16-23  write codes as fp16 (exactly) in the layout the products read, four
+//                warps keys and four values, into rings of R key and R value tiles. Both
+//                query tiles use what is converted once.
+//   warp 24      S = Q K^T (N columns of TMEM per buffer), O += P V (A = P from TMEM,
+//                written over its S). Two buffers per query tile: scores run two key tiles
+//                ahead, so that a softmax does not wait for them.
+//   warps 0-15   softmax, two threads per row, each with half of a tile's keys and of the
+//                output's channels (QT 1: warps 0-7). Per tile the two tell each other
+//                whether a maximum rises by more than kLazy, which is rare (pair_any).
+// TMEM columns: O, 128 for each of two query tiles or 256 for one | 2 QT buffers of N |
+// QT 1: the queries' second addends.
 //
 // Scales cost next to nothing: a page's rows come 16 at a time, so 16 columns of S
 // have one key scale, which joins the factor of the exponent's multiply-add, and one
 // value scale 2^e, whose e joins its addend (see kShift in pa_quant_read.cuh). The sum of
 // the 16 probabilities is multiplied by 2^-e again.
+//
+// Measured: some 4096 tokens each behind 4096 and 2096, 32 heads over 8 of 128 / 128, 775 us in bf16
+// and 937 in fp16 (queries in two addends); the products alone take 360 at the card's
+// bf16 rate. What bounds it is the way of one tile through a softmax, some 2000 cycles, most
+// of them waiting: without the products it takes 721 us, without exponentials and
+// conversion 713, without either 657. One thread per row (64 exponentials each) took 790,
+// tiles of 128 keys with one buffer per query tile no less.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -36,7 +45,7 @@ namespace {
 
 using namespace pa::tc;
 
-constexpr int kConvWarp = 8, kMmaWarp = 16, kCopyWarp = 17, kScaleWarp = 18, kThreads = 20 * 32;
+constexpr int kConvWarp = 16, kMmaWarp = 24, kCopyWarp = 25, kScaleWarp = 26, kThreads = 28 * 32;
 constexpr int kSlab = kRows * 128;  // bytes of a 64-channel slab of 128 query rows
 constexpr int N = 64;               // keys of a tile
 constexpr int kMaxRing = 4, kAhead = 8;  // tiles converted ahead; tiles whose scales are kept
@@ -66,8 +75,7 @@ struct PreP {
 };
 
 // wait_bar in less code (that of a CTA's roles together has to fit the instruction
-// caches) and fewer instructions: waiting warps took two thirds of all issued ones.
-// IDLE: for roles that run ahead, which sleep between two looks.
+// caches) and fewer instructions. IDLE: for roles that run ahead, which sleep between two looks.
 template <bool IDLE>
 __device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t par, volatile int* abort,
                                            int32_t* err) {
@@ -173,8 +181,37 @@ __device__ __forceinline__ void unpack_f32(uint64_t v, float* a, float* b) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v));
 }
 // Registers of a warpgroup's threads, out of what the block was launched with:
-// 96 for each of five warpgroups, 2 x kSoftRegs + 2 x kConvRegs + kMmaRegs = 480.
-constexpr int kSoftRegs = 144, kConvRegs = 64, kMmaRegs = 64;
+// 72 for each of seven warpgroups, 4 x kSoftRegs + 2 x kConvRegs + kMmaRegs = 504.
+constexpr int kSoftRegs = 80, kConvRegs = 64, kMmaRegs = 56;
+static_assert(4 * kSoftRegs + 2 * kConvRegs + kMmaRegs <= 7 * 72, "registers");
+// Two warps that share 32 rows of a query tile.
+__device__ __forceinline__ void pair_sync(int pair) {
+  __syncwarp();
+  asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory");
+}
+__device__ __forceinline__ bool pair_any(int pair, bool x) {
+  uint32_t any;
+  __syncwarp();
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, %2, 64, p;\n"
+      " selp.b32 %0, 1, 0, q;\n}\n"
+      : "=r"(any)
+      : "r"((uint32_t)x), "r"(pair + 1)
+      : "memory");
+  return any;
+}
+// Floats as integers of the same order.
+__device__ __forceinline__ int ordered(float x) {
+  const int i = __float_as_int(x);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int i) {
+  return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+// 2^-e of a whole number e held as a float.
+__device__ __forceinline__ float inverse_pow2(float e) {
+  return __int_as_float((127 << 23) - (__float_as_int(e + 12582912.f) << 23));
+}
 template <int R>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
@@ -185,14 +222,14 @@ __device__ __forceinline__ void fewer_registers() {
 }
 // The query rows of a tile (token, head), normalized and rotated, as fp16 in
 // swizzled slabs; mult: what takes the factor of the lane's row back, times the scale. Rows behind
-// the last are zeros. By the tile's four warps. Rows in two addends (two_addends): the
+// the last are zeros. By the tile's eight warps, 16 rows each: rows of the warp's quad from
+// 16 part on. mult: of the 32 rows, by way of s_row. Rows in two addends (two_addends): the
 // second one into rest_s, laid out the same, and from there into TMEM where rest_t names
 // columns.
 template <typename T>
 __device__ __noinline__ void load_query(const PreP& A, const Unit& u, int g, int tile, int rows,
-                                        int warp, int lane, uint8_t* q_s, uint8_t* rest_s,
-                                        uint32_t rest_t, float* mult) {
-  float own = 0.f;  // of row 32 warp + lane
+                                        int warp, int part, int pair, int lane, uint8_t* q_s,
+                                        uint8_t* rest_s, uint32_t rest_t, float* s_row, float* mult) {
   const ReadP& P = A.R;
   int lpr = 2;
   while (lpr * 8 < P.hs) lpr <<= 1;
@@ -204,7 +241,7 @@ __device__ __noinline__ void load_query(const PreP& A, const Unit& u, int g, int
   constexpr bool kRest = std::is_same<T, __half>::value;
   // all rows on their way, to the places where they are changed
 #pragma unroll 4
-  for (int r0 = 0; r0 < 32; r0 += step) {
+  for (int r0 = 16 * part; r0 < 16 * part + 16; r0 += step) {
     const int row = warp * 32 + r0 + lane / lpr;
     const bool live = row < rows;
     const int tok = live ? row / P.grp : 0, h = live ? row - tok * P.grp : 0;
@@ -215,8 +252,9 @@ __device__ __noinline__ void load_query(const PreP& A, const Unit& u, int g, int
                    "l"(live ? src : reinterpret_cast<const T*>(P.query)), "r"(live ? 16 : 0)
                    : "memory");
   }
-  if (P.rd > 0 && warp * 32 + lane < rows) {  // and the rows' angles
-    const int64_t at = (u.pos + tile * A.tpc + (warp * 32 + lane) / P.grp) * half;
+  const int mine = warp * 32 + 16 * part + lane;
+  if (P.rd > 0 && lane < 16 && mine < rows) {  // and the rows' angles
+    const int64_t at = (u.pos + tile * A.tpc + mine / P.grp) * half;
     for (int c = 0; c < half; c += 64) {
       asm volatile("prefetch.global.L1 [%0];" ::"l"(reinterpret_cast<const T*>(P.cos_cache) + at + c));
       asm volatile("prefetch.global.L1 [%0];" ::"l"(reinterpret_cast<const T*>(P.sin_cache) + at + c));
@@ -224,7 +262,7 @@ __device__ __noinline__ void load_query(const PreP& A, const Unit& u, int g, int
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1
-  for (int r0 = 0; r0 < 32; r0 += step) {
+  for (int r0 = 16 * part; r0 < 16 * part + 16; r0 += step) {
     const int row = warp * 32 + r0 + lane / lpr;
     const bool live = row < rows;
     float x[8];
@@ -242,13 +280,13 @@ __device__ __noinline__ void load_query(const PreP& A, const Unit& u, int g, int
       *place(row) = hx;
       if (kRest && P.two) *(place(row) + ((rest_s - q_s) >> 4)) = rest;
     }
-    const float v = __shfl_sync(0xffffffffu, back, ((lane - r0) & (step - 1)) * lpr);
-    if (lane >= r0 && lane < r0 + step) own = v;
+    if ((lane & (lpr - 1)) == 0) s_row[row] = back;
   }
+  __syncwarp();
+  pair_sync(pair);
   if (kRest && rest_t) {  // (channels behind hs are not multiplied)
-    __syncwarp();
     const int row = warp * 32 + lane;
-    for (int c = 0; c < A.slabs; ++c) {
+    for (int c = part; c < A.slabs; c += 2) {
       uint32_t w[32];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -260,7 +298,7 @@ __device__ __noinline__ void load_query(const PreP& A, const Unit& u, int g, int
     tmem_wait_st();
     tc_fence_before();
   }
-  *mult = own * (P.cap_in > 0.f ? P.cap_in : P.scale_log2);
+  *mult = s_row[warp * 32 + lane] * (P.cap_in > 0.f ? P.cap_in : P.scale_log2);
 }
 
 // mma_ss and mma_ts with descriptors of a common upper word.
@@ -312,7 +350,9 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
   extern __shared__ uint8_t smem_raw[];
   __shared__ Unit s_unit;
   __shared__ Bars bars_s;
-  __shared__ float4 s_scale[kAhead][kSegs];  // key scale, exponent e of the value's, 2^-e
+  __shared__ float2 s_scale[kAhead][kSegs];  // key scale, exponent e of the value's
+  __shared__ int s_row[QT * kRows];  // rows' factors, maxima, sums, in turn
+  __shared__ uint8_t s_fail[QT * 4];
   __shared__ int2 s_in[kAhead];  // segments with a key, a value scale (or nothing to see), a bit each
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
@@ -348,16 +388,16 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
     for (int i = lane; i < kNumBars; i += 32) {
       uint64_t* at = all + i;
       uint32_t count = 1;
-      if (at == &bars->q_full) count = QT * 4;
+      if (at == &bars->q_full) count = QT * 8;
       if ((at >= bars->k_full && at < bars->k_full + kMaxRing) ||
           (at >= bars->v_full && at < bars->v_full + kMaxRing))
         count = 4;
-      if ((at >= bars->p_full && at < bars->p_full + 4) ||
-          (at >= bars->c_empty && at < bars->c_empty + 4))
-        count = 4;
+      if (at >= bars->c_empty && at < bars->c_empty + 4) count = 4;
+      if (at >= bars->p_full && at < bars->p_full + 4) count = 8;
       mbar_init(smem_u32(at), count);
     }
     if (lane < 16) bars->odd[lane] = 0;
+    if (lane < QT * 4) s_fail[lane] = 0;
     if (lane == 0) bars->bad = bars->abort = bars->any_odd = 0;
     fence_barrier_init();
   } else if (warp == kMmaWarp) {
@@ -385,12 +425,15 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
   auto wait_idle = [&](uint64_t* bar, uint32_t par) {
     return wait_short<true>(smem_u32(bar), par, abort, P.err_flags);
   };
-  const int qt = QT == 2 ? warp >> 2 : 0;  // (softmax warps)
+  const int qt = QT == 2 ? (warp >> 2) & 1 : 0;  // (softmax warps)
+  const int half = QT == 2 ? warp >> 3 : warp >> 2;  // of a tile's keys, and of the channels
   const int quad = warp & 3, row = quad * 32 + lane;
   const int tok0 = qt * A.tpc, ntok = run ? max(0, min(A.tpc, U.ntok - tok0)) : 0;
   const int rows = ntok * P.grp;
   const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
-  const bool soft = warp < (QT == 2 ? 8 : 4);
+  const bool soft = warp < QT * 8;
+  const int pair = qt * 4 + quad;
+  int* row_at = &s_row[qt * kRows + row];
   float m = -INFINITY, l = 0.f;
   bool ok = true;
 
@@ -401,11 +444,16 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
       // =================== softmax ===================
       uint8_t* q_t = q_s + qt * q_bytes;
       float mult;
-      if (P.bf16) load_query<__nv_bfloat16>(A, U, g, qt, rows, quad, lane, q_t, q_t, 0, &mult);
-      else load_query<__half>(A, U, g, qt, rows, quad, lane, q_t, QT == 2 ? q_t + QT * q_bytes : k_s,
-                              QT == 1 && TWO ? lane_addr + kColRest : 0, &mult);
+      float* s_back = reinterpret_cast<float*>(&s_row[qt * kRows]);
+      if (P.bf16) load_query<__nv_bfloat16>(A, U, g, qt, rows, quad, half, pair, lane, q_t, q_t, 0, s_back,
+                                            &mult);
+      else load_query<__half>(A, U, g, qt, rows, quad, half, pair, lane, q_t,
+                              QT == 2 ? q_t + QT * q_bytes : k_s,
+                              QT == 1 && TWO ? lane_addr + kColRest : 0, s_back, &mult);
       fence_proxy_async();
       arrive_warp(&bars->q_full, lane);
+      pair_sync(pair);
+      if (half == 0) *row_at = ordered(-INFINITY);
       // keys counted from the first tile's first one
       const int64_t key0 = (int64_t)U.begin * N, pos_r = U.pos + tok0 + row / P.grp;
       const int last_r = (int)((P.cross ? U.pos_hi : min(pos_r, U.pos_hi)) - key0);
@@ -421,34 +469,26 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
         const int j0 = k * N;
         const bool edge = j0 < lo_hi || j0 + N - 1 > last0;
         // (S comes behind the conversion of its keys, and that behind the tile's scales)
-        ok = __all_sync(0xffffffffu, wait(&bars->s_full[buf], par));
-        if (!ok) break;
+        ok = __all_sync(0xffffffffu, ok && wait(&bars->s_full[buf], par));
         tc_fence_after();
-        const float4* scale = s_scale[k % kAhead];
-        uint32_t x[N / 32][32];
-#pragma unroll
-        for (int c = 0; c < N / 32; ++c) tmem_ld32_nowait(cols + c * 32, x[c]);
+        uint32_t x[32];
+        tmem_ld32_nowait(cols + half * 32, x);
+        const float2 sc[2] = {s_scale[k % kAhead][2 * half], s_scale[k % kAhead][2 * half + 1]};
         tmem_wait_ld();
+        reg_fence(x);
+        if (edge) {  // bits of the columns that the row sees
+          const int j1 = j0 + half * 32;
+          const int a = min(32, max(0, lo_r - j1)), b = max(-1, min(31, last_r - j1)) + 1;
+          const uint32_t seen = (b < 32 ? (1u << b) - 1 : ~0u) & (a < 32 ? ~0u << a : 0u);
 #pragma unroll
-        for (int c = 0; c < N / 32; ++c) reg_fence(x[c]);
-        float top = -INFINITY;
-        if (edge) {
-          const int c0 = max(0, lo_r - j0), c1 = max(-1, min(N - 1, last_r - j0));  // seen columns
-#pragma unroll
-          for (int c = 0; c < N / 32; ++c) {
-            // bits c0 - 32 c .. c1 - 32 c
-            const int a = min(32, max(0, c0 - 32 * c)), b = min(32, max(0, c1 + 1 - 32 * c));
-            const uint32_t seen = (b < 32 ? (1u << b) - 1 : ~0u) & (a < 32 ? ~0u << a : 0u);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) hide_unless(seen & (1u << e), x[c][e]);
-          }
+          for (int e = 0; e < 32; ++e) hide_unless(seen & (1u << e), x[e]);
         }
         // (a masked score, -inf, times 0 would be NaN)
-        auto factor_of = [&](const float4& sc) { return fmaxf(sc.x * mult, 1e-37f); };
-        auto at = [&](int i) { return __uint_as_float(x[i / 32][i % 32]); };
+        auto factor_of = [&](const float2& c) { return fmaxf(c.x * mult, 1e-37f); };
+        auto at = [&](int i) { return __uint_as_float(x[i]); };
+        float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kSegs; ++i) {
-          const float4 sc = scale[i];
+        for (int i = 0; i < 2; ++i) {
           float v0 = max3(at(16 * i), at(16 * i + 1), at(16 * i + 2));
           float v1 = max3(at(16 * i + 3), at(16 * i + 4), at(16 * i + 5));
 #pragma unroll
@@ -457,87 +497,105 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
             v1 = max3(v1, at(16 * i + e + 2), at(16 * i + e + 3));
           }
           v0 = max3(fmaxf(v0, v1), at(16 * i + 14), at(16 * i + 15));
-          const float f = factor_of(sc);
+          const float f = factor_of(sc[i]);
           if (CAP) v0 = v0 == -INFINITY ? v0 : capped(P, v0 * f);
-          top = fmaxf(top, fmaf(v0, CAP ? 1.f : f, sc.y));
+          top = fmaxf(top, fmaf(v0, CAP ? 1.f : f, sc[i].y));
         }
+        // The row's maximum goes by both halves. (Both warps have read their scores behind
+        // this, and P may go over them. A wait that ran out is told there: neither warp
+        // may wait for the other alone.)
         float factor = 1.f;
-        if (top > m + kLazy) {
-          factor = ex2(m - top);  // (from -inf: 0)
-          m = top;
-          l *= factor;
+        if (!ok && lane == 0) s_fail[pair] = 1;
+        tc_fence_before();
+        const bool rise = pair_any(pair, top > m + kLazy || !ok);
+        tc_fence_after();
+        if (rise) {
+          atomicMax(row_at, ordered(top));
+          pair_sync(pair);
+          ok = *const_cast<volatile uint8_t*>(&s_fail[pair]) == 0;
+          if (!ok) break;
+          const float both = unordered(*const_cast<volatile int*>(row_at));
+          if (both > m + kLazy) {
+            factor = ex2(m - both);  // (from -inf: 0)
+            m = both;
+            l *= factor;
+          }
         }
         const float nm = kShift - (m == -INFINITY ? 0.f : m);
+        // in passes over the registers, so that the exponentials issue back to back
+        float v[32];
 #pragma unroll
-        for (int c = 0; c < N / 32; ++c) {
-          // in passes over the registers, so that the exponentials issue back to back
-          float v[32];
-          float4 sc[2];
+        for (int h = 0; h < 2; ++h) {
+          const float f = factor_of(sc[h]);
+          const float fe = CAP ? 1.f : f, add = nm + sc[h].y;
+          const uint64_t f2 = pack_f32(fe, fe), a2 = pack_f32(add, add);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            sc[h] = scale[2 * c + h];
-            const float f = factor_of(sc[h]);
-            const float fe = CAP ? 1.f : f, add = nm + sc[h].y;
-            const uint64_t f2 = pack_f32(fe, fe), a2 = pack_f32(add, add);
-#pragma unroll
-            for (int e = 16 * h; e < 16 * h + 16; e += 2) {
-              float a = __uint_as_float(x[c][e]), b = __uint_as_float(x[c][e + 1]);
-              if (CAP) {
-                a = a == -INFINITY ? a : capped(P, a * f);
-                b = b == -INFINITY ? b : capped(P, b * f);
-              }
-              uint64_t y;
-              asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(pack_f32(a, b)), "l"(f2), "l"(a2));
-              unpack_f32(y, &v[e], &v[e + 1]);
+          for (int e = 16 * h; e < 16 * h + 16; e += 2) {
+            float a = at(e), b = at(e + 1);
+            if (CAP) {
+              a = a == -INFINITY ? a : capped(P, a * f);
+              b = b == -INFINITY ? b : capped(P, b * f);
             }
+            uint64_t y;
+            asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(pack_f32(a, b)), "l"(f2), "l"(a2));
+            unpack_f32(y, &v[e], &v[e + 1]);
           }
+        }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = ex2(v[e]);
-          uint32_t p[16];
-          uint64_t sum[4];
+        for (int e = 0; e < 32; ++e) v[e] = ex2(v[e]);
+        uint32_t p[16];
+        uint64_t sum[4];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            p[e] = pack2<__half>(v[2 * e], v[2 * e + 1]);
-            const uint64_t p2 = pack_f32(v[2 * e], v[2 * e + 1]);
-            const int q = (e >> 3) * 2 + (e & 1);  // two sums for each scale
-            if ((e & 7) < 2) sum[q] = p2;
-            else asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[q]) : "l"(p2));
-          }
-          tmem_st16(cols + c * 16, p);
+        for (int e = 0; e < 16; ++e) {
+          p[e] = pack2<__half>(v[2 * e], v[2 * e + 1]);
+          const uint64_t p2 = pack_f32(v[2 * e], v[2 * e + 1]);
+          const int q = (e >> 3) * 2 + (e & 1);  // two sums for each scale
+          if ((e & 7) < 2) sum[q] = p2;
+          else asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[q]) : "l"(p2));
+        }
+        tmem_st16(cols + half * 16, p);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[2 * h]) : "l"(sum[2 * h + 1]));
-            float a, b;
-            unpack_f32(sum[2 * h], &a, &b);
-            l = fmaf(a + b, sc[h].z, l);
-          }
+        for (int h = 0; h < 2; ++h) {
+          asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[2 * h]) : "l"(sum[2 * h + 1]));
+          float a, b;
+          unpack_f32(sum[2 * h], &a, &b);
+          l = fmaf(a + b, inverse_pow2(sc[h].y), l);
         }
         if (k > 0 && __any_sync(0xffffffffu, factor != 1.f)) {
           ok = __all_sync(0xffffffffu, wait(&bars->pv_done[qt], (k - 1) & 1));
-          if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < P.vhs; c += 128) {  // (columns behind vhs are nobody's)
-            uint32_t o[4][32];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tmem_ld32_nowait(o_addr + c + i * 32, o[i]);
+          for (int c = half * 32; c < P.vhs && ok; c += 64) {  // (columns behind vhs are nobody's)
+            uint32_t o[32];
+            tmem_ld32_nowait(o_addr + c, o);
             tmem_wait_ld();
+            reg_fence(o);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              reg_fence(o[i]);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[i][e] = __float_as_uint(__uint_as_float(o[i][e]) * factor);
-              tmem_st32(o_addr + c + i * 32, o[i]);
-            }
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+            tmem_st32(o_addr + c, o);
           }
         }
         tmem_wait_st();
         tc_fence_before();
-        arrive_warp(&bars->p_full[buf], lane);
+        if (ok) arrive_warp(&bars->p_full[buf], lane);
       }
       grid_dep_launch();
       if (ok) ok = __all_sync(0xffffffffu, wait(&bars->drain, 0));
       tc_fence_after();
+      // both halves' sums
+      if (!ok && lane == 0) s_fail[pair] = 1;
+      __syncwarp();
+      pair_sync(pair);
+      if (half == 1) *row_at = __float_as_int(l);
+      pair_sync(pair);
+      if (half == 0) {
+        l += __int_as_float(*row_at);
+        *row_at = __float_as_int(l);
+      }
+      __syncwarp();
+      pair_sync(pair);
+      l = __int_as_float(*const_cast<volatile int*>(row_at));
+      ok = *const_cast<volatile uint8_t*>(&s_fail[pair]) == 0;
     }
     if (P.early) grid_dep_wait();
     // =================== outputs ===================
@@ -554,7 +612,7 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
             if (j <= pos_r && j >= pos_r - back) l = NAN;
           }
       }
-      if (bad && lane == 0) raise_flag(P.err_flags, PA_DEVERR_BLOCK);
+      if (bad && lane == 0 && half == 0) raise_flag(P.err_flags, PA_DEVERR_BLOCK);
       const uint32_t o_addr = lane_addr + (QT == 2 ? qt * 128 : 0);
       if (A.splits == 1) {
         float sum = l;
@@ -564,7 +622,7 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
         const float inv = 1.f / sum;
         __half* dst = reinterpret_cast<__half*>(P.out) + ((U.t + tok0 + tok) * P.H + h) * P.vhs;
 #pragma unroll 1
-        for (int c = 0; c < P.vhs; c += 16) {
+        for (int c = half * 16; c < P.vhs; c += 32) {
           uint32_t r[16], w[8];
           if (n > 0) tmem_ld16(o_addr + c, r);
 #pragma unroll
@@ -580,7 +638,7 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
         const int64_t at = (int64_t)blockIdx.x * (QT * kRows) + qt * kRows + row;
         float* dst = A.ws_o + at * P.vhs;
 #pragma unroll 1
-        for (int c = 0; c < P.vhs; c += 16) {
+        for (int c = half * 16; c < P.vhs; c += 32) {
           uint32_t r[16];
           tmem_ld16(o_addr + c, r);
           if (live)
@@ -588,7 +646,7 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
             for (int e = 0; e < 16; e += 4)
               *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
         }
-        if (live) A.ws_ml[at] = make_float2(bad ? NAN : m, l);
+        if (live && half == 0) A.ws_ml[at] = make_float2(bad ? NAN : m, l);
       }
     }
   } else if (warp < kMmaWarp) {
@@ -686,7 +744,7 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
         const int steps = P.hs >> 4;
         const uint32_t k_base = smem_u32(k_s), v_base = smem_u32(v_s), q_base = smem_u32(q_s);
         // Descriptors by their lower words (the upper ones stay as they are), with offsets
-        // fixed at compile time in a slab: an MMA takes its thread some 12 cycles to issue
+        // fixed at compile time in a slab: an MMA takes its thread 15 to 60 cycles to issue
         // so, and 75 to 100 with offsets worked out step by step.
         const uint64_t qk_proto = sdesc(q_base, 16, 1024), v_proto = sdesc(v_base, kKBox, 1024);
         const uint32_t qk_hi = (uint32_t)(qk_proto >> 32), v_hi = (uint32_t)(v_proto >> 32);
@@ -849,8 +907,7 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
         const unsigned vb = __ballot_sync(0xffffffffu, vin || pg0 < 0);
         constexpr unsigned kAll = (1u << kSegs) - 1;
         if (lane < kSegs)
-          s_scale[k % kAhead][lane] = make_float4(kin ? sc0.x : 1.f, vin ? ve : kLeast,
-                                                  pow2(-(vin ? ve : kLeast)), 0.f);
+          s_scale[k % kAhead][lane] = make_float2(kin ? sc0.x : 1.f, vin ? ve : kLeast);
         if (lane == 0) s_in[k % kAhead] = make_int2(kb & kAll, vb & kAll);
         arrive_warp(&bars->sc_full[k % kAhead], lane);
         pg0 = pg1;
