@@ -43,10 +43,11 @@
  *
  * Arithmetic: products accumulate in f32, softmax is f32, out is rounded once.
  * Operands of the products are fp16 whatever the dtype: codes exactly, the
- * rotated query times a power of two that brings its row's largest channel
- * to 2^14 (11 bits of each channel, and none lost down to 2^-28 of the
- * largest), probabilities times the values' scales relative to the row's
- * largest such product (11 bits, down to 2^-22 of it; 2^-33 of it at worst below).
+ * query times a power of two that brings its row's largest channel to 2^14
+ * (11 bits of each channel, none lost down to 2^-28 of the largest; with fp16
+ * out and rotation or norm, which leave more than 11 bits, two addends: 22),
+ * probabilities times the values' scales relative to the row's largest such
+ * product (11 bits, down to 2^-22 of it; 2^-33 of it at worst below).
  */
 #ifndef PA_QUANT_H
 #define PA_QUANT_H

@@ -83,7 +83,8 @@ def attend(query, kc, vc, scales, cos, sin, cumseq, past, table, p, head_sink=No
     roundings: the output's own (at most u |out|, u = 2^-8 or 2^-11); those of the fp16 operands, taken
     as independent, six times their root sum of squares with 2^-11 each (probabilities n_p, query n_q);
     f32 accumulation, which may cut off 2^-23 in each of n / 16 additions of 16 keys; and the fp16 floor
-    of probabilities, 2^-36 of the row's largest product of probability and scale for each key."""
+    of probabilities, 2^-36 of the row's largest product of probability and scale for each key (an eighth
+    of what the header allows: half of fp16's least step 2^-24 against a largest product of 2^8 or more)."""
     H, kv, hs = p["num_heads"], p["kv_num_heads"], p["head_size"]
     vhs, bs = p["v_head_size"] or hs, p["block_size"]
     scale = p["scale"] or hs ** -0.5
