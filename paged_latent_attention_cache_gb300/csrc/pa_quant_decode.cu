@@ -11,7 +11,8 @@ namespace {
 using namespace rows;
 
 // Joins the parts of a unit: a warp for four accumulators of a block of rows and every
-// kSlices-th part, then the slices.
+// kSlices-th part, then the slices. Bound by latency: 4 to 7 us. (A warp for all parts: two
+// sequences of up to 131072 keys took 2.6 us longer.)
 constexpr int kSlices = 4;
 template <int VP, int NB>
 __global__ void __launch_bounds__(64 * VP * NB * kSlices)
