@@ -352,7 +352,7 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
   __shared__ Bars bars_s;
   __shared__ float2 s_scale[kAhead][kSegs];  // key scale, exponent e of the value's
   __shared__ int s_row[QT * kRows];  // rows' factors, maxima, sums, in turn
-  __shared__ uint8_t s_fail[QT * 4];
+  __shared__ int s_fail[QT * 4];  // 1 + the tile at which a pair's warps give up
   __shared__ int2 s_in[kAhead];  // segments with a key, a value scale (or nothing to see), a bit each
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
@@ -505,14 +505,16 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
         // this, and P may go over them. A wait that ran out is told there: neither warp
         // may wait for the other alone.)
         float factor = 1.f;
-        if (!ok && lane == 0) s_fail[pair] = 1;
+        if (!ok && lane == 0) s_fail[pair] = k + 1;
         tc_fence_before();
         const bool rise = pair_any(pair, top > m + kLazy || !ok);
         tc_fence_after();
         if (rise) {
           atomicMax(row_at, ordered(top));
           pair_sync(pair);
-          ok = *const_cast<volatile uint8_t*>(&s_fail[pair]) == 0;
+          // (the other may be a tile ahead, and give up there)
+          const int fail = *const_cast<volatile int*>(&s_fail[pair]);
+          ok = fail == 0 || fail > k + 1;
           if (!ok) break;
           const float both = unordered(*const_cast<volatile int*>(row_at));
           if (both > m + kLazy) {
@@ -595,7 +597,7 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
       __syncwarp();
       pair_sync(pair);
       l = __int_as_float(*const_cast<volatile int*>(row_at));
-      ok = *const_cast<volatile uint8_t*>(&s_fail[pair]) == 0;
+      ok = *const_cast<volatile int*>(&s_fail[pair]) == 0;
     }
     if (P.early) grid_dep_wait();
     // =================== outputs ===================
