@@ -100,10 +100,12 @@ quant_combine_kernel(const __grid_constant__ DecP A) {
 // Host side
 // ---------------------------------------------------------------------------
 // What a unit counts on the line beside its tiles: its query's rows, the joining of its
-// warps and its results take a CTA as long as some 20 tiles. Without it, parts with many
-// short units were the last ones by far. Measured with 0, 12, 20, 40 (us): 32 sequences
-// of 90 to 1500 keys, 16 heads of 64, 50.2, 32.1, 29.3, 29.8; of 256 to 1024 keys, 8 kv heads
-// of 128 with 4 query heads each, 24.3, 18.8, 19.1, 21.5; of 1024 to 8192, 71.0, 67.5, 66.4, 67.2.
+// warps and its results take a CTA as long as some 20 tiles, with 16 rows 40. Without it,
+// parts with many short units were the last ones by far. Measured with 0, 12, 20, 40 (us).
+// 8 rows: 32 sequences of 90 to 1500 keys, 16 heads of 64, 50.2, 32.1, 29.3, 29.8; of 256 to
+// 1024 keys, 8 kv heads of 128 with 4 query heads each, 24.3, 18.8, 19.1, 21.5; of 1024 to 8192,
+// 71.0, 67.5, 66.4, 67.2. 16 rows: two sequences of 60000 to 131072 keys, 4 kv heads with 16 each,
+// 66.7, 62.7, 61.2, 59.1; drafts of 3 to 7 tokens over 2000 to 16000, 113, 101, 97.5, 93.9.
 constexpr int kExtra = 20;
 
 struct Plan {
@@ -151,7 +153,7 @@ cudaError_t launch_rows(const Geometry& g, const QuantArgs& a, bool decode) {
   A.rows = 8 * p.nb;
   A.tile = 16 * p.th;
   A.box = std::min(g.bs, A.tile);
-  A.extra = kExtra;
+  A.extra = kExtra * p.nb;
   A.min_part = 2 * kWarps;
   const int64_t units =
       decode ? nseq * g.kvh * ((A.R.grp + A.rows - 1) / A.rows)
