@@ -11,8 +11,9 @@
  *   scales      float32 [num_blocks, kvH, 2]         of keys and of values
  *
  * A scale is 2^e with e in -48..48, or 0 where its page has none yet (any
- * other value counts as 0). A page's scales belong to the page: pa_pages.h
- * carries them along as a tensor of PA_PAGE_WHOLE.
+ * other value counts as 0). The rows of a page without one are zeros, whatever
+ * their codes. A page's scales belong to the page: pa_pages.h carries them along
+ * as a tensor of PA_PAGE_WHOLE.
  *
  * Write: for page p and kv head g, x = the rows of the call in that page (keys:
  * after RMSNorm and RoPE, in f32; values as they are), and of either cache

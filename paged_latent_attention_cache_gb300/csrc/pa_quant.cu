@@ -423,7 +423,10 @@ quant_restore_kernel(const __grid_constant__ RestoreArgs A) {
         c = *reinterpret_cast<const uint4*>(src + at * 16);
         const float2 two = A.scales[(int64_t)page * A.kvh + at / per];
         s = is_key ? two.x : two.y;
-        if (scale_exponent(s) == kNone) s = 0.f;
+        if (scale_exponent(s) == kNone) {  // (zeros, whatever the codes: 0 times NaN is NaN)
+          c = make_uint4(0, 0, 0, 0);
+          s = 0.f;
+        }
       }
       restore16<T>(c, s, dst);
     }

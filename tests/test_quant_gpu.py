@@ -325,6 +325,36 @@ def test_restore_any_range_and_errors():
     assert op.error_flags() & B.PA_DEVERR_CONTEXT
 
 
+@pytest.mark.parametrize("dtype", [P.BF16, P.F16])
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("none", [0.0, -0.0, 3.0, -1.0, 2.0 ** 49, math.inf, math.nan])
+def test_pages_without_a_scale_are_zeros(none, which, dtype):
+    """Whatever their codes, NaN among them: read back, in decode and in prefill of few and of many tokens. The
+    other cache's rows of the page, which have a scale, and the pages beside it keep theirs."""
+    for q, nd in (([1, 1], 2), ([3, 2], 0), ([40, 30], 0)):
+        c = Case(q, [100, 90], dtype=dtype, rd=0, seed=44)
+        t, op = c.tensors(), c.op()
+        op.write(t["key"], t["value"], t["kc"], t["vc"], t["scales"], None, None, t["slots"], t["cum"], t["past"])
+        page = int(c.table[0, 2])
+        cache = t["vc" if which else "kc"]
+        t["scales"][page, :, which] = none
+        cache[page] = 0x7F
+        cum, past = c.dev([0, 100, 190], torch.int32), c.dev([0, 0], torch.int32)
+        read = lambda: [*op.restore(t["kc"], t["vc"], t["scales"], cum, past, t["table"], 190),
+                        op.attend(t["query"], t["kc"], t["vc"], t["scales"], None, None, t["cum"], t["past"], t["table"], nd)]
+        got = read()
+        assert op.error_flags() == 0
+        assert not got[which][32:48].any()
+        cache[page] = 0
+        t["scales"][page, :, which] = 1.0
+        want = read()
+        assert all(torch.equal(a, b) and torch.isfinite(a).all() for a, b in zip(got[:2], want[:2]))
+        # (a page's scale of nothing is the least one in the values' exponents: other roundings)
+        assert torch.isfinite(got[2]).all()
+        caches = [t["kc"].cpu().numpy(), t["vc"].cpu().numpy(), t["scales"].cpu().numpy()]
+        _check_out(got[2], *c.oracle(caches))
+
+
 # --------------------------------------------------------------------------------------- attention
 
 DECODES = [
