@@ -2,6 +2,7 @@
 // and the one that joins its parts.
 #include <algorithm>
 
+#include "pa_quant_plan.h"
 #include "pa_quant_rows.cuh"
 
 namespace pa {
@@ -139,10 +140,11 @@ size_t rows_workspace(const Geometry& g, int64_t nseq) {
 cudaError_t launch_rows(const Geometry& g, const QuantArgs& a, bool decode) {
   DecP A{};
   A.R = read_params(g, a);
-  const int64_t nseq = A.R.nseq, tokens = decode ? nseq : a.num_tokens;
+  const int64_t nseq = A.R.nseq, tokens = decode ? nseq : a.num_tokens;  // (at most)
   // rows of a sequence: all have as many in decode; otherwise the mean says whether a
   // unit takes 8 or 16
-  const int64_t rows = (tokens * A.R.grp + nseq - 1) / nseq;
+  const int64_t mean = decode ? nseq : range_tokens(a.num_tokens, a.num_seqs, nseq);
+  const int64_t rows = (mean * A.R.grp + nseq - 1) / nseq;
   const Plan p = plan_of(g, nseq, rows);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   A.ws_o = reinterpret_cast<float4*>(ws);

@@ -37,6 +37,7 @@
 #include <type_traits>
 
 #include "pa_diff_common.cuh"
+#include "pa_quant_plan.h"
 #include "pa_quant_read.cuh"
 
 namespace pa {
@@ -65,12 +66,12 @@ constexpr int kNumBars = 1 + 4 * kMaxRing + 8 + kAhead + 3 + 8;
 
 struct PreP {
   ReadP R;
-  float* ws_o;   // [units * kvh * splits][QT * 128][vhs]
-  float2* ws_ml; // [units * kvh * splits][QT * 128] maximum (log2 domain; NaN: an invalid page), sum
+  float* ws_o;   // [planned * splits][QT * 128][vhs]
+  float2* ws_ml; // [planned * splits][QT * 128] maximum (log2 domain; NaN: an invalid page), sum
   int64_t num_slots;
   int box;       // rows of a copy: min(bs, N)
   int tpc;       // tokens of a query tile
-  int splits;    // CTAs per unit
+  int planned, splits;  // units x kv heads that are split, CTAs of each (see prefill_part)
   int slabs, vslabs, klpr, vlpr;  // 64-channel slabs, lanes for a row's 8-byte pieces
 };
 
@@ -104,7 +105,7 @@ struct Unit {
 // Unit `unit` of the batch, by a warp: the sequences' units in order, the last
 // ones (with the most keys) first. first..: what is filled in for all lanes.
 template <int QT>
-__device__ Unit resolve(const PreP& A, int unit, int split, int lane) {
+__device__ Unit resolve(const PreP& A, int unit, int split, int splits, int lane) {
   const ReadP& P = A.R;
   const int per = QT * A.tpc;
   auto units_of = [&](int i, int* q0, int* q) {
@@ -157,9 +158,9 @@ __device__ Unit resolve(const PreP& A, int unit, int split, int lane) {
         u.status = PA_DEVERR_POSITION;
       if (u.status == 0 && u.pos_hi >= u.lo) {
         const int first = (int)(u.lo / N), all = (int)(u.pos_hi / N) + 1 - first;
-        const int s0 = (int)((int64_t)all * split / A.splits);
+        const int s0 = (int)((int64_t)all * split / splits);
         u.begin = first + s0;
-        u.n = (int)((int64_t)all * (split + 1) / A.splits) - s0;
+        u.n = (int)((int64_t)all * (split + 1) / splits) - s0;
       }
       return u;
     }
@@ -366,12 +367,12 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
   constexpr int kColRest = kColS + 2 * N;
   uint8_t* v_s = k_s + R * k_bytes;
   uint8_t* codes = v_s + R * v_bytes;  // C key tiles, C value tiles
-  const int split = blockIdx.x % A.splits, rest = blockIdx.x / A.splits;
-  const int g = rest % P.kvh, unit = rest / P.kvh;
+  const PrefillPart part = prefill_part(blockIdx.x, A.planned, A.splits);
+  const int split = part.split, g = part.at % P.kvh, unit = part.at / P.kvh;
 
   if (!P.early) grid_dep_wait();
   if (warp == 0) {
-    Unit u = resolve<QT>(A, unit, split, lane);
+    Unit u = resolve<QT>(A, unit, split, part.splits, lane);
     if (u.status > 1) {  // invalid positions: told, and zeros
       if (lane == 0 && g == 0 && split == 0) raise_flag(P.err_flags, u.status);
       const int64_t t0 = max((int64_t)0, u.t), t1 = min(u.t + u.ntok, P.num_tokens);
@@ -616,7 +617,7 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
       }
       if (bad && lane == 0 && half == 0) raise_flag(P.err_flags, PA_DEVERR_BLOCK);
       const uint32_t o_addr = lane_addr + (QT == 2 ? qt * 128 : 0);
-      if (A.splits == 1) {
+      if (part.splits == 1) {
         float sum = l;
         if (P.head_sink && live) sum += ex2(to_f32(P, P.head_sink, h) * kLog2e - m + kShift);
         // (the sum is NaN where a NaN was seen)
@@ -936,9 +937,7 @@ __global__ void __launch_bounds__(256) quant_join_kernel(const __grid_constant__
   const ReadP& P = A.R;
   const int unit = blockIdx.x / P.kvh, g = blockIdx.x - unit * P.kvh;
   if (threadIdx.x < 32) {
-    PreP whole = A;
-    whole.splits = 1;
-    const Unit u = resolve<QT>(whole, unit, 0, threadIdx.x);
+    const Unit u = resolve<QT>(A, unit, 0, 1, threadIdx.x);
     if (threadIdx.x == 0) s_unit = u;
   }
   __syncthreads();
@@ -999,7 +998,8 @@ size_t shared_bytes(const Geometry& g, const PreP& A, int qt, int ring, int code
 }
 
 template <int QT, int R, int C, bool CAP, bool TWO>
-cudaError_t launch_one(const Geometry& g, const QuantArgs& a, const PreP& A, int64_t ctas) {
+cudaError_t launch_one(const Geometry& g, const QuantArgs& a, const PreP& A,
+                       const PrefillGrid& grid) {
   static std::atomic<bool> configured[64];
   auto kern = quant_prefill_kernel<QT, R, C, CAP, TWO>;
   const size_t smem = shared_bytes(g, A, QT, R, C);
@@ -1010,19 +1010,21 @@ cudaError_t launch_one(const Geometry& g, const QuantArgs& a, const PreP& A, int
   CUtensorMap kmap, vmap;
   if ((e = codes_map(&kmap, a.key_cache, g, g.hs, 0, A.box)) != cudaSuccess) return e;
   if ((e = codes_map(&vmap, a.value_cache, g, g.vhs, 0, A.box)) != cudaSuccess) return e;
-  e = launch_pdl(kern, dim3((unsigned)(ctas * A.splits)), dim3(kThreads), smem, a.stream, kmap, vmap,
+  e = launch_pdl(kern, dim3((unsigned)grid.launched()), dim3(kThreads), smem, a.stream, kmap, vmap,
                  A);
   if (e != cudaSuccess || A.splits == 1) return e;
-  return launch_pdl(quant_join_kernel<QT>, dim3((unsigned)ctas, QT * kRows * (g.vhs / 4) / 256), dim3(256), 0, a.stream, A);
+  return launch_pdl(quant_join_kernel<QT>,
+                    dim3((unsigned)grid.planned, QT * kRows * (g.vhs / 4) / 256), dim3(256), 0,
+                    a.stream, A);
 }
 
 template <int QT, int R, int C>
-cudaError_t launch(const Geometry& g, const QuantArgs& a, const PreP& A, int64_t ctas) {
+cudaError_t launch(const Geometry& g, const QuantArgs& a, const PreP& A, const PrefillGrid& grid) {
   if (g.softcap > 0.f)
-    return A.R.two ? launch_one<QT, R, C, true, true>(g, a, A, ctas)
-                   : launch_one<QT, R, C, true, false>(g, a, A, ctas);
-  return A.R.two ? launch_one<QT, R, C, false, true>(g, a, A, ctas)
-                 : launch_one<QT, R, C, false, false>(g, a, A, ctas);
+    return A.R.two ? launch_one<QT, R, C, true, true>(g, a, A, grid)
+                   : launch_one<QT, R, C, true, false>(g, a, A, grid);
+  return A.R.two ? launch_one<QT, R, C, false, true>(g, a, A, grid)
+                 : launch_one<QT, R, C, false, false>(g, a, A, grid);
 }
 
 // Batches with so few query rows per sequence and kv head, on average, go to the kernel
@@ -1047,7 +1049,8 @@ size_t prefill_workspace(const Geometry& g, int64_t nseq) {
 
 cudaError_t launch_prefill(const Geometry& g, const QuantArgs& a) {
   const int64_t nseq = a.seq_end - a.seq_begin;
-  if (a.num_tokens * (g.H / g.kvh) <= kFewRows * nseq) return launch_rows(g, a, false);
+  const int64_t tokens = range_tokens(a.num_tokens, a.num_seqs, nseq);
+  if (tokens * (g.H / g.kvh) <= kFewRows * nseq) return launch_rows(g, a, false);
   PreP A{};
   A.R = read_params(g, a);
   const int qt = query_tiles(g, A.R.two);
@@ -1065,17 +1068,16 @@ cudaError_t launch_prefill(const Geometry& g, const QuantArgs& a) {
   A.num_slots = (int64_t)g.num_blocks * g.bs;
   A.ws_o = static_cast<float*>(a.workspace);
   A.ws_ml = reinterpret_cast<float2*>(A.ws_o + (size_t)g.num_sms * qt * kRows * g.vhs);
-  // (a sequence with tokens has at most one unit that is not full)
-  const int64_t units = a.num_tokens / (qt * A.tpc) + std::min((int64_t)A.R.nseq, a.num_tokens);
-  const int64_t ctas = units * g.kvh;
-  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  // parts of four tiles at least, as long as there are SMs
-  const int64_t tiles = ((int64_t)g.max_blocks * g.bs + N - 1) / N;
-  A.splits = (int)std::max<int64_t>(1, std::min<int64_t>(g.num_sms / ctas, tiles / 4));
+  const PrefillGrid grid =
+      prefill_grid(a.num_tokens, tokens, A.R.nseq, g.kvh, qt * A.tpc,
+                   ((int64_t)g.max_blocks * g.bs + N - 1) / N, g.num_sms);
+  if (grid.launched() > INT32_MAX) return cudaErrorInvalidConfiguration;
+  A.planned = (int)grid.planned;
+  A.splits = grid.splits;
   // four tiles converted ahead where they fit
-  if (qt == 1) return launch<1, 2, 1>(g, a, A, ctas);
-  return shared_bytes(g, A, 2, 4, 2) <= kMaxShared ? launch<2, 4, 2>(g, a, A, ctas)
-                                                   : launch<2, 2, 2>(g, a, A, ctas);
+  if (qt == 1) return launch<1, 2, 1>(g, a, A, grid);
+  return shared_bytes(g, A, 2, 4, 2) <= kMaxShared ? launch<2, 4, 2>(g, a, A, grid)
+                                                   : launch<2, 2, 2>(g, a, A, grid);
 }
 
 }  // namespace quant

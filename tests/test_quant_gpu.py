@@ -469,6 +469,44 @@ def test_mixed_batch():
     _run(c, 3)
 
 
+@pytest.mark.parametrize("q,past,kw", [
+    ([5, 3, 4, 5], [2000, 500, 33, 1000], dict(heads=8, kv=2, hs=128)), ([200], [1500], dict(heads=8, kv=2)),
+    ([70, 20], [700, 1200], dict(heads=4, kv=1, dtype=P.F16)), ([1, 2], [900, 40], dict(heads=16, kv=2)),
+    ([60], [900], dict(heads=4, kv=2, hs=256, vhs=256))])
+def test_a_range_does_not_depend_on_what_stands_beside_it(q, past, kw):
+    """Prefill sequences beside many decode sequences take the same way, bit for bit, as by themselves."""
+    nd = 120
+    c = Case([1] * nd + q, list(range(nd)) + past, bs=64, seed=45, **kw)
+    t, op = c.tensors(), c.op()
+    op.write(t["key"], t["value"], t["kc"], t["vc"], t["scales"], t["cos"], t["sin"], t["slots"], t["cum"], t["past"])
+    out = op.attend(t["query"], t["kc"], t["vc"], t["scales"], t["cos"], t["sin"], t["cum"], t["past"], t["table"], nd)
+    alone = op.attend(t["query"][nd:].contiguous(), t["kc"], t["vc"], t["scales"], t["cos"], t["sin"],
+                      t["cum"][nd:] - nd, t["past"][nd:].contiguous(), t["table"][nd:].contiguous(), 0)
+    assert op.error_flags() == 0
+    _check_out(out, *c.oracle([t["kc"].cpu().numpy(), t["vc"].cpu().numpy(), t["scales"].cpu().numpy()]))
+    assert torch.equal(out[nd:], alone)
+
+
+@pytest.mark.parametrize("q", [[3, 4], [150, 40], [600]])
+def test_a_range_among_sequences_without_tokens(q):
+    """More tokens than the others' number makes likely: rows outside the range stay, all of it is there."""
+    n = 300
+    c = Case([0] * n + q + [0] * n, [0] * n + [400, 70][:len(q)] + [0] * n, heads=4, kv=2, bs=64, seed=46)
+    t, op = c.tensors(), c.op()
+    op.write(t["key"], t["value"], t["kc"], t["vc"], t["scales"], t["cos"], t["sin"], t["slots"], t["cum"], t["past"])
+    want = c.oracle([t["kc"].cpu().numpy(), t["vc"].cpu().numpy(), t["scales"].cpu().numpy()])
+    out = torch.full((c.T, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+    args = (t["query"], t["kc"], t["vc"], t["scales"], t["cos"], t["sin"], t["cum"], t["past"], t["table"], out)
+    op.prefill(*args, n, n + len(q))
+    assert op.error_flags() == 0
+    _check_out(out, *want)
+    out.fill_(7.0)
+    op.prefill(*args, n + len(q) - 1, n + len(q))
+    first = c.T - q[-1]
+    assert op.error_flags() == 0 and bool((out[:first] == 7).all())
+    _check_out(out[first:], want[0][first:], want[1][first:])
+
+
 def test_scales_apart():
     """Pages whose scales lie far apart: values of 2^-48 .. 2^40 in one row's keys, and empty pages of
     zeros among them."""

@@ -1,0 +1,101 @@
+"""How reads over 8-bit caches are spread over the GPU (csrc/pa_quant_plan.h): plain host arithmetic, compiled
+by itself."""
+import ctypes
+import itertools
+import os
+import shutil
+import subprocess
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "paged_latent_attention_cache_gb300", "csrc")
+SHIM = r"""
+#include "pa_quant_plan.h"
+using namespace pa::quant;
+extern "C" {
+int64_t tokens_of(int64_t t, int64_t b, int64_t n) { return range_tokens(t, b, n); }
+void grid_of(int64_t t, int64_t r, int64_t n, int64_t kvh, int64_t per, int64_t tiles, int sms, int64_t* out) {
+  const PrefillGrid g = prefill_grid(t, r, n, kvh, per, tiles, sms);
+  out[0] = g.ctas; out[1] = g.planned; out[2] = g.splits; out[3] = g.launched();
+}
+void part_of(int cta, int planned, int splits, int* out) {
+  const PrefillPart p = prefill_part(cta, planned, splits);
+  out[0] = p.at; out[1] = p.split; out[2] = p.splits;
+}
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    cxx = shutil.which("g++")
+    if not cxx:
+        pytest.skip("no host compiler")
+    d = tmp_path_factory.mktemp("plan")
+    (d / "plan.cpp").write_text(SHIM)
+    subprocess.run([cxx, "-std=c++17", "-Wall", "-Werror", "-shared", "-fPIC", "-I", CSRC, str(d / "plan.cpp"), "-o",
+                    str(d / "plan.so")], check=True)
+    lib = ctypes.CDLL(str(d / "plan.so"))
+    i64 = ctypes.c_int64
+    lib.tokens_of.restype, lib.tokens_of.argtypes = i64, [i64] * 3
+    lib.grid_of.argtypes = [i64] * 6 + [ctypes.c_int, ctypes.POINTER(i64)]
+    lib.part_of.argtypes = [ctypes.c_int] * 3 + [ctypes.POINTER(ctypes.c_int)]
+
+    class Plan:
+        tokens = staticmethod(lib.tokens_of)
+
+        @staticmethod
+        def grid(*a):
+            out = (i64 * 4)()
+            lib.grid_of(*a, out)
+            return tuple(out)
+
+        @staticmethod
+        def part(*a):
+            out = (ctypes.c_int * 3)()
+            lib.part_of(*a, out)
+            return tuple(out)
+    return Plan
+
+
+def test_a_range_beside_decode_sequences_is_planned_as_by_itself(plan):
+    for decode, new, nseq in itertools.product((0, 1, 7, 200, 1000), (4, 20, 200, 4096), (1, 4)):
+        tokens = plan.tokens(decode + new, decode + nseq, nseq)
+        assert tokens == new == plan.tokens(new, nseq, nseq)
+        alone = plan.grid(new, new, nseq, 8, 64, 100, 152)
+        both = plan.grid(decode + new, tokens, nseq, 8, 64, 100, 152)
+        assert both[1:3] == alone[1:3] and alone[0] == alone[1]
+
+
+def test_whatever_the_offsets_every_unit_has_its_place(plan):
+    """Sequences outside the range without tokens, ranges in the middle, one token, many sequences."""
+    for num_tokens, num_seqs, nseq, kvh, per, tiles, sms in itertools.product(
+            (1, 5, 300, 4000), (1, 3, 256, 4096), (1, 2, 200), (1, 8), (1, 64, 256), (1, 9, 1000), (1, 148, 152)):
+        if nseq > num_seqs:
+            continue
+        tokens = plan.tokens(num_tokens, num_seqs, nseq)
+        assert 1 <= tokens <= num_tokens
+        ctas, planned, splits, launched = plan.grid(num_tokens, tokens, nseq, kvh, per, tiles, sms)
+        assert 1 <= planned <= ctas and splits >= 1 and launched == ctas + planned * (splits - 1)
+        # units of any offsets that rise: all in one sequence, or spread over as many as there are
+        for n in (1, min(nseq, num_tokens)):
+            assert ((num_tokens - n + 1 + per - 1) // per + n - 1) * kvh <= ctas
+        assert splits == 1 or planned * splits <= sms  # (the workspace holds as many parts)
+        assert splits == 1 or splits <= tiles // 4
+
+
+def test_parts_cover_every_unit_once(plan):
+    for planned, splits, more in itertools.product((1, 3, 16), (1, 2, 9), (0, 1, 40)):
+        seen = {}
+        for cta in range(planned * splits + more):
+            at, split, n = plan.part(cta, planned, splits)
+            assert 0 <= split < n
+            if n > 1:
+                assert cta == at * n + split < planned * splits  # (where the joining kernel looks for it)
+            assert seen.setdefault(at, n) == n or split == 0
+            seen[(at, split)] = cta
+        units = sorted(k for k in seen if isinstance(k, int))
+        assert units == list(range(planned + more))
+        assert all((at, s) in seen for at in units for s in range(seen[at]))
+        assert sum(isinstance(k, tuple) for k in seen) == planned * splits + more
