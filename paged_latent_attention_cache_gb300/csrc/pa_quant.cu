@@ -8,6 +8,7 @@
 
 #include "pa_quant_common.cuh"
 #include "pa_quant_internal.h"
+#include "pa_quant_plan.h"
 
 namespace pa {
 
@@ -31,21 +32,13 @@ constexpr int kMaxBlock = 4096;  // rows of a page
 // first(b + 1) - first(b) >= q / bs + 2. So a CTA finds its sequence by a search
 // over cumseq, an offset per thread at a time.
 //
-// Bound by instructions for prompts (14200 new tokens of 8 kv heads of 128 / 128, 94 MB:
+// Bound by instructions for prompts (14740 new tokens of 8 kv heads of 128 / 128, 94 MB:
 // 39.5 us, 2.4 TB/s) and by its chain of loads for single tokens (4.4 us). All rows of a
 // run are on their way to shared memory (cp.async) before its slots are looked at; each
 // thread copies just what it will read, so no barrier stands between. The rotated keys
 // stay there in f32 for their encoding. With a load per row where it was used those tokens
 // took 66 us, with keys rotated twice 52.
 // ---------------------------------------------------------------------------
-// Write: shared memory for a run's rows, and threads. Warps by the kilobyte of rows:
-// what a run waits for is other runs' time, and the more rows there are the fewer runs an
-// SM holds. 128 threads up to kFewBytes of rows, 256 up to half of kRowBytes, then 512
-// with all of it. Measured with 128, 256, 512 threads (us; 14200 tokens as above):
-// pages of 16 rows 42.6, 58.5, 114.8; 32: 37.8, 43.1, 66.8; 64: 47.7, 39.5, 49.0; 128: 70.3, 53.2, 43.3;
-// one row for each of 32 sequences 4.4, 5.2, 7.1.
-constexpr int kRowBytes = 96 * 1024, kFewBytes = 24 * 1024;
-
 struct WriteArgs {
   const void* key;
   const void* value;
@@ -616,22 +609,15 @@ pa_status pa_quant_write(const pa_quant_params* p, const void* key, const void* 
   int lpr = 2;
   while (lpr * 8 < g.hs || lpr * 8 < g.vhs) lpr *= 2;
   const int row_bytes = (2 * g.hs + g.vhs) * 2;
-  // rows of a run, as the batch has them on average; see kFewBytes
-  const int64_t mean = std::min<int64_t>(g.bs, (num_tokens + num_seqs - 1) / num_seqs) * row_bytes;
-  const int threads = mean <= quant::kFewBytes ? 128 : mean <= quant::kRowBytes / 2 ? 256 : 512;
-  const int room = threads == 512 ? quant::kRowBytes : quant::kRowBytes / 2;
-  const int at_once = threads / lpr;
-  int cap = room / row_bytes / at_once * at_once;
-  if (cap > g.bs) cap = (g.bs + at_once - 1) / at_once * at_once;
-  const size_t smem = (size_t)cap * row_bytes + g.bs;
+  const quant::WritePlan plan =
+      quant::write_plan(num_tokens, num_seqs, g.kvh, g.bs, lpr, row_bytes, g.num_sms);
+  const size_t smem = (size_t)plan.cap * row_bytes + g.bs;
   const quant::WriteArgs A{key, value, cos_cache, sin_cache, k_norm_weight, slot_mapping, cumseq,
                            past, (uint8_t*)key_cache, (uint8_t*)value_cache, (float2*)scales,
                            err_flags, num_tokens, (int64_t)g.num_blocks * g.bs, num_seqs, g.kvh,
                            g.hs, g.vhs, g.ro, g.rd, g.interleaved, g.cos_rows, g.bs, g.max_blocks,
-                           g.rms_eps, lpr, cap};
-  // (first(num_seqs) numbers; see the kernel)
-  const int64_t runs = 2 * (int64_t)num_seqs + num_tokens / g.bs;
-  const dim3 grid((unsigned)runs, (unsigned)g.kvh);
+                           g.rms_eps, lpr, plan.cap};
+  const dim3 grid((unsigned)plan.runs, (unsigned)g.kvh);
   auto go = [&](auto* typed, auto th) {
     auto kern = quant::quant_write_kernel<std::remove_pointer_t<decltype(typed)>, th()>;
     static std::atomic<bool> configured[64];
@@ -646,7 +632,7 @@ pa_status pa_quant_write(const pa_quant_params* p, const void* key, const void* 
     return quant::launch(kern, grid, th(), smem, stream, A, "8-bit write launch");
   };
   auto typed = [&](auto* t) {
-    switch (threads) {
+    switch (plan.threads) {
       case 128: return go(t, std::integral_constant<int, 128>());
       case 256: return go(t, std::integral_constant<int, 256>());
       default: return go(t, std::integral_constant<int, 512>());

@@ -26,6 +26,43 @@ inline int64_t range_tokens(int64_t num_tokens, int64_t num_seqs, int64_t nseq) 
   return std::max<int64_t>(1, num_tokens - (num_seqs - nseq));
 }
 
+// Write: threads of a CTA (a run, the tokens of one sequence in one page, and a kv head),
+// and rows that its shared memory holds at once; a run of more goes in pieces.
+//
+// Threads: warps by the kilobyte of rows, for what a run waits for is other runs' time, and
+// the more rows there are the fewer runs an SM holds. 128 threads up to kFewBytes of rows, 256
+// up to half of kRowBytes, then 512 with all of it. Measured with 128, 256, 512 threads (us; four
+// prompts of 14740 tokens, 8 kv heads of 128 / 128): pages of 16 rows 42.6, 58.5, 114.8; 32: 37.8,
+// 43.1, 66.8; 64: 47.7, 39.5, 49.0; 128: 70.3, 53.2, 43.3; one row for each of 32 sequences 4.4, 5.2, 7.1.
+//
+// Rows: a page, as long as all CTAs run at once so, or else the mean of the runs, 8 at least. Many CTAs of
+// single tokens that each hold room for a page run in several waves, and the last one keeps
+// room from the read behind it: its three CTAs an SM come to two and one. Both in us, room for
+// pages of 64 rows and by the mean, heads as above: 512 single tokens 32.0, 21.3; write and read of
+// 200 sequences with a new token each 255, 195, of 400 325, 230, of 200 and a chunk of 200 tokens 300, 244;
+// of 64 and a prompt of 1000 147, 149. Where one wave is enough, 8 and a chunk of 300: 67, 71.
+constexpr int kRowBytes = 96 * 1024, kFewBytes = 24 * 1024;
+constexpr int kSharedOfSm = 228 * 1024, kSharedOfCta = 1024;  // (the latter beside its own)
+struct WritePlan {
+  int threads, cap;
+  int64_t runs;  // numbers of runs, used or not (see quant_write_kernel)
+};
+// lanes: of a row, a power of two; row_bytes: of shared memory
+inline WritePlan write_plan(int64_t num_tokens, int64_t num_seqs, int64_t kvh, int bs, int lanes,
+                            int row_bytes, int num_sms) {
+  WritePlan w;
+  w.runs = 2 * num_seqs + num_tokens / bs;
+  const int64_t mean = std::min<int64_t>(bs, (num_tokens + num_seqs - 1) / num_seqs);
+  w.threads = mean * row_bytes <= kFewBytes ? 128 : mean * row_bytes <= kRowBytes / 2 ? 256 : 512;
+  const int at_once = w.threads / lanes;
+  const int room = (w.threads == 512 ? kRowBytes : kRowBytes / 2) / row_bytes / at_once * at_once;
+  auto rows = [&](int64_t n) { return (int)std::min<int64_t>(room, (n + at_once - 1) / at_once * at_once); };
+  w.cap = rows(bs);
+  const int64_t at_a_time = kSharedOfSm / (w.cap * row_bytes + bs + kSharedOfCta) * (int64_t)num_sms;
+  if (w.runs * kvh > at_a_time) w.cap = std::min(w.cap, rows(std::max<int64_t>(mean, 8)));
+  return w;
+}
+
 // The grid of the prefill kernel, a CTA per unit (`per` consecutive tokens of a sequence) and
 // kv head. Where the planned ones are few, each is split: `splits` CTAs share its keys.
 struct PrefillGrid {

@@ -187,6 +187,18 @@ def test_write_many_sequences():
         _check_caches(c, t, c.oracle_write())
 
 
+@pytest.mark.parametrize("kw", [dict(bs=64, hs=128), dict(bs=128, hs=64, vhs=256, inter=1), dict(bs=256, hs=32, rd=0), dict(bs=16, hs=256)])
+def test_write_long_among_many_short(kw):
+    """Full pages in pieces beside single tokens: NaN and infinities in one piece and not in the others."""
+    n = 700
+    c = Case([1] * n + [300, 70, 2], list(range(n)) + [5, 0, 62], kv=2, heads=2, seed=47, **kw)
+    c.value[n + 130, 0, 3], c.value[n + 131, 1, 4], c.key[n + 250, 1, -1] = np.inf, np.nan, np.nan
+    t, op = c.tensors(), c.op()
+    op.write(t["key"], t["value"], t["kc"], t["vc"], t["scales"], t["cos"], t["sin"], t["slots"], t["cum"], t["past"])
+    assert op.error_flags() == 0
+    _check_caches(c, t, c.oracle_write())
+
+
 def test_write_borders_and_extremes():
     """Magnitudes at and beside 448 * 2^e, zeros, subnormals, the largest values, infinities and NaN."""
     for dtype in (P.BF16, P.F16):

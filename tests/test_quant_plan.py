@@ -19,6 +19,10 @@ void grid_of(int64_t t, int64_t r, int64_t n, int64_t kvh, int64_t per, int64_t 
   const PrefillGrid g = prefill_grid(t, r, n, kvh, per, tiles, sms);
   out[0] = g.ctas; out[1] = g.planned; out[2] = g.splits; out[3] = g.launched();
 }
+void write_of(int64_t t, int64_t n, int64_t kvh, int bs, int lanes, int row_bytes, int sms, int64_t* out) {
+  const WritePlan w = write_plan(t, n, kvh, bs, lanes, row_bytes, sms);
+  out[0] = w.threads; out[1] = w.cap; out[2] = w.runs;
+}
 void part_of(int cta, int planned, int splits, int* out) {
   const PrefillPart p = prefill_part(cta, planned, splits);
   out[0] = p.at; out[1] = p.split; out[2] = p.splits;
@@ -40,6 +44,7 @@ def plan(tmp_path_factory):
     i64 = ctypes.c_int64
     lib.tokens_of.restype, lib.tokens_of.argtypes = i64, [i64] * 3
     lib.grid_of.argtypes = [i64] * 6 + [ctypes.c_int, ctypes.POINTER(i64)]
+    lib.write_of.argtypes = [i64] * 3 + [ctypes.c_int] * 4 + [ctypes.POINTER(i64)]
     lib.part_of.argtypes = [ctypes.c_int] * 3 + [ctypes.POINTER(ctypes.c_int)]
 
     class Plan:
@@ -49,6 +54,12 @@ def plan(tmp_path_factory):
         def grid(*a):
             out = (i64 * 4)()
             lib.grid_of(*a, out)
+            return tuple(out)
+
+        @staticmethod
+        def write(*a):
+            out = (i64 * 3)()
+            lib.write_of(*a, out)
             return tuple(out)
 
         @staticmethod
@@ -99,3 +110,25 @@ def test_parts_cover_every_unit_once(plan):
         assert units == list(range(planned + more))
         assert all((at, s) in seen for at in units for s in range(seen[at]))
         assert sum(isinstance(k, tuple) for k in seen) == planned * splits + more
+
+
+def test_write_holds_what_its_runs_bring(plan):
+    """In pieces of whole rounds of its threads, within its shared memory; single tokens of large batches do
+    not each hold room for a page."""
+    for tokens, seqs, kvh, bs, (hs, vhs) in itertools.product(
+            (1, 32, 200, 5000, 100000), (1, 32, 512, 5000), (1, 8), (16, 64, 128, 4096),
+            ((16, 16), (64, 128), (128, 128), (192, 128), (256, 256), (16, 256))):
+        lanes = 2
+        while lanes * 8 < max(hs, vhs):
+            lanes *= 2
+        row = (2 * hs + vhs) * 2
+        threads, cap, runs = plan.write(tokens, seqs, kvh, bs, lanes, row, 152)
+        assert threads in (128, 256, 512) and cap > 0 and cap % (threads // lanes) == 0
+        assert cap * row <= (96 if threads == 512 else 48) * 1024 and cap < bs + threads // lanes
+        assert runs >= 2 * seqs + tokens // bs
+        waves = runs * kvh / (152 * (228 * 1024 // (cap * row + bs + 1024)))
+        brings = max(8, min(bs, -(-tokens // seqs)))
+        assert waves <= 1 or cap < brings + threads // lanes
+    assert plan.write(512, 512, 8, 64, 16, 768, 152)[:2] == (128, 8)
+    assert plan.write(32, 32, 8, 64, 16, 768, 152)[:2] == (128, 64)
+    assert plan.write(14740, 4, 8, 64, 16, 768, 152)[:2] == (256, 64)
