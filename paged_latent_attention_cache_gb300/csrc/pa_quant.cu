@@ -553,7 +553,7 @@ pa_status check_read(Phase ph, const pa_quant_params* p, QuantArgs* args, Geomet
 
 pa_status launch_read(Phase ph, const Geometry& g, const QuantArgs& a) {
   if (a.num_tokens == 0 || a.seq_end == a.seq_begin) return PA_OK;
-  const cudaError_t e = ph == Phase::kDecode ? launch_rows(g, a, true) : launch_prefill(g, a);
+  const cudaError_t e = ph == Phase::kDecode ? launch_rows(g, a, true, kAnyTokens) : launch_prefill(g, a);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();  // not left behind for a later call
     return fail(PA_ERR_CUDA, "attention over an 8-bit cache: %s", cudaGetErrorString(e));

@@ -137,7 +137,7 @@ size_t rows_workspace(const Geometry& g, int64_t nseq) {
   return std::max(p.o + p.ml, q.o + q.ml) + p.line + p.units;
 }
 
-cudaError_t launch_rows(const Geometry& g, const QuantArgs& a, bool decode) {
+cudaError_t launch_rows(const Geometry& g, const QuantArgs& a, bool decode, int32_t few) {
   DecP A{};
   A.R = read_params(g, a);
   const int64_t nseq = A.R.nseq, tokens = decode ? nseq : a.num_tokens;  // (at most)
@@ -152,6 +152,7 @@ cudaError_t launch_rows(const Geometry& g, const QuantArgs& a, bool decode) {
   A.ws_line = reinterpret_cast<int64_t*>(ws + p.o + p.ml);
   A.ws_units = reinterpret_cast<int32_t*>(ws + p.o + p.ml + p.line);
   A.decode = decode;
+  A.few = few;
   A.rows = 8 * p.nb;
   A.tile = 16 * p.th;
   A.box = std::min(g.bs, A.tile);

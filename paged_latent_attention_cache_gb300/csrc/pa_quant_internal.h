@@ -33,9 +33,9 @@ struct QuantArgs {
 };
 
 // Few query rows per sequence (pa_quant_decode.cu): decode, and prefill of a few
-// tokens; workspace bytes for nseq sequences
+// tokens (sequences of at most `few`); workspace bytes for nseq sequences
 size_t rows_workspace(const Geometry& g, int64_t nseq);
-cudaError_t launch_rows(const Geometry& g, const QuantArgs& a, bool decode);
+cudaError_t launch_rows(const Geometry& g, const QuantArgs& a, bool decode, int32_t few);
 // prefill (pa_quant_prefill.cu), which hands few rows to launch_rows; workspace bytes
 size_t prefill_workspace(const Geometry& g, int64_t nseq);
 cudaError_t launch_prefill(const Geometry& g, const QuantArgs& a);

@@ -63,21 +63,54 @@ inline WritePlan write_plan(int64_t num_tokens, int64_t num_seqs, int64_t kvh, i
   return w;
 }
 
-// The grid of the prefill kernel, a CTA per unit (`per` consecutive tokens of a sequence) and
-// kv head. Where the planned ones are few, each is split: `splits` CTAs share its keys.
+// Which kernel takes a prefill range: the one for few rows takes sequences of at most `few`
+// tokens, the one for many rows the others; either is left out where nothing is left for it.
+//
+// Batches with at most kFewRows query rows per sequence and kv head, on average, go to the kernel
+// for few rows, which reads the keys once per 16 of them; the other takes as long whatever
+// their number, up to two tiles of 128. Measured, rows there and here (us; 8 kv heads of 128
+// with 4 query heads each): 16 sequences of 2000 to 16000 keys 16 rows 76, 270; 48: 167, 273;
+// 64: 214, 274; 96: 309, 274; 32 sequences of 100 to 1000 keys 48: 64, 68; 64: 84, 70.
+//
+// In such a batch one sequence may still be long, and nothing tells the host. From kBothRows
+// rows in all on, both kernels are launched, and sequences of more than kLongRows are the
+// other one's. With one kernel and with both (us; heads as above): 300 sequences of one token over 100
+// to 1000 keys and one of 8192 rows 852, 252; one of 8192 behind 8000 keys 1813, 517; 64 over 500
+// to 4000 and one of 2048 behind 8000 404, 203; one of 512 behind none 93, 105. A launch that finds nothing
+// costs 8 to 14: 128 drafts of 5 tokens 477, 490; below kBothRows it would be 32 of 12 tokens 98,
+// 111. (The reverse, single tokens beside a prompt that lifts the mean, is left to the one kernel:
+// 64 and a prompt of 2000 tokens 267, with both 189, but 32 sequences of 16 tokens 50, with both 83.)
+constexpr int64_t kFewRows = 48, kLongRows = 1024, kBothRows = 2048;
+constexpr int32_t kAnyTokens = INT32_MAX;
+struct ReadChoice {
+  int32_t few;
+  bool rows, many;
+};
+inline ReadChoice choose_kernels(int64_t tokens, int64_t nseq, int64_t group) {
+  if (tokens * group > kFewRows * nseq) return {0, false, true};
+  if (tokens * group <= kBothRows) return {kAnyTokens, true, false};
+  return {(int32_t)(kLongRows / group), true, true};
+}
+
+// The grid of the prefill kernel, a CTA per unit (`per` consecutive tokens of a sequence of more
+// than `few`) and kv head. Where the planned ones are few, each is split: `splits` CTAs share its
+// keys.
 struct PrefillGrid {
   int64_t ctas;     // units and kv heads, at most (whatever the offsets)
   int64_t planned;  // of them those that are split
-  int splits;
+  int splits = 1;
   int64_t launched() const { return ctas + planned * (splits - 1); }
 };
-inline PrefillGrid prefill_grid(int64_t num_tokens, int64_t tokens, int64_t nseq, int64_t kvh,
-                                int64_t per, int64_t tiles, int num_sms) {
-  // (a sequence with tokens has at most one unit that is not full)
-  auto units = [&](int64_t t) { return (t / per + std::min(nseq, t)) * kvh; };
+inline PrefillGrid prefill_grid(int64_t num_tokens, int64_t tokens, int64_t nseq, int64_t few,
+                                int64_t kvh, int64_t per, int64_t tiles, int num_sms) {
+  // (a sequence with so many tokens has at most one unit that is not full)
+  auto units = [&](int64_t t) { return (t / per + std::min(nseq, t / (few + 1))) * kvh; };
   PrefillGrid g;
   g.ctas = units(num_tokens);
-  g.planned = std::min(g.ctas, units(tokens));
+  // (beside sequences for the other kernel: one, with the tokens that they leave)
+  g.planned = few > 0 ? (std::max<int64_t>(0, tokens - nseq) / per + 1) * kvh : units(tokens);
+  g.planned = std::min(g.ctas, g.planned);
+  if (g.planned == 0) return g;  // (no such sequence at all)
   // parts of four tiles at least, as long as there are SMs
   g.splits = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms / g.planned, tiles / 4));
   return g;

@@ -71,6 +71,7 @@ struct PreP {
   int64_t num_slots;
   int box;       // rows of a copy: min(bs, N)
   int tpc;       // tokens of a query tile
+  int few;       // sequences of no more tokens are another kernel's
   int planned, splits;  // units x kv heads that are split, CTAs of each (see prefill_part)
   int slabs, vslabs, klpr, vlpr;  // 64-channel slabs, lanes for a row's 8-byte pieces
 };
@@ -113,6 +114,7 @@ __device__ Unit resolve(const PreP& A, int unit, int split, int splits, int lane
     if (i < P.nseq) {
       *q0 = P.cumseq[P.seq_begin + i];
       *q = (int)((uint32_t)P.cumseq[P.seq_begin + i + 1] - (uint32_t)*q0);  // (of any offsets)
+      if (*q <= A.few) *q = 0;
     }
     return *q > 0 ? (*q - 1) / per + 1 : 0;
   };
@@ -1029,13 +1031,6 @@ cudaError_t launch(const Geometry& g, const QuantArgs& a, const PreP& A, const P
                  : launch_one<QT, R, C, false, false>(g, a, A, grid);
 }
 
-// Batches with so few query rows per sequence and kv head, on average, go to the kernel
-// for few rows, which reads the keys once per 16 of them; here they take as long whatever
-// their number, up to two tiles of 128. Measured, rows there and here (us; 8 kv heads of 128
-// with 4 query heads each): 16 sequences of 2000 to 16000 keys 16 rows 76, 270; 48: 167, 273;
-// 64: 214, 274; 96: 309, 274; 32 sequences of 100 to 1000 keys 48: 64, 68; 64: 84, 70.
-constexpr int64_t kFewRows = 48;
-
 // One query tile where two accumulators do not fit in TMEM, or two queries beside
 // the rings in shared memory.
 int query_tiles(const Geometry& g, int two) {
@@ -1052,7 +1047,11 @@ size_t prefill_workspace(const Geometry& g, int64_t nseq) {
 cudaError_t launch_prefill(const Geometry& g, const QuantArgs& a) {
   const int64_t nseq = a.seq_end - a.seq_begin;
   const int64_t tokens = range_tokens(a.num_tokens, a.num_seqs, nseq);
-  if (tokens * (g.H / g.kvh) <= kFewRows * nseq) return launch_rows(g, a, false);
+  const ReadChoice choice = choose_kernels(tokens, nseq, g.H / g.kvh);
+  if (choice.rows) {
+    const cudaError_t e = launch_rows(g, a, false, choice.few);
+    if (e != cudaSuccess || !choice.many) return e;
+  }
   PreP A{};
   A.R = read_params(g, a);
   const int qt = query_tiles(g, A.R.two);
@@ -1071,9 +1070,12 @@ cudaError_t launch_prefill(const Geometry& g, const QuantArgs& a) {
   A.ws_o = static_cast<float*>(a.workspace);
   A.ws_ml = reinterpret_cast<float2*>(A.ws_o + (size_t)g.num_sms * qt * kRows * g.vhs);
   const PrefillGrid grid =
-      prefill_grid(a.num_tokens, tokens, A.R.nseq, g.kvh, qt * A.tpc,
+      prefill_grid(a.num_tokens, tokens, A.R.nseq, choice.few, g.kvh, qt * A.tpc,
                    ((int64_t)g.max_blocks * g.bs + N - 1) / N, g.num_sms);
+  if (grid.planned == 0) return cudaSuccess;
   if (grid.launched() > INT32_MAX) return cudaErrorInvalidConfiguration;
+  A.few = choice.few;
+  if (choice.rows) A.R.early = 0;  // (behind the other kernel, not behind the write)
   A.planned = (int)grid.planned;
   A.splits = grid.splits;
   // four tiles converted ahead where they fit

@@ -51,6 +51,7 @@ struct DecP {
   int64_t* ws_line;  // [nseq + 1] length of the line before each sequence, then that of a part
   int32_t* ws_units; // [nseq + 1] units before each sequence, then all
   int decode;        // one token per sequence, others are told
+  int few;           // otherwise: sequences of more tokens are another kernel's
   int rows;          // 8 NB
   int tile;          // keys: 16 TH
   int box;           // rows of a copy: min(bs, tile)
@@ -75,14 +76,16 @@ __device__ __forceinline__ Span span_of(const DecP& A, int b) {
   s.pos = past;
   s.hi = P.cross ? past - 1 : past + q - 1;
   s.lo = P.window >= 0 ? max((int64_t)0, past - P.window) : 0;
-  s.rows = q > 0 && c0 >= 0 && c1 <= P.num_tokens && (q == 1 || !A.decode);
-  s.err = A.decode && q != 1                                     ? PA_DEVERR_DECODE_QLEN
+  const bool mine = A.decode || q <= A.few;
+  s.rows = mine && q > 0 && c0 >= 0 && c1 <= P.num_tokens && (q == 1 || !A.decode);
+  s.err = !mine                                                  ? 0
+          : A.decode && q != 1                                     ? PA_DEVERR_DECODE_QLEN
           : q < 0 || (q > 0 && !s.rows)                          ? PA_DEVERR_CUMSEQ
           : q > 0 && (past < 0 || s.hi >= (int64_t)P.max_blocks * P.bs) ? PA_DEVERR_CONTEXT
           : q > 0 && P.rd > 0 && s.hi >= P.cos_rows              ? PA_DEVERR_POSITION
                                                                  : 0;
   s.first = (int)(s.lo / A.tile);
-  s.tiles = s.err || q <= 0 || s.hi < s.lo ? 0 : (int)(s.hi / A.tile) - s.first + 1;
+  s.tiles = !mine || s.err || q <= 0 || s.hi < s.lo ? 0 : (int)(s.hi / A.tile) - s.first + 1;
   s.chunks = s.tiles ? (s.q * P.grp + A.rows - 1) / A.rows : 0;
   return s;
 }

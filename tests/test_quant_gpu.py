@@ -519,6 +519,74 @@ def test_a_range_among_sequences_without_tokens(q):
     _check_out(out[first:], want[0][first:], want[1][first:])
 
 
+SKEWED = [  # few rows on average: 1 and 300 tokens, and sequences of 1024 rows and a token more
+    dict(q=[1] * 100 + [300] + [1] * 20, past=list(range(100)) + [600] + [7] * 20, heads=8, kv=1),
+    dict(q=[0, 3] * 120 + [256, 257] + [2] * 60, past=[5, 90] * 120 + [0, 300] + [64] * 60, heads=4, kv=1, bs=64, sink=True),
+    dict(q=[400] + [1] * 90, past=[100] + [30] * 90, heads=16, kv=2, window=50, softcap=8.0),
+    dict(q=[1] * 90 + [150], past=[40] * 90 + [0], heads=16, kv=1, hs=256, vhs=256, inter=1, norm=True),
+]
+
+
+@pytest.mark.parametrize("dtype", [P.BF16, P.F16])
+@pytest.mark.parametrize("kw", SKEWED)
+def test_long_sequences_among_short_ones(kw, dtype):
+    _run(Case(dtype=dtype, seed=48, **kw), 0)
+
+
+def test_long_and_short_sequences_tell_their_errors():
+    """Each kernel tells of its own sequences, and the others keep their results."""
+    B = _binding()
+    c = Case([1] * 100 + [300] + [1] * 20, list(range(100)) + [600] + [7] * 20, heads=8, kv=1, seed=49)
+    op, t = c.op(), c.tensors()
+    op.write(t["key"], t["value"], t["kc"], t["vc"], t["scales"], t["cos"], t["sin"], t["slots"], t["cum"], t["past"])
+    ref, tol = c.oracle(c.oracle_write())
+    rows = lambda b: slice(int(c.cum[b]), int(c.cum[b + 1]))
+    assert c.cum[101] == 400
+
+    def run(change):
+        x = {k: v.clone() if v is not None else None for k, v in t.items()}
+        change(x)
+        op.reset_error_flags()
+        out = torch.full((c.T, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+        op.attend(x["query"], x["kc"], x["vc"], x["scales"], x["cos"], x["sin"], x["cum"], x["past"], x["table"], 0, out=out)
+        return out, op.error_flags()
+
+    def others(out, gone):
+        keep = np.ones(c.T, bool)
+        keep[rows(gone)] = False
+        _check_out(out[torch.from_numpy(keep).cuda()], ref[keep], tol[keep])
+
+    for b, page in ((99, 0), (100, 2)):  # a short one, the long one
+        for bad in (-1, c.p["num_blocks"]):
+            out, flags = run(lambda x: x["table"][b, page].fill_(bad))
+            assert flags == B.PA_DEVERR_BLOCK and not out[rows(b)].any()
+            if b == 100:
+                others(out, b)
+        for past in (-1, c.mb * 16, 2 ** 31 - 1):
+            out, flags = run(lambda x: x["past"][b].fill_(past))
+            assert flags == B.PA_DEVERR_CONTEXT and not out[rows(b)].any()
+            others(out, b)
+    for at, value in ((101, c.T + 1), (100, 2 ** 31 - 1), (0, -5), (0, -(2 ** 31)), (100, 500)):
+        out, flags = run(lambda x: x["cum"][at].fill_(value))
+        assert flags & B.PA_DEVERR_CUMSEQ
+
+
+def test_long_and_short_sequences_captured():
+    c = Case([1] * 100 + [300] + [1] * 20, list(range(100)) + [600] + [7] * 20, heads=8, kv=1, seed=50)
+    t, op = c.tensors(), c.op()
+    want = c.forward(op, t, 0).clone()
+    assert torch.equal(c.forward(op, t, 0), want)
+    t2, out = c.tensors(), torch.zeros_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.forward(op, t2, 0, out=out)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
 def test_scales_apart():
     """Pages whose scales lie far apart: values of 2^-48 .. 2^40 in one row's keys, and empty pages of
     zeros among them."""

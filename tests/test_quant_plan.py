@@ -15,8 +15,13 @@ SHIM = r"""
 using namespace pa::quant;
 extern "C" {
 int64_t tokens_of(int64_t t, int64_t b, int64_t n) { return range_tokens(t, b, n); }
-void grid_of(int64_t t, int64_t r, int64_t n, int64_t kvh, int64_t per, int64_t tiles, int sms, int64_t* out) {
-  const PrefillGrid g = prefill_grid(t, r, n, kvh, per, tiles, sms);
+void choose(int64_t t, int64_t n, int64_t group, int* out) {
+  const ReadChoice c = choose_kernels(t, n, group);
+  out[0] = c.few; out[1] = c.rows; out[2] = c.many;
+}
+void grid_of(int64_t t, int64_t r, int64_t n, int64_t few, int64_t kvh, int64_t per, int64_t tiles, int sms,
+             int64_t* out) {
+  const PrefillGrid g = prefill_grid(t, r, n, few, kvh, per, tiles, sms);
   out[0] = g.ctas; out[1] = g.planned; out[2] = g.splits; out[3] = g.launched();
 }
 void write_of(int64_t t, int64_t n, int64_t kvh, int bs, int lanes, int row_bytes, int sms, int64_t* out) {
@@ -43,7 +48,8 @@ def plan(tmp_path_factory):
     lib = ctypes.CDLL(str(d / "plan.so"))
     i64 = ctypes.c_int64
     lib.tokens_of.restype, lib.tokens_of.argtypes = i64, [i64] * 3
-    lib.grid_of.argtypes = [i64] * 6 + [ctypes.c_int, ctypes.POINTER(i64)]
+    lib.choose.argtypes = [i64] * 3 + [ctypes.POINTER(ctypes.c_int)]
+    lib.grid_of.argtypes = [i64] * 7 + [ctypes.c_int, ctypes.POINTER(i64)]
     lib.write_of.argtypes = [i64] * 3 + [ctypes.c_int] * 4 + [ctypes.POINTER(i64)]
     lib.part_of.argtypes = [ctypes.c_int] * 3 + [ctypes.POINTER(ctypes.c_int)]
 
@@ -51,10 +57,16 @@ def plan(tmp_path_factory):
         tokens = staticmethod(lib.tokens_of)
 
         @staticmethod
-        def grid(*a):
+        def grid(tokens, planned, nseq, *a, few=0):
             out = (i64 * 4)()
-            lib.grid_of(*a, out)
+            lib.grid_of(tokens, planned, nseq, few, *a, out)
             return tuple(out)
+
+        @staticmethod
+        def choose(*a):
+            out = (ctypes.c_int * 3)()
+            lib.choose(*a, out)
+            return out[0], bool(out[1]), bool(out[2])
 
         @staticmethod
         def write(*a):
@@ -132,3 +144,32 @@ def test_write_holds_what_its_runs_bring(plan):
     assert plan.write(512, 512, 8, 64, 16, 768, 152)[:2] == (128, 8)
     assert plan.write(32, 32, 8, 64, 16, 768, 152)[:2] == (128, 64)
     assert plan.write(14740, 4, 8, 64, 16, 768, 152)[:2] == (256, 64)
+
+
+def test_a_long_sequence_among_short_ones_has_the_kernel_for_long_ones(plan):
+    """Both kernels where a batch of few rows on average may hold a long sequence, and no row without a kernel."""
+    for tokens, nseq, group in itertools.product((1, 4, 80, 640, 3300, 100000), (1, 2, 16, 301, 5000), (1, 3, 4, 16, 128)):
+        few, rows, many = plan.choose(tokens, nseq, group)
+        assert rows or many
+        assert rows == (tokens * group <= 48 * nseq) and (few > 0) == rows
+        if not many:  # whatever the offsets, no sequence is long
+            assert tokens * group <= 2048 and few >= tokens
+        if rows and many:
+            assert 48 < few * group <= 1024 and (few + 1) * group > 1024 and few < tokens
+    assert plan.choose(3300, 301, 4) == (256, True, True)
+    assert plan.choose(80, 16, 4)[1:] == (True, False)
+    assert plan.choose(2000, 1, 4) == (0, False, True)
+
+
+def test_long_sequences_have_a_place_each(plan):
+    """Beside any number of short ones, as many long ones as the tokens allow."""
+    for tokens, nseq, per, few in itertools.product((700, 3300, 100000), (15, 301, 5000), (1, 64, 256), (8, 256, 1024)):
+        if tokens <= few:
+            continue
+        ctas, planned, splits, launched = plan.grid(tokens, tokens, nseq, 8, per, 1000, 152, few=few)
+        assert 1 <= planned <= ctas and launched == ctas + planned * (splits - 1)
+        assert splits == 1 or planned * splits <= 152
+        for n in {1, 2, min(nseq, tokens // (few + 1))}:  # n long ones, all but one just long enough
+            last = tokens - (n - 1) * (few + 1)
+            if n >= 1 and last > few:
+                assert (-(-last // per) + (n - 1) * -(-(few + 1) // per)) * 8 <= ctas
