@@ -509,14 +509,15 @@ class QuantizedAttention:
     def _tensors(self, dtype, names, *tensors):
         index = self._index
         for t in tensors:
-            if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+            if t is None or t.dtype is not dtype or t.get_device() != index or \
+                    not t.is_contiguous():
                 name = names.split()[[x is t for x in tensors].index(True)]
                 _require(False, f"{name} must be a contiguous {dtype} tensor on {self.device}")
 
     def _check_caches(self, key_cache, value_cache, scales, cumseq, past):
         p, index = self.params, self._index
         for t in (key_cache, value_cache):
-            if (t.dtype is not torch.uint8 and t.dtype is not torch.float8_e4m3fn) or \
+            if t is None or (t.dtype is not torch.uint8 and t.dtype is not torch.float8_e4m3fn) or \
                     t.get_device() != index or not t.is_contiguous():
                 name = "key_cache" if t is key_cache else "value_cache"
                 _require(False, f"{name} must be a contiguous uint8 or float8_e4m3fn tensor on "
@@ -658,6 +659,7 @@ class QuantizedAttention:
         """Reads without a write: decode over sequences [0, num_decode_seqs) and
         prefill over the rest; returns ``out``. (``past`` as in ``forward``: what
         was cached before the tokens of ``query``, or with ``cross`` all there is.)"""
+        _require(query is not None and past is not None, "query and past are required")
         nseq = past.size(0)
         _require(0 <= num_decode_seqs <= nseq, "num_decode_seqs must be in 0..num_seqs")
         with _device(self._index):
@@ -684,6 +686,7 @@ class QuantizedAttention:
                 stream=None) -> torch.Tensor:
         """Write phase over all tokens, then decode over sequences [0,
         num_decode_seqs) and prefill over the rest; returns ``out``."""
+        _require(query is not None and past is not None, "query and past are required")
         nseq = past.size(0)
         _require(not self.params.cross, "cross attention writes and attends apart: see attend")
         _require(0 <= num_decode_seqs <= nseq, "num_decode_seqs must be in 0..num_seqs")

@@ -883,6 +883,33 @@ def test_arguments_refused():
     assert op.error_flags() == 0
 
 
+@pytest.mark.parametrize("name", ["query", "key", "value", "kc", "vc", "scales", "cos", "sin", "cum", "past", "table", "slots"])
+def test_a_tensor_left_out_is_refused_as_a_bad_argument(name):
+    PaError = _binding().PaError
+    c = Case([2, 1], [20, 30], seed=21)
+    t, op = c.tensors(), c.op()
+    with pytest.raises(PaError):
+        c.forward(op, {**t, name: None}, 0)
+    if name in ("query", "kc", "vc", "scales", "cos", "sin", "cum", "past", "table"):
+        x = {**t, name: None}
+        with pytest.raises(PaError):
+            op.attend(x["query"], x["kc"], x["vc"], x["scales"], x["cos"], x["sin"], x["cum"], x["past"], x["table"], 0)
+        out = torch.empty(3, 512, dtype=torch.bfloat16, device="cuda")
+        with pytest.raises(PaError):
+            op.prefill(x["query"], x["kc"], x["vc"], x["scales"], x["cos"], x["sin"], x["cum"], x["past"], x["table"], out)
+    if name in ("key", "value", "kc", "vc", "scales", "cos", "sin", "cum", "past", "slots"):
+        x = {**t, name: None}
+        with pytest.raises(PaError):
+            op.write(x["key"], x["value"], x["kc"], x["vc"], x["scales"], x["cos"], x["sin"], x["slots"], x["cum"], x["past"])
+    if name in ("kc", "vc", "scales", "cum", "past", "table"):
+        x = {**t, name: None}
+        with pytest.raises(PaError):
+            op.restore(x["kc"], x["vc"], x["scales"], x["cum"], x["past"], x["table"], 3)
+    with pytest.raises(PaError):
+        op.decode(t["query"], t["kc"], t["vc"], t["scales"], t["cos"], t["sin"], t["cum"], t["past"], t["table"], None)
+    assert op.error_flags() == 0
+
+
 def test_nothing_to_do():
     c = Case([0, 0], [20, 30], seed=22)
     t, op = c.tensors(), c.op()
