@@ -80,14 +80,18 @@ typedef struct pa_quant_params {
   int32_t flags;              /* PA_FLAG_AFTER_WRITE / PA_FLAG_OWN_SLOTS             */
 } pa_quant_params;
 
+/* PA_FLAG_OWN_SLOTS is accepted and changes nothing here: every read waits for
+ * the write before its first cache row. (A write may change all rows and the scale
+ * of a page that it appends to, so rows below past[b] are not untouched by it.) */
+
 pa_status pa_quant_validate(const pa_quant_params* p);
 
 /* Write phase, as defined above. Arguments and errors as pa_separate_write,
  * and: slot_mapping[t] is a row of the same number in its page as token t's
  * position has (slot % bs == position % bs), and the tokens of one sequence
  * whose positions lie in one page share a page; a token that breaks either
- * sets PA_DEVERR_SLOT and is skipped. No page may be named by two sequences of
- * a call. (An encoder's states are written as a sequence's tokens from past 0.) */
+ * sets PA_DEVERR_SLOT and is skipped. A page is named by tokens of one
+ * sequence and one page of positions only, in a call. (An encoder's states are written as a sequence's tokens from past 0.) */
 pa_status pa_quant_write(const pa_quant_params* p, const void* key, const void* value,
                          int64_t num_tokens, const void* cos_cache, const void* sin_cache,
                          const void* k_norm_weight, const int32_t* slot_mapping,

@@ -446,6 +446,8 @@ class QuantizedAttention:
     with ``cross`` the attention of a decoder's tokens to an encoder's states in
     it. Holds the parameters, the workspace and the error word; calls of one
     object share its workspace: order them (one stream, or events).
+    ``own_slots`` is taken as by the other modes and changes nothing here (a write may
+    change every row of a page that it appends to).
 
     ``query`` [T, H*hs], ``key`` [T, kvH*hs], ``value`` [T, kvH*vhs] in ``dtype``;
     ``key_cache`` [num_blocks, bs, kvH, hs] and ``value_cache`` [num_blocks, bs, kvH,

@@ -53,7 +53,7 @@ struct WriteArgs {
   float2* scales;
   int32_t* err_flags;
   int64_t num_tokens, num_slots;
-  int num_seqs, kvh, hs, vhs, ro, rd, interleaved, cos_rows, bs, max_blocks;
+  int num_seqs, kvh, hs, vhs, ro, rd, interleaved, cos_rows, bs;
   float eps;
   int lpr;  // lanes per row: a power of two >= max(hs, vhs) / 8
   int cap;  // rows that shared memory holds at once
@@ -615,8 +615,8 @@ pa_status pa_quant_write(const pa_quant_params* p, const void* key, const void* 
   const quant::WriteArgs A{key, value, cos_cache, sin_cache, k_norm_weight, slot_mapping, cumseq,
                            past, (uint8_t*)key_cache, (uint8_t*)value_cache, (float2*)scales,
                            err_flags, num_tokens, (int64_t)g.num_blocks * g.bs, num_seqs, g.kvh,
-                           g.hs, g.vhs, g.ro, g.rd, g.interleaved, g.cos_rows, g.bs, g.max_blocks,
-                           g.rms_eps, lpr, plan.cap};
+                           g.hs, g.vhs, g.ro, g.rd, g.interleaved, g.cos_rows, g.bs, g.rms_eps,
+                           lpr, plan.cap};
   const dim3 grid((unsigned)plan.runs, (unsigned)g.kvh);
   auto go = [&](auto* typed, auto th) {
     auto kern = quant::quant_write_kernel<std::remove_pointer_t<decltype(typed)>, th()>;

@@ -178,13 +178,6 @@ __device__ __forceinline__ uint32_t pack_out(const ReadP& P, float a, float b) {
   return P.bf16 ? tc::pack2<__nv_bfloat16>(a, b) : tc::pack2<__half>(a, b);
 }
 
-// Two E4M3 codes (the low 16 bits) as fp16.
-__device__ __forceinline__ uint32_t codes2(uint32_t two) {
-  uint32_t r;
-  asm("{\n .reg .b16 h;\n cvt.u16.u32 h, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(r) : "r"(two));
-  return r;
-}
-
 // Shared memory by its address (pointers into an aligned region become generic loads,
 // which take several times as long).
 __device__ __forceinline__ uint4 lds128(uint32_t a) {

@@ -476,6 +476,26 @@ def test_fp16_keeps_its_bits(q, past, kw):
     assert np.linalg.norm(off) < 3.3e-4 * np.linalg.norm(want), np.linalg.norm(off) / np.linalg.norm(want)
 
 
+def test_own_slots_with_a_page_that_grows():
+    """The promise changes no result, also where the call's rows rescale what is read below them."""
+    for q, nd in (([1, 1, 1], 3), ([40, 3, 70], 0)):
+        c = Case(q, [200, 77, 20], bs=64, seed=51)
+        c.key *= 64.0
+        c.value *= 64.0
+        t, op = c.tensors(), c.op()
+        want = c.forward(op, t, nd)
+        for own in (False, True):
+            t, op = c.tensors(), c.op(own_slots=own)
+            before = t["scales"].clone()
+            op.write(t["key"], t["value"], t["kc"], t["vc"], t["scales"], t["cos"], t["sin"], t["slots"], t["cum"], t["past"])
+            out = torch.empty_like(want)
+            (op.decode if nd else op.prefill)(t["query"], t["kc"], t["vc"], t["scales"], t["cos"], t["sin"], t["cum"],
+                                              t["past"], t["table"], out, after_write=True)
+            assert op.error_flags() == 0 and torch.equal(out, want)
+            page = int(c.table[0, 3])
+            assert bool((t["scales"][page] > before[page]).all())
+
+
 def test_mixed_batch():
     c = Case([1, 1, 1, 50, 9], [10, 300, 64, 20, 0], sink=True, seed=13)
     _run(c, 3)
