@@ -32,12 +32,12 @@ constexpr int kMaxBlock = 4096;  // rows of a page
 // first(b + 1) - first(b) >= q / bs + 2. So a CTA finds its sequence by a search
 // over cumseq, an offset per thread at a time.
 //
-// Bound by instructions for prompts (14740 new tokens of 8 kv heads of 128 / 128, 94 MB:
-// 39.5 us, 2.4 TB/s) and by its chain of loads for single tokens (4.4 us). All rows of a
-// run are on their way to shared memory (cp.async) before its slots are looked at; each
-// thread copies just what it will read, so no barrier stands between. The rotated keys
-// stay there in f32 for their encoding. With a load per row where it was used those tokens
-// took 66 us, with keys rotated twice 52.
+// Bound by instructions for prompts, some 225 per eight channels (14740 new tokens of 8 kv
+// heads of 128 / 128, 94 MB: 39.5 us, 2.4 TB/s), and by its chain of loads for single tokens
+// (32 of them 4.4 us). All rows of a run are on their way to shared memory (cp.async) before its
+// slots are looked at; each thread copies just what it will read, so no barrier stands between.
+// The rotated keys stay there in f32 for their encoding. With a load per row where it was used
+// those tokens took 66 us, with keys rotated twice 52. Threads and shared memory: write_plan.
 // ---------------------------------------------------------------------------
 struct WriteArgs {
   const void* key;

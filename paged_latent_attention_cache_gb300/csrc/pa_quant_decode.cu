@@ -107,6 +107,10 @@ quant_combine_kernel(const __grid_constant__ DecP A) {
 // 1024 keys, 8 kv heads of 128 with 4 query heads each, 24.3, 18.8, 19.1, 21.5; of 1024 to 8192,
 // 71.0, 67.5, 66.4, 67.2. 16 rows: two sequences of 60000 to 131072 keys, 4 kv heads with 16 each,
 // 66.7, 62.7, 61.2, 59.1; drafts of 3 to 7 tokens over 2000 to 16000, 113, 101, 97.5, 93.9.
+// Tiles of 16 keys (head sizes above 128) cost about as much each, their channels being more:
+// 0, 12, 20, 40, 80 at 256 / 256, 32 heads over 8: 90 to 1500 keys 71.3, 39.9, 37.6, 37.0, 39.9;
+// 1024 to 8192 117, 110, 108, 109, 115; 64 over 4 (16 rows) 61.5, 32.2, 33.6, 36.5, 45.1 and
+// 91.3, 79.3, 78.0, 74.6, 85.1. (Furthest off: 16 heads of 128 / 256 over 90 to 1500, 54.4 and with 40 48.5.)
 constexpr int kExtra = 20;
 
 struct Plan {

@@ -1,6 +1,6 @@
 // Attention over 8-bit caches for few query rows (include/pa_quant.h): decode, one new
 // token per sequence, and prefill of a few tokens each. Bound by HBM where there is much to
-// read: 32 sequences of 8192 to 65536 keys, 32 heads over 8 of 128 / 128, 426 us, 5.8 TB/s;
+// read: 32 sequences of 8192 to 65536 keys, 32 heads over 8 of 128 / 128, 422 us, 5.7 TB/s;
 // of 1024 to 8192 66 us, 4.6 TB/s, some 15 us of which are the plan, the first copies and
 // the joining of parts; 32 of 90 to 1500, 16 heads of 64, 29 us, 1.8 TB/s.
 //
@@ -186,7 +186,10 @@ __device__ __forceinline__ float inverse(const ReadP& P, int g, int r0, int r, i
 // CTAs per SM and the shared memory of one: rings, query, joining buffers. Twelve
 // warps an SM where the registers allow it: with eight (one CTA of 255 registers a
 // thread) 32 sequences of 1024 to 8192 keys (32 heads over 8, 128 / 128) took 104 us where
-// twelve took 90.
+// twelve took 90. With values above 128 channels and 16 rows a unit a thread's 255 registers do not
+// hold everything, and 8 to 96 bytes of it go by local memory; 32 sequences of 1024 to 8192 keys:
+// 64 heads over 4 of 128 / 256 70 us in bf16, 78 in fp16 (3.2, 2.9 TB/s; with 128 / 128 none spill but
+// fp16's 8 rows, 8 bytes), five tokens each of 32 heads over 8 192 and 214.
 template <int KP, int VP, int NB, int TH, bool LO>
 struct Shape {
   static constexpr int kCtas = TH == 2 && NB == 1 ? 3 : 2;
@@ -782,8 +785,8 @@ cudaError_t launch_one(const Geometry& g, const QuantArgs& a, const DecP& A) {
 }
 
 // The kernel for head sizes up to 64 kp and 128 vp and 8 nb rows a unit; tiles of 32 keys
-// where a ring of them fits (the long sequences above 396 us, with tiles of 16 436), or
-// else of 16.
+// where a ring of them fits (the long sequences above 422 us, with tiles of 16 and two CTAs an SM
+// 441; 32 of 90 to 1500 keys, 16 heads of 64, 29 and 39), or else of 16.
 template <bool LO>
 cudaError_t launch_rows_kernel(const Geometry& g, const QuantArgs& a, const DecP& A, int kp, int vp,
                                int nb) {
