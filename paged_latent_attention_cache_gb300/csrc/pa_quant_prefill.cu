@@ -342,7 +342,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return m;
 }
 
-template <int QT, int R, int C, bool CAP, bool TWO>
+// CAP: 0 no softcap, 1 one, 2 a wide one (capped).
+template <int QT, int R, int C, int CAP, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1)
 quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PreP A) {
@@ -502,7 +503,7 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
           }
           v0 = max3(fmaxf(v0, v1), at(16 * i + 14), at(16 * i + 15));
           const float f = factor_of(sc[i]);
-          if (CAP) v0 = v0 == -INFINITY ? v0 : capped(P, v0 * f);
+          if (CAP) v0 = v0 == -INFINITY ? v0 : capped<CAP == 2>(P, v0 * f);
           top = fmaxf(top, fmaf(v0, CAP ? 1.f : f, sc[i].y));
         }
         // The row's maximum goes by both halves. (Both warps have read their scores behind
@@ -539,8 +540,8 @@ quant_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
           for (int e = 16 * h; e < 16 * h + 16; e += 2) {
             float a = at(e), b = at(e + 1);
             if (CAP) {
-              a = a == -INFINITY ? a : capped(P, a * f);
-              b = b == -INFINITY ? b : capped(P, b * f);
+              a = a == -INFINITY ? a : capped<CAP == 2>(P, a * f);
+              b = b == -INFINITY ? b : capped<CAP == 2>(P, b * f);
             }
             uint64_t y;
             asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(pack_f32(a, b)), "l"(f2), "l"(a2));
@@ -1001,7 +1002,7 @@ size_t shared_bytes(const Geometry& g, const PreP& A, int qt, int ring, int code
          (size_t)ring * (A.slabs + A.vslabs) * N * 128 + (size_t)codes * N * (g.hs + g.vhs);
 }
 
-template <int QT, int R, int C, bool CAP, bool TWO>
+template <int QT, int R, int C, int CAP, bool TWO>
 cudaError_t launch_one(const Geometry& g, const QuantArgs& a, const PreP& A,
                        const PrefillGrid& grid) {
   static std::atomic<bool> configured[64];
@@ -1024,11 +1025,12 @@ cudaError_t launch_one(const Geometry& g, const QuantArgs& a, const PreP& A,
 
 template <int QT, int R, int C>
 cudaError_t launch(const Geometry& g, const QuantArgs& a, const PreP& A, const PrefillGrid& grid) {
-  if (g.softcap > 0.f)
-    return A.R.two ? launch_one<QT, R, C, true, true>(g, a, A, grid)
-                   : launch_one<QT, R, C, true, false>(g, a, A, grid);
-  return A.R.two ? launch_one<QT, R, C, false, true>(g, a, A, grid)
-                 : launch_one<QT, R, C, false, false>(g, a, A, grid);
+  auto of = [&](auto cap) {
+    return A.R.two ? launch_one<QT, R, C, cap(), true>(g, a, A, grid)
+                   : launch_one<QT, R, C, cap(), false>(g, a, A, grid);
+  };
+  if (A.R.cap_in <= 0.f) return of(std::integral_constant<int, 0>());
+  return A.R.cap_wide ? of(std::integral_constant<int, 2>()) : of(std::integral_constant<int, 1>());
 }
 
 // One query tile where two accumulators do not fit in TMEM, or two queries beside

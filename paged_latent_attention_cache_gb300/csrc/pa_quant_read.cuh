@@ -47,6 +47,7 @@ struct ReadP {
   float scale_log2;  // scale * log2(e)
   float cap_in;      // scale / softcap, 0 without softcap
   float cap_out;     // softcap * log2(e)
+  int cap_wide;      // softcap above kWideCap
   float eps;
 };
 
@@ -59,6 +60,13 @@ struct ReadP {
 inline bool two_addends(const Geometry& g, const QuantArgs& a) {
   return g.dtype != PA_DTYPE_BF16 && (g.rd > 0 || a.q_norm);
 }
+
+// From 2^60 on a softcap moves no score by a place of its f32 value (by s^2 / (3 softcap^2) of
+// it, scores below 2^48), and its reciprocal times the scales would leave f32's range.
+// Above kWideCap its tanh goes by capped<true> (1e-7 of 128 is 1.3e-5 of a score, a twentieth of
+// an fp16 output's rounding; up to it long prefill takes 1242 us, above 1905).
+constexpr float kWideCap = 128.f;
+inline float softcap_of(const Geometry& g) { return g.softcap < 0x1p60f ? g.softcap : 0.f; }
 
 inline ReadP read_params(const Geometry& g, const QuantArgs& a) {
   ReadP P{};
@@ -97,8 +105,10 @@ inline ReadP read_params(const Geometry& g, const QuantArgs& a) {
   P.early = (g.flags & PA_FLAG_AFTER_WRITE) ? 1 : 0;
   P.two = two_addends(g, a);
   P.scale_log2 = g.scale * kLog2e;
-  P.cap_in = g.softcap > 0.f ? g.scale / g.softcap : 0.f;
-  P.cap_out = g.softcap * kLog2e;
+  const float softcap = softcap_of(g);
+  P.cap_in = softcap > 0.f ? g.scale / softcap : 0.f;
+  P.cap_out = softcap * kLog2e;
+  P.cap_wide = softcap > kWideCap;
   P.eps = g.rms_eps;
   return P;
 }
@@ -122,9 +132,15 @@ inline cudaError_t codes_map(CUtensorMap* map, const void* base, const Geometry&
              : cudaErrorInvalidValue;
 }
 
-// log2e times the softcapped score whose ratio to softcap is x.
+// log2e times the softcapped score whose ratio to softcap is x. tanh_ex2 is some 1e-7 off
+// whatever x is, and a softcap far above the scores magnifies that to more than they are: with
+// WIDE, tanh's series below 1/4 (the next term is 1382 / 155925 x^10 < 9e-9 of the result).
+template <bool WIDE>
 __device__ __forceinline__ float capped(const ReadP& P, float x) {
-  return P.cap_out * tanh_ex2(x);
+  if (!WIDE) return P.cap_out * tanh_ex2(x);
+  const float t = x * x;
+  const float r = fmaf(fmaf(fmaf(62.f / 2835.f, t, -17.f / 315.f), t, 2.f / 15.f), t, -1.f / 3.f);
+  return P.cap_out * (fabsf(x) < 0.25f ? fmaf(x * t, r, x) : tanh_ex2(x));
 }
 
 // Eight channels of a query row as fp16, the row times a power of two that

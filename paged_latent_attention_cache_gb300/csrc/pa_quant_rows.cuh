@@ -187,7 +187,7 @@ __device__ __forceinline__ float inverse(const ReadP& P, int g, int r0, int r, i
 // warps an SM where the registers allow it: with eight (one CTA of 255 registers a
 // thread) 32 sequences of 1024 to 8192 keys (32 heads over 8, 128 / 128) took 104 us where
 // twelve took 90. With values above 128 channels and 16 rows a unit a thread's 255 registers do not
-// hold everything, and 8 to 96 bytes of it go by local memory; 32 sequences of 1024 to 8192 keys:
+// hold everything, and up to 96 bytes of it go by local memory; 32 sequences of 1024 to 8192 keys:
 // 64 heads over 4 of 128 / 256 70 us in bf16, 78 in fp16 (3.2, 2.9 TB/s; with 128 / 128 none spill but
 // fp16's 8 rows, 8 bytes), five tokens each of 32 heads over 8 192 and 214.
 template <int KP, int VP, int NB, int TH, bool LO>
@@ -535,16 +535,21 @@ quant_rows_kernel(const __grid_constant__ CUtensorMap kmap,
       }
       // scores of keys 16 h + kappa (c[0], c[1]) and + 8 for rows 2 t and 2 t + 1
       const int j0 = tile * kTile;
+      auto scale_scores = [&](auto cap, auto wide) {
 #pragma unroll
-      for (int h = 0; h < TH; ++h)
+        for (int h = 0; h < TH; ++h)
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float f = ks[h] * mult[nb][e & 1];
-            c[h][nb][e] = P.cap_in > 0.f ? capped(P, c[h][nb][e] * f) + ev[h]
-                                         : fmaf(c[h][nb][e], f, ev[h]);
-          }
+            for (int e = 0; e < 4; ++e) {
+              const float f = ks[h] * mult[nb][e & 1];
+              c[h][nb][e] = cap() ? capped<wide()>(P, c[h][nb][e] * f) + ev[h]
+                                  : fmaf(c[h][nb][e], f, ev[h]);
+            }
+      };
+      if (P.cap_in <= 0.f) scale_scores(std::false_type(), std::false_type());
+      else if (!P.cap_wide) scale_scores(std::true_type(), std::false_type());
+      else scale_scores(std::true_type(), std::true_type());
       if (j0 < all_lo || j0 + kTile - 1 > all_hi) {
         // an end of what the rows see: unseen values become zeros (0 times NaN is NaN),
         // and a NaN among values that only some rows see goes over to their scores

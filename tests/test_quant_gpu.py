@@ -388,6 +388,22 @@ def test_decode(kw, dtype):
     _run(Case(dtype=dtype, **kw), len(kw["q"]))
 
 
+@pytest.mark.parametrize("softcap", [0.3, 128.0, 129.0, 3e2, 1e4, 1e6, 1e9, 1e18, 2e18, 3e38])
+@pytest.mark.parametrize("q", [[1, 1], [3, 2], [60, 9]])
+def test_softcaps_of_any_size(q, softcap):
+    """One far above the scores leaves them as they are, one below them all but decides them. (Some outputs are
+    below 2^-14, where fp16 values are 2^-24 apart and rounding moves one by up to 2^-25.)"""
+    for kw in (dict(), dict(hs=256, vhs=256)):
+        c = Case(q, [400, 90], dtype=P.F16, softcap=softcap, gain=4.0, seed=52, **kw)
+        t, op = c.tensors(), c.op()
+        out = c.forward(op, t, 2 if q == [1, 1] else 0)
+        assert op.error_flags() == 0
+        want = c.oracle_write()
+        _check_caches(c, t, want)
+        ref, tol = c.oracle(want)
+        _check_out(out, ref, tol + 2.0 ** -25)
+
+
 PREFILLS = [
     dict(q=[1], past=[0]), dict(q=[2], past=[0]), dict(q=[3, 1, 0, 5], past=[0, 30, 7, 16]), dict(q=[130], past=[0]),
     dict(q=[70, 20], past=[100, 300], bs=64), dict(q=[129, 64], past=[127, 0], heads=4, kv=4), dict(q=[40, 30], past=[90, 0], heads=3, kv=1),
